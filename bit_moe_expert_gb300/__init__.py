@@ -27,7 +27,10 @@ EXPORTED = ("moe_status_string", "moe_device_sm_count", "moe_prepack_bytes", "mo
             "moe_router_logits", "moe_route_x", "moe_layer_x", "moe_topk_wide",
             "moe_forward_workspace_bytes",
             "moe_forward", "moe_layer_workspace_bytes", "moe_layer", "moe_check_status", "moe_profile_enable", "moe_profile_kernel_count",
-            "moe_profile_kernel_name", "moe_profile_read", "moe_profile_reset", "moe_debug_decode")
+            "moe_profile_kernel_name", "moe_profile_read", "moe_profile_reset", "moe_debug_decode",
+            "moe_route_scored", "moe_mx_scale_bytes", "moe_mx_prepack_scales", "moe_mx_quantize", "moe_mx_dequant",
+            "moe_mx_matmul", "moe_mx_linear_workspace_bytes", "moe_mx_linear", "moe_mx_forward_workspace_bytes",
+            "moe_mx_forward", "moe_mx_layer_workspace_bytes", "moe_mx_layer")
 
 
 class MoeError(RuntimeError):
@@ -48,6 +51,19 @@ class _Routing(C.Structure):
     _fields_ = [("ids", C.c_void_p), ("w", C.c_void_p), ("counts", C.c_void_p), ("offsets", C.c_void_p),
                 ("perm", C.c_void_p), ("inv_perm", C.c_void_p), ("block_map", C.c_void_p),
                 ("num_blocks", C.c_void_p), ("block_rows", C.c_int)]
+
+
+class _Scoring(C.Structure):
+    _fields_ = [("score", C.c_int), ("bias", C.c_void_p), ("n_group", C.c_int), ("topk_group", C.c_int),
+                ("group_top", C.c_int), ("renormalize", C.c_int), ("scale", C.c_float)]
+
+
+class _MxMat(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("sp", C.c_void_p)]
+
+
+class _MxExperts(C.Structure):
+    _fields_ = [("gate", _MxMat), ("up", _MxMat), ("down", _MxMat), ("n_experts", C.c_int)]
 
 
 _lib_handle = None
@@ -122,6 +138,24 @@ def lib(path: Optional[str] = None):
         L.moe_profile_reset.restype = None
         L.moe_debug_decode.restype = C.c_int
         L.moe_debug_decode.argtypes = [C.c_longlong, C.c_int]
+        i, p, sz, mat = C.c_int, C.c_void_p, C.c_size_t, C.POINTER(_MxMat)
+        ex = C.POINTER(_MxExperts)
+        for name, restype, argtypes in (
+                ("moe_route_scored", i, [p, C.POINTER(_Scoring), i, i, i, i, C.POINTER(_Routing), p, sz, p]),
+                ("moe_mx_scale_bytes", sz, [i, i, i]),
+                ("moe_mx_prepack_scales", i, [p, i, i, i, p, p]),
+                ("moe_mx_quantize", i, [p, i, i, i, C.c_longlong, mat, p]),
+                ("moe_mx_dequant", i, [mat, i, i, i, i, p, p]),
+                ("moe_mx_matmul", i, [mat, i, mat, i, i, p, i, p, sz, p]),
+                ("moe_mx_linear_workspace_bytes", sz, [i, i, i]),
+                ("moe_mx_linear", i, [p, i, i, i, C.c_longlong, mat, i, p, i, p, sz, p]),
+                ("moe_mx_forward_workspace_bytes", sz, [i] * 7),
+                ("moe_mx_forward", i, [p, i, i, i, i, ex, ex, i, C.POINTER(_Routing), p, p, sz, p]),
+                ("moe_mx_layer_workspace_bytes", sz, [i] * 7),
+                ("moe_mx_layer", i, [p, C.POINTER(_Scoring), p, i, i, i, i, i, ex, ex, i, C.POINTER(_Routing), p, p,
+                                     sz, p])):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = restype, argtypes
         _lib_handle = L
     return _lib_handle
 
@@ -407,6 +441,255 @@ def moe_profile_read() -> dict:
     return out
 
 
+# ----------------------------------------------------------------------- scored routing, MXFP4
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+@dataclasses.dataclass
+class Scoring:
+    """How moe_route_scored scores a token's logits (see include/moe.h): softmax or sigmoid scores, a bias for the
+    selection (fp32 [E] on the device, or None), groups, weights renormalised over the selection and scaled."""
+    score: str = "softmax"
+    bias: "object" = None
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 2
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def _c(self, E: int) -> _Scoring:
+        key = (self.score, self.bias, self.n_group, self.topk_group, self.group_top, self.renormalize, self.scale, E)
+        c = self.__dict__.get("_cc")
+        if c is None or c[0][1] is not key[1] or c[0][0] != key[0] or c[0][2:] != key[2:]:
+            if self.score not in SCORES:
+                raise ValueError(f"score {self.score!r}: one of {sorted(SCORES)}")
+            if self.bias is not None:
+                _tensor("bias", self.bias, ("float32",), (E,))
+            top = 1 if self.n_group == 1 else self.group_top
+            c = (key, _Scoring(SCORES[self.score], _ptr(self.bias), self.n_group, self.topk_group, top,
+                               1 if self.renormalize else 0, self.scale))
+            self.__dict__["_cc"] = c
+        return c[1]
+
+
+def _tensor(name: str, t, dtypes, shape=None) -> None:
+    """A contiguous CUDA tensor of one of the types and, where given, of the shape."""
+    if str(t.dtype)[6:] not in dtypes:  # "torch.float32" -> "float32"
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, expected a CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+_DTYPES = {"torch.bfloat16": 0, "torch.int16": 0, "torch.float16": 1, "torch.float32": 2}
+
+
+def _dtype(name: str, t) -> int:
+    """moe_dtype of a tensor (int16: bf16 bit patterns)."""
+    d = _DTYPES.get(str(t.dtype))
+    if d is None:
+        raise ValueError(f"{name}: {t.dtype}, expected bfloat16, int16 (bf16 bits), float16 or float32")
+    return d
+
+
+def _rows(name: str, t):
+    """(rows, columns, elements between rows) of a 2-D CUDA tensor with contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: elements of a row are {step} apart, expected 1")
+    return rows, cols, (ld if rows > 1 else cols)
+
+
+def moe_mx_scale_bytes(E: int, N: int, K: int) -> int:
+    return int(lib().moe_mx_scale_bytes(E, N, K))
+
+
+@dataclasses.dataclass
+class MxMat:
+    """A stack of MXFP4 matrices on the device: q uint8 [E][N][K/2] (two codes a byte, the lower column in the low
+    nibble), sp uint8 [E][ceil(N/128)][ceil(K/128)][512] (packed scales, see include/moe_mx.h)."""
+    q: "object"
+    sp: "object"
+
+    @staticmethod
+    def empty(E: int, N: int, K: int, device="cuda") -> "MxMat":
+        """Room for E matrices, e.g. as the result of moe_mx_quantize (E = 1)."""
+        import torch
+        n = moe_mx_scale_bytes(E, N, K)
+        if n == 0:
+            raise ValueError(f"no MXFP4 matrices of E={E}, N={N}, K={K}: K is a positive multiple of 32")
+        return MxMat(torch.empty((E, N, K // 2), dtype=torch.uint8, device=device),
+                     torch.empty((E, -(-N // 128), -(-K // 128), 512), dtype=torch.uint8, device=device))
+
+    @property
+    def shape(self):
+        """(E, N, K)"""
+        E, N, half = self.q.shape
+        return int(E), int(N), 2 * int(half)
+
+    def _c(self) -> _MxMat:
+        c = self.__dict__.get("_cc")
+        if c is None or c[0] is not self.q or c[1] is not self.sp:
+            _tensor("q", self.q, ("uint8",))
+            if self.q.dim() != 3:
+                raise ValueError(f"q: shape {tuple(self.q.shape)}, expected [E][N][K/2]")
+            E, N, K = self.shape
+            _tensor("sp", self.sp, ("uint8",), (E, -(-N // 128), -(-K // 128), 512))
+            c = (self.q, self.sp, _MxMat(_ptr(self.q), _ptr(self.sp)), (E, N, K))
+            self.__dict__["_cc"] = c
+        return c[2]
+
+    def _c_and_shape(self):
+        st = self._c()
+        return st, self.__dict__["_cc"][3]
+
+
+@dataclasses.dataclass
+class MxExperts:
+    """One expert set: gate and up [E][I][d], down [E][d][I]."""
+    gate: MxMat
+    up: MxMat
+    down: MxMat
+
+    def _c_and_sizes(self):
+        """The C struct and (E, I, d)."""
+        c = self.__dict__.get("_cc")
+        g, u, dn = self.gate._c(), self.up._c(), self.down._c()
+        if c is None or c[0] is not g or c[1] is not u or c[2] is not dn:
+            E, I, d = self.gate.shape
+            if self.up.shape != (E, I, d) or self.down.shape != (E, d, I):
+                raise ValueError(f"gate {self.gate.shape}, up {self.up.shape}, down {self.down.shape}: expected "
+                                 f"(E, I, d) twice and (E, d, I)")
+            c = (g, u, dn, _MxExperts(g, u, dn, E), (E, I, d))
+            self.__dict__["_cc"] = c
+        return c[3], c[4]
+
+
+def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Routing, ws, stream=None) -> None:
+    """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
+    _tensor("logits", logits, ("float32",))
+    T, E = logits.shape
+    r = out._c()
+    sc = scoring._c(E)
+    _check("moe_route_scored", lib().moe_route_scored(_ptr(logits), C.byref(sc), T, E, k, block_rows, C.byref(r),
+                                                      _ptr(ws), ws.numel(), _stream(stream)))
+    out.block_rows = r.block_rows
+
+
+def moe_mx_prepack_scales(scale, sp, stream=None) -> None:
+    """scale uint8 [E][N][K/32] (E8M0, row-major) -> sp [E][ceil(N/128)][ceil(K/128)][512]."""
+    _tensor("scale", scale, ("uint8",))
+    E, N, G = scale.shape
+    _tensor("sp", sp, ("uint8",), (E, -(-N // 128), -(-G // 4), 512))
+    _check("moe_mx_prepack_scales", lib().moe_mx_prepack_scales(_ptr(scale), E, N, 32 * G, _ptr(sp), _stream(stream)))
+
+
+def moe_mx_quantize(X, out: MxMat, stream=None) -> None:
+    """X [rows][K] (bf16, fp16 or fp32; rows may be strided) -> out, an MxMat of (1, rows, K)."""
+    rows, K, ld = _rows("X", X)
+    m, shape = out._c_and_shape()
+    if shape != (1, rows, K):
+        raise ValueError(f"out: {shape}, expected (1, {rows}, {K})")
+    _check("moe_mx_quantize", lib().moe_mx_quantize(_ptr(X), _dtype("X", X), rows, K, ld, C.byref(m), _stream(stream)))
+
+
+def moe_mx_dequant(m: MxMat, W, stream=None) -> None:
+    """W (bf16 or fp32, E*N*K elements) = the values of m."""
+    st, (E, N, K) = m._c_and_shape()
+    _tensor("W", W, ("bfloat16", "int16", "float16", "float32"))
+    if W.numel() != E * N * K:
+        raise ValueError(f"W: {W.numel()} elements, expected {E * N * K}")
+    _check("moe_mx_dequant", lib().moe_mx_dequant(C.byref(st), E, N, K, _dtype("W", W), _ptr(W), _stream(stream)))
+
+
+def _y(Y, T: int, N: int) -> int:
+    _tensor("Y", Y, ("bfloat16", "int16", "float16", "float32"), (T, N))
+    return _dtype("Y", Y)
+
+
+def _one(name: str, W: MxMat):
+    st, (E, N, K) = W._c_and_shape()
+    if E != 1:
+        raise ValueError(f"{name}: {E} matrices, expected one")
+    return st, N, K
+
+
+def moe_mx_matmul(A: MxMat, W: MxMat, Y, ws, stream=None) -> None:
+    """Y [M][N] (bf16 or fp32) = A (1, M, K) times W (1, N, K), transposed."""
+    a, M, K = _one("A", A)
+    w, N, Kw = _one("W", W)
+    if K != Kw:
+        raise ValueError(f"A has {K} columns, W {Kw}")
+    _check("moe_mx_matmul", lib().moe_mx_matmul(C.byref(a), M, C.byref(w), N, K, _ptr(Y), _y(Y, M, N), _ptr(ws),
+                                                ws.numel(), _stream(stream)))
+
+
+def moe_mx_linear_workspace_bytes(T: int, N: int, K: int) -> int:
+    return int(lib().moe_mx_linear_workspace_bytes(T, N, K))
+
+
+def moe_mx_linear(X, W: MxMat, Y, ws, stream=None) -> None:
+    """Y [T][N] = MXFP4(X [T][K]) times W (1, N, K), transposed: a linear layer with MXFP4 weights."""
+    T, K, ld = _rows("X", X)
+    w, N, Kw = _one("W", W)
+    if K != Kw:
+        raise ValueError(f"X has {K} columns, W {Kw}")
+    _check("moe_mx_linear", lib().moe_mx_linear(_ptr(X), _dtype("X", X), T, K, ld, C.byref(w), N, _ptr(Y), _y(Y, T, N),
+                                                _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_mx_forward_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
+    return int(lib().moe_mx_forward_workspace_bytes(T, d, I, E, k, I_shared, block_rows))
+
+
+def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
+    """C structs and sizes of an expert call, shapes checked."""
+    _tensor("X", X, ("bfloat16", "int16"))
+    T, d = X.shape
+    re, (E, I, dr) = routed._c_and_sizes()
+    se, I_sh = None, 0
+    if shared is not None:
+        s, (Es, I_sh, ds) = shared._c_and_sizes()
+        if Es != 1 or ds != d:
+            raise ValueError(f"shared: ({Es}, {I_sh}, {ds}), expected one expert of width {d}")
+        se = C.byref(s)
+    if dr != d:
+        raise ValueError(f"X is {d} wide, the experts {dr}")
+    _tensor("Y", Y, ("bfloat16", "int16"), (T, d))
+    return T, d, E, I, I_sh, C.byref(re), se
+
+
+def moe_mx_forward(X, routed: MxExperts, shared: Optional[MxExperts], routing: Routing, Y, ws, stream=None) -> None:
+    """The expert layer on MXFP4 weights, for a routing of moe_route or moe_route_scored."""
+    T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
+    rr = routing._c()
+    _check("moe_mx_forward", lib().moe_mx_forward(_ptr(X), T, d, I, int(routing.ids.shape[1]), re, se, I_sh,
+                                                  C.byref(rr), _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_mx_layer_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
+    return int(lib().moe_mx_layer_workspace_bytes(T, d, I, E, k, I_shared, block_rows))
+
+
+def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optional[MxExperts], k: int, block_rows: int,
+                 out: Routing, Y, ws, stream=None) -> None:
+    """moe_route_scored + moe_mx_forward in one call."""
+    T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
+    _tensor("logits", logits, ("float32",), (T, E))
+    r = out._c()
+    sc = scoring._c(E)
+    _check("moe_mx_layer", lib().moe_mx_layer(_ptr(logits), C.byref(sc), _ptr(X), T, d, I, k, block_rows, re, se, I_sh,
+                                              C.byref(r), _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)))
+    out.block_rows = r.block_rows
+
+
 # ----------------------------------------------------------------------- weight preparation
 
 def moe_dequant_experts(m: QMat, bits: int, W, stream=None) -> None:
@@ -451,3 +734,27 @@ def prepare_experts(ex: dict, device="cuda", stream=None) -> Experts:
         del qd
         mats[name] = QMat(qp, sb)
     return Experts(**mats)
+
+
+def prepare_mx_experts(ex: dict, device="cuda", stream=None) -> MxExperts:
+    """Device copy of one MXFP4 expert set.
+
+    ex maps "gate", "up", "down" to (q, scale): q uint8 [E][N][K/2], scale uint8 E8M0 [E][N][K/32], as NumPy arrays or
+    torch tensors.  The scales are packed once with moe_mx_prepack_scales; the codes are used as they are.
+    """
+    import numpy as np
+    import torch
+
+    def dev(a):
+        return (torch.from_numpy(np.ascontiguousarray(a)) if isinstance(a, np.ndarray) else a).to(device).contiguous()
+
+    mats = {}
+    for name in ("gate", "up", "down"):
+        q, s = (dev(a) for a in ex[name])
+        E, N, G = s.shape
+        if tuple(q.shape) != (E, N, 16 * G):
+            raise ValueError(f"{name}: codes {tuple(q.shape)} do not match scales {tuple(s.shape)}")
+        sp = torch.empty((E, -(-N // 128), -(-G // 4), 512), dtype=torch.uint8, device=device)
+        moe_mx_prepack_scales(s, sp, stream)
+        mats[name] = MxMat(q, sp)
+    return MxExperts(**mats)

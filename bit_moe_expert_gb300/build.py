@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libbitmoe.so")
-SOURCES = ["api.cu", "route.cu", "router.cu", "topk_wide.cu", "decode.cu", "gemm.cu", "profile.cu"]
+SOURCES = ["api.cu", "route.cu", "router.cu", "topk_wide.cu", "decode.cu", "gemm.cu", "mx.cu", "mx_gemm.cu", "mx_api.cu",
+           "profile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -30,7 +31,7 @@ def nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(INCLUDE, "moe.h"), os.path.join(INCLUDE, "moe_profile.h")]
+    files += [os.path.join(INCLUDE, f) for f in ("moe.h", "moe_mx.h", "moe_profile.h")]
     return files
 
 

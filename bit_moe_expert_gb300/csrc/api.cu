@@ -249,6 +249,21 @@ std::mutex g_func_mu;
 
 }  // namespace
 
+// MXFP4 codes of `rows` rows of row_bytes bytes: boxes of one 128-byte line x
+// box_rows rows, 128-byte swizzle (the K-major operand layout of the tensor
+// cores); bytes and rows past the end read as zeros
+bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows) {
+  if (!get_encoder()) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool pdl_enabled() { return env_flag("MOE_PDL", true); }
+
+int device_sms() { return sm_count(); }
+
 cudaError_t set_max_dynamic_smem(const void* func, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -282,6 +297,40 @@ cudaError_t occupancy_per_sm(const void* func, int threads, size_t smem, int* pe
   if (g_func_n < kFuncEntries) g_func[g_func_n++] = FuncEntry{dev, func, threads, smem, n};
   *per_sm = n;
   return cudaSuccess;
+}
+
+moe_status check_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
+                        const moe_routing* out) {
+  if (!out || !sc || T < 0 || E < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxE || k > kMaxK || k > E) return MOE_ERR_UNSUPPORTED;
+  if (block_rows < 1 || block_rows > kMaxBlockRows) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * k > (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+  if (sc->score != MOE_SCORE_SOFTMAX && sc->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (sc->n_group < 1 || E % sc->n_group != 0) return MOE_ERR_INVALID_ARG;
+  if (sc->n_group > 32) return MOE_ERR_UNSUPPORTED;  // one lane per group
+  const int size = E / sc->n_group;
+  if (sc->topk_group < 1 || sc->topk_group > sc->n_group || k > sc->topk_group * size) return MOE_ERR_INVALID_ARG;
+  if (sc->group_top < 1 || sc->group_top > 2 || (sc->n_group > 1 && sc->group_top > size)) return MOE_ERR_INVALID_ARG;
+  if (!(sc->scale - sc->scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // NaN or infinite
+  if (reinterpret_cast<uintptr_t>(sc->bias) & 3u) return MOE_ERR_INVALID_ARG;
+  if (!out->counts || !out->offsets || !out->block_map || !out->num_blocks) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !out->ids || !out->w || !out->perm || !out->inv_perm)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status route_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
+                        moe_routing* out, void* ws, uint32_t* status, moe_stream stream) {
+  out->block_rows = block_rows;
+  const RouteOut o{out->ids,  out->w,        out->counts,    out->offsets,
+                   out->perm, out->inv_perm, out->block_map, out->num_blocks};
+  const RouteScore score{sc->bias,       sc->score == MOE_SCORE_SIGMOID ? 1 : 0,
+                         sc->n_group,    sc->topk_group,
+                         sc->group_top,  sc->renormalize ? 1 : 0,
+                         sc->scale};
+  if (launch_route(logits, T, E, k, block_rows, o, ws, reinterpret_cast<cudaStream_t>(stream), pdl_enabled(), status,
+                   &score) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 }  // namespace bm
@@ -370,6 +419,15 @@ moe_status moe_route(const float* logits, int T, int E, int k, int block_rows, m
   if (launch_route(logits, T, E, k, block_rows, o, ws, reinterpret_cast<cudaStream_t>(stream), pdl) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
+}
+
+moe_status moe_route_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
+                            moe_routing* out, void* ws, size_t ws_bytes, moe_stream stream) {
+  const moe_status st = check_scored(logits, sc, T, E, k, block_rows, out);
+  if (st != MOE_OK) return st;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < moe_route_workspace_bytes(T, E, k))
+    return MOE_ERR_WORKSPACE;
+  return route_scored(logits, sc, T, E, k, block_rows, out, ws, nullptr, stream);
 }
 
 moe_status moe_router_logits(const uint16_t* X, int T, int d, const uint16_t* W_r, int E, float* logits,

@@ -22,6 +22,10 @@ enum KernelKind {
   kKCombine,
   kKPrepack,
   kKTopkWide,  // exact top-K of wide rows
+  kKMxQuantize,  // MXFP4 quantisation (with or without the scatter to the routing's rows)
+  kKMxGemm,      // MXFP4 dense product
+  kKMxGateUp,
+  kKMxDown,
   kKernelKinds
 };
 void timer_begin(int id, cudaStream_t s);
@@ -44,10 +48,19 @@ struct RouteOut {
 cudaError_t set_max_dynamic_smem(const void* func, int bytes);
 cudaError_t occupancy_per_sm(const void* func, int threads, size_t smem, int* per_sm);
 
+// How a row is scored (include/moe.h, moe_scoring).
+struct RouteScore {
+  const float* bias;  // [E] or null
+  int sigmoid, n_group, topk_group, group_top, renormalize;
+  float scale;
+};
+
 size_t route_hist_elems(int T, int E);
-// status: where device-side errors go (null: the workspace header's status word)
+// status: where device-side errors go (null: the workspace header's status word);
+// score: null for the softmax over the selected logits
 cudaError_t launch_route(const float* logits, int T, int E, int k, int block_rows, const RouteOut& out, void* ws,
-                         cudaStream_t stream, bool pdl, uint32_t* status = nullptr);
+                         cudaStream_t stream, bool pdl, uint32_t* status = nullptr,
+                         const RouteScore* score = nullptr);
 cudaError_t launch_prepack_codes(const uint32_t* q, int E, int N, int K, int bits, uint32_t* qp,
                                  cudaStream_t stream);
 cudaError_t launch_prepack(const uint16_t* scale, const uint16_t* bias, int E, int N, int K, uint32_t* sb,
@@ -157,5 +170,86 @@ struct GemmActMaps {
 
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMaps* shared, const GemmActMaps* act,
                         cudaStream_t stream, bool pdl);
+
+// Y[t] = bf16(sum_j w[t][j] ypart[inv_perm[t k + j]] + ypart[T k + t]), the second term with has_shared.
+cudaError_t launch_combine(const float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
+                           bool has_shared, uint16_t* Y, uint32_t* status, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- host helpers of api.cu
+bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows);
+bool pdl_enabled();  // the environment variable MOE_PDL
+int device_sms();    // 0: no device
+// moe_route_scored's checks of everything but the workspace, and its launch (status as for launch_route).
+moe_status check_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
+                        const moe_routing* out);
+moe_status route_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
+                        moe_routing* out, void* ws, uint32_t* status, moe_stream stream);
+
+// ---------------------------------------------------------------- MXFP4
+constexpr int kMxBlock = 32;       // values along K that share a scale
+constexpr int kMxPieceRows = 128;  // one 512-byte piece of packed scales: 128 rows x 4 blocks
+constexpr int kMxPieceK = 128;
+constexpr int kMxPieceBytes = 512;
+inline size_t mx_pieces(long long rows, int K) {
+  return static_cast<size_t>((rows + kMxPieceRows - 1) / kMxPieceRows) * ((K + kMxPieceK - 1) / kMxPieceK);
+}
+
+cudaError_t launch_mx_prepack(const uint8_t* scale, int E, int N, int K, uint8_t* sp, cudaStream_t stream);
+// type: 0 bf16, 1 fp16, 2 fp32
+cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, uint8_t* sp,
+                               int num_sms, cudaStream_t stream, bool pdl);
+cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W, int num_sms,
+                              cudaStream_t stream, bool pdl);
+
+// Where the quantised rows of an expert layer go: assignment a = t k + j to row
+// inv_perm[a], its scales to that row's tile (entry b of the block map holds
+// slot b of the scales, rows counted from the tile's first); with a shared
+// expert token t also to row T k + t, slots max_blocks + t / shared_rows.
+struct MxScatter {
+  const int32_t* inv_perm;
+  const int32_t* block_map;
+  const int32_t* num_blocks;
+  uint32_t* status;
+  int T, k, max_blocks, shared_rows;  // shared_rows = 0: no shared expert
+};
+cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint8_t* q, uint8_t* sp,
+                              cudaStream_t stream, bool pdl);
+
+constexpr int kMxBM = 128;      // rows of the MMA's M operand
+constexpr int kMxStageK = 256;  // K of a pipeline stage: one 128-byte line of codes a row
+constexpr int kMxMaxBN = 128;   // tokens of an expert tile at most
+
+// M operand and N operand as TMA maps of code bytes (128-byte boxes, 128-byte swizzle).
+struct MxLinearArgs {
+  const uint8_t *sp_m, *sp_n;  // packed scales of the M and the N operand
+  void* Y;
+  long long stride_m, stride_n;  // of Y, in elements
+  uint32_t* status;
+  int rows_m, rows_n, K, bn, num_sms;
+  int y_fp32;
+};
+struct MxLinearMaps {
+  CUtensorMap m, n;
+};
+cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cudaStream_t stream, bool pdl);
+
+struct MxExpertArgs {
+  const int32_t* block_map;
+  const int32_t* num_blocks;
+  const uint8_t *sp_gate_r, *sp_up_r, *sp_down_r, *sp_gate_s, *sp_up_s, *sp_down_s;  // weights' packed scales
+  const uint8_t* sp_x;         // X's, by tile slot
+  uint8_t *sp_h_r, *sp_h_s;    // h's: by routed slot, by shared tile
+  uint8_t *q_h_r, *q_h_s;      // h's codes [A][I/2], [T][I_shared/2]
+  float* ypart;                // [A + T][d]
+  uint32_t* status;
+  int T, d, I, k, I_shared, E, num_sms, max_blocks;
+  int bn_r, bn_s;              // tile heights in MMA columns (multiples of 16): routed, shared
+};
+struct MxExpertMaps {
+  CUtensorMap gate_r, up_r, down_r, gate_s, up_s, down_s;  // codes [E * N][K/2], box (128 bytes, 128 rows)
+  CUtensorMap x_r, x_s;        // X's codes [A + T][d/2], box (128 bytes, bn_r / bn_s rows)
+  CUtensorMap h_r, h_s;        // h's codes
+};
+cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream);
 
 }  // namespace bm

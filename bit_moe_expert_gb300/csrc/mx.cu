@@ -1,0 +1,301 @@
+// MXFP4 quantisation and its inverse: 32 consecutive values along K share a
+// power-of-two scale, every value is an E2M1 code (include/moe_mx.h).
+//
+// The scale needs no logarithm: floor(log2 a) of an fp32 magnitude is its
+// exponent field, so the E8M0 byte is that field minus 2 (2 = the exponent of
+// E2M1's largest power of two), and 2^-e is the float whose exponent field is
+// 254 minus the byte.  The multiplication by it is exact (a power of two), so
+// the only rounding is the conversion to E2M1.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace bm {
+namespace {
+
+enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+
+// Eight consecutive values of a row, as loaded and as fp32.
+template <int kType>
+struct Load8 {
+  uint4 v[kType == kFp32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* row, int c) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<size_t>(c) * (kType == kFp32 ? 4 : 2));
+    v[0] = __ldg(p);
+    if constexpr (kType == kFp32) v[1] = __ldg(p + 1);
+  }
+  __device__ __forceinline__ void zero() {
+    v[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (kType == kFp32) v[1] = v[0];
+  }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+    if constexpr (kType == kBf16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    } else if constexpr (kType == kFp16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        f[2 * j] = p.x;
+        f[2 * j + 1] = p.y;
+      }
+    } else {
+      const uint32_t u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[j] = __uint_as_float(w[j]);
+        f[4 + j] = __uint_as_float(u[j]);
+      }
+    }
+  }
+};
+
+// The warp's 256 values, eight a lane (a block is four lanes): the lane's eight
+// codes, and the scale bytes of the lane's half of the warp (four blocks, one
+// 32-bit word).  Lanes past the row's end hold zeros and get the byte 0.
+template <int kType>
+__device__ __forceinline__ uint32_t quantize8(const Load8<kType>& x, uint32_t& scales, int lane) {
+  float f[8];
+  x.floats(f);
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  const uint32_t byte = mx_scale_byte(a);
+  const float inv = mx_inverse_scale(byte);
+  uint32_t code = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) code |= f32x2_to_e2m1x2(f[2 * j] * inv, f[2 * j + 1] * inv) << (8 * j);
+  scales = byte << (8 * ((lane >> 2) & 3));
+  scales |= __shfl_xor_sync(0xffffffffu, scales, 4);
+  scales |= __shfl_xor_sync(0xffffffffu, scales, 8);
+  return code;
+}
+
+// One warp per 256 values of a row, kUnits of them in flight.
+constexpr int kQuantThreads = 256;
+constexpr int kUnits = 4;
+template <int kType>
+__global__ void __launch_bounds__(kQuantThreads)
+    mx_quantize_kernel(const void* __restrict__ X, int rows, int K, long long ldx, uint8_t* __restrict__ q,
+                       uint8_t* __restrict__ sp) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int segs = (K + 255) / 256;
+  const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
+  const long long units = static_cast<long long>(rows) * segs;
+  const long long warps = static_cast<long long>(gridDim.x) * (kQuantThreads / 32);
+  const int esize = kType == kFp32 ? 4 : 2;
+  for (long long u0 = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += warps * kUnits) {
+    Load8<kType> x[kUnits];
+    int row[kUnits], col[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const long long u = u0 + warps * i;
+      row[i] = u < units ? static_cast<int>(u / segs) : -1;
+      col[i] = static_cast<int>(u - static_cast<long long>(row[i]) * segs) * 256 + 8 * lane;
+      if (row[i] >= 0 && col[i] < K)
+        x[i].load(static_cast<const char*>(X) + static_cast<size_t>(row[i]) * ldx * esize, col[i]);
+      else
+        x[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (row[i] < 0) break;  // the same for the whole warp
+      uint32_t scales;
+      const uint32_t code = quantize8(x[i], scales, lane);
+      if (col[i] < K) *reinterpret_cast<uint32_t*>(q + static_cast<size_t>(row[i]) * (K / 2) + col[i] / 2) = code;
+      if ((lane & 15) == 0 && col[i] < K)
+        *reinterpret_cast<uint32_t*>(sp + mx_scale_offset(row[i], col[i] / kMxPieceK, pieces)) = scales;
+    }
+  }
+}
+
+// X's rows quantised once and written to the rows of their assignments: one CTA
+// per token, one warp per 256 values.
+constexpr int kScatterThreads = 256;
+__global__ void __launch_bounds__(kScatterThreads)
+    mx_scatter_kernel(const uint16_t* __restrict__ X, int d, MxScatter s, uint8_t* __restrict__ q,
+                      uint8_t* __restrict__ sp) {
+  __shared__ long long s_row[kMaxK + 1];    // destination rows of the codes, -1: none
+  __shared__ long long s_scale[kMaxK + 1];  // byte offset of piece 0 of the row's scales
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int pieces = (d + kMxPieceK - 1) / kMxPieceK;
+  const int t = blockIdx.x;
+  const int n = s.k + (s.shared_rows > 0 ? 1 : 0);
+  Load8<kBf16> x;
+  int c = (threadIdx.x >> 5) * 256 + 8 * lane;
+  const uint16_t* row = X + static_cast<size_t>(t) * d;
+  if (c < d) x.load(row, c); else x.zero();
+  if (threadIdx.x < n) {
+    const int j = threadIdx.x;
+    long long to = -1, at = 0;
+    if (j == s.k) {
+      to = static_cast<long long>(s.T) * s.k + t;
+      at = mx_scale_offset(t % s.shared_rows, 0, pieces) +
+           static_cast<long long>(s.max_blocks + t / s.shared_rows) * pieces * kMxPieceBytes;
+    } else {
+      const int p = __ldg(s.inv_perm + static_cast<size_t>(t) * s.k + j);
+      // the last tile that starts at or before p
+      int lo = 0, hi = min(max(*s.num_blocks, 0), s.max_blocks);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(s.block_map + 3 * mid + 1) <= p) lo = mid; else hi = mid;
+      }
+      const int r = hi > 0 ? p - __ldg(s.block_map + 3 * lo + 1) : -1;
+      if (p >= 0 && p < s.T * s.k && r >= 0 && r < kMxMaxBN) {
+        to = p;
+        at = mx_scale_offset(r, 0, pieces) + static_cast<long long>(lo) * pieces * kMxPieceBytes;
+      } else {
+        record_status(s.status, MOE_ERR_INVALID_ARG);
+      }
+    }
+    s_row[j] = to;
+    s_scale[j] = at;
+  }
+  __syncthreads();
+  for (int base = 0; base < d; base += 8 * kScatterThreads) {
+    if (base > 0) {
+      c += 8 * kScatterThreads;
+      if (c < d) x.load(row, c); else x.zero();
+    }
+    if (c - 8 * lane >= d) break;  // the same for the whole warp
+    uint32_t scales;
+    const uint32_t code = quantize8(x, scales, lane);
+    for (int j = 0; j < n; ++j) {
+      if (s_row[j] < 0) continue;
+      if (c < d) *reinterpret_cast<uint32_t*>(q + static_cast<size_t>(s_row[j]) * (d / 2) + c / 2) = code;
+      if ((lane & 15) == 0 && c < d)
+        *reinterpret_cast<uint32_t*>(sp + s_scale[j] + static_cast<size_t>(c / kMxPieceK) * kMxPieceBytes) = scales;
+    }
+  }
+}
+
+// Eight values a thread: one 32-bit word of codes and the block's scale byte.
+template <int kType>
+__global__ void __launch_bounds__(kQuantThreads)
+    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int E, int N, int K,
+                      void* __restrict__ W) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int w8 = K / 8;
+  const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
+  const size_t per_expert = static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
+  const size_t total = static_cast<size_t>(E) * N * w8;
+  for (size_t i = blockIdx.x * static_cast<size_t>(kQuantThreads) + threadIdx.x; i < total;
+       i += static_cast<size_t>(gridDim.x) * kQuantThreads) {
+    const size_t en = i / w8;
+    const int c = static_cast<int>(i - en * w8) * 8;
+    const int e = static_cast<int>(en / N);
+    const int n = static_cast<int>(en - static_cast<size_t>(e) * N);
+    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
+    const uint8_t byte =
+        __ldg(sp + e * per_expert + mx_scale_offset(n, c / kMxPieceK, pieces) + (c % kMxPieceK) / kMxBlock);
+    const float s = mx_scale(byte);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = mx_code_value(code >> (4 * j)) * s;
+    if constexpr (kType == kFp32) {
+      float4* p = reinterpret_cast<float4*>(W) + 2 * i;
+      p[0] = make_float4(f[0], f[1], f[2], f[3]);
+      p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      reinterpret_cast<uint4*>(W)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// One thread per 32-bit word of the packed scales: four blocks of one row.
+__global__ void mx_prepack_kernel(const uint8_t* __restrict__ scale, int E, int N, int G, uint8_t* __restrict__ sp) {
+  const int pieces = (G + 3) / 4;
+  const int tiles = (N + kMxPieceRows - 1) / kMxPieceRows;
+  const size_t total = static_cast<size_t>(E) * tiles * pieces * (kMxPieceBytes / 4);
+  for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const int w = static_cast<int>(i % (kMxPieceBytes / 4));  // word 4 (r % 32) + r / 32 of the piece
+    size_t p = i / (kMxPieceBytes / 4);
+    const int piece = static_cast<int>(p % pieces);
+    p /= pieces;
+    const int tile = static_cast<int>(p % tiles);
+    const int e = static_cast<int>(p / tiles);
+    const int n = tile * kMxPieceRows + (w >> 2) + 32 * (w & 3);
+    uint32_t v = 0;
+    for (int b = 0; b < 4; ++b)
+      if (n < N && 4 * piece + b < G)
+        v |= static_cast<uint32_t>(scale[(static_cast<size_t>(e) * N + n) * G + 4 * piece + b]) << (8 * b);
+    reinterpret_cast<uint32_t*>(sp)[i] = v;
+  }
+}
+
+// Programmatic dependent launch of `kernel` where `pdl` allows it.
+template <typename... P, typename... A>
+cudaError_t launch(int kind, void (*kernel)(P...), int grid, int threads, cudaStream_t stream, bool pdl, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  timer_begin(kind, stream);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  timer_end(kind, stream);
+  return err;
+}
+
+int blocks_for(size_t threads, int per_block, int most) {
+  const size_t n = (threads + per_block - 1) / per_block;
+  return static_cast<int>(n < 1 ? 1 : n < static_cast<size_t>(most) ? n : most);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_prepack(const uint8_t* scale, int E, int N, int K, uint8_t* sp, cudaStream_t stream) {
+  const size_t words = static_cast<size_t>(E) * mx_pieces(N, K) * (kMxPieceBytes / 4);
+  return launch(kKPrepack, mx_prepack_kernel, blocks_for(words, 256, 65536), 256, stream, false, scale, E, N,
+                K / kMxBlock, sp);
+}
+
+cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, uint8_t* sp,
+                               int num_sms, cudaStream_t stream, bool pdl) {
+  const size_t units = static_cast<size_t>(rows) * ((K + 255) / 256);
+  const int grid = blocks_for(units, kQuantThreads / 32, num_sms * 8);
+  const auto kernel = type == kBf16 ? mx_quantize_kernel<kBf16>
+                                    : (type == kFp16 ? mx_quantize_kernel<kFp16> : mx_quantize_kernel<kFp32>);
+  return launch(kKMxQuantize, kernel, grid, kQuantThreads, stream, pdl, X, rows, K, ldx, q, sp);
+}
+
+cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W, int num_sms,
+                              cudaStream_t stream, bool pdl) {
+  const size_t words = static_cast<size_t>(E) * N * (K / 8);
+  const int grid = blocks_for(words, kQuantThreads, num_sms * 16);
+  return launch(kKMxQuantize, type == kFp32 ? mx_dequant_kernel<kFp32> : mx_dequant_kernel<kBf16>, grid, kQuantThreads,
+                stream, pdl, q, sp, E, N, K, W);
+}
+
+cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint8_t* q, uint8_t* sp,
+                              cudaStream_t stream, bool pdl) {
+  return launch(kKMxQuantize, mx_scatter_kernel, s.T, kScatterThreads, stream, pdl, X, d, s, q, sp);
+}
+
+}  // namespace bm

@@ -12,7 +12,7 @@ namespace {
 
 const char* const kNames[kKernelKinds] = {"route", "decode", "router", "x_gather",
                                           "gemm_gateup", "gemm_down", "combine", "prepack",
-                                          "topk_wide"};
+                                          "topk_wide", "mx_quantize", "mx_gemm", "mx_gateup", "mx_down"};
 
 struct Pending {
   int id;

@@ -263,6 +263,27 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// D[tmem] (+)= (A scaled) * (B scaled)^T, kind::mxf4: E2M1 operands in shared
+// memory, two codes a byte, one E8M0 scale per 32 values along K (two scales
+// per row of the K = 64 MMA) in tensor memory, fp32 accumulate.
+__device__ __forceinline__ void tc_mma_mxfp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t a_scale_tmem, uint32_t b_scale_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale_tmem), "r"(b_scale_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes of shared memory (32 rows of 16 bytes, contiguous) -> four columns
+// of all four 32-lane quarters of tensor memory: the scales of 128 rows x 4
+// blocks.  Ordered before the MMAs that the same thread issues after it.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // Arrives on the mbarrier once every tcgen05 operation this thread issued
 // before has completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
@@ -282,6 +303,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// Each lane reads 8 consecutive 32-bit columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
 }
 
 // Each lane reads 16 consecutive 32-bit columns of its own TMEM lane.
@@ -306,6 +335,28 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_kmajor(uint32_t start_addr) 
   d |= static_cast<uint64_t>(1) << 46;                       // bits 46-47: descriptor version
   d |= static_cast<uint64_t>(2) << 61;                       // bits 61-63: 128-byte swizzle
   return d;
+}
+
+// Shared-memory descriptor of a 512-byte piece of scales for tc_cp_scales: no
+// swizzle, groups of eight 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t start_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((start_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128 >> 4) << 32;  // stride byte offset / 16
+  d |= static_cast<uint64_t>(1) << 46;         // descriptor version
+  return d;
+}
+
+// Instruction descriptor, kind::mxf4: E2M1 A and B (format code 1), E8M0
+// scales, both operands K-major, K = 64.  The MMA takes the scale bytes
+// `scale_id`, `scale_id` + 1 (0 or 2) of each row's four.
+__host__ __device__ constexpr uint32_t idesc_mxfp(int M, int N, uint32_t scale_id) {
+  return (scale_id << 4)                            // B scales' first byte
+         | (1u << 7) | (1u << 10)                   // A, B: E2M1
+         | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+         | (1u << 23)                               // scales: E8M0
+         | (static_cast<uint32_t>(M >> 4) << 24)    // M / 16
+         | (scale_id << 29);                        // A scales' first byte
 }
 
 // Instruction descriptor, kind::f16: fp16 A and B (format code 0), fp32 D,
@@ -375,6 +426,18 @@ __device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two fp32 values -> two E2M1 codes (round to nearest even, magnitudes above 6
+// to 6) in bits 0..3 (lo) and 4..7 (hi).
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
   return r;
 }
 

@@ -16,6 +16,10 @@
 // that chain: extra CTAs after the routing CTAs select the top k of 8 tokens
 // each again (the same function, so the same selection) and write only the
 // weights; they wait for nothing, so they run beside the routing CTAs.
+//
+// Scored routing (softmax or logistic scores, a bias, groups; kScored): the
+// same kernel with warp_scored_topk as the selection.  Its weights come from
+// fp32 scores that the selection has at hand, so there are no weight CTAs.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -43,23 +47,17 @@ constexpr int kBasesSmemLimit = 96 * 1024;  // per-chunk bases kept in shared me
 constexpr int kWeightTokensPerCta = 8;
 static_assert(kWeightTokensPerCta <= kRouteWarps, "a weight CTA's tokens fit its warps");
 
-constexpr int kRouteMaxDevices = 64;
-struct RouteSetup {
-  bool done;
-  int resident8, resident32;  // CTAs of route_kernel<8>, <32> resident at once (no dynamic shared memory)
-};
-RouteSetup g_route_setup[kRouteMaxDevices] = {};
-std::mutex g_route_setup_mu;
-
-// kPL: logits per lane (E <= 32 * kPL).
-template <int kPL>
+// kPL: logits per lane (E <= 32 * kPL).  kScored: select and weigh by `score`.
+template <int kPL, bool kScored>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __restrict__ logits, int T, int E,
                                                               int k, int block_rows, RouteOut out,
                                                               WsHeader* hdr, uint32_t* status,
                                                               int32_t* __restrict__ chunk_hist,
                                                               int32_t* __restrict__ local_rank, int bases_in_smem,
-                                                              int gridsync, int nroute) {
-  extern __shared__ int32_t s_bases[];  // [nchunks][E] exclusive per-chunk bases (last CTA, when they fit)
+                                                              int gridsync, int nroute, RouteScore score) {
+  // [nchunks][E] exclusive per-chunk bases (last CTA, when they fit), or, before them, each warp's E values
+  // (scored routing with groups)
+  extern __shared__ int32_t s_bases[];
   __shared__ int32_t s_ids[kRouteTokensPerCta * kMaxK];
   __shared__ int32_t s_rank[kRouteTokensPerCta * kMaxK];
   __shared__ int32_t s_cnt[kMaxE];
@@ -109,7 +107,25 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
       atomicOr(&s_mask[sel_i], 1u << tl);
     }
   };
-  if constexpr (kPL == 8) {
+  if constexpr (kScored) {
+    float* buf = reinterpret_cast<float*>(s_bases) + warp * E;
+    for (int tl = warp; tl < ntok; tl += kRouteWarps) {
+      const float* row = logits + static_cast<size_t>(t0 + tl) * E;
+      float xv[kPL];
+      if constexpr (kPL == 8) {
+        topk_load_row8(row, E, lane, xv);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kPL; ++c) xv[c] = lane + 32 * c < E ? __ldg(row + lane + 32 * c) : 0.0f;
+      }
+      int sel_i;
+      float sel_w;
+      bool finite;
+      warp_scored_topk<kPL>(xv, score, E, k, lane, buf, sel_i, sel_w, finite);
+      if (lane < k) out.w[static_cast<size_t>(t0 + tl) * k + lane] = sel_w;
+      publish(tl, sel_i, finite);
+    }
+  } else if constexpr (kPL == 8) {
     // both of a warp's rows are in flight before either is selected
     static_assert(kRouteTokensPerCta == 2 * kRouteWarps, "two tokens per warp");
     float xv[2][8];
@@ -354,7 +370,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
 }  // namespace
 
 cudaError_t launch_route(const float* logits, int T, int E, int k, int block_rows, const RouteOut& out,
-                         void* ws, cudaStream_t stream, bool pdl, uint32_t* status) {
+                         void* ws, cudaStream_t stream, bool pdl, uint32_t* status,
+                         const RouteScore* score) {
   WsHeader* hdr = static_cast<WsHeader*>(ws);
   if (!status) status = &hdr->status;
   const int nchunks = T > 0 ? (T + kRouteTokensPerCta - 1) / kRouteTokensPerCta : 1;
@@ -363,47 +380,38 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   const size_t bases_bytes = nchunks > 1 ? static_cast<size_t>(nchunks) * E * 4 : 0;
   const int bases_in_smem = (nchunks > 1 && bases_bytes <= static_cast<size_t>(kBasesSmemLimit)) ? 1 : 0;
 
-  // One-time set-up per device (the dynamic shared-memory limit, and how many
-  // CTAs of each instantiation fit at once), under a lock: host threads may
-  // make their first calls on different devices at the same time.
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kRouteMaxDevices) return cudaErrorInvalidDevice;
-  int resident8 = 0, resident32 = 0;
-  {
-    std::lock_guard<std::mutex> lock(g_route_setup_mu);
-    RouteSetup& su = g_route_setup[dev];
-    if (!su.done) {
-      cudaError_t e1 = cudaFuncSetAttribute(route_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBasesSmemLimit);
-      if (e1 != cudaSuccess) return e1;
-      cudaError_t e2 = cudaFuncSetAttribute(route_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBasesSmemLimit);
-      if (e2 != cudaSuccess) return e2;
-      int sms = 0, per8 = 0, per32 = 0;
-      if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per8, route_kernel<8>, kRouteThreads, 0) == cudaSuccess &&
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per32, route_kernel<32>, kRouteThreads, 0) == cudaSuccess) {
-        su.resident8 = sms * per8;
-        su.resident32 = sms * per32;
-      }
-      su.done = true;
-    }
-    resident8 = su.resident8;
-    resident32 = su.resident32;
-  }
+  const RouteScore sc = score ? *score : RouteScore{};
+  const auto kernel = score ? (E <= 256 ? route_kernel<8, true> : route_kernel<32, true>)
+                            : (E <= 256 ? route_kernel<8, false> : route_kernel<32, false>);
+  const size_t group_bytes = score && score->n_group > 1 ? static_cast<size_t>(kRouteWarps) * E * 4 : 0;
+
+  // CTAs resident at once, without the bases (the grid-synchronised mode has none).
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kBasesSmemLimit);
+  if (e != cudaSuccess) return e;
+  e = occupancy_per_sm(reinterpret_cast<const void*>(kernel), kRouteThreads, group_bytes, &per_sm);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int resident = sms * per_sm;
   // Grid-synchronised mode when every chunk's CTA can be resident at once
   // (leaving room for other work); otherwise the last CTA finishes alone.
   // MOE_ROUTE_MODE=ticket or =gridsync forces one of them (A/B and tests; a
   // forced grid-synchronised launch still needs every CTA resident, so it is
   // only taken when they fit).
-  int gridsync = (nchunks > 1 && nchunks <= (E <= 256 ? resident8 : resident32) / 2) ? 1 : 0;
+  int gridsync = (nchunks > 1 && nchunks <= resident / 2) ? 1 : 0;
   if (const char* m = std::getenv("MOE_ROUTE_MODE")) {
     if (!std::strcmp(m, "ticket")) gridsync = 0;
-    if (!std::strcmp(m, "gridsync") && nchunks > 1 && nchunks <= (E <= 256 ? resident8 : resident32)) gridsync = 1;
+    if (!std::strcmp(m, "gridsync") && nchunks > 1 && nchunks <= resident) gridsync = 1;
   }
-  const int nweight = (T + kWeightTokensPerCta - 1) / kWeightTokensPerCta;  // weight CTAs
+  const int nweight = score ? 0 : (T + kWeightTokensPerCta - 1) / kWeightTokensPerCta;  // weight CTAs
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nchunks + nweight);
   cfg.blockDim = dim3(kRouteThreads);
   cfg.dynamicSmemBytes = (bases_in_smem && !gridsync) ? bases_bytes : 0;
+  if (cfg.dynamicSmemBytes < group_bytes) cfg.dynamicSmemBytes = group_bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -412,10 +420,8 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   cfg.numAttrs = 1;
   timer_begin(kKRoute, stream);
   const cudaError_t err =
-      E <= 256 ? cudaLaunchKernelEx(&cfg, route_kernel<8>, logits, T, E, k, block_rows, out, hdr, status,
-                                    chunk_hist, local_rank, bases_in_smem && !gridsync, gridsync, nchunks)
-               : cudaLaunchKernelEx(&cfg, route_kernel<32>, logits, T, E, k, block_rows, out, hdr, status,
-                                    chunk_hist, local_rank, bases_in_smem && !gridsync, gridsync, nchunks);
+      cudaLaunchKernelEx(&cfg, kernel, logits, T, E, k, block_rows, out, hdr, status, chunk_hist, local_rank,
+                         bases_in_smem && !gridsync, gridsync, nchunks, sc);
   timer_end(kKRoute, stream);
   return err;
 }

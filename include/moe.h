@@ -203,6 +203,46 @@ size_t moe_route_workspace_bytes(int T, int E, int k);
 moe_status moe_route(const float* logits, int T, int E, int k, int block_rows, moe_routing* out,
                      void* ws, size_t ws_bytes, moe_stream stream);
 
+/* ------------------------------------------------------------------ routing by scores
+ * How moe_route_scored turns a token's logits l into a selection and weights:
+ *   score    s_e = softmax_e(l), or the logistic function of l_e
+ *   choice   c_e = s_e + bias[e]; without a bias the order of the logits
+ *            themselves (both scores are monotone)
+ *   groups   with n_group > 1 the experts form n_group runs of E/n_group; a
+ *            group's value is the sum of its group_top (1 or 2) largest choices
+ *            (scores, without a bias), and only the topk_group groups of the
+ *            largest value (the lower group among equals) are selected from
+ *   top-k    the k largest choices of those, descending, the lower expert
+ *            first among equals
+ *   weights  the scores (not the choices) of the selection, divided by their
+ *            sum if `renormalize` is set, times `scale`
+ * A logit of -infinity masks its expert: score 0, behind every other expert in
+ * the order.  Where masked experts have to be selected (fewer than k others)
+ * their weight is 0, and a token with nothing but masked experts has weights 0.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  moe_score score;
+  const float* bias; /* fp32 [E] on the device, or NULL */
+  int n_group;       /* 1: no groups */
+  int topk_group;
+  int group_top;     /* 1 or 2 */
+  int renormalize;
+  float scale;
+} moe_scoring;
+
+/* moe_route with these scores: same logits, outputs, workspace
+ * (moe_route_workspace_bytes), limits and errors.  Scores, choices and weights
+ * are in fp32, so the order of choices closer than its rounding is open, but the
+ * same for the same row in every call.  Also required: n_group >= 1 divides E,
+ * 1 <= topk_group <= n_group, group_top 1 or 2 and at most E/n_group, k <=
+ * topk_group * E/n_group (else MOE_ERR_INVALID_ARG); n_group <= 32 (else
+ * MOE_ERR_UNSUPPORTED); scale finite.  A NaN or +infinity among the logits, or a
+ * NaN in the bias, counts as a masked expert and records MOE_ERR_NONFINITE. */
+moe_status moe_route_scored(const float* logits, const moe_scoring* scoring, int T, int E, int k, int block_rows,
+                            moe_routing* out, void* ws, size_t ws_bytes, moe_stream stream);
+
 /* ------------------------------------------------------------------ routing without a workspace
  * moe_route_noalloc: no counterpart on the source pages.  It computes exactly
  * what moe_route computes, into the same caller-owned output arrays, for
