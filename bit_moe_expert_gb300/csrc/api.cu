@@ -323,10 +323,14 @@ moe_status route_scored(const float* logits, const moe_scoring* sc, int T, int E
   out->block_rows = block_rows;
   const RouteOut o{out->ids,  out->w,        out->counts,    out->offsets,
                    out->perm, out->inv_perm, out->block_map, out->num_blocks};
-  const RouteScore score{sc->bias,       sc->score == MOE_SCORE_SIGMOID ? 1 : 0,
-                         sc->n_group,    sc->topk_group,
-                         sc->group_top,  sc->renormalize ? 1 : 0,
-                         sc->scale};
+  RouteScore score{};
+  score.bias = sc->bias;
+  score.sigmoid = sc->score == MOE_SCORE_SIGMOID;
+  score.n_group = sc->n_group;
+  score.topk_group = sc->topk_group;
+  score.group_top = sc->group_top;
+  score.renormalize = sc->renormalize != 0;
+  score.scale = sc->scale;
   if (launch_route(logits, T, E, k, block_rows, o, ws, reinterpret_cast<cudaStream_t>(stream), pdl_enabled(), status,
                    &score) != cudaSuccess)
     return MOE_ERR_CUDA;

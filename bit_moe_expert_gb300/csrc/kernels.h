@@ -48,11 +48,20 @@ struct RouteOut {
 cudaError_t set_max_dynamic_smem(const void* func, int bytes);
 cudaError_t occupancy_per_sm(const void* func, int threads, size_t smem, int* per_sm);
 
+// x / n for 0 <= x, n <= 1024 as (x * small_inverse(n)) >> 20: with m = ceil(2^20 / n), x m / 2^20 exceeds x / n by
+// x (m n - 2^20) / (2^20 n) < 1/n, since x (n - 1) < 2^20.
+inline uint32_t small_inverse(int n) { return ((1u << 20) + n - 1) / n; }
+
 // How a row is scored (include/moe.h, moe_scoring).
 struct RouteScore {
   const float* bias;  // [E] or null
   int sigmoid, n_group, topk_group, group_top, renormalize;
   float scale;
+  // set by launch_route, so that the kernel divides nothing:
+  int per_lane;     // experts per lane: lane l holds per_lane l .. per_lane l + per_lane - 1
+  int group_size;   // E / n_group
+  int group_shift;  // every group is 2^group_shift whole lanes; -1 where it is not
+  uint32_t group_inv;  // small_inverse(group_size)
 };
 
 size_t route_hist_elems(int T, int E);

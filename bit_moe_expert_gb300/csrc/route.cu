@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kGridsyncChunks = 2047;       // chunks of a grid-synchronised launch: their counts are summed in 16 bits
 constexpr int kBasesSmemLimit = 96 * 1024;  // per-chunk bases kept in shared memory up to this size
 // Tokens per weight CTA (one per warp; the CTA's other warps leave at once).
 // fp64 is slow on this GPU and shared by an SM's warps: 8 tokens per CTA
@@ -47,6 +48,12 @@ constexpr int kBasesSmemLimit = 96 * 1024;  // per-chunk bases kept in shared me
 constexpr int kWeightTokensPerCta = 8;
 static_assert(kWeightTokensPerCta <= kRouteWarps, "a weight CTA's tokens fit its warps");
 
+// Shared memory of one warp of scored routing.
+__host__ __device__ inline int scored_bytes(const RouteScore& score, int E) {
+  const int floats = score.n_group > 1 && score.group_shift < 0 ? E : 0;
+  return static_cast<int>(sizeof(ScoredList)) + (4 * floats + 15) / 16 * 16;
+}
+
 // kPL: logits per lane (E <= 32 * kPL).  kScored: select and weigh by `score`.
 template <int kPL, bool kScored>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __restrict__ logits, int T, int E,
@@ -54,9 +61,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
                                                               WsHeader* hdr, uint32_t* status,
                                                               int32_t* __restrict__ chunk_hist,
                                                               int32_t* __restrict__ local_rank, int bases_in_smem,
-                                                              int gridsync, int nroute, RouteScore score) {
-  // [nchunks][E] exclusive per-chunk bases (last CTA, when they fit), or, before them, each warp's E values
-  // (scored routing with groups)
+                                                              int gridsync, int nroute, int tokens, uint32_t k_inv,
+                                                              RouteScore score) {
+  // [nchunks][E] exclusive per-chunk bases (last CTA, when they fit), or, before them, each warp's
+  // ScoredList (scored routing)
   extern __shared__ int32_t s_bases[];
   __shared__ int32_t s_ids[kRouteTokensPerCta * kMaxK];
   __shared__ int32_t s_rank[kRouteTokensPerCta * kMaxK];
@@ -64,10 +72,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
   __shared__ uint32_t s_mask[kMaxE];  // tokens of the chunk (bit = token within the chunk) that chose expert e
   __shared__ int32_t s_off[kMaxE + 1];
   __shared__ int32_t s_boff[kMaxE + 1];
-  __shared__ int32_t s_part[2][kRouteThreads];
+  __shared__ int32_t s_part[2][kRouteWarps];
   __shared__ int32_t s_base[kMaxE];  // grid-synchronised mode: this chunk's base within each expert
   __shared__ int s_is_last;
 
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) s_mask[e] = 0u;
+  // The launch's parameters are read before the wait: each 64-byte line of them
+  // is a miss of several hundred cycles at its first use.
+  asm volatile("" ::"l"(logits), "l"(out.ids), "l"(out.w), "l"(out.counts), "l"(out.offsets), "l"(out.perm),
+               "l"(out.inv_perm), "l"(out.block_map), "l"(out.num_blocks), "l"(hdr), "l"(status));
+  asm volatile("" ::"r"(T), "r"(E), "r"(k), "r"(block_rows), "r"(gridsync), "r"(nroute), "l"(score.bias),
+               "r"(score.n_group), "r"(score.group_shift));
   pdl_wait();  // the previous kernel on the stream may still own our outputs
   pdl_launch_dependents();
 
@@ -75,8 +90,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
   const int lane = threadIdx.x & 31;
   const int chunk = blockIdx.x;
   const int nchunks = nroute;
-  const int t0 = chunk * kRouteTokensPerCta;
-  const int ntok = max(0, min(kRouteTokensPerCta, T - t0));
+  const int t0 = chunk * tokens;
+  const int ntok = max(0, min(tokens, T - t0));
   const int A = T * k;
 
   if (chunk >= nroute) {
@@ -94,8 +109,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
     return;
   }
 
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) s_mask[e] = 0u;
-  __syncthreads();
+  __syncthreads();  // s_mask is clear
 
   // ---- top-k, one warp per token
   static_assert(kRouteTokensPerCta <= 32, "a chunk's tokens are the bits of one word");
@@ -108,22 +122,18 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
     }
   };
   if constexpr (kScored) {
-    float* buf = reinterpret_cast<float*>(s_bases) + warp * E;
+    ScoredList* list = reinterpret_cast<ScoredList*>(reinterpret_cast<char*>(s_bases) + warp * scored_bytes(score, E));
     for (int tl = warp; tl < ntok; tl += kRouteWarps) {
-      const float* row = logits + static_cast<size_t>(t0 + tl) * E;
-      float xv[kPL];
-      if constexpr (kPL == 8) {
-        topk_load_row8(row, E, lane, xv);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kPL; ++c) xv[c] = lane + 32 * c < E ? __ldg(row + lane + 32 * c) : 0.0f;
-      }
-      int sel_i;
-      float sel_w;
-      bool finite;
-      warp_scored_topk<kPL>(xv, score, E, k, lane, buf, sel_i, sel_w, finite);
-      if (lane < k) out.w[static_cast<size_t>(t0 + tl) * k + lane] = sel_w;
-      publish(tl, sel_i, finite);
+      float x[kPL], b[kPL];
+      scored_load<kPL>(logits + static_cast<size_t>(t0 + tl) * E, score.bias, E, score.per_lane, lane, x, b);
+      const bool finite = warp_scored_topk<kPL>(x, b, score, E, k, lane, list, [&](int j, int e, float w) {
+        const int a = tl * k + j;
+        out.ids[static_cast<size_t>(t0) * k + a] = e;
+        out.w[static_cast<size_t>(t0) * k + a] = w;
+        s_ids[a] = e;
+        atomicOr(&s_mask[e], 1u << tl);
+      });
+      if (!finite && lane == 0) record_status(status, MOE_ERR_NONFINITE);
     }
   } else if constexpr (kPL == 8) {
     // both of a warp's rows are in flight before either is selected
@@ -162,7 +172,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
   // chunk that chose e
   const int na = ntok * k;
   for (int a = threadIdx.x; a < na; a += kRouteThreads) {
-    const int tl = a / k;
+    const int tl = static_cast<int>((a * k_inv) >> 20);
     s_rank[a] = __popc(s_mask[s_ids[a]] & ((1u << tl) - 1u));
   }
   for (int e = threadIdx.x; e < E; e += kRouteThreads) s_cnt[e] = __popc(s_mask[e]);
@@ -172,7 +182,20 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
     // Every CTA is resident (the launch is sized for it): publish this chunk's
     // counts, wait for every chunk (bounded spin), then each CTA derives the
     // totals and its own chunk's bases and places its own assignments.
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) chunk_hist[static_cast<size_t>(chunk) * E + e] = s_cnt[e];
+    // A chunk's counts are at most 32: one byte each, four experts a word, so
+    // that 128 chunks of 256 experts are 32 KB and 16 words a thread (as int32
+    // the same sums took 8,700 cycles instead of 1,500).  They lie in the room
+    // of chunk_hist and local_rank, which this mode has no other use for.
+    const int words = (E + 3) / 4;
+    uint32_t* hist = reinterpret_cast<uint32_t*>(chunk_hist);
+    for (int w = threadIdx.x; w < words; w += kRouteThreads) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * w + i < E) v |= static_cast<uint32_t>(s_cnt[4 * w + i]) << (8 * i);
+      hist[static_cast<size_t>(chunk) * words + w] = v;
+    }
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) s_base[e] = 0;
     __syncthreads();
     if (threadIdx.x == 0) {
       atom_add_acq_rel_gpu(&hdr->ticket, 1u);
@@ -185,21 +208,44 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
       }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-      int run = 0, mine = 0;
-      for (int c0 = 0; c0 < nchunks; c0 += 32) {  // 32 loads in flight per round trip
-        int h[32];
+    {
+      // every thread sums one word's column over a share of the chunks: all of
+      // them, and those before this chunk, 16 bits an expert (kGridsyncChunks x
+      // 32 stays below 2^16)
+      const int groups = kRouteThreads / words;  // at least 2: E <= 1024
+      const int w = threadIdx.x % words, g = threadIdx.x / words;
+      if (g < groups) {
+        uint32_t all[2] = {0, 0}, mine[2] = {0, 0};
+        for (int c0 = g; c0 < nchunks; c0 += 16 * groups) {  // 16 loads in flight per round trip
+          uint32_t h[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          h[i] = (c0 + i < nchunks) ? __ldcg(chunk_hist + static_cast<size_t>(c0 + i) * E + e) : 0;
+          for (int i = 0; i < 16; ++i) {
+            const int c = c0 + i * groups;
+            h[i] = c < nchunks ? __ldcg(hist + static_cast<size_t>(c) * words + w) : 0u;
+          }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (c0 + i == chunk) mine = run;
-          run += h[i];
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t even = h[i] & 0x00FF00FFu, odd = (h[i] >> 8) & 0x00FF00FFu;
+            all[0] += even;
+            all[1] += odd;
+            if (c0 + i * groups < chunk) {
+              mine[0] += even;
+              mine[1] += odd;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = (all[i & 1] >> (8 * (i & 2))) & 0xFFFFu, m = (mine[i & 1] >> (8 * (i & 2))) & 0xFFFFu;
+          if (4 * w + i < E) atomicAdd(reinterpret_cast<uint32_t*>(&s_base[4 * w + i]), a | (m << 16));
         }
       }
-      s_cnt[e] = run;
-      s_base[e] = mine;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      const uint32_t v = static_cast<uint32_t>(s_base[e]);
+      s_cnt[e] = static_cast<int>(v & 0xFFFFu);
+      s_base[e] = static_cast<int>(v >> 16);
     }
     __syncthreads();
   } else if (nchunks > 1) {
@@ -244,14 +290,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
 
   // ---- exclusive scans over experts: row offsets and tile offsets
   {
-    const int per = (E + kRouteThreads - 1) / kRouteThreads;
+    static_assert(kMaxE <= 2 * kRouteThreads, "at most two experts a thread");
+    const int per = E <= kRouteThreads ? 1 : 2;
     const int lo = threadIdx.x * per;
-    const int hi = min(E, lo + per);
-    int rs = 0, bs = 0;
-    for (int e = lo; e < hi; ++e) {
-      rs += s_cnt[e];
-      bs += (s_cnt[e] + block_rows - 1) / block_rows;
+    int cnt[2], tiles[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      cnt[i] = i < per && lo + i < E ? s_cnt[lo + i] : 0;
+      tiles[i] = (cnt[i] + block_rows - 1) / block_rows;
     }
+    int rs = cnt[0] + cnt[1], bs = tiles[0] + tiles[1];
     // warp-level inclusive scans of the per-thread sums, then across warps
     int ir = rs, ib = bs;
 #pragma unroll
@@ -268,37 +316,24 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
       s_part[1][warp] = ib;
     }
     __syncthreads();
-    if (warp == 0) {
-      int wr = lane < kRouteWarps ? s_part[0][lane] : 0;
-      int wb = lane < kRouteWarps ? s_part[1][lane] : 0;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int r2 = __shfl_up_sync(0xffffffffu, wr, off);
-        const int b2 = __shfl_up_sync(0xffffffffu, wb, off);
-        if (lane >= off) {
-          wr += r2;
-          wb += b2;
-        }
-      }
-      if (lane < kRouteWarps) {
-        s_part[0][kRouteWarps + lane] = wr;  // inclusive totals per warp
-        s_part[1][kRouteWarps + lane] = wb;
-      }
-    }
-    __syncthreads();
-    const int wbase_r = warp > 0 ? s_part[0][kRouteWarps + warp - 1] : 0;
-    const int wbase_b = warp > 0 ? s_part[1][kRouteWarps + warp - 1] : 0;
+    // sums of the warps before this one, and of all (kRouteWarps <= 32)
+    const int pr = lane < kRouteWarps ? s_part[0][lane] : 0, pb = lane < kRouteWarps ? s_part[1][lane] : 0;
+    const int wbase_r = __reduce_add_sync(0xffffffffu, lane < warp ? pr : 0);
+    const int wbase_b = __reduce_add_sync(0xffffffffu, lane < warp ? pb : 0);
     rs = wbase_r + ir - rs;  // exclusive prefix of this thread's slice
     bs = wbase_b + ib - bs;
-    for (int e = lo; e < hi; ++e) {
-      s_off[e] = rs;
-      s_boff[e] = bs;
-      rs += s_cnt[e];
-      bs += (s_cnt[e] + block_rows - 1) / block_rows;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i < per && lo + i < E) {
+        s_off[lo + i] = rs;
+        s_boff[lo + i] = bs;
+      }
+      rs += cnt[i];
+      bs += tiles[i];
     }
     if (threadIdx.x == kRouteThreads - 1) {
-      s_off[E] = s_part[0][2 * kRouteWarps - 1];
-      s_boff[E] = s_part[1][2 * kRouteWarps - 1];
+      s_off[E] = wbase_r + ir;  // the last thread's inclusive sums
+      s_boff[E] = wbase_b + ib;
     }
   }
   __syncthreads();
@@ -380,10 +415,18 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   const size_t bases_bytes = nchunks > 1 ? static_cast<size_t>(nchunks) * E * 4 : 0;
   const int bases_in_smem = (nchunks > 1 && bases_bytes <= static_cast<size_t>(kBasesSmemLimit)) ? 1 : 0;
 
-  const RouteScore sc = score ? *score : RouteScore{};
+  RouteScore sc = score ? *score : RouteScore{};
+  if (score) {
+    sc.per_lane = (E + 31) / 32;
+    sc.group_size = E / sc.n_group;
+    sc.group_inv = small_inverse(sc.group_size);
+    sc.group_shift = -1;
+    for (int i = 0; i < 6; ++i)
+      if (sc.group_size == sc.per_lane << i) sc.group_shift = i;
+  }
   const auto kernel = score ? (E <= 256 ? route_kernel<8, true> : route_kernel<32, true>)
                             : (E <= 256 ? route_kernel<8, false> : route_kernel<32, false>);
-  const size_t group_bytes = score && score->n_group > 1 ? static_cast<size_t>(kRouteWarps) * E * 4 : 0;
+  const size_t scored_smem = score ? static_cast<size_t>(kRouteWarps) * scored_bytes(sc, E) : 0;
 
   // CTAs resident at once, without the bases (the grid-synchronised mode has none).
   int dev = 0, sms = 0, per_sm = 0;
@@ -391,7 +434,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   if (e != cudaSuccess) return e;
   e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kBasesSmemLimit);
   if (e != cudaSuccess) return e;
-  e = occupancy_per_sm(reinterpret_cast<const void*>(kernel), kRouteThreads, group_bytes, &per_sm);
+  e = occupancy_per_sm(reinterpret_cast<const void*>(kernel), kRouteThreads, scored_smem, &per_sm);
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
@@ -401,17 +444,27 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   // MOE_ROUTE_MODE=ticket or =gridsync forces one of them (A/B and tests; a
   // forced grid-synchronised launch still needs every CTA resident, so it is
   // only taken when they fit).
-  int gridsync = (nchunks > 1 && nchunks <= resident / 2) ? 1 : 0;
+  int gridsync = (nchunks > 1 && nchunks <= kGridsyncChunks && nchunks <= resident / 2) ? 1 : 0;
   if (const char* m = std::getenv("MOE_ROUTE_MODE")) {
     if (!std::strcmp(m, "ticket")) gridsync = 0;
-    if (!std::strcmp(m, "gridsync") && nchunks > 1 && nchunks <= resident) gridsync = 1;
+    if (!std::strcmp(m, "gridsync") && nchunks > 1 && nchunks <= kGridsyncChunks && nchunks <= resident) gridsync = 1;
   }
   const int nweight = score ? 0 : (T + kWeightTokensPerCta - 1) / kWeightTokensPerCta;  // weight CTAs
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nchunks + nweight);
+  // Scored routing, grid-synchronised: one token per warp instead of two where
+  // twice the CTAs still fit.  Selection is a chain of latencies, so a second
+  // token per warp costs as much as the first (777 tokens of 130 experts: 8.5
+  // against 11.0 us).
+  int tokens = kRouteTokensPerCta, nroute = nchunks;
+  const int nhalf = (T + kRouteWarps - 1) / kRouteWarps;
+  if (score && gridsync && nhalf <= kGridsyncChunks && nhalf <= resident / 2) {
+    tokens = kRouteWarps;
+    nroute = nhalf;
+  }
+  cfg.gridDim = dim3(nroute + nweight);
   cfg.blockDim = dim3(kRouteThreads);
   cfg.dynamicSmemBytes = (bases_in_smem && !gridsync) ? bases_bytes : 0;
-  if (cfg.dynamicSmemBytes < group_bytes) cfg.dynamicSmemBytes = group_bytes;
+  if (cfg.dynamicSmemBytes < scored_smem) cfg.dynamicSmemBytes = scored_smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -421,7 +474,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   timer_begin(kKRoute, stream);
   const cudaError_t err =
       cudaLaunchKernelEx(&cfg, kernel, logits, T, E, k, block_rows, out, hdr, status, chunk_hist, local_rank,
-                         bases_in_smem && !gridsync, gridsync, nchunks, sc);
+                         bases_in_smem && !gridsync, gridsync, nroute, tokens, small_inverse(k), sc);
   timer_end(kKRoute, stream);
   return err;
 }

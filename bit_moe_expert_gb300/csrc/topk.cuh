@@ -42,37 +42,6 @@ __device__ __forceinline__ void topk_load_row8(const float* __restrict__ row, in
   }
 }
 
-// k rounds over the lanes' eight values each (see warp_topk_select_sorted_vals;
-// 0 is no candidate): lane j < k receives the key and the expert of round j.
-__device__ __forceinline__ void warp_topk_rounds8(uint64_t (&v)[8], int k, int lane, uint32_t& sel_key, int& sel_i) {
-  constexpr int kNet[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
-                               {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
-#pragma unroll
-  for (int c = 0; c < 19; ++c) {
-    const uint64_t a = v[kNet[c][0]], b = v[kNet[c][1]];
-    v[kNet[c][0]] = a > b ? a : b;
-    v[kNet[c][1]] = a > b ? b : a;
-  }
-  sel_key = 0;
-  sel_i = 0;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t hk = static_cast<uint32_t>(v[0] >> 32);
-    const uint32_t kmax = __reduce_max_sync(0xffffffffu, hk);
-    const unsigned cand = __ballot_sync(0xffffffffu, hk == kmax && v[0] != 0ull);
-    const int win = __ffs(cand) - 1;
-    const uint32_t wlow = __shfl_sync(0xffffffffu, static_cast<uint32_t>(v[0]), win);
-    if (lane == j) {
-      sel_key = kmax;
-      sel_i = static_cast<int>(~wlow);
-    }
-    if (lane == win) {
-#pragma unroll
-      for (int c = 0; c < 7; ++c) v[c] = v[c + 1];
-      v[7] = 0ull;
-    }
-  }
-}
-
 // Selection for E <= 256 from the lanes' loaded logits: lane l holds experts
 // 8l .. 8l+7 as 64-bit values (key << 32 | ~expert), so a larger value is a
 // larger logit or, for equal logits, a lower expert; it sorts them once (a
@@ -90,8 +59,32 @@ __device__ __forceinline__ void warp_topk_select_sorted_vals(const float (&xv)[8
     v[c] = e < E ? (static_cast<uint64_t>(topk_key(xv[c])) << 32) | static_cast<uint32_t>(~e) : 0ull;
   }
   all_finite = __all_sync(0xffffffffu, finite);
-  uint32_t sel_key;
-  warp_topk_rounds8(v, k, lane, sel_key, sel_i);
+  constexpr int kNet[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                               {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+  for (int c = 0; c < 19; ++c) {
+    const uint64_t a = v[kNet[c][0]], b = v[kNet[c][1]];
+    v[kNet[c][0]] = a > b ? a : b;
+    v[kNet[c][1]] = a > b ? b : a;
+  }
+  uint32_t sel_key = 0;
+  sel_i = 0;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t hk = static_cast<uint32_t>(v[0] >> 32);
+    const uint32_t kmax = __reduce_max_sync(0xffffffffu, hk);
+    const unsigned cand = __ballot_sync(0xffffffffu, hk == kmax && v[0] != 0ull);
+    const int win = __ffs(cand) - 1;
+    const uint32_t wlow = __shfl_sync(0xffffffffu, static_cast<uint32_t>(v[0]), win);
+    if (lane == j) {
+      sel_key = kmax;
+      sel_i = static_cast<int>(~wlow);
+    }
+    if (lane == win) {
+#pragma unroll
+      for (int c = 0; c < 7; ++c) v[c] = v[c + 1];
+      v[7] = 0ull;
+    }
+  }
   sel_v = topk_key_value(sel_key);
 }
 
@@ -100,35 +93,6 @@ __device__ __forceinline__ void warp_topk_select_sorted(const float* __restrict_
   float xv[8];
   topk_load_row8(row, E, lane, xv);
   warp_topk_select_sorted_vals(xv, E, k, lane, sel_i, sel_v, all_finite);
-}
-
-// The same for E <= 32 * kPL with expert lane + 32 c at key[c]; a set bit c of
-// `taken` is no candidate.
-template <int kPL>
-__device__ __forceinline__ void warp_topk_rounds_wide(const uint32_t (&key)[kPL], uint32_t taken, int k, int lane,
-                                                      uint32_t& sel_key, int& sel_i) {
-  sel_key = 0;  // lane j keeps the j-th selected key
-  sel_i = 0;
-  for (int j = 0; j < k; ++j) {
-    // lane-local best: largest key, lowest index among equal keys
-    uint32_t bk = 0;
-    int bi = 0x7FFFFFFF;
-#pragma unroll
-    for (int c = 0; c < kPL; ++c) {
-      if (!((taken >> c) & 1u) && (key[c] > bk || bi == 0x7FFFFFFF)) {
-        bk = key[c];
-        bi = lane + 32 * c;
-      }
-    }
-    const uint32_t kmax = __reduce_max_sync(0xffffffffu, bi == 0x7FFFFFFF ? 0u : bk);
-    const int win = static_cast<int>(
-        __reduce_min_sync(0xffffffffu, (bi != 0x7FFFFFFF && bk == kmax) ? static_cast<uint32_t>(bi) : 0xFFFFFFFFu));
-    if ((win & 31) == lane) taken |= 1u << (win >> 5);
-    if (lane == j) {
-      sel_key = kmax;
-      sel_i = win;
-    }
-  }
 }
 
 // Selection.  row: E <= 32 * kPL fp32 logits.  On return lane j < k holds the
@@ -159,8 +123,28 @@ __device__ __forceinline__ void warp_topk_select(const float* __restrict__ row, 
   }
   all_finite = __all_sync(0xffffffffu, finite);
 
-  uint32_t sel_key;
-  warp_topk_rounds_wide<kPL>(key, taken, k, lane, sel_key, sel_i);
+  uint32_t sel_key = 0;  // lane j keeps the j-th selected key
+  sel_i = 0;
+  for (int j = 0; j < k; ++j) {
+    // lane-local best: largest key, lowest index among equal keys
+    uint32_t bk = 0;
+    int bi = 0x7FFFFFFF;
+#pragma unroll
+    for (int c = 0; c < kPL; ++c) {
+      if (!((taken >> c) & 1u) && (key[c] > bk || bi == 0x7FFFFFFF)) {
+        bk = key[c];
+        bi = lane + 32 * c;
+      }
+    }
+    const uint32_t kmax = __reduce_max_sync(0xffffffffu, bi == 0x7FFFFFFF ? 0u : bk);
+    const int win = static_cast<int>(
+        __reduce_min_sync(0xffffffffu, (bi != 0x7FFFFFFF && bk == kmax) ? static_cast<uint32_t>(bi) : 0xFFFFFFFFu));
+    if ((win & 31) == lane) taken |= 1u << (win >> 5);
+    if (lane == j) {
+      sel_key = kmax;
+      sel_i = win;
+    }
+  }
   // back from key to float
   const uint32_t su = (sel_key & 0x80000000u) ? (sel_key & 0x7FFFFFFFu) : ~sel_key;
   sel_v = __uint_as_float(su);
@@ -183,46 +167,69 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) { return topk_key_value(__reduce_max_sync(0xffffffffu, topk_key(v))); }
 
-// The expert at position c of a lane's kPL logits (the layouts of the two
-// selections above).
+// Shared memory of a warp that selects by scores: the list of candidates, then,
+// where groups do not fall on whole lanes (group_shift -1), E floats.
+struct ScoredList {
+  uint2 key_e[32];
+  float s[32];
+};
+
+// A row's logits and the bias, in flight together (-infinity and 0 past E).
 template <int kPL>
-__device__ __forceinline__ int lane_expert(int lane, int c) {
-  return kPL == 8 ? 8 * lane + c : lane + 32 * c;
+__device__ __forceinline__ void scored_load(const float* __restrict__ row, const float* __restrict__ bias, int E,
+                                            int pl, int lane, float (&x)[kPL], float (&b)[kPL]) {
+  if (kPL == 8 && E == 256 && ((reinterpret_cast<uintptr_t>(row) | reinterpret_cast<uintptr_t>(bias)) & 15u) == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(row) + 2 * lane + h);
+      const float4 u = bias ? __ldg(reinterpret_cast<const float4*>(bias) + 2 * lane + h) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+      b[4 * h] = u.x, b[4 * h + 1] = u.y, b[4 * h + 2] = u.z, b[4 * h + 3] = u.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < kPL; ++c) {
+    const int e = pl * lane + c;
+    const bool in = c < pl && e < E;
+    x[c] = in ? __ldcg(row + e) : -INFINITY;
+    b[c] = in && bias ? __ldg(bias + e) : 0.0f;
+  }
 }
 
-// Selection and weights of one row by scores: xv holds the lane's logits
-// (anything past E).  On return lane j < k holds the j-th expert and its weight;
-// every lane learns whether the row and the bias had no NaN and no +infinity.
-// buf: E floats of shared memory of this warp's own, used with groups only.
+// Selection and weights of one row by scores (include/moe.h, moe_scoring), x
+// and b from scored_load.  Calls publish(j, expert, weight) once for every slot
+// j < k, each in some lane; returns whether the row and the bias had no NaN and
+// no +infinity.
 //
-// Groups: the values go to shared memory and lane g reads group g's, each lane
-// starting at another place of its run so that runs of 32 do not meet in one
-// bank.  With 8 groups of 32 that is 32 loads for the two largest of every
-// group, where a reduction over the lanes' registers takes ten shuffles a group
-// and value.
-template <int kPL>
-__device__ __forceinline__ void warp_scored_topk(const float (&xv)[kPL], const RouteScore& sc, int E, int k, int lane,
-                                                 float* buf, int& sel_i, float& sel_w, bool& all_ok) {
+// No serial rounds over k: the k-th largest of the lanes' own maxima bounds the
+// k-th largest choice from below, so the experts at or above it (about k to 2k
+// of them) go to a list in shared memory, and each lane counts for one of them
+// how many come before it.  k rounds of a maximum over the warp took 3,400
+// cycles of a token's 8,400 with k = 8; more than 32 candidates (k close to 32,
+// or many equal choices) still take them.
+template <int kPL, typename Publish>
+__device__ __forceinline__ bool warp_scored_topk(const float (&x)[kPL], const float (&b)[kPL], const RouteScore& sc,
+                                                 int E, int k, int lane, ScoredList* list, Publish publish) {
   const float kNone = -INFINITY;
-  float s[kPL];         // scores
-  float choice[kPL];
+  const uint32_t kAll = 0xffffffffu;
+  const int pl = sc.per_lane;
+  float s[kPL], choice[kPL];
   bool ok = true;
   float mx = kNone;
 #pragma unroll
   for (int c = 0; c < kPL; ++c) {
-    const bool in = lane_expert<kPL>(lane, c) < E;
-    const bool bad = in && !(xv[c] < INFINITY);
+    const bool bad = !(x[c] < INFINITY);
     ok &= !bad;
-    choice[c] = in && !bad ? xv[c] : kNone;  // the logit, -infinity for a masked expert
+    choice[c] = bad ? kNone : x[c];  // the logit, -infinity for a masked expert
     mx = fmaxf(mx, choice[c]);
   }
   if (sc.sigmoid) {
 #pragma unroll
-    for (int c = 0; c < kPL; ++c) s[c] = 1.0f / (1.0f + expf(-choice[c]));  // exp(inf) = inf: a masked expert gets 0
+    for (int c = 0; c < kPL; ++c) s[c] = __fdividef(1.0f, 1.0f + expf(-choice[c]));  // a masked expert: 1 / inf
   } else {
-    mx = warp_max(mx);
+    mx = topk_key_value(__reduce_max_sync(kAll, topk_key(mx)));
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < kPL; ++c) {
@@ -230,89 +237,152 @@ __device__ __forceinline__ void warp_scored_topk(const float (&xv)[kPL], const R
       sum += s[c];
     }
     sum = warp_sum(sum);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
 #pragma unroll
     for (int c = 0; c < kPL; ++c) s[c] *= inv;
   }
   if (sc.bias) {
 #pragma unroll
     for (int c = 0; c < kPL; ++c) {
-      const int e = lane_expert<kPL>(lane, c);
-      if (e < E) {
-        const float b = __ldg(sc.bias + e);
-        const float v = s[c] + b;
-        ok &= v == v;
-        choice[c] = choice[c] > kNone && v == v ? v : kNone;
-      }
+      const float v = s[c] + b[c];
+      ok &= v == v;
+      choice[c] = choice[c] > kNone && v == v ? v : kNone;
     }
   }
-  all_ok = __all_sync(0xffffffffu, ok);
+  ok = __all_sync(kAll, ok);
 
-  uint32_t kept = 0xffffffffu;  // groups that are selected from
-  const int gsize = E / sc.n_group;
+  uint32_t kept = kAll;  // groups that are selected from
+  const int size = sc.group_size;
+  const bool whole = sc.group_shift >= 0;
   if (sc.n_group > 1) {
+    // group g's value ends up in lane g (smem) or in all of its lanes
+    float m1 = kNone, m2 = kNone, mine;
+    int group, shift;
+    if (whole) {
 #pragma unroll
-    for (int c = 0; c < kPL; ++c) {
-      const int e = lane_expert<kPL>(lane, c);
-      if (e < E) buf[e] = sc.bias || !(choice[c] > kNone) ? choice[c] : s[c];
-    }
-    __syncwarp();
-    float m1 = kNone, m2 = kNone;
-    if (lane < sc.n_group) {
-      int i = lane % gsize;
-      for (int n = 0; n < gsize; ++n) {
-        const float v = buf[lane * gsize + i];
+      for (int c = 0; c < kPL; ++c) {
+        const float v = sc.bias || !(choice[c] > kNone) ? choice[c] : s[c];
         m2 = fmaxf(m2, fminf(m1, v));
         m1 = fmaxf(m1, v);
-        if (++i == gsize) i = 0;
+      }
+      for (int off = 1; off < (1 << sc.group_shift); off <<= 1) {
+        const float o1 = __shfl_xor_sync(kAll, m1, off), o2 = __shfl_xor_sync(kAll, m2, off);
+        m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+        m1 = fmaxf(m1, o1);
+      }
+      group = lane >> sc.group_shift;
+      shift = sc.group_shift;
+    } else {
+      float* buf = reinterpret_cast<float*>(list + 1);
+#pragma unroll
+      for (int c = 0; c < kPL; ++c) {
+        const int e = pl * lane + c;
+        if (c < pl && e < E) buf[e] = sc.bias || !(choice[c] > kNone) ? choice[c] : s[c];
+      }
+      __syncwarp();
+      if (lane < sc.n_group) {
+        // each lane starts at another place of its run, so that runs of 32 do not meet in one bank
+        int i = lane % size;
+        for (int n = 0; n < size; ++n) {
+          const float v = buf[lane * size + i];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+          if (++i == size) i = 0;
+        }
+      }
+      group = lane;
+      shift = 0;
+    }
+    mine = sc.group_top == 2 && m2 > kNone ? m1 + m2 : m1;
+    int rank = 0;
+    for (int g0 = 0; g0 < sc.n_group; g0 += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = __shfl_sync(kAll, mine, (g0 + i) << shift);
+        if (g0 + i < sc.n_group) rank += (v > mine || (v == mine && g0 + i < group)) ? 1 : 0;
       }
     }
-    const float mine = sc.group_top == 2 && m2 > kNone ? m1 + m2 : m1;
-    int rank = 0;
-    for (int g = 0; g < sc.n_group; ++g) {
-      const float v = __shfl_sync(0xffffffffu, mine, g);
-      rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
-    }
-    kept = __ballot_sync(0xffffffffu, lane < sc.n_group && rank < sc.topk_group);
-    __syncwarp();  // buf may be written for the next row
+    kept = __ballot_sync(kAll, group < sc.n_group && rank < sc.topk_group);
   }
 
-  uint32_t sel_key;
-  if constexpr (kPL == 8) {
-    uint64_t v[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int e = 8 * lane + c;
-      const bool in = e < E && (sc.n_group == 1 || ((kept >> (e / gsize)) & 1u));
-      v[c] = in ? (static_cast<uint64_t>(topk_key(choice[c])) << 32) | static_cast<uint32_t>(~e) : 0ull;
-    }
-    warp_topk_rounds8(v, k, lane, sel_key, sel_i);
-  } else {
-    uint32_t key[kPL], taken = 0;
-#pragma unroll
-    for (int c = 0; c < kPL; ++c) {
-      const int e = lane + 32 * c;
-      const bool in = e < E && (sc.n_group == 1 || ((kept >> (e / gsize)) & 1u));
-      key[c] = topk_key(choice[c]);
-      if (!in) taken |= 1u << c;
-    }
-    warp_topk_rounds_wide<kPL>(key, taken, k, lane, sel_key, sel_i);
-  }
-
-  const int owner = kPL == 8 ? sel_i >> 3 : sel_i & 31;
-  const int at = kPL == 8 ? sel_i & 7 : sel_i >> 5;
-  float w = 0.0f;
+  // keys: 0 for an expert that cannot be selected (a choice's key is never 0)
+  uint32_t key[kPL];
+  uint32_t lane_max = 0;
 #pragma unroll
   for (int c = 0; c < kPL; ++c) {
-    const float v = __shfl_sync(0xffffffffu, s[c], owner);
-    if (at == c) w = v;
+    const int e = pl * lane + c;
+    bool in = c < pl && e < E;
+    if (sc.n_group > 1) in = in && ((kept >> (whole ? lane : (e * sc.group_inv) >> 20)) & 1u);
+    key[c] = in ? topk_key(choice[c]) : 0u;
+    lane_max = max(lane_max, key[c]);
   }
-  if (lane >= k) w = 0.0f;
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) above += __shfl_sync(kAll, lane_max, j) > lane_max ? 1 : 0;
+  const uint32_t theta = max(1u, __reduce_min_sync(kAll, above < k ? lane_max : kAll));
+
+  int n = 0;
+#pragma unroll
+  for (int c = 0; c < kPL; ++c) {
+    const bool is = key[c] >= theta;
+    const uint32_t m = __ballot_sync(kAll, is);
+    const int at = n + __popc(m & ((1u << lane) - 1u));
+    if (is && at < 32) {
+      list->key_e[at] = make_uint2(key[c], static_cast<uint32_t>(pl * lane + c));
+      list->s[at] = s[c];
+    }
+    n += __popc(m);
+  }
+  if (n > 32) {
+    // k rounds: the largest key, the lowest expert among equals
+    uint32_t sel_e = 0;
+    float sel_s = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int c = 0; c < kPL; ++c) best = max(best, key[c]);
+      const uint32_t top = __reduce_max_sync(kAll, best);
+      const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;  // the lowest lane holds the lowest experts
+      uint32_t e = 0;
+      float es = 0.0f;
+      bool found = lane != owner;
+#pragma unroll
+      for (int c = 0; c < kPL; ++c) {
+        if (!found && key[c] == top) {
+          found = true;
+          e = pl * lane + c;
+          es = s[c];
+          key[c] = 0;
+        }
+      }
+      e = __shfl_sync(kAll, e, owner);
+      es = __shfl_sync(kAll, es, owner);
+      if (lane == j) sel_e = e, sel_s = es;
+    }
+    __syncwarp();
+    if (lane < k) {
+      list->key_e[lane] = make_uint2(static_cast<uint32_t>(32 - lane), sel_e);  // in order already
+      list->s[lane] = sel_s;
+    }
+    n = k;
+  }
+  __syncwarp();
+  const uint2 me = lane < n ? list->key_e[lane] : make_uint2(0u, 0u);
+  float w = lane < n ? list->s[lane] : 0.0f;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint2 o = list->key_e[j];
+    rank += (o.x > me.x || (o.x == me.x && o.y < me.y)) ? 1 : 0;
+  }
+  const bool selected = lane < n && rank < k;
+  if (!selected) w = 0.0f;
   if (sc.renormalize) {
     const float sum = warp_sum(w);
-    w = sum > 0.0f ? w / sum : 0.0f;
+    w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
   }
-  sel_w = w * sc.scale;
+  if (selected) publish(rank, static_cast<int>(me.y), w * sc.scale);
+  __syncwarp();  // the list may be written for the next row
+  return ok;
 }
 
 }  // namespace bm
