@@ -459,41 +459,50 @@ class Scoring:
     scale: float = 1.0
 
     def _c(self, E: int) -> _Scoring:
-        key = (self.score, self.bias, self.n_group, self.topk_group, self.group_top, self.renormalize, self.scale, E)
+        # rebuilt only when a field changed
         c = self.__dict__.get("_cc")
-        if c is None or c[0][1] is not key[1] or c[0][0] != key[0] or c[0][2:] != key[2:]:
+        key = (self.score, self.n_group, self.topk_group, self.group_top, self.renormalize, self.scale, E)
+        if c is None or c[0] is not self.bias or c[1] != key:
             if self.score not in SCORES:
                 raise ValueError(f"score {self.score!r}: one of {sorted(SCORES)}")
             if self.bias is not None:
-                _tensor("bias", self.bias, ("float32",), (E,))
+                _tensor("bias", self.bias, (_FP32,), (E,))
             top = 1 if self.n_group == 1 else self.group_top
-            c = (key, _Scoring(SCORES[self.score], _ptr(self.bias), self.n_group, self.topk_group, top,
-                               1 if self.renormalize else 0, self.scale))
+            c = (self.bias, key, _Scoring(SCORES[self.score], _ptr(self.bias), self.n_group, self.topk_group, top,
+                                          1 if self.renormalize else 0, self.scale))
             self.__dict__["_cc"] = c
-        return c[1]
+        return c[2]
 
 
-def _tensor(name: str, t, dtypes, shape=None) -> None:
-    """A contiguous CUDA tensor of one of the types and, where given, of the shape."""
-    if str(t.dtype)[6:] not in dtypes:  # "torch.float32" -> "float32"
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(dtypes)}")
+_BF16, _FP16, _FP32, _U8 = 0, 1, 2, 3  # the first three as moe_dtype
+_DTYPE_NAMES = {"bfloat16": _BF16, "int16": _BF16, "float16": _FP16, "float32": _FP32, "uint8": _U8}
+_dtype_codes = {}  # torch.dtype -> code, filled as types are met
+
+
+def _code(t) -> int:
+    """The type code of a tensor (int16 stands for bf16 bit patterns), -1 for another type."""
+    d = t.dtype
+    c = _dtype_codes.get(d)
+    if c is None:
+        c = _dtype_codes[d] = _DTYPE_NAMES.get(str(d)[6:], -1)  # "torch.float32" -> "float32"
+    return c
+
+
+def _tensor(name: str, t, codes, shape=None) -> int:
+    """The type code of t, a contiguous CUDA tensor of one of the types and, where given, of the shape."""
+    c = _code(t)
+    if c not in codes:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(n for n, v in _DTYPE_NAMES.items() if v in codes)}")
     if not t.is_cuda:
         raise ValueError(f"{name}: on {t.device}, expected a CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return c
 
 
-_DTYPES = {"torch.bfloat16": 0, "torch.int16": 0, "torch.float16": 1, "torch.float32": 2}
-
-
-def _dtype(name: str, t) -> int:
-    """moe_dtype of a tensor (int16: bf16 bit patterns)."""
-    d = _DTYPES.get(str(t.dtype))
-    if d is None:
-        raise ValueError(f"{name}: {t.dtype}, expected bfloat16, int16 (bf16 bits), float16 or float32")
-    return d
+_FLOATS = (_BF16, _FP16, _FP32)
 
 
 def _rows(name: str, t):
@@ -501,6 +510,8 @@ def _rows(name: str, t):
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name}: expected a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
     rows, cols = t.shape
+    if _code(t) not in _FLOATS:
+        raise ValueError(f"{name}: {t.dtype}, expected bfloat16, int16 (bf16 bits), float16 or float32")
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name}: elements of a row are {step} apart, expected 1")
@@ -537,11 +548,11 @@ class MxMat:
     def _c(self) -> _MxMat:
         c = self.__dict__.get("_cc")
         if c is None or c[0] is not self.q or c[1] is not self.sp:
-            _tensor("q", self.q, ("uint8",))
+            _tensor("q", self.q, (_U8,))
             if self.q.dim() != 3:
                 raise ValueError(f"q: shape {tuple(self.q.shape)}, expected [E][N][K/2]")
             E, N, K = self.shape
-            _tensor("sp", self.sp, ("uint8",), (E, -(-N // 128), -(-K // 128), 512))
+            _tensor("sp", self.sp, (_U8,), (E, -(-N // 128), -(-K // 128), 512))
             c = (self.q, self.sp, _MxMat(_ptr(self.q), _ptr(self.sp)), (E, N, K))
             self.__dict__["_cc"] = c
         return c[2]
@@ -560,21 +571,22 @@ class MxExperts:
 
     def _c_and_sizes(self):
         """The C struct and (E, I, d)."""
+        # rebuilt only when a matrix or one of its tensors was replaced (identity checks only)
         c = self.__dict__.get("_cc")
-        g, u, dn = self.gate._c(), self.up._c(), self.down._c()
-        if c is None or c[0] is not g or c[1] is not u or c[2] is not dn:
-            E, I, d = self.gate.shape
-            if self.up.shape != (E, I, d) or self.down.shape != (E, d, I):
-                raise ValueError(f"gate {self.gate.shape}, up {self.up.shape}, down {self.down.shape}: expected "
-                                 f"(E, I, d) twice and (E, d, I)")
-            c = (g, u, dn, _MxExperts(g, u, dn, E), (E, I, d))
+        g, u, dn = self.gate, self.up, self.down
+        if (c is None or c[0] is not g or c[1] is not u or c[2] is not dn or c[3] is not g.q or c[4] is not g.sp
+                or c[5] is not u.q or c[6] is not u.sp or c[7] is not dn.q or c[8] is not dn.sp):
+            E, I, d = g.shape
+            if u.shape != (E, I, d) or dn.shape != (E, d, I):
+                raise ValueError(f"gate {g.shape}, up {u.shape}, down {dn.shape}: expected (E, I, d) twice and (E, d, I)")
+            c = (g, u, dn, g.q, g.sp, u.q, u.sp, dn.q, dn.sp, _MxExperts(g._c(), u._c(), dn._c(), E), (E, I, d))
             self.__dict__["_cc"] = c
-        return c[3], c[4]
+        return c[9], c[10]
 
 
 def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Routing, ws, stream=None) -> None:
     """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
-    _tensor("logits", logits, ("float32",))
+    _tensor("logits", logits, (_FP32,))
     T, E = logits.shape
     r = out._c()
     sc = scoring._c(E)
@@ -585,9 +597,9 @@ def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Rou
 
 def moe_mx_prepack_scales(scale, sp, stream=None) -> None:
     """scale uint8 [E][N][K/32] (E8M0, row-major) -> sp [E][ceil(N/128)][ceil(K/128)][512]."""
-    _tensor("scale", scale, ("uint8",))
+    _tensor("scale", scale, (_U8,))
     E, N, G = scale.shape
-    _tensor("sp", sp, ("uint8",), (E, -(-N // 128), -(-G // 4), 512))
+    _tensor("sp", sp, (_U8,), (E, -(-N // 128), -(-G // 4), 512))
     _check("moe_mx_prepack_scales", lib().moe_mx_prepack_scales(_ptr(scale), E, N, 32 * G, _ptr(sp), _stream(stream)))
 
 
@@ -597,21 +609,16 @@ def moe_mx_quantize(X, out: MxMat, stream=None) -> None:
     m, shape = out._c_and_shape()
     if shape != (1, rows, K):
         raise ValueError(f"out: {shape}, expected (1, {rows}, {K})")
-    _check("moe_mx_quantize", lib().moe_mx_quantize(_ptr(X), _dtype("X", X), rows, K, ld, C.byref(m), _stream(stream)))
+    _check("moe_mx_quantize", lib().moe_mx_quantize(_ptr(X), _code(X), rows, K, ld, C.byref(m), _stream(stream)))
 
 
 def moe_mx_dequant(m: MxMat, W, stream=None) -> None:
     """W (bf16 or fp32, E*N*K elements) = the values of m."""
     st, (E, N, K) = m._c_and_shape()
-    _tensor("W", W, ("bfloat16", "int16", "float16", "float32"))
+    t = _tensor("W", W, _FLOATS)
     if W.numel() != E * N * K:
         raise ValueError(f"W: {W.numel()} elements, expected {E * N * K}")
-    _check("moe_mx_dequant", lib().moe_mx_dequant(C.byref(st), E, N, K, _dtype("W", W), _ptr(W), _stream(stream)))
-
-
-def _y(Y, T: int, N: int) -> int:
-    _tensor("Y", Y, ("bfloat16", "int16", "float16", "float32"), (T, N))
-    return _dtype("Y", Y)
+    _check("moe_mx_dequant", lib().moe_mx_dequant(C.byref(st), E, N, K, t, _ptr(W), _stream(stream)))
 
 
 def _one(name: str, W: MxMat):
@@ -627,7 +634,7 @@ def moe_mx_matmul(A: MxMat, W: MxMat, Y, ws, stream=None) -> None:
     w, N, Kw = _one("W", W)
     if K != Kw:
         raise ValueError(f"A has {K} columns, W {Kw}")
-    _check("moe_mx_matmul", lib().moe_mx_matmul(C.byref(a), M, C.byref(w), N, K, _ptr(Y), _y(Y, M, N), _ptr(ws),
+    _check("moe_mx_matmul", lib().moe_mx_matmul(C.byref(a), M, C.byref(w), N, K, _ptr(Y), _tensor("Y", Y, _FLOATS, (M, N)), _ptr(ws),
                                                 ws.numel(), _stream(stream)))
 
 
@@ -641,7 +648,7 @@ def moe_mx_linear(X, W: MxMat, Y, ws, stream=None) -> None:
     w, N, Kw = _one("W", W)
     if K != Kw:
         raise ValueError(f"X has {K} columns, W {Kw}")
-    _check("moe_mx_linear", lib().moe_mx_linear(_ptr(X), _dtype("X", X), T, K, ld, C.byref(w), N, _ptr(Y), _y(Y, T, N),
+    _check("moe_mx_linear", lib().moe_mx_linear(_ptr(X), _code(X), T, K, ld, C.byref(w), N, _ptr(Y), _tensor("Y", Y, _FLOATS, (T, N)),
                                                 _ptr(ws), ws.numel(), _stream(stream)))
 
 
@@ -651,7 +658,7 @@ def moe_mx_forward_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_sha
 
 def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
     """C structs and sizes of an expert call, shapes checked."""
-    _tensor("X", X, ("bfloat16", "int16"))
+    _tensor("X", X, (_BF16,))
     T, d = X.shape
     re, (E, I, dr) = routed._c_and_sizes()
     se, I_sh = None, 0
@@ -662,7 +669,7 @@ def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
         se = C.byref(s)
     if dr != d:
         raise ValueError(f"X is {d} wide, the experts {dr}")
-    _tensor("Y", Y, ("bfloat16", "int16"), (T, d))
+    _tensor("Y", Y, (_BF16,), (T, d))
     return T, d, E, I, I_sh, C.byref(re), se
 
 
@@ -682,7 +689,7 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
                  out: Routing, Y, ws, stream=None) -> None:
     """moe_route_scored + moe_mx_forward in one call."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
-    _tensor("logits", logits, ("float32",), (T, E))
+    _tensor("logits", logits, (_FP32,), (T, E))
     r = out._c()
     sc = scoring._c(E)
     _check("moe_mx_layer", lib().moe_mx_layer(_ptr(logits), C.byref(sc), _ptr(X), T, d, I, k, block_rows, re, se, I_sh,

@@ -259,6 +259,35 @@ struct MxExpertMaps {
   CUtensorMap x_r, x_s;        // X's codes [A + T][d/2], box (128 bytes, bn_r / bn_s rows)
   CUtensorMap h_r, h_s;        // h's codes
 };
+// Few tokens (at most kMxFewT): the activations are quantised inside the products.
+constexpr int kMxFewT = 32;
+struct MxFewLinearArgs {
+  const void* X;       // [T][K], rows ldx elements apart
+  const uint8_t* sp;   // packed scales of W [N][K]
+  void* Y;             // [T][N]
+  uint32_t* status;
+  long long ldx;
+  int T, N, K, y_fp32;
+};
+bool mx_few_linear_fits(int T, int K);
+// type of X as for launch_mx_quantize; w: codes of W, box (128 bytes, 128 rows)
+cudaError_t launch_mx_few_linear(const MxFewLinearArgs& a, int type, const CUtensorMap& w, cudaStream_t stream, bool pdl);
+
+struct MxFewArgs {
+  const uint16_t* X;         // [T][d] bf16
+  const int32_t *perm, *inv_perm, *block_map, *num_blocks;
+  const float* w;            // [T][k]
+  const uint8_t *sp_gate_r, *sp_up_r, *sp_down_r, *sp_gate_s, *sp_up_s, *sp_down_s;
+  float* gu;                 // [A + T][2][max(I, I_shared)]: gate and up of every row
+  float* ypart;              // [A + T][d]
+  uint16_t* Y;               // [T][d] bf16
+  uint32_t* arrived;         // [ceil(d / 128)] arrival counters, zero between calls
+  uint32_t* status;
+  int T, d, I, k, I_shared, E, max_blocks, bn;  // bn: MMA columns of a tile
+};
+bool mx_few_fits(int T, int d, int I, int I_shared);
+cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl);
+
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream);
 
 }  // namespace bm

@@ -17,73 +17,34 @@
 namespace bm {
 namespace {
 
-enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+// One warp per 256 values of a row, kUnits of them in flight.
+constexpr int kQuantThreads = 256;
+constexpr int kUnits = 4;
 
-// Eight consecutive values of a row, as loaded and as fp32.
-template <int kType>
-struct Load8 {
-  uint4 v[kType == kFp32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* row, int c) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<size_t>(c) * (kType == kFp32 ? 4 : 2));
-    v[0] = __ldg(p);
-    if constexpr (kType == kFp32) v[1] = __ldg(p + 1);
+// The rows and 256-value segments that a warp of the grid takes in turn.
+struct RowWalk {
+  long long row;
+  int seg;
+  int segs, row_step, seg_step;
+  __device__ __forceinline__ explicit RowWalk(int K) {
+    segs = (K + 255) / 256;
+    const int first = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
+    const int warps = gridDim.x * (kQuantThreads / 32);
+    row = first / segs;
+    seg = first % segs;
+    row_step = warps / segs;
+    seg_step = warps % segs;
   }
-  __device__ __forceinline__ void zero() {
-    v[0] = make_uint4(0, 0, 0, 0);
-    if constexpr (kType == kFp32) v[1] = v[0];
-  }
-  __device__ __forceinline__ void floats(float (&f)[8]) const {
-    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-    if constexpr (kType == kBf16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    } else if constexpr (kType == kFp16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        f[2 * j] = p.x;
-        f[2 * j + 1] = p.y;
-      }
-    } else {
-      const uint32_t u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[j] = __uint_as_float(w[j]);
-        f[4 + j] = __uint_as_float(u[j]);
-      }
+  __device__ __forceinline__ void next() {
+    row += row_step;
+    seg += seg_step;
+    if (seg >= segs) {
+      seg -= segs;
+      ++row;
     }
   }
 };
 
-// The warp's 256 values, eight a lane (a block is four lanes): the lane's eight
-// codes, and the scale bytes of the lane's half of the warp (four blocks, one
-// 32-bit word).  Lanes past the row's end hold zeros and get the byte 0.
-template <int kType>
-__device__ __forceinline__ uint32_t quantize8(const Load8<kType>& x, uint32_t& scales, int lane) {
-  float f[8];
-  x.floats(f);
-  uint32_t a = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  const uint32_t byte = mx_scale_byte(a);
-  const float inv = mx_inverse_scale(byte);
-  uint32_t code = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) code |= f32x2_to_e2m1x2(f[2 * j] * inv, f[2 * j + 1] * inv) << (8 * j);
-  scales = byte << (8 * ((lane >> 2) & 3));
-  scales |= __shfl_xor_sync(0xffffffffu, scales, 4);
-  scales |= __shfl_xor_sync(0xffffffffu, scales, 8);
-  return code;
-}
-
-// One warp per 256 values of a row, kUnits of them in flight.
-constexpr int kQuantThreads = 256;
-constexpr int kUnits = 4;
 template <int kType>
 __global__ void __launch_bounds__(kQuantThreads)
     mx_quantize_kernel(const void* __restrict__ X, int rows, int K, long long ldx, uint8_t* __restrict__ q,
@@ -91,27 +52,25 @@ __global__ void __launch_bounds__(kQuantThreads)
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int segs = (K + 255) / 256;
   const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
-  const long long units = static_cast<long long>(rows) * segs;
-  const long long warps = static_cast<long long>(gridDim.x) * (kQuantThreads / 32);
   const int esize = kType == kFp32 ? 4 : 2;
-  for (long long u0 = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); u0 < units; u0 += warps * kUnits) {
+  RowWalk at(K);
+  while (at.row < rows) {
     Load8<kType> x[kUnits];
-    int row[kUnits], col[kUnits];
+    long long row[kUnits];
+    int col[kUnits];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const long long u = u0 + warps * i;
-      row[i] = u < units ? static_cast<int>(u / segs) : -1;
-      col[i] = static_cast<int>(u - static_cast<long long>(row[i]) * segs) * 256 + 8 * lane;
-      if (row[i] >= 0 && col[i] < K)
+    for (int i = 0; i < kUnits; ++i, at.next()) {
+      row[i] = at.row;
+      col[i] = at.seg * 256 + 8 * lane;
+      if (row[i] < rows && col[i] < K)
         x[i].load(static_cast<const char*>(X) + static_cast<size_t>(row[i]) * ldx * esize, col[i]);
       else
         x[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      if (row[i] < 0) break;  // the same for the whole warp
+      if (row[i] >= rows) break;  // the same for the whole warp
       uint32_t scales;
       const uint32_t code = quantize8(x[i], scales, lane);
       if (col[i] < K) *reinterpret_cast<uint32_t*>(q + static_cast<size_t>(row[i]) * (K / 2) + col[i] / 2) = code;
@@ -183,42 +142,53 @@ __global__ void __launch_bounds__(kScatterThreads)
   }
 }
 
-// Eight values a thread: one 32-bit word of codes and the block's scale byte.
+// The same division of work: one warp per 256 values, eight a lane.
 template <int kType>
 __global__ void __launch_bounds__(kQuantThreads)
-    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int E, int N, int K,
+    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int N, int K, long long rows,
                       void* __restrict__ W) {
   pdl_wait();
   pdl_launch_dependents();
-  const int w8 = K / 8;
+  const int lane = threadIdx.x & 31;
   const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
   const size_t per_expert = static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
-  const size_t total = static_cast<size_t>(E) * N * w8;
-  for (size_t i = blockIdx.x * static_cast<size_t>(kQuantThreads) + threadIdx.x; i < total;
-       i += static_cast<size_t>(gridDim.x) * kQuantThreads) {
-    const size_t en = i / w8;
-    const int c = static_cast<int>(i - en * w8) * 8;
-    const int e = static_cast<int>(en / N);
-    const int n = static_cast<int>(en - static_cast<size_t>(e) * N);
-    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
-    const uint8_t byte =
-        __ldg(sp + e * per_expert + mx_scale_offset(n, c / kMxPieceK, pieces) + (c % kMxPieceK) / kMxBlock);
-    const float s = mx_scale(byte);
-    float f[8];
+  RowWalk at(K);
+  while (at.row < rows) {
+    uint32_t code[kUnits];
+    uint8_t byte[kUnits];
+    size_t to[kUnits];
+    bool in[kUnits];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = mx_code_value(code >> (4 * j)) * s;
-    if constexpr (kType == kFp32) {
-      float4* p = reinterpret_cast<float4*>(W) + 2 * i;
-      p[0] = make_float4(f[0], f[1], f[2], f[3]);
-      p[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-      uint32_t o[4];
+    for (int i = 0; i < kUnits; ++i, at.next()) {
+      const int c = at.seg * 256 + 8 * lane;
+      in[i] = at.row < rows && c < K;
+      if (!in[i]) continue;
+      const long long e = at.row / N;
+      const int n = static_cast<int>(at.row - e * N);
+      to[i] = static_cast<size_t>(at.row) * (K / 8) + c / 8;
+      code[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + to[i]);
+      byte[i] = __ldg(sp + e * per_expert + mx_scale_offset(n, c / kMxPieceK, pieces) + (c % kMxPieceK) / kMxBlock);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < kUnits; ++i) {
+      if (!in[i]) continue;
+      const float s = mx_scale(byte[i]);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = mx_code_value(code[i] >> (4 * j)) * s;
+      if constexpr (kType == kFp32) {
+        float4* p = reinterpret_cast<float4*>(W) + 2 * to[i];
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+          o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        reinterpret_cast<uint4*>(W)[to[i]] = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      reinterpret_cast<uint4*>(W)[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -287,10 +257,10 @@ cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long lo
 
 cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W, int num_sms,
                               cudaStream_t stream, bool pdl) {
-  const size_t words = static_cast<size_t>(E) * N * (K / 8);
-  const int grid = blocks_for(words, kQuantThreads, num_sms * 16);
+  const size_t rows = static_cast<size_t>(E) * N;
+  const int grid = blocks_for(rows * ((K + 255) / 256), kQuantThreads / 32, num_sms * 8);
   return launch(kKMxQuantize, type == kFp32 ? mx_dequant_kernel<kFp32> : mx_dequant_kernel<kBf16>, grid, kQuantThreads,
-                stream, pdl, q, sp, E, N, K, W);
+                stream, pdl, q, sp, N, K, static_cast<long long>(rows), W);
 }
 
 cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint8_t* q, uint8_t* sp,

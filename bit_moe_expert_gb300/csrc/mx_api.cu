@@ -78,12 +78,13 @@ int shared_tile_rows(int T, int block_rows) {
 }
 
 struct ExpertLayout {
-  size_t q_x, sp_x, q_h_r, q_h_s, sp_h_r, sp_h_s, ypart, total;
+  size_t q_x, sp_x, q_h_r, q_h_s, sp_h_r, sp_h_s, ypart, gu, total;
   int max_blocks, bn_r, bn_s;
+  bool few;  // the products for few tokens
 };
 
 ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
-  ExpertLayout L;
+  ExpertLayout L{};
   L.max_blocks = moe_route_max_blocks(T, E, k, block_rows);
   L.bn_r = routed_rows(block_rows);
   L.bn_s = shared_tile_rows(T < 1 ? 1 : T, block_rows);
@@ -95,13 +96,19 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
     o = round256(o + bytes);
     return at;
   };
+  L.ypart = take(rows * d * 4);
+  L.few = T <= kMxFewT && mx_few_fits(T, d, I, I_shared);
+  if (L.few) {
+    L.gu = take(rows * 2 * (I > I_shared ? I : I_shared) * 4);
+    L.total = o;
+    return L;
+  }
   L.q_x = take(rows * (d / 2));
   L.sp_x = take((L.max_blocks + tiles_s) * scale_bytes(1, d));
   L.q_h_r = take(A * (I / 2));
   L.q_h_s = take(static_cast<size_t>(T) * (I_shared / 2));
   L.sp_h_r = take(L.max_blocks * scale_bytes(1, I));
   L.sp_h_s = take(I_shared > 0 ? tiles_s * scale_bytes(1, I_shared) : 0);
-  L.ypart = take(rows * d * 4);
   L.total = o;
   return L;
 }
@@ -126,6 +133,16 @@ moe_status check_experts(const uint16_t* X, int T, int d, int I, int k, const mo
   return MOE_OK;
 }
 
+template <typename A>
+void set_scales(A* a, const moe_mx_experts* routed, const moe_mx_experts* shared) {
+  a->sp_gate_r = routed->gate.sp;
+  a->sp_up_r = routed->up.sp;
+  a->sp_down_r = routed->down.sp;
+  a->sp_gate_s = shared ? shared->gate.sp : nullptr;
+  a->sp_up_s = shared ? shared->up.sp : nullptr;
+  a->sp_down_s = shared ? shared->down.sp : nullptr;
+}
+
 moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_experts* routed,
                    const moe_mx_experts* shared, int I_shared, const moe_routing* r, uint16_t* Y, void* ws,
                    moe_stream stream) {
@@ -137,19 +154,59 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
   const int num_sms = device_sms();
   if (num_sms <= 0) return MOE_ERR_CUDA;
 
+  const long long A = static_cast<long long>(T) * k, rows = A + (shared ? T : 0);
+  const long long EI = static_cast<long long>(E) * I, Ed = static_cast<long long>(E) * d;
+  uint32_t* status = &static_cast<WsHeader*>(ws)->status;
+  float* ypart = reinterpret_cast<float*>(w + L.ypart);
+  MxExpertMaps maps;
+  bool ok = encode_mx_codes(&maps.gate_r, routed->gate.q, EI, d / 2, kMxBM) &&
+            encode_mx_codes(&maps.up_r, routed->up.q, EI, d / 2, kMxBM) &&
+            encode_mx_codes(&maps.down_r, routed->down.q, Ed, I / 2, kMxBM);
+  if (shared)
+    ok = ok && encode_mx_codes(&maps.gate_s, shared->gate.q, I_shared, d / 2, kMxBM) &&
+         encode_mx_codes(&maps.up_s, shared->up.q, I_shared, d / 2, kMxBM) &&
+         encode_mx_codes(&maps.down_s, shared->down.q, d, I_shared / 2, kMxBM);
+  else  // never read without a shared expert
+    maps.gate_s = maps.up_s = maps.down_s = maps.gate_r;
+  if (!ok) return MOE_ERR_CUDA;
+
+  if (L.few) {
+    maps.x_r = maps.x_s = maps.h_r = maps.h_s = maps.gate_r;  // not read
+    MxFewArgs a{};
+    a.X = X;
+    a.perm = r->perm;
+    a.inv_perm = r->inv_perm;
+    a.block_map = r->block_map;
+    a.num_blocks = r->num_blocks;
+    a.w = r->w;
+    set_scales(&a, routed, shared);
+    a.gu = reinterpret_cast<float*>(w + L.gu);
+    a.ypart = ypart;
+    a.Y = Y;
+    a.arrived = static_cast<WsHeader*>(ws)->mx_arrived;
+    a.status = status;
+    a.T = T;
+    a.d = d;
+    a.I = I;
+    a.k = k;
+    a.I_shared = I_shared;
+    a.E = E;
+    a.max_blocks = L.max_blocks;
+    a.bn = round16(T);
+    return launch_mx_few_experts(a, maps, st, pdl_enabled()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+
   MxExpertArgs a{};
   a.block_map = r->block_map;
   a.num_blocks = r->num_blocks;
-  a.sp_gate_r = routed->gate.sp;
-  a.sp_up_r = routed->up.sp;
-  a.sp_down_r = routed->down.sp;
+  set_scales(&a, routed, shared);
   a.sp_x = w + L.sp_x;
   a.sp_h_r = w + L.sp_h_r;
   a.sp_h_s = w + L.sp_h_s;
   a.q_h_r = w + L.q_h_r;
   a.q_h_s = w + L.q_h_s;
-  a.ypart = reinterpret_cast<float*>(w + L.ypart);
-  a.status = &static_cast<WsHeader*>(ws)->status;
+  a.ypart = ypart;
+  a.status = status;
   a.T = T;
   a.d = d;
   a.I = I;
@@ -160,28 +217,12 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
   a.max_blocks = L.max_blocks;
   a.bn_r = L.bn_r;
   a.bn_s = L.bn_s;
-
-  const long long A = static_cast<long long>(T) * k, rows = A + (shared ? T : 0);
-  const long long EI = static_cast<long long>(E) * I, Ed = static_cast<long long>(E) * d;
-  MxExpertMaps maps;
-  bool ok = encode_mx_codes(&maps.gate_r, routed->gate.q, EI, d / 2, kMxBM) &&
-            encode_mx_codes(&maps.up_r, routed->up.q, EI, d / 2, kMxBM) &&
-            encode_mx_codes(&maps.down_r, routed->down.q, Ed, I / 2, kMxBM) &&
-            encode_mx_codes(&maps.x_r, w + L.q_x, rows, d / 2, L.bn_r) &&
-            encode_mx_codes(&maps.h_r, a.q_h_r, A, I / 2, L.bn_r);
-  if (shared) {
-    a.sp_gate_s = shared->gate.sp;
-    a.sp_up_s = shared->up.sp;
-    a.sp_down_s = shared->down.sp;
-    ok = ok && encode_mx_codes(&maps.gate_s, shared->gate.q, I_shared, d / 2, kMxBM) &&
-         encode_mx_codes(&maps.up_s, shared->up.q, I_shared, d / 2, kMxBM) &&
-         encode_mx_codes(&maps.down_s, shared->down.q, d, I_shared / 2, kMxBM) &&
-         encode_mx_codes(&maps.x_s, w + L.q_x, rows, d / 2, L.bn_s) &&
+  ok = encode_mx_codes(&maps.x_r, w + L.q_x, rows, d / 2, L.bn_r) && encode_mx_codes(&maps.h_r, a.q_h_r, A, I / 2, L.bn_r);
+  if (shared)
+    ok = ok && encode_mx_codes(&maps.x_s, w + L.q_x, rows, d / 2, L.bn_s) &&
          encode_mx_codes(&maps.h_s, a.q_h_s, T, I_shared / 2, L.bn_s);
-  } else {  // never read without a shared expert
-    maps.gate_s = maps.up_s = maps.down_s = maps.gate_r;
+  else
     maps.x_s = maps.h_s = maps.x_r;
-  }
   if (!ok) return MOE_ERR_CUDA;
 
   const MxScatter sc{r->inv_perm, r->block_map, r->num_blocks, a.status, T, k, L.max_blocks, shared ? L.bn_s : 0};
@@ -258,11 +299,20 @@ moe_status moe_mx_linear(const void* X, moe_dtype x_type, int T, int K, long lon
   if (st != MOE_OK) return st;
   if (!ws_ok(ws, ws_bytes, moe_mx_linear_workspace_bytes(T, N, K))) return MOE_ERR_WORKSPACE;
   if (T == 0) return MOE_OK;
+  uint32_t* status = &static_cast<WsHeader*>(ws)->status;
+  if (mx_few_linear_fits(T, K)) {
+    const MxFewLinearArgs a{X, W->sp, Y, status, ldx, T, N, K, y_type == MOE_FP32};
+    CUtensorMap map;
+    if (!encode_mx_codes(&map, W->q, N, K / 2, kMxBM) ||
+        launch_mx_few_linear(a, x_type, map, reinterpret_cast<cudaStream_t>(stream), pdl_enabled()) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
   uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
   const moe_mx_mat xq{w, w + round256(static_cast<size_t>(T) * (K / 2))};
   st = moe_mx_quantize(X, x_type, T, K, ldx, &xq, stream);
   if (st != MOE_OK) return st;
-  return matmul(xq, T, *W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
+  return matmul(xq, T, *W, N, K, Y, y_type, status, stream);
 }
 
 size_t moe_mx_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
@@ -277,7 +327,7 @@ moe_status moe_mx_forward(const uint16_t* X, int T, int d, int I, int k, const m
   if (st != MOE_OK) return st;
   if (!r) return MOE_ERR_INVALID_ARG;
   if (r->block_rows < 1 || r->block_rows > kMaxBlockRows) return MOE_ERR_UNSUPPORTED;
-  if (T > 0 && (!r->w || !r->inv_perm || !r->block_map || !r->num_blocks)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!r->w || !r->perm || !r->inv_perm || !r->block_map || !r->num_blocks)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes,
              moe_mx_forward_workspace_bytes(T, d, I, routed->n_experts, k, I_shared, r->block_rows)))
     return MOE_ERR_WORKSPACE;
@@ -287,7 +337,7 @@ moe_status moe_mx_forward(const uint16_t* X, int T, int d, int I, int k, const m
 size_t moe_mx_layer_workspace_bytes(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
   const size_t f = moe_mx_forward_workspace_bytes(T, d, I, E, k, I_shared, block_rows);
   const size_t r = moe_route_workspace_bytes(T, E, k);
-  return f && r ? f + r : 0;
+  return f && r ? (f > r ? f : r) : 0;
 }
 
 moe_status moe_mx_layer(const float* logits, const moe_scoring* scoring, const uint16_t* X, int T, int d, int I, int k,
@@ -299,10 +349,8 @@ moe_status moe_mx_layer(const float* logits, const moe_scoring* scoring, const u
   st = check_scored(logits, scoring, T, E, k, block_rows, r);
   if (st != MOE_OK) return st;
   if (!ws_ok(ws, ws_bytes, moe_mx_layer_workspace_bytes(T, d, I, E, k, I_shared, block_rows))) return MOE_ERR_WORKSPACE;
-  // the routing's own workspace follows the forward's; both report into the first header
-  uint8_t* route_ws =
-      static_cast<uint8_t*>(ws) + moe_mx_forward_workspace_bytes(T, d, I, E, k, I_shared, block_rows);
-  st = route_scored(logits, scoring, T, E, k, block_rows, r, route_ws, &static_cast<WsHeader*>(ws)->status, stream);
+  // one header for both, and after it the same room: the products start when the routing has completed
+  st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, nullptr, stream);
   if (st != MOE_OK) return st;
   return forward(X, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
 }

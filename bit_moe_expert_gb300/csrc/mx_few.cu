@@ -1,0 +1,535 @@
+// MXFP4 products for few tokens (one decoded token to kMxFewT): what bounds
+// them is the weights' stream and the number of dependent launches, so the
+// activations are quantised inside the products.  A CTA takes one tile of 128
+// weight rows over all of K; its loads are in flight while eight warps turn the
+// tokens' activations into the N operand in shared memory (codes in the 128-byte
+// swizzle the MMA reads, scales in pieces), which costs every CTA the same few
+// kilobytes from L2 that a quantised copy would.
+//
+// Linear layer: one launch.  Expert layer: two after the routing,
+//   gate/up  one matrix a CTA (gate or up), fp32 results to memory;
+//   down     the prologue forms h = MX(silu(gate) up) of the tile's rows; the
+//            last CTA to finish among those of the same 128 columns of Y (a
+//            counter, no wait) adds the experts' rows up in slot order.
+// K is not split: a token's sums are the bits that larger batches give.
+//
+// Weights are asked for before the wait for the previous kernel where their
+// address is known by then: a linear layer's, the shared expert's, and in the
+// down product the routed experts' too, since the gate/up kernel lets its
+// successor start only after its own wait, when the routing has completed.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace bm {
+namespace {
+
+enum Mode { kLinear, kGateUp, kDown };
+
+constexpr int kProducerWarp = 0;
+constexpr int kMmaWarp = 1;
+constexpr int kWorkWarp0 = 2;  // prologue and epilogue
+constexpr int kWorkWarps = 8;
+constexpr int kThreads = (kWorkWarp0 + kWorkWarps) * 32;
+constexpr uint32_t kBarWork = 1;  // named barrier of the work warps
+constexpr int kMaxRing = 8;       // stages of weights in flight (K = 256 each)
+constexpr int kABytes = kMxBM * 128;
+constexpr int kPairBytes = 2 * kMxPieceBytes;
+constexpr int kSmemFixed = 1024 + 1024;  // barriers, alignment
+constexpr int kSmemLimit = 227 * 1024;
+// tensor memory: accumulator, two sets of a stage's scales of the weights and of the tokens
+constexpr uint32_t kTmemCols = 64;
+constexpr uint32_t kTmemSA = 32, kTmemSB = 48;
+static_assert(kMxFewT <= static_cast<int>(kTmemSA), "one accumulator column a token");
+
+struct Plan {
+  int bn, stages, ring;  // stages: of K = 256, at most, in an item
+  __host__ __device__ int b_bytes() const { return bn * 128; }
+  __host__ __device__ int smem() const { return ring * (kABytes + kPairBytes) + stages * (b_bytes() + kPairBytes) + kSmemFixed; }
+};
+
+Plan make_plan(int bn, int K) {
+  Plan p{bn, (K + kMxStageK - 1) / kMxStageK, 0};
+  p.ring = p.stages < kMaxRing ? p.stages : kMaxRing;
+  while (p.ring > 2 && p.smem() > kSmemLimit) --p.ring;
+  return p;
+}
+
+struct Item {
+  const CUtensorMap* map;
+  const uint8_t* scales;  // the weight tile's first piece
+  int row_m, mt, K;       // first weight row in the map, tile of 128 rows, depth
+  int rows, row0, N;      // tokens of the tile, the first one's row, weight rows of the matrix
+  int mat;                // gate/up: 0 gate, 1 up
+  bool shared, ok, some;  // some: false past the last item
+};
+
+struct LinearParams {
+  MxFewLinearArgs a;
+  CUtensorMap w;
+};
+struct ExpertParams {
+  MxFewArgs a;
+  MxExpertMaps maps;
+};
+template <int kMode>
+struct Params {
+  using type = ExpertParams;
+};
+template <>
+struct Params<kLinear> {
+  using type = LinearParams;
+};
+
+__device__ __forceinline__ int pieces_of(int K) { return (K + kMxPieceK - 1) / kMxPieceK; }
+
+template <int kMode>
+__device__ __forceinline__ Item get_item(const LinearParams& p) {
+  Item m{};
+  m.mt = blockIdx.x;
+  m.map = &p.w;
+  m.K = p.a.K;
+  m.N = p.a.N;
+  m.rows = p.a.T;
+  m.row_m = m.mt * kMxBM;
+  m.scales = p.a.sp + static_cast<size_t>(m.mt) * pieces_of(m.K) * kMxPieceBytes;
+  m.ok = m.some = true;
+  return m;
+}
+
+// Tiles of the experts' rows: the shared expert's first, then the block map's.
+__device__ __forceinline__ int routed_tiles(const MxFewArgs& a) {
+  const int nb = *reinterpret_cast<const volatile int32_t*>(a.num_blocks);
+  return nb < 0 || nb > a.max_blocks ? 0 : nb;
+}
+
+template <int kMode>
+__device__ __forceinline__ Item get_item(const ExpertParams& p) {
+  const MxFewArgs& a = p.a;
+  constexpr bool kGU = kMode == kGateUp;
+  constexpr int kMats = kGU ? 2 : 1;
+  Item m{};
+  int i = blockIdx.x;
+  const int mt_s = a.I_shared > 0 ? ((kGU ? a.I_shared : a.d) + kMxBM - 1) / kMxBM : 0;
+  const int mt_r = ((kGU ? a.I : a.d) + kMxBM - 1) / kMxBM;
+  int e = 0;
+  if (i < mt_s * kMats) {
+    m.shared = m.ok = m.some = true;
+    m.rows = a.T;
+    m.row0 = 0;
+    m.N = kGU ? a.I_shared : a.d;
+    m.K = kGU ? a.d : a.I_shared;
+  } else {
+    i -= mt_s * kMats;
+    const int tile = i / (mt_r * kMats);
+    i -= tile * (mt_r * kMats);
+    m.some = tile < routed_tiles(a);
+    if (!m.some) return m;
+    const volatile int32_t* b = a.block_map + 3 * tile;
+    e = b[0];
+    m.row0 = b[1];
+    m.rows = b[2];
+    m.N = kGU ? a.I : a.d;
+    m.K = kGU ? a.d : a.I;
+    m.ok = e >= 0 && e < a.E && m.rows >= 1 && m.rows <= a.bn && m.row0 >= 0 && m.row0 + m.rows <= a.T * a.k;
+  }
+  m.mat = i % kMats;
+  m.mt = i / kMats;
+  if (!m.ok) return m;
+  const MxExpertMaps& t = p.maps;
+  if (kGU) {
+    m.map = m.mat ? (m.shared ? &t.up_s : &t.up_r) : (m.shared ? &t.gate_s : &t.gate_r);
+    m.scales = m.mat ? (m.shared ? a.sp_up_s : a.sp_up_r) : (m.shared ? a.sp_gate_s : a.sp_gate_r);
+  } else {
+    m.map = m.shared ? &t.down_s : &t.down_r;
+    m.scales = m.shared ? a.sp_down_s : a.sp_down_r;
+  }
+  m.row_m = e * m.N + m.mt * kMxBM;
+  m.scales += (static_cast<size_t>(e) * ((m.N + kMxPieceRows - 1) / kMxPieceRows) + m.mt) * pieces_of(m.K) * kMxPieceBytes;
+  return m;
+}
+
+// One warp's 256 values of row r, stage s of the N operand.
+__device__ __forceinline__ void put_row(uint8_t* b, uint8_t* sf, const Plan& p, int r, int s, uint32_t code, uint32_t scales,
+                                        int lane) {
+  *reinterpret_cast<uint32_t*>(b + s * p.b_bytes() + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)) = code;
+  if ((lane & 15) == 0)
+    *reinterpret_cast<uint32_t*>(sf + s * kPairBytes + (lane >> 4) * kMxPieceBytes + (r & 31) * 16) = scales;
+}
+
+// The N operand from activations: row r of the tile is row_of(r).
+template <int kType, typename RowOf>
+__device__ __forceinline__ void quantise_rows(uint8_t* b, uint8_t* sf, const Plan& p, const Item& m, int warp, int lane,
+                                              RowOf row_of) {
+  const int stages = (m.K + kMxStageK - 1) / kMxStageK;
+  constexpr int kU = 4;  // units of a row and a stage in flight
+  for (int u0 = warp; u0 < m.rows * stages; u0 += kU * kWorkWarps) {
+    Load8<kType> x[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int u = u0 + i * kWorkWarps, c = (u % stages) * kMxStageK + 8 * lane;
+      if (u < m.rows * stages && c < m.K) x[i].load(row_of(u / stages), c); else x[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int u = u0 + i * kWorkWarps;
+      if (u >= m.rows * stages) break;
+      uint32_t scales;
+      const uint32_t code = quantize8(x[i], scales, lane);
+      put_row(b, sf, p, u / stages, u % stages, code, scales, lane);
+    }
+  }
+}
+
+template <int kMode, int kType>
+__device__ __forceinline__ void prologue(const LinearParams& p, uint8_t* b, uint8_t* sf, const Plan& plan, const Item& m,
+                                         int warp, int lane) {
+  const char* x = static_cast<const char*>(p.a.X);
+  const size_t pitch = static_cast<size_t>(p.a.ldx) * (kType == kFp32 ? 4 : 2);
+  quantise_rows<kType>(b, sf, plan, m, warp, lane, [&](int r) { return x + r * pitch; });
+}
+
+template <int kMode, int kType>
+__device__ __forceinline__ void prologue(const ExpertParams& p, uint8_t* b, uint8_t* sf, const Plan& plan, const Item& m,
+                                         int warp, int lane) {
+  const MxFewArgs& a = p.a;
+  if constexpr (kMode == kGateUp) {
+    quantise_rows<kBf16>(b, sf, plan, m, warp, lane, [&](int r) {
+      int t = m.shared ? r : __ldg(a.perm + m.row0 + r) / a.k;
+      if (t < 0 || t >= a.T) {  // a malformed permutation
+        record_status(a.status, MOE_ERR_INVALID_ARG);
+        t = 0;
+      }
+      return a.X + static_cast<size_t>(t) * a.d;
+    });
+  } else {
+    // h: a warp per row and block of 32 columns, one column a lane; blocks past
+    // I in the last pair that an MMA reads are zeros
+    const int pitch = max(a.I, a.I_shared);
+    const int blocks = m.K / kMxBlock, blocks_up = (blocks + 1) & ~1;
+    const float* gu = a.gu + static_cast<size_t>(m.shared ? a.T * a.k : m.row0) * 2 * pitch + lane;
+    constexpr int kU = 4;
+    for (int u0 = warp; u0 < m.rows * blocks_up; u0 += kU * kWorkWarps) {
+      float g[kU], up[kU];
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const int u = u0 + i * kWorkWarps, r = u / blocks_up, c = u % blocks_up;
+        const bool in = u < m.rows * blocks_up && c < blocks;
+        const float* at = gu + static_cast<size_t>(r) * 2 * pitch + c * kMxBlock;
+        g[i] = in ? __ldcg(at) : 0.0f;
+        up[i] = in ? __ldcg(at + pitch) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const int u = u0 + i * kWorkWarps, r = u / blocks_up, c = u % blocks_up;
+        if (u >= m.rows * blocks_up) break;
+        const float v = mx_swiglu(g[i], up[i]);
+        const uint32_t byte = c < blocks ? mx_warp_scale_byte(v) : 0u;
+        uint32_t code = (f32x2_to_e2m1x2(v * mx_inverse_scale(byte), 0.0f) & 15u) << (4 * (lane & 7));
+        code |= __shfl_xor_sync(0xffffffffu, code, 1);
+        code |= __shfl_xor_sync(0xffffffffu, code, 2);
+        code |= __shfl_xor_sync(0xffffffffu, code, 4);
+        const int s = c >> 3, chunk = c & 7;  // 32 codes: one 16-byte chunk of the stage's line
+        if ((lane & 7) == 0)
+          *reinterpret_cast<uint32_t*>(b + s * plan.b_bytes() + r * 128 + ((chunk ^ (r & 7)) << 4) + 4 * (lane >> 3)) = code;
+        if (lane == 0) sf[s * kPairBytes + (chunk >> 2) * kMxPieceBytes + (r & 31) * 16 + (chunk & 3)] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+// Accumulator column c of this lane's weight row: 16 columns at c0 are in v.
+template <int kMode>
+__device__ __forceinline__ void store16(const LinearParams& p, const Item& m, int n, int c0, const uint32_t (&v)[16]) {
+  const size_t at = static_cast<size_t>(c0) * p.a.N + n;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    if (c0 + c >= m.rows) break;
+    const float y = __uint_as_float(v[c]);
+    if (p.a.y_fp32)
+      static_cast<float*>(p.a.Y)[at + static_cast<size_t>(c) * p.a.N] = y;
+    else
+      static_cast<__nv_bfloat16*>(p.a.Y)[at + static_cast<size_t>(c) * p.a.N] = __float2bfloat16_rn(y);
+  }
+}
+template <int kMode>
+__device__ __forceinline__ void store16(const ExpertParams& p, const Item& m, int n, int c0, const uint32_t (&v)[16]) {
+  const MxFewArgs& a = p.a;
+  const int pitch = max(a.I, a.I_shared);
+  const size_t row = static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0 + c0;
+  float* y = kMode == kGateUp ? a.gu + (row * 2 + m.mat) * pitch + n : a.ypart + row * a.d + n;
+  const size_t step = kMode == kGateUp ? 2 * static_cast<size_t>(pitch) : a.d;
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (c0 + c < m.rows) y[c * step] = __uint_as_float(v[c]);
+}
+
+// Y's columns 128 mt .. 128 mt + 127 of every token: the experts' rows in slot
+// order, the shared expert's last (combine_kernel's arithmetic).
+__device__ __forceinline__ void combine_columns(const MxFewArgs& a, int mt, int i0) {
+  const size_t A = static_cast<size_t>(a.T) * a.k;
+  for (int i = i0; i < a.T * kMxBM; i += kWorkWarps * 32) {
+    const int t = i / kMxBM, n = mt * kMxBM + i % kMxBM;
+    if (n >= a.d) continue;
+    float acc = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      float v[8], wj[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int j = j0 + u;
+        const int pr = j < a.k ? __ldg(a.inv_perm + static_cast<size_t>(t) * a.k + j) : -1;
+        const bool in = pr >= 0 && static_cast<size_t>(pr) < A;
+        if (j < a.k && !in) record_status(a.status, MOE_ERR_INVALID_ARG);
+        wj[u] = in ? __ldg(a.w + static_cast<size_t>(t) * a.k + j) : 0.0f;
+        v[u] = in ? __ldcg(a.ypart + static_cast<size_t>(pr) * a.d + n) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (j0 + u < a.k) acc = fmaf(wj[u], v[u], acc);
+    }
+    if (a.I_shared > 0) acc += __ldcg(a.ypart + (A + t) * a.d + n);
+    a.Y[static_cast<size_t>(t) * a.d + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc));
+  }
+}
+
+template <int kMode, int kType>
+__global__ void __launch_bounds__(kThreads)
+    mx_few_kernel(const __grid_constant__ typename Params<kMode>::type p, const Plan plan) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* b = ring + plan.ring * kABytes;
+  uint8_t* sa = b + plan.stages * plan.b_bytes();
+  uint8_t* sb = sa + plan.ring * kPairBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + plan.stages * kPairBytes);
+  uint64_t* empty = full + kMaxRing;
+  uint64_t* b_full = empty + kMaxRing;
+  uint64_t* acc_full = b_full + 1;
+  uint64_t* done = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* last_flag = const_cast<int*>(abort_flag) + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < plan.ring; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(b_full, kWorkWarps);
+    mbar_init(acc_full, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint32_t* status = p.a.status;
+  auto fail = [&]() {
+    record_status(status, MOE_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      // the routed experts of the gate/up product are known only after the wait
+      bool early = true;
+      if constexpr (kMode == kGateUp) early = static_cast<int>(blockIdx.x) < 2 * ((p.a.I_shared + kMxBM - 1) / kMxBM);
+      if (!early) pdl_wait();
+      const Item m = get_item<kMode>(p);
+      if (m.some && m.ok) {
+        const int pieces = pieces_of(m.K);
+        int stage = 0, filled = 0;
+        uint32_t phase = 0;
+        for (int k0 = 0; k0 < pieces; k0 += 2, ++filled) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+            fail();
+            break;
+          }
+          const uint32_t sbytes = min(2, pieces - k0) * kMxPieceBytes;
+          mbar_arrive_expect_tx(&full[stage], kABytes + sbytes);
+          tma_load_2d(ring + stage * kABytes, m.map, &full[stage], k0 * 64, m.row_m);
+          bulk_g2s(sa + stage * kPairBytes, m.scales + static_cast<size_t>(k0) * kMxPieceBytes, sbytes, &full[stage]);
+          if (++stage == plan.ring) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        // never leave while a load into this CTA's shared memory may be in flight
+        for (int i = 0; i < min(filled, plan.ring); ++i) {
+          stage = stage == 0 ? plan.ring - 1 : stage - 1;
+          if (stage == plan.ring - 1) phase ^= 1;
+          if (!mbar_wait(&full[stage], phase, nullptr)) record_status(status, MOE_ERR_TIMEOUT);
+        }
+      }
+      if (early) pdl_wait();
+    }
+    __syncwarp();
+  } else {
+    pdl_wait();
+    pdl_launch_dependents();
+    const Item m = get_item<kMode>(p);
+    if (warp == kMmaWarp) {
+      if (m.some && m.ok) {
+        const int pieces = pieces_of(m.K), n64 = (m.K + 63) / 64;
+        const int bn = (m.rows + 15) & ~15;
+        int stage = 0;
+        uint32_t phase = 0, set = 0;
+        bool ok = mbar_wait(b_full, 0, abort_flag);
+        if (!ok) fail();
+        for (int k0 = 0; ok && k0 < pieces; k0 += 2) {
+          ok = mbar_wait(&full[stage], phase, abort_flag);
+          if (!ok) {
+            fail();
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const int np = min(2, pieces - k0), s = k0 >> 1;
+            const uint32_t ta = tmem + kTmemSA + 8 * set, tb = tmem + kTmemSB + 8 * set;
+            for (int j = 0; j < np; ++j) {
+              tc_cp_scales(ta + 4 * j, smem_desc_scales(smem_u32(sa) + stage * kPairBytes + j * kMxPieceBytes));
+              tc_cp_scales(tb + 4 * j, smem_desc_scales(smem_u32(sb) + s * kPairBytes + j * kMxPieceBytes));
+            }
+            const uint64_t ad = smem_desc_sw128_kmajor(smem_u32(ring) + stage * kABytes);
+            const uint64_t bd = smem_desc_sw128_kmajor(smem_u32(b) + s * plan.b_bytes());
+            const int nk = min(4, n64 - 2 * k0);
+            for (int kk = 0; kk < nk; ++kk)
+              tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, idesc_mxfp(kMxBM, bn, 2 * (kk & 1)), ta + 4 * (kk >> 1),
+                          tb + 4 * (kk >> 1), (k0 | kk) ? 1u : 0u);
+            tc_commit(&empty[stage]);
+            if (k0 + 2 >= pieces) tc_commit(acc_full);
+          }
+          __syncwarp();
+          set ^= 1;
+          if (++stage == plan.ring) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        // every MMA has completed before tensor memory is released
+        if (elect_one()) {
+          tc_commit(done);
+          if (!mbar_wait(done, 0, nullptr)) record_status(status, MOE_ERR_TIMEOUT);
+        }
+        __syncwarp();
+      }
+    } else if (m.some) {
+      const int ww = warp - kWorkWarp0;
+      bool done = false;
+      if (m.ok) {
+        prologue<kMode, kType>(p, b, sb, plan, m, ww, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_full);
+        done = mbar_wait(acc_full, 0, abort_flag);
+        __syncwarp();
+        if (done) {
+          tc_fence_after();
+          const int lanegrp = warp & 3, c0 = 16 * (ww >> 2);
+          const int n = m.mt * kMxBM + 32 * lanegrp + lane;
+          if (c0 < m.rows) {  // the same for the whole warp
+            uint32_t v[16];
+            tmem_ld16(tmem + (static_cast<uint32_t>(lanegrp * 32) << 16) + c0, v);
+            tc_wait_ld();
+            if (n < m.N) store16<kMode>(p, m, n, c0, v);
+          }
+          tc_fence_before();
+        } else if (lane == 0) {
+          fail();
+        }
+      } else if (lane == 0) {
+        record_status(status, MOE_ERR_INVALID_ARG);
+      }
+      if constexpr (kMode == kDown) {
+        // every product of these columns counts itself, a skipped one too
+        __threadfence();
+        bar_sync_or(kBarWork, kWorkWarps * 32, false);
+        if (ww == 0 && lane == 0) {
+          const uint32_t all = routed_tiles(p.a) + (p.a.I_shared > 0 ? 1 : 0);
+          const bool last = atom_add_acq_rel_gpu(&p.a.arrived[m.mt], 1u) == all - 1;
+          if (last) p.a.arrived[m.mt] = 0;  // ready for the next call
+          *last_flag = last;
+        }
+        bar_sync_or(kBarWork, kWorkWarps * 32, false);
+        if (*last_flag) {
+          __threadfence();
+          combine_columns(p.a, m.mt, ww * 32 + lane);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int kMode, int kType>
+cudaError_t launch(int kind, const typename Params<kMode>::type& p, const Plan& plan, int grid, cudaStream_t stream,
+                   bool pdl) {
+  const auto kernel = mx_few_kernel<kMode, kType>;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), plan.smem());
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = plan.smem();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  timer_begin(kind, stream);
+  e = cudaLaunchKernelEx(&cfg, kernel, p, plan);
+  timer_end(kind, stream);
+  return e;
+}
+
+int round16(int x) { return (x + 15) & ~15; }
+bool fits(int bn, int K) {
+  const Plan p = make_plan(bn, K);
+  return p.smem() <= kSmemLimit;
+}
+
+}  // namespace
+
+bool mx_few_linear_fits(int T, int K) { return T <= kMxFewT && fits(round16(T), K); }
+
+cudaError_t launch_mx_few_linear(const MxFewLinearArgs& a, int type, const CUtensorMap& w, cudaStream_t stream, bool pdl) {
+  const LinearParams p{a, w};
+  const Plan plan = make_plan(round16(a.T), a.K);
+  const int grid = (a.N + kMxBM - 1) / kMxBM;
+  if (type == kBf16) return launch<kLinear, kBf16>(kKMxGemm, p, plan, grid, stream, pdl);
+  if (type == kFp16) return launch<kLinear, kFp16>(kKMxGemm, p, plan, grid, stream, pdl);
+  return launch<kLinear, kFp32>(kKMxGemm, p, plan, grid, stream, pdl);
+}
+
+bool mx_few_fits(int T, int d, int I, int I_shared) {
+  const int bn = round16(T);
+  return T <= kMxFewT && (d + kMxBM - 1) / kMxBM <= static_cast<int>(sizeof(WsHeader::mx_arrived) / 4) && fits(bn, d) &&
+         fits(bn, I > I_shared ? I : I_shared);
+}
+
+cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl) {
+  const ExpertParams p{a, maps};
+  const int tiles = a.T * a.k < a.max_blocks ? a.T * a.k : a.max_blocks;  // every tile holds an assignment
+  const int mt = (a.I + kMxBM - 1) / kMxBM, mt_s = (a.I_shared + kMxBM - 1) / kMxBM, mt_d = (a.d + kMxBM - 1) / kMxBM;
+  const cudaError_t e = launch<kGateUp, kBf16>(kKMxGateUp, p, make_plan(a.bn, a.d), 2 * (tiles * mt + mt_s), stream, pdl);
+  if (e != cudaSuccess) return e;
+  const int I = a.I > a.I_shared ? a.I : a.I_shared;
+  return launch<kDown, kBf16>(kKMxDown, p, make_plan(a.bn, I), mt_d * (tiles + (a.I_shared > 0 ? 1 : 0)), stream, pdl);
+}
+
+}  // namespace bm

@@ -216,9 +216,8 @@ __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, c
       float h[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float gv = __uint_as_float(g[c + i]);
-        const float v = __fdividef(gv, 1.0f + __expf(-gv)) * __uint_as_float(u[c + i]);
-        const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
+        const float v = mx_swiglu(__uint_as_float(g[c + i]), __uint_as_float(u[c + i]));
+        const uint32_t byte = mx_warp_scale_byte(v);
         bytes[c >> 2] |= byte << (8 * ((c + i) & 3));
         h[i] = v * mx_inverse_scale(byte);
       }

@@ -15,7 +15,8 @@ struct WsHeader {
   uint32_t route_done;  // routing kernel (grid-synchronised mode): CTAs that have finished
   uint32_t dec_gen;     // decode kernel: calls so far; call g counts its barrier arrivals in dec_count[g % 2]
   uint32_t dec_count[2];
-  uint32_t pad[58];
+  uint32_t mx_arrived[56];  // MXFP4 experts, few tokens: finished products per 128 columns of Y; reset by the last
+  uint32_t pad[2];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header must be 256 bytes");
 

@@ -153,7 +153,8 @@ def test_matmul(M, N, K, y_kind):
 
 
 @pytest.mark.parametrize("M,N,K,x_kind", [(1, 2048, 2048, "bf16"), (5, 100, 96, "fp16"), (128, 96, 256, "fp32"),
-                                          (333, 1001, 2816, "fp16"), (140, 64, 416, "fp32")])
+                                          (333, 1001, 2816, "fp16"), (140, 64, 416, "fp32"), (32, 300, 1184, "bf16"),
+                                          (33, 300, 1184, "bf16"), (3, 40, 12320, "bf16"), (3, 40, 16416, "fp32")])
 def test_linear(M, N, K, x_kind):
     rng = np.random.default_rng(M + N)
     x = torch.from_numpy(rng.standard_normal((M, K + 32)).astype(np.float32)).to(TYPES[x_kind]).cuda()[:, :K]
@@ -237,6 +238,8 @@ LAYERS = [  # T, d, I, I_shared, E, k, block_rows
     (2, 96, 32, 0, 4, 4, 16),            # one block of 32 a row of h
     (40, 288, 160, 96, 8, 3, 32),        # no size a multiple of 64
     (40, 288, 160, 96, 8, 3, 20),        # tiles of a height that is no multiple of 16
+    (32, 288, 160, 96, 8, 3, 16),        # several tiles of an expert among few tokens
+    (17, 2048, 96, 512, 12, 5, 64),      # a shared expert wider than the routed ones
     (300, 512, 224, 256, 6, 2, 128),     # full tiles, one accumulator
     (300, 512, 224, 0, 6, 2, 96),
     (150, 320, 704, 64, 5, 1, 64),
