@@ -236,6 +236,7 @@ struct MxLinearArgs {
   uint32_t* status;
   int rows_m, rows_n, K, bn, num_sms;
   int y_fp32;
+  int weights_n;  // the weights are the N side (else the M side)
 };
 struct MxLinearMaps {
   CUtensorMap m, n;

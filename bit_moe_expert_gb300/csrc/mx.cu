@@ -23,8 +23,7 @@ constexpr int kUnits = 4;
 
 // The rows and 256-value segments that a warp of the grid takes in turn.
 struct RowWalk {
-  long long row;
-  int seg;
+  int row, seg;
   int segs, row_step, seg_step;
   __device__ __forceinline__ explicit RowWalk(int K) {
     segs = (K + 255) / 256;
@@ -57,8 +56,7 @@ __global__ void __launch_bounds__(kQuantThreads)
   RowWalk at(K);
   while (at.row < rows) {
     Load8<kType> x[kUnits];
-    long long row[kUnits];
-    int col[kUnits];
+    int row[kUnits], col[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i, at.next()) {
       row[i] = at.row;
@@ -142,49 +140,51 @@ __global__ void __launch_bounds__(kScatterThreads)
   }
 }
 
-// The same division of work: one warp per 256 values, eight a lane.
+// The same division of work within each matrix (blockIdx.y).
 template <int kType>
 __global__ void __launch_bounds__(kQuantThreads)
-    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int N, int K, long long rows,
-                      void* __restrict__ W) {
+    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int N, int K, void* __restrict__ W) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
-  const size_t per_expert = static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
+  const size_t matrix = static_cast<size_t>(blockIdx.y) * N;
+  sp += blockIdx.y * static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
   RowWalk at(K);
-  while (at.row < rows) {
+  while (at.row < N) {
     uint32_t code[kUnits];
-    uint8_t byte[kUnits];
+    uint32_t byte[kUnits];
     size_t to[kUnits];
     bool in[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i, at.next()) {
       const int c = at.seg * 256 + 8 * lane;
-      in[i] = at.row < rows && c < K;
+      in[i] = at.row < N && c < K;
       if (!in[i]) continue;
-      const long long e = at.row / N;
-      const int n = static_cast<int>(at.row - e * N);
-      to[i] = static_cast<size_t>(at.row) * (K / 8) + c / 8;
+      to[i] = (matrix + at.row) * (K / 8) + c / 8;
       code[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + to[i]);
-      byte[i] = __ldg(sp + e * per_expert + mx_scale_offset(n, c / kMxPieceK, pieces) + (c % kMxPieceK) / kMxBlock);
+      byte[i] = __ldg(sp + mx_scale_offset(at.row, c / kMxPieceK, pieces) + (c % kMxPieceK) / kMxBlock);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (!in[i]) continue;
       const float s = mx_scale(byte[i]);
-      float f[8];
+      float2 f[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mx_code_value(code[i] >> (4 * j)) * s;
+      for (int j = 0; j < 4; ++j) {
+        f[j] = e2m1x2_to_float2(code[i] >> (8 * j));
+        f[j].x *= s;
+        f[j].y *= s;
+      }
       if constexpr (kType == kFp32) {
         float4* p = reinterpret_cast<float4*>(W) + 2 * to[i];
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        p[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        p[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
       } else {
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+          const __nv_bfloat162 b = __float22bfloat162_rn(f[j]);
           o[j] = *reinterpret_cast<const uint32_t*>(&b);
         }
         reinterpret_cast<uint4*>(W)[to[i]] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -217,12 +217,12 @@ __global__ void mx_prepack_kernel(const uint8_t* __restrict__ scale, int E, int 
 
 // Programmatic dependent launch of `kernel` where `pdl` allows it.
 template <typename... P, typename... A>
-cudaError_t launch(int kind, void (*kernel)(P...), int grid, int threads, cudaStream_t stream, bool pdl, A... args) {
+cudaError_t launch(int kind, void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, bool pdl, A... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -257,10 +257,10 @@ cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long lo
 
 cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W, int num_sms,
                               cudaStream_t stream, bool pdl) {
-  const size_t rows = static_cast<size_t>(E) * N;
-  const int grid = blocks_for(rows * ((K + 255) / 256), kQuantThreads / 32, num_sms * 8);
-  return launch(kKMxQuantize, type == kFp32 ? mx_dequant_kernel<kFp32> : mx_dequant_kernel<kBf16>, grid, kQuantThreads,
-                stream, pdl, q, sp, N, K, static_cast<long long>(rows), W);
+  const int most = num_sms * 8 / E;
+  const int grid = blocks_for(static_cast<size_t>(N) * ((K + 255) / 256), kQuantThreads / 32, most > 1 ? most : 1);
+  return launch(kKMxQuantize, type == kFp32 ? mx_dequant_kernel<kFp32> : mx_dequant_kernel<kBf16>, dim3(grid, E),
+                kQuantThreads, stream, pdl, q, sp, N, K, W);
 }
 
 cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint8_t* q, uint8_t* sp,

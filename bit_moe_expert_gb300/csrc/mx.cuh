@@ -28,17 +28,11 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FC00000u : byte == 0u ? 0x00400000u : byte << 23);
 }
 
-// Value of the E2M1 code in bits 0..3.
-__device__ __forceinline__ float mx_code_value(uint32_t code) {
-  // the two exponent bits and the mantissa bit at fp32's exponent and top
-  // mantissa bits stand for the value times 2^-126; code 1 (0.5) is subnormal there
-  return __uint_as_float(((code & 8u) << 28) | ((code & 7u) << 22)) * 0x1p126f;
-}
-
 // Byte offset of the four scales of row r, 128-column piece `piece`, in packed
 // scales with `pieces` pieces a row.
-__device__ __forceinline__ long long mx_scale_offset(long long r, int piece, int pieces) {
-  return ((r / kMxPieceRows) * pieces + piece) * kMxPieceBytes + (r % 32) * 16 + ((r % kMxPieceRows) / 32) * 4;
+__device__ __forceinline__ long long mx_scale_offset(int r, int piece, int pieces) {
+  return (static_cast<long long>(r / kMxPieceRows) * pieces + piece) * kMxPieceBytes + (r % 32) * 16 +
+         ((r % kMxPieceRows) / 32) * 4;
 }
 
 enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };

@@ -10,6 +10,7 @@ namespace bm {
 namespace {
 
 constexpr int kMaxK_mx = 1 << 20;  // columns of a matrix
+constexpr int kMaxRows = 1 << 30;  // rows (row indexes and TMA coordinates are 32-bit)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ws_ok(const void* ws, size_t have, size_t need) {
@@ -31,13 +32,14 @@ size_t scale_bytes(long long rows, int K) { return mx_pieces(rows, K) * kMxPiece
 moe_status check_x(const void* X, moe_dtype type, int rows, int K, long long ldx) {
   if (rows < 0 || !size_ok(1, K) || !type_ok(type) || ldx < K || (ldx * type_bytes(type)) % 16 != 0)
     return MOE_ERR_INVALID_ARG;
+  if (rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (rows > 0 && (!X || !aligned16(X))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
 moe_status check_matmul(int M, const moe_mx_mat* W, int N, int K, const void* Y, moe_dtype y_type) {
   if (M < 0 || !size_ok(N, K) || !W || !mat_ok(*W) || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
-  if (y_type == MOE_FP16) return MOE_ERR_UNSUPPORTED;
+  if (y_type == MOE_FP16 || M > kMaxRows || N > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (M > 0 && (!Y || !aligned16(Y))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -61,6 +63,7 @@ moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K,
   a.rows_n = swap ? M : N;
   a.stride_m = swap ? 1 : N;
   a.stride_n = swap ? N : 1;
+  a.weights_n = !swap;
   a.bn = swap ? round16(M) : 256;
   if (!encode_mx_codes(&maps.m, m.q, a.rows_m, K / 2, kMxBM) || !encode_mx_codes(&maps.n, n.q, a.rows_n, K / 2, a.bn))
     return MOE_ERR_CUDA;
@@ -267,7 +270,7 @@ moe_status moe_mx_quantize(const void* X, moe_dtype type, int rows, int K, long 
 
 moe_status moe_mx_dequant(const moe_mx_mat* m, int E, int N, int K, moe_dtype type, void* W, moe_stream stream) {
   if (!m || !mat_ok(*m) || E < 1 || !size_ok(N, K) || !type_ok(type) || !W || !aligned16(W)) return MOE_ERR_INVALID_ARG;
-  if (type == MOE_FP16) return MOE_ERR_UNSUPPORTED;
+  if (type == MOE_FP16 || E > 65535 || N > kMaxRows) return MOE_ERR_UNSUPPORTED;
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
   return launch_mx_dequant(m->q, m->sp, E, N, K, type, W, sms, reinterpret_cast<cudaStream_t>(stream),

@@ -14,10 +14,10 @@
 // tokens; for many, tokens are the M side, whose tensor-memory lanes then hold
 // rows of Y, and 256 columns of Y a tile halve the reads of the tokens' codes.
 //
-// Roles (one persistent CTA per SM): warp 0 TMA producer, warp 1 MMA issuer
-// (copies a stage's scales from shared to tensor memory, then multiplies: the
-// tensor pipeline keeps the order), warps 2-9 epilogue, two per quarter of the
-// tensor-memory lanes.  Every wait is bounded and records MOE_ERR_TIMEOUT.
+// Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
+// activations' loads, warp 2 MMA issuer (copies a stage's scales from shared to
+// tensor memory, then multiplies: the tensor pipeline keeps the order), warps
+// 3-10 epilogue, two per quarter of the tensor-memory lanes.  Every wait is bounded and records MOE_ERR_TIMEOUT.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,17 +30,20 @@ namespace {
 
 enum Mode { kLinear, kGateUp, kDown };
 
-constexpr int kProducerWarp = 0;
-constexpr int kMmaWarp = 1;
-constexpr int kEpiWarp0 = 2;
+constexpr int kWeightsWarp = 0;
+constexpr int kActivationsWarp = 1;
+constexpr int kMmaWarp = 2;
+constexpr int kEpiWarp0 = 3;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 12;
+constexpr int kMaxAccs = 8;
 constexpr int kCodeBytesM = kMxBM * 128;   // one matrix's codes of a stage
 constexpr int kPairBytes = 2 * kMxPieceBytes;  // a stage's scales of 128 rows
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kSmemFixed = 1024 /* barriers */ + 1024 /* alignment */;
+constexpr int kEntries = 256;  // items of a CTA, from its first, whose Entry is in shared memory
+constexpr int kSmemFixed = 1024 /* barriers */ + 16 * kEntries + 1024 /* alignment */;
 
 // How a launch divides shared and tensor memory; bn: the N side's columns at most.
 struct Plan {
@@ -56,8 +59,9 @@ Plan make_plan(int mats, int bn) {
   p.stage_bytes = mats * (kCodeBytesM + kPairBytes) + bn * 128 + p.row_tiles * kPairBytes;
   p.stages = (kSmemLimit - kSmemFixed) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  // a second accumulator lets the epilogue of one item run beside the next one's products
-  p.acc_bufs = 2 * mats * bn + 2 * scale_cols(mats, p.row_tiles) <= static_cast<int>(kTmemCols) ? 2 : 1;
+  // further accumulators let the epilogue of one item run beside the next ones' products
+  p.acc_bufs = (static_cast<int>(kTmemCols) - 2 * scale_cols(mats, p.row_tiles)) / (mats * bn);
+  if (p.acc_bufs > kMaxAccs) p.acc_bufs = kMaxAccs;
   return p;
 }
 
@@ -67,13 +71,26 @@ struct Item {
   int row_m, row_n;                // first rows of the codes
   int mt, rows, K, box;            // M tile, valid N rows, depth, N rows that the TMA box brings
   int row0, slot;                  // experts: first row among the assignments (or tokens), tile slot
+  int groups;                      // 128-row groups of scales on the N side
+  bool weights_n;                  // the weights are the N side (dense product)
   bool shared, ok;
 };
 
+// This CTA's items: local index i stands for item first + i * step, dealt out in
+// turn, so that CTAs running together read neighbouring tiles (runs of
+// consecutive items per CTA cost the 512-token layer's gate/up product 65
+// instead of 53 us).
 struct Sched {
-  int nb, mt_r, mt_s, n_routed, n_total;
+  int mt_r, mt_s;  // M tiles of a routed and of a shared tile
+  int n_routed;    // expert products: items below are routed
+  int first, n, step;
 };
 
+// What an item's id stands for, as every role needs it.
+struct Entry {
+  int e, row0, rows;  // expert (-1: malformed), first row, rows
+  int at;             // mt + 2^15 slot, or -1 - (mt + 2^15 tile) for the shared expert
+};
 template <int kMode>
 struct Args {
   using type = MxExpertArgs;
@@ -90,16 +107,23 @@ __device__ __forceinline__ int pieces_of(int K) { return (K + kMxPieceK - 1) / k
 __device__ __forceinline__ Sched make_sched(const MxLinearArgs& a, const Plan& p, bool) {
   Sched s{};
   s.mt_r = (a.rows_m + kMxBM - 1) / kMxBM;
-  s.n_total = s.mt_r * ((a.rows_n + p.bn - 1) / p.bn);
+  const int total = s.mt_r * ((a.rows_n + p.bn - 1) / p.bn);
+  s.first = blockIdx.x;
+  s.step = gridDim.x;
+  s.n = (total - s.first + s.step - 1) / s.step;
   return s;
 }
 
-__device__ __forceinline__ Item get_item(const MxLinearArgs& a, const MxLinearMaps& maps, const Plan& p, const Sched& s,
-                                         int it, bool) {
+__device__ __forceinline__ Entry make_entry(const MxLinearArgs&, const Sched& s, int it) {
+  return Entry{0, 0, it / s.mt_r, it % s.mt_r};  // rows: the N tile
+}
+
+__device__ __forceinline__ Item get_item(const MxLinearArgs& a, const MxLinearMaps& maps, const Plan& p,
+                                         const Entry& en, bool) {
   Item m{};
   const int pieces = pieces_of(a.K);
-  m.mt = it % s.mt_r;
-  const int nt = it / s.mt_r;
+  m.mt = en.at;
+  const int nt = en.rows;
   m.m0 = &maps.m;
   m.n = &maps.n;
   m.row_m = m.mt * kMxBM;
@@ -109,65 +133,83 @@ __device__ __forceinline__ Item get_item(const MxLinearArgs& a, const MxLinearMa
   m.box = p.bn;
   m.sm0 = a.sp_m + static_cast<size_t>(m.mt) * pieces * kMxPieceBytes;
   m.sn = a.sp_n + static_cast<size_t>(m.row_n / kMxPieceRows) * pieces * kMxPieceBytes;
+  m.groups = (m.rows + kMxPieceRows - 1) / kMxPieceRows;
+  m.weights_n = a.weights_n;
   m.ok = true;
   return m;
 }
 
 __device__ __forceinline__ Sched make_sched(const MxExpertArgs& a, const Plan&, bool gate_up) {
   Sched s{};
-  s.nb = *a.num_blocks;
-  if (s.nb < 0 || s.nb > a.max_blocks) {
+  int nb = *reinterpret_cast<const volatile int32_t*>(a.num_blocks);
+  if (nb < 0 || nb > a.max_blocks) {
     if (threadIdx.x == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
-    s.nb = 0;
+    nb = 0;
   }
   s.mt_r = ((gate_up ? a.I : a.d) + kMxBM - 1) / kMxBM;
   s.mt_s = ((gate_up ? a.I_shared : a.d) + kMxBM - 1) / kMxBM;
-  s.n_routed = s.nb * s.mt_r;
-  s.n_total = s.n_routed + (a.I_shared > 0 ? (a.T + a.bn_s - 1) / a.bn_s * s.mt_s : 0);
+  s.n_routed = nb * s.mt_r;
+  const int total = s.n_routed + (a.I_shared > 0 ? (a.T + a.bn_s - 1) / a.bn_s * s.mt_s : 0);
+  s.first = blockIdx.x;
+  s.step = gridDim.x;
+  s.n = (total - s.first + s.step - 1) / s.step;
   return s;
 }
 
-__device__ __forceinline__ Item get_item(const MxExpertArgs& a, const MxExpertMaps& maps, const Plan&, const Sched& s,
-                                         int it, bool gate_up) {
-  Item m{};
-  int e, N;
+__device__ __forceinline__ Entry make_entry(const MxExpertArgs& a, const Sched& s, int it) {
+  Entry en;
   if (it < s.n_routed) {
     const int blk = it / s.mt_r;
-    m.mt = it % s.mt_r;
-    e = __ldg(a.block_map + 3 * blk);
-    m.row0 = __ldg(a.block_map + 3 * blk + 1);
-    m.rows = __ldg(a.block_map + 3 * blk + 2);
-    m.slot = blk;
-    m.box = a.bn_r;
-    N = gate_up ? a.I : a.d;
-    m.K = gate_up ? a.d : a.I;
-    m.ok = e >= 0 && e < a.E && m.rows >= 1 && m.rows <= a.bn_r && m.row0 >= 0 && m.row0 + m.rows <= a.T * a.k;
-    if (!m.ok) return m;
-    m.m0 = gate_up ? &maps.gate_r : &maps.down_r;
-    m.m1 = &maps.up_r;
-    m.n = gate_up ? &maps.x_r : &maps.h_r;
-    m.sm0 = gate_up ? a.sp_gate_r : a.sp_down_r;
-    m.sm1 = a.sp_up_r;
-    m.row_n = m.row0;
+    const volatile int32_t* b = a.block_map + 3 * static_cast<size_t>(blk);
+    en.e = b[0];
+    en.row0 = b[1];
+    en.rows = b[2];
+    en.at = (it - blk * s.mt_r) + (blk << 15);
+    const bool ok = en.e >= 0 && en.e < a.E && en.rows >= 1 && en.rows <= a.bn_r && en.row0 >= 0 &&
+                    en.row0 + en.rows <= a.T * a.k;
+    if (!ok) en.e = -1;
   } else {
-    const int j = it - s.n_routed;
-    m.shared = true;
-    m.slot = j / s.mt_s;
-    m.mt = j % s.mt_s;
-    e = 0;
-    m.row0 = m.slot * a.bn_s;
-    m.rows = min(a.bn_s, a.T - m.row0);
-    m.box = a.bn_s;
-    N = gate_up ? a.I_shared : a.d;
-    m.K = gate_up ? a.d : a.I_shared;
-    m.ok = true;
+    const int j = it - s.n_routed, tile = j / s.mt_s;
+    en.e = 0;
+    en.row0 = tile * a.bn_s;
+    en.rows = min(a.bn_s, a.T - en.row0);
+    en.at = -1 - ((j - tile * s.mt_s) + (tile << 15));
+  }
+  return en;
+}
+
+__device__ __forceinline__ Item get_item(const MxExpertArgs& a, const MxExpertMaps& maps, const Plan&, const Entry& en,
+                                         bool gate_up) {
+  Item m{};
+  m.ok = en.e >= 0;
+  if (!m.ok) return m;
+  const int e = en.e;
+  m.row0 = en.row0;
+  m.rows = en.rows;
+  m.shared = en.at < 0;
+  const int at = m.shared ? -1 - en.at : en.at;
+  m.mt = at & 0x7FFF;
+  m.slot = at >> 15;
+  const int I = m.shared ? a.I_shared : a.I;
+  const int N = gate_up ? I : a.d;
+  m.K = gate_up ? a.d : I;
+  m.box = m.shared ? a.bn_s : a.bn_r;
+  if (m.shared) {
     m.m0 = gate_up ? &maps.gate_s : &maps.down_s;
     m.m1 = &maps.up_s;
     m.n = gate_up ? &maps.x_s : &maps.h_s;
     m.sm0 = gate_up ? a.sp_gate_s : a.sp_down_s;
     m.sm1 = a.sp_up_s;
     m.row_n = gate_up ? a.T * a.k + m.row0 : m.row0;
+  } else {
+    m.m0 = gate_up ? &maps.gate_r : &maps.down_r;
+    m.m1 = &maps.up_r;
+    m.n = gate_up ? &maps.x_r : &maps.h_r;
+    m.sm0 = gate_up ? a.sp_gate_r : a.sp_down_r;
+    m.sm1 = a.sp_up_r;
+    m.row_n = m.row0;
   }
+  m.groups = 1;
   const int pieces = pieces_of(m.K);
   const size_t tile = (static_cast<size_t>(e) * ((N + kMxPieceRows - 1) / kMxPieceRows) + m.mt) * pieces * kMxPieceBytes;
   m.sm0 += tile;
@@ -298,7 +340,8 @@ __device__ __forceinline__ void epilogue(const MxLinearArgs& a, const Item& m, c
   }
 }
 
-template <int kMode>
+// kRowTiles: 128-row groups of scales of the N side (bn up to 128, or 256).
+template <int kMode, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ typename Args<kMode>::maps maps,
                    const __grid_constant__ typename Args<kMode>::type a, const Plan p) {
@@ -309,19 +352,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(stages + p.stages * p.stage_bytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* done = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + kMaxAccs;
+  uint64_t* done = acc_empty + kMaxAccs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Entry* entries = reinterpret_cast<Entry*>(stages + p.stages * p.stage_bytes + 1024);
+  static_assert(sizeof(Entry) == 16, "room of the entries");
 
-  const int warp = threadIdx.x >> 5;
+  // the same in all lanes, so that the roles' branches are known to be uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
+  // The routing has completed by now (the kernel before this one lets this one
+  // start only after its own wait), so only the activations are waited for.
+  const Sched s = make_sched(a, p, kGU);
+  for (int i = threadIdx.x; i < min(s.n, kEntries); i += kThreads) entries[i] = make_entry(a, s, s.first + i * s.step);
+  auto item = [&](int i) {
+    return get_item(a, maps, p, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
+  };
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);  // the weights' and the activations' expect_tx; their bytes complete the phase
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < p.acc_bufs; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], kEpiWarps);
     }
@@ -338,48 +391,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  pdl_wait();
-  pdl_launch_dependents();
-
-  const Sched s = make_sched(a, p, kGU);
   auto fail = [&]() {
     record_status(a.status, MOE_ERR_TIMEOUT);
     *abort_flag = 1;
   };
 
-  if (warp == kProducerWarp) {
+  if (warp == kWeightsWarp || warp == kActivationsWarp) {
+    // one thread for the weights, which starts before the wait, and one for the activations
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, used_mask = 0, last_parity = 0;
+      const bool weights = warp == kWeightsWarp;
+      if (!weights) pdl_wait();
+      int stage = 0, filled = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      for (int it = blockIdx.x; it < s.n_total && ok; it += gridDim.x) {
-        const Item m = get_item(a, maps, p, s, it, kGU);
+      for (int i = 0; i < s.n && ok; ++i) {
+        const Item m = item(i);
         if (!m.ok) continue;
         const int pieces = pieces_of(m.K);
-        // 128-row groups of the N side that exist (the dense product's last tile may have one less)
-        const int groups = (m.rows + kMxPieceRows - 1) / kMxPieceRows;
-        for (int k0 = 0; k0 < pieces; k0 += 2) {
+        const bool n_side = weights == m.weights_n;
+        const uint32_t codes = n_side ? m.box * 128 : kMats * kCodeBytesM;
+        const int scales = n_side ? m.groups : kMats;
+        const size_t group = static_cast<size_t>(pieces) * kMxPieceBytes;
+        const uint8_t *s0 = n_side ? m.sn : m.sm0, *s1 = n_side ? m.sn + group : m.sm1;
+        for (int k0 = 0; k0 < pieces; k0 += 2, ++filled) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          uint8_t* st = stages + stage * p.stage_bytes;
-          uint8_t* sf = st + kMats * kCodeBytesM + p.bn * 128;
-          const uint32_t sbytes = min(2, pieces - k0) * kMxPieceBytes;
+          uint8_t* st = stages + stage * p.stage_bytes + (n_side ? kMats * kCodeBytesM : 0);
+          uint8_t* sf = stages + stage * p.stage_bytes + kMats * kCodeBytesM + p.bn * 128 + (n_side ? kMats * kPairBytes : 0);
           uint64_t* bar = &full[stage];
-          mbar_arrive_expect_tx(bar, kMats * kCodeBytesM + m.box * 128 + (kMats + groups) * sbytes);
-          tma_load_2d(st, m.m0, bar, k0 * 64, m.row_m);
-          if (kGU) tma_load_2d(st + kCodeBytesM, m.m1, bar, k0 * 64, m.row_m);
-          tma_load_2d(st + kMats * kCodeBytesM, m.n, bar, k0 * 64, m.row_n);
-          const size_t at = static_cast<size_t>(k0) * kMxPieceBytes;
-          bulk_g2s(sf, m.sm0 + at, sbytes, bar);
-          if (kGU) bulk_g2s(sf + kPairBytes, m.sm1 + at, sbytes, bar);
-          for (int g = 0; g < groups; ++g)
-            bulk_g2s(sf + (kMats + g) * kPairBytes, m.sn + static_cast<size_t>(g) * pieces * kMxPieceBytes + at, sbytes,
-                     bar);
-          used_mask |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          const uint32_t sbytes = min(2, pieces - k0) * kMxPieceBytes;
+          mbar_arrive_expect_tx(bar, codes + scales * sbytes);
+          if (n_side) {
+            tma_load_2d(st, m.n, bar, k0 * 64, m.row_n);
+          } else {
+            tma_load_2d(st, m.m0, bar, k0 * 64, m.row_m);
+            if (kGU) tma_load_2d(st + kCodeBytesM, m.m1, bar, k0 * 64, m.row_m);
+          }
+          bulk_g2s(sf, s0, sbytes, bar);
+          if (scales > 1) bulk_g2s(sf + kPairBytes, s1, sbytes, bar);
+          s0 += kPairBytes;
+          s1 += kPairBytes;
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
@@ -387,76 +441,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // never leave while a load into this CTA's shared memory may be in flight
-      for (int i = 0; i < p.stages; ++i)
-        if ((used_mask >> i) & 1u) {
-          if (!mbar_wait(&full[i], (last_parity >> i) & 1u, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
-        }
+      for (int i = 0; i < min(filled, p.stages); ++i) {
+        stage = stage == 0 ? p.stages - 1 : stage - 1;
+        if (stage == p.stages - 1) phase ^= 1;
+        if (!mbar_wait(&full[stage], phase, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
+      }
+      if (weights) pdl_wait();
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
+    pdl_wait();
+    pdl_launch_dependents();
+    // One thread issues everything; what it issues is computed by the whole warp
+    // from values that are the same in all lanes (votes, shuffles from lane 0),
+    // which lets the compiler keep descriptors and addresses in uniform
+    // registers.  The issue loop is what bounds short products otherwise: at
+    // K = 512 a stage took 1,000 cycles to issue.
     const uint32_t stage0 = smem_u32(stages);
     // tensor memory: the accumulators, then two sets of a stage's scales
     const uint32_t sf_tmem = tmem + p.acc_bufs * kMats * p.bn;
+    constexpr int kScaleCols = scale_cols(kMats, kRowTiles);
+    const uint64_t ad0 = smem_desc_sw128_kmajor(stage0);
+    const uint64_t bd0 = smem_desc_sw128_kmajor(stage0 + kMats * kCodeBytesM);
+    const uint64_t sd0 = smem_desc_scales(stage0 + kMats * kCodeBytesM + p.bn * 128);
+    const uint32_t stage_step = static_cast<uint32_t>(p.stage_bytes) >> 4;  // in the descriptors' address fields
     int stage = 0, accb = 0;
-    uint32_t phase = 0, accphase = 0, set = 0;
+    uint32_t phase = 0, accphase = 0, set = 0, at = 0;
     bool ok = true;
-    for (int it = blockIdx.x; it < s.n_total && ok; it += gridDim.x) {
-      const Item m = get_item(a, maps, p, s, it, kGU);
-      if (!m.ok) continue;
-      const int bn = tile_n(m.rows);
-      if (!mbar_wait(&acc_empty[accb], accphase ^ 1, abort_flag)) {
+    for (int i = 0; i < s.n && ok; ++i) {
+      const Item m = item(i);
+      const int rows = __shfl_sync(0xffffffffu, m.ok ? m.rows : 0, 0);
+      if (rows == 0) continue;
+      const int n64 = (__shfl_sync(0xffffffffu, m.K, 0) + 63) / 64;
+      const int bn = tile_n(rows);
+      const uint32_t idesc0 = idesc_mxfp(kMxBM, bn, 0), idesc1 = idesc_mxfp(kMxBM, bn, 2);
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[accb], accphase ^ 1, abort_flag))) {
         fail();
         break;
       }
       tc_fence_after();
       const uint32_t d = tmem + accb * kMats * p.bn;
-      const int n64 = (m.K + 63) / 64;
-      const int pieces = pieces_of(m.K);
-      for (int k0 = 0; k0 < pieces; k0 += 2) {
-        if (!mbar_wait(&full[stage], phase, abort_flag)) {
+      for (int k = 0; k < n64; k += 4) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag))) {
           fail();
           ok = false;
           break;
         }
         tc_fence_after();
+        const uint64_t ad = ad0 + at, bd = bd0 + at, sd = sd0 + at;
+        const uint32_t ta = sf_tmem + set * kScaleCols, tb = ta + 8 * kMats;
         if (elect_one()) {
-          const uint32_t st = stage0 + stage * p.stage_bytes;
-          const uint32_t sf = st + kMats * kCodeBytesM + p.bn * 128;
-          const uint32_t ts = sf_tmem + set * scale_cols(kMats, p.row_tiles);
-          const int np = min(2, pieces - k0);
-          for (int j = 0; j < np; ++j) {
-            const uint64_t sd = smem_desc_scales(sf + j * kMxPieceBytes);
 #pragma unroll
-            for (int i = 0; i < kMats; ++i)
-              tc_cp_scales(ts + 8 * i + 4 * j, sd + static_cast<uint64_t>(i * (kPairBytes >> 4)));
-            for (int g = 0; g < p.row_tiles; ++g)
-              tc_cp_scales(ts + 8 * kMats + 4 * p.row_tiles * j + 4 * g,
-                           sd + static_cast<uint64_t>((kMats + g) * (kPairBytes >> 4)));
+          for (int j = 0; j < 2; ++j) {
+            if (j == 1 && k + 2 >= n64) break;
+#pragma unroll
+            for (int mat = 0; mat < kMats; ++mat)
+              tc_cp_scales(ta + 8 * mat + 4 * j, sd + mat * (kPairBytes >> 4) + j * (kMxPieceBytes >> 4));
+#pragma unroll
+            for (int g = 0; g < kRowTiles; ++g)
+              tc_cp_scales(tb + 4 * kRowTiles * j + 4 * g, sd + (kMats + g) * (kPairBytes >> 4) + j * (kMxPieceBytes >> 4));
           }
-          const uint64_t ad = smem_desc_sw128_kmajor(st);
-          const uint64_t bd = smem_desc_sw128_kmajor(st + kMats * kCodeBytesM);
-          const int nk = min(4, n64 - 2 * k0);
-          for (int kk = 0; kk < nk; ++kk) {
-            const uint32_t idesc = idesc_mxfp(kMxBM, bn, 2 * (kk & 1));
-            const uint32_t tb = ts + 8 * kMats + 4 * p.row_tiles * (kk >> 1);
-            const uint32_t acc = (k0 | kk) ? 1u : 0u;
 #pragma unroll
-            for (int i = 0; i < kMats; ++i)
-              tc_mma_mxfp(d + i * p.bn, ad + static_cast<uint64_t>(i * (kCodeBytesM >> 4) + 2 * kk), bd + 2 * kk, idesc,
-                          ts + 8 * i + 4 * (kk >> 1), tb, acc);
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk > 0 && k + kk >= n64) break;
+#pragma unroll
+            for (int mat = 0; mat < kMats; ++mat)
+              tc_mma_mxfp(d + mat * p.bn, ad + mat * (kCodeBytesM >> 4) + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0,
+                          ta + 8 * mat + 4 * (kk >> 1), tb + 4 * kRowTiles * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
           }
           tc_commit(&empty[stage]);
+          if (k + 4 >= n64) tc_commit(&acc_full[accb]);
         }
         __syncwarp();
         set ^= 1;
+        at += stage_step;
         if (++stage == p.stages) {
           stage = 0;
+          at = 0;
           phase ^= 1;
         }
       }
-      if (!ok) break;
-      if (elect_one()) tc_commit(&acc_full[accb]);
-      __syncwarp();
       if (++accb == p.acc_bufs) {
         accb = 0;
         accphase ^= 1;
@@ -469,12 +533,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
+    pdl_wait();
+    pdl_launch_dependents();
     const int lanegrp = warp & 3;
     const int colpart = (warp - kEpiWarp0) >> 2;
     int accb = 0;
     uint32_t accphase = 0;
-    for (int it = blockIdx.x; it < s.n_total; it += gridDim.x) {
-      const Item m = get_item(a, maps, p, s, it, kGU);
+    for (int i = 0; i < s.n; ++i) {
+      const Item m = item(i);
       if (!m.ok) {
         if (lane == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
         continue;
@@ -503,11 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int kMode>
+template <int kMode, int kRowTiles>
 cudaError_t launch(int kind, const typename Args<kMode>::maps& maps, const typename Args<kMode>::type& a, const Plan& p,
                    int grid, cudaStream_t stream, bool pdl) {
   const int smem = p.stages * p.stage_bytes + kSmemFixed;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_kernel<kMode>), smem);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_kernel<kMode, kRowTiles>), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -520,7 +586,7 @@ cudaError_t launch(int kind, const typename Args<kMode>::maps& maps, const typen
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   timer_begin(kind, stream);
-  e = cudaLaunchKernelEx(&cfg, mx_gemm_kernel<kMode>, maps, a, p);
+  e = cudaLaunchKernelEx(&cfg, mx_gemm_kernel<kMode, kRowTiles>, maps, a, p);
   timer_end(kind, stream);
   return e;
 }
@@ -531,14 +597,16 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cu
   const Plan p = make_plan(1, a.bn);
   const long long items = static_cast<long long>((a.rows_m + kMxBM - 1) / kMxBM) * ((a.rows_n + a.bn - 1) / a.bn);
   if (items > (1ll << 30)) return cudaErrorInvalidValue;
-  return launch<kLinear>(kKMxGemm, maps, a, p, static_cast<int>(items < a.num_sms ? items : a.num_sms), stream, pdl);
+  const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
+  return p.row_tiles == 1 ? launch<kLinear, 1>(kKMxGemm, maps, a, p, grid, stream, pdl)
+                          : launch<kLinear, 2>(kKMxGemm, maps, a, p, grid, stream, pdl);
 }
 
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream) {
   const int bn = a.I_shared > 0 && a.bn_s > a.bn_r ? a.bn_s : a.bn_r;
-  const cudaError_t e = launch<kGateUp>(kKMxGateUp, maps, a, make_plan(2, bn), a.num_sms, stream, true);
+  const cudaError_t e = launch<kGateUp, 1>(kKMxGateUp, maps, a, make_plan(2, bn), a.num_sms, stream, true);
   if (e != cudaSuccess) return e;
-  return launch<kDown>(kKMxDown, maps, a, make_plan(1, bn), a.num_sms, stream, true);
+  return launch<kDown, 1>(kKMxDown, maps, a, make_plan(1, bn), a.num_sms, stream, true);
 }
 
 }  // namespace bm

@@ -441,6 +441,24 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   return r;
 }
 
+// The values of the two E2M1 codes in bits 0..3 (x) and 4..7 (y).
+__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t codes) {
+  uint32_t h;  // f16x2: exact
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(h)
+      : "r"(codes));
+  float2 f;
+  asm("{\n\t.reg .f16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.f32.f16 %0, l;\n\t"
+      "cvt.f32.f16 %1, h;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
 // Warp-wide D += A B on the tensor cores, m16n8k16, fp32 accumulators; A and B
 // both bf16 (kBF16) or both fp16, two 16-bit elements per register (the lower
 // index in the low half).  Fragment ownership, g = lane/4, q = lane%4:
