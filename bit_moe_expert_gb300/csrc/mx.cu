@@ -17,30 +17,24 @@
 namespace bm {
 namespace {
 
-// One warp per 256 values of a row, kUnits of them in flight.
+// One CTA per 256 columns of 32 rows: those of a 128-row tile whose number mod
+// 32 is one of eight, warp w the rows w mod 8, + 32, + 64 and + 96.  The packed
+// scales of these four rows are neighbours, so a warp writes (or reads) its
+// scales of 128 columns as one 16-byte word (four 4-byte words cost 7 of 38 us
+// at 8192 x 8192), and consecutive CTAs read along the rows.
 constexpr int kQuantThreads = 256;
 constexpr int kUnits = 4;
-
-// The rows and 256-value segments that a warp of the grid takes in turn.
-struct RowWalk {
-  int row, seg;
-  int segs, row_step, seg_step;
-  __device__ __forceinline__ explicit RowWalk(int K) {
-    segs = (K + 255) / 256;
-    const int first = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
-    const int warps = gridDim.x * (kQuantThreads / 32);
-    row = first / segs;
-    seg = first % segs;
-    row_step = warps / segs;
-    seg_step = warps % segs;
-  }
-  __device__ __forceinline__ void next() {
-    row += row_step;
-    seg += seg_step;
-    if (seg >= segs) {
-      seg -= segs;
-      ++row;
-    }
+struct Patch {
+  int row, col;       // first row and column of this lane
+  long long scales;   // byte offset of the 16 bytes of this lane's 128 columns
+  __device__ __forceinline__ explicit Patch(int K) {
+    const int segs = (K + 255) / 256, pieces = (K + kMxPieceK - 1) / kMxPieceK;
+    const int lane = threadIdx.x & 31;
+    const int seg = blockIdx.x % segs, part = blockIdx.x / segs;  // part: 4 a tile
+    const int r = (part & 3) * 8 + (threadIdx.x >> 5);
+    row = (part >> 2) * kMxPieceRows + r;
+    col = seg * 256 + 8 * lane;
+    scales = (static_cast<long long>(part >> 2) * pieces + col / kMxPieceK) * kMxPieceBytes + r * 16;
   }
 };
 
@@ -48,32 +42,73 @@ template <int kType>
 __global__ void __launch_bounds__(kQuantThreads)
     mx_quantize_kernel(const void* __restrict__ X, int rows, int K, long long ldx, uint8_t* __restrict__ q,
                        uint8_t* __restrict__ sp) {
+  const Patch at(K);
+  const int lane = threadIdx.x & 31;
+  const int esize = kType == kFp32 ? 4 : 2;
   pdl_wait();
   pdl_launch_dependents();
+  Load8<kType> x[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (at.row + 32 * i < rows && at.col < K)
+      x[i].load(static_cast<const char*>(X) + static_cast<size_t>(at.row + 32 * i) * ldx * esize, at.col);
+    else
+      x[i].zero();
+  }
+  uint32_t scales[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t code = quantize8(x[i], scales[i], lane);
+    if (at.row + 32 * i < rows && at.col < K)
+      *reinterpret_cast<uint32_t*>(q + static_cast<size_t>(at.row + 32 * i) * (K / 2) + at.col / 2) = code;
+  }
+  if ((lane & 15) == 0 && at.row < rows && at.col < K)
+    *reinterpret_cast<uint4*>(sp + at.scales) = make_uint4(scales[0], scales[1], scales[2], scales[3]);
+}
+
+// The same division of work within each matrix (blockIdx.y).
+template <int kType>
+__global__ void __launch_bounds__(kQuantThreads)
+    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int N, int K, void* __restrict__ W) {
+  const Patch at(K);
   const int lane = threadIdx.x & 31;
   const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
-  const int esize = kType == kFp32 ? 4 : 2;
-  RowWalk at(K);
-  while (at.row < rows) {
-    Load8<kType> x[kUnits];
-    int row[kUnits], col[kUnits];
+  const size_t matrix = static_cast<size_t>(blockIdx.y) * N;
+  sp += blockIdx.y * static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (at.row >= N || at.col >= K) return;
+  uint32_t code[kUnits];
+  const size_t first = (matrix + at.row) * (K / 8) + at.col / 8;  // in words of eight codes
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i, at.next()) {
-      row[i] = at.row;
-      col[i] = at.seg * 256 + 8 * lane;
-      if (row[i] < rows && col[i] < K)
-        x[i].load(static_cast<const char*>(X) + static_cast<size_t>(row[i]) * ldx * esize, col[i]);
-      else
-        x[i].zero();
+  for (int i = 0; i < kUnits; ++i)
+    code[i] = at.row + 32 * i < N ? __ldg(reinterpret_cast<const uint32_t*>(q) + first + static_cast<size_t>(32 * i) * (K / 8)) : 0u;
+  const uint4 sw = __ldg(reinterpret_cast<const uint4*>(sp + at.scales));
+  const uint32_t scales[kUnits] = {sw.x, sw.y, sw.z, sw.w};
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (at.row + 32 * i >= N) break;
+    const size_t to = first + static_cast<size_t>(32 * i) * (K / 8);
+    const float s = mx_scale((scales[i] >> (8 * ((lane >> 2) & 3))) & 255u);
+    float2 f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = e2m1x2_to_float2(code[i] >> (8 * j));
+      f[j].x *= s;
+      f[j].y *= s;
     }
+    if constexpr (kType == kFp32) {
+      float4* p = reinterpret_cast<float4*>(W) + 2 * to;
+      p[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      p[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    } else {
+      uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      if (row[i] >= rows) break;  // the same for the whole warp
-      uint32_t scales;
-      const uint32_t code = quantize8(x[i], scales, lane);
-      if (col[i] < K) *reinterpret_cast<uint32_t*>(q + static_cast<size_t>(row[i]) * (K / 2) + col[i] / 2) = code;
-      if ((lane & 15) == 0 && col[i] < K)
-        *reinterpret_cast<uint32_t*>(sp + mx_scale_offset(row[i], col[i] / kMxPieceK, pieces)) = scales;
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __float22bfloat162_rn(f[j]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      reinterpret_cast<uint4*>(W)[to] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -140,59 +175,6 @@ __global__ void __launch_bounds__(kScatterThreads)
   }
 }
 
-// The same division of work within each matrix (blockIdx.y).
-template <int kType>
-__global__ void __launch_bounds__(kQuantThreads)
-    mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sp, int N, int K, void* __restrict__ W) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int pieces = (K + kMxPieceK - 1) / kMxPieceK;
-  const size_t matrix = static_cast<size_t>(blockIdx.y) * N;
-  sp += blockIdx.y * static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
-  RowWalk at(K);
-  while (at.row < N) {
-    uint32_t code[kUnits];
-    uint32_t byte[kUnits];
-    size_t to[kUnits];
-    bool in[kUnits];
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i, at.next()) {
-      const int c = at.seg * 256 + 8 * lane;
-      in[i] = at.row < N && c < K;
-      if (!in[i]) continue;
-      to[i] = (matrix + at.row) * (K / 8) + c / 8;
-      code[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + to[i]);
-      byte[i] = __ldg(sp + mx_scale_offset(at.row, c / kMxPieceK, pieces) + (c % kMxPieceK) / kMxBlock);
-    }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      if (!in[i]) continue;
-      const float s = mx_scale(byte[i]);
-      float2 f[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[j] = e2m1x2_to_float2(code[i] >> (8 * j));
-        f[j].x *= s;
-        f[j].y *= s;
-      }
-      if constexpr (kType == kFp32) {
-        float4* p = reinterpret_cast<float4*>(W) + 2 * to[i];
-        p[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-        p[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-      } else {
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 b = __float22bfloat162_rn(f[j]);
-          o[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        reinterpret_cast<uint4*>(W)[to[i]] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    }
-  }
-}
-
 // One thread per 32-bit word of the packed scales: four blocks of one row.
 __global__ void mx_prepack_kernel(const uint8_t* __restrict__ scale, int E, int N, int G, uint8_t* __restrict__ sp) {
   const int pieces = (G + 3) / 4;
@@ -238,6 +220,11 @@ int blocks_for(size_t threads, int per_block, int most) {
   return static_cast<int>(n < 1 ? 1 : n < static_cast<size_t>(most) ? n : most);
 }
 
+// CTAs of a matrix's quantisation: 256 columns of 32 rows each.
+size_t patches(int rows, int K) {
+  return static_cast<size_t>((rows + kMxPieceRows - 1) / kMxPieceRows) * 4 * ((K + 255) / 256);
+}
+
 }  // namespace
 
 cudaError_t launch_mx_prepack(const uint8_t* scale, int E, int N, int K, uint8_t* sp, cudaStream_t stream) {
@@ -247,19 +234,19 @@ cudaError_t launch_mx_prepack(const uint8_t* scale, int E, int N, int K, uint8_t
 }
 
 cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, uint8_t* sp,
-                               int num_sms, cudaStream_t stream, bool pdl) {
-  const size_t units = static_cast<size_t>(rows) * ((K + 255) / 256);
-  const int grid = blocks_for(units, kQuantThreads / 32, num_sms * 8);
+                               cudaStream_t stream, bool pdl) {
+  const size_t grid = patches(rows, K);
+  if (grid > 0x7FFFFFFFu) return cudaErrorInvalidValue;
   const auto kernel = type == kBf16 ? mx_quantize_kernel<kBf16>
                                     : (type == kFp16 ? mx_quantize_kernel<kFp16> : mx_quantize_kernel<kFp32>);
-  return launch(kKMxQuantize, kernel, grid, kQuantThreads, stream, pdl, X, rows, K, ldx, q, sp);
+  return launch(kKMxQuantize, kernel, dim3(static_cast<unsigned>(grid)), kQuantThreads, stream, pdl, X, rows, K, ldx, q, sp);
 }
 
-cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W, int num_sms,
+cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W,
                               cudaStream_t stream, bool pdl) {
-  const int most = num_sms * 8 / E;
-  const int grid = blocks_for(static_cast<size_t>(N) * ((K + 255) / 256), kQuantThreads / 32, most > 1 ? most : 1);
-  return launch(kKMxQuantize, type == kFp32 ? mx_dequant_kernel<kFp32> : mx_dequant_kernel<kBf16>, dim3(grid, E),
+  const size_t grid = patches(N, K);
+  if (grid > 0x7FFFFFFFu) return cudaErrorInvalidValue;
+  return launch(kKMxQuantize, type == kFp32 ? mx_dequant_kernel<kFp32> : mx_dequant_kernel<kBf16>, dim3(static_cast<unsigned>(grid), E),
                 kQuantThreads, stream, pdl, q, sp, N, K, W);
 }
 

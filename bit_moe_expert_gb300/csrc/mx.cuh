@@ -83,16 +83,17 @@ template <int kType>
 __device__ __forceinline__ uint32_t quantize8(const Load8<kType>& x, uint32_t& scales, int lane) {
   float f[8];
   x.floats(f);
-  uint32_t a = 0;
+  float m = fabsf(f[0]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  for (int j = 1; j < 8; ++j) m = max_nan(m, fabsf(f[j]));
+  uint32_t a = __float_as_uint(m);  // a NaN's bits are above infinity's
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
   const uint32_t byte = mx_scale_byte(a);
   const float inv = mx_inverse_scale(byte);
-  uint32_t code = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) code |= f32x2_to_e2m1x2(f[2 * j] * inv, f[2 * j + 1] * inv) << (8 * j);
+  for (int j = 0; j < 8; ++j) f[j] *= inv;
+  const uint32_t code = f32x8_to_e2m1x8(f);
   scales = byte << (8 * ((lane >> 2) & 3));
   scales |= __shfl_xor_sync(0xffffffffu, scales, 4);
   scales |= __shfl_xor_sync(0xffffffffu, scales, 8);

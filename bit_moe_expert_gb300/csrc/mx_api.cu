@@ -260,9 +260,7 @@ moe_status moe_mx_quantize(const void* X, moe_dtype type, int rows, int K, long 
   if (st != MOE_OK) return st;
   if (!out || !mat_ok(*out)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  const int sms = device_sms();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  return launch_mx_quantize(X, type, rows, K, ldx, out->q, out->sp, sms, reinterpret_cast<cudaStream_t>(stream),
+  return launch_mx_quantize(X, type, rows, K, ldx, out->q, out->sp, reinterpret_cast<cudaStream_t>(stream),
                             pdl_enabled()) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
@@ -271,9 +269,7 @@ moe_status moe_mx_quantize(const void* X, moe_dtype type, int rows, int K, long 
 moe_status moe_mx_dequant(const moe_mx_mat* m, int E, int N, int K, moe_dtype type, void* W, moe_stream stream) {
   if (!m || !mat_ok(*m) || E < 1 || !size_ok(N, K) || !type_ok(type) || !W || !aligned16(W)) return MOE_ERR_INVALID_ARG;
   if (type == MOE_FP16 || E > 65535 || N > kMaxRows) return MOE_ERR_UNSUPPORTED;
-  const int sms = device_sms();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  return launch_mx_dequant(m->q, m->sp, E, N, K, type, W, sms, reinterpret_cast<cudaStream_t>(stream),
+  return launch_mx_dequant(m->q, m->sp, E, N, K, type, W, reinterpret_cast<cudaStream_t>(stream),
                            pdl_enabled()) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;

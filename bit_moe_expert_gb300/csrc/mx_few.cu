@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* last_flag = const_cast<int*>(abort_flag) + 1;
 
-  const int warp = threadIdx.x >> 5;
+  // the same in all lanes, so that the roles' branches are known to be uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < plan.ring; ++i) {
@@ -379,38 +380,46 @@ __global__ void __launch_bounds__(kThreads)
     pdl_launch_dependents();
     const Item m = get_item<kMode>(p);
     if (warp == kMmaWarp) {
-      if (m.some && m.ok) {
-        const int pieces = pieces_of(m.K), n64 = (m.K + 63) / 64;
-        const int bn = (m.rows + 15) & ~15;
-        int stage = 0;
-        uint32_t phase = 0, set = 0;
-        bool ok = mbar_wait(b_full, 0, abort_flag);
+      // issued by one thread, computed by the warp from values that are the same
+      // in all lanes (uniform registers)
+      const int rows = __shfl_sync(0xffffffffu, m.some && m.ok ? m.rows : 0, 0);
+      if (rows > 0) {
+        const int n64 = (__shfl_sync(0xffffffffu, m.K, 0) + 63) / 64;
+        const int bn = (rows + 15) & ~15;
+        const uint32_t idesc0 = idesc_mxfp(kMxBM, bn, 0), idesc1 = idesc_mxfp(kMxBM, bn, 2);
+        const uint64_t ad0 = smem_desc_sw128_kmajor(smem_u32(ring)), bd0 = smem_desc_sw128_kmajor(smem_u32(b));
+        const uint64_t sa0 = smem_desc_scales(smem_u32(sa)), sb0 = smem_desc_scales(smem_u32(sb));
+        int stage = 0, s = 0;
+        uint32_t phase = 0;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(b_full, 0, abort_flag));
         if (!ok) fail();
-        for (int k0 = 0; ok && k0 < pieces; k0 += 2) {
-          ok = mbar_wait(&full[stage], phase, abort_flag);
+        for (int k = 0; ok && k < n64; k += 4, ++s) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag));
           if (!ok) {
             fail();
             break;
           }
           tc_fence_after();
+          const uint64_t ad = ad0 + stage * (kABytes >> 4), bd = bd0 + static_cast<uint32_t>(s * plan.b_bytes() >> 4);
+          const uint64_t ad_s = sa0 + stage * (kPairBytes >> 4), bd_s = sb0 + s * (kPairBytes >> 4);
+          const uint32_t ta = tmem + kTmemSA + 8 * (s & 1), tb = tmem + kTmemSB + 8 * (s & 1);
           if (elect_one()) {
-            const int np = min(2, pieces - k0), s = k0 >> 1;
-            const uint32_t ta = tmem + kTmemSA + 8 * set, tb = tmem + kTmemSB + 8 * set;
-            for (int j = 0; j < np; ++j) {
-              tc_cp_scales(ta + 4 * j, smem_desc_scales(smem_u32(sa) + stage * kPairBytes + j * kMxPieceBytes));
-              tc_cp_scales(tb + 4 * j, smem_desc_scales(smem_u32(sb) + s * kPairBytes + j * kMxPieceBytes));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (j == 1 && k + 2 >= n64) break;
+              tc_cp_scales(ta + 4 * j, ad_s + j * (kMxPieceBytes >> 4));
+              tc_cp_scales(tb + 4 * j, bd_s + j * (kMxPieceBytes >> 4));
             }
-            const uint64_t ad = smem_desc_sw128_kmajor(smem_u32(ring) + stage * kABytes);
-            const uint64_t bd = smem_desc_sw128_kmajor(smem_u32(b) + s * plan.b_bytes());
-            const int nk = min(4, n64 - 2 * k0);
-            for (int kk = 0; kk < nk; ++kk)
-              tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, idesc_mxfp(kMxBM, bn, 2 * (kk & 1)), ta + 4 * (kk >> 1),
-                          tb + 4 * (kk >> 1), (k0 | kk) ? 1u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk > 0 && k + kk >= n64) break;
+              tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0, ta + 4 * (kk >> 1), tb + 4 * (kk >> 1),
+                          (k > 0 || kk > 0) ? 1u : 0u);
+            }
             tc_commit(&empty[stage]);
-            if (k0 + 2 >= pieces) tc_commit(acc_full);
+            if (k + 4 >= n64) tc_commit(acc_full);
           }
           __syncwarp();
-          set ^= 1;
           if (++stage == plan.ring) {
             stage = 0;
             phase ^= 1;

@@ -429,8 +429,8 @@ __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
   return r;
 }
 
-// Two fp32 values -> two E2M1 codes (round to nearest even, magnitudes above 6
-// to 6) in bits 0..3 (lo) and 4..7 (hi).
+// fp32 values -> E2M1 codes (round to nearest even, magnitudes above 6 to 6),
+// the first value's in bits 0..3.
 __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   uint32_t r;
   asm("{\n\t.reg .b8 b;\n\t"
@@ -438,6 +438,24 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
       "mov.b32 %0, {b, 0, 0, 0};\n\t}"
       : "=r"(r)
       : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&f)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+// The larger value; NaN if either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
