@@ -165,14 +165,19 @@ def _check(fn: str, status: int):
         raise MoeError(fn, status)
 
 
+_raw_stream = None  # (the current stream's raw handle of a device, the current device), found at the first call
+
+
 def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:  # the current stream's handle without building a Stream object (~0.2 against ~3 us)
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # the handle without building a Stream object (~0.2 against ~3 us)
+        _raw_stream = (raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream), torch.cuda.current_device)
+    return _raw_stream[0](_raw_stream[1]())
 
 
 def _ptr(t) -> int:

@@ -44,6 +44,35 @@ moe_status check_matmul(int M, const moe_mx_mat* W, int N, int K, const void* Y,
   return MOE_OK;
 }
 
+// Which operand of the dense product is the MMA's M side (tiles of 128 rows), and
+// the height bn of the other's tiles.  Modelled time in clocks, fitted to
+// FITTED: a CTA's tiles in turn, each a stage of K = 256 after another at the
+// rate its bytes arrive, and the filling of the pipeline and the epilogue.
+// Tokens are the M side only where Y's rows take 16-byte stores (a lane then
+// holds part of a row; otherwise neighbouring lanes hold neighbours of a row).
+struct Shape {
+  bool weights_m;
+  int bn;
+};
+Shape linear_shape(int M, int N, int K, int y_bytes, int num_sms) {
+  Shape best{true, 0};
+  double least = 0;
+  for (int weights_m = 0; weights_m < 2; ++weights_m) {
+    if (!weights_m && static_cast<long long>(N) * y_bytes % 16 != 0) continue;
+    const int P = weights_m ? N : M, Q = weights_m ? M : N;
+    for (int bn : {64, 128, 256, Q <= kMxMaxBN ? round16(Q) : 64}) {
+      const double tiles = static_cast<double>((P + kMxBM - 1) / kMxBM) * ((Q + bn - 1) / bn);
+      const double turns = static_cast<double>(static_cast<long long>((tiles + num_sms - 1) / num_sms));
+      const double clocks = turns * ((K + kMxStageK - 1) / kMxStageK * (290 + 2.3 * bn) + 1500 + 8 * bn);
+      if (best.bn == 0 || clocks < least) {
+        least = clocks;
+        best = Shape{weights_m != 0, bn};
+      }
+    }
+  }
+  return best;
+}
+
 moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K, void* Y, moe_dtype y_type,
                   uint32_t* status, moe_stream stream) {
   MxLinearArgs a{};
@@ -54,17 +83,16 @@ moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K,
   a.status = status;
   a.num_sms = device_sms();
   if (a.num_sms <= 0) return MOE_ERR_CUDA;
-  // few tokens: the weights are the M side, every token in one N tile
-  const bool swap = M <= kMxMaxBN;
-  const moe_mx_mat &m = swap ? W : A, &n = swap ? A : W;
+  const Shape sh = linear_shape(M, N, K, a.y_fp32 ? 4 : 2, a.num_sms);
+  const moe_mx_mat &m = sh.weights_m ? W : A, &n = sh.weights_m ? A : W;
   a.sp_m = m.sp;
   a.sp_n = n.sp;
-  a.rows_m = swap ? N : M;
-  a.rows_n = swap ? M : N;
-  a.stride_m = swap ? 1 : N;
-  a.stride_n = swap ? N : 1;
-  a.weights_n = !swap;
-  a.bn = swap ? round16(M) : 256;
+  a.rows_m = sh.weights_m ? N : M;
+  a.rows_n = sh.weights_m ? M : N;
+  a.stride_m = sh.weights_m ? 1 : N;
+  a.stride_n = sh.weights_m ? N : 1;
+  a.weights_n = !sh.weights_m;
+  a.bn = sh.bn;
   if (!encode_mx_codes(&maps.m, m.q, a.rows_m, K / 2, kMxBM) || !encode_mx_codes(&maps.n, n.q, a.rows_n, K / 2, a.bn))
     return MOE_ERR_CUDA;
   return launch_mx_linear(a, maps, reinterpret_cast<cudaStream_t>(stream), pdl_enabled()) == cudaSuccess ? MOE_OK

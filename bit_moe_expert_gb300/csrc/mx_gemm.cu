@@ -474,6 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rows == 0) continue;
       const int n64 = (__shfl_sync(0xffffffffu, m.K, 0) + 63) / 64;
       const int bn = tile_n(rows);
+      // a tile that starts inside a 128-row piece (64 rows high) finds its scales further on, 32 rows a column
+      const uint32_t shift = kMode == kLinear ? __shfl_sync(0xffffffffu, m.row_n % kMxPieceRows, 0) / 32 : 0;
       const uint32_t idesc0 = idesc_mxfp(kMxBM, bn, 0), idesc1 = idesc_mxfp(kMxBM, bn, 2);
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[accb], accphase ^ 1, abort_flag))) {
         fail();
@@ -490,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint64_t ad = ad0 + at, bd = bd0 + at, sd = sd0 + at;
         const uint32_t ta = sf_tmem + set * kScaleCols, tb = ta + 8 * kMats;
+        const uint32_t tbm = tb + shift;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int mat = 0; mat < kMats; ++mat)
               tc_mma_mxfp(d + mat * p.bn, ad + mat * (kCodeBytesM >> 4) + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0,
-                          ta + 8 * mat + 4 * (kk >> 1), tb + 4 * kRowTiles * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
+                          ta + 8 * mat + 4 * (kk >> 1), tbm + 4 * kRowTiles * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
           }
           tc_commit(&empty[stage]);
           if (k + 4 >= n64) tc_commit(&acc_full[accb]);

@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr size_t kOneChunkSmem = 12 * 1024;  // dynamic shared memory beside the static arrays without raising the limit
 constexpr int kGridsyncChunks = 2047;       // chunks of a grid-synchronised launch: their counts are summed in 16 bits
 constexpr int kBasesSmemLimit = 96 * 1024;  // per-chunk bases kept in shared memory up to this size
 // Tokens per weight CTA (one per warp; the CTA's other warps leave at once).
@@ -428,26 +429,28 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
                             : (E <= 256 ? route_kernel<8, false> : route_kernel<32, false>);
   const size_t scored_smem = score ? static_cast<size_t>(kRouteWarps) * scored_bytes(sc, E) : 0;
 
-  // CTAs resident at once, without the bases (the grid-synchronised mode has none).
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kBasesSmemLimit);
-  if (e != cudaSuccess) return e;
-  e = occupancy_per_sm(reinterpret_cast<const void*>(kernel), kRouteThreads, scored_smem, &per_sm);
-  if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int resident = sms * per_sm;
-  // Grid-synchronised mode when every chunk's CTA can be resident at once
-  // (leaving room for other work); otherwise the last CTA finishes alone.
-  // MOE_ROUTE_MODE=ticket or =gridsync forces one of them (A/B and tests; a
-  // forced grid-synchronised launch still needs every CTA resident, so it is
-  // only taken when they fit).
-  int gridsync = (nchunks > 1 && nchunks <= kGridsyncChunks && nchunks <= resident / 2) ? 1 : 0;
-  if (const char* m = std::getenv("MOE_ROUTE_MODE")) {
-    if (!std::strcmp(m, "ticket")) gridsync = 0;
-    if (!std::strcmp(m, "gridsync") && nchunks > 1 && nchunks <= kGridsyncChunks && nchunks <= resident) gridsync = 1;
+  int gridsync = 0, resident = 0;
+  if (nchunks > 1) {  // one chunk needs none of this, and its call is all host time
+    // CTAs resident at once, without the bases (the grid-synchronised mode has none).
+    int per_sm = 0;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kBasesSmemLimit);
+    if (e != cudaSuccess) return e;
+    e = occupancy_per_sm(reinterpret_cast<const void*>(kernel), kRouteThreads, scored_smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    resident = device_sms() * per_sm;
+    // Grid-synchronised mode when every chunk's CTA can be resident at once
+    // (leaving room for other work); otherwise the last CTA finishes alone.
+    // MOE_ROUTE_MODE=ticket or =gridsync forces one of them (A/B and tests; a
+    // forced grid-synchronised launch still needs every CTA resident, so it is
+    // only taken when they fit).
+    gridsync = (nchunks <= kGridsyncChunks && nchunks <= resident / 2) ? 1 : 0;
+    if (const char* m = std::getenv("MOE_ROUTE_MODE")) {
+      if (!std::strcmp(m, "ticket")) gridsync = 0;
+      if (!std::strcmp(m, "gridsync") && nchunks <= kGridsyncChunks && nchunks <= resident) gridsync = 1;
+    }
+  } else if (scored_smem > kOneChunkSmem) {
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kBasesSmemLimit);
+    if (e != cudaSuccess) return e;
   }
   const int nweight = score ? 0 : (T + kWeightTokensPerCta - 1) / kWeightTokensPerCta;  // weight CTAs
   cudaLaunchConfig_t cfg = {};
