@@ -48,7 +48,14 @@ static_assert(kMxFewT <= static_cast<int>(kTmemSA), "one accumulator column a to
 struct Plan {
   int bn, stages, ring;  // stages: of K = 256, at most, in an item
   __host__ __device__ int b_bytes() const { return bn * 128; }
-  __host__ __device__ int smem() const { return ring * (kABytes + kPairBytes) + stages * (b_bytes() + kPairBytes) + kSmemFixed; }
+  // The tokens' scales: at most 32 rows, so of the four words of 16 bytes that
+  // a copy to tensor memory takes per row, two are a stage's two pieces along K
+  // instead of groups of 32 rows: one copy a stage, not two (a copy holds the
+  // tensor pipeline up for about 65 clocks).
+  __host__ __device__ int sb_bytes() const { return stages * kMxPieceBytes; }
+  __host__ __device__ int smem() const {
+    return ring * (kABytes + kPairBytes) + stages * b_bytes() + sb_bytes() + kSmemFixed;
+  }
 };
 
 Plan make_plan(int bn, int K) {
@@ -126,12 +133,13 @@ __device__ __forceinline__ Item get_item(const ExpertParams& p) {
     i -= mt_s * kMats;
     const int tile = i / (mt_r * kMats);
     i -= tile * (mt_r * kMats);
-    m.some = tile < routed_tiles(a);
-    if (!m.some) return m;
+    // the entry exists (the grid has at most max_blocks tiles), whether valid or not: one round trip for all of it
     const volatile int32_t* b = a.block_map + 3 * tile;
     e = b[0];
     m.row0 = b[1];
     m.rows = b[2];
+    m.some = tile < routed_tiles(a);
+    if (!m.some) return m;
     m.N = kGU ? a.I : a.d;
     m.K = kGU ? a.d : a.I;
     m.ok = e >= 0 && e < a.E && m.rows >= 1 && m.rows <= a.bn && m.row0 >= 0 && m.row0 + m.rows <= a.T * a.k;
@@ -157,7 +165,7 @@ __device__ __forceinline__ void put_row(uint8_t* b, uint8_t* sf, const Plan& p, 
                                         int lane) {
   *reinterpret_cast<uint32_t*>(b + s * p.b_bytes() + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)) = code;
   if ((lane & 15) == 0)
-    *reinterpret_cast<uint32_t*>(sf + s * kPairBytes + (lane >> 4) * kMxPieceBytes + (r & 31) * 16) = scales;
+    *reinterpret_cast<uint32_t*>(sf + s * kMxPieceBytes + r * 16 + 8 * (lane >> 4)) = scales;
 }
 
 // The N operand from activations: row r of the tile is row_of(r).
@@ -235,7 +243,7 @@ __device__ __forceinline__ void prologue(const ExpertParams& p, uint8_t* b, uint
         const int s = c >> 3, chunk = c & 7;  // 32 codes: one 16-byte chunk of the stage's line
         if ((lane & 7) == 0)
           *reinterpret_cast<uint32_t*>(b + s * plan.b_bytes() + r * 128 + ((chunk ^ (r & 7)) << 4) + 4 * (lane >> 3)) = code;
-        if (lane == 0) sf[s * kPairBytes + (chunk >> 2) * kMxPieceBytes + (r & 31) * 16 + (chunk & 3)] = static_cast<uint8_t>(byte);
+        if (lane == 0) sf[s * kMxPieceBytes + r * 16 + 8 * (chunk >> 2) + (chunk & 3)] = static_cast<uint8_t>(byte);
       }
     }
   }
@@ -267,32 +275,64 @@ __device__ __forceinline__ void store16(const ExpertParams& p, const Item& m, in
     if (c0 + c < m.rows) y[c * step] = __uint_as_float(v[c]);
 }
 
+// Up to eight of a token's slots: their rows (-1: none) and weights.
+struct Slots {
+  int row[8];
+  float w[8];
+  // those of thread i's first token from slot j0 on
+  __device__ __forceinline__ void load(const MxFewArgs& a, int i, int j0 = 0) {
+    const int t = i / kMxBM, A = a.T * a.k;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = t < a.T && j0 + u < a.k;
+      row[u] = in ? __ldg(a.inv_perm + t * a.k + j0 + u) : -1;
+      w[u] = in ? __ldg(a.w + t * a.k + j0 + u) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (t >= a.T || j0 + u >= a.k) continue;
+      if (row[u] < 0 || row[u] >= A) {  // a malformed permutation
+        record_status(a.status, MOE_ERR_INVALID_ARG);
+        row[u] = -1;
+      }
+    }
+  }
+};
+
 // Y's columns 128 mt .. 128 mt + 127 of every token: the experts' rows in slot
-// order, the shared expert's last (combine_kernel's arithmetic).
-__device__ __forceinline__ void combine_columns(const MxFewArgs& a, int mt, int i0) {
+// order, the shared expert's last (combine_kernel's arithmetic).  `slots`: the
+// first token's first slots, loaded ahead.
+__device__ __forceinline__ void combine_columns(const MxFewArgs& a, int mt, int i0, Slots& slots) {
   const size_t A = static_cast<size_t>(a.T) * a.k;
   for (int i = i0; i < a.T * kMxBM; i += kWorkWarps * 32) {
     const int t = i / kMxBM, n = mt * kMxBM + i % kMxBM;
-    if (n >= a.d) continue;
     float acc = 0.0f;
+    const bool in = n < a.d;
+    const float sh = in && a.I_shared > 0 ? __ldcg(a.ypart + (A + t) * a.d + n) : 0.0f;
     for (int j0 = 0; j0 < a.k; j0 += 8) {
-      float v[8], wj[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int j = j0 + u;
-        const int pr = j < a.k ? __ldg(a.inv_perm + static_cast<size_t>(t) * a.k + j) : -1;
-        const bool in = pr >= 0 && static_cast<size_t>(pr) < A;
-        if (j < a.k && !in) record_status(a.status, MOE_ERR_INVALID_ARG);
-        wj[u] = in ? __ldg(a.w + static_cast<size_t>(t) * a.k + j) : 0.0f;
-        v[u] = in ? __ldcg(a.ypart + static_cast<size_t>(pr) * a.d + n) : 0.0f;
-      }
+      if (i != i0 || j0 > 0) slots.load(a, i, j0);
+      float v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (j0 + u < a.k) acc = fmaf(wj[u], v[u], acc);
+        v[u] = in && slots.row[u] >= 0 ? __ldcg(a.ypart + static_cast<size_t>(slots.row[u]) * a.d + n) : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (slots.row[u] >= 0) acc = fmaf(slots.w[u], v[u], acc);
     }
-    if (a.I_shared > 0) acc += __ldcg(a.ypart + (A + t) * a.d + n);
-    a.Y[static_cast<size_t>(t) * a.d + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc));
+    if (a.I_shared > 0) acc += sh;
+    if (in) a.Y[static_cast<size_t>(t) * a.d + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc));
   }
+}
+
+__device__ __forceinline__ int shared_items(const LinearParams&) { return 0; }
+__device__ __forceinline__ int shared_items(const ExpertParams& p) {  // of the gate/up product
+  return 2 * ((p.a.I_shared + kMxBM - 1) / kMxBM);
+}
+
+// Lane 0's value.
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (static_cast<uint64_t>(__shfl_sync(0xffffffffu, static_cast<uint32_t>(v >> 32), 0)) << 32) |
+         __shfl_sync(0xffffffffu, static_cast<uint32_t>(v), 0);
 }
 
 template <int kMode, int kType>
@@ -303,7 +343,7 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* b = ring + plan.ring * kABytes;
   uint8_t* sa = b + plan.stages * plan.b_bytes();
   uint8_t* sb = sa + plan.ring * kPairBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sb + plan.stages * kPairBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + plan.sb_bytes());
   uint64_t* empty = full + kMaxRing;
   uint64_t* b_full = empty + kMaxRing;
   uint64_t* acc_full = b_full + 1;
@@ -340,45 +380,49 @@ __global__ void __launch_bounds__(kThreads)
     *abort_flag = 1;
   };
 
+  // The routed experts of the gate/up product are known only after the wait.
+  const bool early = kMode != kGateUp || static_cast<int>(blockIdx.x) < shared_items(p);
+  if (!early || warp != kProducerWarp) {
+    if (kMode != kDown) pdl_wait();
+  }
+  // (the down product's routing has completed: see above)
+  const Item m = get_item<kMode>(p);
+  if (kMode == kDown && warp != kProducerWarp) pdl_wait();
+  if (warp != kProducerWarp) pdl_launch_dependents();
+
   if (warp == kProducerWarp) {
-    if (lane == 0) {
-      // the routed experts of the gate/up product are known only after the wait
-      bool early = true;
-      if constexpr (kMode == kGateUp) early = static_cast<int>(blockIdx.x) < 2 * ((p.a.I_shared + kMxBM - 1) / kMxBM);
-      if (!early) pdl_wait();
-      const Item m = get_item<kMode>(p);
-      if (m.some && m.ok) {
-        const int pieces = pieces_of(m.K);
-        int stage = 0, filled = 0;
-        uint32_t phase = 0;
-        for (int k0 = 0; k0 < pieces; k0 += 2, ++filled) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
-            fail();
-            break;
-          }
-          const uint32_t sbytes = min(2, pieces - k0) * kMxPieceBytes;
-          mbar_arrive_expect_tx(&full[stage], kABytes + sbytes);
-          tma_load_2d(ring + stage * kABytes, m.map, &full[stage], k0 * 64, m.row_m);
-          bulk_g2s(sa + stage * kPairBytes, m.scales + static_cast<size_t>(k0) * kMxPieceBytes, sbytes, &full[stage]);
-          if (++stage == plan.ring) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-        // never leave while a load into this CTA's shared memory may be in flight
-        for (int i = 0; i < min(filled, plan.ring); ++i) {
-          stage = stage == 0 ? plan.ring - 1 : stage - 1;
-          if (stage == plan.ring - 1) phase ^= 1;
-          if (!mbar_wait(&full[stage], phase, nullptr)) record_status(status, MOE_ERR_TIMEOUT);
-        }
+    // one thread issues; what it issues is the same in all lanes (uniform registers)
+    const int n = __shfl_sync(0xffffffffu, m.some && m.ok ? pieces_of(m.K) : 0, 0);
+    const int row_m = __shfl_sync(0xffffffffu, m.row_m, 0);
+    const CUtensorMap* map = reinterpret_cast<const CUtensorMap*>(uniform64(reinterpret_cast<uint64_t>(m.map)));
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>(uniform64(reinterpret_cast<uint64_t>(m.scales)));
+    int stage = 0, filled = 0;
+    uint32_t phase = 0;
+    for (int k0 = 0; k0 < n; k0 += 2, ++filled) {
+      if (!mbar_wait_quick(&empty[stage], phase ^ 1, abort_flag)) {
+        fail();
+        break;
       }
-      if (early) pdl_wait();
+      if (elect_one()) {
+        const uint32_t sbytes = min(2, n - k0) * kMxPieceBytes;
+        mbar_arrive_expect_tx(&full[stage], kABytes + sbytes);
+        tma_load_2d(ring + stage * kABytes, map, &full[stage], k0 * 64, row_m);
+        bulk_g2s(sa + stage * kPairBytes, scales + static_cast<size_t>(k0) * kMxPieceBytes, sbytes, &full[stage]);
+      }
+      __syncwarp();
+      if (++stage == plan.ring) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    __syncwarp();
+    // never leave while a load into this CTA's shared memory may be in flight
+    for (int i = 0; i < min(filled, plan.ring); ++i) {
+      stage = stage == 0 ? plan.ring - 1 : stage - 1;
+      if (stage == plan.ring - 1) phase ^= 1;
+      if (!mbar_wait(&full[stage], phase, nullptr)) record_status(status, MOE_ERR_TIMEOUT);
+    }
+    if (early) pdl_wait();
   } else {
-    pdl_wait();
-    pdl_launch_dependents();
-    const Item m = get_item<kMode>(p);
     if (warp == kMmaWarp) {
       // issued by one thread, computed by the warp from values that are the same
       // in all lanes (uniform registers)
@@ -391,30 +435,28 @@ __global__ void __launch_bounds__(kThreads)
         const uint64_t sa0 = smem_desc_scales(smem_u32(sa)), sb0 = smem_desc_scales(smem_u32(sb));
         int stage = 0, s = 0;
         uint32_t phase = 0;
-        bool ok = __all_sync(0xffffffffu, mbar_wait(b_full, 0, abort_flag));
-        if (!ok) fail();
-        for (int k = 0; ok && k < n64; k += 4, ++s) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag));
-          if (!ok) {
-            fail();
-            break;
-          }
+        // a wait that gives up is recorded and the loop goes on (its later waits
+        // end at the flag): leaving it would make the loop's state differ
+        // between lanes, as far as the compiler can tell
+        if (!mbar_wait_quick(b_full, 0, abort_flag)) fail();
+        for (int k = 0; k < n64; k += 4, ++s) {
+          if (!mbar_wait_quick(&full[stage], phase, abort_flag)) fail();
           tc_fence_after();
           const uint64_t ad = ad0 + stage * (kABytes >> 4), bd = bd0 + static_cast<uint32_t>(s * plan.b_bytes() >> 4);
-          const uint64_t ad_s = sa0 + stage * (kPairBytes >> 4), bd_s = sb0 + s * (kPairBytes >> 4);
-          const uint32_t ta = tmem + kTmemSA + 8 * (s & 1), tb = tmem + kTmemSB + 8 * (s & 1);
+          const uint64_t ad_s = sa0 + stage * (kPairBytes >> 4);
+          const uint32_t ta = tmem + kTmemSA + 8 * (s & 1), tb = tmem + kTmemSB + 4 * (s & 1);
           if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               if (j == 1 && k + 2 >= n64) break;
               tc_cp_scales(ta + 4 * j, ad_s + j * (kMxPieceBytes >> 4));
-              tc_cp_scales(tb + 4 * j, bd_s + j * (kMxPieceBytes >> 4));
             }
+            tc_cp_scales(tb, sb0 + s * (kMxPieceBytes >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (kk > 0 && k + kk >= n64) break;
-              tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0, ta + 4 * (kk >> 1), tb + 4 * (kk >> 1),
-                          (k > 0 || kk > 0) ? 1u : 0u);
+              tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0, ta + 4 * (kk >> 1),
+                          tb + 2 * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
             }
             tc_commit(&empty[stage]);
             if (k + 4 >= n64) tc_commit(acc_full);
@@ -460,20 +502,20 @@ __global__ void __launch_bounds__(kThreads)
         record_status(status, MOE_ERR_INVALID_ARG);
       }
       if constexpr (kMode == kDown) {
-        // every product of these columns counts itself, a skipped one too
-        __threadfence();
+        // every product of these columns counts itself, a skipped one too; the
+        // counter's release and acquire cover the other threads' stores and
+        // loads through the barriers around it
+        const uint32_t all = routed_tiles(p.a) + (p.a.I_shared > 0 ? 1 : 0);
+        Slots slots;
+        slots.load(p.a, ww * 32 + lane);
         bar_sync_or(kBarWork, kWorkWarps * 32, false);
         if (ww == 0 && lane == 0) {
-          const uint32_t all = routed_tiles(p.a) + (p.a.I_shared > 0 ? 1 : 0);
           const bool last = atom_add_acq_rel_gpu(&p.a.arrived[m.mt], 1u) == all - 1;
           if (last) p.a.arrived[m.mt] = 0;  // ready for the next call
           *last_flag = last;
         }
         bar_sync_or(kBarWork, kWorkWarps * 32, false);
-        if (*last_flag) {
-          __threadfence();
-          combine_columns(p.a, m.mt, ww * 32 + lane);
-        }
+        if (*last_flag) combine_columns(p.a, m.mt, ww * 32 + lane, slots);
       }
     }
   }

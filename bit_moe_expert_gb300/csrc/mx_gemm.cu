@@ -467,8 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stage_step = static_cast<uint32_t>(p.stage_bytes) >> 4;  // in the descriptors' address fields
     int stage = 0, accb = 0;
     uint32_t phase = 0, accphase = 0, set = 0, at = 0;
-    bool ok = true;
-    for (int i = 0; i < s.n && ok; ++i) {
+    // A wait that gives up is recorded and the loop goes on (its later waits end
+    // at the flag): leaving it would make the loop's state differ between lanes,
+    // as far as the compiler can tell.
+    for (int i = 0; i < s.n; ++i) {
       const Item m = item(i);
       const int rows = __shfl_sync(0xffffffffu, m.ok ? m.rows : 0, 0);
       if (rows == 0) continue;
@@ -477,18 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a tile that starts inside a 128-row piece (64 rows high) finds its scales further on, 32 rows a column
       const uint32_t shift = kMode == kLinear ? __shfl_sync(0xffffffffu, m.row_n % kMxPieceRows, 0) / 32 : 0;
       const uint32_t idesc0 = idesc_mxfp(kMxBM, bn, 0), idesc1 = idesc_mxfp(kMxBM, bn, 2);
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[accb], accphase ^ 1, abort_flag))) {
-        fail();
-        break;
-      }
+      if (!mbar_wait_quick(&acc_empty[accb], accphase ^ 1, abort_flag)) fail();
       tc_fence_after();
       const uint32_t d = tmem + accb * kMats * p.bn;
       for (int k = 0; k < n64; k += 4) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag))) {
-          fail();
-          ok = false;
-          break;
-        }
+        if (!mbar_wait_quick(&full[stage], phase, abort_flag)) fail();
         tc_fence_after();
         const uint64_t ad = ad0 + at, bd = bd0 + at, sd = sd0 + at;
         const uint32_t ta = sf_tmem + set * kScaleCols, tb = ta + 8 * kMats;
