@@ -175,8 +175,10 @@ def _stream(stream) -> int:
     if _raw_stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.current_device()  # initialises CUDA, which the call behind it takes for granted
         # the handle without building a Stream object (~0.2 against ~3 us)
-        _raw_stream = (raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream), torch.cuda.current_device)
+        _raw_stream = (raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+                       getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return _raw_stream[0](_raw_stream[1]())
 
 
@@ -463,8 +465,8 @@ class Scoring:
     renormalize: bool = True
     scale: float = 1.0
 
-    def _c(self, E: int) -> _Scoring:
-        # rebuilt only when a field changed
+    def _ref(self, E: int):
+        """A reference to the C struct, rebuilt only when a field changed."""
         c = self.__dict__.get("_cc")
         key = (self.score, self.n_group, self.topk_group, self.group_top, self.renormalize, self.scale, E)
         if c is None or c[0] is not self.bias or c[1] != key:
@@ -473,8 +475,8 @@ class Scoring:
             if self.bias is not None:
                 _tensor("bias", self.bias, (_FP32,), (E,))
             top = 1 if self.n_group == 1 else self.group_top
-            c = (self.bias, key, _Scoring(SCORES[self.score], _ptr(self.bias), self.n_group, self.topk_group, top,
-                                          1 if self.renormalize else 0, self.scale))
+            c = (self.bias, key, C.byref(_Scoring(SCORES[self.score], _ptr(self.bias), self.n_group, self.topk_group,
+                                                  top, 1 if self.renormalize else 0, self.scale)))
             self.__dict__["_cc"] = c
         return c[2]
 
@@ -508,19 +510,22 @@ def _tensor(name: str, t, codes, shape=None) -> int:
 
 
 _FLOATS = (_BF16, _FP16, _FP32)
+_ONLY_BF16, _ONLY_FP32 = (_BF16,), (_FP32,)
 
 
 def _rows(name: str, t):
-    """(rows, columns, elements between rows) of a 2-D CUDA tensor with contiguous rows."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
-    rows, cols = t.shape
-    if _code(t) not in _FLOATS:
+    """(rows, columns, elements between rows, type code) of a 2-D CUDA tensor with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 2-D CUDA tensor, got {tuple(shape)} on {t.device}")
+    rows, cols = shape
+    code = _code(t)
+    if code not in _FLOATS:
         raise ValueError(f"{name}: {t.dtype}, expected bfloat16, int16 (bf16 bits), float16 or float32")
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name}: elements of a row are {step} apart, expected 1")
-    return rows, cols, (ld if rows > 1 else cols)
+    return rows, cols, (ld if rows > 1 else cols), code
 
 
 def moe_mx_scale_bytes(E: int, N: int, K: int) -> int:
@@ -550,7 +555,7 @@ class MxMat:
         E, N, half = self.q.shape
         return int(E), int(N), 2 * int(half)
 
-    def _c(self) -> _MxMat:
+    def _cached(self):
         c = self.__dict__.get("_cc")
         if c is None or c[0] is not self.q or c[1] is not self.sp:
             _tensor("q", self.q, (_U8,))
@@ -558,13 +563,18 @@ class MxMat:
                 raise ValueError(f"q: shape {tuple(self.q.shape)}, expected [E][N][K/2]")
             E, N, K = self.shape
             _tensor("sp", self.sp, (_U8,), (E, -(-N // 128), -(-K // 128), 512))
-            c = (self.q, self.sp, _MxMat(_ptr(self.q), _ptr(self.sp)), (E, N, K))
+            st = _MxMat(_ptr(self.q), _ptr(self.sp))
+            c = (self.q, self.sp, st, (E, N, K), C.byref(st))
             self.__dict__["_cc"] = c
-        return c[2]
+        return c
 
-    def _c_and_shape(self):
-        st = self._c()
-        return st, self.__dict__["_cc"][3]
+    def _c(self) -> _MxMat:
+        return self._cached()[2]
+
+    def _ref_and_shape(self):
+        """A reference to the C struct, and (E, N, K)."""
+        c = self._cached()
+        return c[4], c[3]
 
 
 @dataclasses.dataclass
@@ -574,8 +584,8 @@ class MxExperts:
     up: MxMat
     down: MxMat
 
-    def _c_and_sizes(self):
-        """The C struct and (E, I, d)."""
+    def _ref_and_sizes(self):
+        """A reference to the C struct, and (E, I, d)."""
         # rebuilt only when a matrix or one of its tensors was replaced (identity checks only)
         c = self.__dict__.get("_cc")
         g, u, dn = self.gate, self.up, self.down
@@ -584,20 +594,19 @@ class MxExperts:
             E, I, d = g.shape
             if u.shape != (E, I, d) or dn.shape != (E, d, I):
                 raise ValueError(f"gate {g.shape}, up {u.shape}, down {dn.shape}: expected (E, I, d) twice and (E, d, I)")
-            c = (g, u, dn, g.q, g.sp, u.q, u.sp, dn.q, dn.sp, _MxExperts(g._c(), u._c(), dn._c(), E), (E, I, d))
+            c = (g, u, dn, g.q, g.sp, u.q, u.sp, dn.q, dn.sp, C.byref(_MxExperts(g._c(), u._c(), dn._c(), E)), (E, I, d))
             self.__dict__["_cc"] = c
         return c[9], c[10]
 
 
 def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Routing, ws, stream=None) -> None:
     """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
-    _tensor("logits", logits, (_FP32,))
+    _tensor("logits", logits, _ONLY_FP32)
     T, E = logits.shape
     r = out._c()
-    sc = scoring._c(E)
-    _check("moe_route_scored", lib().moe_route_scored(_ptr(logits), C.byref(sc), T, E, k, block_rows, C.byref(r),
-                                                      _ptr(ws), ws.numel(), _stream(stream)))
-    out.block_rows = r.block_rows
+    _check("moe_route_scored", lib().moe_route_scored(logits.data_ptr(), scoring._ref(E), T, E, k, block_rows, C.byref(r),
+                                                      ws.data_ptr(), ws.numel(), _stream(stream)))
+    out.block_rows = block_rows
 
 
 def moe_mx_prepack_scales(scale, sp, stream=None) -> None:
@@ -610,27 +619,27 @@ def moe_mx_prepack_scales(scale, sp, stream=None) -> None:
 
 def moe_mx_quantize(X, out: MxMat, stream=None) -> None:
     """X [rows][K] (bf16, fp16 or fp32; rows may be strided) -> out, an MxMat of (1, rows, K)."""
-    rows, K, ld = _rows("X", X)
-    m, shape = out._c_and_shape()
+    rows, K, ld, code = _rows("X", X)
+    m, shape = out._ref_and_shape()
     if shape != (1, rows, K):
         raise ValueError(f"out: {shape}, expected (1, {rows}, {K})")
-    _check("moe_mx_quantize", lib().moe_mx_quantize(_ptr(X), _code(X), rows, K, ld, C.byref(m), _stream(stream)))
+    _check("moe_mx_quantize", lib().moe_mx_quantize(X.data_ptr(), code, rows, K, ld, m, _stream(stream)))
 
 
 def moe_mx_dequant(m: MxMat, W, stream=None) -> None:
     """W (bf16 or fp32, E*N*K elements) = the values of m."""
-    st, (E, N, K) = m._c_and_shape()
-    t = _tensor("W", W, _FLOATS)
+    ref, (E, N, K) = m._ref_and_shape()
+    code = _tensor("W", W, _FLOATS)
     if W.numel() != E * N * K:
         raise ValueError(f"W: {W.numel()} elements, expected {E * N * K}")
-    _check("moe_mx_dequant", lib().moe_mx_dequant(C.byref(st), E, N, K, t, _ptr(W), _stream(stream)))
+    _check("moe_mx_dequant", lib().moe_mx_dequant(ref, E, N, K, code, W.data_ptr(), _stream(stream)))
 
 
 def _one(name: str, W: MxMat):
-    st, (E, N, K) = W._c_and_shape()
+    ref, (E, N, K) = W._ref_and_shape()
     if E != 1:
         raise ValueError(f"{name}: {E} matrices, expected one")
-    return st, N, K
+    return ref, N, K
 
 
 def moe_mx_matmul(A: MxMat, W: MxMat, Y, ws, stream=None) -> None:
@@ -639,8 +648,9 @@ def moe_mx_matmul(A: MxMat, W: MxMat, Y, ws, stream=None) -> None:
     w, N, Kw = _one("W", W)
     if K != Kw:
         raise ValueError(f"A has {K} columns, W {Kw}")
-    _check("moe_mx_matmul", lib().moe_mx_matmul(C.byref(a), M, C.byref(w), N, K, _ptr(Y), _tensor("Y", Y, _FLOATS, (M, N)), _ptr(ws),
-                                                ws.numel(), _stream(stream)))
+    y = _tensor("Y", Y, _FLOATS, (M, N))
+    _check("moe_mx_matmul", lib().moe_mx_matmul(a, M, w, N, K, Y.data_ptr(), y, ws.data_ptr(), ws.numel(),
+                                                _stream(stream)))
 
 
 def moe_mx_linear_workspace_bytes(T: int, N: int, K: int) -> int:
@@ -649,12 +659,13 @@ def moe_mx_linear_workspace_bytes(T: int, N: int, K: int) -> int:
 
 def moe_mx_linear(X, W: MxMat, Y, ws, stream=None) -> None:
     """Y [T][N] = MXFP4(X [T][K]) times W (1, N, K), transposed: a linear layer with MXFP4 weights."""
-    T, K, ld = _rows("X", X)
+    T, K, ld, code = _rows("X", X)
     w, N, Kw = _one("W", W)
     if K != Kw:
         raise ValueError(f"X has {K} columns, W {Kw}")
-    _check("moe_mx_linear", lib().moe_mx_linear(_ptr(X), _code(X), T, K, ld, C.byref(w), N, _ptr(Y), _tensor("Y", Y, _FLOATS, (T, N)),
-                                                _ptr(ws), ws.numel(), _stream(stream)))
+    y = _tensor("Y", Y, _FLOATS, (T, N))
+    _check("moe_mx_linear", lib().moe_mx_linear(X.data_ptr(), code, T, K, ld, w, N, Y.data_ptr(), y, ws.data_ptr(),
+                                                ws.numel(), _stream(stream)))
 
 
 def moe_mx_forward_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
@@ -662,28 +673,27 @@ def moe_mx_forward_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_sha
 
 
 def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
-    """C structs and sizes of an expert call, shapes checked."""
-    _tensor("X", X, (_BF16,))
-    T, d = X.shape
-    re, (E, I, dr) = routed._c_and_sizes()
+    """References to the C structs and the sizes of an expert call, shapes checked."""
+    _tensor("X", X, _ONLY_BF16)
+    T, d = shape = X.shape
+    re, (E, I, dr) = routed._ref_and_sizes()
     se, I_sh = None, 0
     if shared is not None:
-        s, (Es, I_sh, ds) = shared._c_and_sizes()
+        se, (Es, I_sh, ds) = shared._ref_and_sizes()
         if Es != 1 or ds != d:
             raise ValueError(f"shared: ({Es}, {I_sh}, {ds}), expected one expert of width {d}")
-        se = C.byref(s)
     if dr != d:
         raise ValueError(f"X is {d} wide, the experts {dr}")
-    _tensor("Y", Y, (_BF16,), (T, d))
-    return T, d, E, I, I_sh, C.byref(re), se
+    _tensor("Y", Y, _ONLY_BF16, shape)
+    return T, d, E, I, I_sh, re, se
 
 
 def moe_mx_forward(X, routed: MxExperts, shared: Optional[MxExperts], routing: Routing, Y, ws, stream=None) -> None:
     """The expert layer on MXFP4 weights, for a routing of moe_route or moe_route_scored."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
     rr = routing._c()
-    _check("moe_mx_forward", lib().moe_mx_forward(_ptr(X), T, d, I, int(routing.ids.shape[1]), re, se, I_sh,
-                                                  C.byref(rr), _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)))
+    _check("moe_mx_forward", lib().moe_mx_forward(X.data_ptr(), T, d, I, int(routing.ids.shape[1]), re, se, I_sh,
+                                                  C.byref(rr), Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_mx_layer_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
@@ -694,12 +704,12 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
                  out: Routing, Y, ws, stream=None) -> None:
     """moe_route_scored + moe_mx_forward in one call."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
-    _tensor("logits", logits, (_FP32,), (T, E))
+    _tensor("logits", logits, _ONLY_FP32, (T, E))
     r = out._c()
-    sc = scoring._c(E)
-    _check("moe_mx_layer", lib().moe_mx_layer(_ptr(logits), C.byref(sc), _ptr(X), T, d, I, k, block_rows, re, se, I_sh,
-                                              C.byref(r), _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)))
-    out.block_rows = r.block_rows
+    _check("moe_mx_layer", lib().moe_mx_layer(logits.data_ptr(), scoring._ref(E), X.data_ptr(), T, d, I, k, block_rows, re,
+                                              se, I_sh, C.byref(r), Y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                              _stream(stream)))
+    out.block_rows = block_rows
 
 
 # ----------------------------------------------------------------------- weight preparation

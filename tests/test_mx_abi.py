@@ -126,11 +126,11 @@ def test_expert_calls_refuse(L):
 def test_binding_refuses_what_the_library_cannot_see():
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError, match="score"):
-        bm.Scoring("relu")._c(4)
+        bm.Scoring("relu")._ref(4)
     with pytest.raises(ValueError, match="CUDA"):
-        bm.Scoring(bias=torch.zeros(4))._c(4)
+        bm.Scoring(bias=torch.zeros(4))._ref(4)
     with pytest.raises(ValueError, match="float64"):
-        bm.Scoring(bias=torch.zeros(4, dtype=torch.float64))._c(4)
+        bm.Scoring(bias=torch.zeros(4, dtype=torch.float64))._ref(4)
     with pytest.raises(ValueError, match="uint8"):
         bm.MxMat(torch.zeros((1, 4, 16)), torch.zeros((1, 1, 1, 512)))._c()
     with pytest.raises(ValueError, match="CUDA"):
