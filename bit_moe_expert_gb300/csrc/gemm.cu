@@ -860,28 +860,17 @@ cudaError_t launch_gemm_t(const GemmArgs& a, const GemmMaps* routed, const GemmM
   timer_end(kKGemmDown, stream);
   if (err != cudaSuccess) return err;
 
-  return launch_combine(a.ypart, a.inv_perm, a.w, a.T, a.d, a.k, a.I_shared > 0, a.Y, a.status, a.num_sms, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_combine(const float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
-                           bool has_shared, uint16_t* Y, uint32_t* status, int num_sms, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(max(1, min(T, num_sms * 8)));
+  cfg.gridDim = dim3(max(1, min(a.T, a.num_sms * 8)));
   cfg.blockDim = dim3(kCombineThreads);
+  cfg.dynamicSmemBytes = 0;
   timer_begin(kKCombine, stream);
-  const cudaError_t err =
-      cudaLaunchKernelEx(&cfg, combine_kernel, ypart, inv_perm, w, T, d, k, has_shared ? 1 : 0, Y, status);
+  err = cudaLaunchKernelEx(&cfg, combine_kernel, static_cast<const float*>(a.ypart), a.inv_perm, a.w, a.T, a.d, a.k,
+                           a.I_shared > 0 ? 1 : 0, a.Y, a.status);
   timer_end(kKCombine, stream);
   return err;
 }
+
+}  // namespace
 
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMaps* shared, const GemmActMaps* act,
                         cudaStream_t stream, bool pdl) {

@@ -180,10 +180,6 @@ struct GemmActMaps {
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMaps* shared, const GemmActMaps* act,
                         cudaStream_t stream, bool pdl);
 
-// Y[t] = bf16(sum_j w[t][j] ypart[inv_perm[t k + j]] + ypart[T k + t]), the second term with has_shared.
-cudaError_t launch_combine(const float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
-                           bool has_shared, uint16_t* Y, uint32_t* status, int num_sms, cudaStream_t stream);
-
 // ---------------------------------------------------------------- host helpers of api.cu
 bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows);
 bool pdl_enabled();  // the environment variable MOE_PDL
@@ -221,6 +217,9 @@ struct MxScatter {
   uint32_t* status;
   int T, k, max_blocks, shared_rows;  // shared_rows = 0: no shared expert
 };
+// Y[t] = bf16(sum_j w[t][j] ypart[inv_perm[t k + j]] + ypart[T k + t]), the second term with has_shared.
+cudaError_t launch_mx_combine(const float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
+                              bool has_shared, uint16_t* Y, uint32_t* status, int num_sms, cudaStream_t stream);
 cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint8_t* q, uint8_t* sp,
                               cudaStream_t stream, bool pdl);
 
@@ -252,6 +251,9 @@ struct MxExpertArgs {
   uint8_t *q_h_r, *q_h_s;      // h's codes [A][I/2], [T][I_shared/2]
   float* ypart;                // [A + T][d]
   uint32_t* status;
+  const int32_t* inv_perm;
+  const float* w;              // [T][k]
+  uint16_t* Y;                 // [T][d] bf16
   int T, d, I, k, I_shared, E, num_sms, max_blocks;
   int bn_r, bn_s;              // tile heights in MMA columns (multiples of 16): routed, shared
 };

@@ -127,8 +127,8 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
     o = round256(o + bytes);
     return at;
   };
-  L.ypart = take(rows * d * 4);
   L.few = T <= kMxFewT && mx_few_fits(T, d, I, I_shared);
+  L.ypart = take(rows * d * 4);
   if (L.few) {
     L.gu = take(rows * 2 * (I > I_shared ? I : I_shared) * 4);
     L.total = o;
@@ -248,6 +248,9 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
   a.max_blocks = L.max_blocks;
   a.bn_r = L.bn_r;
   a.bn_s = L.bn_s;
+  a.inv_perm = r->inv_perm;
+  a.w = r->w;
+  a.Y = Y;
   ok = encode_mx_codes(&maps.x_r, w + L.q_x, rows, d / 2, L.bn_r) && encode_mx_codes(&maps.h_r, a.q_h_r, A, I / 2, L.bn_r);
   if (shared)
     ok = ok && encode_mx_codes(&maps.x_s, w + L.q_x, rows, d / 2, L.bn_s) &&
@@ -258,8 +261,7 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
 
   const MxScatter sc{r->inv_perm, r->block_map, r->num_blocks, a.status, T, k, L.max_blocks, shared ? L.bn_s : 0};
   if (launch_mx_scatter(X, d, sc, w + L.q_x, w + L.sp_x, st, pdl_enabled()) != cudaSuccess ||
-      launch_mx_experts(a, maps, st) != cudaSuccess ||
-      launch_combine(a.ypart, r->inv_perm, r->w, T, d, k, shared != nullptr, Y, a.status, num_sms, st) != cudaSuccess)
+      launch_mx_experts(a, maps, st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }

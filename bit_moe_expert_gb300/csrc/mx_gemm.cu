@@ -17,7 +17,7 @@
 // Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
 // activations' loads, warp 2 MMA issuer (copies a stage's scales from shared to
 // tensor memory, then multiplies: the tensor pipeline keeps the order), warps
-// 3-10 epilogue, two per quarter of the tensor-memory lanes.  Every wait is bounded and records MOE_ERR_TIMEOUT.
+// 3 on epilogue, two or four per quarter of the tensor-memory lanes.  Every wait is bounded and records MOE_ERR_TIMEOUT.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,8 +34,11 @@ constexpr int kWeightsWarp = 0;
 constexpr int kActivationsWarp = 1;
 constexpr int kMmaWarp = 2;
 constexpr int kEpiWarp0 = 3;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+// Epilogue warps, a multiple of four (one per quarter of the tensor-memory lanes).
+template <int kMode>
+constexpr int kEpiWarps = kMode == kGateUp ? 16 : 8;
+template <int kMode>
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps<kMode>) * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAccs = 8;
@@ -247,7 +250,7 @@ __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, c
   uint8_t* hs = (m.shared ? a.sp_h_s : a.sp_h_r) +
                 (static_cast<size_t>(m.slot) * pieces + m.mt) * kMxPieceBytes + lanegrp;
   const bool valid = n0 < I;  // the same for the whole warp; past I the piece's scale bytes are zeros
-  for (int c0 = 8 * colpart; c0 < bn; c0 += 8 * (kEpiWarps / 4)) {
+  for (int c0 = 8 * colpart; c0 < bn; c0 += 8 * (kEpiWarps<kGateUp> / 4)) {
     uint32_t g[8], u[8];
     tmem_ld8(tbase + c0, g);
     tmem_ld8(tbase + p.bn + c0, u);
@@ -282,15 +285,21 @@ __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, c
 __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, const Plan& p, uint32_t tbase, int bn,
                                          int lanegrp, int colpart, int lane, std::integral_constant<int, kDown>) {
   const int n = m.mt * kMxBM + 32 * lanegrp + lane;
-  float* y = a.ypart + (static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0) * a.d + n;
-  for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps / 4)) {
+  const size_t pitch = a.d;
+  float* y = a.ypart + (static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0 + 16 * colpart) * pitch + n;
+  for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps<kDown> / 4), y += 16 * (kEpiWarps<kDown> / 4) * pitch) {
     uint32_t v[16];
     tmem_ld16(tbase + c0, v);
     tc_wait_ld();
-    if (n < a.d) {
+    if (n >= a.d) continue;
+    float* to = y;
+    if (c0 + 16 <= m.rows) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (c0 + c < m.rows) y[static_cast<size_t>(c0 + c) * a.d] = __uint_as_float(v[c]);
+      for (int c = 0; c < 16; ++c, to += pitch) *to = __uint_as_float(v[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c, to += pitch)
+        if (c0 + c < m.rows) *to = __uint_as_float(v[c]);
     }
   }
 }
@@ -307,7 +316,7 @@ __device__ __forceinline__ void epilogue(const MxLinearArgs& a, const Item& m, c
                                          int lanegrp, int colpart, int lane, std::integral_constant<int, kLinear>) {
   const int r = m.row_m + 32 * lanegrp + lane;
   const bool wide = a.stride_n == 1 && a.stride_m % (a.y_fp32 ? 4 : 8) == 0;
-  for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps / 4)) {
+  for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps<kLinear> / 4)) {
     uint32_t v[16];
     tmem_ld16(tbase + c0, v);
     tc_wait_ld();
@@ -342,7 +351,7 @@ __device__ __forceinline__ void epilogue(const MxLinearArgs& a, const Item& m, c
 
 // kRowTiles: 128-row groups of scales of the N side (bn up to 128, or 256).
 template <int kMode, int kRowTiles>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<kMode>, 1)
     mx_gemm_kernel(const __grid_constant__ typename Args<kMode>::maps maps,
                    const __grid_constant__ typename Args<kMode>::type a, const Plan p) {
   constexpr int kMats = kMode == kGateUp ? 2 : 1;
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The routing has completed by now (the kernel before this one lets this one
   // start only after its own wait), so only the activations are waited for.
   const Sched s = make_sched(a, p, kGU);
-  for (int i = threadIdx.x; i < min(s.n, kEntries); i += kThreads) entries[i] = make_entry(a, s, s.first + i * s.step);
+  for (int i = threadIdx.x; i < min(s.n, kEntries); i += kThreads<kMode>) entries[i] = make_entry(a, s, s.first + i * s.step);
   auto item = [&](int i) {
     return get_item(a, maps, p, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
   };
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < p.acc_bufs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpiWarps);
+      mbar_init(&acc_empty[i], kEpiWarps<kMode>);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -578,7 +587,7 @@ cudaError_t launch(int kind, const typename Args<kMode>::maps& maps, const typen
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<kMode>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -602,9 +611,11 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cu
 
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream) {
   const int bn = a.I_shared > 0 && a.bn_s > a.bn_r ? a.bn_s : a.bn_r;
-  const cudaError_t e = launch<kGateUp, 1>(kKMxGateUp, maps, a, make_plan(2, bn), a.num_sms, stream, true);
+  cudaError_t e = launch<kGateUp, 1>(kKMxGateUp, maps, a, make_plan(2, bn), a.num_sms, stream, true);
   if (e != cudaSuccess) return e;
-  return launch<kDown, 1>(kKMxDown, maps, a, make_plan(1, bn), a.num_sms, stream, true);
+  e = launch<kDown, 1>(kKMxDown, maps, a, make_plan(1, bn), a.num_sms, stream, true);
+  if (e != cudaSuccess) return e;
+  return launch_mx_combine(a.ypart, a.inv_perm, a.w, a.T, a.d, a.k, a.I_shared > 0, a.Y, a.status, a.num_sms, stream);
 }
 
 }  // namespace bm
