@@ -260,6 +260,15 @@ bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// E matrices of N rows: the same boxes within one matrix (coordinates: byte, row, matrix), rows past N read as zeros
+bool encode_mx_weights(CUtensorMap* map, const uint8_t* q, int E, int N, int row_bytes, int box_rows) {
+  if (!get_encoder()) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(E)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes) * N};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 bool pdl_enabled() { return env_flag("MOE_PDL", true); }
 
 int device_sms() { return sm_count(); }
@@ -319,7 +328,7 @@ moe_status check_scored(const float* logits, const moe_scoring* sc, int T, int E
 }
 
 moe_status route_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
-                        moe_routing* out, void* ws, uint32_t* status, moe_stream stream) {
+                        moe_routing* out, void* ws, moe_stream stream) {
   out->block_rows = block_rows;
   const RouteOut o{out->ids,  out->w,        out->counts,    out->offsets,
                    out->perm, out->inv_perm, out->block_map, out->num_blocks};
@@ -331,7 +340,7 @@ moe_status route_scored(const float* logits, const moe_scoring* sc, int T, int E
   score.group_top = sc->group_top;
   score.renormalize = sc->renormalize != 0;
   score.scale = sc->scale;
-  if (launch_route(logits, T, E, k, block_rows, o, ws, reinterpret_cast<cudaStream_t>(stream), pdl_enabled(), status,
+  if (launch_route(logits, T, E, k, block_rows, o, ws, reinterpret_cast<cudaStream_t>(stream), pdl_enabled(), nullptr,
                    &score) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
@@ -431,7 +440,7 @@ moe_status moe_route_scored(const float* logits, const moe_scoring* sc, int T, i
   if (st != MOE_OK) return st;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < moe_route_workspace_bytes(T, E, k))
     return MOE_ERR_WORKSPACE;
-  return route_scored(logits, sc, T, E, k, block_rows, out, ws, nullptr, stream);
+  return route_scored(logits, sc, T, E, k, block_rows, out, ws, stream);
 }
 
 moe_status moe_router_logits(const uint16_t* X, int T, int d, const uint16_t* W_r, int E, float* logits,

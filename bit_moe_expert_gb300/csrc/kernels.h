@@ -182,13 +182,14 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMap
 
 // ---------------------------------------------------------------- host helpers of api.cu
 bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows);
+bool encode_mx_weights(CUtensorMap* map, const uint8_t* q, int E, int N, int row_bytes, int box_rows);
 bool pdl_enabled();  // the environment variable MOE_PDL
 int device_sms();    // 0: no device
-// moe_route_scored's checks of everything but the workspace, and its launch (status as for launch_route).
+// moe_route_scored's checks of everything but the workspace, and its launch.
 moe_status check_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
                         const moe_routing* out);
 moe_status route_scored(const float* logits, const moe_scoring* sc, int T, int E, int k, int block_rows,
-                        moe_routing* out, void* ws, uint32_t* status, moe_stream stream);
+                        moe_routing* out, void* ws, moe_stream stream);
 
 // ---------------------------------------------------------------- MXFP4
 constexpr int kMxBlock = 32;       // values along K that share a scale
@@ -227,7 +228,7 @@ constexpr int kMxBM = 128;      // rows of the MMA's M operand
 constexpr int kMxStageK = 256;  // K of a pipeline stage: one 128-byte line of codes a row
 constexpr int kMxMaxBN = 128;   // tokens of an expert tile at most
 
-// M operand and N operand as TMA maps of code bytes (128-byte boxes, 128-byte swizzle).
+// M operand ([1][rows][bytes]) and N operand as TMA maps of code bytes (128-byte boxes, 128-byte swizzle).
 struct MxLinearArgs {
   const uint8_t *sp_m, *sp_n;  // packed scales of the M and the N operand
   void* Y;
@@ -258,7 +259,7 @@ struct MxExpertArgs {
   int bn_r, bn_s;              // tile heights in MMA columns (multiples of 16): routed, shared
 };
 struct MxExpertMaps {
-  CUtensorMap gate_r, up_r, down_r, gate_s, up_s, down_s;  // codes [E * N][K/2], box (128 bytes, 128 rows)
+  CUtensorMap gate_r, up_r, down_r, gate_s, up_s, down_s;  // codes [E][N][K/2], box (128 bytes, 128 rows, 1)
   CUtensorMap x_r, x_s;        // X's codes [A + T][d/2], box (128 bytes, bn_r / bn_s rows)
   CUtensorMap h_r, h_s;        // h's codes
 };
@@ -273,7 +274,7 @@ struct MxFewLinearArgs {
   int T, N, K, y_fp32;
 };
 bool mx_few_linear_fits(int T, int K);
-// type of X as for launch_mx_quantize; w: codes of W, box (128 bytes, 128 rows)
+// type of X as for launch_mx_quantize; w: codes of W [1][N][K/2], box (128 bytes, 128 rows, 1)
 cudaError_t launch_mx_few_linear(const MxFewLinearArgs& a, int type, const CUtensorMap& w, cudaStream_t stream, bool pdl);
 
 struct MxFewArgs {

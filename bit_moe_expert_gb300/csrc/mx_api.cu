@@ -93,7 +93,7 @@ moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K,
   a.stride_n = sh.weights_m ? N : 1;
   a.weights_n = !sh.weights_m;
   a.bn = sh.bn;
-  if (!encode_mx_codes(&maps.m, m.q, a.rows_m, K / 2, kMxBM) || !encode_mx_codes(&maps.n, n.q, a.rows_n, K / 2, a.bn))
+  if (!encode_mx_weights(&maps.m, m.q, 1, a.rows_m, K / 2, kMxBM) || !encode_mx_codes(&maps.n, n.q, a.rows_n, K / 2, a.bn))
     return MOE_ERR_CUDA;
   return launch_mx_linear(a, maps, reinterpret_cast<cudaStream_t>(stream), pdl_enabled()) == cudaSuccess ? MOE_OK
                                                                                                          : MOE_ERR_CUDA;
@@ -186,17 +186,16 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
   if (num_sms <= 0) return MOE_ERR_CUDA;
 
   const long long A = static_cast<long long>(T) * k, rows = A + (shared ? T : 0);
-  const long long EI = static_cast<long long>(E) * I, Ed = static_cast<long long>(E) * d;
   uint32_t* status = &static_cast<WsHeader*>(ws)->status;
   float* ypart = reinterpret_cast<float*>(w + L.ypart);
   MxExpertMaps maps;
-  bool ok = encode_mx_codes(&maps.gate_r, routed->gate.q, EI, d / 2, kMxBM) &&
-            encode_mx_codes(&maps.up_r, routed->up.q, EI, d / 2, kMxBM) &&
-            encode_mx_codes(&maps.down_r, routed->down.q, Ed, I / 2, kMxBM);
+  bool ok = encode_mx_weights(&maps.gate_r, routed->gate.q, E, I, d / 2, kMxBM) &&
+            encode_mx_weights(&maps.up_r, routed->up.q, E, I, d / 2, kMxBM) &&
+            encode_mx_weights(&maps.down_r, routed->down.q, E, d, I / 2, kMxBM);
   if (shared)
-    ok = ok && encode_mx_codes(&maps.gate_s, shared->gate.q, I_shared, d / 2, kMxBM) &&
-         encode_mx_codes(&maps.up_s, shared->up.q, I_shared, d / 2, kMxBM) &&
-         encode_mx_codes(&maps.down_s, shared->down.q, d, I_shared / 2, kMxBM);
+    ok = ok && encode_mx_weights(&maps.gate_s, shared->gate.q, 1, I_shared, d / 2, kMxBM) &&
+         encode_mx_weights(&maps.up_s, shared->up.q, 1, I_shared, d / 2, kMxBM) &&
+         encode_mx_weights(&maps.down_s, shared->down.q, 1, d, I_shared / 2, kMxBM);
   else  // never read without a shared expert
     maps.gate_s = maps.up_s = maps.down_s = maps.gate_r;
   if (!ok) return MOE_ERR_CUDA;
@@ -332,7 +331,7 @@ moe_status moe_mx_linear(const void* X, moe_dtype x_type, int T, int K, long lon
   if (mx_few_linear_fits(T, K)) {
     const MxFewLinearArgs a{X, W->sp, Y, status, ldx, T, N, K, y_type == MOE_FP32};
     CUtensorMap map;
-    if (!encode_mx_codes(&map, W->q, N, K / 2, kMxBM) ||
+    if (!encode_mx_weights(&map, W->q, 1, N, K / 2, kMxBM) ||
         launch_mx_few_linear(a, x_type, map, reinterpret_cast<cudaStream_t>(stream), pdl_enabled()) != cudaSuccess)
       return MOE_ERR_CUDA;
     return MOE_OK;
@@ -379,7 +378,7 @@ moe_status moe_mx_layer(const float* logits, const moe_scoring* scoring, const u
   if (st != MOE_OK) return st;
   if (!ws_ok(ws, ws_bytes, moe_mx_layer_workspace_bytes(T, d, I, E, k, I_shared, block_rows))) return MOE_ERR_WORKSPACE;
   // one header for both, and after it the same room: the products start when the routing has completed
-  st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, nullptr, stream);
+  st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, stream);
   if (st != MOE_OK) return st;
   return forward(X, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
 }

@@ -68,7 +68,7 @@ Plan make_plan(int bn, int K) {
 struct Item {
   const CUtensorMap* map;
   const uint8_t* scales;  // the weight tile's first piece
-  int row_m, mt, K;       // first weight row in the map, tile of 128 rows, depth
+  int e, row_m, mt, K;    // matrix and first row of the weights, tile of 128 rows, depth
   int rows, row0, N;      // tokens of the tile, the first one's row, weight rows of the matrix
   int mat;                // gate/up: 0 gate, 1 up
   bool shared, ok, some;  // some: false past the last item
@@ -155,7 +155,8 @@ __device__ __forceinline__ Item get_item(const ExpertParams& p) {
     m.map = m.shared ? &t.down_s : &t.down_r;
     m.scales = m.shared ? a.sp_down_s : a.sp_down_r;
   }
-  m.row_m = e * m.N + m.mt * kMxBM;
+  m.row_m = m.mt * kMxBM;
+  m.e = e;
   m.scales += (static_cast<size_t>(e) * ((m.N + kMxPieceRows - 1) / kMxPieceRows) + m.mt) * pieces_of(m.K) * kMxPieceBytes;
   return m;
 }
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads)
   if (warp == kProducerWarp) {
     // one thread issues; what it issues is the same in all lanes (uniform registers)
     const int n = __shfl_sync(0xffffffffu, m.some && m.ok ? pieces_of(m.K) : 0, 0);
-    const int row_m = __shfl_sync(0xffffffffu, m.row_m, 0);
+    const int row_m = __shfl_sync(0xffffffffu, m.row_m, 0), e = __shfl_sync(0xffffffffu, m.e, 0);
     const CUtensorMap* map = reinterpret_cast<const CUtensorMap*>(uniform64(reinterpret_cast<uint64_t>(m.map)));
     const uint8_t* scales = reinterpret_cast<const uint8_t*>(uniform64(reinterpret_cast<uint64_t>(m.scales)));
     int stage = 0, filled = 0;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) {
         const uint32_t sbytes = min(2, n - k0) * kMxPieceBytes;
         mbar_arrive_expect_tx(&full[stage], kABytes + sbytes);
-        tma_load_2d(ring + stage * kABytes, map, &full[stage], k0 * 64, row_m);
+        tma_load_3d(ring + stage * kABytes, map, &full[stage], k0 * 64, row_m, e);
         bulk_g2s(sa + stage * kPairBytes, scales + static_cast<size_t>(k0) * kMxPieceBytes, sbytes, &full[stage]);
       }
       __syncwarp();

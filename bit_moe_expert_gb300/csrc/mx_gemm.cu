@@ -71,7 +71,7 @@ Plan make_plan(int mats, int bn) {
 struct Item {
   const CUtensorMap *m0, *m1, *n;  // codes of the M side's matrices and of the N side
   const uint8_t *sm0, *sm1, *sn;   // their scales: the item's first pieces
-  int row_m, row_n;                // first rows of the codes
+  int e, row_m, row_n;             // matrix of the M side; first rows of the codes
   int mt, rows, K, box;            // M tile, valid N rows, depth, N rows that the TMA box brings
   int row0, slot;                  // experts: first row among the assignments (or tokens), tile slot
   int groups;                      // 128-row groups of scales on the N side
@@ -217,7 +217,8 @@ __device__ __forceinline__ Item get_item(const MxExpertArgs& a, const MxExpertMa
   const size_t tile = (static_cast<size_t>(e) * ((N + kMxPieceRows - 1) / kMxPieceRows) + m.mt) * pieces * kMxPieceBytes;
   m.sm0 += tile;
   m.sm1 += tile;
-  m.row_m = e * N + m.mt * kMxBM;
+  m.row_m = m.mt * kMxBM;
+  m.e = e;
   const uint8_t* sn = gate_up ? a.sp_x : (m.shared ? a.sp_h_s : a.sp_h_r);
   m.sn = sn + static_cast<size_t>(gate_up && m.shared ? a.max_blocks + m.slot : m.slot) * pieces * kMxPieceBytes;
   return m;
@@ -436,8 +437,8 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
           if (n_side) {
             tma_load_2d(st, m.n, bar, k0 * 64, m.row_n);
           } else {
-            tma_load_2d(st, m.m0, bar, k0 * 64, m.row_m);
-            if (kGU) tma_load_2d(st + kCodeBytesM, m.m1, bar, k0 * 64, m.row_m);
+            tma_load_3d(st, m.m0, bar, k0 * 64, m.row_m, m.e);
+            if (kGU) tma_load_3d(st + kCodeBytesM, m.m1, bar, k0 * 64, m.row_m, m.e);
           }
           bulk_g2s(sf, s0, sbytes, bar);
           if (scales > 1) bulk_g2s(sf + kPairBytes, s1, sbytes, bar);
