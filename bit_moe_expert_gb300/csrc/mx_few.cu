@@ -337,7 +337,7 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
 }
 
 template <int kMode, int kType>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     mx_few_kernel(const __grid_constant__ typename Params<kMode>::type p, const Plan plan) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads)
     int stage = 0, filled = 0;
     uint32_t phase = 0;
     for (int k0 = 0; k0 < n; k0 += 2, ++filled) {
-      if (!mbar_wait_quick(&empty[stage], phase ^ 1, abort_flag)) {
+      if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
         fail();
         break;
       }
@@ -436,17 +436,15 @@ __global__ void __launch_bounds__(kThreads)
         const uint64_t sa0 = smem_desc_scales(smem_u32(sa)), sb0 = smem_desc_scales(smem_u32(sb));
         int stage = 0, s = 0;
         uint32_t phase = 0;
-        // a wait that gives up is recorded and the loop goes on (its later waits
-        // end at the flag): leaving it would make the loop's state differ
-        // between lanes, as far as the compiler can tell
-        if (!mbar_wait_quick(b_full, 0, abort_flag)) fail();
+        const bool leader = elect_one();
+        mbar_wait_issue(b_full, 0, abort_flag, status);
         for (int k = 0; k < n64; k += 4, ++s) {
-          if (!mbar_wait_quick(&full[stage], phase, abort_flag)) fail();
+          mbar_wait_issue(&full[stage], phase, abort_flag, status);
           tc_fence_after();
           const uint64_t ad = ad0 + stage * (kABytes >> 4), bd = bd0 + static_cast<uint32_t>(s * plan.b_bytes() >> 4);
           const uint64_t ad_s = sa0 + stage * (kPairBytes >> 4);
           const uint32_t ta = tmem + kTmemSA + 8 * (s & 1), tb = tmem + kTmemSB + 4 * (s & 1);
-          if (elect_one()) {
+          if (leader) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               if (j == 1 && k + 2 >= n64) break;
@@ -462,14 +460,14 @@ __global__ void __launch_bounds__(kThreads)
             tc_commit(&empty[stage]);
             if (k + 4 >= n64) tc_commit(acc_full);
           }
-          __syncwarp();
           if (++stage == plan.ring) {
             stage = 0;
             phase ^= 1;
           }
         }
         // every MMA has completed before tensor memory is released
-        if (elect_one()) {
+        __syncwarp();
+        if (leader) {
           tc_commit(done);
           if (!mbar_wait(done, 0, nullptr)) record_status(status, MOE_ERR_TIMEOUT);
         }
@@ -478,11 +476,13 @@ __global__ void __launch_bounds__(kThreads)
     } else if (m.some) {
       const int ww = warp - kWorkWarp0;
       bool done = false;
+      Slots slots;  // of the first token that this thread may have to sum up (down product)
       if (m.ok) {
         prologue<kMode, kType>(p, b, sb, plan, m, ww, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full);
+        if constexpr (kMode == kDown) slots.load(p.a, ww * 32 + lane);  // beside the MMAs
         done = mbar_wait(acc_full, 0, abort_flag);
         __syncwarp();
         if (done) {
@@ -507,8 +507,7 @@ __global__ void __launch_bounds__(kThreads)
         // counter's release and acquire cover the other threads' stores and
         // loads through the barriers around it
         const uint32_t all = routed_tiles(p.a) + (p.a.I_shared > 0 ? 1 : 0);
-        Slots slots;
-        slots.load(p.a, ww * 32 + lane);
+        if (!m.ok) slots.load(p.a, ww * 32 + lane);
         bar_sync_or(kBarWork, kWorkWarps * 32, false);
         if (ww == 0 && lane == 0) {
           const bool last = atom_add_acq_rel_gpu(&p.a.arrived[m.mt], 1u) == all - 1;

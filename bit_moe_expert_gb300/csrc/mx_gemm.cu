@@ -477,9 +477,7 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
     const uint32_t stage_step = static_cast<uint32_t>(p.stage_bytes) >> 4;  // in the descriptors' address fields
     int stage = 0, accb = 0;
     uint32_t phase = 0, accphase = 0, set = 0, at = 0;
-    // A wait that gives up is recorded and the loop goes on (its later waits end
-    // at the flag): leaving it would make the loop's state differ between lanes,
-    // as far as the compiler can tell.
+    const bool leader = elect_one();
     for (int i = 0; i < s.n; ++i) {
       const Item m = item(i);
       const int rows = __shfl_sync(0xffffffffu, m.ok ? m.rows : 0, 0);
@@ -489,16 +487,16 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
       // a tile that starts inside a 128-row piece (64 rows high) finds its scales further on, 32 rows a column
       const uint32_t shift = kMode == kLinear ? __shfl_sync(0xffffffffu, m.row_n % kMxPieceRows, 0) / 32 : 0;
       const uint32_t idesc0 = idesc_mxfp(kMxBM, bn, 0), idesc1 = idesc_mxfp(kMxBM, bn, 2);
-      if (!mbar_wait_quick(&acc_empty[accb], accphase ^ 1, abort_flag)) fail();
+      mbar_wait_issue(&acc_empty[accb], accphase ^ 1, abort_flag, a.status);
       tc_fence_after();
       const uint32_t d = tmem + accb * kMats * p.bn;
       for (int k = 0; k < n64; k += 4) {
-        if (!mbar_wait_quick(&full[stage], phase, abort_flag)) fail();
+        mbar_wait_issue(&full[stage], phase, abort_flag, a.status);
         tc_fence_after();
         const uint64_t ad = ad0 + at, bd = bd0 + at, sd = sd0 + at;
         const uint32_t ta = sf_tmem + set * kScaleCols, tb = ta + 8 * kMats;
         const uint32_t tbm = tb + shift;
-        if (elect_one()) {
+        if (leader) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (j == 1 && k + 2 >= n64) break;
@@ -520,7 +518,6 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
           tc_commit(&empty[stage]);
           if (k + 4 >= n64) tc_commit(&acc_full[accb]);
         }
-        __syncwarp();
         set ^= 1;
         at += stage_step;
         if (++stage == p.stages) {
@@ -535,7 +532,8 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
       }
     }
     // every MMA has completed before tensor memory is released
-    if (elect_one()) {
+    __syncwarp();
+    if (leader) {
       tc_commit(done);
       if (!mbar_wait(done, 0, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
     }

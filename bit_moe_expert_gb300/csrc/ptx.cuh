@@ -89,14 +89,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// The same wait with everything but the first try out of line: in a loop that
-// issues tensor-core work the inlined form cost 140 clocks an iteration even
-// where the phase had completed.
-static __device__ __noinline__ bool mbar_wait_more(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_wait(bar, parity, abort);
+// The same wait for loops that issue tensor-core work, everything but the first
+// try out of line (inline, with the record of a failure, it cost up to 140
+// clocks an iteration even where the phase had completed).  A wait that gives
+// up records MOE_ERR_TIMEOUT, raises the flag and returns like any other: the
+// loop's state then stays the same in all lanes, and its later waits end at the
+// flag.
+static __device__ __noinline__ void mbar_wait_more(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (mbar_wait(bar, parity, abort)) return;
+  record_status(status, MOE_ERR_TIMEOUT);
+  *abort = 1;
 }
-__device__ __forceinline__ bool mbar_wait_quick(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_try_wait(bar, parity) || mbar_wait_more(bar, parity, abort);
+__device__ __forceinline__ void mbar_wait_issue(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (!mbar_try_wait(bar, parity)) mbar_wait_more(bar, parity, abort, status);
 }
 
 // Named barrier with an OR-reduction: every one of the `nthreads` threads
