@@ -434,35 +434,45 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t idesc0 = idesc_mxfp(kMxBM, bn, 0), idesc1 = idesc_mxfp(kMxBM, bn, 2);
         const uint64_t ad0 = smem_desc_sw128_kmajor(smem_u32(ring)), bd0 = smem_desc_sw128_kmajor(smem_u32(b));
         const uint64_t sa0 = smem_desc_scales(smem_u32(sa)), sb0 = smem_desc_scales(smem_u32(sb));
-        int stage = 0, s = 0;
+        int stage = 0;
         uint32_t phase = 0;
         const bool leader = elect_one();
         mbar_wait_issue(b_full, 0, abort_flag, status);
-        for (int k = 0; k < n64; k += 4, ++s) {
-          mbar_wait_issue(&full[stage], phase, abort_flag, status);
+        // two stages a turn, one in each set of scales: a turn's own cost (waits,
+        // branches, addresses: some 300 clocks) is more than the MMAs'
+        for (int k = 0; k < n64; k += 8) {
+          int st[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            st[h] = stage;
+            if (h == 1 && k + 4 >= n64) break;
+            mbar_wait_issue(&full[stage], phase, abort_flag, status);
+            if (++stage == plan.ring) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
           tc_fence_after();
-          const uint64_t ad = ad0 + stage * (kABytes >> 4), bd = bd0 + static_cast<uint32_t>(s * plan.b_bytes() >> 4);
-          const uint64_t ad_s = sa0 + stage * (kPairBytes >> 4);
-          const uint32_t ta = tmem + kTmemSA + 8 * (s & 1), tb = tmem + kTmemSB + 4 * (s & 1);
           if (leader) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (j == 1 && k + 2 >= n64) break;
-              tc_cp_scales(ta + 4 * j, ad_s + j * (kMxPieceBytes >> 4));
-            }
-            tc_cp_scales(tb, sb0 + s * (kMxPieceBytes >> 4));
+            for (int h = 0; h < 2; ++h) {
+              const int kh = k + 4 * h, s = kh >> 2;
+              if (h == 1 && kh >= n64) break;
+              const uint64_t ad = ad0 + st[h] * (kABytes >> 4), bd = bd0 + static_cast<uint32_t>(s * plan.b_bytes() >> 4);
+              const uint64_t ad_s = sa0 + st[h] * (kPairBytes >> 4);
+              const uint32_t ta = tmem + kTmemSA + 8 * h, tb = tmem + kTmemSB + 4 * h;
+              tc_cp_scales(ta, ad_s);
+              if (kh + 2 < n64) tc_cp_scales(ta + 4, ad_s + (kMxPieceBytes >> 4));
+              tc_cp_scales(tb, sb0 + s * (kMxPieceBytes >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk > 0 && k + kk >= n64) break;
-              tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0, ta + 4 * (kk >> 1),
-                          tb + 2 * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kk > 0 && kh + kk >= n64) break;
+                tc_mma_mxfp(tmem, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0, ta + 4 * (kk >> 1),
+                            tb + 2 * (kk >> 1), (kh > 0 || kk > 0) ? 1u : 0u);
+              }
+              tc_commit(&empty[st[h]]);
             }
-            tc_commit(&empty[stage]);
-            if (k + 4 >= n64) tc_commit(acc_full);
-          }
-          if (++stage == plan.ring) {
-            stage = 0;
-            phase ^= 1;
+            if (k + 8 >= n64) tc_commit(acc_full);
           }
         }
         // every MMA has completed before tensor memory is released
