@@ -228,18 +228,17 @@ constexpr int kMxBM = 128;      // rows of the MMA's M operand
 constexpr int kMxStageK = 256;  // K of a pipeline stage: one 128-byte line of codes a row
 constexpr int kMxMaxBN = 128;   // tokens of an expert tile at most
 
-// M operand ([1][rows][bytes]) and N operand as TMA maps of code bytes (128-byte boxes, 128-byte swizzle).
 struct MxLinearArgs {
-  const uint8_t *sp_m, *sp_n;  // packed scales of the M and the N operand
-  void* Y;
-  long long stride_m, stride_n;  // of Y, in elements
+  const uint8_t *sp_w, *sp_x;  // packed scales of the weights and of the tokens
+  void* Y;                     // [M][N]
   uint32_t* status;
-  int rows_m, rows_n, K, bn, num_sms;
-  int y_fp32;
-  int weights_n;  // the weights are the N side (else the M side)
+  int M, N, K;
+  int bn;  // height of the tokens' tiles: 64, 128, 256, or a multiple of 16 up to 128 that holds all M
+  int num_sms, y_fp32;
 };
 struct MxLinearMaps {
-  CUtensorMap m, n;
+  CUtensorMap w;  // codes [1][N][K/2], box (128 bytes, 128 rows, 1)
+  CUtensorMap x;  // codes [M][K/2], box (128 bytes, bn rows)
 };
 cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cudaStream_t stream, bool pdl);
 
@@ -263,8 +262,17 @@ struct MxExpertMaps {
   CUtensorMap x_r, x_s;        // X's codes [A + T][d/2], box (128 bytes, bn_r / bn_s rows)
   CUtensorMap h_r, h_s;        // h's codes
 };
-// Few tokens (at most kMxFewT): the activations are quantised inside the products.
-constexpr int kMxFewT = 32;
+// Few tokens: the activations are quantised inside the products, by every CTA
+// again.  That pays while it is short beside the launch that it saves:
+//   linear layer    up to kMxFewValues values of X: 8 x 2048 5.3 us against 6.1
+//                   with X quantised by a kernel of its own, 2 x 8192 10.4
+//                   against 12.6; 8 x 4096 9.0 against 8.4, 16 x 2048 7.7 against 6.1
+//   expert layer    while the gate/up product's CTAs are at most one per SM
+//                   (kMxFewItems): d = 2048, I = 512, 8 + 1 experts: 2 tokens
+//                   18.1 us against 19.6, 4 tokens 26.5 against 23.2
+constexpr int kMxFewT = 32;  // tokens at most (accumulator columns)
+constexpr int kMxFewValues = 16384;
+constexpr int kMxFewItems = 152;
 struct MxFewLinearArgs {
   const void* X;       // [T][K], rows ldx elements apart
   const uint8_t* sp;   // packed scales of W [N][K]
@@ -289,7 +297,7 @@ struct MxFewArgs {
   uint32_t* status;
   int T, d, I, k, I_shared, E, max_blocks, bn;  // bn: MMA columns of a tile
 };
-bool mx_few_fits(int T, int d, int I, int I_shared);
+bool mx_few_fits(int T, int d, int I, int I_shared, int k, int max_blocks);
 cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl);
 
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream);

@@ -44,30 +44,22 @@ moe_status check_matmul(int M, const moe_mx_mat* W, int N, int K, const void* Y,
   return MOE_OK;
 }
 
-// Which operand of the dense product is the MMA's M side (tiles of 128 rows), and
-// the height bn of the other's tiles.  Modelled time in clocks, fitted to
-// FITTED: a CTA's tiles in turn, each a stage of K = 256 after another at the
-// rate its bytes arrive, and the filling of the pipeline and the epilogue.
-// Tokens are the M side only where Y's rows take 16-byte stores (a lane then
-// holds part of a row; otherwise neighbouring lanes hold neighbours of a row).
-struct Shape {
-  bool weights_m;
-  int bn;
-};
-Shape linear_shape(int M, int N, int K, int y_bytes, int num_sms) {
-  Shape best{true, 0};
+// Height of the dense product's token tiles, by a modelled time in clocks: a
+// CTA's tiles in turn, each a stage of K = 256 after another at the rate its
+// bytes arrive and are read, then the epilogue.  Measured (bf16 Y, 64 / 128 / 256
+// high, quantisation included): 256 x 2048 -> 2048 6.1 / 6.8 / 8.5 us, 512 x 4096
+// -> 8192 21.3 / 14.8 / 13.6 us, 333 x 2816 -> 1001 7.2 / 7.5 / 9.1 us, 1024 x
+// 2048 -> 2048 8.9 / 8.3 / 9.2 us: the model picks the least of each.
+int linear_tile(int M, int N, int K, int num_sms) {
+  int best = 0;
   double least = 0;
-  for (int weights_m = 0; weights_m < 2; ++weights_m) {
-    if (!weights_m && static_cast<long long>(N) * y_bytes % 16 != 0) continue;
-    const int P = weights_m ? N : M, Q = weights_m ? M : N;
-    for (int bn : {64, 128, 256, Q <= kMxMaxBN ? round16(Q) : 64}) {
-      const double tiles = static_cast<double>((P + kMxBM - 1) / kMxBM) * ((Q + bn - 1) / bn);
-      const double turns = static_cast<double>(static_cast<long long>((tiles + num_sms - 1) / num_sms));
-      const double clocks = turns * ((K + kMxStageK - 1) / kMxStageK * (290 + 2.3 * bn) + 1500 + 8 * bn);
-      if (best.bn == 0 || clocks < least) {
-        least = clocks;
-        best = Shape{weights_m != 0, bn};
-      }
+  for (int bn : {64, 128, 256, M <= kMxMaxBN ? round16(M) : 64}) {
+    const long long tiles = static_cast<long long>((N + kMxBM - 1) / kMxBM) * ((M + bn - 1) / bn);
+    const double turns = static_cast<double>((tiles + num_sms - 1) / num_sms);
+    const double clocks = turns * ((K + kMxStageK - 1) / kMxStageK * (290 + 2.3 * bn) + 1500 + 8 * bn);
+    if (best == 0 || clocks < least) {
+      least = clocks;
+      best = bn;
     }
   }
   return best;
@@ -77,23 +69,18 @@ moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K,
                   uint32_t* status, moe_stream stream) {
   MxLinearArgs a{};
   MxLinearMaps maps;
-  a.K = K;
+  a.sp_w = W.sp;
+  a.sp_x = A.sp;
   a.Y = Y;
-  a.y_fp32 = y_type == MOE_FP32;
   a.status = status;
+  a.M = M;
+  a.N = N;
+  a.K = K;
   a.num_sms = device_sms();
   if (a.num_sms <= 0) return MOE_ERR_CUDA;
-  const Shape sh = linear_shape(M, N, K, a.y_fp32 ? 4 : 2, a.num_sms);
-  const moe_mx_mat &m = sh.weights_m ? W : A, &n = sh.weights_m ? A : W;
-  a.sp_m = m.sp;
-  a.sp_n = n.sp;
-  a.rows_m = sh.weights_m ? N : M;
-  a.rows_n = sh.weights_m ? M : N;
-  a.stride_m = sh.weights_m ? 1 : N;
-  a.stride_n = sh.weights_m ? N : 1;
-  a.weights_n = !sh.weights_m;
-  a.bn = sh.bn;
-  if (!encode_mx_weights(&maps.m, m.q, 1, a.rows_m, K / 2, kMxBM) || !encode_mx_codes(&maps.n, n.q, a.rows_n, K / 2, a.bn))
+  a.bn = linear_tile(M, N, K, a.num_sms);
+  a.y_fp32 = y_type == MOE_FP32;
+  if (!encode_mx_weights(&maps.w, W.q, 1, N, K / 2, kMxBM) || !encode_mx_codes(&maps.x, A.q, M, K / 2, a.bn))
     return MOE_ERR_CUDA;
   return launch_mx_linear(a, maps, reinterpret_cast<cudaStream_t>(stream), pdl_enabled()) == cudaSuccess ? MOE_OK
                                                                                                          : MOE_ERR_CUDA;
@@ -127,7 +114,7 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
     o = round256(o + bytes);
     return at;
   };
-  L.few = T <= kMxFewT && mx_few_fits(T, d, I, I_shared);
+  L.few = mx_few_fits(T, d, I, I_shared, k, L.max_blocks);
   L.ypart = take(rows * d * 4);
   if (L.few) {
     L.gu = take(rows * 2 * (I > I_shared ? I : I_shared) * 4);

@@ -1,4 +1,4 @@
-// MXFP4 products for few tokens (one decoded token to kMxFewT): what bounds
+// MXFP4 products for few tokens (one decoded token to a few): what bounds
 // them is the weights' stream and the number of dependent launches, so the
 // activations are quantised inside the products.  A CTA takes one tile of 128
 // weight rows over all of K; its loads are in flight while eight warps turn the
@@ -566,7 +566,9 @@ bool fits(int bn, int K) {
 
 }  // namespace
 
-bool mx_few_linear_fits(int T, int K) { return T <= kMxFewT && fits(round16(T), K); }
+bool mx_few_linear_fits(int T, int K) {
+  return T <= kMxFewT && static_cast<long long>(T) * K <= kMxFewValues && fits(round16(T), K);
+}
 
 cudaError_t launch_mx_few_linear(const MxFewLinearArgs& a, int type, const CUtensorMap& w, cudaStream_t stream, bool pdl) {
   const LinearParams p{a, w};
@@ -577,17 +579,27 @@ cudaError_t launch_mx_few_linear(const MxFewLinearArgs& a, int type, const CUten
   return launch<kLinear, kFp32>(kKMxGemm, p, plan, grid, stream, pdl);
 }
 
-bool mx_few_fits(int T, int d, int I, int I_shared) {
+namespace {
+// Tiles of the routed experts at most (every tile holds an assignment), and the gate/up product's CTAs.
+int few_tiles(int T, int k, int max_blocks) { return T * k < max_blocks ? T * k : max_blocks; }
+long long few_items(int T, int I, int I_shared, int k, int max_blocks) {
+  const long long mt = (I + kMxBM - 1) / kMxBM, mt_s = (I_shared + kMxBM - 1) / kMxBM;
+  return 2 * (few_tiles(T, k, max_blocks) * mt + mt_s);
+}
+}  // namespace
+
+bool mx_few_fits(int T, int d, int I, int I_shared, int k, int max_blocks) {
   const int bn = round16(T);
-  return T <= kMxFewT && (d + kMxBM - 1) / kMxBM <= static_cast<int>(sizeof(WsHeader::mx_arrived) / 4) && fits(bn, d) &&
+  return T <= kMxFewT && few_items(T, I, I_shared, k, max_blocks) <= kMxFewItems &&
+         (d + kMxBM - 1) / kMxBM <= static_cast<int>(sizeof(WsHeader::mx_arrived) / 4) && fits(bn, d) &&
          fits(bn, I > I_shared ? I : I_shared);
 }
 
 cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl) {
   const ExpertParams p{a, maps};
-  const int tiles = a.T * a.k < a.max_blocks ? a.T * a.k : a.max_blocks;  // every tile holds an assignment
-  const int mt = (a.I + kMxBM - 1) / kMxBM, mt_s = (a.I_shared + kMxBM - 1) / kMxBM, mt_d = (a.d + kMxBM - 1) / kMxBM;
-  const cudaError_t e = launch<kGateUp, kBf16>(kKMxGateUp, p, make_plan(a.bn, a.d), 2 * (tiles * mt + mt_s), stream, pdl);
+  const int tiles = few_tiles(a.T, a.k, a.max_blocks), mt_d = (a.d + kMxBM - 1) / kMxBM;
+  const cudaError_t e = launch<kGateUp, kBf16>(kKMxGateUp, p, make_plan(a.bn, a.d),
+                                               static_cast<int>(few_items(a.T, a.I, a.I_shared, a.k, a.max_blocks)), stream, pdl);
   if (e != cudaSuccess) return e;
   const int I = a.I > a.I_shared ? a.I : a.I_shared;
   return launch<kDown, kBf16>(kKMxDown, p, make_plan(a.bn, I), mt_d * (tiles + (a.I_shared > 0 ? 1 : 0)), stream, pdl);

@@ -8,11 +8,12 @@
 // the pipeline is K = 256: one 128-byte line of codes a row (the widest swizzle
 // atom), two 512-byte pieces of scales per 128 rows, four MMAs of K = 64.
 //
-// The expert layer puts the weights on the M = 128 side and a tile's tokens
-// (16..128) on the N side, so that an expert with few tokens streams its
-// weights once and pads only tokens.  The dense product does the same for few
-// tokens; for many, tokens are the M side, whose tensor-memory lanes then hold
-// rows of Y, and 256 columns of Y a tile halve the reads of the tokens' codes.
+// The weights are the M = 128 side and the tokens the N side: an expert with few
+// tokens streams its weights once and pads only tokens (tiles of 16..128), and
+// the dense product's epilogue has neighbouring columns of Y in neighbouring
+// lanes, whatever the width of Y (tokens on the M side, with 16-byte stores per
+// lane, took 216 us instead of 205 at 8192^3).  Dense tiles are 64, 128 or 256
+// tokens high.
 //
 // Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
 // activations' loads, warp 2 MMA issuer (copies a stage's scales from shared to
@@ -69,13 +70,12 @@ Plan make_plan(int mats, int bn) {
 }
 
 struct Item {
-  const CUtensorMap *m0, *m1, *n;  // codes of the M side's matrices and of the N side
+  const CUtensorMap *m0, *m1, *n;  // codes of the weights (one or two matrices) and of the tokens
   const uint8_t *sm0, *sm1, *sn;   // their scales: the item's first pieces
   int e, row_m, row_n;             // matrix of the M side; first rows of the codes
   int mt, rows, K, box;            // M tile, valid N rows, depth, N rows that the TMA box brings
   int row0, slot;                  // experts: first row among the assignments (or tokens), tile slot
   int groups;                      // 128-row groups of scales on the N side
-  bool weights_n;                  // the weights are the N side (dense product)
   bool shared, ok;
 };
 
@@ -109,8 +109,8 @@ __device__ __forceinline__ int pieces_of(int K) { return (K + kMxPieceK - 1) / k
 
 __device__ __forceinline__ Sched make_sched(const MxLinearArgs& a, const Plan& p, bool) {
   Sched s{};
-  s.mt_r = (a.rows_m + kMxBM - 1) / kMxBM;
-  const int total = s.mt_r * ((a.rows_n + p.bn - 1) / p.bn);
+  s.mt_r = (a.N + kMxBM - 1) / kMxBM;
+  const int total = s.mt_r * ((a.M + p.bn - 1) / p.bn);
   s.first = blockIdx.x;
   s.step = gridDim.x;
   s.n = (total - s.first + s.step - 1) / s.step;
@@ -127,17 +127,16 @@ __device__ __forceinline__ Item get_item(const MxLinearArgs& a, const MxLinearMa
   const int pieces = pieces_of(a.K);
   m.mt = en.at;
   const int nt = en.rows;
-  m.m0 = &maps.m;
-  m.n = &maps.n;
+  m.m0 = &maps.w;
+  m.n = &maps.x;
   m.row_m = m.mt * kMxBM;
   m.row_n = nt * p.bn;
-  m.rows = min(p.bn, a.rows_n - m.row_n);
+  m.rows = min(p.bn, a.M - m.row_n);
   m.K = a.K;
   m.box = p.bn;
-  m.sm0 = a.sp_m + static_cast<size_t>(m.mt) * pieces * kMxPieceBytes;
-  m.sn = a.sp_n + static_cast<size_t>(m.row_n / kMxPieceRows) * pieces * kMxPieceBytes;
+  m.sm0 = a.sp_w + static_cast<size_t>(m.mt) * pieces * kMxPieceBytes;
+  m.sn = a.sp_x + static_cast<size_t>(m.row_n / kMxPieceRows) * pieces * kMxPieceBytes;
   m.groups = (m.rows + kMxPieceRows - 1) / kMxPieceRows;
-  m.weights_n = a.weights_n;
   m.ok = true;
   return m;
 }
@@ -305,47 +304,27 @@ __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, c
   }
 }
 
-__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// dense: Y rounded once.  With tokens on the M side (stride_n 1) a lane owns 16
-// consecutive elements of a row, stored as 16-byte words where the rows are
-// aligned to them; otherwise the lanes' elements are the neighbours.
+// dense: Y rounded once; 32 lanes write neighbouring columns of a row.
 __device__ __forceinline__ void epilogue(const MxLinearArgs& a, const Item& m, const Plan& p, uint32_t tbase, int bn,
                                          int lanegrp, int colpart, int lane, std::integral_constant<int, kLinear>) {
-  const int r = m.row_m + 32 * lanegrp + lane;
-  const bool wide = a.stride_n == 1 && a.stride_m % (a.y_fp32 ? 4 : 8) == 0;
+  const int n = m.row_m + 32 * lanegrp + lane;
+  const size_t pitch = a.N;
   for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps<kLinear> / 4)) {
     uint32_t v[16];
     tmem_ld16(tbase + c0, v);
     tc_wait_ld();
-    if (r >= a.rows_m) continue;
-    const size_t at = static_cast<size_t>(r) * a.stride_m + static_cast<size_t>(m.row_n + c0) * a.stride_n;
+    if (n >= a.N) continue;
+    const size_t at = static_cast<size_t>(m.row_n + c0) * pitch + n;
     if (a.y_fp32) {
       float* y = static_cast<float*>(a.Y) + at;
-      if (wide && c0 + 16 <= m.rows) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          reinterpret_cast<uint4*>(y)[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c0 + c < m.rows) y[c * a.stride_n] = __uint_as_float(v[c]);
-      }
+      for (int c = 0; c < 16; ++c, y += pitch)
+        if (c0 + c < m.rows) *y = __uint_as_float(v[c]);
     } else {
       __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + at;
-      if (wide && c0 + 16 <= m.rows) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          reinterpret_cast<uint4*>(y)[c] = make_uint4(bf16x2(v[8 * c], v[8 * c + 1]), bf16x2(v[8 * c + 2], v[8 * c + 3]),
-                                                      bf16x2(v[8 * c + 4], v[8 * c + 5]), bf16x2(v[8 * c + 6], v[8 * c + 7]));
-      } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c0 + c < m.rows) y[c * a.stride_n] = __float2bfloat16_rn(__uint_as_float(v[c]));
-      }
+      for (int c = 0; c < 16; ++c, y += pitch)
+        if (c0 + c < m.rows) *y = __float2bfloat16_rn(__uint_as_float(v[c]));
     }
   }
 }
@@ -418,27 +397,26 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
         const Item m = item(i);
         if (!m.ok) continue;
         const int pieces = pieces_of(m.K);
-        const bool n_side = weights == m.weights_n;
-        const uint32_t codes = n_side ? m.box * 128 : kMats * kCodeBytesM;
-        const int scales = n_side ? m.groups : kMats;
+        const uint32_t codes = weights ? kMats * kCodeBytesM : m.box * 128;
+        const int scales = weights ? kMats : m.groups;
         const size_t group = static_cast<size_t>(pieces) * kMxPieceBytes;
-        const uint8_t *s0 = n_side ? m.sn : m.sm0, *s1 = n_side ? m.sn + group : m.sm1;
+        const uint8_t *s0 = weights ? m.sm0 : m.sn, *s1 = weights ? m.sm1 : m.sn + group;
         for (int k0 = 0; k0 < pieces; k0 += 2, ++filled) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          uint8_t* st = stages + stage * p.stage_bytes + (n_side ? kMats * kCodeBytesM : 0);
-          uint8_t* sf = stages + stage * p.stage_bytes + kMats * kCodeBytesM + p.bn * 128 + (n_side ? kMats * kPairBytes : 0);
+          uint8_t* st = stages + stage * p.stage_bytes + (weights ? 0 : kMats * kCodeBytesM);
+          uint8_t* sf = stages + stage * p.stage_bytes + kMats * kCodeBytesM + p.bn * 128 + (weights ? 0 : kMats * kPairBytes);
           uint64_t* bar = &full[stage];
           const uint32_t sbytes = min(2, pieces - k0) * kMxPieceBytes;
           mbar_arrive_expect_tx(bar, codes + scales * sbytes);
-          if (n_side) {
-            tma_load_2d(st, m.n, bar, k0 * 64, m.row_n);
-          } else {
+          if (weights) {
             tma_load_3d(st, m.m0, bar, k0 * 64, m.row_m, m.e);
             if (kGU) tma_load_3d(st + kCodeBytesM, m.m1, bar, k0 * 64, m.row_m, m.e);
+          } else {
+            tma_load_2d(st, m.n, bar, k0 * 64, m.row_n);
           }
           bulk_g2s(sf, s0, sbytes, bar);
           if (scales > 1) bulk_g2s(sf + kPairBytes, s1, sbytes, bar);
@@ -601,7 +579,7 @@ cudaError_t launch(int kind, const typename Args<kMode>::maps& maps, const typen
 
 cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cudaStream_t stream, bool pdl) {
   const Plan p = make_plan(1, a.bn);
-  const long long items = static_cast<long long>((a.rows_m + kMxBM - 1) / kMxBM) * ((a.rows_n + a.bn - 1) / a.bn);
+  const long long items = static_cast<long long>((a.N + kMxBM - 1) / kMxBM) * ((a.M + a.bn - 1) / a.bn);
   if (items > (1ll << 30)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
   return p.row_tiles == 1 ? launch<kLinear, 1>(kKMxGemm, maps, a, p, grid, stream, pdl)

@@ -154,7 +154,9 @@ def test_matmul(M, N, K, y_kind):
 
 @pytest.mark.parametrize("M,N,K,x_kind", [(1, 2048, 2048, "bf16"), (5, 100, 96, "fp16"), (128, 96, 256, "fp32"),
                                           (333, 1001, 2816, "fp16"), (140, 64, 416, "fp32"), (32, 300, 1184, "bf16"),
-                                          (33, 300, 1184, "bf16"), (3, 40, 12320, "bf16"), (3, 40, 16416, "fp32")])
+                                          (33, 300, 1184, "bf16"), (3, 40, 12320, "bf16"), (3, 40, 16416, "fp32"),
+                                          (1, 40, 12320, "bf16"), (8, 200, 2048, "bf16"), (17, 300, 960, "fp32"),
+                                          (32, 130, 512, "fp16")])
 def test_linear(M, N, K, x_kind):
     rng = np.random.default_rng(M + N)
     x = torch.from_numpy(rng.standard_normal((M, K + 32)).astype(np.float32)).to(TYPES[x_kind]).cuda()[:, :K]
