@@ -52,8 +52,13 @@ static_assert(kWeightTokensPerCta <= kRouteWarps, "a weight CTA's tokens fit its
 // Shared memory of one warp of scored routing.
 __host__ __device__ inline int scored_bytes(const RouteScore& score, int E) {
   const int floats = score.n_group > 1 && score.group_shift < 0 ? E : 0;
-  return static_cast<int>(sizeof(ScoredList)) + (4 * floats + 15) / 16 * 16;
+  return static_cast<int>(E <= 256 ? sizeof(ScoredList<8>) : sizeof(ScoredList<32>)) + (4 * floats + 15) / 16 * 16;
 }
+
+// What a launch of the routing kernel does: all of it (its chunks meeting at a
+// barrier over the grid, or the last CTA finishing), or scored routing's
+// selection and then, in a second launch, the placement.
+enum RoutePhase { kWhole, kSelect, kPlace };
 
 // kPL: logits per lane (E <= 32 * kPL).  kScored: select and weigh by `score`.
 template <int kPL, bool kScored>
@@ -62,8 +67,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
                                                               WsHeader* hdr, uint32_t* status,
                                                               int32_t* __restrict__ chunk_hist,
                                                               int32_t* __restrict__ local_rank, int bases_in_smem,
-                                                              int gridsync, int nroute, int tokens, uint32_t k_inv,
-                                                              RouteScore score) {
+                                                              int gridsync, int nroute, int tokens, int phase,
+                                                              uint32_t k_inv, RouteScore score) {
   // [nchunks][E] exclusive per-chunk bases (last CTA, when they fit), or, before them, each warp's
   // ScoredList (scored routing)
   extern __shared__ int32_t s_bases[];
@@ -122,8 +127,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
       atomicOr(&s_mask[sel_i], 1u << tl);
     }
   };
-  if constexpr (kScored) {
-    ScoredList* list = reinterpret_cast<ScoredList*>(reinterpret_cast<char*>(s_bases) + warp * scored_bytes(score, E));
+  if (kScored && phase == kPlace) {
+    for (int a = threadIdx.x; a < ntok * k; a += kRouteThreads) {
+      const int e = __ldcg(out.ids + static_cast<size_t>(t0) * k + a);
+      s_ids[a] = e;
+      atomicOr(&s_mask[e], 1u << ((a * k_inv) >> 20));
+    }
+  } else if constexpr (kScored) {
+    ScoredList<kPL>* list =
+        reinterpret_cast<ScoredList<kPL>*>(reinterpret_cast<char*>(s_bases) + warp * scored_bytes(score, E));
     for (int tl = warp; tl < ntok; tl += kRouteWarps) {
       float x[kPL], b[kPL];
       scored_load<kPL>(logits + static_cast<size_t>(t0 + tl) * E, score.bias, E, score.per_lane, lane, x, b);
@@ -194,11 +206,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (4 * w + i < E) v |= static_cast<uint32_t>(s_cnt[4 * w + i]) << (8 * i);
-      hist[static_cast<size_t>(chunk) * words + w] = v;
+      if (phase != kPlace) hist[static_cast<size_t>(chunk) * words + w] = v;
     }
+    if (phase == kSelect) return;
     for (int e = threadIdx.x; e < E; e += kRouteThreads) s_base[e] = 0;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && phase == kWhole) {
       atom_add_acq_rel_gpu(&hdr->ticket, 1u);
       const long long tw = clock64();
       while (ld_acquire_gpu(&hdr->ticket) < static_cast<uint32_t>(nchunks)) {
@@ -363,6 +376,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
       out.perm[pos] = ga;
       out.inv_perm[ga] = pos;
     }
+    if (phase != kWhole) return;
     __syncthreads();
     if (threadIdx.x == 0 && atom_add_acq_rel_gpu(&hdr->route_done, 1u) == static_cast<uint32_t>(nchunks - 1)) {
       // every CTA has passed the barrier: ready for the next call
@@ -425,11 +439,12 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
     for (int i = 0; i < 6; ++i)
       if (sc.group_size == sc.per_lane << i) sc.group_shift = i;
   }
-  const auto kernel = score ? (E <= 256 ? route_kernel<8, true> : route_kernel<32, true>)
+  const auto kernel = score ? (E <= 256 ? route_kernel<8, true> : E <= 512 ? route_kernel<16, true> : route_kernel<32, true>)
                             : (E <= 256 ? route_kernel<8, false> : route_kernel<32, false>);
   const size_t scored_smem = score ? static_cast<size_t>(kRouteWarps) * scored_bytes(sc, E) : 0;
 
   int gridsync = 0, resident = 0;
+  bool forced = false;  // MOE_ROUTE_MODE is set
   if (nchunks > 1) {  // one chunk needs none of this, and its call is all host time
     // CTAs resident at once, without the bases (the grid-synchronised mode has none).
     int per_sm = 0;
@@ -445,6 +460,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
     // only taken when they fit).
     gridsync = (nchunks <= kGridsyncChunks && nchunks <= resident / 2) ? 1 : 0;
     if (const char* m = std::getenv("MOE_ROUTE_MODE")) {
+      forced = *m != 0;
       if (!std::strcmp(m, "ticket")) gridsync = 0;
       if (!std::strcmp(m, "gridsync") && nchunks <= kGridsyncChunks && nchunks <= resident) gridsync = 1;
     }
@@ -454,19 +470,25 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   }
   const int nweight = score ? 0 : (T + kWeightTokensPerCta - 1) / kWeightTokensPerCta;  // weight CTAs
   cudaLaunchConfig_t cfg = {};
-  // Scored routing, grid-synchronised: one token per warp instead of two where
-  // twice the CTAs still fit.  Selection is a chain of latencies, so a second
-  // token per warp costs as much as the first (777 tokens of 130 experts: 8.5
-  // against 11.0 us).
+  // Scored routing of several chunks.  Up to one CTA per SM with one token per
+  // warp (selection is a chain of latencies: a second token costs as much as the
+  // first): selection and placement in two launches, which no barrier holds up
+  // (1024 tokens of 256 experts 8.6 us, at the barrier 9.1).  More chunks: two
+  // tokens per warp at the barrier (4096 tokens 12.5 us, in two launches 14.8);
+  // where they are not resident together, in two launches (8192 tokens 20 us),
+  // as long as the counts' sums fit.
   int tokens = kRouteTokensPerCta, nroute = nchunks;
   const int nhalf = (T + kRouteWarps - 1) / kRouteWarps;
-  if (score && gridsync && nhalf <= kGridsyncChunks && nhalf <= resident / 2) {
+  const bool single = nhalf <= device_sms();
+  const bool split = score && nchunks > 1 && !forced && (single || !gridsync) && nchunks <= kGridsyncChunks;
+  if (split && single) {
     tokens = kRouteWarps;
     nroute = nhalf;
   }
+  if (split) gridsync = 0;
   cfg.gridDim = dim3(nroute + nweight);
   cfg.blockDim = dim3(kRouteThreads);
-  cfg.dynamicSmemBytes = (bases_in_smem && !gridsync) ? bases_bytes : 0;
+  cfg.dynamicSmemBytes = (bases_in_smem && !gridsync && !split) ? bases_bytes : 0;
   if (cfg.dynamicSmemBytes < scored_smem) cfg.dynamicSmemBytes = scored_smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -474,12 +496,18 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  timer_begin(kKRoute, stream);
-  const cudaError_t err =
-      cudaLaunchKernelEx(&cfg, kernel, logits, T, E, k, block_rows, out, hdr, status, chunk_hist, local_rank,
-                         bases_in_smem && !gridsync, gridsync, nroute, tokens, small_inverse(k), sc);
-  timer_end(kKRoute, stream);
-  return err;
+  auto run = [&](RoutePhase phase) {
+    timer_begin(kKRoute, stream);
+    const cudaError_t err =
+        cudaLaunchKernelEx(&cfg, kernel, logits, T, E, k, block_rows, out, hdr, status, chunk_hist, local_rank,
+                           bases_in_smem && !gridsync && !split, gridsync || split ? 1 : 0, nroute, tokens,
+                           static_cast<int>(phase), small_inverse(k), sc);
+    timer_end(kKRoute, stream);
+    return err;
+  };
+  if (!split) return run(kWhole);
+  const cudaError_t err = run(kSelect);
+  return err != cudaSuccess ? err : run(kPlace);
 }
 
 size_t route_hist_elems(int T, int E) {

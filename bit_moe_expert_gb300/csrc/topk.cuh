@@ -170,9 +170,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Shared memory of a warp that selects by scores: the list of candidates, then,
 // where groups do not fall on whole lanes (group_shift -1), E floats.
+// Rows of up to 256 experts keep 32 candidates, wider ones 128.
+template <int kPL>
+constexpr int kScoredList = kPL == 8 ? 32 : 128;
+template <int kPL>
 struct ScoredList {
-  uint2 key_e[32];
-  float s[32];
+  uint2 key_e[kScoredList<kPL>];
+  float s[kScoredList<kPL>];
 };
 
 // A row's logits and the bias, in flight together (-infinity and 0 past E).
@@ -207,11 +211,11 @@ __device__ __forceinline__ void scored_load(const float* __restrict__ row, const
 // k-th largest choice from below, so the experts at or above it (about k to 2k
 // of them) go to a list in shared memory, and each lane counts for one of them
 // how many come before it.  k rounds of a maximum over the warp took 3,400
-// cycles of a token's 8,400 with k = 8; more than 32 candidates (k close to 32,
-// or many equal choices) still take them.
+// cycles of a token's 8,400 with k = 8; more candidates than the list holds (k
+// close to 32, or many equal choices) still take them.
 template <int kPL, typename Publish>
 __device__ __forceinline__ bool warp_scored_topk(const float (&x)[kPL], const float (&b)[kPL], const RouteScore& sc,
-                                                 int E, int k, int lane, ScoredList* list, Publish publish) {
+                                                 int E, int k, int lane, ScoredList<kPL>* list, Publish publish) {
   const float kNone = -INFINITY;
   const uint32_t kAll = 0xffffffffu;
   const int pl = sc.per_lane;
@@ -327,13 +331,41 @@ __device__ __forceinline__ bool warp_scored_topk(const float (&x)[kPL], const fl
     const bool is = key[c] >= theta;
     const uint32_t m = __ballot_sync(kAll, is);
     const int at = n + __popc(m & ((1u << lane) - 1u));
-    if (is && at < 32) {
+    if (is && at < kScoredList<kPL>) {
       list->key_e[at] = make_uint2(key[c], static_cast<uint32_t>(pl * lane + c));
       list->s[at] = s[c];
     }
     n += __popc(m);
   }
-  if (n > 32) {
+  if (n > 32 && n <= kScoredList<kPL>) {
+    // as below, up to four candidates a lane; the selection goes to the list's front
+    __syncwarp();
+    constexpr int kEach = kScoredList<kPL> / 32;
+    uint2 c[kEach];
+    float cs[kEach];
+    int cr[kEach];
+#pragma unroll
+    for (int h = 0; h < kEach; ++h) {
+      const bool in = lane + 32 * h < n;
+      c[h] = in ? list->key_e[lane + 32 * h] : make_uint2(0u, 0u);
+      cs[h] = in ? list->s[lane + 32 * h] : 0.0f;
+      cr[h] = in ? 0 : k;
+    }
+    for (int j = 0; j < n; ++j) {
+      const uint2 o = list->key_e[j];
+#pragma unroll
+      for (int h = 0; h < kEach; ++h) cr[h] += (o.x > c[h].x || (o.x == c[h].x && o.y < c[h].y)) ? 1 : 0;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < kEach; ++h) {
+      if (cr[h] < k) {
+        list->key_e[cr[h]] = c[h];
+        list->s[cr[h]] = cs[h];
+      }
+    }
+    n = k;
+  } else if (n > 32) {
     // k rounds: the largest key, the lowest expert among equals
     uint32_t sel_e = 0;
     float sel_s = 0.0f;

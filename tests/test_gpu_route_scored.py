@@ -77,6 +77,10 @@ CASES = [  # T, E, k, block_rows, bias, kw
     (70, 1024, 32, 128, True, _kw("sigmoid", 16, 4)),          # the wide selection
     (20, 300, 9, 100, True, _kw("softmax", 3, 2)),
     (2000, 64, 4, 128, True, _kw("sigmoid", 8, 4)),            # many chunks of tokens
+    (30, 1024, 16, 64, True, _kw("sigmoid", 16, 8)),           # more candidates than lanes
+    (40, 352, 8, 64, False, _kw("softmax", 4, 2)),             # between the narrow and the wide selection
+    (3, 513, 32, 16, True, _kw("sigmoid")),
+    (6000, 32, 2, 64, False, _kw("softmax")),                  # chunks that are not resident together
 ]
 
 
@@ -98,8 +102,8 @@ def test_against_the_definition(T, E, k, block_rows, with_bias, kw):
     assert bm.moe_check_status(ws) == 0
 
 
-@pytest.mark.parametrize("mode", ["ticket", "gridsync"])
-def test_both_ways_of_placing_many_chunks(mode, monkeypatch):
+@pytest.mark.parametrize("mode", ["ticket", "gridsync", ""])
+def test_every_way_of_placing_many_chunks(mode, monkeypatch):
     monkeypatch.setenv("MOE_ROUTE_MODE", mode)
     rng = np.random.default_rng(9)
     kw = _kw("softmax", 8, 4)
