@@ -131,31 +131,40 @@ __global__ void __launch_bounds__(kScatterThreads)
   int c = (threadIdx.x >> 5) * 256 + 8 * lane;
   const uint16_t* row = X + static_cast<size_t>(t) * d;
   if (c < d) x.load(row, c); else x.zero();
-  if (threadIdx.x < n) {
-    const int j = threadIdx.x;
+  for (int j = threadIdx.x >> 5; j < n; j += kScatterThreads / 32) {
     long long to = -1, at = 0;
     if (j == s.k) {
       to = static_cast<long long>(s.T) * s.k + t;
       at = mx_scale_offset(t % s.shared_rows, 0, pieces) +
            static_cast<long long>(s.max_blocks + t / s.shared_rows) * pieces * kMxPieceBytes;
     } else {
+      // the last tile that starts at or before p, 32 places at a time: two or
+      // three round trips instead of one for each halving
       const int p = __ldg(s.inv_perm + static_cast<size_t>(t) * s.k + j);
-      // the last tile that starts at or before p
-      int lo = 0, hi = min(max(*s.num_blocks, 0), s.max_blocks);
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(s.block_map + 3 * mid + 1) <= p) lo = mid; else hi = mid;
+      int lo = 0, n_left = min(max(*s.num_blocks, 0), s.max_blocks);  // among lo .. lo + n_left - 1
+      int first = -1;
+      while (n_left > 0) {
+        const int step = (n_left + 31) / 32;
+        const int i = lane * step;
+        const int v = i < n_left ? __ldg(s.block_map + 3 * (lo + i) + 1) : 0x7FFFFFFF;
+        const int before = __popc(__ballot_sync(0xffffffffu, v <= p));  // the tiles' starts ascend
+        if (before == 0) break;
+        first = __shfl_sync(0xffffffffu, v, before - 1);
+        lo += (before - 1) * step;
+        n_left = step == 1 ? 0 : min(step, n_left - (before - 1) * step);
       }
-      const int r = hi > 0 ? p - __ldg(s.block_map + 3 * lo + 1) : -1;
-      if (p >= 0 && p < s.T * s.k && r >= 0 && r < kMxMaxBN) {
+      const int r = first >= 0 ? p - first : -1;
+      if (p >= 0 && p < s.T * s.k && r >= 0 && r < kMxMaxBN && lo < s.max_blocks) {
         to = p;
         at = mx_scale_offset(r, 0, pieces) + static_cast<long long>(lo) * pieces * kMxPieceBytes;
-      } else {
+      } else if (lane == 0) {
         record_status(s.status, MOE_ERR_INVALID_ARG);
       }
     }
-    s_row[j] = to;
-    s_scale[j] = at;
+    if (lane == 0) {
+      s_row[j] = to;
+      s_scale[j] = at;
+    }
   }
   __syncthreads();
   for (int base = 0; base < d; base += 8 * kScatterThreads) {
