@@ -35,11 +35,25 @@ constexpr int kWeightsWarp = 0;
 constexpr int kActivationsWarp = 1;
 constexpr int kMmaWarp = 2;
 constexpr int kEpiWarp0 = 3;
-// Epilogue warps, a multiple of four (one per quarter of the tensor-memory lanes).
-template <int kMode>
-constexpr int kEpiWarps = kMode == kGateUp ? 16 : 8;
-template <int kMode>
-constexpr int kThreads = (kEpiWarp0 + kEpiWarps<kMode>) * 32;
+// A launch's variant.  kRowTiles: 128-row groups of scales of the tokens (tiles of
+// up to 128, or of 256).  kHold: there is room for one accumulator only, so the
+// epilogue takes its columns into registers and releases it before it works on
+// them (8192^3 200 -> 195 us, 4096^3 42.4 -> 37.5; gate/up of 4096 tokens in
+// tiles of 128 75 -> 62); with more accumulators nothing waits for it, and the
+// registers would keep the CTA from starting beside the previous kernel's (256 x
+// 2048 -> 2048 6.1 -> 7.1 us).
+template <int kMode_, int kRowTiles_, bool kHold_>
+struct Variant {
+  static constexpr int kMode = kMode_, kRowTiles = kRowTiles_;
+  static constexpr bool kHold = kHold_;
+  // epilogue warps, a multiple of four (one per quarter of the tensor-memory lanes)
+  static constexpr int kEpiWarps = kMode == kGateUp || kHold ? 16 : 8;
+  static constexpr int kParts = kEpiWarps / 4;  // shares of the columns
+  static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+  // what one turn of the epilogue's loop takes: groups of eight (gate/up) or 16 columns
+  static constexpr int kGroup = kMode == kGateUp ? 8 : 16;
+  static constexpr int kHeld = kHold ? 128 * kRowTiles / (kGroup * kParts) : 1;
+};
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAccs = 8;
@@ -241,8 +255,9 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t v, int lane) {
 // consecutive columns of h, one block, so a token's largest magnitude is one
 // reduction over the lanes; eight tokens' codes are turned by a nibble
 // transposition into words of eight columns of one token.
-__device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, const Plan& p, uint32_t tbase, int bn,
-                                         int lanegrp, int colpart, int lane, std::integral_constant<int, kGateUp>) {
+template <typename V, typename Release>
+__device__ __forceinline__ void epilogue_gate_up(const MxExpertArgs& a, const Item& m, const Plan& p, uint32_t tbase,
+                                                 int bn, int lanegrp, int colpart, int lane, Release release) {
   const int I = m.shared ? a.I_shared : a.I;
   const int n0 = m.mt * kMxBM + 32 * lanegrp;
   const int pieces = pieces_of(I);
@@ -250,90 +265,133 @@ __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, c
   uint8_t* hs = (m.shared ? a.sp_h_s : a.sp_h_r) +
                 (static_cast<size_t>(m.slot) * pieces + m.mt) * kMxPieceBytes + lanegrp;
   const bool valid = n0 < I;  // the same for the whole warp; past I the piece's scale bytes are zeros
-  for (int c0 = 8 * colpart; c0 < bn; c0 += 8 * (kEpiWarps<kGateUp> / 4)) {
-    uint32_t g[8], u[8];
-    tmem_ld8(tbase + c0, g);
-    tmem_ld8(tbase + p.bn + c0, u);
+  int first = 8 * colpart;
+  do {  // with kHold, one turn
+    uint32_t g[V::kHeld][8], u[V::kHeld][8];
+#pragma unroll
+    for (int i = 0; i < V::kHeld; ++i) {
+      const int c0 = first + 8 * V::kParts * i;
+      if (c0 < bn) {
+        tmem_ld8(tbase + c0, g[i]);
+        tmem_ld8(tbase + p.bn + c0, u[i]);
+      }
+    }
     tc_wait_ld();
-    uint32_t code = 0, bytes[2] = {0, 0};
+    if (V::kHold) release();
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {
-      float h[2];
+    for (int i = 0; i < V::kHeld; ++i) {
+      const int c0 = first + 8 * V::kParts * i;
+      if (c0 >= m.rows) break;
+      uint32_t code = 0, bytes[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float v = mx_swiglu(__uint_as_float(g[c + i]), __uint_as_float(u[c + i]));
-        const uint32_t byte = mx_warp_scale_byte(v);
-        bytes[c >> 2] |= byte << (8 * ((c + i) & 3));
-        h[i] = v * mx_inverse_scale(byte);
+      for (int c = 0; c < 8; c += 2) {
+        float h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float v = mx_swiglu(__uint_as_float(g[i][c + j]), __uint_as_float(u[i][c + j]));
+          const uint32_t byte = mx_warp_scale_byte(v);
+          bytes[c >> 2] |= byte << (8 * ((c + j) & 3));
+          h[j] = v * mx_inverse_scale(byte);
+        }
+        code |= f32x2_to_e2m1x2(h[0], h[1]) << (4 * c);
       }
-      code |= f32x2_to_e2m1x2(h[0], h[1]) << (4 * c);
-    }
-    code = transpose_nibbles(code, lane);
-    const int r = c0 + (lane & 7);
-    if (r < m.rows) {
-      if (valid) *reinterpret_cast<uint32_t*>(hq + static_cast<size_t>(r) * (I / 2)) = code;
-      if (lane < 8) {
-        const uint32_t word = (lane & 4) ? bytes[1] : bytes[0];
-        hs[(r % 32) * 16 + (r / 32) * 4] = valid ? static_cast<uint8_t>(word >> (8 * (lane & 3))) : 0;
+      code = transpose_nibbles(code, lane);
+      const int r = c0 + (lane & 7);
+      if (r < m.rows) {
+        if (valid) *reinterpret_cast<uint32_t*>(hq + static_cast<size_t>(r) * (I / 2)) = code;
+        if (lane < 8) {
+          const uint32_t word = (lane & 4) ? bytes[1] : bytes[0];
+          hs[(r % 32) * 16 + (r / 32) * 4] = valid ? static_cast<uint8_t>(word >> (8 * (lane & 3))) : 0;
+        }
       }
     }
-  }
+    first += 8 * V::kParts * V::kHeld;
+  } while (!V::kHold && first < bn);
+  if (!V::kHold) release();
 }
 
-// down: fp32 rows of the experts' outputs, routed ones in permuted order, then
-// the shared expert's in token order; 32 lanes write one 128-byte line.
+// Sixteen rows of a lane's column of the result, of which `valid` exist; `at`:
+// the first one's element, the others `pitch` apart.
+template <typename Store>
+__device__ __forceinline__ void store_rows(size_t at, size_t pitch, int valid, const uint32_t (&v)[16], Store store) {
+  if (valid >= 16) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c, at += pitch) store(at, __uint_as_float(v[c]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 16; ++c, at += pitch)
+      if (c < valid) store(at, __uint_as_float(v[c]));
+  }
+}
+struct OutF32 {
+  float* y;
+  __device__ __forceinline__ void rows(size_t at, size_t pitch, int valid, const uint32_t (&v)[16]) const {
+    store_rows(at, pitch, valid, v, [&](size_t i, float x) { y[i] = x; });
+  }
+};
+struct OutLinear {
+  void* y;
+  int fp32;
+  __device__ __forceinline__ void rows(size_t at, size_t pitch, int valid, const uint32_t (&v)[16]) const {
+    if (fp32)
+      store_rows(at, pitch, valid, v, [&](size_t i, float x) { static_cast<float*>(y)[i] = x; });
+    else
+      store_rows(at, pitch, valid, v, [&](size_t i, float x) { static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(x); });
+  }
+};
+
+// down and dense: a lane's column n of the tile's rows, from row `row0` of the
+// result on; 32 lanes write neighbouring columns of a row.
+template <typename V, typename Out, typename Release>
+__device__ __forceinline__ void epilogue_rows(Out out, size_t row0, int n, int N, int rows, uint32_t tbase, int bn,
+                                              int colpart, Release release) {
+  const size_t pitch = N;
+  int first = 16 * colpart;
+  do {  // with kHold, one turn
+    uint32_t v[V::kHeld][16];
+#pragma unroll
+    for (int i = 0; i < V::kHeld; ++i) {
+      const int c0 = first + 16 * V::kParts * i;
+      if (c0 < bn) tmem_ld16(tbase + c0, v[i]);
+    }
+    tc_wait_ld();
+    if (V::kHold) release();
+    if (n < N) {
+#pragma unroll
+      for (int i = 0; i < V::kHeld; ++i) {
+        const int c0 = first + 16 * V::kParts * i;
+        if (c0 < rows) out.rows((row0 + c0) * pitch + n, pitch, rows - c0, v[i]);
+      }
+    }
+    first += 16 * V::kParts * V::kHeld;
+  } while (!V::kHold && first < bn);
+  if (!V::kHold) release();
+}
+
+template <typename V, typename Release>
 __device__ __forceinline__ void epilogue(const MxExpertArgs& a, const Item& m, const Plan& p, uint32_t tbase, int bn,
-                                         int lanegrp, int colpart, int lane, std::integral_constant<int, kDown>) {
-  const int n = m.mt * kMxBM + 32 * lanegrp + lane;
-  const size_t pitch = a.d;
-  float* y = a.ypart + (static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0 + 16 * colpart) * pitch + n;
-  for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps<kDown> / 4), y += 16 * (kEpiWarps<kDown> / 4) * pitch) {
-    uint32_t v[16];
-    tmem_ld16(tbase + c0, v);
-    tc_wait_ld();
-    if (n >= a.d) continue;
-    float* to = y;
-    if (c0 + 16 <= m.rows) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c, to += pitch) *to = __uint_as_float(v[c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 16; ++c, to += pitch)
-        if (c0 + c < m.rows) *to = __uint_as_float(v[c]);
-    }
+                                         int lanegrp, int colpart, int lane, Release release) {
+  if constexpr (V::kMode == kGateUp) {
+    epilogue_gate_up<V>(a, m, p, tbase, bn, lanegrp, colpart, lane, release);
+  } else {
+    // fp32 rows of the experts' outputs, routed ones in permuted order, then the shared expert's in token order
+    epilogue_rows<V>(OutF32{a.ypart}, static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0,
+                     m.mt * kMxBM + 32 * lanegrp + lane, a.d, m.rows, tbase, bn, colpart, release);
   }
 }
 
-// dense: Y rounded once; 32 lanes write neighbouring columns of a row.
-__device__ __forceinline__ void epilogue(const MxLinearArgs& a, const Item& m, const Plan& p, uint32_t tbase, int bn,
-                                         int lanegrp, int colpart, int lane, std::integral_constant<int, kLinear>) {
+template <typename V, typename Release>
+__device__ __forceinline__ void epilogue(const MxLinearArgs& a, const Item& m, const Plan&, uint32_t tbase, int bn,
+                                         int lanegrp, int colpart, int lane, Release release) {
   const int n = m.row_m + 32 * lanegrp + lane;
-  const size_t pitch = a.N;
-  for (int c0 = 16 * colpart; c0 < bn; c0 += 16 * (kEpiWarps<kLinear> / 4)) {
-    uint32_t v[16];
-    tmem_ld16(tbase + c0, v);
-    tc_wait_ld();
-    if (n >= a.N) continue;
-    const size_t at = static_cast<size_t>(m.row_n + c0) * pitch + n;
-    if (a.y_fp32) {
-      float* y = static_cast<float*>(a.Y) + at;
-#pragma unroll
-      for (int c = 0; c < 16; ++c, y += pitch)
-        if (c0 + c < m.rows) *y = __uint_as_float(v[c]);
-    } else {
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + at;
-#pragma unroll
-      for (int c = 0; c < 16; ++c, y += pitch)
-        if (c0 + c < m.rows) *y = __float2bfloat16_rn(__uint_as_float(v[c]));
-    }
-  }
+  epilogue_rows<V>(OutLinear{a.Y, a.y_fp32}, m.row_n, n, a.N, m.rows, tbase, bn, colpart, release);
 }
 
-// kRowTiles: 128-row groups of scales of the N side (bn up to 128, or 256).
-template <int kMode, int kRowTiles>
-__global__ void __launch_bounds__(kThreads<kMode>, 1)
-    mx_gemm_kernel(const __grid_constant__ typename Args<kMode>::maps maps,
-                   const __grid_constant__ typename Args<kMode>::type a, const Plan p) {
+template <typename V>
+__global__ void __launch_bounds__(V::kThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ typename Args<V::kMode>::maps maps,
+                   const __grid_constant__ typename Args<V::kMode>::type a, const Plan p) {
+  constexpr int kMode = V::kMode, kRowTiles = V::kRowTiles;
   constexpr int kMats = kMode == kGateUp ? 2 : 1;
   constexpr bool kGU = kMode == kGateUp;
   extern __shared__ uint8_t smem_raw[];
@@ -354,7 +412,7 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
   // The routing has completed by now (the kernel before this one lets this one
   // start only after its own wait), so only the activations are waited for.
   const Sched s = make_sched(a, p, kGU);
-  for (int i = threadIdx.x; i < min(s.n, kEntries); i += kThreads<kMode>) entries[i] = make_entry(a, s, s.first + i * s.step);
+  for (int i = threadIdx.x; i < min(s.n, kEntries); i += V::kThreads) entries[i] = make_entry(a, s, s.first + i * s.step);
   auto item = [&](int i) {
     return get_item(a, maps, p, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
   };
@@ -365,7 +423,7 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
     }
     for (int i = 0; i < p.acc_bufs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpiWarps<kMode>);
+      mbar_init(&acc_empty[i], V::kEpiWarps);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -536,10 +594,12 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t tbase = tmem + (static_cast<uint32_t>(lanegrp * 32) << 16) + accb * kMats * p.bn;
-      epilogue(a, m, p, tbase, tile_n(m.rows), lanegrp, colpart, lane, std::integral_constant<int, kMode>{});
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[accb]);
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[accb]);
+      };
+      epilogue<V>(a, m, p, tbase, tile_n(m.rows), lanegrp, colpart, lane, release);
       if (++accb == p.acc_bufs) {
         accb = 0;
         accphase ^= 1;
@@ -553,24 +613,24 @@ __global__ void __launch_bounds__(kThreads<kMode>, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int kMode, int kRowTiles>
-cudaError_t launch(int kind, const typename Args<kMode>::maps& maps, const typename Args<kMode>::type& a, const Plan& p,
-                   int grid, cudaStream_t stream, bool pdl) {
+template <typename V>
+cudaError_t launch(int kind, const typename Args<V::kMode>::maps& maps, const typename Args<V::kMode>::type& a,
+                   const Plan& p, int grid, cudaStream_t stream, bool pdl) {
   const int smem = p.stages * p.stage_bytes + kSmemFixed;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_kernel<kMode, kRowTiles>), smem);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(mx_gemm_kernel<V>), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads<kMode>);
+  cfg.blockDim = dim3(V::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   timer_begin(kind, stream);
-  e = cudaLaunchKernelEx(&cfg, mx_gemm_kernel<kMode, kRowTiles>, maps, a, p);
+  e = cudaLaunchKernelEx(&cfg, mx_gemm_kernel<V>, maps, a, p);
   timer_end(kind, stream);
   return e;
 }
@@ -582,15 +642,17 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cu
   const long long items = static_cast<long long>((a.N + kMxBM - 1) / kMxBM) * ((a.M + a.bn - 1) / a.bn);
   if (items > (1ll << 30)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
-  return p.row_tiles == 1 ? launch<kLinear, 1>(kKMxGemm, maps, a, p, grid, stream, pdl)
-                          : launch<kLinear, 2>(kKMxGemm, maps, a, p, grid, stream, pdl);
+  return p.row_tiles == 1 ? launch<Variant<kLinear, 1, false>>(kKMxGemm, maps, a, p, grid, stream, pdl)
+                          : launch<Variant<kLinear, 2, true>>(kKMxGemm, maps, a, p, grid, stream, pdl);
 }
 
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream) {
   const int bn = a.I_shared > 0 && a.bn_s > a.bn_r ? a.bn_s : a.bn_r;
-  cudaError_t e = launch<kGateUp, 1>(kKMxGateUp, maps, a, make_plan(2, bn), a.num_sms, stream, true);
+  const Plan p = make_plan(2, bn);
+  cudaError_t e = p.acc_bufs == 1 ? launch<Variant<kGateUp, 1, true>>(kKMxGateUp, maps, a, p, a.num_sms, stream, true)
+                                  : launch<Variant<kGateUp, 1, false>>(kKMxGateUp, maps, a, p, a.num_sms, stream, true);
   if (e != cudaSuccess) return e;
-  e = launch<kDown, 1>(kKMxDown, maps, a, make_plan(1, bn), a.num_sms, stream, true);
+  e = launch<Variant<kDown, 1, false>>(kKMxDown, maps, a, make_plan(1, bn), a.num_sms, stream, true);
   if (e != cudaSuccess) return e;
   return launch_mx_combine(a.ypart, a.inv_perm, a.w, a.T, a.d, a.k, a.I_shared > 0, a.Y, a.status, a.num_sms, stream);
 }
