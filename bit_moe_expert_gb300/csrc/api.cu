@@ -269,6 +269,15 @@ bool encode_mx_weights(CUtensorMap* map, const uint8_t* q, int E, int N, int row
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// packed scales as rows of one 512-byte piece, boxes of two pieces; pieces past the end read as zeros
+bool encode_mx_scales(CUtensorMap* map, const uint8_t* sp, long long pieces) {
+  if (!get_encoder()) return false;
+  const cuuint64_t dims[2] = {kMxPieceBytes / 4, static_cast<cuuint64_t>(pieces)};
+  const cuuint64_t strides[1] = {kMxPieceBytes};
+  const cuuint32_t box[2] = {kMxPieceBytes / 4, 2};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, sp, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 bool pdl_enabled() { return env_flag("MOE_PDL", true); }
 
 int device_sms() { return sm_count(); }

@@ -183,6 +183,7 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMap
 // ---------------------------------------------------------------- host helpers of api.cu
 bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows);
 bool encode_mx_weights(CUtensorMap* map, const uint8_t* q, int E, int N, int row_bytes, int box_rows);
+bool encode_mx_scales(CUtensorMap* map, const uint8_t* sp, long long pieces);
 bool pdl_enabled();  // the environment variable MOE_PDL
 int device_sms();    // 0: no device
 // moe_route_scored's checks of everything but the workspace, and its launch.
@@ -240,6 +241,13 @@ struct MxLinearMaps {
   CUtensorMap w;  // codes [1][N][K/2], box (128 bytes, 128 rows, 1)
   CUtensorMap x;  // codes [M][K/2], box (128 bytes, bn rows)
 };
+// The same product by pairs of CTAs, 256 weight rows x 256 tokens a pair.
+constexpr int kMxPair = 1 << 16;  // MxLinearArgs::bn of this form; no height of a tile
+struct MxPairMaps {
+  CUtensorMap w, x;    // codes, boxes of 128 rows
+  CUtensorMap sw, sx;  // packed scales as [pieces][128] words, box (128, 2)
+};
+cudaError_t launch_mx_pair(const MxLinearArgs& a, const MxPairMaps& maps, cudaStream_t stream, bool pdl);
 cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cudaStream_t stream, bool pdl);
 
 struct MxExpertArgs {

@@ -50,25 +50,37 @@ moe_status check_matmul(int M, const moe_mx_mat* W, int N, int K, const void* Y,
 // high, quantisation included): 256 x 2048 -> 2048 6.1 / 6.8 / 8.5 us, 512 x 4096
 // -> 8192 21.3 / 14.8 / 13.6 us, 333 x 2816 -> 1001 7.2 / 7.5 / 9.1 us, 1024 x
 // 2048 -> 2048 8.9 / 8.3 / 9.2 us: the model picks the least of each.
+//
+// Returns kMxPair, tiles of 256 x 256 by pairs of CTAs, where tiles of 256 are best,
+// each pair has a second one (the first starts later than a CTA's own) and their
+// stages outweigh the epilogue.  Measured (fp32 Y, the product alone, one CTA / a
+// pair): 8192 x 8192 -> 8192 180 / 158 us, 16384 x 2048 -> 4096 75.3 / 62.7 us,
+// 4096 x 4096 -> 4096 32.7 / 30.3 us, 5001 x 1056 -> 4099 31.3 / 27.8 us, 2048 x
+// 4096 -> 4096 17.3 / 17.4 us; without a second tile 512 x 8192 -> 8192 14.6 / 15.4
+// us, 2048 x 2048 -> 2048 7.9 / 8.8 us; of few stages 2048 x 1024 -> 4096 9.6 / 9.9
+// us, 16384 x 512 -> 8192 85.5 / 91.0 us.
 int linear_tile(int M, int N, int K, int num_sms) {
   int best = 0;
   double least = 0;
+  const int stages = (K + kMxStageK - 1) / kMxStageK;
+  auto tiles = [&](int rows, int cols) {
+    return static_cast<long long>((N + rows - 1) / rows) * ((M + cols - 1) / cols);
+  };
   for (int bn : {64, 128, 256, M <= kMxMaxBN ? round16(M) : 64}) {
-    const long long tiles = static_cast<long long>((N + kMxBM - 1) / kMxBM) * ((M + bn - 1) / bn);
-    const double turns = static_cast<double>((tiles + num_sms - 1) / num_sms);
-    const double clocks = turns * ((K + kMxStageK - 1) / kMxStageK * (290 + 2.3 * bn) + 1500 + 8 * bn);
+    const double turns = static_cast<double>((tiles(kMxBM, bn) + num_sms - 1) / num_sms);
+    const double clocks = turns * (stages * (290 + 2.3 * bn) + 1500 + 8 * bn);
     if (best == 0 || clocks < least) {
       least = clocks;
       best = bn;
     }
   }
+  if (best == 256 && stages > 4 && tiles(2 * kMxBM, 256) > num_sms / 2) return kMxPair;
   return best;
 }
 
 moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K, void* Y, moe_dtype y_type,
                   uint32_t* status, moe_stream stream) {
   MxLinearArgs a{};
-  MxLinearMaps maps;
   a.sp_w = W.sp;
   a.sp_x = A.sp;
   a.Y = Y;
@@ -80,10 +92,20 @@ moe_status matmul(const moe_mx_mat& A, int M, const moe_mx_mat& W, int N, int K,
   if (a.num_sms <= 0) return MOE_ERR_CUDA;
   a.bn = linear_tile(M, N, K, a.num_sms);
   a.y_fp32 = y_type == MOE_FP32;
-  if (!encode_mx_weights(&maps.w, W.q, 1, N, K / 2, kMxBM) || !encode_mx_codes(&maps.x, A.q, M, K / 2, a.bn))
-    return MOE_ERR_CUDA;
-  return launch_mx_linear(a, maps, reinterpret_cast<cudaStream_t>(stream), pdl_enabled()) == cudaSuccess ? MOE_OK
-                                                                                                         : MOE_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (a.bn == kMxPair) {
+    MxPairMaps maps;
+    if (encode_mx_weights(&maps.w, W.q, 1, N, K / 2, kMxBM) && encode_mx_codes(&maps.x, A.q, M, K / 2, kMxBM) &&
+        encode_mx_scales(&maps.sw, W.sp, static_cast<long long>(mx_pieces(N, K))) &&
+        encode_mx_scales(&maps.sx, A.sp, static_cast<long long>(mx_pieces(M, K))))
+      e = launch_mx_pair(a, maps, st, pdl_enabled());
+  } else {
+    MxLinearMaps maps;
+    if (encode_mx_weights(&maps.w, W.q, 1, N, K / 2, kMxBM) && encode_mx_codes(&maps.x, A.q, M, K / 2, a.bn))
+      e = launch_mx_linear(a, maps, st, pdl_enabled());
+  }
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Tile heights of an expert call in MMA columns.  The shared expert's tiles are

@@ -22,6 +22,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "kernels.h"
 #include "mx.cuh"
 #include "ptx.cuh"
@@ -613,6 +615,211 @@ __global__ void __launch_bounds__(V::kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
+// ------------------------------------------------------------------ pairs of CTAs
+// The dense product's tile of 128 x 256 is bound by shared memory (48 KB of MMA
+// reads and 51 KB of loads a stage, 790 clocks at 128 bytes a clock, against 512
+// of MMA).  A pair of CTAs (a cluster of two, on two SMs that share a tensor
+// operation: cta_group::2) takes 256 weight rows x 256 tokens: each holds half of
+// the weight rows and half of the tokens, and the MMA reads the other half from
+// the peer, so a CTA's stage is 32 KB of reads and 35 KB of loads, and the 510
+// clocks measured are the MMA's (8192 x 8192 -> 8192, fp32 Y: 180 -> 158 us; the
+// first six stages of a tile still take about 900 each).  linear_tile says where it
+// pays.
+//
+// Rank 0 issues copies and MMAs for both.  Every load of the pair completes on
+// rank 0's barrier `full`, which rank 0 alone arms, for the bytes of both; a commit
+// arrives at `empty` (and `acc_full`) of both ranks; both ranks' epilogue warps arrive
+// at rank 0's `acc_empty`.
+constexpr int kPairRows = 2 * kMxBM;
+constexpr int kPairHalf = kMxBM * 128;  // a CTA's half of an operand's codes of a stage
+constexpr int kPairStage = 2 * kPairHalf + 3 * kPairBytes;
+constexpr int kPairStages = 6;
+constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 1024;
+constexpr int kPairScaleCols = 8 + 16;  // of a stage: this CTA's weight rows, all tokens
+using PairVariant = Variant<kLinear, 2, true>;
+static_assert(kPairSmem <= kSmemLimit, "shared memory of a pair's CTA");
+
+__global__ void __launch_bounds__(PairVariant::kThreads, 1)
+    mx_pair_kernel(const __grid_constant__ MxPairMaps maps, const __grid_constant__ MxLinearArgs a) {
+  using V = PairVariant;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + kPairStages * kPairStage);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* acc_full = empty + kPairStages;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* done = acc_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full[i], 2);  // rank 0's weights' and activations' expect_tx, for the bytes of both ranks
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 2 * V::kEpiWarps);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive_release();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int pieces = pieces_of(a.K);
+  const int mts = (a.N + kPairRows - 1) / kPairRows;
+  const int items = mts * ((a.M + kPairRows - 1) / kPairRows);
+  const int step = static_cast<int>(gridDim.x >> 1), first = static_cast<int>(blockIdx.x >> 1);
+  auto fail = [&]() {
+    record_status(a.status, MOE_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp == kWeightsWarp || warp == kActivationsWarp) {
+    const bool weights = warp == kWeightsWarp;
+    if (lane == 0) {
+      if (!weights) pdl_wait();
+      int stage = 0;
+      uint32_t phase = 0, filled = 0;
+      bool ok = true;
+      for (int it = first; it < items && ok; it += step) {
+        const int mt = it % mts, nt = it / mts;
+        for (int k0 = 0; k0 < pieces; k0 += 2, ++filled) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          uint8_t* st = stages + stage * kPairStage;
+          uint8_t* sf = st + 2 * kPairHalf;
+          const uint32_t bar = mapa_shared(&full[stage], 0);
+          if (weights) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kPairHalf + kPairBytes));
+            tma_load_3d_pair(st, &maps.w, bar, k0 * 64, mt * kPairRows + rank * kMxBM, 0);
+            tma_load_2d_pair(sf, &maps.sw, bar, 0, (2 * mt + rank) * pieces + k0);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kPairHalf + 2 * kPairBytes));
+            tma_load_2d_pair(st + kPairHalf, &maps.x, bar, k0 * 64, nt * kPairRows + rank * kMxBM);
+            tma_load_2d_pair(sf + kPairBytes, &maps.sx, bar, 0, 2 * nt * pieces + k0);
+            tma_load_2d_pair(sf + 2 * kPairBytes, &maps.sx, bar, 0, (2 * nt + 1) * pieces + k0);
+          }
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // never leave while a load into this CTA's shared memory may be in flight: the commit of a stage's MMAs, which
+      // waited for its loads, frees it
+      const int n = filled < kPairStages ? static_cast<int>(filled) : kPairStages;
+      for (int i = 0; i < n && ok; ++i) {
+        stage = stage == 0 ? kPairStages - 1 : stage - 1;
+        if (stage == kPairStages - 1) phase ^= 1;
+        if (!mbar_wait(&empty[stage], phase, abort_flag)) {
+          fail();
+          ok = false;
+        }
+      }
+      if (weights) pdl_wait();
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (rank == 0) {
+      const uint32_t stage0 = smem_u32(stages);
+      const uint64_t ad0 = smem_desc_sw128_kmajor(stage0), bd0 = smem_desc_sw128_kmajor(stage0 + kPairHalf);
+      const uint64_t sd0 = smem_desc_scales(stage0 + 2 * kPairHalf);
+      const uint32_t idesc0 = idesc_mxfp(kPairRows, 256, 0), idesc1 = idesc_mxfp(kPairRows, 256, 2);
+      const int n64 = (a.K + 63) / 64;
+      const bool leader = elect_one();
+      int stage = 0;
+      uint32_t phase = 0, accphase = 0, set = 0, at = 0;
+      for (int it = first; it < items; it += step) {
+        mbar_wait_issue(acc_empty, accphase ^ 1, abort_flag, a.status);
+        tc_fence_after();
+        for (int k = 0; k < n64; k += 4) {
+          mbar_wait_issue(&full[stage], phase, abort_flag, a.status);
+          tc_fence_after();
+          const uint64_t ad = ad0 + at, bd = bd0 + at, sd = sd0 + at;
+          const uint32_t ta = tmem + 256 + set * kPairScaleCols, tb = ta + 8;
+          if (leader) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (j == 1 && k + 2 >= n64) break;
+              const uint64_t sj = sd + j * (kMxPieceBytes >> 4);
+              tc_cp_scales_pair(ta + 4 * j, sj);
+              tc_cp_scales_pair(tb + 8 * j, sj + (kPairBytes >> 4));
+              tc_cp_scales_pair(tb + 8 * j + 4, sj + 2 * (kPairBytes >> 4));
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk > 0 && k + kk >= n64) break;
+              tc_mma_mxfp_pair(tmem, ad + 2 * kk, bd + 2 * kk, (kk & 1) ? idesc1 : idesc0, ta + 4 * (kk >> 1),
+                               tb + 8 * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
+            }
+            tc_commit_pair(&empty[stage]);
+            if (k + 4 >= n64) tc_commit_pair(acc_full);
+          }
+          set ^= 1;
+          at += kPairStage >> 4;
+          if (++stage == kPairStages) {
+            stage = 0;
+            at = 0;
+            phase ^= 1;
+          }
+        }
+        accphase ^= 1;
+      }
+      __syncwarp();
+      if (leader) tc_commit_pair(done);
+    }
+    // every MMA has completed, and the last arrival at both ranks has come, before tensor memory is released
+    __syncwarp();
+    if (lane == 0 && !mbar_wait(done, 0, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
+    __syncwarp();
+  } else {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lanegrp = warp & 3, colpart = (warp - kEpiWarp0) >> 2;
+    const uint32_t acc_empty0 = mapa_shared(acc_empty, 0);
+    uint32_t accphase = 0;
+    for (int it = first; it < items; it += step) {
+      if (!mbar_wait(acc_full, accphase, abort_flag)) {
+        if (lane == 0) fail();
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0);
+      };
+      const int mt = it % mts, nt = it / mts;
+      const int n = mt * kPairRows + rank * kMxBM + 32 * lanegrp + lane;
+      epilogue_rows<V>(OutLinear{a.Y, a.y_fp32}, nt * kPairRows, n, a.N, min(kPairRows, a.M - nt * kPairRows),
+                       tmem + (static_cast<uint32_t>(lanegrp * 32) << 16), kPairRows, colpart, release);
+      accphase ^= 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves, or frees tensor memory, while the other may still reach its barriers or operands
+  cluster_arrive_release();
+  cluster_wait();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
 template <typename V>
 cudaError_t launch(int kind, const typename Args<V::kMode>::maps& maps, const typename Args<V::kMode>::type& a,
                    const Plan& p, int grid, cudaStream_t stream, bool pdl) {
@@ -644,6 +851,69 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearMaps& maps, cu
   const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
   return p.row_tiles == 1 ? launch<Variant<kLinear, 1, false>>(kKMxGemm, maps, a, p, grid, stream, pdl)
                           : launch<Variant<kLinear, 2, true>>(kKMxGemm, maps, a, p, grid, stream, pdl);
+}
+
+namespace {
+// Pairs of mx_pair_kernel that the device runs at once (SMs that a cluster can
+// take in twos), found once per device.
+cudaError_t pairs_resident(int* most) {
+  static std::mutex mu;
+  static int known[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(PairVariant::kThreads);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    known[dev] = n;
+  }
+  *most = known[dev];
+  return cudaSuccess;
+}
+}  // namespace
+
+cudaError_t launch_mx_pair(const MxLinearArgs& a, const MxPairMaps& maps, cudaStream_t stream, bool pdl) {
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(mx_pair_kernel), kPairSmem);
+  if (e != cudaSuccess) return e;
+  const long long items = static_cast<long long>((a.N + kPairRows - 1) / kPairRows) * ((a.M + kPairRows - 1) / kPairRows);
+  if (items > (1ll << 30)) return cudaErrorInvalidValue;
+  int most = 0;  // pairs that run at once
+  e = pairs_resident(&most);
+  if (e != cudaSuccess) return e;
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  const int pairs = static_cast<int>(items < most ? items : most);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(PairVariant::kThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  timer_begin(kKMxGemm, stream);
+  e = cudaLaunchKernelEx(&cfg, mx_pair_kernel, maps, a);
+  timer_end(kKMxGemm, stream);
+  return e;
 }
 
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream) {

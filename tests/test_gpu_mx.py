@@ -184,6 +184,29 @@ def test_a_nan_stays_in_its_row():
         assert bad[[7, 11]].all() and not np.delete(bad, [7, 11], 0).any()
 
 
+@pytest.mark.parametrize("M,N,K,y_kind", [(4865, 4353, 1312, "fp32"), (5001, 4099, 1056, "bf16"), (2600, 2100, 3392, "fp32")])
+def test_large_products(M, N, K, y_kind):
+    """Sizes for pairs of CTAs, with last tiles of one row and stages past K: values, a row of NaN, the bits of a row alone."""
+    rng = np.random.default_rng(M + N)
+    x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).cuda()
+    x[M - 2, K - 1] = float("nan")
+    wm = mx_ref.draw_matrix(rng, 1, N, K)
+    w, y = _mat(wm), torch.full((M + 1, N), 7.0, dtype=TYPES[y_kind], device="cuda")
+    ws = bm.workspace(bm.moe_mx_linear_workspace_bytes(M, N, K))
+    for _ in range(2):
+        bm.moe_mx_linear(x, w, y[:M], ws)
+    rows = [0, 127, 128, 256, M - 1]
+    alone = [torch.empty((1, N), dtype=TYPES[y_kind], device="cuda") for _ in rows]
+    for r, one in zip(rows, alone):
+        bm.moe_mx_linear(x[r:r + 1], w, one, ws)
+    torch.cuda.synchronize()
+    assert bm.moe_check_status(ws) == 0
+    assert torch.equal(torch.cat(alone), y[rows]) and torch.isnan(y[M - 2]).all() and (y[M] == 7).all()
+    keep = np.delete(np.arange(M), M - 2)
+    got, xv = y.double().cpu().numpy()[keep], mx_ref.rounded(x.double().cpu().numpy()[keep])
+    assert _product_error(got, xv, mx_ref.weights(wm)[0], K, y_kind == "bf16") <= 0
+
+
 def test_a_row_does_not_depend_on_its_batch():
     """The same bits for a token alone, among few and among many."""
     rng = np.random.default_rng(6)
