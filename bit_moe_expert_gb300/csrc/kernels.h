@@ -220,7 +220,7 @@ struct MxScatter {
   int T, k, max_blocks, shared_rows;  // shared_rows = 0: no shared expert
 };
 // Y[t] = bf16(sum_j w[t][j] ypart[inv_perm[t k + j]] + ypart[T k + t]), the second term with has_shared.
-cudaError_t launch_mx_combine(const float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
+cudaError_t launch_mx_combine(float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
                               bool has_shared, uint16_t* Y, uint32_t* status, int num_sms, cudaStream_t stream);
 cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint8_t* q, uint8_t* sp,
                               cudaStream_t stream, bool pdl);
