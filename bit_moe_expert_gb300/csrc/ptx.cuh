@@ -531,6 +531,17 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&f)[8]) {
       : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
+// Approximate, subnormals as zeros; 0 for a finite a over a b from 2^126 on.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float div_approx(float a, float b) {
+  float r;
+  asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // The larger value; NaN if either is NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
