@@ -207,6 +207,40 @@ def test_large_products(M, N, K, y_kind):
     assert _product_error(got, xv, mx_ref.weights(wm)[0], K, y_kind == "bf16") <= 0
 
 
+@pytest.mark.parametrize("K", [32, 1312])
+def test_offsets_past_32_bits(K):
+    """Elements past 2^31 of Y (one CTA a tile, and pairs): the bits of the same rows alone."""
+    M, N = 70001, 32776
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(M, K, device="cuda", generator=gen, dtype=torch.float32).to(torch.bfloat16)
+    w = _quantise(torch.randn(N, K, device="cuda", generator=gen, dtype=torch.float32))
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = bm.workspace(bm.moe_mx_linear_workspace_bytes(M, N, K))
+    bm.moe_mx_linear(x, w, y, ws)
+    some = torch.cat([torch.arange(0, 130), torch.arange(65500, 65630), torch.arange(M - 130, M)])
+    alone = torch.empty((len(some), N), dtype=torch.bfloat16, device="cuda")
+    bm.moe_mx_linear(x[some].contiguous(), w, alone, ws)
+    torch.cuda.synchronize()
+    assert bm.moe_check_status(ws) == 0 and torch.equal(alone, y[some])
+
+
+def test_quantise_offsets_past_32_bits():
+    rows, K = 70001, 65536
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+    x.view(-1)[:] = 1.0
+    x[-200:] = torch.randn(200, K, device="cuda").to(torch.bfloat16)
+    m, part = _quantise(x), _quantise(x[rows // 128 * 128 - 128:])  # from a piece's first row on
+    n = part.q.shape[1]
+    assert n >= 100 and torch.equal(m.q[0, -n:], part.q[0])
+    assert torch.equal(m.sp.view(-1)[-part.sp.numel():], part.sp.view(-1))
+    back = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+    bm.moe_mx_dequant(m, back)
+    some = torch.empty((n, K), dtype=torch.bfloat16, device="cuda")
+    bm.moe_mx_dequant(part, some)
+    torch.cuda.synchronize()
+    assert torch.equal(back[-n:], some) and (back[0] == 1).all()
+
+
 def test_a_row_does_not_depend_on_its_batch():
     """The same bits for a token alone, among few and among many."""
     rng = np.random.default_rng(6)
