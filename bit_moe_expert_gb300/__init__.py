@@ -1,9 +1,10 @@
 """GB300-native 4-bit groupwise-affine mixture-of-experts layer (sm_103a).
 
-Thin Python binding over the C ABI in include/moe.h.  The functions carry the C
-names and only marshal arguments (torch tensors -> device pointers, the current
-CUDA stream); every step of the layer runs in the CUDA library.  There is no
-fallback: if the library is missing or a call fails, an exception is raised.
+Thin Python binding over the C ABI in include/moe.h and include/moe_mx.h (MXFP4
+weights).  The functions carry the C names and only marshal arguments (torch
+tensors -> device pointers, the current CUDA stream); every step of the layer runs
+in the CUDA library.  There is no fallback: if the library is missing or a call
+fails, an exception is raised.
 """
 from __future__ import annotations
 
