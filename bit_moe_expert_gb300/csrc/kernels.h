@@ -218,6 +218,7 @@ struct MxScatter {
   const int32_t* num_blocks;
   uint32_t* status;
   int T, k, max_blocks, shared_rows;  // shared_rows = 0: no shared expert
+  bool x_ready;                       // X was complete before the kernel before this one
 };
 // Y[t] = bf16(sum_j w[t][j] ypart[inv_perm[t k + j]] + ypart[T k + t]), the second term with has_shared.
 cudaError_t launch_mx_combine(float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,

@@ -185,7 +185,7 @@ void set_scales(A* a, const moe_mx_experts* routed, const moe_mx_experts* shared
 
 moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_experts* routed,
                    const moe_mx_experts* shared, int I_shared, const moe_routing* r, uint16_t* Y, void* ws,
-                   moe_stream stream) {
+                   bool after_routing, moe_stream stream) {
   if (T == 0) return MOE_OK;
   const int E = routed->n_experts;
   const ExpertLayout L = expert_layout(T, d, I, E, k, I_shared, r->block_rows);
@@ -267,7 +267,8 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
     maps.x_s = maps.h_s = maps.x_r;
   if (!ok) return MOE_ERR_CUDA;
 
-  const MxScatter sc{r->inv_perm, r->block_map, r->num_blocks, a.status, T, k, L.max_blocks, shared ? L.bn_s : 0};
+  const MxScatter sc{r->inv_perm, r->block_map, r->num_blocks, a.status, T, k, L.max_blocks,
+                     shared ? L.bn_s : 0, after_routing};
   if (launch_mx_scatter(X, d, sc, w + L.q_x, w + L.sp_x, st, pdl_enabled()) != cudaSuccess ||
       launch_mx_experts(a, maps, st) != cudaSuccess)
     return MOE_ERR_CUDA;
@@ -368,7 +369,7 @@ moe_status moe_mx_forward(const uint16_t* X, int T, int d, int I, int k, const m
   if (!ws_ok(ws, ws_bytes,
              moe_mx_forward_workspace_bytes(T, d, I, routed->n_experts, k, I_shared, r->block_rows)))
     return MOE_ERR_WORKSPACE;
-  return forward(X, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
+  return forward(X, T, d, I, k, routed, shared, I_shared, r, Y, ws, false, stream);
 }
 
 size_t moe_mx_layer_workspace_bytes(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
@@ -389,7 +390,7 @@ moe_status moe_mx_layer(const float* logits, const moe_scoring* scoring, const u
   // one header for both, and after it the same room: the products start when the routing has completed
   st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, stream);
   if (st != MOE_OK) return st;
-  return forward(X, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
+  return forward(X, T, d, I, k, routed, shared, I_shared, r, Y, ws, true, stream);
 }
 
 }  // extern "C"
