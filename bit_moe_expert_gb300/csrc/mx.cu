@@ -346,7 +346,7 @@ cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N,
 
 cudaError_t launch_mx_combine(float* ypart, const int32_t* inv_perm, const float* w, int T, int d, int k,
                               bool has_shared, uint16_t* Y, uint32_t* status, int num_sms, cudaStream_t stream) {
-  const int grid = blocks_for(static_cast<size_t>(T) * ((d + 127) / 128), kCombineThreads / 32, num_sms * 32);
+  const int grid = blocks_for(static_cast<size_t>(T) * ((d + 127) / 128), kCombineThreads / 32, num_sms * 16);
   return launch(kKCombine, mx_combine_kernel, grid, kCombineThreads, stream, true, ypart, inv_perm, w, T, d, k,
                 has_shared ? 1 : 0, Y, status);
 }
