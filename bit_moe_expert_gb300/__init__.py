@@ -166,21 +166,25 @@ def _check(fn: str, status: int):
         raise MoeError(fn, status)
 
 
-_raw_stream = None  # (the current stream's raw handle of a device, the current device), found at the first call
+_raw_stream = _raw_device = None  # the current stream's raw handle of a device, and the current device; from the first call
+
+
+def _find_stream_calls() -> None:
+    global _raw_stream, _raw_device
+    import torch
+    torch.cuda.current_device()  # initialises CUDA, which the calls below take for granted
+    # the handle without building a Stream object (~0.2 against ~3 us)
+    _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
-    global _raw_stream
     if _raw_stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        torch.cuda.current_device()  # initialises CUDA, which the call behind it takes for granted
-        # the handle without building a Stream object (~0.2 against ~3 us)
-        _raw_stream = (raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream),
-                       getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
-    return _raw_stream[0](_raw_stream[1]())
+        _find_stream_calls()
+    return _raw_stream(_raw_device())
 
 
 def _ptr(t) -> int:
@@ -267,18 +271,22 @@ class Routing:
                        block_map=torch.empty((mb, 3), **i32), num_blocks=torch.zeros(1, **i32),
                        block_rows=block_rows)
 
-    def _c(self) -> _Routing:
+    def _cached(self):
+        """The buffers, the C struct and a reference to it."""
         c = self.__dict__.get("_cc")
         if (c is None or c[0] is not self.ids or c[1] is not self.w or c[2] is not self.counts
                 or c[3] is not self.offsets or c[4] is not self.perm or c[5] is not self.inv_perm
                 or c[6] is not self.block_map or c[7] is not self.num_blocks):
             bufs = (self.ids, self.w, self.counts, self.offsets, self.perm, self.inv_perm, self.block_map,
                     self.num_blocks)
-            c = bufs + (_Routing(*(_ptr(b) for b in bufs), self.block_rows),)
+            st = _Routing(*(_ptr(b) for b in bufs), self.block_rows)
+            c = bufs + (st, C.byref(st))
             self.__dict__["_cc"] = c
-        st = c[8]
-        st.block_rows = self.block_rows
-        return st
+        c[8].block_rows = self.block_rows
+        return c
+
+    def _c(self) -> _Routing:
+        return self._cached()[8]
 
 
 def workspace(nbytes: int, device="cuda"):
@@ -498,7 +506,9 @@ def _code(t) -> int:
 
 def _tensor(name: str, t, codes, shape=None) -> int:
     """The type code of t, a contiguous CUDA tensor of one of the types and, where given, of the shape."""
-    c = _code(t)
+    c = _dtype_codes.get(t.dtype)
+    if c is None:
+        c = _code(t)
     if c not in codes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(n for n, v in _DTYPE_NAMES.items() if v in codes)}")
     if not t.is_cuda:
@@ -520,7 +530,9 @@ def _rows(name: str, t):
     if len(shape) != 2 or not t.is_cuda:
         raise ValueError(f"{name}: expected a 2-D CUDA tensor, got {tuple(shape)} on {t.device}")
     rows, cols = shape
-    code = _code(t)
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        code = _code(t)
     if code not in _FLOATS:
         raise ValueError(f"{name}: {t.dtype}, expected bfloat16, int16 (bf16 bits), float16 or float32")
     ld, step = t.stride()
@@ -556,26 +568,25 @@ class MxMat:
         E, N, half = self.q.shape
         return int(E), int(N), 2 * int(half)
 
-    def _cached(self):
-        c = self.__dict__.get("_cc")
-        if c is None or c[0] is not self.q or c[1] is not self.sp:
-            _tensor("q", self.q, (_U8,))
-            if self.q.dim() != 3:
-                raise ValueError(f"q: shape {tuple(self.q.shape)}, expected [E][N][K/2]")
-            E, N, K = self.shape
-            _tensor("sp", self.sp, (_U8,), (E, -(-N // 128), -(-K // 128), 512))
-            st = _MxMat(_ptr(self.q), _ptr(self.sp))
-            c = (self.q, self.sp, st, (E, N, K), C.byref(st))
-            self.__dict__["_cc"] = c
-        return c
-
-    def _c(self) -> _MxMat:
-        return self._cached()[2]
+    _known = (0, 0, None)  # q, sp, (a reference to the C struct, (E, N, K), the struct)
 
     def _ref_and_shape(self):
-        """A reference to the C struct, and (E, N, K)."""
-        c = self._cached()
-        return c[4], c[3]
+        """A reference to the C struct, (E, N, K), and the struct: rebuilt only when a tensor was replaced."""
+        q, sp, known = self._known
+        if q is not self.q or sp is not self.sp:
+            q, sp = self.q, self.sp
+            _tensor("q", q, (_U8,))
+            if q.dim() != 3:
+                raise ValueError(f"q: shape {tuple(q.shape)}, expected [E][N][K/2]")
+            E, N, K = self.shape
+            _tensor("sp", sp, (_U8,), (E, -(-N // 128), -(-K // 128), 512))
+            st = _MxMat(_ptr(q), _ptr(sp))
+            known = (C.byref(st), (E, N, K), st)
+            self._known = (q, sp, known)
+        return known
+
+    def _c(self) -> _MxMat:
+        return self._ref_and_shape()[2]
 
 
 @dataclasses.dataclass
@@ -604,9 +615,11 @@ def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Rou
     """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
     _tensor("logits", logits, _ONLY_FP32)
     T, E = logits.shape
-    r = out._c()
-    _check("moe_route_scored", lib().moe_route_scored(logits.data_ptr(), scoring._ref(E), T, E, k, block_rows, C.byref(r),
-                                                      ws.data_ptr(), ws.numel(), _stream(stream)))
+    r = out._cached()[9]
+    status = lib().moe_route_scored(logits.data_ptr(), scoring._ref(E), T, E, k, block_rows, r, ws.data_ptr(),
+                                    ws.numel(), _stream(stream))
+    if status:
+        _check("moe_route_scored", status)
     out.block_rows = block_rows
 
 
@@ -615,29 +628,35 @@ def moe_mx_prepack_scales(scale, sp, stream=None) -> None:
     _tensor("scale", scale, (_U8,))
     E, N, G = scale.shape
     _tensor("sp", sp, (_U8,), (E, -(-N // 128), -(-G // 4), 512))
-    _check("moe_mx_prepack_scales", lib().moe_mx_prepack_scales(_ptr(scale), E, N, 32 * G, _ptr(sp), _stream(stream)))
+    status = lib().moe_mx_prepack_scales(_ptr(scale), E, N, 32 * G, _ptr(sp), _stream(stream))
+    if status:
+        _check("moe_mx_prepack_scales", status)
 
 
 def moe_mx_quantize(X, out: MxMat, stream=None) -> None:
     """X [rows][K] (bf16, fp16 or fp32; rows may be strided) -> out, an MxMat of (1, rows, K)."""
     rows, K, ld, code = _rows("X", X)
-    m, shape = out._ref_and_shape()
+    m, shape, _ = out._ref_and_shape()
     if shape != (1, rows, K):
         raise ValueError(f"out: {shape}, expected (1, {rows}, {K})")
-    _check("moe_mx_quantize", lib().moe_mx_quantize(X.data_ptr(), code, rows, K, ld, m, _stream(stream)))
+    status = lib().moe_mx_quantize(X.data_ptr(), code, rows, K, ld, m, _stream(stream))
+    if status:
+        _check("moe_mx_quantize", status)
 
 
 def moe_mx_dequant(m: MxMat, W, stream=None) -> None:
     """W (bf16 or fp32, E*N*K elements) = the values of m."""
-    ref, (E, N, K) = m._ref_and_shape()
+    ref, (E, N, K), _ = m._ref_and_shape()
     code = _tensor("W", W, _FLOATS)
     if W.numel() != E * N * K:
         raise ValueError(f"W: {W.numel()} elements, expected {E * N * K}")
-    _check("moe_mx_dequant", lib().moe_mx_dequant(ref, E, N, K, code, W.data_ptr(), _stream(stream)))
+    status = lib().moe_mx_dequant(ref, E, N, K, code, W.data_ptr(), _stream(stream))
+    if status:
+        _check("moe_mx_dequant", status)
 
 
 def _one(name: str, W: MxMat):
-    ref, (E, N, K) = W._ref_and_shape()
+    ref, (E, N, K), _ = W._ref_and_shape()
     if E != 1:
         raise ValueError(f"{name}: {E} matrices, expected one")
     return ref, N, K
@@ -650,8 +669,9 @@ def moe_mx_matmul(A: MxMat, W: MxMat, Y, ws, stream=None) -> None:
     if K != Kw:
         raise ValueError(f"A has {K} columns, W {Kw}")
     y = _tensor("Y", Y, _FLOATS, (M, N))
-    _check("moe_mx_matmul", lib().moe_mx_matmul(a, M, w, N, K, Y.data_ptr(), y, ws.data_ptr(), ws.numel(),
-                                                _stream(stream)))
+    status = lib().moe_mx_matmul(a, M, w, N, K, Y.data_ptr(), y, ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        _check("moe_mx_matmul", status)
 
 
 def moe_mx_linear_workspace_bytes(T: int, N: int, K: int) -> int:
@@ -665,8 +685,10 @@ def moe_mx_linear(X, W: MxMat, Y, ws, stream=None) -> None:
     if K != Kw:
         raise ValueError(f"X has {K} columns, W {Kw}")
     y = _tensor("Y", Y, _FLOATS, (T, N))
-    _check("moe_mx_linear", lib().moe_mx_linear(X.data_ptr(), code, T, K, ld, w, N, Y.data_ptr(), y, ws.data_ptr(),
-                                                ws.numel(), _stream(stream)))
+    status = lib().moe_mx_linear(X.data_ptr(), code, T, K, ld, w, N, Y.data_ptr(), y, ws.data_ptr(), ws.numel(),
+                                 _stream(stream))
+    if status:
+        _check("moe_mx_linear", status)
 
 
 def moe_mx_forward_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
@@ -692,9 +714,11 @@ def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
 def moe_mx_forward(X, routed: MxExperts, shared: Optional[MxExperts], routing: Routing, Y, ws, stream=None) -> None:
     """The expert layer on MXFP4 weights, for a routing of moe_route or moe_route_scored."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
-    rr = routing._c()
-    _check("moe_mx_forward", lib().moe_mx_forward(X.data_ptr(), T, d, I, int(routing.ids.shape[1]), re, se, I_sh,
-                                                  C.byref(rr), Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    rr = routing._cached()[9]
+    status = lib().moe_mx_forward(X.data_ptr(), T, d, I, int(routing.ids.shape[1]), re, se, I_sh, rr,
+                                  Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        _check("moe_mx_forward", status)
 
 
 def moe_mx_layer_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
@@ -706,10 +730,11 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
     """moe_route_scored + moe_mx_forward in one call."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
     _tensor("logits", logits, _ONLY_FP32, (T, E))
-    r = out._c()
-    _check("moe_mx_layer", lib().moe_mx_layer(logits.data_ptr(), scoring._ref(E), X.data_ptr(), T, d, I, k, block_rows, re,
-                                              se, I_sh, C.byref(r), Y.data_ptr(), ws.data_ptr(), ws.numel(),
-                                              _stream(stream)))
+    r = out._cached()[9]
+    status = lib().moe_mx_layer(logits.data_ptr(), scoring._ref(E), X.data_ptr(), T, d, I, k, block_rows, re, se, I_sh,
+                                r, Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        _check("moe_mx_layer", status)
     out.block_rows = block_rows
 
 
