@@ -729,6 +729,11 @@ __global__ void __launch_bounds__(PairVariant::kThreads, 1)
           ok = false;
         }
       }
+      if (!ok) {  // what counts a copy's bytes is rank 0's: wait as long as no copy takes (a millisecond)
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
       if (weights) pdl_wait();
     }
     __syncwarp();
