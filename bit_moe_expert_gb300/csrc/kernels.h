@@ -229,6 +229,8 @@ cudaError_t launch_mx_scatter(const uint16_t* X, int d, const MxScatter& s, uint
 constexpr int kMxBM = 128;      // rows of the MMA's M operand
 constexpr int kMxStageK = 256;  // K of a pipeline stage: one 128-byte line of codes a row
 constexpr int kMxMaxBN = 128;   // tokens of an expert tile at most
+constexpr int kMxMaxCols = 1 << 20;        // columns of a matrix; of an expert's matrices also rows
+constexpr long long kMxMaxItems = 1 << 30;  // items (tiles times M tiles) of an expert product: 32-bit indexes
 
 struct MxLinearArgs {
   const uint8_t *sp_w, *sp_x;  // packed scales of the weights and of the tokens

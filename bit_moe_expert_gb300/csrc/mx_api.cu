@@ -9,7 +9,6 @@
 namespace bm {
 namespace {
 
-constexpr int kMaxK_mx = 1 << 20;  // columns of a matrix
 constexpr int kMaxRows = 1 << 30;  // rows (row indexes and TMA coordinates are 32-bit)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -19,7 +18,7 @@ bool ws_ok(const void* ws, size_t have, size_t need) {
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int round16(int x) { return (x + 15) & ~15; }
 
-bool size_ok(int N, int K) { return N >= 1 && K >= kMxBlock && K % kMxBlock == 0 && K <= kMaxK_mx; }
+bool size_ok(int N, int K) { return N >= 1 && K >= kMxBlock && K % kMxBlock == 0 && K <= kMxMaxCols; }
 bool mat_ok(const moe_mx_mat& m) { return m.q && m.sp && aligned16(m.q) && aligned16(m.sp); }
 bool experts_ok(const moe_mx_experts* ex) {
   return ex && mat_ok(ex->gate) && mat_ok(ex->up) && mat_ok(ex->down) && ex->n_experts >= 1;
@@ -160,7 +159,7 @@ bool sizes_valid(int T, int d, int I, int E, int k, int I_shared, int block_rows
 
 moe_status check_experts(const uint16_t* X, int T, int d, int I, int k, const moe_mx_experts* routed,
                          const moe_mx_experts* shared, int I_shared, const uint16_t* Y) {
-  if (T < 0 || k < 1 || !size_ok(1, d) || !size_ok(1, I) || I_shared < 0 || I_shared % kMxBlock || I_shared > kMaxK_mx)
+  if (T < 0 || k < 1 || !size_ok(1, d) || !size_ok(1, I) || I_shared < 0 || I_shared % kMxBlock || I_shared > kMxMaxCols)
     return MOE_ERR_INVALID_ARG;
   if ((shared != nullptr) != (I_shared > 0)) return MOE_ERR_INVALID_ARG;
   if (!experts_ok(routed) || (shared && (!experts_ok(shared) || shared->n_experts != 1))) return MOE_ERR_INVALID_ARG;
@@ -171,6 +170,17 @@ moe_status check_experts(const uint16_t* X, int T, int d, int I, int k, const mo
     return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!X || !Y || !aligned16(X) || !aligned16(Y))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
+}
+
+// Whether the products' items can be counted; everything else has been checked.
+bool items_ok(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
+  auto m_tiles = [](int a, int b) { return static_cast<long long>((a > b ? a : b) + kMxBM - 1) / kMxBM; };
+  long long items = moe_route_max_blocks(T, E, k, block_rows) * m_tiles(d, I);
+  if (I_shared > 0) {
+    const int rows = shared_tile_rows(T < 1 ? 1 : T, block_rows);
+    items += (T + rows - 1) / rows * m_tiles(d, I_shared);
+  }
+  return items <= kMxMaxItems;
 }
 
 template <typename A>
@@ -365,6 +375,7 @@ moe_status moe_mx_forward(const uint16_t* X, int T, int d, int I, int k, const m
   if (st != MOE_OK) return st;
   if (!r) return MOE_ERR_INVALID_ARG;
   if (r->block_rows < 1 || r->block_rows > kMaxBlockRows) return MOE_ERR_UNSUPPORTED;
+  if (!items_ok(T, d, I, routed->n_experts, k, I_shared, r->block_rows)) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!r->w || !r->perm || !r->inv_perm || !r->block_map || !r->num_blocks)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes,
              moe_mx_forward_workspace_bytes(T, d, I, routed->n_experts, k, I_shared, r->block_rows)))
@@ -386,6 +397,7 @@ moe_status moe_mx_layer(const float* logits, const moe_scoring* scoring, const u
   const int E = routed->n_experts;
   st = check_scored(logits, scoring, T, E, k, block_rows, r);
   if (st != MOE_OK) return st;
+  if (!items_ok(T, d, I, E, k, I_shared, block_rows)) return MOE_ERR_UNSUPPORTED;
   if (!ws_ok(ws, ws_bytes, moe_mx_layer_workspace_bytes(T, d, I, E, k, I_shared, block_rows))) return MOE_ERR_WORKSPACE;
   // one header for both, and after it the same room: the products start when the routing has completed
   st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, stream);

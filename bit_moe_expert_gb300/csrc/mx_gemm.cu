@@ -113,9 +113,12 @@ struct Sched {
 
 // What an item's id stands for, as every role needs it.
 struct Entry {
-  int e, row0, rows;  // expert (-1: malformed), first row, rows
-  int at;             // mt + 2^15 slot, or -1 - (mt + 2^15 tile) for the shared expert
+  int e, row0;    // expert (-1: malformed) and first row; dense: 0 and the M tile
+  int slot;       // entry of the block map, the shared expert's tile of tokens, or the dense product's N tile
+  uint32_t what;  // experts: M tile + 2^16 rows + 2^31 for the shared expert
 };
+constexpr uint32_t kEntryShared = 1u << 31;
+static_assert(kMxMaxCols / kMxBM <= 1 << 16 && kMxMaxBN < 1 << 15, "an Entry's M tile and rows");
 template <int kMode>
 struct Args {
   using type = MxExpertArgs;
@@ -140,15 +143,15 @@ __device__ __forceinline__ Sched make_sched(const MxLinearArgs& a, const Plan& p
 }
 
 __device__ __forceinline__ Entry make_entry(const MxLinearArgs&, const Sched& s, int it) {
-  return Entry{0, 0, it / s.mt_r, it % s.mt_r};  // rows: the N tile
+  return Entry{0, it % s.mt_r, it / s.mt_r, 0};
 }
 
 __device__ __forceinline__ Item get_item(const MxLinearArgs& a, const MxLinearMaps& maps, const Plan& p,
                                          const Entry& en, bool) {
   Item m{};
   const int pieces = pieces_of(a.K);
-  m.mt = en.at;
-  const int nt = en.rows;
+  m.mt = en.row0;
+  const int nt = en.slot;
   m.m0 = &maps.w;
   m.n = &maps.x;
   m.row_m = m.mt * kMxBM;
@@ -183,21 +186,22 @@ __device__ __forceinline__ Sched make_sched(const MxExpertArgs& a, const Plan&, 
 __device__ __forceinline__ Entry make_entry(const MxExpertArgs& a, const Sched& s, int it) {
   Entry en;
   if (it < s.n_routed) {
-    const int blk = it / s.mt_r;
-    const volatile int32_t* b = a.block_map + 3 * static_cast<size_t>(blk);
+    en.slot = it / s.mt_r;
+    const volatile int32_t* b = a.block_map + 3 * static_cast<size_t>(en.slot);
     en.e = b[0];
     en.row0 = b[1];
-    en.rows = b[2];
-    en.at = (it - blk * s.mt_r) + (blk << 15);
-    const bool ok = en.e >= 0 && en.e < a.E && en.rows >= 1 && en.rows <= a.bn_r && en.row0 >= 0 &&
-                    en.row0 + en.rows <= a.T * a.k;
+    const int rows = b[2];
+    const bool ok = en.e >= 0 && en.e < a.E && rows >= 1 && rows <= a.bn_r && en.row0 >= 0 &&
+                    en.row0 + rows <= a.T * a.k;
     if (!ok) en.e = -1;
+    en.what = static_cast<uint32_t>(it - en.slot * s.mt_r) | static_cast<uint32_t>(rows) << 16;
   } else {
-    const int j = it - s.n_routed, tile = j / s.mt_s;
+    const int j = it - s.n_routed;
+    en.slot = j / s.mt_s;
     en.e = 0;
-    en.row0 = tile * a.bn_s;
-    en.rows = min(a.bn_s, a.T - en.row0);
-    en.at = -1 - ((j - tile * s.mt_s) + (tile << 15));
+    en.row0 = en.slot * a.bn_s;
+    en.what = kEntryShared | static_cast<uint32_t>(j - en.slot * s.mt_s) |
+              static_cast<uint32_t>(min(a.bn_s, a.T - en.row0)) << 16;
   }
   return en;
 }
@@ -209,11 +213,10 @@ __device__ __forceinline__ Item get_item(const MxExpertArgs& a, const MxExpertMa
   if (!m.ok) return m;
   const int e = en.e;
   m.row0 = en.row0;
-  m.rows = en.rows;
-  m.shared = en.at < 0;
-  const int at = m.shared ? -1 - en.at : en.at;
-  m.mt = at & 0x7FFF;
-  m.slot = at >> 15;
+  m.rows = static_cast<int>(en.what >> 16 & 0x7FFFu);
+  m.shared = (en.what & kEntryShared) != 0;
+  m.mt = static_cast<int>(en.what & 0xFFFFu);
+  m.slot = en.slot;
   const int I = m.shared ? a.I_shared : a.I;
   const int N = gate_up ? I : a.d;
   m.K = gate_up ? a.d : I;

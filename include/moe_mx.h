@@ -99,7 +99,9 @@ size_t moe_mx_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_s
  * with MX() the rounding of moe_mx_quantize; the products, SwiGLU and the sums
  * over experts (in slot order, the shared expert last) are in fp32, the second
  * MX() takes the fp32 SwiGLU, and Y is rounded to bf16 once.
- * Arguments as for moe_forward; d, I and I_shared multiples of 32. */
+ * Arguments as for moe_forward; d, I and I_shared multiples of 32.
+ * MOE_ERR_UNSUPPORTED also where moe_route_max_blocks times ceil(max(d, I) /
+ * 128), plus the shared expert's tiles likewise, is above 2^30. */
 moe_status moe_mx_forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_experts* routed,
                           const moe_mx_experts* shared, int I_shared, const moe_routing* r, uint16_t* Y, void* ws,
                           size_t ws_bytes, moe_stream stream);

@@ -370,3 +370,31 @@ def test_a_malformed_block_map_is_reported():
     bm.moe_mx_forward(layer.x, layer.routed, None, r, y, ws)
     torch.cuda.synchronize()
     assert bm.STATUS_NAMES[bm.moe_check_status(ws)] == "MOE_ERR_INVALID_ARG"
+
+
+@pytest.mark.parametrize("T,E,k,block_rows", [
+    (131080, 256, 8, 16),     # more than 2^16 tiles of the routed experts
+    (6291560, 2, 1, 96),      # and of the shared expert's tokens
+])
+def test_layer_of_more_tiles_than_16_bits_count(T, E, k, block_rows):
+    """The bits of the same tokens in a smaller batch, those of the last tiles among them."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    d, I, I_shared = 64, 32, 32
+    x = torch.randn(T, d, device="cuda", generator=gen, dtype=torch.float32).to(torch.bfloat16)
+    logits = torch.randn(T, E, device="cuda", generator=gen, dtype=torch.float32)
+    layer = _Layer(T, 1, d, I, I_shared, E)
+    sc = bm.Scoring("sigmoid")
+
+    def run(x, logits, block_rows):
+        r = bm.Routing.empty(x.shape[0], E, k, block_rows)
+        ws = bm.workspace(bm.moe_mx_layer_workspace_bytes(x.shape[0], d, I, E, k, I_shared, block_rows))
+        y = torch.full(x.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+        bm.moe_mx_layer(logits, sc, x, layer.routed, layer.shared, k, block_rows, r, y, ws)
+        torch.cuda.synchronize()
+        assert bm.moe_check_status(ws) == 0
+        return y, r
+
+    y, r = run(x, logits, block_rows)
+    assert int(r.num_blocks.item()) > 1 << 16 and torch.isfinite(y).all()
+    some = torch.cat([torch.arange(1000), torch.arange(T - 20000, T)]).cuda()
+    assert torch.equal(y[some], run(x[some], logits[some], 128)[0])

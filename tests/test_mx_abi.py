@@ -123,6 +123,26 @@ def test_expert_calls_refuse(L):
     assert bm.moe_mx_forward_workspace_bytes(8, 256, 90, 16, 2, 0, 16) == 0
 
 
+@pytest.mark.parametrize("layer", [False, True])
+def test_expert_calls_refuse_more_items_than_are_counted(L, layer):
+    """Tiles times 128-row tiles of an expert's matrices up to 2^30, of the routed experts and of the shared one."""
+    m = bm._MxMat(FAKE, FAKE)
+
+    def call(T, d, k, E, I_sh, br):
+        ex, sh = bm._MxExperts(m, m, m, E), bm._MxExperts(m, m, m, 1)
+        r = bm._Routing(*([FAKE] * 8), br)
+        a = (C.byref(ex), C.byref(sh) if I_sh else None, I_sh, C.byref(r), FAKE, FAKE, 0, None)  # no workspace
+        if layer:
+            return L.moe_mx_layer(FAKE, C.byref(_scoring()), FAKE, T, d, 32, k, br, *a)
+        return L.moe_mx_forward(FAKE, T, d, 32, k, *a)
+
+    # 2^20 columns are 2^13 M tiles; T k + E = 2^17 tiles of them are exactly 2^30
+    assert call(T=(1 << 17) - 4, d=1 << 20, k=1, E=4, I_sh=0, br=1) == WORKSPACE
+    assert call(T=(1 << 17) - 3, d=1 << 20, k=1, E=4, I_sh=0, br=1) == UNSUPPORTED
+    assert call(T=(1 << 17) - 4, d=1 << 20, k=1, E=4, I_sh=32, br=1) == UNSUPPORTED  # the shared expert's tiles
+    assert call(T=8193, d=256, k=8, E=256, I_sh=32, br=1) == WORKSPACE               # past 2^16 tiles is fine
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError, match="score"):
