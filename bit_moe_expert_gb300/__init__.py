@@ -634,7 +634,9 @@ def moe_mx_prepack_scales(scale, sp, stream=None) -> None:
 
 
 def moe_mx_quantize(X, out: MxMat, stream=None) -> None:
-    """X [rows][K] (bf16, fp16 or fp32; rows may be strided) -> out, an MxMat of (1, rows, K)."""
+    """X [rows][K] (bf16, fp16 or fp32; rows may be strided) -> out, an MxMat of (1, rows, K).
+
+    A product that takes `out` as its weights may be the next call on the stream."""
     rows, K, ld, code = _rows("X", X)
     m, shape, _ = out._ref_and_shape()
     if shape != (1, rows, K):

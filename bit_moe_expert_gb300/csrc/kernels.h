@@ -202,9 +202,9 @@ inline size_t mx_pieces(long long rows, int K) {
 }
 
 cudaError_t launch_mx_prepack(const uint8_t* scale, int E, int N, int K, uint8_t* sp, cudaStream_t stream);
-// type: 0 bf16, 1 fp16, 2 fp32
+// type: 0 bf16, 1 fp16, 2 fp32; early: the next kernel may start beside this one (the result is no weights)
 cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, uint8_t* sp,
-                               cudaStream_t stream, bool pdl);
+                               bool early, cudaStream_t stream, bool pdl);
 cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W,
                               cudaStream_t stream, bool pdl);
 

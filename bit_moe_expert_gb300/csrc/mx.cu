@@ -24,6 +24,11 @@ namespace {
 // scales of these four rows are neighbours, so a warp writes (or reads) its
 // scales of 128 columns as one 16-byte word (four 4-byte words cost 7 of 38 us
 // at 8192 x 8192), and consecutive CTAs read along the rows.
+//
+// The products read weights before they wait for the kernel before them, so a
+// kernel whose result may be weights lets no other start before it has completed:
+// the quantisation starts its successor early only inside a linear layer, where
+// its result is the activations (`early`), and the inverse never does.
 constexpr int kQuantThreads = 256;
 constexpr int kUnits = 4;
 struct Patch {
@@ -43,12 +48,12 @@ struct Patch {
 template <int kType>
 __global__ void __launch_bounds__(kQuantThreads)
     mx_quantize_kernel(const void* __restrict__ X, int rows, int K, long long ldx, uint8_t* __restrict__ q,
-                       uint8_t* __restrict__ sp) {
+                       uint8_t* __restrict__ sp, int early) {
   const Patch at(K);
   const int lane = threadIdx.x & 31;
   const int esize = kType == kFp32 ? 4 : 2;
   pdl_wait();
-  pdl_launch_dependents();
+  if (early) pdl_launch_dependents();
   Load8<kType> x[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
@@ -78,7 +83,6 @@ __global__ void __launch_bounds__(kQuantThreads)
   const size_t matrix = static_cast<size_t>(blockIdx.y) * N;
   sp += blockIdx.y * static_cast<size_t>((N + kMxPieceRows - 1) / kMxPieceRows) * pieces * kMxPieceBytes;
   pdl_wait();
-  pdl_launch_dependents();
   if (at.row >= N || at.col >= K) return;
   uint32_t code[kUnits];
   const size_t first = (matrix + at.row) * (K / 8) + at.col / 8;  // in words of eight codes
@@ -330,12 +334,13 @@ cudaError_t launch_mx_prepack(const uint8_t* scale, int E, int N, int K, uint8_t
 }
 
 cudaError_t launch_mx_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, uint8_t* sp,
-                               cudaStream_t stream, bool pdl) {
+                               bool early, cudaStream_t stream, bool pdl) {
   const size_t grid = patches(rows, K);
   if (grid > 0x7FFFFFFFu) return cudaErrorInvalidValue;
   const auto kernel = type == kBf16 ? mx_quantize_kernel<kBf16>
                                     : (type == kFp16 ? mx_quantize_kernel<kFp16> : mx_quantize_kernel<kFp32>);
-  return launch(kKMxQuantize, kernel, dim3(static_cast<unsigned>(grid)), kQuantThreads, stream, pdl, X, rows, K, ldx, q, sp);
+  return launch(kKMxQuantize, kernel, dim3(static_cast<unsigned>(grid)), kQuantThreads, stream, pdl, X, rows, K, ldx, q, sp,
+                early ? 1 : 0);
 }
 
 cudaError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sp, int E, int N, int K, int type, void* W,

@@ -309,7 +309,7 @@ moe_status moe_mx_quantize(const void* X, moe_dtype type, int rows, int K, long 
   if (st != MOE_OK) return st;
   if (!out || !mat_ok(*out)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  return launch_mx_quantize(X, type, rows, K, ldx, out->q, out->sp, reinterpret_cast<cudaStream_t>(stream),
+  return launch_mx_quantize(X, type, rows, K, ldx, out->q, out->sp, false, reinterpret_cast<cudaStream_t>(stream),
                             pdl_enabled()) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
@@ -358,8 +358,9 @@ moe_status moe_mx_linear(const void* X, moe_dtype x_type, int T, int K, long lon
   }
   uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
   const moe_mx_mat xq{w, w + round256(static_cast<size_t>(T) * (K / 2))};
-  st = moe_mx_quantize(X, x_type, T, K, ldx, &xq, stream);
-  if (st != MOE_OK) return st;
+  if (launch_mx_quantize(X, x_type, T, K, ldx, xq.q, xq.sp, true, reinterpret_cast<cudaStream_t>(stream),
+                         pdl_enabled()) != cudaSuccess)
+    return MOE_ERR_CUDA;
   return matmul(xq, T, *W, N, K, Y, y_type, status, stream);
 }
 

@@ -17,7 +17,11 @@
  * caller; nothing allocated; asynchronous on `stream`; capturable; checks on the
  * host before any launch; workspaces zero-filled once, 256-byte aligned, one
  * call in flight per workspace, device-side errors in their status word
- * (moe_check_status).
+ * (moe_check_status).  Products read weights before waiting for the previous
+ * kernel on the stream; after moe_mx_quantize, moe_mx_prepack_scales and
+ * moe_mx_dequant, which let no kernel start before they have completed, they may
+ * follow directly.  Weights that any other kernel wrote are separated as moe.h
+ * says.
  */
 #ifndef BIT_MOE_EXPERT_GB300_MOE_MX_H
 #define BIT_MOE_EXPERT_GB300_MOE_MX_H

@@ -398,3 +398,82 @@ def test_layer_of_more_tiles_than_16_bits_count(T, E, k, block_rows):
     assert int(r.num_blocks.item()) > 1 << 16 and torch.isfinite(y).all()
     some = torch.cat([torch.arange(1000), torch.arange(T - 20000, T)]).cuda()
     assert torch.equal(y[some], run(x[some], logits[some], 128)[0])
+
+
+class _Rewritten:
+    """Two fp32 matrices, written in turn into one MxMat that holds the other's codes when it is overwritten."""
+
+    def __init__(self, N, K, seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.w = [torch.randn(N, K, device="cuda", generator=gen, dtype=torch.float32) * 2.0 ** i for i in (0, 3)]
+        self.m = bm.MxMat.empty(1, N, K)
+
+    def results(self, call, sync):
+        """call()'s clones after each rewriting, with or without a synchronisation between the two."""
+        got = []
+        for i in range(8):
+            bm.moe_mx_quantize(self.w[i % 2], self.m)
+            if sync:
+                torch.cuda.synchronize()
+            got.append(call().clone())
+        torch.cuda.synchronize()
+        return torch.stack(got)
+
+
+@pytest.mark.parametrize("kind", ["linear", "matmul", "pair"])
+def test_a_product_right_after_its_weights(kind):
+    """moe_mx_quantize into weights, then at once the product with them: the results of a synchronised program."""
+    M, N, K = {"linear": (1, 2048, 2048), "matmul": (300, 2048, 2048), "pair": (4096, 4352, 1312)}[kind]
+    w = _Rewritten(N, K, 1)
+    x = torch.randn(M, K, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    a = _quantise(x)
+    ws = bm.workspace(bm.moe_mx_linear_workspace_bytes(M, N, K))
+
+    def call():
+        if kind == "linear":
+            bm.moe_mx_linear(x, w.m, y, ws)
+        else:
+            bm.moe_mx_matmul(a, w.m, y, ws)
+        return y
+
+    want = w.results(call, True)
+    assert not torch.equal(want[0], want[1])
+    assert torch.equal(w.results(call, False), want) and bm.moe_check_status(ws) == 0
+
+
+def test_an_expert_layer_right_after_the_shared_experts_weights():
+    layer = _Layer(8, 1, 512, 96, 128, 8)
+    w = _Rewritten(128, 512, 2)
+    layer.shared.gate = w.m
+    r = bm.Routing.empty(1, 8, 2, 16)
+    bm.moe_route(layer.logits, 2, 16, r, bm.workspace(bm.moe_route_workspace_bytes(1, 8, 2)))
+    ws = bm.workspace(bm.moe_mx_forward_workspace_bytes(1, 512, 96, 8, 2, 128, 16))
+    y = torch.empty((1, 512), dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        bm.moe_mx_forward(layer.x, layer.routed, layer.shared, r, y, ws)
+        return y
+
+    want = w.results(call, True)
+    assert not torch.equal(want[0], want[1]) and torch.equal(w.results(call, False), want)
+
+
+def test_router_logits_right_after_the_routers_weights():
+    """moe_mx_dequant writes bf16 weights of another kernel that reads them early."""
+    E, d = 256, 2048
+    ms = [_quantise(torch.randn(E, d, device="cuda", dtype=torch.float32) * 2.0 ** i) for i in (0, 3)]
+    W = torch.empty((E, d), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(1, d, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    logits = torch.empty((1, E), dtype=torch.float32, device="cuda")
+    got = {}
+    for sync in (True, False):
+        got[sync] = []
+        for i in range(8):
+            bm.moe_mx_dequant(ms[i % 2], W)
+            if sync:
+                torch.cuda.synchronize()
+            bm.moe_router_logits(x, W, logits)
+            got[sync].append(logits.clone())
+    torch.cuda.synchronize()
+    assert not torch.equal(got[True][0], got[True][1]) and torch.equal(torch.stack(got[True]), torch.stack(got[False]))
