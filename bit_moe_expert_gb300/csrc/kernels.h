@@ -306,8 +306,10 @@ struct MxFewArgs {
   uint16_t* Y;               // [T][d] bf16
   uint32_t* arrived;         // [ceil(d / 128)] arrival counters, zero between calls
   uint32_t* status;
-  int T, d, I, k, I_shared, E, max_blocks, bn;  // bn: MMA columns of a tile
+  int T, d, I, k, I_shared, E;
+  int tiles, bn;             // tiles of the routed experts launched (mx_few_tiles), MMA columns of a tile
 };
+int mx_few_tiles(int T, int k, int max_blocks);
 bool mx_few_fits(int T, int d, int I, int I_shared, int k, int max_blocks);
 cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl);
 

@@ -240,7 +240,7 @@ moe_status forward(const uint16_t* X, int T, int d, int I, int k, const moe_mx_e
     a.k = k;
     a.I_shared = I_shared;
     a.E = E;
-    a.max_blocks = L.max_blocks;
+    a.tiles = mx_few_tiles(T, k, L.max_blocks);
     a.bn = round16(T);
     return launch_mx_few_experts(a, maps, st, pdl_enabled()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }

@@ -111,10 +111,12 @@ __device__ __forceinline__ Item get_item(const LinearParams& p) {
   return m;
 }
 
-// Tiles of the experts' rows: the shared expert's first, then the block map's.
+// Tiles of the experts' rows: the shared expert's first, then the block map's, of
+// which a routing has at least one and as many as are launched at most; none of a
+// malformed one.
 __device__ __forceinline__ int routed_tiles(const MxFewArgs& a) {
   const int nb = *reinterpret_cast<const volatile int32_t*>(a.num_blocks);
-  return nb < 0 || nb > a.max_blocks ? 0 : nb;
+  return nb < 1 || nb > a.tiles ? 0 : nb;
 }
 
 template <int kMode>
@@ -137,7 +139,7 @@ __device__ __forceinline__ Item get_item(const ExpertParams& p) {
     i -= mt_s * kMats;
     const int tile = i / (mt_r * kMats);
     i -= tile * (mt_r * kMats);
-    // the entry exists (the grid has at most max_blocks tiles), whether valid or not: one round trip for all of it
+    // the entry exists (the block map has room for all tiles launched), whether valid or not: one round trip for all of it
     const volatile int32_t* b = a.block_map + 3 * tile;
     e = b[0];
     m.row0 = b[1];
@@ -531,6 +533,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         bar_sync_or(kBarWork, kWorkWarps * 32, false);
         if (*last_flag) combine_columns(p.a, m.mt, ww * 32 + lane, slots);
       }
+    } else if constexpr (kMode != kLinear) {  // past the last item
+      if (threadIdx.x == kWorkWarp0 * 32 && routed_tiles(p.a) == 0) record_status(status, MOE_ERR_INVALID_ARG);
     }
   }
 
@@ -583,30 +587,32 @@ cudaError_t launch_mx_few_linear(const MxFewLinearArgs& a, int type, const CUten
   return launch<kLinear, kFp32>(kKMxGemm, p, plan, grid, stream, pdl);
 }
 
+// Tiles of the routed experts at most (every tile holds an assignment).
+int mx_few_tiles(int T, int k, int max_blocks) { return T * k < max_blocks ? T * k : max_blocks; }
+
 namespace {
-// Tiles of the routed experts at most (every tile holds an assignment), and the gate/up product's CTAs.
-int few_tiles(int T, int k, int max_blocks) { return T * k < max_blocks ? T * k : max_blocks; }
-long long few_items(int T, int I, int I_shared, int k, int max_blocks) {
+// The gate/up product's CTAs.
+long long few_items(int I, int I_shared, int tiles) {
   const long long mt = (I + kMxBM - 1) / kMxBM, mt_s = (I_shared + kMxBM - 1) / kMxBM;
-  return 2 * (few_tiles(T, k, max_blocks) * mt + mt_s);
+  return 2 * (tiles * mt + mt_s);
 }
 }  // namespace
 
 bool mx_few_fits(int T, int d, int I, int I_shared, int k, int max_blocks) {
   const int bn = round16(T);
-  return T <= kMxFewT && few_items(T, I, I_shared, k, max_blocks) <= kMxFewItems &&
+  return T <= kMxFewT && few_items(I, I_shared, mx_few_tiles(T, k, max_blocks)) <= kMxFewItems &&
          (d + kMxBM - 1) / kMxBM <= static_cast<int>(sizeof(WsHeader::mx_arrived) / 4) && fits(bn, d) &&
          fits(bn, I > I_shared ? I : I_shared);
 }
 
 cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl) {
   const ExpertParams p{a, maps};
-  const int tiles = few_tiles(a.T, a.k, a.max_blocks), mt_d = (a.d + kMxBM - 1) / kMxBM;
+  const int mt_d = (a.d + kMxBM - 1) / kMxBM;
   const cudaError_t e = launch<kGateUp, kBf16>(kKMxGateUp, p, make_plan(a.bn, a.d),
-                                               static_cast<int>(few_items(a.T, a.I, a.I_shared, a.k, a.max_blocks)), stream, pdl);
+                                               static_cast<int>(few_items(a.I, a.I_shared, a.tiles)), stream, pdl);
   if (e != cudaSuccess) return e;
   const int I = a.I > a.I_shared ? a.I : a.I_shared;
-  return launch<kDown, kBf16>(kKMxDown, p, make_plan(a.bn, I), mt_d * (tiles + (a.I_shared > 0 ? 1 : 0)), stream, pdl);
+  return launch<kDown, kBf16>(kKMxDown, p, make_plan(a.bn, I), mt_d * (a.tiles + (a.I_shared > 0 ? 1 : 0)), stream, pdl);
 }
 
 }  // namespace bm

@@ -169,7 +169,7 @@ __device__ __forceinline__ Item get_item(const MxLinearArgs& a, const MxLinearMa
 __device__ __forceinline__ Sched make_sched(const MxExpertArgs& a, const Plan&, bool gate_up) {
   Sched s{};
   int nb = *reinterpret_cast<const volatile int32_t*>(a.num_blocks);
-  if (nb < 0 || nb > a.max_blocks) {
+  if (nb < 1 || nb > min(a.max_blocks, a.T * a.k)) {  // every tile holds an assignment
     if (threadIdx.x == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
     nb = 0;
   }

@@ -477,3 +477,26 @@ def test_router_logits_right_after_the_routers_weights():
             got[sync].append(logits.clone())
     torch.cuda.synchronize()
     assert not torch.equal(got[True][0], got[True][1]) and torch.equal(torch.stack(got[True]), torch.stack(got[False]))
+
+
+@pytest.mark.parametrize("T,I_shared", [(2, 0), (2, 64), (40, 0), (40, 64)])  # the products for few tokens, and for more
+def test_a_malformed_number_of_tiles_is_reported_and_harms_no_later_call(T, I_shared):
+    E, k, br = 8, 2, 16
+    layer = _Layer(9, T, 256, 96, I_shared, E)
+    sc = bm.Scoring("softmax")
+    want, _ = layer.run(sc, k, br)
+    r = bm.Routing.empty(T, E, k, br)
+    r.block_map.zero_()
+    bm.moe_route_scored(layer.logits, sc, k, br, r, bm.workspace(bm.moe_route_workspace_bytes(T, E, k)))
+    torch.cuda.synchronize()
+    good = int(r.num_blocks.item())
+    most = bm.moe_route_max_blocks(T, E, k, br)
+    ws = bm.workspace(bm.moe_mx_forward_workspace_bytes(T, 256, 96, E, k, I_shared, br))
+    for bad in (0, -1, T * k + 1, most + 1):
+        for n, status in ((bad, "MOE_ERR_INVALID_ARG"), (good, "MOE_OK"), (good, "MOE_OK")):
+            r.num_blocks.fill_(n)
+            y = torch.full((T, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+            bm.moe_mx_forward(layer.x, layer.routed, layer.shared, r, y, ws)
+            torch.cuda.synchronize()
+            assert bm.STATUS_NAMES[bm.moe_check_status(ws)] == status, (bad, n)
+            assert n != good or torch.equal(y, want), (bad, n)
