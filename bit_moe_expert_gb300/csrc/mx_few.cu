@@ -148,7 +148,7 @@ __device__ __forceinline__ Item get_item(const ExpertParams& p) {
     if (!m.some) return m;
     m.N = kGU ? a.I : a.d;
     m.K = kGU ? a.d : a.I;
-    m.ok = e >= 0 && e < a.E && m.rows >= 1 && m.rows <= a.bn && m.row0 >= 0 && m.row0 + m.rows <= a.T * a.k;
+    m.ok = e >= 0 && e < a.E && m.rows >= 1 && m.rows <= a.bn && m.row0 >= 0 && m.row0 <= a.T * a.k - m.rows;
   }
   m.mat = i % kMats;
   m.mt = i / kMats;

@@ -192,7 +192,7 @@ __device__ __forceinline__ Entry make_entry(const MxExpertArgs& a, const Sched& 
     en.row0 = b[1];
     const int rows = b[2];
     const bool ok = en.e >= 0 && en.e < a.E && rows >= 1 && rows <= a.bn_r && en.row0 >= 0 &&
-                    en.row0 + rows <= a.T * a.k;
+                    en.row0 <= a.T * a.k - rows;
     if (!ok) en.e = -1;
     en.what = static_cast<uint32_t>(it - en.slot * s.mt_r) | static_cast<uint32_t>(rows) << 16;
   } else {

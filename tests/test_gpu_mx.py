@@ -500,3 +500,20 @@ def test_a_malformed_number_of_tiles_is_reported_and_harms_no_later_call(T, I_sh
             torch.cuda.synchronize()
             assert bm.STATUS_NAMES[bm.moe_check_status(ws)] == status, (bad, n)
             assert n != good or torch.equal(y, want), (bad, n)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("entry", [[0, 2 ** 31 - 5, 16], [0, -2 ** 31, 1], [0, 0, -2 ** 31], [0, 0, 2 ** 31 - 1],
+                                   [2 ** 31 - 1, 0, 1], [-1, 0, 1]])
+def test_a_tile_at_the_ends_of_32_bits_is_reported(T, entry):
+    """Such an entry of the block map is skipped: sums of its numbers that wrap do not let it pass."""
+    layer = _Layer(4, T, 256, 96, 0, 4)
+    r = bm.Routing.empty(T, 4, 2, 16)
+    bm.moe_route(layer.logits, 2, 16, r, bm.workspace(bm.moe_route_workspace_bytes(T, 4, 2)))
+    torch.cuda.synchronize()
+    r.block_map[1] = torch.tensor(entry, dtype=torch.int32)
+    ws = bm.workspace(bm.moe_mx_forward_workspace_bytes(T, 256, 96, 4, 2, 0, 16))
+    y = torch.empty((T, 256), dtype=torch.bfloat16, device="cuda")
+    bm.moe_mx_forward(layer.x, layer.routed, None, r, y, ws)
+    torch.cuda.synchronize()
+    assert bm.STATUS_NAMES[bm.moe_check_status(ws)] == "MOE_ERR_INVALID_ARG"
