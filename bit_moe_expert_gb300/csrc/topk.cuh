@@ -230,8 +230,14 @@ __device__ __forceinline__ bool warp_scored_topk(const float (&x)[kPL], const fl
     mx = fmaxf(mx, choice[c]);
   }
   if (sc.sigmoid) {
+    // from -80 down 1 / (1 + e^-l) is e^l in fp32, to its smallest subnormal: the approximate quotient is 0 for a
+    // denominator from 2^126 on (l < -87.3)
 #pragma unroll
-    for (int c = 0; c < kPL; ++c) s[c] = __fdividef(1.0f, 1.0f + expf(-choice[c]));  // a masked expert: 1 / inf
+    for (int c = 0; c < kPL; ++c) {
+      const bool low = choice[c] < -80.0f;  // a masked expert: e^-inf = 0
+      const float z = expf(low ? choice[c] : -choice[c]);
+      s[c] = low ? z : __fdividef(1.0f, 1.0f + z);
+    }
   } else {
     mx = topk_key_value(__reduce_max_sync(kAll, topk_key(mx)));
     float sum = 0.0f;
@@ -409,7 +415,11 @@ __device__ __forceinline__ bool warp_scored_topk(const float (&x)[kPL], const fl
   const bool selected = lane < n && rank < k;
   if (!selected) w = 0.0f;
   if (sc.renormalize) {
-    const float sum = warp_sum(w);
+    float sum = warp_sum(w);
+    if (sum < 0x1p-64f) {  // up to where the approximate quotient holds; exact
+      sum *= 0x1p100f;
+      w *= 0x1p100f;
+    }
     w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
   }
   if (selected) publish(rank, static_cast<int>(me.y), w * sc.scale);

@@ -219,6 +219,7 @@ moe_status moe_route(const float* logits, int T, int E, int k, int block_rows, m
  * A logit of -infinity masks its expert: score 0, behind every other expert in
  * the order.  Where masked experts have to be selected (fewer than k others)
  * their weight is 0, and a token with nothing but masked experts has weights 0.
+ * Scores are fp32, subnormal ones included; one below 2^-149 is 0.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 

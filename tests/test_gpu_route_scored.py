@@ -214,3 +214,34 @@ def test_no_tokens_another_stream_and_a_graph():
         g.replay()
     torch.cuda.synchronize()
     _check(out, ids, w, 64, 16)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 300])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("low,high", [(-95, -88), (-90, -78)])
+def test_scores_at_the_end_of_the_range(score, E, renormalize, low, high):
+    """Selected scores down to e^-95: weights keep their shares.  A score is off by two units of its last place (2^-149 for
+    a subnormal one), a sum of k by as much of each, and the rest is as above."""
+    rng = np.random.default_rng(E)
+    k = 4
+    T = 40
+    l = rng.uniform(low, high, (T, E)).astype(np.float32)
+    bias = None
+    if score == "softmax":  # the largest logit is 0; the bias takes the selection to the small ones
+        l[:, 0] = 0.0
+        bias = (1 + np.arange(E) / E).astype(np.float32)
+        bias[0] = -2.0
+    kw = _kw(score, renormalize=renormalize, scale=1.5)
+    ids, w, gap = _reference(l, bias, k, kw)
+    out, ws = _run(l, bias, k, 16, kw)
+    assert bm.moe_check_status(ws) == 0
+    got_ids, got = out.ids.cpu().numpy(), out.w.cpu().numpy().astype(np.float64)
+    np.testing.assert_array_equal(got_ids, ids)
+    s = np.take_along_axis(mx_ref.scores(l, score), ids, 1)
+    unit = 2 * 2.0 ** -149
+    if renormalize:
+        tol = w * (W_RTOL + unit / s + k * unit / s.sum(1, keepdims=True))
+    else:
+        tol = w * W_RTOL + (1.5 + 1) * unit
+    assert (np.abs(got - w) <= tol).all(), np.max(np.abs(got - w) / tol)
