@@ -272,21 +272,24 @@ class Routing:
                        block_rows=block_rows)
 
     def _cached(self):
-        """The buffers, the C struct and a reference to it."""
-        c = self.__dict__.get("_cc")
-        if (c is None or c[0] is not self.ids or c[1] is not self.w or c[2] is not self.counts
-                or c[3] is not self.offsets or c[4] is not self.perm or c[5] is not self.inv_perm
-                or c[6] is not self.block_map or c[7] is not self.num_blocks):
-            bufs = (self.ids, self.w, self.counts, self.offsets, self.perm, self.inv_perm, self.block_map,
-                    self.num_blocks)
-            st = _Routing(*(_ptr(b) for b in bufs), self.block_rows)
-            c = bufs + (st, C.byref(st))
-            self.__dict__["_cc"] = c
-        c[8].block_rows = self.block_rows
+        """The buffers' addresses, the C struct and a reference to it: rebuilt where an address changed."""
+        c = self._known
+        try:
+            at = [self.ids.data_ptr(), self.w.data_ptr(), self.counts.data_ptr(), self.offsets.data_ptr(),
+                  self.perm.data_ptr(), self.inv_perm.data_ptr(), self.block_map.data_ptr(), self.num_blocks.data_ptr()]
+        except AttributeError:  # a buffer that is None
+            at = [_ptr(b) for b in (self.ids, self.w, self.counts, self.offsets, self.perm, self.inv_perm,
+                                    self.block_map, self.num_blocks)]
+        if c[0] != at:
+            st = _Routing(*at, self.block_rows)
+            c = self._known = (at, st, C.byref(st))
+        c[1].block_rows = self.block_rows
         return c
 
+    _known = (None, None, None)
+
     def _c(self) -> _Routing:
-        return self._cached()[8]
+        return self._cached()[1]
 
 
 def workspace(nbytes: int, device="cuda"):
@@ -475,9 +478,9 @@ class Scoring:
     scale: float = 1.0
 
     def _ref(self, E: int):
-        """A reference to the C struct, rebuilt only when a field changed."""
+        """A reference to the C struct, rebuilt only when a field or the bias's address changed."""
         c = self.__dict__.get("_cc")
-        key = (self.score, self.n_group, self.topk_group, self.group_top, self.renormalize, self.scale, E)
+        key = (self.score, self.n_group, self.topk_group, self.group_top, self.renormalize, self.scale, E, _ptr(self.bias))
         if c is None or c[0] is not self.bias or c[1] != key:
             if self.score not in SCORES:
                 raise ValueError(f"score {self.score!r}: one of {sorted(SCORES)}")
@@ -568,13 +571,13 @@ class MxMat:
         E, N, half = self.q.shape
         return int(E), int(N), 2 * int(half)
 
-    _known = (0, 0, None)  # q, sp, (a reference to the C struct, (E, N, K), the struct)
+    _known = (None, None, 0, 0, 0, None)  # q, sp, their addresses, q's size, what _ref_and_shape gives
 
     def _ref_and_shape(self):
-        """A reference to the C struct, (E, N, K), and the struct: rebuilt only when a tensor was replaced."""
-        q, sp, known = self._known
-        if q is not self.q or sp is not self.sp:
-            q, sp = self.q, self.sp
+        """A reference to the C struct, (E, N, K), and the struct: rebuilt where a tensor, its memory or size changed."""
+        q, sp = self.q, self.sp
+        kq, ks, aq, asp, size, known = self._known
+        if q is not kq or sp is not ks or q.data_ptr() != aq or sp.data_ptr() != asp or q.numel() != size:
             _tensor("q", q, (_U8,))
             if q.dim() != 3:
                 raise ValueError(f"q: shape {tuple(q.shape)}, expected [E][N][K/2]")
@@ -582,7 +585,7 @@ class MxMat:
             _tensor("sp", sp, (_U8,), (E, -(-N // 128), -(-K // 128), 512))
             st = _MxMat(_ptr(q), _ptr(sp))
             known = (C.byref(st), (E, N, K), st)
-            self._known = (q, sp, known)
+            self._known = (q, sp, st.q, st.sp, q.numel(), known)
         return known
 
     def _c(self) -> _MxMat:
@@ -598,24 +601,25 @@ class MxExperts:
 
     def _ref_and_sizes(self):
         """A reference to the C struct, and (E, I, d)."""
-        # rebuilt only when a matrix or one of its tensors was replaced (identity checks only)
-        c = self.__dict__.get("_cc")
-        g, u, dn = self.gate, self.up, self.down
-        if (c is None or c[0] is not g or c[1] is not u or c[2] is not dn or c[3] is not g.q or c[4] is not g.sp
-                or c[5] is not u.q or c[6] is not u.sp or c[7] is not dn.q or c[8] is not dn.sp):
-            E, I, d = g.shape
-            if u.shape != (E, I, d) or dn.shape != (E, d, I):
-                raise ValueError(f"gate {g.shape}, up {u.shape}, down {dn.shape}: expected (E, I, d) twice and (E, d, I)")
-            c = (g, u, dn, g.q, g.sp, u.q, u.sp, dn.q, dn.sp, C.byref(_MxExperts(g._c(), u._c(), dn._c(), E)), (E, I, d))
-            self.__dict__["_cc"] = c
-        return c[9], c[10]
+        # rebuilt where a matrix's was: that is the same object until then
+        g, u, dn = self.gate._ref_and_shape(), self.up._ref_and_shape(), self.down._ref_and_shape()
+        kg, ku, kd, known = self._known
+        if g is not kg or u is not ku or dn is not kd:
+            E, I, d = g[1]
+            if u[1] != (E, I, d) or dn[1] != (E, d, I):
+                raise ValueError(f"gate {g[1]}, up {u[1]}, down {dn[1]}: expected (E, I, d) twice and (E, d, I)")
+            known = (C.byref(_MxExperts(g[2], u[2], dn[2], E)), (E, I, d))
+            self._known = (g, u, dn, known)
+        return known
+
+    _known = (None, None, None, None)
 
 
 def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Routing, ws, stream=None) -> None:
     """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
     _tensor("logits", logits, _ONLY_FP32)
     T, E = logits.shape
-    r = out._cached()[9]
+    r = out._cached()[2]
     status = lib().moe_route_scored(logits.data_ptr(), scoring._ref(E), T, E, k, block_rows, r, ws.data_ptr(),
                                     ws.numel(), _stream(stream))
     if status:
@@ -716,7 +720,7 @@ def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
 def moe_mx_forward(X, routed: MxExperts, shared: Optional[MxExperts], routing: Routing, Y, ws, stream=None) -> None:
     """The expert layer on MXFP4 weights, for a routing of moe_route or moe_route_scored."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
-    rr = routing._cached()[9]
+    rr = routing._cached()[2]
     status = lib().moe_mx_forward(X.data_ptr(), T, d, I, int(routing.ids.shape[1]), re, se, I_sh, rr,
                                   Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
@@ -732,7 +736,7 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
     """moe_route_scored + moe_mx_forward in one call."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
     _tensor("logits", logits, _ONLY_FP32, (T, E))
-    r = out._cached()[9]
+    r = out._cached()[2]
     status = lib().moe_mx_layer(logits.data_ptr(), scoring._ref(E), X.data_ptr(), T, d, I, k, block_rows, re, se, I_sh,
                                 r, Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:

@@ -517,3 +517,36 @@ def test_a_tile_at_the_ends_of_32_bits_is_reported(T, entry):
     bm.moe_mx_forward(layer.x, layer.routed, None, r, y, ws)
     torch.cuda.synchronize()
     assert bm.STATUS_NAMES[bm.moe_check_status(ws)] == "MOE_ERR_INVALID_ARG"
+
+
+def test_new_memory_under_the_same_tensors():
+    """Weights, the bias and a routing's buffers that were given other memory: the results of newly made objects."""
+    a, b = _Layer(20, 24, 256, 96, 64, 8), _Layer(21, 24, 256, 96, 64, 8)
+    bias = [torch.randn(8, device="cuda") for _ in range(2)]
+
+    def run(layer, scoring, r, x, logits):
+        y = torch.empty((24, 256), dtype=torch.bfloat16, device="cuda")
+        ws = bm.workspace(bm.moe_mx_layer_workspace_bytes(24, 256, 96, 8, 2, 64, 16))
+        bm.moe_mx_layer(logits, scoring, x, layer.routed, layer.shared, 2, 16, r, y, ws)
+        torch.cuda.synchronize()
+        return y, r.ids.clone()
+
+    fresh = run(b, bm.Scoring("sigmoid", bias[1].clone()), bm.Routing.empty(24, 8, 2, 16), a.x, a.logits)
+    sc, r = bm.Scoring("sigmoid", bias[0]), bm.Routing.empty(24, 8, 2, 16)
+    run(a, sc, r, a.x, a.logits)
+    old = []  # kept, so that nothing else gets their memory
+
+    def replace(t, by):
+        old.append(t.data)
+        t.data = by.clone()
+
+    for name in ("gate", "up", "down"):
+        for mine, other in ((a.routed, b.routed), (a.shared, b.shared)):
+            replace(getattr(mine, name).q, getattr(other, name).q)
+            replace(getattr(mine, name).sp, getattr(other, name).sp)
+    replace(sc.bias, bias[1])
+    for name in ("ids", "w", "counts", "offsets", "perm", "inv_perm", "block_map", "num_blocks"):
+        replace(getattr(r, name), getattr(r, name))
+        getattr(r, name).fill_(-1)
+    y, ids = run(a, sc, r, a.x, a.logits)
+    assert torch.equal(ids, fresh[1]) and torch.equal(y, fresh[0])

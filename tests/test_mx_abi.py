@@ -159,6 +159,79 @@ def test_binding_refuses_what_the_library_cannot_see():
         bm.MxMat.empty(1, 4, 40, device="cpu")
 
 
+class _Dtype:
+    def __init__(self, name):
+        self.name = name
+
+    def __str__(self):
+        return "torch." + self.name
+
+
+_UINT8, _FLOAT32 = _Dtype("uint8"), _Dtype("float32")
+
+
+class _Tensor:
+    """What the binding asks of a CUDA tensor, whose memory can be replaced as by set_ or an assignment to .data."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, at, shape, dtype):
+        self.at, self.shape, self.dtype = at, shape, dtype
+
+    def data_ptr(self):
+        return self.at
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+
+def _fake_mat(at, E, N, K):
+    return bm.MxMat(_Tensor(at, (E, N, K // 2), _UINT8), _Tensor(at + 8, (E, -(-N // 128), -(-K // 128), 512), _UINT8))
+
+
+def test_structs_follow_their_tensors_memory():
+    """A tensor that keeps its identity but not its memory or size: the next call gets the new ones."""
+    m = _fake_mat(1024, 1, 128, 64)
+    assert m._c().q == 1024 and m._c() is m._c()
+    m.q.at = 2048
+    assert m._c().q == 2048
+    m.sp.at = 4096
+    assert m._c().sp == 4096
+    m.q.shape = (1, 64, 32)
+    assert m._ref_and_shape()[1] == (1, 64, 64)
+
+    ex = bm.MxExperts(_fake_mat(16, 2, 96, 256), _fake_mat(32, 2, 96, 256), _fake_mat(48, 2, 256, 96))
+    first = ex._ref_and_sizes()
+    assert ex._ref_and_sizes()[0] is first[0] and first[1] == (2, 96, 256)
+    for mat, name in ((ex.gate, "gate"), (ex.up, "up"), (ex.down, "down")):
+        for field in ("q", "sp"):
+            getattr(mat, field).at += 4096
+            got = getattr(ex._ref_and_sizes()[0]._obj, name)
+            assert getattr(got, field) == getattr(mat, field).at, (name, field)
+    ex.up.q.shape = (2, 64, 128)
+    with pytest.raises(ValueError, match="expected"):
+        ex._ref_and_sizes()
+
+    sc = bm.Scoring(bias=_Tensor(64, (8,), _FLOAT32))
+    assert sc._ref(8)._obj.bias == 64
+    sc.bias.at = 128
+    assert sc._ref(8)._obj.bias == 128
+
+    names = ("ids", "w", "counts", "offsets", "perm", "inv_perm", "block_map", "num_blocks")
+    r = bm.Routing(*(_Tensor(16 * i, (4,), None) for i in range(1, 9)), block_rows=16)
+    assert r._c().ids == 16 and r._c() is r._c()
+    for n in names:
+        getattr(r, n).at += 1024
+        assert getattr(r._c(), n) == getattr(r, n).at, n
+    r.ids = None
+    assert r._c().ids is None and r._c().w == r.w.at
+
+
 def test_reference_rounding():
     """The tests' own MXFP4: the worked values of the E2M1 grid, its ties and its saturation."""
     x = np.zeros((1, 32))
