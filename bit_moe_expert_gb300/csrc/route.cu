@@ -362,9 +362,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const float* __res
       const int cnt = s_cnt[e];
       int b = s_boff[e];
       for (int r = 0; r < cnt; r += block_rows, ++b) {
-        out.block_map[3 * b + 0] = e;
-        out.block_map[3 * b + 1] = s_off[e] + r;
-        out.block_map[3 * b + 2] = min(block_rows, cnt - r);
+        int32_t* const entry = out.block_map + 3 * static_cast<size_t>(b);  // 3 b passes 2^31 with 2^30 tiles of one row
+        entry[0] = e;
+        entry[1] = s_off[e] + r;
+        entry[2] = min(block_rows, cnt - r);
       }
     }
   }

@@ -245,3 +245,24 @@ def test_scores_at_the_end_of_the_range(score, E, renormalize, low, high):
     else:
         tol = w * W_RTOL + (1.5 + 1) * unit
     assert (np.abs(got - w) <= tol).all(), np.max(np.abs(got - w) / tol)
+
+
+@pytest.mark.parametrize("scored", [True, False])
+def test_a_block_map_past_2_31_elements(scored):
+    """Tiles of one row, all experts selected: tile b is (b / T, b, 1)."""
+    T, E, k = (1 << 31) // 3 // 32 + 9999, 32, 32
+    lg = torch.zeros((T, E), dtype=torch.float32, device="cuda")
+    out = bm.Routing.empty(T, E, k, 1)
+    ws = bm.workspace(bm.moe_route_workspace_bytes(T, E, k))
+    if scored:
+        bm.moe_route_scored(lg, bm.Scoring(**_kw("softmax")), k, 1, out, ws)
+    else:
+        bm.moe_route(lg, k, 1, out, ws)
+    torch.cuda.synchronize()
+    assert bm.moe_check_status(ws) == 0
+    n = int(out.num_blocks.item())
+    assert n == T * k and 3 * n > 1 << 31
+    for b0 in range(0, n, 1 << 26):
+        b = torch.arange(b0, min(n, b0 + (1 << 26)), device="cuda")
+        want = torch.stack([b // T, b, torch.ones_like(b)], 1).to(torch.int32)
+        assert torch.equal(out.block_map[b0:b0 + len(b)], want), b0
