@@ -550,3 +550,14 @@ def test_new_memory_under_the_same_tensors():
         getattr(r, name).fill_(-1)
     y, ids = run(a, sc, r, a.x, a.logits)
     assert torch.equal(ids, fresh[1]) and torch.equal(y, fresh[0])
+
+
+@pytest.mark.parametrize("T,d,I,I_shared,E,k,block_rows", [
+    (1000, 256, 96, 64, 64, 6, 128),
+    (700, 160, 96, 0, 130, 4, 32),
+    (2000, 128, 160, 96, 40, 3, 96),
+])
+def test_layer_of_many_tokens_and_experts(T, d, I, I_shared, E, k, block_rows):
+    layer = _Layer(T + E, T, d, I, I_shared, E)
+    y, r = layer.run(bm.Scoring("sigmoid", scale=1.5), k, block_rows, runs=2)
+    layer.check(y, r)

@@ -266,3 +266,46 @@ def test_a_block_map_past_2_31_elements(scored):
         b = torch.arange(b0, min(n, b0 + (1 << 26)), device="cuda")
         want = torch.stack([b // T, b, torch.ones_like(b)], 1).to(torch.int32)
         assert torch.equal(out.block_map[b0:b0 + len(b)], want), b0
+
+
+def _settled(rng, T, E, k, bias, kw):
+    """Logits whose selection hangs on no less than GAP, and the reference."""
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    ids, w, gap = _reference(l, bias, k, kw)
+    for _ in range(20):
+        bad = gap < GAP
+        if not bad.any():
+            break
+        l[bad] = rng.standard_normal((int(bad.sum()), E)).astype(np.float32)
+        ids[bad], w[bad], gap[bad] = _reference(l[bad], bias, k, kw)
+    assert not (gap < GAP).any()
+    return l, ids, w
+
+
+@pytest.mark.parametrize("mode", ["ticket", "gridsync", ""])
+@pytest.mark.parametrize("T,E,k,n_group,topk_group", [
+    (700, 256, 4, 8, 4),     # bases in shared memory beside the candidates
+    (4000, 64, 4, 8, 4),     # between one chunk an SM and half of what is resident: the barrier without being asked
+    (700, 300, 6, 3, 2),     # groups that fall on no whole lanes: the widest use of shared memory
+])
+def test_every_way_of_placing_selects_by_the_definition(T, E, k, n_group, topk_group, mode, monkeypatch):
+    monkeypatch.setenv("MOE_ROUTE_MODE", mode)
+    rng = np.random.default_rng(T + E)
+    kw = _kw("sigmoid", n_group, topk_group, scale=2.5)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    l, ids, w = _settled(rng, T, E, k, bias, kw)
+    out, ws = _run(l, bias, k, 32, kw)
+    _check(out, ids, w, E, 32)
+    assert bm.moe_check_status(ws) == 0
+
+
+def test_more_chunks_than_the_counts_sums_hold():
+    """Past 65,504 tokens the last CTA places everything, with the bases in global memory."""
+    rng = np.random.default_rng(12)
+    T, E, k = 66000, 16, 2
+    kw = _kw("sigmoid", 4, 2)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    l, ids, w = _settled(rng, T, E, k, bias, kw)
+    out, ws = _run(l, bias, k, 128, kw)
+    _check(out, ids, w, E, 128)
+    assert bm.moe_check_status(ws) == 0
