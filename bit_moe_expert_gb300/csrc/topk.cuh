@@ -416,11 +416,15 @@ __device__ __forceinline__ bool warp_scored_topk(const float (&x)[kPL], const fl
   if (!selected) w = 0.0f;
   if (sc.renormalize) {
     float sum = warp_sum(w);
-    if (sum < 0x1p-64f) {  // up to where the approximate quotient holds; exact
+    if (sum < 0x1p-64f) {  // up to where the approximate reciprocal holds; exact
       sum *= 0x1p100f;
       w *= 0x1p100f;
     }
-    w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
+    // A quotient by the reciprocal, corrected once by its residual (Markstein, 1990): a selection of one then has
+    // weight 1 and equal scores have equal shares, exactly, as the sums of products that a rounding of Y to bf16 finds
+    // halfway between two values need.  (An IEEE division took 0.3 us of a token's 4.1.)
+    const float inv = __fdividef(1.0f, sum), q = w * inv;
+    w = sum > 0.0f ? fmaf(fmaf(-q, sum, w), inv, q) : 0.0f;
   }
   if (selected) publish(rank, static_cast<int>(me.y), w * sc.scale);
   __syncwarp();  // the list may be written for the next row

@@ -309,3 +309,26 @@ def test_more_chunks_than_the_counts_sums_hold():
     out, ws = _run(l, bias, k, 128, kw)
     _check(out, ids, w, E, 128)
     assert bm.moe_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [16, 300])
+def test_weights_that_have_an_exact_value(score, E):
+    """One expert selected, or a power of two of equal ones: exactly scale / k, whatever the scores."""
+    rng = np.random.default_rng(E)
+    T = 500
+    for k in (1, 2, 8):
+        l = np.full((T, E), -30.0, np.float32)
+        for t in range(T):
+            l[t, rng.permutation(E)[:k]] = rng.uniform(-20, 20)
+        for scale in (1.0, 2.5):
+            out, _ = _run(l, None, k, 16, _kw(score, scale=scale))
+            assert (out.w.cpu().numpy() == np.float32(scale / k)).all(), k
+
+
+@pytest.mark.parametrize("E", [1, 16, 512])
+def test_scores_that_have_an_exact_value(E):
+    """Without renormalisation: equal shares of a power of two, the logistic function at 0 and far above it."""
+    for score, l, want in (("softmax", 3.0, 1 / E), ("sigmoid", 0.0, 0.5), ("sigmoid", 40.0, 1.0)):
+        out, _ = _run(np.full((20, E), l, np.float32), None, 1, 16, _kw(score, renormalize=False, scale=2.5))
+        assert (out.w.cpu().numpy() == np.float32(2.5 * want)).all(), (score, l)
