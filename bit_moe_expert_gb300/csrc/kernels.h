@@ -275,12 +275,14 @@ struct MxExpertMaps {
 };
 // Few tokens: the activations are quantised inside the products, by every CTA
 // again.  That pays while it is short beside the launch that it saves:
-//   linear layer    up to kMxFewValues values of X: 8 x 2048 5.3 us against 6.1
-//                   with X quantised by a kernel of its own, 2 x 8192 10.4
-//                   against 12.6; 8 x 4096 9.0 against 8.4, 16 x 2048 7.7 against 6.1
-//   expert layer    while the gate/up product's CTAs are at most one per SM
-//                   (kMxFewItems): d = 2048, I = 512, 8 + 1 experts: 2 tokens
-//                   18.1 us against 19.6, 4 tokens 26.5 against 23.2
+//   linear layer    up to kMxFewValues values of X: 8 x 2048 5.1 us against 5.9
+//                   with X quantised by a kernel of its own, 2 x 8192 10.1
+//                   against 12.4; 8 x 4096 8.7 against 8.0, 16 x 2048 7.4 against 5.9
+//   expert layer    up to kMxFewItems CTAs of the gate/up product, as many as this
+//                   GPU has SMs: d = 2048, I = 512, 8 + 1 experts: one token 15.2
+//                   us against 18.0, 2 tokens 17.4 against 19.0, 4 tokens 27.7
+//                   against 23.4.  A constant: the workspace's layout goes by it
+//                   and is asked for without a device.
 constexpr int kMxFewT = 32;  // tokens at most (accumulator columns)
 constexpr int kMxFewValues = 16384;
 constexpr int kMxFewItems = 152;

@@ -6,8 +6,8 @@
 // E2M1's largest power of two), and 2^-e is the float whose exponent field is
 // 254 minus the byte.  The multiplication by it is exact (a power of two), so
 // the only rounding is the conversion to E2M1.  Both directions are bound by
-// memory: 8192 x 8192 bf16 27.1 us to codes and 26.1 back (25.0 for the bytes at
-// the rate of a copy), 512 x 2048 1.8 us each (a launch).
+// memory: 8192 x 8192 bf16 27.0 us to codes and 26.0 back (25.0 for the bytes at
+// the rate of a copy), 512 x 2048 1.6 and 1.3 us (a launch).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

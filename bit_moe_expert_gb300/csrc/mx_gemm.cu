@@ -21,10 +21,11 @@
 // 3 on epilogue, two or four per quarter of the tensor-memory lanes.  Every wait
 // is bounded and records MOE_ERR_TIMEOUT.
 //
-// Measured: experts of d = 2048, I = 512, 8 of 256 + shared, 512 tokens in tiles of
-// 32: gate/up 38 us for 285 MB of weights, down 25 us for 143 MB and 38 MB of rows
-// (bound by memory); 4096 tokens in tiles of 128: 60 us, and 70 us with 302 MB of
-// rows written; dense 333 x 2816 -> 1001 5 us, 512 x 4096 -> 8192 10 us.
+// Measured, each kernel alone between events: experts of d = 2048, I = 512, 8 of 256
+// + shared, 512 tokens in tiles of 32: gate/up 44 us for 285 MB of weights, down 31
+// us for 143 MB and 38 MB of rows (bound by memory); 4096 tokens in tiles of 128: 65
+// us, and 76 us with 302 MB of rows written.  Inside a layer they overlap with their
+// neighbours.  Dense: 333 x 2816 -> 1001 5 us, 512 x 4096 -> 8192 10 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,10 +47,10 @@ constexpr int kEpiWarp0 = 3;
 // A launch's variant.  kRowTiles: 128-row groups of scales of the tokens (tiles of
 // up to 128, or of 256).  kHold: there is room for one accumulator only, so the
 // epilogue takes its columns into registers and releases it before it works on
-// them (8192^3 200 -> 195 us, 4096^3 42.4 -> 37.5; gate/up of 4096 tokens in
-// tiles of 128 75 -> 62); with more accumulators nothing waits for it, and the
-// registers would keep the CTA from starting beside the previous kernel's (256 x
-// 2048 -> 2048 6.1 -> 7.1 us).
+// them (8192^3 200 -> 195 us, 4096^3 42.4 -> 37.5, both before the pairs below;
+// gate/up of 4096 tokens in tiles of 128 75.5 -> 65, the layer 224 -> 213); with
+// more accumulators nothing waits for it, and the registers would keep the CTA from
+// starting beside the previous kernel's (256 x 2048 -> 2048 6.1 -> 7.1 us).
 template <int kMode_, int kRowTiles_, bool kHold_>
 struct Variant {
   static constexpr int kMode = kMode_, kRowTiles = kRowTiles_;
@@ -266,9 +267,9 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t v, int lane) {
 // consecutive columns of h, one block, so a token's largest magnitude is one
 // reduction over the lanes; eight tokens' codes are turned by a nibble
 // transposition into words of eight columns of one token.  (Two tokens' exponents
-// to a word and shuffles that halve the words, 11 for eight tokens, came out slower
-// than a reduction each: 4096 tokens 66.5 -> 68.5 us; without any of this
-// arithmetic and its stores the product takes 62.)
+// to a word and shuffles that halve the words, 11 for eight tokens, came out 2 us
+// slower than a reduction each at 4096 tokens; without any of this arithmetic and
+// its stores the product takes 60 instead of 65.)
 template <typename V, typename Release>
 __device__ __forceinline__ void epilogue_gate_up(const MxExpertArgs& a, const Item& m, const Plan& p, uint32_t tbase,
                                                  int bn, int lanegrp, int colpart, int lane, Release release) {

@@ -1,5 +1,6 @@
-// GPU-resident routing in one launch: top-k, histogram, exclusive scan, stable
-// scatter and tile block map, with no host round trip ("Perplexity's Lily
+// GPU-resident routing: top-k, histogram, exclusive scan, stable scatter and tile
+// block map, in one launch (scored routing of some sizes: two, see the end of this
+// comment), with no host round trip ("Perplexity's Lily
 // Beats MLX-LM on MacBook M5", section "Prefill: keep routing on the GPU,
 // dequantize in flight": histogram, prefix scan, scatter and block map after
 // every top-8 selection, kept inside one GPU submission).
@@ -8,7 +9,9 @@
 // and selects their top k.  It then writes its
 // per-expert counts and, for every assignment, the rank among the chunk's
 // assignments to the same expert (computed in assignment order, so the result
-// is stable).  The last CTA to finish (an atomic ticket, no spin wait) reduces
+// is stable).  Where all CTAs are resident together they meet at a bounded
+// barrier, and each sums the chunks' counts and places its own assignments;
+// otherwise the last CTA to finish (an atomic ticket, no spin wait) reduces
 // the chunk counts into counts/offsets, turns them into per-chunk bases, places
 // every assignment, and writes the block map.
 //
@@ -20,8 +23,11 @@
 // Scored routing (softmax or logistic scores, a bias, groups; kScored): the
 // same kernel with warp_scored_topk as the selection.  Its weights come from
 // fp32 scores that the selection has at hand, so there are no weight CTAs.
-// Bound by latency: of 256 experts in 8 groups, top 8, one token 4.1 us, 4096
-// tokens 11.9 (4.7 MB, 0.7 us of memory); launches back to back.
+// Several chunks take selection and placement in two launches, in chunks of 16
+// tokens, up to one CTA per SM (2432 tokens of 152 SMs), one launch at the barrier
+// while its CTAs are resident, and two launches again beyond (launch_route).
+// Bound by latency: of 256 experts in 8 groups, top 8, one token 4.1 us, 1024
+// tokens 8.3, 4096 tokens 12.1 (4.7 MB, 0.7 us of memory); in a CUDA graph.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -479,7 +485,7 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int block_row
   // (1024 tokens of 256 experts 8.6 us, at the barrier 9.1).  More chunks: two
   // tokens per warp at the barrier (4096 tokens 12.5 us, in two launches 14.8);
   // where they are not resident together, in two launches (8192 tokens 20 us),
-  // as long as the counts' sums fit.
+  // as long as the counts' sums fit; else the last CTA places everything.
   int tokens = kRouteTokensPerCta, nroute = nchunks;
   const int nhalf = (T + kRouteWarps - 1) / kRouteWarps;
   const bool single = nhalf <= device_sms();

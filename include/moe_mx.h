@@ -102,7 +102,8 @@ size_t moe_mx_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_s
  *   FFN(x) = MX(silu(MX(x) Wg^T) * (MX(x) Wu^T)) Wd^T
  * with MX() the rounding of moe_mx_quantize; the products, SwiGLU and the sums
  * over experts (in slot order, the shared expert last) are in fp32, the second
- * MX() takes the fp32 SwiGLU, and Y is rounded to bf16 once.
+ * MX() takes the fp32 SwiGLU (in it, silu of a value below -87.3 is 0), and Y is
+ * rounded to bf16 once.
  * Arguments as for moe_forward; d, I and I_shared multiples of 32.
  * MOE_ERR_UNSUPPORTED also where moe_route_max_blocks times ceil(max(d, I) /
  * 128), plus the shared expert's tiles likewise, is above 2^30. */
