@@ -1,7 +1,7 @@
 """GB300-native 4-bit groupwise-affine mixture-of-experts layer (sm_103a).
 
-Thin Python binding over the C ABI in include/moe.h and include/moe_mx.h (MXFP4
-weights).  The functions carry the C names and only marshal arguments (torch
+Thin Python binding over the C ABI in include/moe.h, include/moe_mx.h (MXFP4
+weights) and include/moe_blk.h (block-scaled 8-bit weights, the RMS norm).  The functions carry the C names and only marshal arguments (torch
 tensors -> device pointers, the current CUDA stream); every step of the layer runs
 in the CUDA library.  There is no fallback: if the library is missing or a call
 fails, an exception is raised.
@@ -31,7 +31,10 @@ EXPORTED = ("moe_status_string", "moe_device_sm_count", "moe_prepack_bytes", "mo
             "moe_profile_kernel_name", "moe_profile_read", "moe_profile_reset", "moe_debug_decode",
             "moe_route_scored", "moe_mx_scale_bytes", "moe_mx_prepack_scales", "moe_mx_quantize", "moe_mx_dequant",
             "moe_mx_matmul", "moe_mx_linear_workspace_bytes", "moe_mx_linear", "moe_mx_forward_workspace_bytes",
-            "moe_mx_forward", "moe_mx_layer_workspace_bytes", "moe_mx_layer")
+            "moe_mx_forward", "moe_mx_layer_workspace_bytes", "moe_mx_layer",
+            "moe_blk_quantize", "moe_blk_quantize_weights", "moe_blk_dequant", "moe_blk_dequant_weights",
+            "moe_blk_matmul", "moe_blk_linear_workspace_bytes", "moe_blk_linear", "moe_rmsnorm",
+            "moe_blk_forward_workspace_bytes", "moe_blk_forward", "moe_blk_layer_workspace_bytes", "moe_blk_layer")
 
 
 class MoeError(RuntimeError):
@@ -65,6 +68,14 @@ class _MxMat(C.Structure):
 
 class _MxExperts(C.Structure):
     _fields_ = [("gate", _MxMat), ("up", _MxMat), ("down", _MxMat), ("n_experts", C.c_int)]
+
+
+class _BlkMat(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("s", C.c_void_p)]
+
+
+class _BlkExperts(C.Structure):
+    _fields_ = [("gate", _BlkMat), ("up", _BlkMat), ("down", _BlkMat), ("n_experts", C.c_int)]
 
 
 _lib_handle = None
@@ -141,6 +152,7 @@ def lib(path: Optional[str] = None):
         L.moe_debug_decode.argtypes = [C.c_longlong, C.c_int]
         i, p, sz, mat = C.c_int, C.c_void_p, C.c_size_t, C.POINTER(_MxMat)
         ex = C.POINTER(_MxExperts)
+        blk, bex, ll = C.POINTER(_BlkMat), C.POINTER(_BlkExperts), C.c_longlong
         for name, restype, argtypes in (
                 ("moe_route_scored", i, [p, C.POINTER(_Scoring), i, i, i, i, C.POINTER(_Routing), p, sz, p]),
                 ("moe_mx_scale_bytes", sz, [i, i, i]),
@@ -154,7 +166,20 @@ def lib(path: Optional[str] = None):
                 ("moe_mx_forward", i, [p, i, i, i, i, ex, ex, i, C.POINTER(_Routing), p, p, sz, p]),
                 ("moe_mx_layer_workspace_bytes", sz, [i] * 7),
                 ("moe_mx_layer", i, [p, C.POINTER(_Scoring), p, i, i, i, i, i, ex, ex, i, C.POINTER(_Routing), p, p,
-                                     sz, p])):
+                                     sz, p]),
+                ("moe_blk_quantize", i, [p, i, i, i, ll, blk, p]),
+                ("moe_blk_quantize_weights", i, [p, i, i, i, i, blk, p]),
+                ("moe_blk_dequant", i, [blk, i, i, i, p, p]),
+                ("moe_blk_dequant_weights", i, [blk, i, i, i, i, p, p]),
+                ("moe_blk_matmul", i, [blk, i, blk, i, i, p, i, p, sz, p]),
+                ("moe_blk_linear_workspace_bytes", sz, [i, i, i]),
+                ("moe_blk_linear", i, [p, i, i, i, ll, blk, i, p, i, p, sz, p]),
+                ("moe_rmsnorm", i, [p, i, i, i, ll, p, p, i, p, i, C.c_float, p, i, blk, p]),
+                ("moe_blk_forward_workspace_bytes", sz, [i] * 7),
+                ("moe_blk_forward", i, [p, blk, i, i, i, i, bex, bex, i, C.POINTER(_Routing), p, p, sz, p]),
+                ("moe_blk_layer_workspace_bytes", sz, [i] * 7),
+                ("moe_blk_layer", i, [p, C.POINTER(_Scoring), p, blk, i, i, i, i, i, bex, bex, i, C.POINTER(_Routing), p,
+                                      p, sz, p])):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = restype, argtypes
         _lib_handle = L
@@ -493,8 +518,8 @@ class Scoring:
         return c[2]
 
 
-_BF16, _FP16, _FP32, _U8 = 0, 1, 2, 3  # the first three as moe_dtype
-_DTYPE_NAMES = {"bfloat16": _BF16, "int16": _BF16, "float16": _FP16, "float32": _FP32, "uint8": _U8}
+_BF16, _FP16, _FP32, _U8, _E4M3 = 0, 1, 2, 3, 4  # the first three as moe_dtype
+_DTYPE_NAMES = {"bfloat16": _BF16, "int16": _BF16, "float16": _FP16, "float32": _FP32, "uint8": _U8, "float8_e4m3fn": _E4M3}
 _dtype_codes = {}  # torch.dtype -> code, filled as types are met
 
 
@@ -741,6 +766,251 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
                                 r, Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
         _check("moe_mx_layer", status)
+    out.block_rows = block_rows
+
+
+# ----------------------------------------------------------------------- block-scaled 8-bit floating point, RMS norm
+
+_CODES = (_U8, _E4M3)
+
+
+@dataclasses.dataclass
+class _BlkCodes:
+    """Codes q (uint8 or float8_e4m3fn) and scales s (fp32) on the device, see include/moe_blk.h."""
+    q: "object"
+    s: "object"
+
+    _known = (None, None, 0, 0, 0, None)  # q, s, their addresses, q's size, what _ref_and_shape gives
+
+    def _ref_and_shape(self):
+        """A reference to the C struct, the shape, and the struct: rebuilt where a tensor, its memory or size changed."""
+        q, s = self.q, self.s
+        kq, ks, aq, at, size, known = self._known
+        if q is not kq or s is not ks or q.data_ptr() != aq or s.data_ptr() != at or q.numel() != size:
+            _tensor("q", q, _CODES)
+            shape, scales = self._shapes()
+            _tensor("s", s, _ONLY_FP32, scales)
+            aq, at = q.data_ptr(), s.data_ptr()
+            st = _BlkMat(aq, at)
+            known = (C.byref(st), shape, st)
+            self._known = (q, s, aq, at, q.numel(), known)
+        return known
+
+
+class BlkMat(_BlkCodes):
+    """A stack of weight matrices: q [E][N][K], s [E][ceil(N/128)][ceil(K/128)], as checkpoints hold them."""
+
+    @staticmethod
+    def empty(E: int, N: int, K: int, device="cuda") -> "BlkMat":
+        """Room for E matrices, e.g. as the result of moe_blk_quantize_weights."""
+        import torch
+        return BlkMat(torch.empty((E, N, K), dtype=torch.uint8, device=device),
+                      torch.empty((E, -(-N // 128), -(-K // 128)), dtype=torch.float32, device=device))
+
+    def _shapes(self):
+        if self.q.dim() != 3:
+            raise ValueError(f"q: shape {tuple(self.q.shape)}, expected [E][N][K]")
+        E, N, K = self.q.shape
+        return (E, N, K), (E, -(-N // 128), -(-K // 128))
+
+
+class BlkAct(_BlkCodes):
+    """Activations: q [rows][K], s [ceil(K/128)][rows up to a multiple of 4]."""
+
+    @staticmethod
+    def empty(rows: int, K: int, device="cuda") -> "BlkAct":
+        """Room for the result of moe_blk_quantize or moe_rmsnorm."""
+        import torch
+        return BlkAct(torch.empty((rows, K), dtype=torch.uint8, device=device),
+                      torch.empty((-(-K // 128), (rows + 3) // 4 * 4), dtype=torch.float32, device=device))
+
+    def _shapes(self):
+        if self.q.dim() != 2:
+            raise ValueError(f"q: shape {tuple(self.q.shape)}, expected [rows][K]")
+        rows, K = self.q.shape
+        return (rows, K), (-(-K // 128), (rows + 3) // 4 * 4)
+
+
+@dataclasses.dataclass
+class BlkExperts:
+    """One expert set: gate and up [E][I][d], down [E][d][I]."""
+    gate: BlkMat
+    up: BlkMat
+    down: BlkMat
+
+    def _ref_and_sizes(self):
+        """A reference to the C struct, and (E, I, d)."""
+        # rebuilt where a matrix's was: that is the same object until then
+        g, u, dn = self.gate._ref_and_shape(), self.up._ref_and_shape(), self.down._ref_and_shape()
+        kg, ku, kd, known = self._known
+        if g is not kg or u is not ku or dn is not kd:
+            E, I, d = g[1]
+            if u[1] != (E, I, d) or dn[1] != (E, d, I):
+                raise ValueError(f"gate {g[1]}, up {u[1]}, down {dn[1]}: expected (E, I, d) twice and (E, d, I)")
+            known = (C.byref(_BlkExperts(g[2], u[2], dn[2], E)), (E, I, d))
+            self._known = (g, u, dn, known)
+        return known
+
+    _known = (None, None, None, None)
+
+
+def moe_blk_quantize(X, out: BlkAct, stream=None) -> None:
+    """X [rows][K] (bf16, fp16 or fp32; rows may be strided) -> out: a scale per row and 128 columns."""
+    rows, K, ld, code = _rows("X", X)
+    m, shape, _ = out._ref_and_shape()
+    if type(out) is not BlkAct or shape != (rows, K):
+        raise ValueError(f"out: {type(out).__name__} of {shape}, expected BlkAct of ({rows}, {K})")
+    status = lib().moe_blk_quantize(X.data_ptr(), code, rows, K, ld, m, _stream(stream))
+    if status:
+        _check("moe_blk_quantize", status)
+
+
+def moe_blk_quantize_weights(W, out: BlkMat, stream=None) -> None:
+    """W [E][N][K] (bf16, fp16 or fp32) -> out: a scale per block of 128 x 128.
+
+    A product that takes `out` as its weights may be the next call on the stream."""
+    code = _tensor("W", W, _FLOATS)
+    m, shape, _ = out._ref_and_shape()
+    if type(out) is not BlkMat or W.shape != shape:
+        raise ValueError(f"out: {type(out).__name__} of {shape}, expected BlkMat of {tuple(W.shape)}")
+    status = lib().moe_blk_quantize_weights(W.data_ptr(), code, *shape, m, _stream(stream))
+    if status:
+        _check("moe_blk_quantize_weights", status)
+
+
+def moe_blk_dequant(m, X, stream=None) -> None:
+    """X (bf16, fp16 or fp32, m's shape) = the values of m, a BlkAct or a BlkMat."""
+    ref, shape, _ = m._ref_and_shape()
+    code = _tensor("X", X, _FLOATS, shape)
+    fn = lib().moe_blk_dequant if type(m) is BlkAct else lib().moe_blk_dequant_weights
+    status = fn(ref, *shape, code, X.data_ptr(), _stream(stream))
+    if status:
+        _check("moe_blk_dequant", status)
+
+
+def _blk_one(W: BlkMat, K: int):
+    ref, shape, _ = W._ref_and_shape()
+    if type(W) is not BlkMat or shape[0] != 1:
+        raise ValueError(f"W: {type(W).__name__} of {shape}, expected a BlkMat of one matrix")
+    if shape[2] != K:
+        raise ValueError(f"the activations have {K} columns, W {shape[2]}")
+    return ref, shape[1]
+
+
+def moe_blk_matmul(A: BlkAct, W: BlkMat, Y, ws, stream=None) -> None:
+    """Y [M][N] (bf16, fp16 or fp32) = A (M, K) times W (1, N, K), transposed."""
+    a, shape, _ = A._ref_and_shape()
+    if type(A) is not BlkAct:
+        raise ValueError(f"A: {type(A).__name__}, expected BlkAct")
+    M, K = shape
+    w, N = _blk_one(W, K)
+    y = _tensor("Y", Y, _FLOATS, (M, N))
+    status = lib().moe_blk_matmul(a, M, w, N, K, Y.data_ptr(), y, ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        _check("moe_blk_matmul", status)
+
+
+def moe_blk_linear_workspace_bytes(T: int, N: int, K: int) -> int:
+    return int(lib().moe_blk_linear_workspace_bytes(T, N, K))
+
+
+def moe_blk_linear(X, W: BlkMat, Y, ws, stream=None) -> None:
+    """Y [T][N] = quantised X [T][K] times W (1, N, K), transposed: a linear layer with block-scaled 8-bit weights."""
+    T, K, ld, code = _rows("X", X)
+    w, N = _blk_one(W, K)
+    y = _tensor("Y", Y, _FLOATS, (T, N))
+    status = lib().moe_blk_linear(X.data_ptr(), code, T, K, ld, w, N, Y.data_ptr(), y, ws.data_ptr(), ws.numel(),
+                                  _stream(stream))
+    if status:
+        _check("moe_blk_linear", status)
+
+
+def moe_rmsnorm(X, gamma, eps: float, residual=None, stream_out=None, Y=None, out: Optional[BlkAct] = None,
+                stream=None) -> None:
+    """r = X + residual (written to stream_out, by default the residual itself), y = r / sqrt(mean(r^2) + eps) * gamma.
+
+    X [T][d] (bf16, fp16 or fp32; rows may be strided); residual [T][d] of X's type or fp32, or None; gamma [d], bf16 or
+    fp32.  y goes to Y [T][d] (bf16, fp16 or fp32), quantised to out, or to both."""
+    T, d, ld, code = _rows("X", X)
+    shape = X.shape
+    rp = op = yp = 0
+    rt = yt = code
+    if residual is not None:
+        rt = _tensor("residual", residual, _FLOATS, shape)
+        rp = op = residual.data_ptr()
+        if stream_out is not None:
+            if _tensor("stream_out", stream_out, _FLOATS, shape) != rt:
+                raise ValueError(f"stream_out: {stream_out.dtype}, the residual {residual.dtype}")
+            op = stream_out.data_ptr()
+    elif stream_out is not None:
+        raise ValueError("stream_out without a residual")
+    gt = _tensor("gamma", gamma, _GAMMA, (d,))
+    if Y is not None:
+        yt = _tensor("Y", Y, _FLOATS, shape)
+        yp = Y.data_ptr()
+    q = None
+    if out is not None:
+        q, qshape, _ = out._ref_and_shape()
+        if type(out) is not BlkAct or qshape != shape:
+            raise ValueError(f"out: {type(out).__name__} of {qshape}, expected BlkAct of {tuple(shape)}")
+    status = lib().moe_rmsnorm(X.data_ptr(), code, T, d, ld, rp, op, rt, gamma.data_ptr(), gt, eps, yp, yt, q,
+                               _stream(stream))
+    if status:
+        _check("moe_rmsnorm", status)
+
+
+_GAMMA = (_BF16, _FP32)
+
+
+def moe_blk_forward_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
+    return int(lib().moe_blk_forward_workspace_bytes(T, d, I, E, k, I_shared, block_rows))
+
+
+def _blk_sets(X, routed: BlkExperts, shared: Optional[BlkExperts], Y):
+    """References to the C structs and the sizes of an expert call, shapes checked."""
+    if type(X) is BlkAct:
+        xq, shape, _ = X._ref_and_shape()
+        xp = 0
+    else:
+        _tensor("X", X, _ONLY_BF16)
+        xq, shape, xp = None, X.shape, X.data_ptr()
+    T, d = shape
+    re, (E, I, dr) = routed._ref_and_sizes()
+    se, I_sh = None, 0
+    if shared is not None:
+        se, (Es, I_sh, ds) = shared._ref_and_sizes()
+        if Es != 1 or ds != d:
+            raise ValueError(f"shared: ({Es}, {I_sh}, {ds}), expected one expert of width {d}")
+    if dr != d:
+        raise ValueError(f"X is {d} wide, the experts {dr}")
+    _tensor("Y", Y, _ONLY_BF16, shape)
+    return T, d, E, I, I_sh, re, se, xp, xq
+
+
+def moe_blk_forward(X, routed: BlkExperts, shared: Optional[BlkExperts], routing: Routing, Y, ws, stream=None) -> None:
+    """The expert layer on block-scaled 8-bit weights; X: bf16 [T][d], or a BlkAct taken as it is."""
+    T, d, E, I, I_sh, re, se, xp, xq = _blk_sets(X, routed, shared, Y)
+    rr = routing._cached()[2]
+    status = lib().moe_blk_forward(xp, xq, T, d, I, int(routing.ids.shape[1]), re, se, I_sh, rr, Y.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        _check("moe_blk_forward", status)
+
+
+def moe_blk_layer_workspace_bytes(T: int, d: int, I: int, E: int, k: int, I_shared: int, block_rows: int) -> int:
+    return int(lib().moe_blk_layer_workspace_bytes(T, d, I, E, k, I_shared, block_rows))
+
+
+def moe_blk_layer(logits, scoring: Scoring, X, routed: BlkExperts, shared: Optional[BlkExperts], k: int, block_rows: int,
+                  out: Routing, Y, ws, stream=None) -> None:
+    """moe_route_scored + moe_blk_forward in one call."""
+    T, d, E, I, I_sh, re, se, xp, xq = _blk_sets(X, routed, shared, Y)
+    _tensor("logits", logits, _ONLY_FP32, (T, E))
+    r = out._cached()[2]
+    status = lib().moe_blk_layer(logits.data_ptr(), scoring._ref(E), xp, xq, T, d, I, k, block_rows, re, se, I_sh, r,
+                                 Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        _check("moe_blk_layer", status)
     out.block_rows = block_rows
 
 

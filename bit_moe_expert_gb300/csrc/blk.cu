@@ -1,0 +1,457 @@
+// Block-scaled 8-bit floating point: quantisation, its inverse, and the RMS norm
+// with the residual's addition (include/moe_blk.h).
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "blk.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace bm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ activations
+// A warp takes 256 columns (eight a lane, a block in either half) of four
+// neighbouring rows, whose scales of a block are neighbours too: one 16-byte
+// store.  Bound by memory.
+//
+// The products read weights before they wait for the kernel before them, so what
+// may write weights lets no kernel start before it has completed; this one writes
+// activations and starts its successor at once.
+constexpr int kRowsAWarp = 4;
+struct Patch {
+  int row, col;
+  __device__ __forceinline__ Patch(int K) {
+    const int segs = (K + 255) / 256;
+    const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    row = unit / segs * kRowsAWarp;
+    col = unit % segs * 256 + 8 * (threadIdx.x & 31);
+  }
+};
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads)
+    blk_quantize_kernel(const void* __restrict__ X, int rows, int K, long long ldx, uint8_t* __restrict__ q,
+                        float* __restrict__ s) {
+  const Patch at(K);
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (at.row >= rows) return;
+  Load8<kType> x[kRowsAWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsAWarp; ++i) {
+    if (at.row + i < rows && at.col < K)
+      x[i].load(static_cast<const char*>(X) + (at.row + i) * static_cast<size_t>(ldx) * (kType == kFp32 ? 4 : 2), at.col);
+    else
+      x[i].zero();
+  }
+  float scale[kRowsAWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsAWarp; ++i) {
+    float f[8];
+    x[i].floats(f);
+    scale[i] = blk_scale(half_warp_max(largest_bits(f)));
+    if (at.row + i < rows && at.col < K)
+      *reinterpret_cast<uint2*>(q + static_cast<size_t>(at.row + i) * K + at.col) = blk_codes8(f, blk_inverse(scale[i]));
+  }
+  if ((lane & 15) == 0 && at.col < K)
+    *reinterpret_cast<float4*>(s + static_cast<size_t>(at.col / kBlk) * blk_scale_rows(rows) + at.row) =
+        make_float4(scale[0], scale[1], scale[2], scale[3]);
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads)
+    blk_dequant_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s, int rows, int K, void* __restrict__ X) {
+  const Patch at(K);
+  pdl_wait();
+  if (at.row >= rows || at.col >= K) return;
+  uint2 code[kRowsAWarp];
+#pragma unroll
+  for (int i = 0; i < kRowsAWarp; ++i)
+    code[i] = at.row + i < rows ? __ldg(reinterpret_cast<const uint2*>(q + static_cast<size_t>(at.row + i) * K + at.col))
+                                : make_uint2(0, 0);
+  const float4 s4 = __ldg(reinterpret_cast<const float4*>(s + static_cast<size_t>(at.col / kBlk) * blk_scale_rows(rows) + at.row));
+  const float scale[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+  for (int i = 0; i < kRowsAWarp; ++i) {
+    if (at.row + i >= rows) break;
+    float f[8], lo[4], hi[4];
+    e4m3x4_to_f32(code[i].x, lo);
+    e4m3x4_to_f32(code[i].y, hi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = lo[j] * scale[i];
+      f[4 + j] = hi[j] * scale[i];
+    }
+    store8(kType, X, static_cast<size_t>(at.row + i) * K + at.col, f);
+  }
+}
+
+// ------------------------------------------------------------------ weights
+// One CTA per block of 128 x 128, all of it in registers between the maximum and
+// the codes: a half warp per row and pass, eight passes of 16 rows.  Lets no
+// kernel start early (its result may be weights).
+constexpr int kPasses = 128 / (kThreads / 16);
+struct Block {
+  int row0, r, col;   // first row of the block, this thread's first row in it, its first column
+  size_t matrix;      // rows before the matrix
+  size_t scale;       // place of the scale
+  __device__ __forceinline__ Block(int N, int K) {
+    const int kb = (K + kBlk - 1) / kBlk, nb = (N + kBlk - 1) / kBlk;
+    const unsigned b = blockIdx.x;
+    const int e = b / (static_cast<unsigned>(nb) * kb), i = b - static_cast<unsigned>(e) * nb * kb;
+    row0 = i / kb * kBlk;
+    r = threadIdx.x >> 4;
+    col = i % kb * kBlk + 8 * (threadIdx.x & 15);
+    matrix = static_cast<size_t>(e) * N;
+    scale = b;
+  }
+};
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads)
+    blk_quantize_weights_kernel(const void* __restrict__ W, int N, int K, uint8_t* __restrict__ q, float* __restrict__ s) {
+  __shared__ uint32_t s_max[kThreads / 32];
+  const Block at(N, K);
+  pdl_wait();
+  Load8<kType> x[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int n = at.row0 + at.r + i * (kThreads / 16);
+    if (n < N && at.col < K)
+      x[i].load(static_cast<const char*>(W) + (at.matrix + n) * K * (kType == kFp32 ? 4 : 2), at.col);
+    else
+      x[i].zero();
+  }
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    float f[8];
+    x[i].floats(f);
+    a = max(a, largest_bits(f));
+  }
+  a = __reduce_max_sync(0xffffffffu, a);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) a = max(a, s_max[i]);
+  const float scale = blk_scale(a), inv = blk_inverse(scale);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int n = at.row0 + at.r + i * (kThreads / 16);
+    float f[8];
+    x[i].floats(f);
+    if (n < N && at.col < K) *reinterpret_cast<uint2*>(q + (at.matrix + n) * K + at.col) = blk_codes8(f, inv);
+  }
+  if (threadIdx.x == 0) s[at.scale] = scale;
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads)
+    blk_dequant_weights_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s, int N, int K, void* __restrict__ W) {
+  const Block at(N, K);
+  pdl_wait();
+  const float scale = __ldg(s + at.scale);
+  uint2 code[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int n = at.row0 + at.r + i * (kThreads / 16);
+    code[i] = n < N && at.col < K ? __ldg(reinterpret_cast<const uint2*>(q + (at.matrix + n) * K + at.col)) : make_uint2(0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int n = at.row0 + at.r + i * (kThreads / 16);
+    if (n >= N || at.col >= K) continue;
+    float f[8], lo[4], hi[4];
+    e4m3x4_to_f32(code[i].x, lo);
+    e4m3x4_to_f32(code[i].y, hi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = lo[j] * scale;
+      f[4 + j] = hi[j] * scale;
+    }
+    store8(kType, W, (at.matrix + n) * K + at.col, f);
+  }
+}
+
+// ------------------------------------------------------------------ RMS norm
+// One CTA per row, the row in registers (eight columns a thread and chunk: a
+// block of 128 columns is a half warp).  Everything is fp32; what has to be more
+// exact is a pair (hi, lo) of fp32 numbers whose sum is the value:
+//   the sum of squares   eight at a time in fp32, the sums of eight added as
+//                        pairs (the addition's error by Knuth's two-sum), about
+//                        2^-28 of it in all;
+//   1 / sqrt(mean + eps) the hardware's estimate y0 and one Newton step, y0 (1 +
+//                        (1 - v y0^2) / 2), whose residual is formed with fused
+//                        multiply-adds.
+// y = r hi gamma is then off by less than 2^-21 of itself.  Where the codes of y
+// (1 - 2^-21) and y (1 + 2^-21) differ, one value in some 10^5, the thread's
+// values are evaluated in 64 bits; the block's scale likewise.  (fp64 for all
+// would bound the kernel: an SM does two operations a clock.)
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return Pair{s.hi, s.lo + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Pair warp_sum(Pair a) {
+#pragma unroll
+  for (int i = 16; i > 0; i /= 2)
+    a = add(a, Pair{__shfl_xor_sync(0xffffffffu, a.hi, i), __shfl_xor_sync(0xffffffffu, a.lo, i)});
+  return a;
+}
+// 1 / sqrt(sum / d + eps)
+__device__ __forceinline__ Pair inverse_root(Pair sum, float d, float eps) {
+  const float q = __fdiv_rn(sum.hi, d);
+  const float q2 = (fmaf(-q, d, sum.hi) + sum.lo) / d;
+  Pair v = two_sum(q, eps);
+  v.lo += q2;
+  const float y = rsqrtf(v.hi);
+  const float p = __fmul_rn(y, y), pe = fmaf(y, y, -p);
+  float t = fmaf(-v.hi, p, 1.0f);  // 1 - v y^2, small
+  t = fmaf(-v.hi, pe, t);
+  t = fmaf(-v.lo, p, t);
+  const float c = 0.5f * y * t;
+  const float hi = y + c;
+  return Pair{hi, c - (hi - y)};
+}
+
+// The float nearest to x that rounds to fewer bits as x does: cut towards zero, the last bit set where that cut something.
+__device__ __forceinline__ float odd_float(double x) {
+  const float f = __double2float_rz(x);
+  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+enum Residual { kNone, kSame, kWide };
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const void* gamma;
+  void* y;
+  uint8_t* q;
+  float* s;
+  long long ldx;
+  float eps;
+  int T, d, gamma_fp32, y_type;
+};
+
+constexpr float kNormError = 4.76837158e-7f;  // 2^-21
+
+// The eight values of y in 64 bits.
+__device__ __noinline__ void exact_values(const float (&r)[8], const float (&g)[8], Pair inv, double (&y)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    y[j] = static_cast<double>(r[j]) * (static_cast<double>(inv.hi) + static_cast<double>(inv.lo)) * static_cast<double>(g[j]);
+}
+
+template <int kType, int kResidual, int kChunks>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_kernel(const NormArgs a) {
+  constexpr int kRType = kResidual == kWide ? kFp32 : kType;
+  __shared__ Pair s_sum[32];
+  const int warps = blockDim.x >> 5;
+  const size_t row = blockIdx.x;
+  const int stride = 8 * blockDim.x;
+  int c = 8 * threadIdx.x;
+  constexpr bool kGammaEarly = kChunks < 4;  // more would not fit the registers of 1024 threads
+  float g[kGammaEarly ? kChunks : 1][8], r[kChunks][8];
+  auto load_gamma = [&](int i, int to) {
+    if (c + i * stride >= a.d) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[to][j] = 0.0f;
+    } else if (a.gamma_fp32) {
+      Load8<kFp32> v;
+      v.load(a.gamma, c + i * stride);
+      v.floats(g[to]);
+    } else {
+      Load8<kBf16> v;
+      v.load(a.gamma, c + i * stride);
+      v.floats(g[to]);
+    }
+  };
+  pdl_wait();
+  pdl_launch_dependents();
+  const char* x = static_cast<const char*>(a.x) + row * static_cast<size_t>(a.ldx) * (kType == kFp32 ? 4 : 2);
+  {
+    Load8<kType> v[kChunks];
+    Load8<kRType> w[kResidual == kNone ? 1 : kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (c + i * stride < a.d) v[i].load(x, c + i * stride); else v[i].zero();
+      if constexpr (kResidual != kNone) {
+        const char* p = static_cast<const char*>(a.residual) + row * a.d * (kRType == kFp32 ? 4 : 2);
+        if (c + i * stride < a.d) w[i].load(p, c + i * stride); else w[i].zero();
+      }
+    }
+    if constexpr (kGammaEarly) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) load_gamma(i, i);
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      v[i].floats(r[i]);
+      if constexpr (kResidual != kNone) {
+        float f[8];
+        w[i].floats(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          r[i][j] += f[j];
+          if constexpr (kRType == kBf16) r[i][j] = __bfloat162float(__float2bfloat16_rn(r[i][j]));
+          if constexpr (kRType == kFp16) r[i][j] = __half2float(__float2half_rn(r[i][j]));
+        }
+        if (c + i * stride < a.d) store8<kRType>(static_cast<char*>(a.residual_out) + (row * a.d + c + i * stride) * (kRType == kFp32 ? 4 : 2), r[i]);
+      }
+    }
+  }
+  Pair sum{0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    float q = r[i][0] * r[i][0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) q = fmaf(r[i][j], r[i][j], q);
+    sum = add(sum, Pair{q, 0.0f});
+  }
+  sum = warp_sum(sum);
+  if (warps > 1) {
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    const int l = threadIdx.x & 31;
+    sum = warp_sum(l < warps ? s_sum[l] : Pair{0.0f, 0.0f});
+  }
+  const Pair inv = inverse_root(sum, static_cast<float>(a.d), a.eps);
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int col = c + i * stride;
+    if (col - 8 * static_cast<int>(threadIdx.x & 31) >= a.d) break;  // the same for the whole warp
+    const int gi = kGammaEarly ? i : 0;
+    if constexpr (!kGammaEarly) load_gamma(i, 0);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = r[i][j] * inv.hi * g[gi][j];
+    if (a.y && col < a.d) store8(a.y_type, a.y, row * a.d + col, y);
+    if (!a.q) continue;
+    const float m = __uint_as_float(half_warp_max(largest_bits(y)));
+    float s = blk_scale(__float_as_uint(m * (1.0f - kNormError)));
+    if (__any_sync(0xffffffffu, __float_as_uint(s) != __float_as_uint(blk_scale(__float_as_uint(m * (1.0f + kNormError)))))) {
+      double v[8], most = 0.0;
+      exact_values(r[i], g[gi], inv, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = fmax(most, fabs(v[j]));
+#pragma unroll
+      for (int k = 1; k < 16; k *= 2) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, k));
+      if (m == m) s = blk_scale(__float_as_uint(odd_float(most)));
+    }
+    const float t = blk_inverse(s);
+    uint2 code = blk_codes8(y, t * (1.0f - kNormError));
+    const uint2 other = blk_codes8(y, t * (1.0f + kNormError));
+    if (code.x != other.x || code.y != other.y) {
+      double v[8];
+      exact_values(r[i], g[gi], inv, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = odd_float(v[j] * static_cast<double>(t));
+      code = blk_codes8(y, 1.0f);
+    }
+    if (col < a.d) {
+      *reinterpret_cast<uint2*>(a.q + row * a.d + col) = code;
+      if ((threadIdx.x & 15) == 0) a.s[static_cast<size_t>(col / kBlk) * blk_scale_rows(a.T) + row] = s;
+    }
+  }
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(int kind, void (*kernel)(P...), unsigned grid, int threads, cudaStream_t stream, bool pdl, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  timer_begin(kind, stream);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  timer_end(kind, stream);
+  return err;
+}
+
+// CTAs of Patch: units of four rows x 256 columns, a warp each.
+size_t patches(int rows, int K) {
+  const size_t units = static_cast<size_t>((rows + kRowsAWarp - 1) / kRowsAWarp) * ((K + 255) / 256);
+  return (units + kThreads / 32 - 1) / (kThreads / 32);
+}
+constexpr size_t kMaxUnits = 0x7FFFFFFFu / (kThreads / 32);  // a unit's number is an int
+
+template <int kType>
+cudaError_t launch_norm(const NormArgs& a, int residual, cudaStream_t stream, bool pdl) {
+  // two chunks a thread, or more where a CTA would have too many threads; one for few rows, where latency counts
+  int chunks = a.T < 512 ? 1 : 2;
+  while (a.d > 8 * 1024 * chunks) chunks *= 2;
+  const int threads = ((a.d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32;
+  auto pick = [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    return chunks == 1 ? rmsnorm_kernel<kType, R, 1> : chunks == 2 ? rmsnorm_kernel<kType, R, 2> : rmsnorm_kernel<kType, R, 4>;
+  };
+  const auto kernel = residual == kNone   ? pick(std::integral_constant<int, kNone>{})
+                      : residual == kSame ? pick(std::integral_constant<int, kSame>{})
+                                          : pick(std::integral_constant<int, kWide>{});
+  return launch(kKNorm, kernel, static_cast<unsigned>(a.T), threads, stream, pdl, a);
+}
+
+}  // namespace
+
+cudaError_t launch_blk_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, float* s,
+                                cudaStream_t stream, bool pdl) {
+  const size_t grid = patches(rows, K);
+  if (grid > kMaxUnits) return cudaErrorInvalidValue;
+  const auto kernel = type == kBf16 ? blk_quantize_kernel<kBf16> : type == kFp16 ? blk_quantize_kernel<kFp16> : blk_quantize_kernel<kFp32>;
+  return launch(kKBlkQuantize, kernel, static_cast<unsigned>(grid), kThreads, stream, pdl, X, rows, K, ldx, q, s);
+}
+
+cudaError_t launch_blk_dequant(const uint8_t* q, const float* s, int rows, int K, int type, void* X, cudaStream_t stream,
+                               bool pdl) {
+  const size_t grid = patches(rows, K);
+  if (grid > kMaxUnits) return cudaErrorInvalidValue;
+  const auto kernel = type == kBf16 ? blk_dequant_kernel<kBf16> : type == kFp16 ? blk_dequant_kernel<kFp16> : blk_dequant_kernel<kFp32>;
+  return launch(kKBlkQuantize, kernel, static_cast<unsigned>(grid), kThreads, stream, pdl, q, s, rows, K, X);
+}
+
+cudaError_t launch_blk_quantize_weights(const void* W, int type, int E, int N, int K, uint8_t* q, float* s,
+                                        cudaStream_t stream, bool pdl) {
+  const size_t grid = E * blk_weight_scales(N, K);
+  if (grid > 0x7FFFFFFFu) return cudaErrorInvalidValue;
+  const auto kernel = type == kBf16   ? blk_quantize_weights_kernel<kBf16>
+                      : type == kFp16 ? blk_quantize_weights_kernel<kFp16>
+                                      : blk_quantize_weights_kernel<kFp32>;
+  return launch(kKBlkQuantize, kernel, static_cast<unsigned>(grid), kThreads, stream, pdl, W, N, K, q, s);
+}
+
+cudaError_t launch_blk_dequant_weights(const uint8_t* q, const float* s, int E, int N, int K, int type, void* W,
+                                       cudaStream_t stream, bool pdl) {
+  const size_t grid = E * blk_weight_scales(N, K);
+  if (grid > 0x7FFFFFFFu) return cudaErrorInvalidValue;
+  const auto kernel = type == kBf16   ? blk_dequant_weights_kernel<kBf16>
+                      : type == kFp16 ? blk_dequant_weights_kernel<kFp16>
+                                      : blk_dequant_weights_kernel<kFp32>;
+  return launch(kKBlkQuantize, kernel, static_cast<unsigned>(grid), kThreads, stream, pdl, q, s, N, K, W);
+}
+
+cudaError_t launch_rmsnorm(const RmsNorm& n, cudaStream_t stream, bool pdl) {
+  const NormArgs a{n.x, n.residual, n.residual_out, n.gamma, n.y, n.q, n.s, n.ldx, n.eps, n.T, n.d, n.gamma_fp32, n.y_type};
+  const int residual = !n.residual ? kNone : n.residual_type == n.x_type ? kSame : kWide;
+  return n.x_type == kBf16   ? launch_norm<kBf16>(a, residual, stream, pdl)
+         : n.x_type == kFp16 ? launch_norm<kFp16>(a, residual, stream, pdl)
+                             : launch_norm<kFp32>(a, residual, stream, pdl);
+}
+
+}  // namespace bm

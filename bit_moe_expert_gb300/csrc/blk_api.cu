@@ -1,0 +1,296 @@
+// Host side of include/moe_blk.h: argument checks, workspace layouts and
+// launches.  Nothing here allocates device memory or synchronises.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "kernels.h"
+#include "moe_blk.h"
+
+namespace bm {
+namespace {
+
+constexpr int kMaxRows = 1 << 30;  // rows (row indexes and TMA coordinates are 32-bit)
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool ws_ok(const void* ws, size_t have, size_t need) {
+  return ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && need > 0 && have >= need;
+}
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+cudaStream_t cuda(moe_stream s) { return reinterpret_cast<cudaStream_t>(s); }
+moe_status done(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+bool cols_ok(int K) { return K >= 16 && K % 16 == 0 && K <= kBlkMaxCols; }
+bool size_ok(int N, int K) { return N >= 1 && cols_ok(K); }
+bool mat_ok(const moe_blk_mat* m) { return m && m->q && m->s && aligned16(m->q) && aligned16(m->s); }
+bool experts_ok(const moe_blk_experts* ex) {
+  return ex && mat_ok(&ex->gate) && mat_ok(&ex->up) && mat_ok(&ex->down) && ex->n_experts >= 1;
+}
+int type_bytes(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
+bool type_ok(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
+size_t act_scale_bytes(long long rows, int K) { return static_cast<size_t>(blk_scale_rows(rows)) * blk_count(K) * 4; }
+
+moe_status check_x(const void* X, moe_dtype type, int rows, int K, long long ldx) {
+  if (rows < 0 || !cols_ok(K) || !type_ok(type) || ldx < K || (ldx * type_bytes(type)) % 16 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && (!X || !aligned16(X))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status check_weights(const void* W, moe_dtype type, int E, int N, int K, const moe_blk_mat* m) {
+  if (E < 1 || !size_ok(N, K) || !type_ok(type) || !W || !aligned16(W) || !mat_ok(m)) return MOE_ERR_INVALID_ARG;
+  if (N > kMaxRows || static_cast<double>(E) * blk_weight_scales(N, K) > 2147483647.0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_matmul(int M, const moe_blk_mat* W, int N, int K, const void* Y, moe_dtype y_type) {
+  if (M < 0 || !size_ok(N, K) || !mat_ok(W) || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
+  if (M > kMaxRows || N > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (M > 0 && (!Y || !aligned16(Y))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status few_linear(const BlkX& x, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type, moe_stream stream) {
+  const BlkFewLinearArgs a{x, W->q, W->s, Y, M, N, K, y_type};
+  return done(launch_blk_few_linear(a, cuda(stream), pdl_enabled()));
+}
+
+moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type, uint32_t*,
+                  moe_stream stream) {
+  return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
+}
+
+struct ExpertLayout {
+  size_t h, ypart, total;
+  int max_blocks;
+};
+
+ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
+  ExpertLayout L{};
+  L.max_blocks = moe_route_max_blocks(T, E, k, block_rows);
+  const size_t A = static_cast<size_t>(T) * k, rows = A + (I_shared > 0 ? T : 0);
+  size_t o = sizeof(WsHeader);
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o = round256(o + bytes);
+    return at;
+  };
+  L.ypart = take(rows * d * 4);
+  L.h = take(rows * (I > I_shared ? I : I_shared) * 4);
+  L.total = o;
+  return L;
+}
+
+bool expert_cols_ok(int n) { return n >= 32 && n % 32 == 0 && n <= kBlkMaxCols; }
+bool sizes_valid(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
+  return T >= 0 && expert_cols_ok(d) && expert_cols_ok(I) && (I_shared == 0 || expert_cols_ok(I_shared)) && E >= 1 && k >= 1 &&
+         block_rows >= 1 && block_rows <= kMaxBlockRows;
+}
+
+moe_status check_experts(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I, int k, const moe_blk_experts* routed,
+                         const moe_blk_experts* shared, int I_shared, const uint16_t* Y) {
+  if (T < 0 || k < 1 || !expert_cols_ok(d) || !expert_cols_ok(I) || (I_shared != 0 && !expert_cols_ok(I_shared)))
+    return MOE_ERR_INVALID_ARG;
+  if ((shared != nullptr) != (I_shared > 0)) return MOE_ERR_INVALID_ARG;
+  if (!experts_ok(routed) || (shared && (!experts_ok(shared) || shared->n_experts != 1))) return MOE_ERR_INVALID_ARG;
+  const int E = routed->n_experts;
+  if (E > kMaxE || k > kMaxK || k > E) return MOE_ERR_UNSUPPORTED;
+  // rows of the tensor maps and the launch's items are 32-bit
+  if (static_cast<long long>(T) * (k + 1) > (1ll << 30) || static_cast<long long>(E) * (d > I ? d : I) > (1ll << 30))
+    return MOE_ERR_UNSUPPORTED;
+  if ((X != nullptr) == (XQ != nullptr) && T > 0) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!Y || !aligned16(Y) || (X && !aligned16(X)) || (XQ && !mat_ok(XQ)))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Whether the products' items can be counted; everything else has been checked.
+bool items_ok(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
+  auto m_tiles = [](int a, int b) { return static_cast<long long>(blk_count(a > b ? a : b)); };
+  long long items = moe_route_max_blocks(T, E, k, block_rows) * m_tiles(d, I);
+  if (I_shared > 0) items += blk_count(T < 1 ? 1 : T) * m_tiles(d, I_shared);
+  return items <= kBlkMaxItems;
+}
+
+BlkWeights weights(const moe_blk_experts* ex) {
+  if (!ex) return BlkWeights{};
+  return BlkWeights{ex->gate.q, ex->up.q, ex->down.q, ex->gate.s, ex->up.s, ex->down.s};
+}
+
+moe_status forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I, int k, const moe_blk_experts* routed,
+                   const moe_blk_experts* shared, int I_shared, const moe_routing* r, uint16_t* Y, void* ws,
+                   moe_stream stream) {
+  if (T == 0) return MOE_OK;
+  const int E = routed->n_experts;
+  const ExpertLayout L = expert_layout(T, d, I, E, k, I_shared, r->block_rows);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  BlkFewArgs a{};
+  a.x = X ? BlkX{X, nullptr, d, 0, MOE_BF16} : BlkX{XQ->q, XQ->s, d, blk_scale_rows(T), kBlkCodes};
+  a.routed = weights(routed);
+  a.shared = weights(shared);
+  a.perm = r->perm;
+  a.inv_perm = r->inv_perm;
+  a.block_map = r->block_map;
+  a.num_blocks = r->num_blocks;
+  a.w = r->w;
+  a.h = reinterpret_cast<float*>(w + L.h);
+  a.ypart = reinterpret_cast<float*>(w + L.ypart);
+  a.y = Y;
+  a.status = &static_cast<WsHeader*>(ws)->status;
+  a.T = T;
+  a.d = d;
+  a.I = I;
+  a.k = k;
+  a.I_shared = I_shared;
+  a.E = E;
+  a.tiles = T * k < L.max_blocks ? T * k : L.max_blocks;
+  a.rows = r->block_rows;
+  a.num_sms = device_sms();
+  if (a.num_sms <= 0) return MOE_ERR_CUDA;
+  return done(launch_blk_few_experts(a, cuda(stream), pdl_enabled()));
+}
+
+}  // namespace
+}  // namespace bm
+
+using namespace bm;
+
+extern "C" {
+
+moe_status moe_blk_quantize(const void* X, moe_dtype type, int rows, int K, long long ldx, const moe_blk_mat* out,
+                            moe_stream stream) {
+  const moe_status st = check_x(X, type, rows, K, ldx);
+  if (st != MOE_OK) return st;
+  if (!mat_ok(out)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  return done(launch_blk_quantize(X, type, rows, K, ldx, out->q, out->s, cuda(stream), pdl_enabled()));
+}
+
+moe_status moe_blk_quantize_weights(const void* W, moe_dtype type, int E, int N, int K, const moe_blk_mat* out,
+                                    moe_stream stream) {
+  const moe_status st = check_weights(W, type, E, N, K, out);
+  if (st != MOE_OK) return st;
+  return done(launch_blk_quantize_weights(W, type, E, N, K, out->q, out->s, cuda(stream), pdl_enabled()));
+}
+
+moe_status moe_blk_dequant(const moe_blk_mat* a, int rows, int K, moe_dtype type, void* X, moe_stream stream) {
+  const moe_status st = check_x(X, type, rows, K, K);
+  if (st != MOE_OK) return st;
+  if (!mat_ok(a)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  return done(launch_blk_dequant(a->q, a->s, rows, K, type, X, cuda(stream), pdl_enabled()));
+}
+
+moe_status moe_blk_dequant_weights(const moe_blk_mat* m, int E, int N, int K, moe_dtype type, void* W, moe_stream stream) {
+  const moe_status st = check_weights(W, type, E, N, K, m);
+  if (st != MOE_OK) return st;
+  return done(launch_blk_dequant_weights(m->q, m->s, E, N, K, type, W, cuda(stream), pdl_enabled()));
+}
+
+moe_status moe_blk_matmul(const moe_blk_mat* A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
+                          void* ws, size_t ws_bytes, moe_stream stream) {
+  const moe_status st = check_matmul(M, W, N, K, Y, y_type);
+  if (st != MOE_OK) return st;
+  if (!mat_ok(A)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, sizeof(WsHeader))) return MOE_ERR_WORKSPACE;
+  if (M == 0) return MOE_OK;
+  return matmul(*A, M, W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
+}
+
+size_t moe_blk_linear_workspace_bytes(int T, int N, int K) {
+  if (T < 0 || !size_ok(N, K)) return 0;
+  return sizeof(WsHeader) + round256(static_cast<size_t>(T) * K) + round256(act_scale_bytes(T, K));
+}
+
+moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long long ldx, const moe_blk_mat* W, int N,
+                          void* Y, moe_dtype y_type, void* ws, size_t ws_bytes, moe_stream stream) {
+  moe_status st = check_x(X, x_type, T, K, ldx);
+  if (st != MOE_OK) return st;
+  st = check_matmul(T, W, N, K, Y, y_type);
+  if (st != MOE_OK) return st;
+  if (!ws_ok(ws, ws_bytes, moe_blk_linear_workspace_bytes(T, N, K))) return MOE_ERR_WORKSPACE;
+  if (T == 0) return MOE_OK;
+  uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
+  const moe_blk_mat xq{w, reinterpret_cast<float*>(w + round256(static_cast<size_t>(T) * K))};
+  if (T <= 8) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
+  if (launch_blk_quantize(X, x_type, T, K, ldx, xq.q, xq.s, cuda(stream), pdl_enabled()) != cudaSuccess) return MOE_ERR_CUDA;
+  return matmul(xq, T, W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
+}
+
+moe_status moe_rmsnorm(const void* X, moe_dtype x_type, int T, int d, long long ldx, const void* residual,
+                       void* residual_out, moe_dtype residual_type, const void* gamma, moe_dtype gamma_type, float eps,
+                       void* Y, moe_dtype y_type, const moe_blk_mat* out, moe_stream stream) {
+  const moe_status st = check_x(X, x_type, T, d, ldx);
+  if (st != MOE_OK) return st;
+  if (!gamma || !aligned16(gamma) || (gamma_type != MOE_BF16 && gamma_type != MOE_FP32)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if ((residual != nullptr) != (residual_out != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (residual && (!aligned16(residual) || !aligned16(residual_out) || (residual_type != x_type && residual_type != MOE_FP32)))
+    return MOE_ERR_INVALID_ARG;
+  if (!Y && !out) return MOE_ERR_INVALID_ARG;
+  if (Y && (!aligned16(Y) || !type_ok(y_type))) return MOE_ERR_INVALID_ARG;
+  if (out && !mat_ok(out)) return MOE_ERR_INVALID_ARG;
+  if (d > kNormMaxCols) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  RmsNorm n{};
+  n.x = X;
+  n.residual = residual;
+  n.residual_out = residual_out;
+  n.gamma = gamma;
+  n.y = Y;
+  n.q = out ? out->q : nullptr;
+  n.s = out ? out->s : nullptr;
+  n.ldx = ldx;
+  n.eps = eps;
+  n.T = T;
+  n.d = d;
+  n.x_type = x_type;
+  n.residual_type = residual_type;
+  n.gamma_fp32 = gamma_type == MOE_FP32;
+  n.y_type = y_type;
+  return done(launch_rmsnorm(n, cuda(stream), pdl_enabled()));
+}
+
+size_t moe_blk_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
+  if (!sizes_valid(T, d, I, E, k, I_shared, block_rows)) return 0;
+  return expert_layout(T, d, I, E, k, I_shared, block_rows).total;
+}
+
+moe_status moe_blk_forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I, int k,
+                           const moe_blk_experts* routed, const moe_blk_experts* shared, int I_shared,
+                           const moe_routing* r, uint16_t* Y, void* ws, size_t ws_bytes, moe_stream stream) {
+  const moe_status st = check_experts(X, XQ, T, d, I, k, routed, shared, I_shared, Y);
+  if (st != MOE_OK) return st;
+  if (!r) return MOE_ERR_INVALID_ARG;
+  if (r->block_rows < 1 || r->block_rows > kMaxBlockRows) return MOE_ERR_UNSUPPORTED;
+  if (!items_ok(T, d, I, routed->n_experts, k, I_shared, r->block_rows)) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!r->w || !r->perm || !r->inv_perm || !r->block_map || !r->num_blocks)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, moe_blk_forward_workspace_bytes(T, d, I, routed->n_experts, k, I_shared, r->block_rows)))
+    return MOE_ERR_WORKSPACE;
+  return forward(X, XQ, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
+}
+
+size_t moe_blk_layer_workspace_bytes(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
+  const size_t f = moe_blk_forward_workspace_bytes(T, d, I, E, k, I_shared, block_rows);
+  const size_t r = moe_route_workspace_bytes(T, E, k);
+  return f && r ? (f > r ? f : r) : 0;
+}
+
+moe_status moe_blk_layer(const float* logits, const moe_scoring* scoring, const uint16_t* X, const moe_blk_mat* XQ,
+                         int T, int d, int I, int k, int block_rows, const moe_blk_experts* routed,
+                         const moe_blk_experts* shared, int I_shared, moe_routing* r, uint16_t* Y, void* ws,
+                         size_t ws_bytes, moe_stream stream) {
+  moe_status st = check_experts(X, XQ, T, d, I, k, routed, shared, I_shared, Y);
+  if (st != MOE_OK) return st;
+  const int E = routed->n_experts;
+  st = check_scored(logits, scoring, T, E, k, block_rows, r);
+  if (st != MOE_OK) return st;
+  if (!items_ok(T, d, I, E, k, I_shared, block_rows)) return MOE_ERR_UNSUPPORTED;
+  if (!ws_ok(ws, ws_bytes, moe_blk_layer_workspace_bytes(T, d, I, E, k, I_shared, block_rows))) return MOE_ERR_WORKSPACE;
+  // one header for both, and after it the same room: the products start when the routing has completed
+  st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, stream);
+  if (st != MOE_OK) return st;
+  return forward(X, XQ, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
+}
+
+}  // extern "C"

@@ -26,6 +26,11 @@ enum KernelKind {
   kKMxGemm,      // MXFP4 dense product
   kKMxGateUp,
   kKMxDown,
+  kKNorm,         // RMS norm
+  kKBlkQuantize,  // block-scaled 8-bit quantisation (with or without the scatter to the routing's rows) and its inverse
+  kKBlkGemm,      // block-scaled dense product
+  kKBlkGateUp,
+  kKBlkDown,
   kKernelKinds
 };
 void timer_begin(int id, cudaStream_t s);
@@ -316,5 +321,75 @@ bool mx_few_fits(int T, int d, int I, int I_shared, int k, int max_blocks);
 cudaError_t launch_mx_few_experts(const MxFewArgs& a, const MxExpertMaps& maps, cudaStream_t stream, bool pdl);
 
 cudaError_t launch_mx_experts(const MxExpertArgs& a, const MxExpertMaps& maps, cudaStream_t stream);
+
+// ---------------------------------------------------------------- block-scaled 8-bit floating point
+constexpr int kBlk = 128;               // rows and columns of a block of weights, columns of one of activations
+constexpr int kBlkMaxCols = 1 << 20;    // columns of a matrix; of an expert's matrices also rows
+constexpr long long kBlkMaxItems = 1 << 30;
+constexpr int kNormMaxCols = 32768;
+__host__ __device__ constexpr int blk_count(int n) { return (n + kBlk - 1) / kBlk; }
+// pitch of the activations' scales
+__host__ __device__ constexpr long long blk_scale_rows(long long rows) { return (rows + 3) & ~3ll; }
+inline size_t blk_weight_scales(int N, int K) { return static_cast<size_t>(blk_count(N)) * blk_count(K); }
+
+// types: 0 bf16, 1 fp16, 2 fp32
+cudaError_t launch_blk_quantize(const void* X, int type, int rows, int K, long long ldx, uint8_t* q, float* s,
+                                cudaStream_t stream, bool pdl);
+cudaError_t launch_blk_dequant(const uint8_t* q, const float* s, int rows, int K, int type, void* X, cudaStream_t stream,
+                               bool pdl);
+cudaError_t launch_blk_quantize_weights(const void* W, int type, int E, int N, int K, uint8_t* q, float* s,
+                                        cudaStream_t stream, bool pdl);
+cudaError_t launch_blk_dequant_weights(const uint8_t* q, const float* s, int E, int N, int K, int type, void* W,
+                                       cudaStream_t stream, bool pdl);
+
+struct RmsNorm {
+  const void* x;
+  const void* residual;  // null: none
+  void* residual_out;
+  const void* gamma;
+  void* y;               // null: none
+  uint8_t* q;            // null: none
+  float* s;
+  long long ldx;
+  float eps;
+  int T, d, x_type, residual_type, gamma_fp32, y_type;
+};
+cudaError_t launch_rmsnorm(const RmsNorm& n, cudaStream_t stream, bool pdl);
+
+// Activations of a product: values of a type, rows ldx elements apart, or codes and scales.
+constexpr int kBlkCodes = 3;  // the "type" of codes
+struct BlkX {
+  const void* x;
+  const float* s;  // codes: the scales [ceil(K/128)][pitch]
+  long long ldx, pitch;
+  int type;
+};
+struct BlkFewLinearArgs {
+  BlkX x;
+  const uint8_t* w;
+  const float* sw;
+  void* y;
+  int T, N, K, y_type;
+};
+cudaError_t launch_blk_few_linear(const BlkFewLinearArgs& a, cudaStream_t stream, bool pdl);
+
+struct BlkWeights {
+  const uint8_t *gate, *up, *down;
+  const float *s_gate, *s_up, *s_down;
+};
+struct BlkFewArgs {
+  BlkX x;
+  BlkWeights routed, shared;
+  const int32_t *perm, *inv_perm, *block_map, *num_blocks;
+  const float* w;
+  float* h;       // [A + T][max(I, I_shared)]
+  float* ypart;   // [A + T][d]
+  uint16_t* y;
+  uint32_t* status;
+  int T, d, I, k, I_shared, E;
+  int tiles, rows;  // tiles of the routed experts launched, rows of a tile at most
+  int num_sms;
+};
+cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl);
 
 }  // namespace bm

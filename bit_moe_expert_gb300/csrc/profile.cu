@@ -12,7 +12,8 @@ namespace {
 
 const char* const kNames[kKernelKinds] = {"route", "decode", "router", "x_gather",
                                           "gemm_gateup", "gemm_down", "combine", "prepack",
-                                          "topk_wide", "mx_quantize", "mx_gemm", "mx_gateup", "mx_down"};
+                                          "topk_wide", "mx_quantize", "mx_gemm", "mx_gateup", "mx_down",
+                                          "rmsnorm", "blk_quantize", "blk_gemm", "blk_gateup", "blk_down"};
 
 struct Pending {
   int id;

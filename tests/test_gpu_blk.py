@@ -1,0 +1,296 @@
+"""Block-scaled 8-bit floating point: quantisation and its inverse exactly, products and expert layers against 64 bits.
+
+Products: the codes' products are exact, so an error comes from the fp32 accumulation alone.  The tensor cores add 32
+products at a time and may drop bits below the last place of the largest: two last places (2^-22) of the sum of
+magnitudes for each of the four additions of a block of 128.  Then the two scales' product and its product with the
+block's sum (2^-24 each), and one addition (2^-24 of the sum so far) per block, and up to 16 more where the blocks are
+added up in shares: |Y - Y64| <= bound = (4 2^-22 + (K/128 + 18) 2^-24) sum_k |a_k w_k|.  Rounding is monotone, so a Y
+in fewer bits lies between the values nearest to Y64 - bound and Y64 + bound: exact but for the sum.
+
+Expert layers: the hidden values are rounded to E4M3 from fp32 sums here and from 64 bits in the reference.  They differ
+by about 1e-6 of themselves, so about 3e-5 of them (that over the spacing of E4M3, 1/16 to 1/8) land on the other side of
+a rounding, by at most 1/8 of themselves: 7e-4 of the norm of h and of Y.  With bf16's own 2^-9/sqrt(3): relative L2 error
+below 3e-3.  One such value moves an element of Y by its share of it, about 1/sqrt(I) of the root mean square; a few at
+once stay below 3/sqrt(I) + 2^-8."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import bit_moe_expert_gb300 as bm  # noqa: E402
+import blk_ref  # noqa: E402
+import mx_ref  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_moe_expert_gb300 import build
+    build.build()
+    bm.lib()
+
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def _to(x, kind):
+    return torch.from_numpy(np.asarray(x, np.float32)).to(TYPES[kind]).cuda()
+
+
+def _mat(mat):
+    return bm.BlkMat(*(torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in mat))
+
+
+def _act(v, s):
+    """E4M3 values [rows][K] and scales [rows][blocks] -> a BlkAct whose padding is NaN."""
+    a = bm.BlkAct.empty(*v.shape)
+    a.s.fill_(float("nan"))
+    a.q.copy_(torch.from_numpy(blk_ref.encode(v)))
+    a.s[:, :v.shape[0]] = torch.from_numpy(np.ascontiguousarray(s.T.astype(np.float32)))
+    return a
+
+
+def _check_codes(q, s, v64, s64):
+    """Codes (as bytes) and scales [rows][blocks] against the reference's, NaN blocks aside."""
+    np.testing.assert_array_equal(s, s64)
+    ok = ~np.isnan(blk_ref.spread(s64, v64.shape[-1]))
+    np.testing.assert_array_equal(blk_ref.decode(q)[ok], v64[ok])
+
+
+ROWS = [(1, 16), (1, 2048), (3, 48), (5, 128), (33, 160), (130, 272), (7, 4112), (1000, 528), (2, 20000)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,K", ROWS)
+def test_quantise_rows(kind, rows, K):
+    rng = np.random.default_rng(rows + K)
+    x = _to(rng.standard_normal((rows, K)) * np.exp2(rng.integers(-12, 12, (rows, 1))), kind)
+    a = bm.BlkAct.empty(rows, K)
+    bm.moe_blk_quantize(x, a)
+    x64 = x.double().cpu().numpy()
+    v, s = blk_ref.quantise(x64)
+    _check_codes(a.q.cpu().numpy(), a.s.cpu().numpy()[:, :rows].T, v, s)
+    for out in TYPES:
+        y = torch.empty((rows, K), dtype=TYPES[out], device="cuda")
+        bm.moe_blk_dequant(a, y)
+        want = torch.from_numpy(v * blk_ref.spread(s, K)).to(TYPES[out])
+        assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("E,N,K", [(1, 1, 16), (1, 128, 128), (3, 131, 416), (2, 704, 272), (1, 257, 2064)])
+def test_quantise_weights(kind, E, N, K):
+    rng = np.random.default_rng(E + N + K)
+    w = _to(rng.standard_normal((E, N, K)) * np.exp2(rng.integers(-9, 9, (E, N, 1))), kind)
+    m = bm.BlkMat.empty(E, N, K)
+    bm.moe_blk_quantize_weights(w, m)
+    v, s = blk_ref.quantise_weights(w.double().cpu().numpy())
+    np.testing.assert_array_equal(m.s.cpu().numpy(), s)
+    np.testing.assert_array_equal(blk_ref.decode(m.q.cpu().numpy()), v)
+    for out in TYPES:
+        y = torch.empty((E, N, K), dtype=TYPES[out], device="cuda")
+        bm.moe_blk_dequant(m, y)
+        want = torch.from_numpy(blk_ref.weights((blk_ref.encode(v), s))).to(TYPES[out])
+        assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_quantise_edges(kind):
+    """Ties at every scale; magnitudes at and next to 448; zeros; the smallest and largest numbers; NaN and infinity."""
+    g = blk_ref.GRID
+    ties = np.concatenate([(g[:-1] + g[1:]) / 2, [448.0]])           # 126 midpoints and the largest code
+    ties = np.concatenate([ties, [-448.0]]) * np.where(np.arange(128) % 3 == 0, -1, 1)
+    info = torch.finfo(TYPES[kind])
+    rows = [ties * 2.0 ** e for e in (-6, 0, 5)] if kind != "bf16" else [ties, ties * 2.0 ** -20, ties * 2.0 ** 40]
+    for top in (447.0, 448.0, 450.0, 512.0, 224.0):
+        rows.append(np.where(np.arange(128) == 5, top, np.arange(128) / 7))
+    rows += [np.zeros(128), np.where(np.arange(128) == 3, info.max, 1.0), np.where(np.arange(128) == 3, -info.max, 0.0)]
+    rows += [np.full(128, info.tiny), np.where(np.arange(128) % 2, info.smallest_normal / 2, 0.0)]
+    rows += [np.where(np.arange(128) == 9, np.nan, ties), np.where(np.arange(128) == 31, -np.inf, ties)]
+    x = torch.tensor(np.stack(rows), dtype=torch.float64).to(TYPES[kind]).cuda()
+    a = bm.BlkAct.empty(*x.shape)
+    bm.moe_blk_quantize(x, a)
+    v, s = blk_ref.quantise(x.double().cpu().numpy())
+    _check_codes(a.q.cpu().numpy(), a.s.cpu().numpy()[:, :len(rows)].T, v, s)
+    y = torch.empty(x.shape, dtype=torch.float32, device="cuda")
+    bm.moe_blk_dequant(a, y)
+    y = y.cpu().numpy()
+    assert np.isnan(y[-2:]).all()
+    # bf16's and fp32's largest number is 255 and more 2^120: the nearest code (steps of 16) stands for 256 2^120 = 2^128,
+    # which fp32 rounds to infinity
+    with np.errstate(over="ignore"):
+        np.testing.assert_array_equal(y[:-2], (v * blk_ref.spread(s, 128))[:-2].astype(np.float32))
+    m = bm.BlkMat.empty(len(rows), 1, 128)
+    bm.moe_blk_quantize_weights(x.view(-1, 1, 128), m)
+    _check_codes(m.q.cpu().numpy()[:, 0], m.s.cpu().numpy()[:, 0], v, s)
+
+
+def test_quantise_strided_rows_and_another_stream():
+    rng = np.random.default_rng(1)
+    x = _to(rng.standard_normal((40, 512)), "bf16")[3:29, 64:240]
+    a = bm.BlkAct.empty(26, 176)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    bm.moe_blk_quantize(x, a, stream=st)
+    torch.cuda.synchronize()
+    _check_codes(a.q.cpu().numpy(), a.s.cpu().numpy()[:, :26].T, *blk_ref.quantise(x.double().cpu().numpy()))
+
+
+SIZES = [(1, 1, 16), (1, 2048, 2048), (1, 130, 48), (2, 8, 4112), (3, 33, 160), (8, 200, 1040), (9, 64, 128), (16, 128, 64),
+         (17, 200, 272), (63, 129, 512), (128, 513, 288), (129, 129, 512), (200, 31, 1056), (300, 700, 2048), (257, 512, 32),
+         (1000, 256, 320), (640, 1000, 4096)]
+
+
+def _assert_product(y, av, wv, K):
+    want = av @ wv.T
+    bound = (4 * 2.0 ** -22 + (K / 128 + 18) * 2.0 ** -24) * (np.abs(av) @ np.abs(wv).T)
+    low, high = (torch.from_numpy(v).to(y.dtype).double().numpy() for v in (want - bound, want + bound))
+    y = y.double().cpu().numpy()
+    assert np.isfinite(y).all()
+    worst = np.maximum(low - y, y - high)
+    assert worst.max() <= 0, (worst.max(), np.argwhere(worst > 0)[:5], len(np.argwhere(worst > 0)))
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("y_kind", list(TYPES))
+def test_matmul(M, N, K, y_kind):
+    """Operands with any fp32 scales, their padding NaN."""
+    rng = np.random.default_rng(M + N + K)
+    v, s = blk_ref.quantise(rng.standard_normal((M, K)) * np.exp(rng.standard_normal((M, 1))))
+    s = (s * rng.uniform(0.6, 1.7, s.shape)).astype(np.float32)
+    mat = blk_ref.draw_matrix(rng, 1, N, K)
+    ws = bm.workspace(256)
+    y = torch.full((M + 1, N), 7.0, dtype=TYPES[y_kind], device="cuda")
+    bm.moe_blk_matmul(_act(v, s), _mat(mat), y[:M], ws)
+    assert bm.moe_check_status(ws) == 0
+    assert (y[M] == 7).all()                                         # nothing behind the last row
+    _assert_product(y[:M], v * blk_ref.spread(s.astype(np.float64), K), blk_ref.weights(mat)[0], K)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 2048, 2048), (1, 17, 16), (5, 100, 1040), (8, 2048, 512), (9, 300, 272), (333, 1001, 2816)])
+@pytest.mark.parametrize("x_kind", list(TYPES))
+def test_linear(T, N, K, x_kind):
+    rng = np.random.default_rng(T + N + K)
+    x = _to(rng.standard_normal((T, K + 16)), x_kind)[:, :K]         # strided rows
+    mat = blk_ref.draw_matrix(rng, 1, N, K)
+    ws = bm.workspace(bm.moe_blk_linear_workspace_bytes(T, N, K))
+    y = torch.empty((T, N), dtype=torch.float32, device="cuda")
+    bm.moe_blk_linear(x, _mat(mat), y, ws)
+    assert bm.moe_check_status(ws) == 0
+    _assert_product(y, blk_ref.rounded(x.double().cpu().numpy()), blk_ref.weights(mat)[0], K)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_nan_stays_in_its_row_and_column(M):
+    rng = np.random.default_rng(M)
+    v, s = blk_ref.quantise(rng.standard_normal((M, 512)))
+    mat = blk_ref.draw_matrix(rng, 1, 300, 512)
+    mat[0][0, 77, 400] = 0x7F                                        # a NaN weight
+    a = _act(v, s)
+    a.q[1, 130] = 0xFF                                               # a NaN code
+    a.s[0, 2] = float("nan")                                         # a NaN scale
+    y = torch.empty((M, 300), dtype=torch.float32, device="cuda")
+    bm.moe_blk_matmul(a, _mat(mat), y, bm.workspace(256))
+    bad = torch.isnan(y).cpu().numpy()
+    want = np.zeros((M, 300), bool)
+    want[1:3] = want[:, 77] = True
+    np.testing.assert_array_equal(bad, want)
+
+
+def test_weights_just_quantised():
+    """A product may follow its weights' quantisation directly, whatever was in that memory before."""
+    rng = np.random.default_rng(5)
+    T, N, K = 4, 4096, 2048
+    x = _to(rng.standard_normal((T, K)), "bf16")
+    m = bm.BlkMat.empty(1, N, K)
+    ws = bm.workspace(bm.moe_blk_linear_workspace_bytes(64, N, K))
+    for rows in (T, 64):
+        xr = x.repeat(rows // T, 1)
+        for i in range(3):
+            w = _to(rng.standard_normal((1, N, K)), "bf16")
+            m.q.fill_(0x7F)
+            torch.cuda.synchronize()
+            y = torch.empty((rows, N), dtype=torch.float32, device="cuda")
+            bm.moe_blk_quantize_weights(w, m)
+            bm.moe_blk_linear(xr, m, y, ws)
+            v, s = blk_ref.quantise_weights(w.double().cpu().numpy())
+            _assert_product(y, blk_ref.rounded(xr.double().cpu().numpy()), blk_ref.weights((blk_ref.encode(v), s))[0], K)
+
+
+# ------------------------------------------------------------------ expert layers
+
+def _experts(rng, E, d, I):
+    host = [blk_ref.draw_matrix(rng, E, *nk) for nk in ((I, d), (I, d), (d, I))]
+    return host, bm.BlkExperts(*(_mat(m) for m in host))
+
+
+def _routing(ids, w, E, rows):
+    T, k = ids.shape
+    r = bm.Routing.empty(T, E, k, rows)
+    counts, offsets, perm, inv, tiles = mx_ref.tables(ids, E, rows)
+    for name, v in (("ids", ids), ("w", w), ("counts", counts), ("offsets", offsets), ("perm", perm), ("inv_perm", inv)):
+        getattr(r, name).copy_(torch.from_numpy(np.ascontiguousarray(v)))
+    r.block_map[:len(tiles)] = torch.from_numpy(tiles.astype(np.int32)).cuda()
+    r.num_blocks.fill_(len(tiles))
+    return r
+
+
+def _draw_routing(rng, T, E, k, rows, hot=0.0):
+    """Distinct experts per token; with `hot` some experts are far more popular."""
+    p = rng.random((T, E)) + hot * (np.arange(E) < max(1, E // 8))
+    ids = np.argsort(-p, axis=1)[:, :k]
+    w = rng.random((T, k)).astype(np.float32)
+    w /= w.sum(1, keepdims=True)
+    return ids, w, _routing(ids, w, E, rows)
+
+
+def _assert_layer(y, want, I):
+    y = y.double().cpu().numpy()
+    assert np.isfinite(y).all()
+    rel = np.linalg.norm(y - want) / np.linalg.norm(want)
+    rms = np.linalg.norm(want) / np.sqrt(want.size)
+    assert rel < 3e-3, rel
+    assert (np.abs(y - want) <= 2.0 ** -8 * np.abs(want) + 3 / np.sqrt(I) * rms).all()
+
+
+LAYERS = [(1, 256, 96, 0, 8, 2, 16), (1, 2048, 512, 512, 16, 8, 16), (2, 256, 128, 64, 4, 1, 16), (3, 288, 160, 32, 6, 6, 1),
+          (8, 512, 256, 512, 32, 4, 16), (9, 512, 256, 128, 32, 4, 16), (37, 704, 352, 0, 12, 3, 48), (64, 256, 704, 96, 8, 2, 32),
+          (130, 512, 128, 256, 4, 2, 128), (300, 256, 256, 0, 64, 8, 33), (517, 384, 224, 224, 5, 2, 96)]
+
+
+@pytest.mark.parametrize("T,d,I,I_shared,E,k,rows", LAYERS)
+@pytest.mark.parametrize("quantised", [False, True])
+def test_forward(T, d, I, I_shared, E, k, rows, quantised):
+    rng = np.random.default_rng(T + d + I)
+    ids, w, r = _draw_routing(rng, T, E, k, rows, hot=0.5)
+    routed_host, routed = _experts(rng, E, d, I)
+    shared_host, shared = _experts(rng, 1, d, I_shared) if I_shared else (None, None)
+    x = _to(rng.standard_normal((T, d)), "bf16")
+    v, s = blk_ref.quantise(x.double().cpu().numpy())
+    ws = bm.workspace(bm.moe_blk_forward_workspace_bytes(T, d, I, E, k, I_shared, rows))
+    y = torch.full((T + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):                                               # the workspace is ready for the next call
+        bm.moe_blk_forward(_act(v, s) if quantised else x, routed, shared, r, y[:T], ws)
+    assert bm.moe_check_status(ws) == 0
+    assert (y[T] == 7).all()
+    _assert_layer(y[:T], blk_ref.layer(v * blk_ref.spread(s, d), routed_host, shared_host, ids, w.astype(np.float64)), I)
+
+
+def test_forward_with_experts_that_nobody_takes_and_one_that_all_take():
+    rng = np.random.default_rng(8)
+    T, d, I, E, k, rows = 100, 256, 128, 9, 2, 32
+    ids = np.stack([np.full(T, 4), np.where(np.arange(T) % 2, 0, 8)], 1)
+    w = rng.random((T, k)).astype(np.float32)
+    w[3] = 0
+    r = _routing(ids, w, E, rows)
+    host, routed = _experts(rng, E, d, I)
+    x = _to(rng.standard_normal((T, d)), "bf16")
+    x[5] = 0
+    ws = bm.workspace(bm.moe_blk_forward_workspace_bytes(T, d, I, E, k, 0, rows))
+    y = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    bm.moe_blk_forward(x, routed, None, r, y, ws)
+    assert bm.moe_check_status(ws) == 0
+    assert not y[3].any() and not y[5].any()
+    _assert_layer(y, blk_ref.layer(blk_ref.rounded(x.double().cpu().numpy()), host, None, ids, w.astype(np.float64)), I)
