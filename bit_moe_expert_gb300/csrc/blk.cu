@@ -368,6 +368,90 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// ------------------------------------------------------------------ scatter to the routing's rows
+// X's rows quantised once (or taken as they are) and written to the rows of their
+// assignments: one CTA per token, a warp per 256 columns.  Where the kernel before
+// this one is the routing, which let this one start after its own wait, X is there
+// already and is read while the routing runs.
+template <bool kCodes>
+__global__ void __launch_bounds__(kThreads)
+    blk_scatter_kernel(const BlkX x, int d, const MxScatter s, int pitch, uint8_t* __restrict__ q, float* __restrict__ sx) {
+  __shared__ long long s_row[kMaxK + 1];    // destination rows of the codes, -1: none
+  __shared__ long long s_scale[kMaxK + 1];  // place of the first block's scale
+  if (!s.x_ready) pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int blocks = blk_count(d);
+  const int t = blockIdx.x;
+  const int n = s.k + (s.shared_rows > 0 ? 1 : 0);
+  int c = (threadIdx.x >> 5) * 256 + 8 * lane;
+  uint2 code;
+  float scale;
+  auto take = [&]() {
+    if constexpr (kCodes) {
+      code = c < d ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(x.x) + static_cast<size_t>(t) * d + c))
+                   : make_uint2(0, 0);
+      scale = c < d ? __ldg(x.s + static_cast<size_t>(c / kBlk) * x.pitch + t) : 0.0f;
+    } else {
+      Load8<kBf16> v;
+      if (c < d) v.load(static_cast<const uint16_t*>(x.x) + static_cast<size_t>(t) * d, c); else v.zero();
+      float f[8];
+      v.floats(f);
+      scale = blk_scale(half_warp_max(largest_bits(f)));
+      code = blk_codes8(f, blk_inverse(scale));
+    }
+  };
+  take();
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int j = threadIdx.x >> 5; j < n; j += kThreads / 32) {
+    long long to = -1, at = 0;
+    if (j == s.k) {
+      to = static_cast<long long>(s.T) * s.k + t;
+      at = static_cast<long long>(s.max_blocks + t / s.shared_rows) * blocks * pitch + t % s.shared_rows;
+    } else {
+      // the last tile that starts at or before p, 32 places at a time
+      const int p = __ldg(s.inv_perm + static_cast<size_t>(t) * s.k + j);
+      int lo = 0, n_left = min(max(*s.num_blocks, 0), s.max_blocks);  // among lo .. lo + n_left - 1
+      int first = -1;
+      while (n_left > 0) {
+        const int step = (n_left + 31) / 32;
+        const int i = lane * step;
+        const int v = i < n_left ? __ldg(s.block_map + 3 * static_cast<size_t>(lo + i) + 1) : 0x7FFFFFFF;
+        const int before = __popc(__ballot_sync(0xffffffffu, v <= p));  // the tiles' starts ascend
+        if (before == 0) break;
+        first = __shfl_sync(0xffffffffu, v, before - 1);
+        lo += (before - 1) * step;
+        n_left = step == 1 ? 0 : min(step, n_left - (before - 1) * step);
+      }
+      const int r = first >= 0 ? p - first : -1;
+      if (p >= 0 && p < s.T * s.k && r >= 0 && r < pitch && lo < s.max_blocks) {
+        to = p;
+        at = static_cast<long long>(lo) * blocks * pitch + r;
+      } else if (lane == 0) {
+        record_status(s.status, MOE_ERR_INVALID_ARG);
+      }
+    }
+    if (lane == 0) {
+      s_row[j] = to;
+      s_scale[j] = at;
+    }
+  }
+  __syncthreads();
+  for (int base = 0; base < d; base += 8 * kThreads) {
+    if (base > 0) {
+      c += 8 * kThreads;
+      take();
+    }
+    if (c - 8 * lane >= d) break;  // the same for the whole warp
+    if (c >= d) continue;
+    for (int j = 0; j < n; ++j) {
+      if (s_row[j] < 0) continue;
+      *reinterpret_cast<uint2*>(q + static_cast<size_t>(s_row[j]) * d + c) = code;
+      if ((lane & 15) == 0) sx[s_scale[j] + static_cast<size_t>(c / kBlk) * pitch] = scale;
+    }
+  }
+}
+
 template <typename... P, typename... A>
 cudaError_t launch(int kind, void (*kernel)(P...), unsigned grid, int threads, cudaStream_t stream, bool pdl, A... args) {
   cudaLaunchAttribute attr[1];
@@ -444,6 +528,12 @@ cudaError_t launch_blk_dequant_weights(const uint8_t* q, const float* s, int E, 
                       : type == kFp16 ? blk_dequant_weights_kernel<kFp16>
                                       : blk_dequant_weights_kernel<kFp32>;
   return launch(kKBlkQuantize, kernel, static_cast<unsigned>(grid), kThreads, stream, pdl, q, s, N, K, W);
+}
+
+cudaError_t launch_blk_scatter(const BlkX& x, int d, const MxScatter& s, int pitch, uint8_t* q, float* sx,
+                               cudaStream_t stream, bool pdl) {
+  return launch(kKBlkQuantize, x.type == kBlkCodes ? blk_scatter_kernel<true> : blk_scatter_kernel<false>,
+                static_cast<unsigned>(s.T), kThreads, stream, pdl, x, d, s, pitch, q, sx);
 }
 
 cudaError_t launch_rmsnorm(const RmsNorm& n, cudaStream_t stream, bool pdl) {

@@ -56,28 +56,69 @@ moe_status few_linear(const BlkX& x, int M, const moe_blk_mat* W, int N, int K, 
   return done(launch_blk_few_linear(a, cuda(stream), pdl_enabled()));
 }
 
-moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type, uint32_t*,
-                  moe_stream stream) {
-  return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
+int round16(int x) { return (x + 15) & ~15; }
+
+moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
+                  uint32_t* status, moe_stream stream) {
+  if (M <= kBlkFewT) return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
+  BlkLinearArgs a{};
+  a.sw = W->s;
+  a.sx = A.s;
+  a.y = Y;
+  a.status = status;
+  a.sx_pitch = blk_scale_rows(M);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.y_type = y_type;
+  a.num_sms = device_sms();
+  if (a.num_sms <= 0) return MOE_ERR_CUDA;
+  a.bn = M >= 128 ? 128 : round16(M);
+  BlkLinearMaps maps;
+  if (!encode_mx_weights(&maps.w, W->q, 1, N, K, kBlk) || !encode_mx_codes(&maps.x, A.q, M, K, a.bn)) return MOE_ERR_CUDA;
+  return done(launch_blk_linear(a, maps, cuda(stream), pdl_enabled()));
+}
+
+// Tile heights of an expert call in MMA columns.
+int routed_rows(int block_rows) { return round16(block_rows); }
+int shared_tile_rows(int T, int block_rows) {
+  const int rows = routed_rows(block_rows), most = round16(T < 1 ? 1 : T);
+  return most < rows ? most : rows;
 }
 
 struct ExpertLayout {
-  size_t h, ypart, total;
-  int max_blocks;
+  size_t h, q_x, sx, h_r, h_s, sh_r, sh_s, ypart, total;
+  int max_blocks, bn_r, bn_s, pitch;
+  bool few;  // the products for few tokens
 };
 
 ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
   ExpertLayout L{};
   L.max_blocks = moe_route_max_blocks(T, E, k, block_rows);
+  L.bn_r = routed_rows(block_rows);
+  L.bn_s = shared_tile_rows(T, block_rows);
+  L.pitch = L.bn_r > L.bn_s ? L.bn_r : L.bn_s;
   const size_t A = static_cast<size_t>(T) * k, rows = A + (I_shared > 0 ? T : 0);
+  const size_t tiles_s = I_shared > 0 ? (T + L.bn_s - 1) / L.bn_s : 0;
   size_t o = sizeof(WsHeader);
   auto take = [&o](size_t bytes) {
     const size_t at = o;
     o = round256(o + bytes);
     return at;
   };
+  L.few = T <= kBlkFewT;
   L.ypart = take(rows * d * 4);
-  L.h = take(rows * (I > I_shared ? I : I_shared) * 4);
+  if (L.few) {
+    L.h = take(rows * (I > I_shared ? I : I_shared) * 4);
+    L.total = o;
+    return L;
+  }
+  L.q_x = take(rows * d);
+  L.sx = take((L.max_blocks + tiles_s) * blk_count(d) * L.pitch * 4);
+  L.h_r = take(A * I);
+  L.h_s = take(static_cast<size_t>(T) * I_shared);
+  L.sh_r = take(static_cast<size_t>(L.max_blocks) * blk_count(I) * L.pitch * 4);
+  L.sh_s = take(tiles_s * blk_count(I_shared) * L.pitch * 4);
   L.total = o;
   return L;
 }
@@ -119,35 +160,86 @@ BlkWeights weights(const moe_blk_experts* ex) {
 
 moe_status forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I, int k, const moe_blk_experts* routed,
                    const moe_blk_experts* shared, int I_shared, const moe_routing* r, uint16_t* Y, void* ws,
-                   moe_stream stream) {
+                   bool after_routing, moe_stream stream) {
   if (T == 0) return MOE_OK;
   const int E = routed->n_experts;
   const ExpertLayout L = expert_layout(T, d, I, E, k, I_shared, r->block_rows);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  BlkFewArgs a{};
-  a.x = X ? BlkX{X, nullptr, d, 0, MOE_BF16} : BlkX{XQ->q, XQ->s, d, blk_scale_rows(T), kBlkCodes};
-  a.routed = weights(routed);
-  a.shared = weights(shared);
-  a.perm = r->perm;
-  a.inv_perm = r->inv_perm;
+  uint32_t* status = &static_cast<WsHeader*>(ws)->status;
+  const int num_sms = device_sms();
+  if (num_sms <= 0) return MOE_ERR_CUDA;
+  const BlkX x = X ? BlkX{X, nullptr, d, 0, MOE_BF16} : BlkX{XQ->q, XQ->s, d, blk_scale_rows(T), kBlkCodes};
+  if (L.few) {
+    BlkFewArgs a{};
+    a.x = x;
+    a.routed = weights(routed);
+    a.shared = weights(shared);
+    a.perm = r->perm;
+    a.inv_perm = r->inv_perm;
+    a.block_map = r->block_map;
+    a.num_blocks = r->num_blocks;
+    a.w = r->w;
+    a.h = reinterpret_cast<float*>(w + L.h);
+    a.ypart = reinterpret_cast<float*>(w + L.ypart);
+    a.y = Y;
+    a.status = status;
+    a.T = T;
+    a.d = d;
+    a.I = I;
+    a.k = k;
+    a.I_shared = I_shared;
+    a.E = E;
+    a.tiles = T * k < L.max_blocks ? T * k : L.max_blocks;
+    a.rows = r->block_rows;
+    a.num_sms = num_sms;
+    return done(launch_blk_few_experts(a, cuda(stream), pdl_enabled()));
+  }
+
+  const long long A = static_cast<long long>(T) * k, rows = A + (shared ? T : 0);
+  BlkExpertArgs a{};
   a.block_map = r->block_map;
   a.num_blocks = r->num_blocks;
+  a.inv_perm = r->inv_perm;
   a.w = r->w;
-  a.h = reinterpret_cast<float*>(w + L.h);
+  a.routed = weights(routed);
+  a.shared = weights(shared);
+  a.sx = reinterpret_cast<float*>(w + L.sx);
+  a.sh_r = reinterpret_cast<float*>(w + L.sh_r);
+  a.sh_s = reinterpret_cast<float*>(w + L.sh_s);
+  a.h_r = w + L.h_r;
+  a.h_s = w + L.h_s;
   a.ypart = reinterpret_cast<float*>(w + L.ypart);
   a.y = Y;
-  a.status = &static_cast<WsHeader*>(ws)->status;
+  a.status = status;
   a.T = T;
   a.d = d;
   a.I = I;
   a.k = k;
   a.I_shared = I_shared;
   a.E = E;
-  a.tiles = T * k < L.max_blocks ? T * k : L.max_blocks;
-  a.rows = r->block_rows;
-  a.num_sms = device_sms();
-  if (a.num_sms <= 0) return MOE_ERR_CUDA;
-  return done(launch_blk_few_experts(a, cuda(stream), pdl_enabled()));
+  a.num_sms = num_sms;
+  a.max_blocks = L.max_blocks;
+  a.bn_r = L.bn_r;
+  a.bn_s = L.bn_s;
+  a.pitch = L.pitch;
+  BlkExpertMaps maps;
+  bool ok = encode_mx_weights(&maps.gate_r, routed->gate.q, E, I, d, kBlk) &&
+            encode_mx_weights(&maps.up_r, routed->up.q, E, I, d, kBlk) &&
+            encode_mx_weights(&maps.down_r, routed->down.q, E, d, I, kBlk) &&
+            encode_mx_codes(&maps.x_r, w + L.q_x, rows, d, L.bn_r) && encode_mx_codes(&maps.h_r, a.h_r, A, I, L.bn_r);
+  if (shared) {
+    ok = ok && encode_mx_weights(&maps.gate_s, shared->gate.q, 1, I_shared, d, kBlk) &&
+         encode_mx_weights(&maps.up_s, shared->up.q, 1, I_shared, d, kBlk) &&
+         encode_mx_weights(&maps.down_s, shared->down.q, 1, d, I_shared, kBlk) &&
+         encode_mx_codes(&maps.x_s, w + L.q_x, rows, d, L.bn_s) && encode_mx_codes(&maps.h_s, a.h_s, T, I_shared, L.bn_s);
+  } else {  // never read
+    maps.gate_s = maps.up_s = maps.down_s = maps.gate_r;
+    maps.x_s = maps.h_s = maps.x_r;
+  }
+  if (!ok) return MOE_ERR_CUDA;
+  const MxScatter sc{r->inv_perm, r->block_map, r->num_blocks, status, T, k, L.max_blocks, shared ? L.bn_s : 0, after_routing};
+  if (launch_blk_scatter(x, d, sc, L.pitch, w + L.q_x, a.sx, cuda(stream), pdl_enabled()) != cudaSuccess) return MOE_ERR_CUDA;
+  return done(launch_blk_experts(a, maps, cuda(stream), pdl_enabled()));
 }
 
 }  // namespace
@@ -212,7 +304,7 @@ moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long lo
   if (T == 0) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
   const moe_blk_mat xq{w, reinterpret_cast<float*>(w + round256(static_cast<size_t>(T) * K))};
-  if (T <= 8) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
+  if (T <= kBlkFewT) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
   if (launch_blk_quantize(X, x_type, T, K, ldx, xq.q, xq.s, cuda(stream), pdl_enabled()) != cudaSuccess) return MOE_ERR_CUDA;
   return matmul(xq, T, W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
 }
@@ -267,7 +359,7 @@ moe_status moe_blk_forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int 
   if (T > 0 && (!r->w || !r->perm || !r->inv_perm || !r->block_map || !r->num_blocks)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, moe_blk_forward_workspace_bytes(T, d, I, routed->n_experts, k, I_shared, r->block_rows)))
     return MOE_ERR_WORKSPACE;
-  return forward(X, XQ, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
+  return forward(X, XQ, T, d, I, k, routed, shared, I_shared, r, Y, ws, false, stream);
 }
 
 size_t moe_blk_layer_workspace_bytes(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
@@ -290,7 +382,7 @@ moe_status moe_blk_layer(const float* logits, const moe_scoring* scoring, const 
   // one header for both, and after it the same room: the products start when the routing has completed
   st = route_scored(logits, scoring, T, E, k, block_rows, r, ws, stream);
   if (st != MOE_OK) return st;
-  return forward(X, XQ, T, d, I, k, routed, shared, I_shared, r, Y, ws, stream);
+  return forward(X, XQ, T, d, I, k, routed, shared, I_shared, r, Y, ws, true, stream);
 }
 
 }  // extern "C"

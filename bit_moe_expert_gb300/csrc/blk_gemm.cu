@@ -1,0 +1,666 @@
+// Block-scaled 8-bit products on the tensor cores: dense (Y = A W^T) and the
+// expert layer's grouped gate/up and down products.
+//
+// D[n][m] = sum_kb sw[kb] sa[m][kb] sum_{k in kb} w[n][k] a[m][k]: a scale holds for
+// 128 columns, so tcgen05.mma (kind::f8f6f4, E4M3, fp32) adds up one block of 128
+// columns into an accumulator of its own, and warps with the running sums in
+// registers read it, multiply it by the two scales' product and add it (packed fp32
+// operations) while the next blocks multiply into other accumulators.  The scales
+// are any fp32 numbers; nothing of them reaches the tensor cores.
+//
+// The weights are the M = 128 side (a tile's rows share their scale) and the tokens
+// the N side: an expert with few tokens streams its weights once and pads only
+// tokens, and the epilogues have neighbouring columns of a row in neighbouring
+// lanes.  A stage of the pipeline is K = 128: one 128-byte line of codes a row (the
+// widest swizzle atom) and the tokens' scales, four MMAs of K = 32.
+//
+// Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
+// activations' loads, warp 2 the MMAs' issue, warps 4 to 11 the sums: two per
+// quarter of the tensor-memory lanes, the tokens' groups in turn.  Every wait is
+// bounded and records MOE_ERR_TIMEOUT.
+#include <cuda_runtime.h>
+
+#include "blk.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace bm {
+namespace {
+
+enum Mode { kLinear, kGateUp, kDown };
+
+constexpr int kWeightsWarp = 0;
+constexpr int kActivationsWarp = 1;
+constexpr int kMmaWarp = 2;
+constexpr int kSumWarp0 = 4;
+constexpr int kSumWarps = 8;
+constexpr int kParts = kSumWarps / 4;  // shares of the tokens
+constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxStages = 12;
+constexpr int kMaxAccs = 8;
+constexpr int kMatBytes = kBlk * 128;  // one matrix's codes of a stage
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kEntries = 256;          // items of a CTA, from its first, whose Entry is in shared memory
+constexpr int kMaxTile = 128;          // tokens of a tile
+constexpr int kSmemFixed = 1024 /* barriers */ + 16 * kEntries + 2 * 4 * 4 * kMaxTile /* maxima */ + 1024 /* alignment */;
+
+// A launch's variant; kBN: tokens of a tile at most, which the sums' registers are for.
+template <int kMode_, int kBN_>
+struct Variant {
+  static constexpr int kMode = kMode_, kBN = kBN_;
+  static constexpr int kMats = kMode == kGateUp ? 2 : 1;
+  static constexpr int kGroup = kBN == 16 ? 8 : 16;                // tokens that a warp takes at a time
+  static constexpr int kGroups = kBN / (kGroup * kParts);          // of a warp
+  // gate and up sums of 64 tokens take 128 registers: more than 384 threads' equal share, less than is left when
+  // the other four warps give theirs up (128 x 72 + 256 x 216 = 384 x 168)
+  static constexpr bool kUneven = kMats * kBN > 128;
+};
+
+// How a launch divides shared and tensor memory; bn: the tiles' height in columns.
+struct Plan {
+  int bn, stages, stage_bytes, accs, scale_slots;
+};
+Plan make_plan(int mats, int bn) {
+  Plan p;
+  p.bn = bn;
+  p.accs = static_cast<int>(kTmemCols) / (mats * bn);
+  if (p.accs > kMaxAccs) p.accs = kMaxAccs;
+  p.stage_bytes = mats * kMatBytes + bn * 128;
+  for (p.stages = kMaxStages;; --p.stages) {
+    // the scales of a block are read until its accumulator is free again, which may be `accs` stages after the
+    // stage's codes: a ring of their own
+    p.scale_slots = p.stages + p.accs;
+    if (p.stages * p.stage_bytes + p.scale_slots * bn * 4 + kSmemFixed <= kSmemLimit) return p;
+  }
+}
+int plan_smem(const Plan& p) { return p.stages * p.stage_bytes + p.scale_slots * p.bn * 4 + kSmemFixed; }
+
+struct Item {
+  const CUtensorMap *m0, *m1, *n;  // codes of the weights (one or two matrices) and of the tokens
+  const float *s0, *s1, *sn;       // scales: of the weight tile (a block after another), of the tokens' first block
+  long long sn_step;               // from a block's scales of the tokens to the next one's
+  uint32_t sn_bytes;
+  int e, row_m, row_n;             // matrix of the M side; first rows of the codes
+  int mt, rows, K, box;            // M tile, valid tokens, depth, tokens that the TMA box brings
+  int row0, slot;                  // experts: first row among the assignments (or tokens), tile slot
+  bool shared, ok;
+};
+
+// This CTA's items: local index i stands for item first + i * step.
+struct Sched {
+  int mt_r, mt_s;  // M tiles of a routed and of a shared tile
+  int n_routed;    // expert products: items below are routed
+  int first, n, step;
+};
+struct Entry {
+  int e, row0;    // expert (-1: malformed) and first row; dense: 0 and the M tile
+  int slot;       // entry of the block map, the shared expert's tile of tokens, or the dense product's N tile
+  uint32_t what;  // experts: M tile + 2^16 rows + 2^31 for the shared expert
+};
+constexpr uint32_t kEntryShared = 1u << 31;
+static_assert(kBlkMaxCols / kBlk <= 1 << 16 && kMaxTile < 1 << 15, "an Entry's M tile and rows");
+
+template <int kMode>
+struct Args {
+  using type = BlkExpertArgs;
+  using maps = BlkExpertMaps;
+};
+template <>
+struct Args<kLinear> {
+  using type = BlkLinearArgs;
+  using maps = BlkLinearMaps;
+};
+
+__device__ __forceinline__ Sched make_sched(const BlkLinearArgs& a, const Plan& p, bool) {
+  Sched s{};
+  s.mt_r = blk_count(a.N);
+  const int total = s.mt_r * ((a.M + p.bn - 1) / p.bn);
+  s.first = blockIdx.x;
+  s.step = gridDim.x;
+  s.n = (total - s.first + s.step - 1) / s.step;
+  return s;
+}
+__device__ __forceinline__ Entry make_entry(const BlkLinearArgs&, const Sched& s, int it) {
+  return Entry{0, it % s.mt_r, it / s.mt_r, 0};
+}
+__device__ __forceinline__ Item get_item(const BlkLinearArgs& a, const BlkLinearMaps& maps, const Plan& p, const Entry& en,
+                                         bool) {
+  Item m{};
+  m.mt = en.row0;
+  m.m0 = &maps.w;
+  m.n = &maps.x;
+  m.row_m = m.mt * kBlk;
+  m.row_n = en.slot * p.bn;
+  m.rows = min(p.bn, a.M - m.row_n);
+  m.K = a.K;
+  m.box = p.bn;
+  m.s0 = a.sw + static_cast<size_t>(m.mt) * blk_count(a.K);
+  m.sn = a.sx + m.row_n;
+  m.sn_step = a.sx_pitch;
+  m.sn_bytes = 4 * static_cast<uint32_t>(min(static_cast<long long>(p.bn), a.sx_pitch - m.row_n));
+  m.ok = true;
+  return m;
+}
+
+__device__ __forceinline__ Sched make_sched(const BlkExpertArgs& a, const Plan&, bool gate_up) {
+  Sched s{};
+  int nb = *reinterpret_cast<const volatile int32_t*>(a.num_blocks);
+  if (nb < 1 || nb > min(a.max_blocks, a.T * a.k)) {  // every tile holds an assignment
+    if (threadIdx.x == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
+    nb = 0;
+  }
+  s.mt_r = blk_count(gate_up ? a.I : a.d);
+  s.mt_s = blk_count(gate_up ? a.I_shared : a.d);
+  s.n_routed = nb * s.mt_r;
+  const int total = s.n_routed + (a.I_shared > 0 ? (a.T + a.bn_s - 1) / a.bn_s * s.mt_s : 0);
+  s.first = blockIdx.x;
+  s.step = gridDim.x;
+  s.n = (total - s.first + s.step - 1) / s.step;
+  return s;
+}
+__device__ __forceinline__ Entry make_entry(const BlkExpertArgs& a, const Sched& s, int it) {
+  Entry en;
+  if (it < s.n_routed) {
+    en.slot = it / s.mt_r;
+    const volatile int32_t* b = a.block_map + 3 * static_cast<size_t>(en.slot);
+    en.e = b[0];
+    en.row0 = b[1];
+    const int rows = b[2];
+    const bool ok = en.e >= 0 && en.e < a.E && rows >= 1 && rows <= a.bn_r && en.row0 >= 0 &&
+                    en.row0 <= a.T * a.k - rows;
+    if (!ok) en.e = -1;
+    en.what = static_cast<uint32_t>(it - en.slot * s.mt_r) | static_cast<uint32_t>(rows) << 16;
+  } else {
+    const int j = it - s.n_routed;
+    en.slot = j / s.mt_s;
+    en.e = 0;
+    en.row0 = en.slot * a.bn_s;
+    en.what = kEntryShared | static_cast<uint32_t>(j - en.slot * s.mt_s) |
+              static_cast<uint32_t>(min(a.bn_s, a.T - en.row0)) << 16;
+  }
+  return en;
+}
+__device__ __forceinline__ Item get_item(const BlkExpertArgs& a, const BlkExpertMaps& maps, const Plan&, const Entry& en,
+                                         bool gate_up) {
+  Item m{};
+  m.ok = en.e >= 0;
+  if (!m.ok) return m;
+  m.e = en.e;
+  m.row0 = en.row0;
+  m.rows = static_cast<int>(en.what >> 16 & 0x7FFFu);
+  m.shared = (en.what & kEntryShared) != 0;
+  m.mt = static_cast<int>(en.what & 0xFFFFu);
+  m.slot = en.slot;
+  const int I = m.shared ? a.I_shared : a.I;
+  const int N = gate_up ? I : a.d;
+  m.K = gate_up ? a.d : I;
+  m.box = m.shared ? a.bn_s : a.bn_r;
+  const BlkWeights& w = m.shared ? a.shared : a.routed;
+  if (m.shared) {
+    m.m0 = gate_up ? &maps.gate_s : &maps.down_s;
+    m.m1 = &maps.up_s;
+    m.n = gate_up ? &maps.x_s : &maps.h_s;
+    m.row_n = gate_up ? a.T * a.k + m.row0 : m.row0;
+  } else {
+    m.m0 = gate_up ? &maps.gate_r : &maps.down_r;
+    m.m1 = &maps.up_r;
+    m.n = gate_up ? &maps.x_r : &maps.h_r;
+    m.row_n = m.row0;
+  }
+  const int blocks = blk_count(m.K);
+  const size_t tile = (static_cast<size_t>(m.e) * blk_count(N) + m.mt) * blocks;
+  m.s0 = (gate_up ? w.s_gate : w.s_down) + tile;
+  m.s1 = w.s_up + tile;
+  m.row_m = m.mt * kBlk;
+  const float* sn = gate_up ? a.sx : (m.shared ? a.sh_s : a.sh_r);
+  m.sn = sn + static_cast<size_t>(gate_up && m.shared ? a.max_blocks + m.slot : m.slot) * blocks * a.pitch;
+  m.sn_step = a.pitch;
+  m.sn_bytes = 4 * static_cast<uint32_t>(m.box);
+  return m;
+}
+
+__device__ __forceinline__ int tile_n(int rows) { return (rows + 15) & ~15; }
+
+// Two fp32 numbers in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
+template <int n>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[n]) {
+  if constexpr (n == 8) tmem_ld8(taddr, v); else tmem_ld16(taddr, v);
+}
+
+// A warp's sums: two tokens to a register pair, for each of its groups.
+template <typename V>
+struct Sums {
+  uint64_t v[V::kMats][V::kGroups][V::kGroup / 2];
+  __device__ __forceinline__ float get(int mat, int g, int c) const {
+    float lo, hi;
+    unpack2(v[mat][g][c >> 1], lo, hi);
+    return c & 1 ? hi : lo;
+  }
+};
+
+// Four bytes of four lanes (4i .. 4i+3), byte j of lane i to byte i of lane j.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t v, int lane) {
+  uint32_t t = __shfl_xor_sync(0xffffffffu, v, 2);
+  v = (lane & 2) ? __byte_perm(v, t, 0x3276) : __byte_perm(v, t, 0x5410);
+  t = __shfl_xor_sync(0xffffffffu, v, 1);
+  return (lane & 1) ? __byte_perm(v, t, 0x3715) : __byte_perm(v, t, 0x6240);
+}
+
+// gate/up: h = silu(gate) up, quantised here.  A tile's 128 columns are one block
+// of h: a token's largest magnitude is a reduction over the lanes and the share's
+// four warps.  meet(): waits for those (false: given up).
+template <typename V, typename Meet>
+__device__ __forceinline__ bool epilogue(const BlkExpertArgs& a, const Item& m, Sums<V>& acc, int quarter, int part, int lane,
+                                         uint32_t (*maxima)[kMaxTile], Meet meet) {
+  if constexpr (V::kMode == kGateUp) {
+    const int I = m.shared ? a.I_shared : a.I;
+    const int n0 = m.mt * kBlk + 32 * quarter;
+#pragma unroll
+    for (int g = 0; g < V::kGroups; ++g) {
+      const int c0 = V::kGroup * (g * kParts + part);
+      if (c0 >= m.rows) break;
+      uint32_t most = 0;
+#pragma unroll
+      for (int c = 0; c < V::kGroup; c += 2) {  // h takes gate's place
+        const uint32_t h0 = __float_as_uint(blk_swiglu(acc.get(0, g, c), acc.get(V::kMats - 1, g, c)));
+        const uint32_t h1 = __float_as_uint(blk_swiglu(acc.get(0, g, c + 1), acc.get(V::kMats - 1, g, c + 1)));
+        acc.v[0][g][c >> 1] = pack2(h0, h1);
+        const uint32_t x0 = __reduce_max_sync(0xffffffffu, h0 & 0x7FFFFFFFu), x1 = __reduce_max_sync(0xffffffffu, h1 & 0x7FFFFFFFu);
+        if (lane == c) most = x0;
+        if (lane == c + 1) most = x1;
+      }
+      if (lane < V::kGroup) maxima[quarter][c0 + lane] = most;
+    }
+    if (!meet()) return false;
+    uint8_t* hq = (m.shared ? a.h_s : a.h_r) + static_cast<size_t>(m.row0) * I + n0 + 4 * (lane >> 2);
+    float* hs = (m.shared ? a.sh_s : a.sh_r) + (static_cast<size_t>(m.slot) * blk_count(I) + m.mt) * a.pitch;
+    const bool valid = n0 + 4 * (lane >> 2) < I;
+#pragma unroll
+    for (int g = 0; g < V::kGroups; ++g) {
+      const int c0 = V::kGroup * (g * kParts + part);
+      if (c0 >= m.rows) break;
+      float inv = 0.0f;  // of token c0 + lane
+      if (lane < V::kGroup) {
+        const int c = c0 + lane;
+        const float s = blk_scale(max(max(maxima[0][c], maxima[1][c]), max(maxima[2][c], maxima[3][c])));
+        inv = blk_inverse(s);
+        if (quarter == 0 && c < m.rows) hs[c] = s;
+      }
+#pragma unroll
+      for (int c = 0; c < V::kGroup; c += 4) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = acc.get(0, g, c + i) * __shfl_sync(0xffffffffu, inv, c + i);
+        const uint32_t code = transpose_bytes(f32x4_to_e4m3x4(f[0], f[1], f[2], f[3]), lane);
+        const int r = c0 + c + (lane & 3);
+        if (r < m.rows && valid) *reinterpret_cast<uint32_t*>(hq + static_cast<size_t>(r) * I) = code;
+      }
+    }
+  } else {
+    // fp32 rows of the experts' outputs, routed ones in permuted order, then the shared expert's in token order
+    const int n = m.mt * kBlk + 32 * quarter + lane;
+    if (n >= a.d) return true;
+    float* y = a.ypart + (static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0) * a.d + n;
+#pragma unroll
+    for (int g = 0; g < V::kGroups; ++g) {
+      const int c0 = V::kGroup * (g * kParts + part);
+#pragma unroll
+      for (int c = 0; c < V::kGroup; ++c)
+        if (c0 + c < m.rows) y[static_cast<size_t>(c0 + c) * a.d] = acc.get(0, g, c);
+    }
+  }
+  return true;
+}
+template <typename V, typename Meet>
+__device__ __forceinline__ bool epilogue(const BlkLinearArgs& a, const Item& m, Sums<V>& acc, int quarter, int part, int lane,
+                                         uint32_t (*)[kMaxTile], Meet) {
+  const int n = m.row_m + 32 * quarter + lane;
+  if (n >= a.N) return true;
+#pragma unroll
+  for (int g = 0; g < V::kGroups; ++g) {
+    const int c0 = V::kGroup * (g * kParts + part);
+#pragma unroll
+    for (int c = 0; c < V::kGroup; ++c)
+      if (c0 + c < m.rows) store1(a.y_type, a.y, (static_cast<size_t>(m.row_n) + c0 + c) * a.N + n, acc.get(0, g, c));
+  }
+  return true;
+}
+
+template <typename V>
+__global__ void __launch_bounds__(kThreads, 1)
+    blk_gemm_kernel(const __grid_constant__ typename Args<V::kMode>::maps maps,
+                    const __grid_constant__ typename Args<V::kMode>::type a, const Plan p) {
+  constexpr int kMats = V::kMats;
+  constexpr bool kGU = V::kMode == kGateUp;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* scales = reinterpret_cast<float*>(stages + p.stages * p.stage_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + p.scale_slots * p.bn);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* acc_empty = acc_full + kMaxAccs;
+  uint64_t* scale_full = acc_empty + kMaxAccs;
+  uint64_t* part_met = scale_full + kMaxStages + kMaxAccs;  // a share's four warps have written their maxima
+  uint64_t* finished = part_met + kParts;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(finished + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Entry* entries = reinterpret_cast<Entry*>(reinterpret_cast<uint8_t*>(full) + 1024);
+  uint32_t(*maxima)[kMaxTile] = reinterpret_cast<uint32_t(*)[kMaxTile]>(entries + kEntries);  // [2 x 4][tokens]
+
+  // the same in all lanes, so that the roles' branches are known to be uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  // The routing has completed by now (the kernel before this one lets this one
+  // start only after its own wait), so only the activations are waited for.
+  const Sched s = make_sched(a, p, kGU);
+  for (int i = threadIdx.x; i < min(s.n, kEntries); i += kThreads) entries[i] = make_entry(a, s, s.first + i * s.step);
+  auto item = [&](int i) {
+    return get_item(a, maps, p, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 2);  // the weights' and the activations' expect_tx; their bytes complete the phase
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < p.accs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kSumWarps);
+    }
+    for (int i = 0; i < p.scale_slots; ++i) mbar_init(&scale_full[i], 1);
+    for (int i = 0; i < kParts; ++i) mbar_init(&part_met[i], 4);
+    mbar_init(finished, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto fail = [&]() {
+    record_status(a.status, MOE_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp < kSumWarp0) {
+    if constexpr (V::kUneven) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kWeightsWarp || warp == kActivationsWarp) {
+      // one thread for the weights, which starts before the wait, and one for the activations
+      if (lane == 0) {
+        const bool weights = warp == kWeightsWarp;
+        if (!weights) pdl_wait();
+        int stage = 0, slot = 0, filled = 0;
+        uint32_t phase = 0, slot_phase = 0;
+        bool ok = true;
+        for (int i = 0; i < s.n && ok; ++i) {
+          const Item m = item(i);
+          if (!m.ok) continue;
+          const int blocks = blk_count(m.K);
+          const float* sn = m.sn;
+          for (int kb = 0; kb < blocks; ++kb, ++filled) {
+            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+              fail();
+              ok = false;
+              break;
+            }
+            uint8_t* st = stages + stage * p.stage_bytes;
+            uint64_t* bar = &full[stage];
+            if (weights) {
+              mbar_arrive_expect_tx(bar, kMats * kMatBytes);
+              tma_load_3d(st, m.m0, bar, kb * kBlk, m.row_m, m.e);
+              if (kGU) tma_load_3d(st + kMatBytes, m.m1, bar, kb * kBlk, m.row_m, m.e);
+            } else {
+              mbar_arrive_expect_tx(bar, m.box * 128);
+              tma_load_2d(st + kMats * kMatBytes, m.n, bar, kb * kBlk, m.row_n);
+              mbar_arrive_expect_tx(&scale_full[slot], m.sn_bytes);
+              bulk_g2s(scales + slot * p.bn, sn, m.sn_bytes, &scale_full[slot]);
+              sn += m.sn_step;
+              if (++slot == p.scale_slots) {
+                slot = 0;
+                slot_phase ^= 1;
+              }
+            }
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        // never leave while a load into this CTA's shared memory may be in flight
+        for (int i = 0; i < min(filled, p.stages); ++i) {
+          stage = stage == 0 ? p.stages - 1 : stage - 1;
+          if (stage == p.stages - 1) phase ^= 1;
+          if (!mbar_wait(&full[stage], phase, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
+        }
+        for (int i = 0; i < min(filled, p.scale_slots) && !weights; ++i) {
+          slot = slot == 0 ? p.scale_slots - 1 : slot - 1;
+          if (slot == p.scale_slots - 1) slot_phase ^= 1;
+          if (!mbar_wait(&scale_full[slot], slot_phase, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
+        }
+        if (weights) pdl_wait();
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      pdl_wait();
+      pdl_launch_dependents();
+      // One thread issues everything; what it issues is computed by the whole warp
+      // from values that are the same in all lanes, which lets the compiler keep
+      // descriptors and addresses in uniform registers.
+      const uint32_t stage0 = smem_u32(stages);
+      const uint64_t ad0 = smem_desc_sw128_kmajor(stage0);
+      const uint64_t bd0 = smem_desc_sw128_kmajor(stage0 + kMats * kMatBytes);
+      const uint32_t stage_step = static_cast<uint32_t>(p.stage_bytes) >> 4;  // in the descriptors' address fields
+      int stage = 0, accb = 0;
+      uint32_t phase = 0, accphase = 0, at = 0;
+      const bool leader = elect_one();
+      for (int i = 0; i < s.n; ++i) {
+        const Item m = item(i);
+        const int rows = __shfl_sync(0xffffffffu, m.ok ? m.rows : 0, 0);
+        if (rows == 0) continue;
+        const int n32 = (__shfl_sync(0xffffffffu, m.K, 0) + 31) / 32;
+        const uint32_t idesc = idesc_e4m3_f32(kBlk, tile_n(rows));
+        for (int k = 0; k < n32; k += 4) {
+          mbar_wait_issue(&acc_empty[accb], accphase ^ 1, abort_flag, a.status);
+          mbar_wait_issue(&full[stage], phase, abort_flag, a.status);
+          tc_fence_after();
+          const uint64_t ad = ad0 + at, bd = bd0 + at;
+          const uint32_t d = tmem + accb * kMats * p.bn;
+          if (leader) {
+#pragma unroll
+            for (int mat = 0; mat < kMats; ++mat)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kk > 0 && k + kk >= n32) break;
+                tc_mma_f8(d + mat * p.bn, ad + mat * (kMatBytes >> 4) + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              }
+            tc_commit(&empty[stage]);
+            tc_commit(&acc_full[accb]);
+          }
+          at += stage_step;
+          if (++stage == p.stages) {
+            stage = 0;
+            at = 0;
+            phase ^= 1;
+          }
+          if (++accb == p.accs) {
+            accb = 0;
+            accphase ^= 1;
+          }
+        }
+      }
+      // every MMA has completed before tensor memory is released
+      __syncwarp();
+      if (leader) {
+        tc_commit(finished);
+        if (!mbar_wait(finished, 0, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  } else {
+    if constexpr (V::kUneven) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    pdl_wait();
+    pdl_launch_dependents();
+    const int quarter = warp & 3, part = (warp - kSumWarp0) >> 2;
+    int accb = 0, slot = 0;
+    uint32_t accphase = 0, slot_phase = 0, parity = 0;
+    bool ok = true;
+    for (int i = 0; i < s.n && ok; ++i) {
+      const Item m = item(i);
+      if (!m.ok) {
+        if (lane == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
+        continue;
+      }
+      const int blocks = blk_count(m.K);
+      Sums<V> acc;
+#pragma unroll
+      for (int mat = 0; mat < kMats; ++mat)
+#pragma unroll
+        for (int g = 0; g < V::kGroups; ++g)
+#pragma unroll
+          for (int c = 0; c < V::kGroup / 2; ++c) acc.v[mat][g][c] = 0;
+      float sw0 = 0.0f, sw1 = 0.0f;  // the weights' scales of 32 blocks, one a lane
+      for (int kb = 0; kb < blocks; ++kb) {
+        if ((kb & 31) == 0) {
+          sw0 = kb + lane < blocks ? __ldg(m.s0 + kb + lane) : 0.0f;
+          if (kGU) sw1 = kb + lane < blocks ? __ldg(m.s1 + kb + lane) : 0.0f;
+        }
+        if (!mbar_wait(&scale_full[slot], slot_phase, abort_flag) || !mbar_wait(&acc_full[accb], accphase, abort_flag)) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + accb * kMats * p.bn;
+        const float* sn = scales + slot * p.bn;
+        uint64_t w[2];
+        {
+          const uint32_t b0 = __float_as_uint(__shfl_sync(0xffffffffu, sw0, kb & 31));
+          w[0] = pack2(b0, b0);
+          const uint32_t b1 = kGU ? __float_as_uint(__shfl_sync(0xffffffffu, sw1, kb & 31)) : 0u;
+          w[1] = pack2(b1, b1);
+        }
+#pragma unroll
+        for (int g = 0; g < V::kGroups; ++g) {
+          const int c0 = V::kGroup * (g * kParts + part);
+          if (c0 < m.rows) {
+            uint32_t d[kMats][V::kGroup];
+#pragma unroll
+            for (int mat = 0; mat < kMats; ++mat) tmem_ld<V::kGroup>(tbase + mat * p.bn + c0, d[mat]);
+            uint64_t sc[V::kGroup / 2];
+#pragma unroll
+            for (int c = 0; c < V::kGroup / 4; ++c) {
+              const uint4 f = *reinterpret_cast<const uint4*>(sn + c0 + 4 * c);
+              sc[2 * c] = pack2(f.x, f.y);
+              sc[2 * c + 1] = pack2(f.z, f.w);
+            }
+            tc_wait_ld();
+#pragma unroll
+            for (int mat = 0; mat < kMats; ++mat)
+#pragma unroll
+              for (int c = 0; c < V::kGroup / 2; ++c)
+                fma2(acc.v[mat][g][c], pack2(d[mat][2 * c], d[mat][2 * c + 1]), mul2(sc[c], w[mat]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[accb]);
+        if (++slot == p.scale_slots) {
+          slot = 0;
+          slot_phase ^= 1;
+        }
+        if (++accb == p.accs) {
+          accb = 0;
+          accphase ^= 1;
+        }
+      }
+      if (!ok) break;
+      ok = epilogue<V>(a, m, acc, quarter, part, lane, maxima + 4 * parity, [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&part_met[part]);
+        const bool met = mbar_wait(&part_met[part], parity, abort_flag);
+        if (!met && lane == 0) fail();
+        __syncwarp();
+        return met;
+      });
+      parity ^= 1;  // a warp two items ahead has met all the others in between: two sets of maxima are enough
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <typename V>
+cudaError_t launch(int kind, const typename Args<V::kMode>::maps& maps, const typename Args<V::kMode>::type& a, int bn,
+                   int grid, cudaStream_t stream, bool pdl) {
+  const Plan p = make_plan(V::kMats, bn);
+  const int smem = plan_smem(p);
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(blk_gemm_kernel<V>), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  timer_begin(kind, stream);
+  e = cudaLaunchKernelEx(&cfg, blk_gemm_kernel<V>, maps, a, p);
+  timer_end(kind, stream);
+  return e;
+}
+
+// The variant for tiles of bn tokens.
+template <int kMode>
+cudaError_t launch_for(int kind, const typename Args<kMode>::maps& maps, const typename Args<kMode>::type& a, int bn,
+                       int grid, cudaStream_t stream, bool pdl) {
+  if (bn <= 16) return launch<Variant<kMode, 16>>(kind, maps, a, bn, grid, stream, pdl);
+  if (bn <= 32) return launch<Variant<kMode, 32>>(kind, maps, a, bn, grid, stream, pdl);
+  if (bn <= 64) return launch<Variant<kMode, 64>>(kind, maps, a, bn, grid, stream, pdl);
+  return launch<Variant<kMode, 128>>(kind, maps, a, bn, grid, stream, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_blk_linear(const BlkLinearArgs& a, const BlkLinearMaps& maps, cudaStream_t stream, bool pdl) {
+  const long long items = static_cast<long long>(blk_count(a.N)) * ((a.M + a.bn - 1) / a.bn);
+  if (items > (1ll << 30)) return cudaErrorInvalidValue;
+  return launch_for<kLinear>(kKBlkGemm, maps, a, a.bn, static_cast<int>(items < a.num_sms ? items : a.num_sms), stream, pdl);
+}
+
+cudaError_t launch_blk_experts(const BlkExpertArgs& a, const BlkExpertMaps& maps, cudaStream_t stream, bool pdl) {
+  cudaError_t e = launch_for<kGateUp>(kKBlkGateUp, maps, a, a.pitch, a.num_sms, stream, pdl);
+  if (e != cudaSuccess) return e;
+  e = launch_for<kDown>(kKBlkDown, maps, a, a.pitch, a.num_sms, stream, pdl);
+  if (e != cudaSuccess) return e;
+  return launch_mx_combine(a.ypart, a.inv_perm, a.w, a.T, a.d, a.k, a.I_shared > 0, a.y, a.status, a.num_sms, stream);
+}
+
+}  // namespace bm

@@ -364,6 +364,8 @@ struct BlkX {
   long long ldx, pitch;
   int type;
 };
+// Few tokens (an MMA's eight columns): weights straight into the registers of warp-level MMAs.
+constexpr int kBlkFewT = 8;
 struct BlkFewLinearArgs {
   BlkX x;
   const uint8_t* w;
@@ -391,5 +393,46 @@ struct BlkFewArgs {
   int num_sms;
 };
 cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl);
+
+// Tensor-core products.
+struct BlkLinearArgs {
+  const float *sw, *sx;  // scales of the weights, and of the tokens [ceil(K/128)][sx_pitch]
+  void* y;               // [M][N]
+  uint32_t* status;
+  long long sx_pitch;
+  int M, N, K, y_type;
+  int bn;  // height of the tokens' tiles: a multiple of 16 up to 128
+  int num_sms;
+};
+struct BlkLinearMaps {
+  CUtensorMap w;  // codes [1][N][K], box (128 bytes, 128 rows, 1)
+  CUtensorMap x;  // codes [M][K], box (128 bytes, bn rows)
+};
+cudaError_t launch_blk_linear(const BlkLinearArgs& a, const BlkLinearMaps& maps, cudaStream_t stream, bool pdl);
+
+struct BlkExpertArgs {
+  const int32_t *block_map, *num_blocks, *inv_perm;
+  const float* w;              // [T][k]
+  BlkWeights routed, shared;
+  // scales of a tile's tokens, [slot][ceil(columns/128)][pitch]: X's (the shared expert's slots after max_blocks), h's
+  float *sx, *sh_r, *sh_s;
+  uint8_t *h_r, *h_s;          // h's codes [A][I], [T][I_shared]
+  float* ypart;                // [A + T][d]
+  uint16_t* y;                 // [T][d] bf16
+  uint32_t* status;
+  int T, d, I, k, I_shared, E, num_sms, max_blocks;
+  int bn_r, bn_s, pitch;       // tile heights in MMA columns (multiples of 16): routed, shared, the larger
+};
+struct BlkExpertMaps {
+  CUtensorMap gate_r, up_r, down_r, gate_s, up_s, down_s;  // codes [E][N][K], box (128 bytes, 128 rows, 1)
+  CUtensorMap x_r, x_s;        // X's codes [A + T][d], box (128 bytes, bn_r / bn_s rows)
+  CUtensorMap h_r, h_s;        // h's codes
+};
+cudaError_t launch_blk_experts(const BlkExpertArgs& a, const BlkExpertMaps& maps, cudaStream_t stream, bool pdl);
+
+// X's rows, quantised once, to the rows of their assignments; s as for
+// launch_mx_scatter, the scales to [slot][ceil(d/128)][pitch] of sx.
+cudaError_t launch_blk_scatter(const BlkX& x, int d, const MxScatter& s, int pitch, uint8_t* q, float* sx,
+                               cudaStream_t stream, bool pdl);
 
 }  // namespace bm

@@ -297,6 +297,18 @@ __device__ __forceinline__ void tc_mma_mxfp(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (8-bit operands, K = 32, fp32
+// accumulate), both operands by descriptor.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // 512 bytes of shared memory (32 rows of 16 bytes, contiguous) -> four columns
 // of all four 32-lane quarters of tensor memory: the scales of 128 rows x 4
 // blocks.  Ordered before the MMAs that the same thread issues after it.
@@ -452,6 +464,10 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return idesc_f16_f32(M, N) | (1u << 7) | (1u << 10);
 }
+
+// Instruction descriptor, kind::f8f6f4: E4M3 A and B (format code 0, as fp16's in
+// kind::f16), fp32 D, both operands K-major, K = 32.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) { return idesc_f16_f32(M, N); }
 
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
