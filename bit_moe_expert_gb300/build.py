@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libbitmoe.so")
 SOURCES = ["api.cu", "route.cu", "router.cu", "topk_wide.cu", "decode.cu", "gemm.cu", "mx.cu", "mx_gemm.cu",
-           "mx_few.cu", "mx_api.cu", "blk.cu", "blk_few.cu", "blk_gemm.cu", "blk_api.cu", "profile.cu"]
+           "mx_few.cu", "mx_api.cu", "blk.cu", "blk_few.cu", "blk_gemm.cu", "blk_wide.cu", "blk_api.cu", "profile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

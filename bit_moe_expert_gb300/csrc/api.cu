@@ -278,6 +278,16 @@ bool encode_mx_scales(CUtensorMap* map, const uint8_t* sp, long long pieces) {
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, sp, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool encode_out_boxes(CUtensorMap* map, const void* y, int elem_bytes, long long rows, int cols) {
+  if (!get_encoder()) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem_bytes};
+  const cuuint32_t box[2] = {32, 32};
+  return elem_bytes == 4
+             ? encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)
+             : encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 bool pdl_enabled() { return env_flag("MOE_PDL", true); }
 
 int device_sms() { return sm_count(); }

@@ -65,6 +65,24 @@ __device__ __forceinline__ float blk_swiglu(float g, float u) {
   return div_approx(g, 1.0f + exp2_approx(g * -1.44269504f)) * u;
 }
 
+// Two fp32 numbers in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
 // |x| of the largest of the lane's values, as bits; a NaN's are above infinity's.
 template <int n>
 __device__ __forceinline__ uint32_t largest_bits(const float (&f)[n]) {

@@ -58,6 +58,14 @@ moe_status few_linear(const BlkX& x, int M, const moe_blk_mat* W, int N, int K, 
 
 int round16(int x) { return (x + 15) & ~15; }
 
+// Height of the dense product's token tiles.
+int linear_tile(int M, int N, int K, int num_sms) {
+  (void)K;
+  const long long wide = static_cast<long long>((N + 255) / 256) * ((M + 127) / 128);
+  if (2 * wide >= num_sms) return 128;
+  return M <= kBlkNarrow ? round16(M) : kBlkNarrow;
+}
+
 moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
                   uint32_t* status, moe_stream stream) {
   if (M <= kBlkFewT) return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
@@ -73,10 +81,19 @@ moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int 
   a.y_type = y_type;
   a.num_sms = device_sms();
   if (a.num_sms <= 0) return MOE_ERR_CUDA;
-  a.bn = M >= 128 ? 128 : round16(M);
+  a.bn = linear_tile(M, N, K, a.num_sms);
+  const bool wide = a.bn > kBlkNarrow;
   BlkLinearMaps maps;
   if (!encode_mx_weights(&maps.w, W->q, 1, N, K, kBlk) || !encode_mx_codes(&maps.x, A.q, M, K, a.bn)) return MOE_ERR_CUDA;
-  return done(launch_blk_linear(a, maps, cuda(stream), pdl_enabled()));
+  if (!wide) {
+    maps.y = maps.x;  // not read
+    return done(launch_blk_linear(a, maps, cuda(stream), pdl_enabled()));
+  }
+  const int bytes = type_bytes(y_type);
+  a.y_boxed = static_cast<long long>(N) * bytes % 16 == 0;
+  maps.y = maps.x;
+  if (a.y_boxed && !encode_out_boxes(&maps.y, Y, bytes, M, N)) return MOE_ERR_CUDA;
+  return done(launch_blk_wide_linear(a, maps, cuda(stream), pdl_enabled()));
 }
 
 // Tile heights of an expert call in MMA columns.
@@ -236,10 +253,14 @@ moe_status forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I
     maps.gate_s = maps.up_s = maps.down_s = maps.gate_r;
     maps.x_s = maps.h_s = maps.x_r;
   }
+  const bool wide = L.pitch > kBlkNarrow;
+  maps.ypart = maps.x_r;
+  if (wide) ok = ok && encode_out_boxes(&maps.ypart, a.ypart, 4, rows, d);
   if (!ok) return MOE_ERR_CUDA;
   const MxScatter sc{r->inv_perm, r->block_map, r->num_blocks, status, T, k, L.max_blocks, shared ? L.bn_s : 0, after_routing};
   if (launch_blk_scatter(x, d, sc, L.pitch, w + L.q_x, a.sx, cuda(stream), pdl_enabled()) != cudaSuccess) return MOE_ERR_CUDA;
-  return done(launch_blk_experts(a, maps, cuda(stream), pdl_enabled()));
+  return done(wide ? launch_blk_wide_experts(a, maps, cuda(stream), pdl_enabled())
+                   : launch_blk_experts(a, maps, cuda(stream), pdl_enabled()));
 }
 
 }  // namespace

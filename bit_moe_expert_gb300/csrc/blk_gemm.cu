@@ -20,14 +20,12 @@
 // bounded and records MOE_ERR_TIMEOUT.
 #include <cuda_runtime.h>
 
-#include "blk.cuh"
+#include "blk_items.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace bm {
 namespace {
-
-enum Mode { kLinear, kGateUp, kDown };
 
 constexpr int kWeightsWarp = 0;
 constexpr int kActivationsWarp = 1;
@@ -42,7 +40,6 @@ constexpr int kMaxAccs = 8;
 constexpr int kMatBytes = kBlk * 128;  // one matrix's codes of a stage
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kEntries = 256;          // items of a CTA, from its first, whose Entry is in shared memory
-constexpr int kMaxTile = 128;          // tokens of a tile
 constexpr int kSmemFixed = 1024 /* barriers */ + 16 * kEntries + 2 * 4 * 4 * kMaxTile /* maxima */ + 1024 /* alignment */;
 
 // A launch's variant; kBN: tokens of a tile at most, which the sums' registers are for.
@@ -76,169 +73,7 @@ Plan make_plan(int mats, int bn) {
 }
 int plan_smem(const Plan& p) { return p.stages * p.stage_bytes + p.scale_slots * p.bn * 4 + kSmemFixed; }
 
-struct Item {
-  const CUtensorMap *m0, *m1, *n;  // codes of the weights (one or two matrices) and of the tokens
-  const float *s0, *s1, *sn;       // scales: of the weight tile (a block after another), of the tokens' first block
-  long long sn_step;               // from a block's scales of the tokens to the next one's
-  uint32_t sn_bytes;
-  int e, row_m, row_n;             // matrix of the M side; first rows of the codes
-  int mt, rows, K, box;            // M tile, valid tokens, depth, tokens that the TMA box brings
-  int row0, slot;                  // experts: first row among the assignments (or tokens), tile slot
-  bool shared, ok;
-};
-
-// This CTA's items: local index i stands for item first + i * step.
-struct Sched {
-  int mt_r, mt_s;  // M tiles of a routed and of a shared tile
-  int n_routed;    // expert products: items below are routed
-  int first, n, step;
-};
-struct Entry {
-  int e, row0;    // expert (-1: malformed) and first row; dense: 0 and the M tile
-  int slot;       // entry of the block map, the shared expert's tile of tokens, or the dense product's N tile
-  uint32_t what;  // experts: M tile + 2^16 rows + 2^31 for the shared expert
-};
-constexpr uint32_t kEntryShared = 1u << 31;
-static_assert(kBlkMaxCols / kBlk <= 1 << 16 && kMaxTile < 1 << 15, "an Entry's M tile and rows");
-
-template <int kMode>
-struct Args {
-  using type = BlkExpertArgs;
-  using maps = BlkExpertMaps;
-};
-template <>
-struct Args<kLinear> {
-  using type = BlkLinearArgs;
-  using maps = BlkLinearMaps;
-};
-
-__device__ __forceinline__ Sched make_sched(const BlkLinearArgs& a, const Plan& p, bool) {
-  Sched s{};
-  s.mt_r = blk_count(a.N);
-  const int total = s.mt_r * ((a.M + p.bn - 1) / p.bn);
-  s.first = blockIdx.x;
-  s.step = gridDim.x;
-  s.n = (total - s.first + s.step - 1) / s.step;
-  return s;
-}
-__device__ __forceinline__ Entry make_entry(const BlkLinearArgs&, const Sched& s, int it) {
-  return Entry{0, it % s.mt_r, it / s.mt_r, 0};
-}
-__device__ __forceinline__ Item get_item(const BlkLinearArgs& a, const BlkLinearMaps& maps, const Plan& p, const Entry& en,
-                                         bool) {
-  Item m{};
-  m.mt = en.row0;
-  m.m0 = &maps.w;
-  m.n = &maps.x;
-  m.row_m = m.mt * kBlk;
-  m.row_n = en.slot * p.bn;
-  m.rows = min(p.bn, a.M - m.row_n);
-  m.K = a.K;
-  m.box = p.bn;
-  m.s0 = a.sw + static_cast<size_t>(m.mt) * blk_count(a.K);
-  m.sn = a.sx + m.row_n;
-  m.sn_step = a.sx_pitch;
-  m.sn_bytes = 4 * static_cast<uint32_t>(min(static_cast<long long>(p.bn), a.sx_pitch - m.row_n));
-  m.ok = true;
-  return m;
-}
-
-__device__ __forceinline__ Sched make_sched(const BlkExpertArgs& a, const Plan&, bool gate_up) {
-  Sched s{};
-  int nb = *reinterpret_cast<const volatile int32_t*>(a.num_blocks);
-  if (nb < 1 || nb > min(a.max_blocks, a.T * a.k)) {  // every tile holds an assignment
-    if (threadIdx.x == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
-    nb = 0;
-  }
-  s.mt_r = blk_count(gate_up ? a.I : a.d);
-  s.mt_s = blk_count(gate_up ? a.I_shared : a.d);
-  s.n_routed = nb * s.mt_r;
-  const int total = s.n_routed + (a.I_shared > 0 ? (a.T + a.bn_s - 1) / a.bn_s * s.mt_s : 0);
-  s.first = blockIdx.x;
-  s.step = gridDim.x;
-  s.n = (total - s.first + s.step - 1) / s.step;
-  return s;
-}
-__device__ __forceinline__ Entry make_entry(const BlkExpertArgs& a, const Sched& s, int it) {
-  Entry en;
-  if (it < s.n_routed) {
-    en.slot = it / s.mt_r;
-    const volatile int32_t* b = a.block_map + 3 * static_cast<size_t>(en.slot);
-    en.e = b[0];
-    en.row0 = b[1];
-    const int rows = b[2];
-    const bool ok = en.e >= 0 && en.e < a.E && rows >= 1 && rows <= a.bn_r && en.row0 >= 0 &&
-                    en.row0 <= a.T * a.k - rows;
-    if (!ok) en.e = -1;
-    en.what = static_cast<uint32_t>(it - en.slot * s.mt_r) | static_cast<uint32_t>(rows) << 16;
-  } else {
-    const int j = it - s.n_routed;
-    en.slot = j / s.mt_s;
-    en.e = 0;
-    en.row0 = en.slot * a.bn_s;
-    en.what = kEntryShared | static_cast<uint32_t>(j - en.slot * s.mt_s) |
-              static_cast<uint32_t>(min(a.bn_s, a.T - en.row0)) << 16;
-  }
-  return en;
-}
-__device__ __forceinline__ Item get_item(const BlkExpertArgs& a, const BlkExpertMaps& maps, const Plan&, const Entry& en,
-                                         bool gate_up) {
-  Item m{};
-  m.ok = en.e >= 0;
-  if (!m.ok) return m;
-  m.e = en.e;
-  m.row0 = en.row0;
-  m.rows = static_cast<int>(en.what >> 16 & 0x7FFFu);
-  m.shared = (en.what & kEntryShared) != 0;
-  m.mt = static_cast<int>(en.what & 0xFFFFu);
-  m.slot = en.slot;
-  const int I = m.shared ? a.I_shared : a.I;
-  const int N = gate_up ? I : a.d;
-  m.K = gate_up ? a.d : I;
-  m.box = m.shared ? a.bn_s : a.bn_r;
-  const BlkWeights& w = m.shared ? a.shared : a.routed;
-  if (m.shared) {
-    m.m0 = gate_up ? &maps.gate_s : &maps.down_s;
-    m.m1 = &maps.up_s;
-    m.n = gate_up ? &maps.x_s : &maps.h_s;
-    m.row_n = gate_up ? a.T * a.k + m.row0 : m.row0;
-  } else {
-    m.m0 = gate_up ? &maps.gate_r : &maps.down_r;
-    m.m1 = &maps.up_r;
-    m.n = gate_up ? &maps.x_r : &maps.h_r;
-    m.row_n = m.row0;
-  }
-  const int blocks = blk_count(m.K);
-  const size_t tile = (static_cast<size_t>(m.e) * blk_count(N) + m.mt) * blocks;
-  m.s0 = (gate_up ? w.s_gate : w.s_down) + tile;
-  m.s1 = w.s_up + tile;
-  m.row_m = m.mt * kBlk;
-  const float* sn = gate_up ? a.sx : (m.shared ? a.sh_s : a.sh_r);
-  m.sn = sn + static_cast<size_t>(gate_up && m.shared ? a.max_blocks + m.slot : m.slot) * blocks * a.pitch;
-  m.sn_step = a.pitch;
-  m.sn_bytes = 4 * static_cast<uint32_t>(m.box);
-  return m;
-}
-
 __device__ __forceinline__ int tile_n(int rows) { return (rows + 15) & ~15; }
-
-// Two fp32 numbers in one 64-bit register.
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
 
 template <int n>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[n]) {
@@ -370,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   // The routing has completed by now (the kernel before this one lets this one
   // start only after its own wait), so only the activations are waited for.
-  const Sched s = make_sched(a, p, kGU);
+  const Sched s = make_sched<kBlk>(a, p.bn, kGU);
   for (int i = threadIdx.x; i < min(s.n, kEntries); i += kThreads) entries[i] = make_entry(a, s, s.first + i * s.step);
   auto item = [&](int i) {
-    return get_item(a, maps, p, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
+    return get_item<kBlk>(a, maps, p.bn, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
   };
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -643,8 +478,7 @@ cudaError_t launch_for(int kind, const typename Args<kMode>::maps& maps, const t
                        int grid, cudaStream_t stream, bool pdl) {
   if (bn <= 16) return launch<Variant<kMode, 16>>(kind, maps, a, bn, grid, stream, pdl);
   if (bn <= 32) return launch<Variant<kMode, 32>>(kind, maps, a, bn, grid, stream, pdl);
-  if (bn <= 64) return launch<Variant<kMode, 64>>(kind, maps, a, bn, grid, stream, pdl);
-  return launch<Variant<kMode, 128>>(kind, maps, a, bn, grid, stream, pdl);
+  return launch<Variant<kMode, 64>>(kind, maps, a, bn, grid, stream, pdl);
 }
 
 }  // namespace

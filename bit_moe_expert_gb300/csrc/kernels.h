@@ -189,6 +189,8 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMap
 bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows);
 bool encode_mx_weights(CUtensorMap* map, const uint8_t* q, int E, int N, int row_bytes, int box_rows);
 bool encode_mx_scales(CUtensorMap* map, const uint8_t* sp, long long pieces);
+// a result [rows][cols] of 2- or 4-byte elements, boxes of 32 x 32 (for stores), swizzled by the rows' 64 or 128 bytes
+bool encode_out_boxes(CUtensorMap* map, const void* y, int elem_bytes, long long rows, int cols);
 bool pdl_enabled();  // the environment variable MOE_PDL
 int device_sms();    // 0: no device
 // moe_route_scored's checks of everything but the workspace, and its launch.
@@ -401,12 +403,14 @@ struct BlkLinearArgs {
   uint32_t* status;
   long long sx_pitch;
   int M, N, K, y_type;
-  int bn;  // height of the tokens' tiles: a multiple of 16 up to 128
+  int bn;  // height of the tokens' tiles: a multiple of 16 up to 128 (wide: 128)
   int num_sms;
+  int y_boxed;  // wide: maps.y is there
 };
 struct BlkLinearMaps {
   CUtensorMap w;  // codes [1][N][K], box (128 bytes, 128 rows, 1)
   CUtensorMap x;  // codes [M][K], box (128 bytes, bn rows)
+  CUtensorMap y;  // wide: the result, box (32 columns, 32 rows)
 };
 cudaError_t launch_blk_linear(const BlkLinearArgs& a, const BlkLinearMaps& maps, cudaStream_t stream, bool pdl);
 
@@ -427,7 +431,12 @@ struct BlkExpertMaps {
   CUtensorMap gate_r, up_r, down_r, gate_s, up_s, down_s;  // codes [E][N][K], box (128 bytes, 128 rows, 1)
   CUtensorMap x_r, x_s;        // X's codes [A + T][d], box (128 bytes, bn_r / bn_s rows)
   CUtensorMap h_r, h_s;        // h's codes
+  CUtensorMap ypart;           // wide: the experts' rows, box (32 columns, 32 rows)
 };
+// Tiles of more than kBlkNarrow tokens: the tokens on the MMA's M side.
+constexpr int kBlkNarrow = 64;
+cudaError_t launch_blk_wide_linear(const BlkLinearArgs& a, const BlkLinearMaps& maps, cudaStream_t stream, bool pdl);
+cudaError_t launch_blk_wide_experts(const BlkExpertArgs& a, const BlkExpertMaps& maps, cudaStream_t stream, bool pdl);
 cudaError_t launch_blk_experts(const BlkExpertArgs& a, const BlkExpertMaps& maps, cudaStream_t stream, bool pdl);
 
 // X's rows, quantised once, to the rows of their assignments; s as for

@@ -140,7 +140,7 @@ def test_quantise_strided_rows_and_another_stream():
 
 SIZES = [(1, 1, 16), (1, 2048, 2048), (1, 130, 48), (2, 8, 4112), (3, 33, 160), (8, 200, 1040), (9, 64, 128), (16, 128, 64),
          (17, 200, 272), (63, 129, 512), (128, 513, 288), (129, 129, 512), (200, 31, 1056), (300, 700, 2048), (257, 512, 32),
-         (1000, 256, 320), (640, 1000, 4096)]
+         (1000, 256, 320), (640, 1000, 4096), (1300, 2080, 400), (2433, 1500, 144), (1000, 2601, 1040), (1537, 4000, 128)]
 
 
 def _assert_product(y, av, wv, K):
