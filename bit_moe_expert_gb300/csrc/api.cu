@@ -282,10 +282,9 @@ bool encode_out_boxes(CUtensorMap* map, const void* y, int elem_bytes, long long
   if (!get_encoder()) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem_bytes};
-  const cuuint32_t box[2] = {32, 32};
-  return elem_bytes == 4
-             ? encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)
-             : encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / elem_bytes), 32};
+  return encode(map, elem_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, y, dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool pdl_enabled() { return env_flag("MOE_PDL", true); }

@@ -75,11 +75,6 @@ int plan_smem(const Plan& p) { return p.stages * p.stage_bytes + p.scale_slots *
 
 __device__ __forceinline__ int tile_n(int rows) { return (rows + 15) & ~15; }
 
-template <int n>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[n]) {
-  if constexpr (n == 8) tmem_ld8(taddr, v); else tmem_ld16(taddr, v);
-}
-
 // A warp's sums: two tokens to a register pair, for each of its groups.
 template <typename V>
 struct Sums {

@@ -10,9 +10,9 @@
 // Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
 // activations' loads, warp 2 the MMAs' issue, warps 4 to 11 the sums: two per
 // quarter of the tensor-memory lanes (32 tokens), 128 columns each.  Rows of
-// results leave through shared memory as TMA stores, 32 x 32 at a time (a lane's
-// own stores would touch a line each); the last, partial 32 rows of an expert by
-// plain stores.  Every wait is bounded and records MOE_ERR_TIMEOUT.
+// results leave through shared memory as TMA stores, 64 bytes of 32 rows at a time
+// (a lane's own stores would touch a line each); the last, partial 32 rows of an
+// expert by plain stores.  Every wait is bounded and records MOE_ERR_TIMEOUT.
 #include <cuda_runtime.h>
 
 #include "blk_items.cuh"
@@ -34,111 +34,137 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kAccs = 2;
 constexpr int kHalfBytes = kBlk * 128;  // 128 rows' codes of a stage
 constexpr int kStageBytes = 3 * kHalfBytes;
-constexpr int kBoxBytes = 32 * 32 * 4;  // a 32 x 32 box of a result on its way out
+constexpr int kBoxBytes = 32 * 64;      // 64 bytes of 32 rows of a result on their way out
+constexpr int kBoxes = 4;               // of a warp
 constexpr int kEntries = 64;            // items of a CTA, from its first, whose Entry is in shared memory
 template <int kMode>
 struct Variant {
-  // with results staged in two boxes a warp, three stages are left
+  // with results staged in boxes, three stages are left
   static constexpr int kStages = kMode == kGateUp ? 4 : 3;
-  static constexpr int kBoxes = kMode == kGateUp ? 0 : 2;
-  static constexpr int kSmem = kStages * kStageBytes + kSumWarps * kBoxes * kBoxBytes + 2 * kParts * kBlk * 4 /* maxima */ +
+  // the tokens' scales of a block are read until its accumulator is free again, which may be kAccs stages after the
+  // stage's codes: a ring of their own
+  static constexpr int kSlots = kStages + kAccs;
+  static constexpr int kSmem = kStages * kStageBytes + (kMode == kGateUp ? 0 : kSumWarps * kBoxes * kBoxBytes) + 2 * kParts * kBlk * 4 /* maxima */ + kSlots * kBlk * 4 /* scales */ +
                                512 /* barriers */ + 16 * kEntries + 1024 /* alignment */;
 };
 static_assert(Variant<kGateUp>::kSmem <= 227 * 1024 && Variant<kDown>::kSmem <= 227 * 1024, "shared memory of a CTA");
 
-// A warp's sums: 128 columns of each lane's token, two to a register pair; gate/up: 64 of gate, then 64 of up.
+constexpr int kOwn = kCols / kParts;  // columns of a warp; gate/up: half of them gate's, then as many of up's
+constexpr int kPiece = 8;            // columns of an accumulator that a warp takes at a time
+
+// A warp's sums: kOwn columns of each lane's token, two to a register pair.
 struct Sums {
-  uint64_t v[4][16];
+  uint64_t v[kOwn / 2];
   __device__ __forceinline__ float get(int c) const {
     float lo, hi;
-    unpack2(v[c >> 5][(c & 31) >> 1], lo, hi);
+    unpack2(v[c >> 1], lo, hi);
     return c & 1 ? hi : lo;
   }
 };
 
-// 32 columns of the warp's 32 tokens as a box of the result: a lane's row in 16-byte chunks, in the order the store's
-// swizzle takes (128-byte rows: chunk ^ row % 8; 64-byte rows: chunk ^ row / 2 % 4).
-template <bool kWideType>
-__device__ __forceinline__ void put_box(uint8_t* box, const Sums& acc, int g, int lane, int type) {
-  if constexpr (kWideType) {
+// A box of the result from column c of the warp's on: a lane's row of 64 bytes, its four 16-byte chunks in the order that
+// the store's swizzle takes (chunk ^ row / 2 % 4).
+template <int kType>
+__device__ __forceinline__ void put_box(uint8_t* box, const Sums& acc, int c, int lane) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<float4*>(box + 128 * lane + 16 * (j ^ (lane & 7))) =
-          make_float4(acc.get(32 * g + 4 * j), acc.get(32 * g + 4 * j + 1), acc.get(32 * g + 4 * j + 2), acc.get(32 * g + 4 * j + 3));
-  } else {
+  for (int j = 0; j < 4; ++j) {
+    uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = acc.get(32 * g + 8 * j + 2 * i), b = acc.get(32 * g + 8 * j + 2 * i + 1);
-        if (type == kFp16) {
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kType == kFp32) {
+        o[i] = __float_as_uint(acc.get(c + 4 * j + i));
+      } else {
+        const float a = acc.get(c + 8 * j + 2 * i), b = acc.get(c + 8 * j + 2 * i + 1);
+        if constexpr (kType == kFp16) {
           o[i] = f32x2_to_f16x2(a, b);
         } else {
           const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
           o[i] = *reinterpret_cast<const uint32_t*>(&p);
         }
       }
-      *reinterpret_cast<uint4*>(box + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+    *reinterpret_cast<uint4*>(box + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
-// The warp's 128 columns of its 32 tokens, of which `rows` exist, from column n0 on: by boxes where `boxed`, else by
-// each lane.  `first`: the first token's row of the result, whose rows are N elements long; `turn`: the warp's next box.
-__device__ __forceinline__ void store_rows(const Sums& acc, const CUtensorMap* map, uint8_t* boxes, int& turn, bool boxed, int type,
+// The warp's columns of its 32 tokens, of which `rows` exist, from column n0 of the result on: by boxes and TMA stores
+// where `boxed`, through a box where the result's rows are `aligned` to 16 bytes, else by each lane.  `first`: the first
+// token's row of the result, whose rows are N elements long; `turn`: the warp's next box.
+template <int kType>
+__device__ __forceinline__ void store_rows(const Sums& acc, const CUtensorMap* map, uint8_t* boxes, int& turn, bool boxed, bool aligned,
                                            void* y, long long first, int rows, int n0, int N, int lane) {
-  if (boxed) {
+  constexpr int kBytes = kType == kFp32 ? 4 : 2, kWide = 64 / kBytes;  // columns of a box
+  if (aligned) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      if (n0 + 32 * g >= N) break;
+    for (int c = 0; c < kOwn; c += kWide) {
+      if (n0 + c >= N) break;
       uint8_t* box = boxes + turn * kBoxBytes;
-      turn ^= 1;
-      if (lane == 0) bulk_wait_group_read<1>();  // the box two turns back, this one, has been read
+      turn = turn + 1 == kBoxes ? 0 : turn + 1;
+      if (lane == 0) bulk_wait_group_read<kBoxes - 1>();  // this box has been read
       __syncwarp();
-      if (type == kFp32) put_box<true>(box, acc, g, lane, type); else put_box<false>(box, acc, g, lane, type);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(map, box, n0 + 32 * g, static_cast<int>(first));
-        bulk_commit_group();
+      put_box<kType>(box, acc, c, lane);
+      if (boxed) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(map, box, n0 + c, static_cast<int>(first));
+          bulk_commit_group();
+        }
+      } else {
+        __syncwarp();
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 8) {  // four lanes a row
+          const int r = r0 + (lane >> 2), col = n0 + c + (lane & 3) * (16 / kBytes);
+          const uint4 v = *reinterpret_cast<const uint4*>(box + 64 * r + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
+          if (r < rows && col < N) *reinterpret_cast<uint4*>(static_cast<char*>(y) + ((first + r) * N + col) * kBytes) = v;
+        }
+        __syncwarp();
+        if (lane == 0) bulk_commit_group();  // an empty one: a box's turn is a group's
       }
     }
   } else if (lane < rows) {
     const size_t at = static_cast<size_t>(first + lane) * N + n0;
 #pragma unroll
-    for (int c = 0; c < 128; ++c)
-      if (n0 + c < N) store1(type, y, at + c, acc.get(c));
+    for (int c = 0; c < kOwn; ++c)
+      if (n0 + c < N) store1(kType, y, at + c, acc.get(c));
   }
 }
 
 __device__ __forceinline__ void epilogue_rows(const BlkLinearArgs& a, const BlkLinearMaps& maps, const Item& m, const Sums& acc,
                                               uint8_t* boxes, int& turn, int quarter, int part, int lane) {
   // (rows and columns past the result's end are not written by a box)
-  store_rows(acc, &maps.y, boxes, turn, a.y_boxed, a.y_type, a.y, static_cast<long long>(m.row_n) + 32 * quarter, m.rows - 32 * quarter,
-             m.row_m + kBlk * part, a.N, lane);
+  const long long first = static_cast<long long>(m.row_n) + 32 * quarter;
+  const int rows = m.rows - 32 * quarter, n0 = m.row_m + kOwn * part;
+  if (a.y_type == kFp32)
+    store_rows<kFp32>(acc, &maps.y, boxes, turn, a.y_boxed, a.y_boxed, a.y, first, rows, n0, a.N, lane);
+  else if (a.y_type == kFp16)
+    store_rows<kFp16>(acc, &maps.y, boxes, turn, a.y_boxed, a.y_boxed, a.y, first, rows, n0, a.N, lane);
+  else
+    store_rows<kBf16>(acc, &maps.y, boxes, turn, a.y_boxed, a.y_boxed, a.y, first, rows, n0, a.N, lane);
 }
 __device__ __forceinline__ void epilogue_rows(const BlkExpertArgs& a, const BlkExpertMaps& maps, const Item& m, const Sums& acc,
                                               uint8_t* boxes, int& turn, int quarter, int part, int lane) {
   // fp32 rows of the experts' outputs, routed ones in permuted order, then the shared expert's in token order: what
   // follows an item's last row is another item's
   const int rows = m.rows - 32 * quarter;
-  store_rows(acc, &maps.ypart, boxes, turn, rows >= 32, kFp32, a.ypart, (m.shared ? static_cast<long long>(a.T) * a.k : 0) + m.row0 + 32 * quarter,
-             rows, m.row_m + kBlk * part, a.d, lane);
+  store_rows<kFp32>(acc, &maps.ypart, boxes, turn, rows >= 32, true, a.ypart,
+                    (m.shared ? static_cast<long long>(a.T) * a.k : 0) + m.row0 + 32 * quarter, rows, m.row_m + kOwn * part, a.d,
+                    lane);
 }
 
-// gate/up: h = silu(gate) up of 64 columns of a lane's token, quantised with the other share's 64 (a block of h).
-// meet(): waits until the other share's maxima have been written (false: given up).
+// gate/up: h = silu(gate) up of kOwn / 2 columns of a lane's token, quantised with the other shares' (a block of h).
+// meet(): waits until their maxima have been written (false: given up).
 template <typename Meet>
 __device__ __forceinline__ bool epilogue_gate_up(const BlkExpertArgs& a, const Item& m, Sums& acc, int quarter, int part, int lane,
                                                  uint32_t (*maxima)[kBlk], Meet meet) {
+  constexpr int kHalf = kOwn / 2;
   const int I = m.shared ? a.I_shared : a.I;
   float most = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 64; c += 2) {  // h takes gate's place
-    const float h0 = blk_swiglu(acc.get(c), acc.get(64 + c)), h1 = blk_swiglu(acc.get(c + 1), acc.get(64 + c + 1));
+  for (int c = 0; c < kHalf; c += 2) {  // h takes gate's place
+    const float h0 = blk_swiglu(acc.get(c), acc.get(kHalf + c)), h1 = blk_swiglu(acc.get(c + 1), acc.get(kHalf + c + 1));
     most = max_nan(most, max_nan(fabsf(h0), fabsf(h1)));
-    acc.v[c >> 5][(c & 31) >> 1] = pack2(__float_as_uint(h0), __float_as_uint(h1));
+    acc.v[c >> 1] = pack2(__float_as_uint(h0), __float_as_uint(h1));
   }
   const int r = 32 * quarter + lane;
   maxima[part][r] = __float_as_uint(most);
@@ -147,10 +173,10 @@ __device__ __forceinline__ bool epilogue_gate_up(const BlkExpertArgs& a, const I
   if (r >= m.rows) return true;
   if (part == 0)
     (m.shared ? a.sh_s : a.sh_r)[(static_cast<size_t>(m.slot) * blk_count(I) + m.mt) * a.pitch + r] = s;
-  const int n0 = m.mt * kBlk + 64 * part;
+  const int n0 = m.mt * kBlk + kHalf * part;
   uint8_t* hq = (m.shared ? a.h_s : a.h_r) + static_cast<size_t>(m.row0 + r) * I + n0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < kHalf / 16; ++j) {
     if (n0 + 16 * j >= I) break;
     uint32_t o[4];
 #pragma unroll
@@ -172,8 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* boxes = stages + kStages * kStageBytes;
-  uint32_t(*maxima)[kBlk] = reinterpret_cast<uint32_t(*)[kBlk]>(boxes + kSumWarps * V::kBoxes * kBoxBytes);  // [2 x parts][tokens]
-  uint64_t* full = reinterpret_cast<uint64_t*>(maxima + 2 * kParts);
+  uint32_t(*maxima)[kBlk] = reinterpret_cast<uint32_t(*)[kBlk]>(boxes + (kGU ? 0 : kSumWarps * kBoxes * kBoxBytes));  // [2 x parts][tokens]
+  float* scales = reinterpret_cast<float*>(maxima + 2 * kParts);  // [slots][tokens]
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + V::kSlots * kBlk);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + kAccs;
@@ -199,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kAccs; ++i) {
-      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_full[i], 2);  // the MMAs' commit, and their issuer, who has seen the stage's scales land
       mbar_init(&acc_empty[i], kSumWarps);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&met[i], kParts);
@@ -221,20 +248,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kSumWarp0) {
-    // 128 sums take more than 384 threads' equal share of the registers: 128 x 72 + 256 x 216 = 384 x 168
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // 128 sums take more than 384 threads' equal share of the registers: 128 x 40 + 256 x 232 = 384 x 168
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kWeightsWarp || warp == kActivationsWarp) {
       // one thread for the weights, which starts before the wait, and one for the activations
       if (lane == 0) {
         const bool weights = warp == kWeightsWarp;
         if (!weights) pdl_wait();
-        int stage = 0, filled = 0;
+        int stage = 0, slot = 0, filled = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int i = 0; i < s.n && ok; ++i) {
           const Item m = item(i);
           if (!m.ok) continue;
           const int blocks = blk_count(m.K);
+          const float* sn = m.sn;
           for (int kb = 0; kb < blocks; ++kb, ++filled) {
             if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
               fail();
@@ -251,8 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               else
                 tma_load_3d(st + 2 * kHalfBytes, m.m0, bar, kb * kBlk, m.row_m + kBlk, m.e);
             } else {
-              mbar_arrive_expect_tx(bar, m.box * 128);
+              mbar_arrive_expect_tx(bar, m.box * 128 + m.sn_bytes);
               tma_load_2d(st, m.n, bar, kb * kBlk, m.row_n);
+              bulk_g2s(scales + slot * kBlk, sn, m.sn_bytes, bar);
+              sn += m.sn_step;
+              if (++slot == V::kSlots) slot = 0;
             }
             if (++stage == kStages) {
               stage = 0;
@@ -297,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_commit(&empty[stage]);
             tc_commit(&acc_full[acc]);
+            mbar_arrive(&acc_full[acc]);
           }
           at += kStageBytes >> 4;
           if (++stage == kStages) {
@@ -317,93 +349,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     pdl_wait();
     pdl_launch_dependents();
     const int quarter = warp & 3, part = (warp - kSumWarp0) >> 2;
     uint32_t acc = 0, accphase = 0, parity = 0;
-    int turn = 0;
+    int turn = 0, slot = 0;
     bool ok = true;
-    // columns of group g in the accumulator
-    auto column = [&](int g) { return kGU ? (g >> 1) * kBlk + 64 * part + 32 * (g & 1) : kBlk * part + 32 * g; };
+    // first column of piece u in the accumulator
+    auto column = [&](int u) {
+      const int c = u * kPiece;
+      return kGU ? c / (kOwn / 2) * kBlk + kOwn / 2 * part + c % (kOwn / 2) : kOwn * part + c;
+    };
     auto wait_full = [&]() {
       if (mbar_wait(&acc_full[acc], accphase, abort_flag)) return true;
       if (lane == 0) fail();
       return false;
     };
     for (int i = 0; i < s.n && ok; ++i) {
-      const Item m = item(i);
-      if (!m.ok) {
-        if (lane == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
-        continue;
+      // what the loop below needs of the item; the rest is taken again after it, and the weights' scales every 32 blocks,
+      // so that their registers are free in between
+      int blocks;
+      bool some;        // of this quarter's tokens
+      {
+        const Item m = item(i);
+        if (!m.ok) {
+          if (lane == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
+          continue;
+        }
+        blocks = blk_count(m.K);
+        some = 32 * quarter < m.rows;
       }
-      const int blocks = blk_count(m.K);
-      const bool some = 32 * quarter < m.rows;  // of this quarter's tokens
       Sums sum;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int c = 0; c < 16; ++c) sum.v[g][c] = 0;
-      // the scales two blocks ahead
-      const float* sn = m.sn + min(32 * quarter + lane, static_cast<int>(m.sn_bytes / 4) - 1);
-      const float *s0 = kGU || part == 0 ? m.s0 : m.s1, *s1 = m.s1;
-      float sx[3], sw0[3], sw1[3];
-      auto scales = [&](int kb, int to) {
-        sx[to] = kb < blocks ? __ldg(sn + kb * m.sn_step) : 0.0f;
-        sw0[to] = kb < blocks ? __ldg(s0 + kb) : 0.0f;
-        sw1[to] = kGU && kb < blocks ? __ldg(s1 + kb) : 0.0f;
-      };
-      scales(0, 0);
-      scales(1, 1);
-      uint32_t d[2][32];
-      ok = wait_full();
-      if (!ok) break;
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-      if (some) tmem_ld32(tmem + lanes + acc * kCols + column(0), d[0]);
+      for (int c = 0; c < kOwn / 2; ++c) sum.v[c] = 0;
+      float sw0 = 0.0f, sw1 = 0.0f;  // the weights' scales of 32 blocks, one a lane
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
       for (int kb = 0; kb < blocks; ++kb) {
-        scales(kb + 2, 2);
+        if ((kb & 31) == 0) {
+          const Item m = item(i);
+          sw0 = sw1 = 0.0f;
+          if (kb + lane < blocks) {
+            sw0 = __ldg((kGU || part < kParts / 2 ? m.s0 : m.s1) + kb + lane);
+            if (kGU) sw1 = __ldg(m.s1 + kb + lane);
+          }
+        }
+        if (!wait_full()) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
         uint64_t w[2];
         {
-          const uint32_t f0 = __float_as_uint(sx[0] * sw0[0]), f1 = __float_as_uint(sx[0] * sw1[0]);
+          const float sx = scales[slot * kBlk + 32 * quarter + lane];
+          if (++slot == V::kSlots) slot = 0;
+          const uint32_t f0 = __float_as_uint(sx * __shfl_sync(0xffffffffu, sw0, kb & 31));
+          const uint32_t f1 = kGU ? __float_as_uint(sx * __shfl_sync(0xffffffffu, sw1, kb & 31)) : 0u;
           w[0] = pack2(f0, f0);
           w[1] = pack2(f1, f1);
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int u = 0; u < kOwn / kPiece; ++u) {
+          uint32_t d[kPiece];
+          tmem_ld<kPiece>(lanes + acc * kCols + column(u), d);
           tc_wait_ld();
-          if (g < 3) {
-            if (some) tmem_ld32(tmem + lanes + acc * kCols + column(g + 1), d[(g + 1) & 1]);
-          } else {
-            // this accumulator has been read: on to the next block's, whose load runs beside the last sums of this one
+          if (u + 1 == kOwn / kPiece) {  // this accumulator has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[acc]);
-            acc ^= 1;
-            accphase ^= acc ^ 1;
-            if (kb + 1 < blocks) {
-              ok = wait_full();
-              if (!ok) break;
-              __syncwarp();
-              tc_fence_after();
-              if (some) tmem_ld32(tmem + lanes + acc * kCols + column(0), d[0]);
-            }
           }
-          if (some) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) fma2(sum.v[g][c], pack2(d[g & 1][2 * c], d[g & 1][2 * c + 1]), w[kGU ? g >> 1 : 0]);
-          }
+          for (int c = 0; c < kPiece / 2; ++c)
+            fma2(sum.v[u * kPiece / 2 + c], pack2(d[2 * c], d[2 * c + 1]), w[kGU ? 2 * u * kPiece / kOwn : 0]);
         }
-        if (!ok) break;
-        sx[0] = sx[1];
-        sx[1] = sx[2];
-        sw0[0] = sw0[1];
-        sw0[1] = sw0[2];
-        sw1[0] = sw1[1];
-        sw1[1] = sw1[2];
+        acc ^= 1;
+        accphase ^= acc ^ 1;
       }
       if (!ok) break;
+      const Item m = item(i);
       if constexpr (kGU) {
         ok = epilogue_gate_up(a, m, sum, quarter, part, lane, maxima + kParts * parity, [&]() {
           __syncwarp();
@@ -415,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
         parity ^= 1;  // a warp two items ahead has met the other one in between: two sets of maxima are enough
       } else if (some) {
-        epilogue_rows(a, maps, m, sum, boxes + (warp - kSumWarp0) * V::kBoxes * kBoxBytes, turn, quarter, part, lane);
+        epilogue_rows(a, maps, m, sum, boxes + (warp - kSumWarp0) * kBoxes * kBoxBytes, turn, quarter, part, lane);
       }
     }
     if (!kGU && lane == 0) bulk_wait_group_all();  // nothing of this CTA's shared memory is read after its end

@@ -189,7 +189,7 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps* routed, const GemmMap
 bool encode_mx_codes(CUtensorMap* map, const uint8_t* q, long long rows, int row_bytes, int box_rows);
 bool encode_mx_weights(CUtensorMap* map, const uint8_t* q, int E, int N, int row_bytes, int box_rows);
 bool encode_mx_scales(CUtensorMap* map, const uint8_t* sp, long long pieces);
-// a result [rows][cols] of 2- or 4-byte elements, boxes of 32 x 32 (for stores), swizzled by the rows' 64 or 128 bytes
+// a result [rows][cols] of 2- or 4-byte elements: boxes of 64 bytes of 32 rows (for stores), 64-byte swizzle
 bool encode_out_boxes(CUtensorMap* map, const void* y, int elem_bytes, long long rows, int cols);
 bool pdl_enabled();  // the environment variable MOE_PDL
 int device_sms();    // 0: no device
@@ -410,7 +410,7 @@ struct BlkLinearArgs {
 struct BlkLinearMaps {
   CUtensorMap w;  // codes [1][N][K], box (128 bytes, 128 rows, 1)
   CUtensorMap x;  // codes [M][K], box (128 bytes, bn rows)
-  CUtensorMap y;  // wide: the result, box (32 columns, 32 rows)
+  CUtensorMap y;  // wide: the result, box (64 bytes, 32 rows)
 };
 cudaError_t launch_blk_linear(const BlkLinearArgs& a, const BlkLinearMaps& maps, cudaStream_t stream, bool pdl);
 
@@ -431,7 +431,7 @@ struct BlkExpertMaps {
   CUtensorMap gate_r, up_r, down_r, gate_s, up_s, down_s;  // codes [E][N][K], box (128 bytes, 128 rows, 1)
   CUtensorMap x_r, x_s;        // X's codes [A + T][d], box (128 bytes, bn_r / bn_s rows)
   CUtensorMap h_r, h_s;        // h's codes
-  CUtensorMap ypart;           // wide: the experts' rows, box (32 columns, 32 rows)
+  CUtensorMap ypart;           // wide: the experts' rows, box (64 bytes, 32 rows)
 };
 // Tiles of more than kBlkNarrow tokens: the tokens on the MMA's M side.
 constexpr int kBlkNarrow = 64;
