@@ -124,12 +124,12 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
     return at;
   };
   L.few = T <= kBlkFewT;
-  L.ypart = take(rows * d * 4);
   if (L.few) {
     L.h = take(rows * (I > I_shared ? I : I_shared) * 4);
     L.total = o;
     return L;
   }
+  L.ypart = take(rows * d * 4);
   L.q_x = take(rows * d);
   L.sx = take((L.max_blocks + tiles_s) * blk_count(d) * L.pitch * 4);
   L.h_r = take(A * I);
@@ -192,12 +192,10 @@ moe_status forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I
     a.routed = weights(routed);
     a.shared = weights(shared);
     a.perm = r->perm;
-    a.inv_perm = r->inv_perm;
     a.block_map = r->block_map;
     a.num_blocks = r->num_blocks;
     a.w = r->w;
     a.h = reinterpret_cast<float*>(w + L.h);
-    a.ypart = reinterpret_cast<float*>(w + L.ypart);
     a.y = Y;
     a.status = status;
     a.T = T;
@@ -207,8 +205,6 @@ moe_status forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I
     a.I_shared = I_shared;
     a.E = E;
     a.tiles = T * k < L.max_blocks ? T * k : L.max_blocks;
-    a.rows = r->block_rows;
-    a.num_sms = num_sms;
     return done(launch_blk_few_experts(a, cuda(stream), pdl_enabled()));
   }
 

@@ -6,8 +6,8 @@
 // turn.  A lane loads 32 consecutive bytes of each of two rows straight from
 // global memory into the A fragments of four warp-level MMAs (m16n8k32, E4M3,
 // fp32 accumulate): which columns an MMA takes together is free as long as both
-// operands agree, so no byte is moved between lanes.  Eight tokens are the MMA's
-// N.  The activations are quantised in the warp that needs them, a block is its
+// operands agree, so no byte is moved between lanes.  Up to eight tokens are the
+// MMA's N.  The activations are quantised in the warp that needs them, a block is its
 // 32 lanes' four values each.  The blocks' sums are scaled and added in fp32, the
 // warps' at the end through shared memory in a fixed order.
 #include <cuda_runtime.h>
@@ -85,54 +85,69 @@ __device__ __forceinline__ uint32_t quantize4(const float (&f)[4], float& scale)
   return f32x4_to_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
 }
 
-// Block kb of row `row` of the activations: codes and scale, as quantize4.
-__device__ __forceinline__ uint32_t x_block(const BlkX& x, long long row, int kb, int K, int lane, float& scale) {
-  const int c = kb * kBlk + 4 * lane;
-  if (x.type == kBlkCodes) {
-    scale = __ldg(x.s + kb * x.pitch + row);
-    return c < K ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(x.x) + row * x.ldx + c)) : 0u;
-  }
-  float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < K) {
-    if (x.type == kFp32) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(x.x) + row * x.ldx + c));
-      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+// A lane's share of a block of 128 columns of one row of activations: as loaded, and as codes and the block's scale.
+template <int kType>
+struct XBlock {
+  uint32_t v[kType == kFp32 ? 4 : kType == kBlkCodes ? 1 : 2];
+  float s;  // codes: their scale
+  __device__ __forceinline__ void load(const BlkX& x, long long row, int kb, int K, int lane) {
+    const int c = kb * kBlk + 4 * lane;
+    const char* p = static_cast<const char*>(x.x) + (row * x.ldx + c) * (kType == kFp32 ? 4 : kType == kBlkCodes ? 1 : 2);
+    const bool in = c < K;
+    if constexpr (kType == kFp32) {
+      const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else if constexpr (kType == kBlkCodes) {
+      v[0] = in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+      s = __ldg(x.s + kb * x.pitch + row);
     } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x.x) + row * x.ldx + c));
-      if (x.type == kFp16) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
-      } else {
-        f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-      }
+      const uint2 u = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+      v[0] = u.x; v[1] = u.y;
     }
   }
-  return quantize4(f, scale);
-}
+  __device__ __forceinline__ uint32_t codes(float& scale) const {
+    if constexpr (kType == kBlkCodes) {
+      scale = s;
+      return v[0];
+    } else if constexpr (kType == kFp32) {
+      const float f[4] = {__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3])};
+      return quantize4(f, scale);
+    } else if constexpr (kType == kFp16) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v[0])), b = __half22float2(*reinterpret_cast<const __half2*>(&v[1]));
+      const float f[4] = {a.x, a.y, b.x, b.y};
+      return quantize4(f, scale);
+    } else {
+      const float f[4] = {__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
+                          __uint_as_float(v[1] & 0xFFFF0000u)};
+      return quantize4(f, scale);
+    }
+  }
+};
 
-// The B fragments of a block of up to eight tokens: token i's codes by
-// code_of(i, scale), for i < n; the others are zeros.  `buf`: 8 x 128 bytes of the
-// warp's own.  sa: the scales of the lane's two accumulator columns, tokens
-// 2 (lane % 4) and the next.
-template <typename CodeOf>
-__device__ __forceinline__ void b_fragments(uint32_t* buf, int n, int lane, Piece& b, float (&sa)[2], CodeOf code_of) {
-  sa[0] = sa[1] = 0.0f;
-  __syncwarp();
-  for (int i = 0; i < n; ++i) {
-    float s;
-    buf[32 * i + lane] = code_of(i, s);
-    if (i == 2 * (lane & 3)) sa[0] = s;
-    if (i == 2 * (lane & 3) + 1) sa[1] = s;
+// A warp's B fragments of a block of up to eight tokens, a column each: put() for
+// the columns that there are, then take().  `buf`: 8 x 128 bytes of the warp's own.
+struct Columns {
+  uint32_t* buf;
+  int lane;
+  uint32_t there = 0;            // columns put
+  float sa[2] = {0.0f, 0.0f};    // scales of the lane's two accumulator columns, 2 (lane % 4) and the next
+  __device__ __forceinline__ Columns(uint32_t* b, int l) : buf(b), lane(l) { __syncwarp(); }
+  __device__ __forceinline__ void put(int column, uint32_t codes, float scale) {
+    buf[32 * column + lane] = codes;
+    there |= 1u << column;
+    if (column == 2 * (lane & 3)) sa[0] = scale;
+    if (column == 2 * (lane & 3) + 1) sa[1] = scale;
   }
-  __syncwarp();
-  b.zero();
-  if ((lane >> 2) < n) {
-    const uint4* p = reinterpret_cast<const uint4*>(buf + 32 * (lane >> 2) + 8 * (lane & 3));
-    b.v[0] = p[0];
-    b.v[1] = p[1];
+  __device__ __forceinline__ void take(Piece& b) const {
+    __syncwarp();
+    b.zero();
+    if (there >> (lane >> 2) & 1) {
+      const uint4* p = reinterpret_cast<const uint4*>(buf + 32 * (lane >> 2) + 8 * (lane & 3));
+      b.v[0] = p[0];
+      b.v[1] = p[1];
+    }
   }
-}
+};
 
 struct Shared {
   uint32_t codes[kWarps][kTokens * 32];
@@ -151,43 +166,67 @@ __device__ __forceinline__ float take_sum(const float (&sums)[kWarps][kRows * kT
   for (int w = 0; w < kWarps; ++w) v += sums[w][i];
   return v;
 }
+__device__ __forceinline__ void add(float (&acc)[4], const float (&d)[4], float s0, float s1) {
+  acc[0] = fmaf(d[0], s0, acc[0]);
+  acc[1] = fmaf(d[1], s1, acc[1]);
+  acc[2] = fmaf(d[2], s0, acc[2]);
+  acc[3] = fmaf(d[3], s1, acc[3]);
+}
 
+template <int kType>
 __global__ void __launch_bounds__(kThreads) blk_few_linear_kernel(const BlkFewLinearArgs a) {
   __shared__ Shared sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, blocks = blk_count(a.K);
   const float* sw = a.sw + static_cast<size_t>(n0 / kBlk) * blocks;
   ABlock w;
-  if (warp < blocks) w.load(a.w, n0, a.N, a.K, warp, lane);
+  float s = 0.0f;
+  auto load = [&](int kb) {
+    if (kb >= blocks) return;
+    w.load(a.w, n0, a.N, a.K, kb, lane);
+    s = __ldg(sw + kb);
+  };
+  load(warp);
   pdl_wait();
   pdl_launch_dependents();
-  for (int t0 = blockIdx.y * kTokens; t0 < a.T; t0 += gridDim.y * kTokens) {
-    const int n = min(kTokens, a.T - t0);
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = warp; kb < blocks; kb += kWarps) {
-      Piece b;
-      float sa[2], d[4];
-      b_fragments(sm.codes[warp], n, lane, b, sa, [&](int i, float& s) { return x_block(a.x, t0 + i, kb, a.K, lane, s); });
-      multiply(d, w, b);
-      const float s = __ldg(sw + kb);
-      if (kb + kWarps < blocks) w.load(a.w, n0, a.N, a.K, kb + kWarps, lane);
-      acc[0] = fmaf(d[0], sa[0] * s, acc[0]);
-      acc[1] = fmaf(d[1], sa[1] * s, acc[1]);
-      acc[2] = fmaf(d[2], sa[0] * s, acc[2]);
-      acc[3] = fmaf(d[3], sa[1] * s, acc[3]);
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int kb = warp; kb < blocks; kb += kWarps) {
+    XBlock<kType> x[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i)
+      if (i < a.T) x[i].load(a.x, i, kb, a.K, lane);
+    Columns c(sm.codes[warp], lane);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      if (i >= a.T) break;
+      float sx;
+      const uint32_t q = x[i].codes(sx);
+      c.put(i, q, sx);
     }
-    put_sums(sm.sums[0][warp], acc, lane);
-    __syncthreads();
-    if (threadIdx.x < kRows * kTokens) {
-      const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-      if (t < n && n0 + r < a.N) store1(a.y_type, a.y, static_cast<size_t>(t0 + t) * a.N + n0 + r, take_sum(sm.sums[0], kTokens * r + t));
-    }
-    __syncthreads();
-    if (t0 + static_cast<int>(gridDim.y) * kTokens < a.T && warp < blocks) w.load(a.w, n0, a.N, a.K, warp, lane);
+    Piece b;
+    float d[4];
+    c.take(b);
+    multiply(d, w, b);
+    add(acc, d, c.sa[0] * s, c.sa[1] * s);
+    load(kb + kWarps);
+  }
+  put_sums(sm.sums[0][warp], acc, lane);
+  __syncthreads();
+  if (threadIdx.x < kRows * kTokens) {
+    const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
+    if (t < a.T && n0 + r < a.N) store1(a.y_type, a.y, static_cast<size_t>(t) * a.N + n0 + r, take_sum(sm.sums[0], kTokens * r + t));
   }
 }
 
-// A tile of the experts' rows.
+// ------------------------------------------------------------------ experts
+// Two launches after the routing.  gate/up: a CTA 16 columns of h of one tile (at
+// most eight rows: a token takes an expert once), fp32 h to memory.  down: a CTA
+// 16 columns of Y over all experts: its warps take the (expert, block of h) pairs
+// in turn, quantise h, and add each token's column with its routing weight, so that
+// nothing is added up between CTAs.  The gate/up kernel lets the down kernel start
+// after its own wait, when the routing has completed: the down kernel asks for its
+// first weights before it waits for h.
+
 struct Tile {
   int e, row0, rows;
   bool shared, ok, some;
@@ -210,110 +249,180 @@ __device__ __forceinline__ Tile get_tile(const BlkFewArgs& a, int i) {
   t.row0 = b[1];
   t.rows = b[2];
   t.some = i < routed_tiles(a);
-  t.ok = t.some && t.e >= 0 && t.e < a.E && t.rows >= 1 && t.rows <= a.rows && t.row0 >= 0 && t.row0 <= a.T * a.k - t.rows;
+  t.ok = t.some && t.e >= 0 && t.e < a.E && t.rows >= 1 && t.rows <= a.T && t.row0 >= 0 && t.row0 <= a.T * a.k - t.rows;
   return t;
 }
 
-// h = silu(gate) up of 16 columns of a tile's rows, in fp32.
-__global__ void __launch_bounds__(kThreads) blk_few_gate_up_kernel(const BlkFewArgs a) {
+template <int kType>
+__global__ void __launch_bounds__(kThreads, 2) blk_few_gate_up_kernel(const BlkFewArgs a) {
   __shared__ Shared sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, blocks = blk_count(a.d);
-  pdl_wait();
-  pdl_launch_dependents();
+  const bool early = a.I_shared > 0 && blockIdx.y == 0;  // the shared expert's weights are known before the wait
+  if (!early) pdl_wait();
   const Tile tile = get_tile(a, blockIdx.y);
   if (!tile.ok) {
+    pdl_launch_dependents();
     if (threadIdx.x == 0 && (tile.some || (blockIdx.x == 0 && routed_tiles(a) == 0))) record_status(a.status, MOE_ERR_INVALID_ARG);
     return;
   }
   const int N = tile.shared ? a.I_shared : a.I;
-  if (n0 >= N) return;
+  if (n0 >= N) {
+    if (early) pdl_wait();
+    pdl_launch_dependents();
+    return;
+  }
   const BlkWeights& m = tile.shared ? a.shared : a.routed;
   const size_t matrix = static_cast<size_t>(tile.e) * N * a.d;
   const size_t sat = (static_cast<size_t>(tile.e) * blk_count(N) + n0 / kBlk) * blocks;
   const size_t first = tile.shared ? static_cast<size_t>(a.T) * a.k : tile.row0;
   const int pitch = max(a.I, a.I_shared);
-  for (int r0 = 0; r0 < tile.rows; r0 += kTokens) {
-    const int n = min(kTokens, tile.rows - r0);
-    float accg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, accu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = warp; kb < blocks; kb += kWarps) {
-      ABlock wg, wu;
-      wg.load(m.gate + matrix, n0, N, a.d, kb, lane);
-      wu.load(m.up + matrix, n0, N, a.d, kb, lane);
-      const float sg = __ldg(m.s_gate + sat + kb), su = __ldg(m.s_up + sat + kb);
-      Piece b;
-      float sa[2], d[4];
-      b_fragments(sm.codes[warp], n, lane, b, sa, [&](int i, float& s) {
-        int t = tile.shared ? r0 + i : __ldg(a.perm + tile.row0 + r0 + i) / a.k;
-        if (t < 0 || t >= a.T) {  // a malformed permutation
-          record_status(a.status, MOE_ERR_INVALID_ARG);
-          t = 0;
-        }
-        return x_block(a.x, t, kb, a.d, lane, s);
-      });
-      multiply(d, wg, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) accg[i] = fmaf(d[i], sa[i & 1] * sg, accg[i]);
-      multiply(d, wu, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) accu[i] = fmaf(d[i], sa[i & 1] * su, accu[i]);
+  ABlock wg, wu;
+  float sg = 0.0f, su = 0.0f;
+  auto load = [&](int kb) {
+    if (kb >= blocks) return;
+    wg.load(m.gate + matrix, n0, N, a.d, kb, lane);
+    wu.load(m.up + matrix, n0, N, a.d, kb, lane);
+    sg = __ldg(m.s_gate + sat + kb);
+    su = __ldg(m.s_up + sat + kb);
+  };
+  load(warp);
+  if (early) pdl_wait();
+  pdl_launch_dependents();
+  int mine = lane;  // the token of row `lane`
+  if (!tile.shared) {
+    mine = lane < tile.rows ? __ldg(a.perm + tile.row0 + lane) / a.k : 0;
+    if (mine < 0 || mine >= a.T) {  // a malformed permutation
+      record_status(a.status, MOE_ERR_INVALID_ARG);
+      mine = 0;
     }
-    put_sums(sm.sums[0][warp], accg, lane);
-    put_sums(sm.sums[1][warp], accu, lane);
-    __syncthreads();
-    if (threadIdx.x < kRows * kTokens) {
-      const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-      if (t < n && n0 + r < N)
-        a.h[(first + r0 + t) * pitch + n0 + r] = blk_swiglu(take_sum(sm.sums[0], kTokens * r + t), take_sum(sm.sums[1], kTokens * r + t));
+  }
+  float accg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, accu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int kb = warp; kb < blocks; kb += kWarps) {
+    Columns c(sm.codes[warp], lane);
+    for (int i0 = 0; i0 < tile.rows; i0 += 2) {  // two rows' loads in flight
+      XBlock<kType> x[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (i0 + i < tile.rows) x[i].load(a.x, __shfl_sync(0xffffffffu, mine, i0 + i), kb, a.d, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i0 + i >= tile.rows) break;
+        float sx;
+        const uint32_t q = x[i].codes(sx);
+        c.put(i0 + i, q, sx);
+      }
     }
-    __syncthreads();
+    Piece b;
+    float d[4];
+    c.take(b);
+    multiply(d, wg, b);
+    add(accg, d, c.sa[0] * sg, c.sa[1] * sg);
+    multiply(d, wu, b);
+    add(accu, d, c.sa[0] * su, c.sa[1] * su);
+    load(kb + kWarps);
+  }
+  put_sums(sm.sums[0][warp], accg, lane);
+  put_sums(sm.sums[1][warp], accu, lane);
+  __syncthreads();
+  if (threadIdx.x < kRows * kTokens) {
+    const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
+    if (t < tile.rows && n0 + r < N)
+      a.h[(first + t) * pitch + n0 + r] = blk_swiglu(take_sum(sm.sums[0], kTokens * r + t), take_sum(sm.sums[1], kTokens * r + t));
   }
 }
 
-// 16 columns of the experts' outputs, in fp32 rows.
+constexpr int kMaxRouted = kTokens * kMaxK;  // tiles and assignments of the routed experts at most
+struct SharedDown {
+  Shared p;
+  int e[kMaxRouted], row0[kMaxRouted], rows[kMaxRouted];  // of a routed tile; no rows: malformed
+  int token[kMaxRouted];                                  // of an assignment's row; -1: malformed
+  float w[kMaxRouted];
+};
 __global__ void __launch_bounds__(kThreads) blk_few_down_kernel(const BlkFewArgs a) {
-  __shared__ Shared sm;
+  __shared__ SharedDown sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * kRows;
+  const int n0 = blockIdx.x * kRows, A = a.T * a.k;
+  const int blocks_r = blk_count(a.I), blocks_s = a.I_shared > 0 ? blk_count(a.I_shared) : 0;
+  // (the routing has completed: see above)
+  const int nb = routed_tiles(a);
+  for (int i = threadIdx.x; i < max(nb, A); i += kThreads) {
+    if (i < nb) {
+      const Tile t = get_tile(a, i + (a.I_shared > 0 ? 1 : 0));
+      sm.e[i] = t.e;
+      sm.row0[i] = t.row0;
+      sm.rows[i] = t.ok ? t.rows : 0;
+    }
+    if (i < A) {
+      const int at = __ldg(a.perm + i);
+      const bool ok = at >= 0 && at < A;
+      sm.token[i] = ok ? at / a.k : -1;
+      sm.w[i] = ok ? __ldg(a.w + at) : 0.0f;
+      if (!ok) record_status(a.status, MOE_ERR_INVALID_ARG);
+    }
+  }
+  __syncthreads();
+  const int units = blocks_s + nb * blocks_r;
+  ABlock w[2];
+  float sw[2] = {0.0f, 0.0f};
+  auto load = [&](int u, ABlock& to, float& s) {
+    if (u >= units) return;
+    const bool shared = u < blocks_s;
+    const int i = shared ? 0 : (u - blocks_s) / blocks_r, kb = shared ? u : u - blocks_s - i * blocks_r;
+    const int e = shared ? 0 : sm.e[i], K = shared ? a.I_shared : a.I;
+    if (!shared && sm.rows[i] == 0) return;
+    const BlkWeights& m = shared ? a.shared : a.routed;
+    to.load(m.down + static_cast<size_t>(e) * a.d * K, n0, a.d, K, kb, lane);
+    s = __ldg(m.s_down + (static_cast<size_t>(e) * blk_count(a.d) + n0 / kBlk) * blk_count(K) + kb);
+  };
+  load(warp, w[0], sw[0]);
+  load(warp + kWarps, w[1], sw[1]);
   pdl_wait();
   pdl_launch_dependents();
-  const Tile tile = get_tile(a, blockIdx.y);
-  if (!tile.ok) return;
-  const int K = tile.shared ? a.I_shared : a.I, blocks = blk_count(K);
-  const BlkWeights& m = tile.shared ? a.shared : a.routed;
-  const uint8_t* w = m.down + static_cast<size_t>(tile.e) * a.d * K;
-  const float* sw = m.s_down + (static_cast<size_t>(tile.e) * blk_count(a.d) + n0 / kBlk) * blocks;
-  const size_t first = tile.shared ? static_cast<size_t>(a.T) * a.k : tile.row0;
   const int pitch = max(a.I, a.I_shared);
-  for (int r0 = 0; r0 < tile.rows; r0 += kTokens) {
-    const int n = min(kTokens, tile.rows - r0);
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = warp; kb < blocks; kb += kWarps) {
-      ABlock wd;
-      wd.load(w, n0, a.d, K, kb, lane);
-      const float s = __ldg(sw + kb);
-      Piece b;
-      float sa[2], d[4];
-      b_fragments(sm.codes[warp], n, lane, b, sa, [&](int i, float& scale) {
-        const int c = kb * kBlk + 4 * lane;
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (c < K) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(a.h + (first + r0 + i) * pitch + c));
-          f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-        }
-        return quantize4(f, scale);
-      });
-      multiply(d, wd, b);
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto take = [&](int u, const ABlock& m, float s) {
+    const bool shared = u < blocks_s;
+    const int i = shared ? 0 : (u - blocks_s) / blocks_r, kb = shared ? u : u - blocks_s - i * blocks_r;
+    const int K = shared ? a.I_shared : a.I, rows = shared ? a.T : sm.rows[i], row0 = shared ? 0 : sm.row0[i];
+    if (rows == 0) return;
+    const int c0 = kb * kBlk + 4 * lane;
+    Columns c(sm.p.codes[warp], lane);
+    for (int r0 = 0; r0 < rows; r0 += 2) {  // two rows' loads in flight
+      float4 v[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], sa[i & 1] * s, acc[i]);
+      for (int j = 0; j < 2; ++j)
+        v[j] = r0 + j < rows && c0 < K ? __ldcg(reinterpret_cast<const float4*>(a.h + ((shared ? A : row0) + r0 + j) * static_cast<size_t>(pitch) + c0))
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (r0 + j >= rows) break;
+        const int t = shared ? r0 + j : sm.token[row0 + r0 + j];
+        const float wt = shared ? 1.0f : sm.w[row0 + r0 + j];
+        const float f[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        float sx;
+        const uint32_t q = quantize4(f, sx);
+        if (t >= 0) c.put(t, q, sx * s * wt);
+      }
     }
-    put_sums(sm.sums[0][warp], acc, lane);
-    __syncthreads();
-    if (threadIdx.x < kRows * kTokens) {
-      const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-      if (t < n && n0 + r < a.d) a.ypart[(first + r0 + t) * a.d + n0 + r] = take_sum(sm.sums[0], kTokens * r + t);
-    }
-    __syncthreads();
+    Piece b;
+    float d[4];
+    c.take(b);
+    multiply(d, m, b);
+    add(acc, d, c.sa[0], c.sa[1]);
+  };
+  for (int u = warp; u < units; u += 2 * kWarps) {
+    take(u, w[0], sw[0]);
+    load(u + 2 * kWarps, w[0], sw[0]);
+    if (u + kWarps < units) take(u + kWarps, w[1], sw[1]);
+    load(u + 3 * kWarps, w[1], sw[1]);
+  }
+  put_sums(sm.p.sums[0][warp], acc, lane);
+  __syncthreads();
+  if (threadIdx.x < kRows * kTokens) {
+    const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
+    if (t < a.T && n0 + r < a.d)
+      a.y[static_cast<size_t>(t) * a.d + n0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(take_sum(sm.p.sums[0], kTokens * r + t)));
   }
 }
 
@@ -337,17 +446,19 @@ cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, cudaStream_t stream, 
 }  // namespace
 
 cudaError_t launch_blk_few_linear(const BlkFewLinearArgs& a, cudaStream_t stream, bool pdl) {
-  const int groups = (a.T + kTokens - 1) / kTokens;
-  return launch(kKBlkGemm, blk_few_linear_kernel, dim3((a.N + kRows - 1) / kRows, groups < 65535 ? groups : 65535), stream, pdl, a);
+  const auto kernel = a.x.type == kBf16   ? blk_few_linear_kernel<kBf16>
+                      : a.x.type == kFp16 ? blk_few_linear_kernel<kFp16>
+                      : a.x.type == kFp32 ? blk_few_linear_kernel<kFp32>
+                                          : blk_few_linear_kernel<kBlkCodes>;
+  return launch(kKBlkGemm, kernel, dim3((a.N + kRows - 1) / kRows), stream, pdl, a);
 }
 
 cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl) {
   const int tiles = a.tiles + (a.I_shared > 0 ? 1 : 0), I = a.I > a.I_shared ? a.I : a.I_shared;
-  cudaError_t e = launch(kKBlkGateUp, blk_few_gate_up_kernel, dim3((I + kRows - 1) / kRows, tiles), stream, pdl, a);
+  const auto gate_up = a.x.type == kBlkCodes ? blk_few_gate_up_kernel<kBlkCodes> : blk_few_gate_up_kernel<kBf16>;
+  const cudaError_t e = launch(kKBlkGateUp, gate_up, dim3((I + kRows - 1) / kRows, tiles), stream, pdl, a);
   if (e != cudaSuccess) return e;
-  e = launch(kKBlkDown, blk_few_down_kernel, dim3((a.d + kRows - 1) / kRows, tiles), stream, pdl, a);
-  if (e != cudaSuccess) return e;
-  return launch_mx_combine(a.ypart, a.inv_perm, a.w, a.T, a.d, a.k, a.I_shared > 0, a.y, a.status, a.num_sms, stream);
+  return launch(kKBlkDown, blk_few_down_kernel, dim3((a.d + kRows - 1) / kRows), stream, pdl, a);
 }
 
 }  // namespace bm

@@ -384,15 +384,13 @@ struct BlkWeights {
 struct BlkFewArgs {
   BlkX x;
   BlkWeights routed, shared;
-  const int32_t *perm, *inv_perm, *block_map, *num_blocks;
+  const int32_t *perm, *block_map, *num_blocks;
   const float* w;
-  float* h;       // [A + T][max(I, I_shared)]
-  float* ypart;   // [A + T][d]
+  float* h;    // [A + T][max(I, I_shared)]
   uint16_t* y;
   uint32_t* status;
   int T, d, I, k, I_shared, E;
-  int tiles, rows;  // tiles of the routed experts launched, rows of a tile at most
-  int num_sms;
+  int tiles;  // tiles of the routed experts launched
 };
 cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl);
 

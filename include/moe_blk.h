@@ -118,8 +118,7 @@ size_t moe_blk_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_
  *   Y[t] = sum_j w[t][j] FFN_{ids[t][j]}(x_t) + FFN_shared(x_t)
  *   FFN(x) = Q(silu(Q(x) Wg^T) * (Q(x) Wu^T)) Wd^T
  * with Q() the rounding of moe_blk_quantize; the products, SwiGLU and the sums
- * over experts (in slot order, the shared expert last) are in fp32, and Y is
- * rounded to bf16 once.
+ * over experts are in fp32, and Y is rounded to bf16 once.
  *   X, XQ   bf16 X [T][d], or the activations XQ [T][d] that moe_rmsnorm or
  *           moe_blk_quantize wrote, taken as they are: one of them, the other
  *           NULL
