@@ -58,6 +58,15 @@ moe_status few_linear(const BlkX& x, int M, const moe_blk_mat* W, int N, int K, 
 
 int round16(int x) { return (x + 15) & ~15; }
 
+// Whether the product for few tokens is the faster one: its time grows with the weights' bytes and, past two MMAs' tokens,
+// with the tokens that go with them, the tensor cores' with the depth.  Measured (us, few / tensor cores; 32 tokens): 2048
+// x 2048 4.3 / 8.4, 4096 x 4096 10.2 / 12.9, 2048 -> 8192 11.0 / 8.5, 8192 x 8192 38 / 22; 8 tokens 2.8 / 8.3 and 18.8 /
+// 20.7 of the first and the last, 16 tokens 21.9 / 21.0 of the last.
+bool few_linear_wins(int M, int N, int K) {
+  if (M <= kBlkFewLinear / 2) return true;
+  return M <= kBlkFewLinear && 0.52e-6 * N * K < 2.5 + 0.00207 * K;
+}
+
 // Height of the dense product's token tiles.
 int linear_tile(int M, int N, int K, int num_sms) {
   (void)K;
@@ -68,7 +77,7 @@ int linear_tile(int M, int N, int K, int num_sms) {
 
 moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
                   uint32_t* status, moe_stream stream) {
-  if (M <= kBlkFewT) return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
+  if (few_linear_wins(M, N, K)) return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
   BlkLinearArgs a{};
   a.sw = W->s;
   a.sx = A.s;
@@ -321,7 +330,7 @@ moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long lo
   if (T == 0) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
   const moe_blk_mat xq{w, reinterpret_cast<float*>(w + round256(static_cast<size_t>(T) * K))};
-  if (T <= kBlkFewT) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
+  if (T == 1) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
   if (launch_blk_quantize(X, x_type, T, K, ldx, xq.q, xq.s, cuda(stream), pdl_enabled()) != cudaSuccess) return MOE_ERR_CUDA;
   return matmul(xq, T, W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
 }

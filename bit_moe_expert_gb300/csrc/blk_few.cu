@@ -21,8 +21,13 @@ namespace {
 
 constexpr int kRows = 16;     // weight rows of a CTA
 constexpr int kTokens = 8;    // an MMA's N
-constexpr int kWarps = 16;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+// A warp's blocks whose weights are in flight together.  Two CTAs an SM hold 128
+// KB of them: with 16 warps of one block each (and one CTA's registers an SM) one
+// token's expert layer took 13.6 us, 1 x 8192 -> 8192 21.8.
+constexpr int kDepth = 4;       // linear, down
+constexpr int kDepthGU = 2;     // gate/up: of both matrices
 
 // D += A B, m16n8k32, E4M3 operands four to a register (lowest index in the
 // lowest byte), fp32 accumulators; g = lane/4, q = lane%4:
@@ -173,49 +178,108 @@ __device__ __forceinline__ void add(float (&acc)[4], const float (&d)[4], float 
   acc[3] = fmaf(d[3], s1, acc[3]);
 }
 
+// One token whose activations are quantised here, each block by the warp that
+// needs it.  (For more tokens every CTA would do that again: 4 x 8192 -> 8192 took
+// 26.7 us, quantised by a kernel of its own 16.)
 template <int kType>
-__global__ void __launch_bounds__(kThreads) blk_few_linear_kernel(const BlkFewLinearArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) blk_one_linear_kernel(const BlkFewLinearArgs a) {
   __shared__ Shared sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, blocks = blk_count(a.K);
   const float* sw = a.sw + static_cast<size_t>(n0 / kBlk) * blocks;
-  ABlock w;
-  float s = 0.0f;
-  auto load = [&](int kb) {
+  ABlock w[kDepth];
+  float s[kDepth];
+  auto load = [&](int kb, int to) {
     if (kb >= blocks) return;
-    w.load(a.w, n0, a.N, a.K, kb, lane);
-    s = __ldg(sw + kb);
+    w[to].load(a.w, n0, a.N, a.K, kb, lane);
+    s[to] = __ldg(sw + kb);
   };
-  load(warp);
+#pragma unroll
+  for (int j = 0; j < kDepth; ++j) load(warp + j * kWarps, j);
   pdl_wait();
   pdl_launch_dependents();
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = warp; kb < blocks; kb += kWarps) {
-    XBlock<kType> x[kTokens];
+  for (int kb0 = warp; kb0 < blocks; kb0 += kDepth * kWarps) {
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i)
-      if (i < a.T) x[i].load(a.x, i, kb, a.K, lane);
-    Columns c(sm.codes[warp], lane);
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      if (i >= a.T) break;
+    for (int j = 0; j < kDepth; ++j) {
+      const int kb = kb0 + j * kWarps;
+      if (kb >= blocks) break;
+      XBlock<kType> x;
+      x.load(a.x, 0, kb, a.K, lane);
+      Columns c(sm.codes[warp], lane);
       float sx;
-      const uint32_t q = x[i].codes(sx);
-      c.put(i, q, sx);
+      const uint32_t q = x.codes(sx);
+      c.put(0, q, sx);
+      Piece b;
+      float d[4];
+      c.take(b);
+      multiply(d, w[j], b);
+      add(acc, d, c.sa[0] * s[j], c.sa[1] * s[j]);
+      load(kb + kDepth * kWarps, j);
     }
-    Piece b;
-    float d[4];
-    c.take(b);
-    multiply(d, w, b);
-    add(acc, d, c.sa[0] * s, c.sa[1] * s);
-    load(kb + kWarps);
   }
   put_sums(sm.sums[0][warp], acc, lane);
   __syncthreads();
-  if (threadIdx.x < kRows * kTokens) {
-    const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-    if (t < a.T && n0 + r < a.N) store1(a.y_type, a.y, static_cast<size_t>(t) * a.N + n0 + r, take_sum(sm.sums[0], kTokens * r + t));
+  if (threadIdx.x < kRows && n0 + threadIdx.x < a.N)
+    store1(a.y_type, a.y, static_cast<size_t>(n0) + threadIdx.x, take_sum(sm.sums[0], kTokens * threadIdx.x));
+}
+
+// Up to 8 kGroups tokens that are quantised already: a lane's 32 bytes of its
+// column's token are the B fragments, as its bytes of two rows are the A fragments.
+template <int kGroups>
+__global__ void __launch_bounds__(kThreads, 2) blk_few_linear_kernel(const BlkFewLinearArgs a) {
+  __shared__ float sums[kGroups][kWarps][kRows * kTokens];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * kRows, blocks = blk_count(a.K);
+  const float* sw = a.sw + static_cast<size_t>(n0 / kBlk) * blocks;
+  constexpr int kHere = kGroups > 1 ? kDepth / 2 : kDepth;  // the tokens' registers take the place of weights
+  ABlock w[kHere];
+  float s[kHere];
+  auto load = [&](int kb, int to) {
+    if (kb >= blocks) return;
+    w[to].load(a.w, n0, a.N, a.K, kb, lane);
+    s[to] = __ldg(sw + kb);
+  };
+#pragma unroll
+  for (int j = 0; j < kHere; ++j) load(warp + j * kWarps, j);
+  pdl_wait();
+  pdl_launch_dependents();
+  float acc[kGroups][4];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
+  const int g8 = lane >> 2, q2 = 2 * (lane & 3);
+  const uint8_t* x = static_cast<const uint8_t*>(a.x.x);
+  for (int kb0 = warp; kb0 < blocks; kb0 += kHere * kWarps) {
+#pragma unroll
+    for (int j = 0; j < kHere; ++j) {
+      const int kb = kb0 + j * kWarps;
+      if (kb >= blocks) break;
+      Piece b[kGroups];
+      float2 sa[kGroups];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int t = kTokens * g + g8;
+        if (t < a.T) b[g].load(x + static_cast<size_t>(t) * a.K, kb * kBlk + 32 * (lane & 3), a.K); else b[g].zero();
+        // (the scales' rows are padded to a multiple of four: a pair that starts at a token is there)
+        const int t2 = kTokens * g + q2;
+        sa[g] = t2 < a.T ? __ldg(reinterpret_cast<const float2*>(a.x.s + kb * a.x.pitch + t2)) : make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        float d[4];
+        multiply(d, w[j], b[g]);
+        add(acc[g], d, sa[g].x * s[j], sa[g].y * s[j]);
+      }
+      load(kb + kHere * kWarps, j);
+    }
   }
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) put_sums(sums[g][warp], acc[g], lane);
+  __syncthreads();
+  const int r = threadIdx.x & 15;
+  if (n0 + r < a.N)
+    for (int t = threadIdx.x >> 4; t < min(a.T, kTokens * kGroups); t += kThreads / kRows)
+      store1(a.y_type, a.y, static_cast<size_t>(t) * a.N + n0 + r, take_sum(sums[t / kTokens], kTokens * r + t % kTokens));
 }
 
 // ------------------------------------------------------------------ experts
@@ -277,16 +341,17 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_gate_up_kernel(const BlkF
   const size_t sat = (static_cast<size_t>(tile.e) * blk_count(N) + n0 / kBlk) * blocks;
   const size_t first = tile.shared ? static_cast<size_t>(a.T) * a.k : tile.row0;
   const int pitch = max(a.I, a.I_shared);
-  ABlock wg, wu;
-  float sg = 0.0f, su = 0.0f;
-  auto load = [&](int kb) {
+  ABlock wg[kDepthGU], wu[kDepthGU];
+  float sg[kDepthGU], su[kDepthGU];
+  auto load = [&](int kb, int to) {
     if (kb >= blocks) return;
-    wg.load(m.gate + matrix, n0, N, a.d, kb, lane);
-    wu.load(m.up + matrix, n0, N, a.d, kb, lane);
-    sg = __ldg(m.s_gate + sat + kb);
-    su = __ldg(m.s_up + sat + kb);
+    wg[to].load(m.gate + matrix, n0, N, a.d, kb, lane);
+    wu[to].load(m.up + matrix, n0, N, a.d, kb, lane);
+    sg[to] = __ldg(m.s_gate + sat + kb);
+    su[to] = __ldg(m.s_up + sat + kb);
   };
-  load(warp);
+#pragma unroll
+  for (int j = 0; j < kDepthGU; ++j) load(warp + j * kWarps, j);
   if (early) pdl_wait();
   pdl_launch_dependents();
   int mine = lane;  // the token of row `lane`
@@ -298,29 +363,34 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_gate_up_kernel(const BlkF
     }
   }
   float accg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, accu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = warp; kb < blocks; kb += kWarps) {
-    Columns c(sm.codes[warp], lane);
-    for (int i0 = 0; i0 < tile.rows; i0 += 2) {  // two rows' loads in flight
-      XBlock<kType> x[2];
+  for (int kb0 = warp; kb0 < blocks; kb0 += kDepthGU * kWarps) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (i0 + i < tile.rows) x[i].load(a.x, __shfl_sync(0xffffffffu, mine, i0 + i), kb, a.d, lane);
+    for (int j = 0; j < kDepthGU; ++j) {
+      const int kb = kb0 + j * kWarps;
+      if (kb >= blocks) break;
+      Columns c(sm.codes[warp], lane);
+      for (int i0 = 0; i0 < tile.rows; i0 += 2) {  // two rows' loads in flight
+        XBlock<kType> x[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i0 + i >= tile.rows) break;
-        float sx;
-        const uint32_t q = x[i].codes(sx);
-        c.put(i0 + i, q, sx);
+        for (int i = 0; i < 2; ++i)
+          if (i0 + i < tile.rows) x[i].load(a.x, __shfl_sync(0xffffffffu, mine, i0 + i), kb, a.d, lane);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i0 + i >= tile.rows) break;
+          float sx;
+          const uint32_t q = x[i].codes(sx);
+          c.put(i0 + i, q, sx);
+        }
       }
+      Piece b;
+      float d[4];
+      c.take(b);
+      multiply(d, wg[j], b);
+      add(accg, d, c.sa[0] * sg[j], c.sa[1] * sg[j]);
+      multiply(d, wu[j], b);
+      add(accu, d, c.sa[0] * su[j], c.sa[1] * su[j]);
+      load(kb + kDepthGU * kWarps, j);
     }
-    Piece b;
-    float d[4];
-    c.take(b);
-    multiply(d, wg, b);
-    add(accg, d, c.sa[0] * sg, c.sa[1] * sg);
-    multiply(d, wu, b);
-    add(accu, d, c.sa[0] * su, c.sa[1] * su);
-    load(kb + kWarps);
   }
   put_sums(sm.sums[0][warp], accg, lane);
   put_sums(sm.sums[1][warp], accu, lane);
@@ -339,7 +409,7 @@ struct SharedDown {
   int token[kMaxRouted];                                  // of an assignment's row; -1: malformed
   float w[kMaxRouted];
 };
-__global__ void __launch_bounds__(kThreads) blk_few_down_kernel(const BlkFewArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) blk_few_down_kernel(const BlkFewArgs a) {
   __shared__ SharedDown sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, A = a.T * a.k;
@@ -363,8 +433,8 @@ __global__ void __launch_bounds__(kThreads) blk_few_down_kernel(const BlkFewArgs
   }
   __syncthreads();
   const int units = blocks_s + nb * blocks_r;
-  ABlock w[2];
-  float sw[2] = {0.0f, 0.0f};
+  ABlock w[kDepth];
+  float sw[kDepth];
   auto load = [&](int u, ABlock& to, float& s) {
     if (u >= units) return;
     const bool shared = u < blocks_s;
@@ -375,8 +445,8 @@ __global__ void __launch_bounds__(kThreads) blk_few_down_kernel(const BlkFewArgs
     to.load(m.down + static_cast<size_t>(e) * a.d * K, n0, a.d, K, kb, lane);
     s = __ldg(m.s_down + (static_cast<size_t>(e) * blk_count(a.d) + n0 / kBlk) * blk_count(K) + kb);
   };
-  load(warp, w[0], sw[0]);
-  load(warp + kWarps, w[1], sw[1]);
+#pragma unroll
+  for (int j = 0; j < kDepth; ++j) load(warp + j * kWarps, w[j], sw[j]);
   pdl_wait();
   pdl_launch_dependents();
   const int pitch = max(a.I, a.I_shared);
@@ -411,11 +481,14 @@ __global__ void __launch_bounds__(kThreads) blk_few_down_kernel(const BlkFewArgs
     multiply(d, m, b);
     add(acc, d, c.sa[0], c.sa[1]);
   };
-  for (int u = warp; u < units; u += 2 * kWarps) {
-    take(u, w[0], sw[0]);
-    load(u + 2 * kWarps, w[0], sw[0]);
-    if (u + kWarps < units) take(u + kWarps, w[1], sw[1]);
-    load(u + 3 * kWarps, w[1], sw[1]);
+  for (int u0 = warp; u0 < units; u0 += kDepth * kWarps) {
+#pragma unroll
+    for (int j = 0; j < kDepth; ++j) {
+      const int u = u0 + j * kWarps;
+      if (u >= units) break;
+      take(u, w[j], sw[j]);
+      load(u + kDepth * kWarps, w[j], sw[j]);
+    }
   }
   put_sums(sm.p.sums[0][warp], acc, lane);
   __syncthreads();
@@ -446,10 +519,12 @@ cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, cudaStream_t stream, 
 }  // namespace
 
 cudaError_t launch_blk_few_linear(const BlkFewLinearArgs& a, cudaStream_t stream, bool pdl) {
-  const auto kernel = a.x.type == kBf16   ? blk_few_linear_kernel<kBf16>
-                      : a.x.type == kFp16 ? blk_few_linear_kernel<kFp16>
-                      : a.x.type == kFp32 ? blk_few_linear_kernel<kFp32>
-                                          : blk_few_linear_kernel<kBlkCodes>;
+  const auto kernel = a.x.type == kBf16   ? blk_one_linear_kernel<kBf16>
+                      : a.x.type == kFp16 ? blk_one_linear_kernel<kFp16>
+                      : a.x.type == kFp32 ? blk_one_linear_kernel<kFp32>
+                      : a.T <= kTokens    ? blk_few_linear_kernel<1>
+                      : a.T <= 2 * kTokens ? blk_few_linear_kernel<2>
+                                           : blk_few_linear_kernel<4>;
   return launch(kKBlkGemm, kernel, dim3((a.N + kRows - 1) / kRows), stream, pdl, a);
 }
 

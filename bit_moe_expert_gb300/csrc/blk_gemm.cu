@@ -68,6 +68,7 @@ Plan make_plan(int mats, int bn) {
     // the scales of a block are read until its accumulator is free again, which may be `accs` stages after the
     // stage's codes: a ring of their own
     p.scale_slots = p.stages + p.accs;
+    if (p.accs > p.stages) p.accs = p.stages;  // (no fewer than six stages are found)
     if (p.stages * p.stage_bytes + p.scale_slots * bn * 4 + kSmemFixed <= kSmemLimit) return p;
   }
 }
@@ -185,10 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* scales = reinterpret_cast<float*>(stages + p.stages * p.stage_bytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + p.scale_slots * p.bn);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* acc_full = empty + kMaxStages;
-  uint64_t* acc_empty = acc_full + kMaxAccs;
-  uint64_t* scale_full = acc_empty + kMaxAccs;
-  uint64_t* part_met = scale_full + kMaxStages + kMaxAccs;  // a share's four warps have written their maxima
+  uint64_t* acc_empty = empty + kMaxStages;
+  uint64_t* part_met = acc_empty + kMaxAccs;  // a share's four warps have written their maxima
   uint64_t* finished = part_met + kParts;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(finished + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -208,13 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 2);  // the weights' and the activations' expect_tx; their bytes complete the phase
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // the MMAs' commit, and their issuer, who has seen the stage's scales land
     }
-    for (int i = 0; i < p.accs; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kSumWarps);
-    }
-    for (int i = 0; i < p.scale_slots; ++i) mbar_init(&scale_full[i], 1);
+    for (int i = 0; i < p.accs; ++i) mbar_init(&acc_empty[i], kSumWarps);
     for (int i = 0; i < kParts; ++i) mbar_init(&part_met[i], 4);
     mbar_init(finished, 1);
     *abort_flag = 0;
@@ -241,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool weights = warp == kWeightsWarp;
         if (!weights) pdl_wait();
         int stage = 0, slot = 0, filled = 0;
-        uint32_t phase = 0, slot_phase = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int i = 0; i < s.n && ok; ++i) {
           const Item m = item(i);
@@ -261,15 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(st, m.m0, bar, kb * kBlk, m.row_m, m.e);
               if (kGU) tma_load_3d(st + kMatBytes, m.m1, bar, kb * kBlk, m.row_m, m.e);
             } else {
-              mbar_arrive_expect_tx(bar, m.box * 128);
+              mbar_arrive_expect_tx(bar, m.box * 128 + m.sn_bytes);
               tma_load_2d(st + kMats * kMatBytes, m.n, bar, kb * kBlk, m.row_n);
-              mbar_arrive_expect_tx(&scale_full[slot], m.sn_bytes);
-              bulk_g2s(scales + slot * p.bn, sn, m.sn_bytes, &scale_full[slot]);
+              bulk_g2s(scales + slot * p.bn, sn, m.sn_bytes, bar);
               sn += m.sn_step;
-              if (++slot == p.scale_slots) {
-                slot = 0;
-                slot_phase ^= 1;
-              }
+              if (++slot == p.scale_slots) slot = 0;
             }
             if (++stage == p.stages) {
               stage = 0;
@@ -282,11 +273,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage = stage == 0 ? p.stages - 1 : stage - 1;
           if (stage == p.stages - 1) phase ^= 1;
           if (!mbar_wait(&full[stage], phase, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
-        }
-        for (int i = 0; i < min(filled, p.scale_slots) && !weights; ++i) {
-          slot = slot == 0 ? p.scale_slots - 1 : slot - 1;
-          if (slot == p.scale_slots - 1) slot_phase ^= 1;
-          if (!mbar_wait(&scale_full[slot], slot_phase, nullptr)) record_status(a.status, MOE_ERR_TIMEOUT);
         }
         if (weights) pdl_wait();
       }
@@ -325,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_mma_f8(d + mat * p.bn, ad + mat * (kMatBytes >> 4) + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
               }
             tc_commit(&empty[stage]);
-            tc_commit(&acc_full[accb]);
+            mbar_arrive(&empty[stage]);
           }
           at += stage_step;
           if (++stage == p.stages) {
@@ -352,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
     const int quarter = warp & 3, part = (warp - kSumWarp0) >> 2;
-    int accb = 0, slot = 0;
-    uint32_t accphase = 0, slot_phase = 0, parity = 0;
+    int accb = 0, slot = 0, stage = 0;
+    uint32_t phase = 0, parity = 0;
     bool ok = true;
     for (int i = 0; i < s.n && ok; ++i) {
       const Item m = item(i);
@@ -375,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sw0 = kb + lane < blocks ? __ldg(m.s0 + kb + lane) : 0.0f;
           if (kGU) sw1 = kb + lane < blocks ? __ldg(m.s1 + kb + lane) : 0.0f;
         }
-        if (!mbar_wait(&scale_full[slot], slot_phase, abort_flag) || !mbar_wait(&acc_full[accb], accphase, abort_flag)) {
+        // the stage's barrier tells that its MMAs have completed, to the loads that take its place and to the sums: it
+        // cannot be a phase further before these have released the accumulator (there are no more of them than stages)
+        if (!mbar_wait(&empty[stage], phase, abort_flag)) {
           if (lane == 0) fail();
           ok = false;
           break;
@@ -416,13 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[accb]);
-        if (++slot == p.scale_slots) {
-          slot = 0;
-          slot_phase ^= 1;
-        }
-        if (++accb == p.accs) {
-          accb = 0;
-          accphase ^= 1;
+        if (++slot == p.scale_slots) slot = 0;
+        if (++accb == p.accs) accb = 0;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
       if (!ok) break;

@@ -366,8 +366,10 @@ struct BlkX {
   long long ldx, pitch;
   int type;
 };
-// Few tokens (an MMA's eight columns): weights straight into the registers of warp-level MMAs.
-constexpr int kBlkFewT = 8;
+// Few tokens: weights straight into the registers of warp-level MMAs.  One token of any type, or up to kBlkFewLinear
+// that are codes; experts up to kBlkFewT (an MMA's eight columns are the most).
+constexpr int kBlkFewT = 2;
+constexpr int kBlkFewLinear = 32;
 struct BlkFewLinearArgs {
   BlkX x;
   const uint8_t* w;
