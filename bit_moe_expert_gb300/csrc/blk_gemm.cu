@@ -14,8 +14,8 @@
 // lanes.  A stage of the pipeline is K = 128: one 128-byte line of codes a row (the
 // widest swizzle atom) and the tokens' scales, four MMAs of K = 32.
 //
-// Roles (one persistent CTA per SM): warps 0 and 1 the weights' and the
-// activations' loads, warp 2 the MMAs' issue, warps 4 to 11 the sums: two per
+// Roles (one persistent CTA per SM): warps 0, 1 and 3 the loads of the weights, of
+// the activations and of their scales, warp 2 the MMAs' issue, warps 4 to 11 the sums: two per
 // quarter of the tensor-memory lanes, the tokens' groups in turn.  Every wait is
 // bounded and records MOE_ERR_TIMEOUT.
 #include <cuda_runtime.h>
@@ -30,6 +30,7 @@ namespace {
 constexpr int kWeightsWarp = 0;
 constexpr int kActivationsWarp = 1;
 constexpr int kMmaWarp = 2;
+constexpr int kScalesWarp = 3;
 constexpr int kSumWarp0 = 4;
 constexpr int kSumWarps = 8;
 constexpr int kParts = kSumWarps / 4;  // shares of the tokens
@@ -95,6 +96,25 @@ __device__ __forceinline__ uint32_t transpose_bytes(uint32_t v, int lane) {
   return (lane & 1) ? __byte_perm(v, t, 0x3715) : __byte_perm(v, t, 0x6240);
 }
 
+// A lane's column of a tile's rows: the first one's place, the others `pitch` apart.
+template <typename V, typename T, typename Round>
+__device__ __forceinline__ void store_columns(T* y, long long pitch, int rows, const Sums<V>& acc, int part, Round round) {
+#pragma unroll
+  for (int g = 0; g < V::kGroups; ++g) {
+    const int c0 = V::kGroup * (g * kParts + part);
+    if (c0 >= rows) break;
+    T* at = y + c0 * pitch;
+    if (c0 + V::kGroup <= rows) {
+#pragma unroll
+      for (int c = 0; c < V::kGroup; ++c, at += pitch) *at = round(acc.get(0, g, c));
+    } else {
+#pragma unroll
+      for (int c = 0; c < V::kGroup; ++c, at += pitch)
+        if (c0 + c < rows) *at = round(acc.get(0, g, c));
+    }
+  }
+}
+
 // gate/up: h = silu(gate) up, quantised here.  A tile's 128 columns are one block
 // of h: a token's largest magnitude is a reduction over the lanes and the share's
 // four warps.  meet(): waits for those (false: given up).
@@ -149,14 +169,8 @@ __device__ __forceinline__ bool epilogue(const BlkExpertArgs& a, const Item& m, 
     // fp32 rows of the experts' outputs, routed ones in permuted order, then the shared expert's in token order
     const int n = m.mt * kBlk + 32 * quarter + lane;
     if (n >= a.d) return true;
-    float* y = a.ypart + (static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0) * a.d + n;
-#pragma unroll
-    for (int g = 0; g < V::kGroups; ++g) {
-      const int c0 = V::kGroup * (g * kParts + part);
-#pragma unroll
-      for (int c = 0; c < V::kGroup; ++c)
-        if (c0 + c < m.rows) y[static_cast<size_t>(c0 + c) * a.d] = acc.get(0, g, c);
-    }
+    store_columns<V>(a.ypart + (static_cast<size_t>(m.shared ? a.T * a.k : 0) + m.row0) * a.d + n, a.d, m.rows, acc, part,
+                     [](float x) { return x; });
   }
   return true;
 }
@@ -165,15 +179,21 @@ __device__ __forceinline__ bool epilogue(const BlkLinearArgs& a, const Item& m, 
                                          uint32_t (*)[kMaxTile], Meet) {
   const int n = m.row_m + 32 * quarter + lane;
   if (n >= a.N) return true;
-#pragma unroll
-  for (int g = 0; g < V::kGroups; ++g) {
-    const int c0 = V::kGroup * (g * kParts + part);
-#pragma unroll
-    for (int c = 0; c < V::kGroup; ++c)
-      if (c0 + c < m.rows) store1(a.y_type, a.y, (static_cast<size_t>(m.row_n) + c0 + c) * a.N + n, acc.get(0, g, c));
-  }
+  const size_t at = static_cast<size_t>(m.row_n) * a.N + n;
+  if (a.y_type == kFp32)
+    store_columns<V>(static_cast<float*>(a.y) + at, a.N, m.rows, acc, part, [](float x) { return x; });
+  else if (a.y_type == kFp16)
+    store_columns<V>(static_cast<__half*>(a.y) + at, a.N, m.rows, acc, part, [](float x) { return __float2half_rn(x); });
+  else
+    store_columns<V>(static_cast<__nv_bfloat16*>(a.y) + at, a.N, m.rows, acc, part, [](float x) { return __float2bfloat16_rn(x); });
   return true;
 }
+
+__device__ __forceinline__ void prefetch_maps(const BlkLinearMaps& m) {
+  tma_prefetch_desc(&m.w);
+  tma_prefetch_desc(&m.x);
+}
+__device__ __forceinline__ void prefetch_maps(const BlkExpertMaps&) {}
 
 template <typename V>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -204,9 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto item = [&](int i) {
     return get_item<kBlk>(a, maps, p.bn, i < kEntries ? entries[i] : make_entry(a, s, s.first + i * s.step), kGU);
   };
+  if (threadIdx.x == 32) prefetch_maps(maps);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], 2);  // the weights' and the activations' expect_tx; their bytes complete the phase
+      mbar_init(&full[i], 3);  // the weights', the activations' and the scales' expect_tx; their bytes complete the phase
       mbar_init(&empty[i], 2);  // the MMAs' commit, and their issuer, who has seen the stage's scales land
     }
     for (int i = 0; i < p.accs; ++i) mbar_init(&acc_empty[i], kSumWarps);
@@ -230,8 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSumWarp0) {
     if constexpr (V::kUneven) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kWeightsWarp || warp == kActivationsWarp) {
-      // one thread for the weights, which starts before the wait, and one for the activations
+    if (warp != kMmaWarp) {
+      // one thread for the weights, which starts before the wait, one for the activations' codes and one for their scales
+      // (each copy takes its thread some 100 clocks to issue)
       if (lane == 0) {
         const bool weights = warp == kWeightsWarp;
         if (!weights) pdl_wait();
@@ -255,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx(bar, kMats * kMatBytes);
               tma_load_3d(st, m.m0, bar, kb * kBlk, m.row_m, m.e);
               if (kGU) tma_load_3d(st + kMatBytes, m.m1, bar, kb * kBlk, m.row_m, m.e);
-            } else {
-              mbar_arrive_expect_tx(bar, m.box * 128 + m.sn_bytes);
+            } else if (warp == kActivationsWarp) {
+              mbar_arrive_expect_tx(bar, m.box * 128);
               tma_load_2d(st + kMats * kMatBytes, m.n, bar, kb * kBlk, m.row_n);
+            } else {
+              mbar_arrive_expect_tx(bar, m.sn_bytes);
               bulk_g2s(scales + slot * p.bn, sn, m.sn_bytes, bar);
               sn += m.sn_step;
               if (++slot == p.scale_slots) slot = 0;
@@ -277,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (weights) pdl_wait();
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else {
       pdl_wait();
       pdl_launch_dependents();
       // One thread issues everything; what it issues is computed by the whole warp
@@ -379,31 +403,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b1 = kGU ? __float_as_uint(__shfl_sync(0xffffffffu, sw1, kb & 31)) : 0u;
           w[1] = pack2(b1, b1);
         }
+        // all groups, whether the tile has rows for them or not (a branch for each costs more: 64 x 8192 -> 8192 27.5
+        // instead of 21.6 us; accumulators and scales end inside what is allocated), the scales beside the loads
+        uint32_t d[V::kGroups][kMats][V::kGroup];
+        uint64_t f[V::kGroups][V::kGroup / 2];
 #pragma unroll
         for (int g = 0; g < V::kGroups; ++g) {
           const int c0 = V::kGroup * (g * kParts + part);
-          if (c0 < m.rows) {
-            uint32_t d[kMats][V::kGroup];
 #pragma unroll
-            for (int mat = 0; mat < kMats; ++mat) tmem_ld<V::kGroup>(tbase + mat * p.bn + c0, d[mat]);
-            uint64_t sc[V::kGroup / 2];
+          for (int mat = 0; mat < kMats; ++mat) tmem_ld<V::kGroup>(tbase + mat * p.bn + c0, d[g][mat]);
 #pragma unroll
-            for (int c = 0; c < V::kGroup / 4; ++c) {
-              const uint4 f = *reinterpret_cast<const uint4*>(sn + c0 + 4 * c);
-              sc[2 * c] = pack2(f.x, f.y);
-              sc[2 * c + 1] = pack2(f.z, f.w);
+          for (int c = 0; c < V::kGroup / 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sn + c0 + 4 * c);
+            f[g][2 * c] = pack2(v.x, v.y);
+            f[g][2 * c + 1] = pack2(v.z, v.w);
+            if (kMats == 1) {
+              f[g][2 * c] = mul2(f[g][2 * c], w[0]);
+              f[g][2 * c + 1] = mul2(f[g][2 * c + 1], w[0]);
             }
-            tc_wait_ld();
-#pragma unroll
-            for (int mat = 0; mat < kMats; ++mat)
-#pragma unroll
-              for (int c = 0; c < V::kGroup / 2; ++c)
-                fma2(acc.v[mat][g][c], pack2(d[mat][2 * c], d[mat][2 * c + 1]), mul2(sc[c], w[mat]));
           }
         }
+        tc_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[accb]);
+#pragma unroll
+        for (int g = 0; g < V::kGroups; ++g)
+#pragma unroll
+          for (int c = 0; c < V::kGroup / 2; ++c)
+#pragma unroll
+            for (int mat = 0; mat < kMats; ++mat)
+              fma2(acc.v[mat][g][c], pack2(d[g][mat][2 * c], d[g][mat][2 * c + 1]), kMats == 1 ? f[g][c] : mul2(f[g][c], w[mat]));
         if (++slot == p.scale_slots) slot = 0;
         if (++accb == p.accs) accb = 0;
         if (++stage == p.stages) {
