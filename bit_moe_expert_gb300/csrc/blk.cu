@@ -247,11 +247,9 @@ struct NormArgs {
 
 constexpr float kNormError = 4.76837158e-7f;  // 2^-21
 
-// The eight values of y in 64 bits.
-__device__ __noinline__ void exact_values(const float (&r)[8], const float (&g)[8], Pair inv, double (&y)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    y[j] = static_cast<double>(r[j]) * (static_cast<double>(inv.hi) + static_cast<double>(inv.lo)) * static_cast<double>(g[j]);
+// y in 64 bits.
+__device__ __forceinline__ double exact_value(float r, float g, Pair inv) {
+  return static_cast<double>(r) * (static_cast<double>(inv.hi) + static_cast<double>(inv.lo)) * static_cast<double>(g);
 }
 
 template <int kType, int kResidual, int kChunks>
@@ -343,10 +341,9 @@ __global__ void __launch_bounds__(1024)
     const float m = __uint_as_float(half_warp_max(largest_bits(y)));
     float s = blk_scale(__float_as_uint(m * (1.0f - kNormError)));
     if (__any_sync(0xffffffffu, __float_as_uint(s) != __float_as_uint(blk_scale(__float_as_uint(m * (1.0f + kNormError)))))) {
-      double v[8], most = 0.0;
-      exact_values(r[i], g[gi], inv, v);
+      double most = 0.0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) most = fmax(most, fabs(v[j]));
+      for (int j = 0; j < 8; ++j) most = fmax(most, fabs(exact_value(r[i][j], g[gi][j], inv)));
 #pragma unroll
       for (int k = 1; k < 16; k *= 2) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, k));
       if (m == m) s = blk_scale(__float_as_uint(odd_float(most)));
@@ -355,10 +352,8 @@ __global__ void __launch_bounds__(1024)
     uint2 code = blk_codes8(y, t * (1.0f - kNormError));
     const uint2 other = blk_codes8(y, t * (1.0f + kNormError));
     if (code.x != other.x || code.y != other.y) {
-      double v[8];
-      exact_values(r[i], g[gi], inv, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = odd_float(v[j] * static_cast<double>(t));
+      for (int j = 0; j < 8; ++j) y[j] = odd_float(exact_value(r[i][j], g[gi][j], inv) * static_cast<double>(t));
       code = blk_codes8(y, 1.0f);
     }
     if (col < a.d) {
@@ -478,8 +473,10 @@ constexpr size_t kMaxUnits = 0x7FFFFFFFu / (kThreads / 32);  // a unit's number 
 
 template <int kType>
 cudaError_t launch_norm(const NormArgs& a, int residual, cudaStream_t stream, bool pdl) {
-  // two chunks a thread, or more where a CTA would have too many threads; one for few rows, where latency counts
-  int chunks = a.T < 512 ? 1 : 2;
+  // one chunk a thread for few rows, where latency counts; more of them where there are many, so that an SM has more
+  // CTAs, which wait for their sums at different times (8192 rows of 8192 with the residual, 1 / 2 / 4 chunks: 159 / 113
+  // / 90 us; 4096 of 2048 25.0 / 23.5 / 24.4)
+  int chunks = a.T < 512 ? 1 : a.d <= 2048 ? 2 : 4;
   while (a.d > 8 * 1024 * chunks) chunks *= 2;
   const int threads = ((a.d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32;
   auto pick = [&](auto r) {

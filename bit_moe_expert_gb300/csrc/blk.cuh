@@ -107,8 +107,11 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t a) {
 
 // Eight codes of values times inv.
 __device__ __forceinline__ uint2 blk_codes8(const float (&f)[8], float inv) {
-  return make_uint2(f32x4_to_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                    f32x4_to_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+  float v[8];
+  const uint64_t i2 = pack2(__float_as_uint(inv), __float_as_uint(inv));
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) unpack2(mul2(pack2(__float_as_uint(f[j]), __float_as_uint(f[j + 1])), i2), v[j], v[j + 1]);
+  return make_uint2(f32x4_to_e4m3x4(v[0], v[1], v[2], v[3]), f32x4_to_e4m3x4(v[4], v[5], v[6], v[7]));
 }
 
 // Eight values to consecutive places of a row of type kType (16-byte aligned).

@@ -278,9 +278,8 @@ extern "C" {
 moe_status moe_blk_quantize(const void* X, moe_dtype type, int rows, int K, long long ldx, const moe_blk_mat* out,
                             moe_stream stream) {
   const moe_status st = check_x(X, type, rows, K, ldx);
-  if (st != MOE_OK) return st;
+  if (st != MOE_OK || rows == 0) return st;
   if (!mat_ok(out)) return MOE_ERR_INVALID_ARG;
-  if (rows == 0) return MOE_OK;
   return done(launch_blk_quantize(X, type, rows, K, ldx, out->q, out->s, cuda(stream), pdl_enabled()));
 }
 
@@ -293,9 +292,8 @@ moe_status moe_blk_quantize_weights(const void* W, moe_dtype type, int E, int N,
 
 moe_status moe_blk_dequant(const moe_blk_mat* a, int rows, int K, moe_dtype type, void* X, moe_stream stream) {
   const moe_status st = check_x(X, type, rows, K, K);
-  if (st != MOE_OK) return st;
+  if (st != MOE_OK || rows == 0) return st;
   if (!mat_ok(a)) return MOE_ERR_INVALID_ARG;
-  if (rows == 0) return MOE_OK;
   return done(launch_blk_dequant(a->q, a->s, rows, K, type, X, cuda(stream), pdl_enabled()));
 }
 
@@ -309,9 +307,9 @@ moe_status moe_blk_matmul(const moe_blk_mat* A, int M, const moe_blk_mat* W, int
                           void* ws, size_t ws_bytes, moe_stream stream) {
   const moe_status st = check_matmul(M, W, N, K, Y, y_type);
   if (st != MOE_OK) return st;
-  if (!mat_ok(A)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, sizeof(WsHeader))) return MOE_ERR_WORKSPACE;
   if (M == 0) return MOE_OK;
+  if (!mat_ok(A)) return MOE_ERR_INVALID_ARG;
   return matmul(*A, M, W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
 }
 
@@ -342,6 +340,7 @@ moe_status moe_rmsnorm(const void* X, moe_dtype x_type, int T, int d, long long 
   if (st != MOE_OK) return st;
   if (!gamma || !aligned16(gamma) || (gamma_type != MOE_BF16 && gamma_type != MOE_FP32)) return MOE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return d > kNormMaxCols ? MOE_ERR_UNSUPPORTED : MOE_OK;
   if ((residual != nullptr) != (residual_out != nullptr)) return MOE_ERR_INVALID_ARG;
   if (residual && (!aligned16(residual) || !aligned16(residual_out) || (residual_type != x_type && residual_type != MOE_FP32)))
     return MOE_ERR_INVALID_ARG;
@@ -349,7 +348,6 @@ moe_status moe_rmsnorm(const void* X, moe_dtype x_type, int T, int d, long long 
   if (Y && (!aligned16(Y) || !type_ok(y_type))) return MOE_ERR_INVALID_ARG;
   if (out && !mat_ok(out)) return MOE_ERR_INVALID_ARG;
   if (d > kNormMaxCols) return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
   RmsNorm n{};
   n.x = X;
   n.residual = residual;

@@ -50,9 +50,6 @@ struct Variant {
   static constexpr int kMats = kMode == kGateUp ? 2 : 1;
   static constexpr int kGroup = kBN == 16 ? 8 : 16;                // tokens that a warp takes at a time
   static constexpr int kGroups = kBN / (kGroup * kParts);          // of a warp
-  // gate and up sums of 64 tokens take 128 registers: more than 384 threads' equal share, less than is left when
-  // the other four warps give theirs up (128 x 72 + 256 x 216 = 384 x 168)
-  static constexpr bool kUneven = kMats * kBN > 128;
 };
 
 // How a launch divides shared and tensor memory; bn: the tiles' height in columns.
@@ -62,14 +59,14 @@ struct Plan {
 Plan make_plan(int mats, int bn) {
   Plan p;
   p.bn = bn;
-  p.accs = static_cast<int>(kTmemCols) / (mats * bn);
-  if (p.accs > kMaxAccs) p.accs = kMaxAccs;
+  const int most = static_cast<int>(kTmemCols) / (mats * bn);
   p.stage_bytes = mats * kMatBytes + bn * 128;
   for (p.stages = kMaxStages;; --p.stages) {
+    p.accs = most < p.stages ? most : p.stages;  // no more than stages: see where the sums wait
+    if (p.accs > kMaxAccs) p.accs = kMaxAccs;
     // the scales of a block are read until its accumulator is free again, which may be `accs` stages after the
     // stage's codes: a ring of their own
     p.scale_slots = p.stages + p.accs;
-    if (p.accs > p.stages) p.accs = p.stages;  // (no fewer than six stages are found)
     if (p.stages * p.stage_bytes + p.scale_slots * bn * 4 + kSmemFixed <= kSmemLimit) return p;
   }
 }
@@ -250,10 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kSumWarp0) {
-    if constexpr (V::kUneven) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp != kMmaWarp) {
       // one thread for the weights, which starts before the wait, one for the activations' codes and one for their scales
-      // (each copy takes its thread some 100 clocks to issue)
       if (lane == 0) {
         const bool weights = warp == kWeightsWarp;
         if (!weights) pdl_wait();
@@ -358,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    if constexpr (V::kUneven) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     pdl_wait();
     pdl_launch_dependents();
     const int quarter = warp & 3, part = (warp - kSumWarp0) >> 2;

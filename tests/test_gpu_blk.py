@@ -294,3 +294,275 @@ def test_forward_with_experts_that_nobody_takes_and_one_that_all_take():
     assert bm.moe_check_status(ws) == 0
     assert not y[3].any() and not y[5].any()
     _assert_layer(y, blk_ref.layer(blk_ref.rounded(x.double().cpu().numpy()), host, None, ids, w.astype(np.float64)), I)
+
+
+# ------------------------------------------------------------------ calls in a program
+
+def _forward_buffers(T, d, I, E, k, I_shared, rows):
+    return (torch.empty((T, d), dtype=torch.bfloat16, device="cuda"),
+            bm.workspace(bm.moe_blk_forward_workspace_bytes(T, d, I, E, k, I_shared, rows)))
+
+
+@pytest.mark.parametrize("T,rows", [(1, 16), (2, 16), (40, 16), (40, 64), (200, 128)])
+def test_a_block_of_a_model(T, rows):
+    """Residual and norm, router projection from its bf16 output, scored routing and experts from its codes, in one call
+    of moe_blk_layer; the next norm adds the result to the stream.  Each step against 64 bits from what the one before
+    gave; the layer also equals routing and experts called one after the other, and itself from a captured graph."""
+    rng = np.random.default_rng(T + rows)
+    d, I, E, k, I_shared = 512, 224, 16, 4, 128
+    x, stream = _to(rng.standard_normal((T, d)), "bf16"), _to(3 * rng.standard_normal((T, d)), "bf16")
+    gamma = _to(1 + 0.2 * rng.standard_normal(d), "bf16")
+    router = _to(rng.standard_normal((E, d)) / np.sqrt(d), "bf16")
+    scoring = bm.Scoring("sigmoid", _to(0.1 * rng.standard_normal(E), "fp32"), n_group=4, topk_group=2, scale=1.5)
+    routed_host, routed = _experts(rng, E, d, I)
+    shared_host, shared = _experts(rng, 1, d, I_shared)
+    normed, act = torch.empty_like(x), bm.BlkAct.empty(T, d)
+    logits = torch.empty((T, E), dtype=torch.float32, device="cuda")
+    r = bm.Routing.empty(T, E, k, rows)
+    y = torch.empty_like(x)
+    ws = bm.workspace(bm.moe_blk_layer_workspace_bytes(T, d, I, E, k, I_shared, rows))
+    before, after = stream.clone(), torch.empty_like(stream)
+    out = bm.BlkAct.empty(T, d)
+
+    def block():
+        bm.moe_rmsnorm(x, gamma, 1e-6, residual=stream, stream_out=after, Y=normed, out=act)
+        bm.moe_router_logits(normed, router, logits)
+        bm.moe_blk_layer(logits, scoring, act, routed, shared, k, rows, r, y, ws)
+        bm.moe_rmsnorm(y, gamma, 1e-6, residual=after, out=out)          # adds to `after` in place
+
+    block()
+    assert bm.moe_check_status(ws) == 0
+    res = (x.double() + before.double()).to(torch.bfloat16)
+    xq = blk_ref.decode(act.q.cpu().numpy()) * blk_ref.spread(act.s.cpu().numpy()[:, :T].T.astype(np.float64), d)
+    want = blk_ref.rounded(blk_ref.norm(res.double().cpu().numpy(), gamma.double().cpu().numpy(), 1e-6))
+    np.testing.assert_array_equal(xq, want)
+    ids, w = r.ids.cpu().numpy(), r.w.double().cpu().numpy()
+    for t in range(T):
+        got = mx_ref.route_row(logits[t].double().cpu().numpy(), "sigmoid", scoring.bias.double().cpu().numpy(), k, 4, 2, 2, True, 1.5)
+        if got[2] > 1e-5:
+            np.testing.assert_array_equal(ids[t], got[0])
+            np.testing.assert_allclose(w[t], got[1], rtol=1e-5)
+    _assert_layer(y, blk_ref.layer(xq, routed_host, shared_host, ids, w), I)
+    assert torch.equal(after, (res.double() + y.double()).to(torch.bfloat16))
+    first = [t.clone() for t in (y, after, out.q, out.s[:, :T])]
+    # one after the other
+    y2, ws2 = _forward_buffers(T, d, I, E, k, I_shared, rows)
+    bm.moe_blk_forward(act, routed, shared, r, y2, ws2)
+    assert torch.equal(y2, y)
+    # from a graph, with other inputs in the same memory in between
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            block()
+    torch.cuda.synchronize()
+    kept = x.clone()
+    x.copy_(_to(rng.standard_normal((T, d)), "bf16"))
+    g.replay()
+    x.copy_(kept)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((y, after, out.q, out.s[:, :T]), first):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own, side by side, give what they give alone."""
+    rng = np.random.default_rng(4)
+    d, I, E, k, rows = 1024, 256, 16, 4, 64
+    _, routed = _experts(rng, E, d, I)
+    m = _mat(blk_ref.draw_matrix(rng, 1, 2080, d))
+    jobs = []
+    for T in (300, 1):
+        x = _to(rng.standard_normal((T, d)), "bf16")
+        _, _, r = _draw_routing(rng, T, E, k, rows)
+        y, ws = _forward_buffers(T, d, I, E, k, 0, rows)
+        z = torch.empty((T, 2080), dtype=torch.float32, device="cuda")
+        jobs.append((x, r, y, ws, z, bm.workspace(bm.moe_blk_linear_workspace_bytes(T, 2080, d)), torch.cuda.Stream()))
+
+    def run(job, stream):
+        x, r, y, ws, z, ws2, _ = job
+        bm.moe_blk_forward(x, routed, None, r, y, ws, stream=stream)
+        bm.moe_blk_linear(x, m, z, ws2, stream=stream)
+
+    alone = []
+    for j in jobs:
+        run(j, None)
+        alone.append((j[2].clone(), j[4].clone()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            run(j, j[6])
+    torch.cuda.synchronize()
+    for j, (y, z) in zip(jobs, alone):
+        assert torch.equal(j[2], y) and torch.equal(j[4], z) and bm.moe_check_status(j[3]) == 0
+
+
+def test_calls_without_rows():
+    a = bm.BlkAct.empty(0, 256)
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    m = _mat(blk_ref.draw_matrix(np.random.default_rng(0), 1, 64, 256))
+    ws = bm.workspace(256)
+    bm.moe_blk_quantize(x, a)
+    bm.moe_blk_dequant(a, x)
+    bm.moe_blk_matmul(a, m, torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), ws)
+    bm.moe_blk_linear(x, m, torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), ws)
+    bm.moe_rmsnorm(x, torch.ones(256, device="cuda"), 1e-6, residual=x, Y=x, out=a)
+    assert bm.moe_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("kind", ["one", "few", "narrow", "wide"])
+def test_a_product_right_after_its_weights(kind):
+    """moe_blk_quantize_weights, then at once the product with them: the results of a synchronised program."""
+    M, N, K = {"one": (1, 2048, 2048), "few": (20, 2048, 2048), "narrow": (300, 2048, 2048), "wide": (2500, 2304, 1040)}[kind]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = [torch.randn(1, N, K, device="cuda", generator=gen) * 2.0 ** i for i in (0, 3)]
+    x = torch.randn(M, K, device="cuda", generator=gen).to(torch.bfloat16)
+    m, a = bm.BlkMat.empty(1, N, K), bm.BlkAct.empty(M, K)
+    bm.moe_blk_quantize(x, a)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws = bm.workspace(bm.moe_blk_linear_workspace_bytes(M, N, K))
+    got = {}
+    for sync in (True, False):
+        got[sync] = []
+        for i in range(8):
+            bm.moe_blk_quantize_weights(w[i % 2], m)
+            if sync:
+                torch.cuda.synchronize()
+            if kind == "one":
+                bm.moe_blk_linear(x, m, y, ws)
+            else:
+                bm.moe_blk_matmul(a, m, y, ws)
+            got[sync].append(y.clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(got[True][0], got[True][1])
+    assert all(torch.equal(p, q) for p, q in zip(got[True], got[False])) and bm.moe_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,rows", [(2, 16), (40, 16), (40, 128)])
+@pytest.mark.parametrize("bad", ["expert", "rows", "first", "count"])
+def test_a_malformed_routing_is_reported_and_harms_no_later_call(T, rows, bad):
+    """Entries that the kernels check: an expert that is not there, more rows than a tile has, rows past the last, no tiles."""
+    rng = np.random.default_rng(T)
+    d, I, E, k = 256, 128, 8, 2
+    _, routed = _experts(rng, E, d, I)
+    _, _, r = _draw_routing(rng, T, E, k, rows)
+    x = _to(rng.standard_normal((T, d)), "bf16")
+    y, ws = _forward_buffers(T, d, I, E, k, 0, rows)
+    bm.moe_blk_forward(x, routed, None, r, y, ws)
+    good = y.clone()
+    assert bm.moe_check_status(ws) == 0
+    saved, tiles = r.block_map.clone(), r.num_blocks.clone()
+    if bad == "count":
+        r.num_blocks.fill_(0)
+    else:
+        column, value = {"expert": (0, E), "rows": (2, 10 ** 6), "first": (1, T * k + 1)}[bad]
+        r.block_map[0, column] = value
+    bm.moe_blk_forward(x, routed, None, r, y, ws)
+    assert bm.moe_check_status(ws) == 1
+    r.block_map.copy_(saved)
+    r.num_blocks.copy_(tiles)
+    bm.moe_blk_forward(x, routed, None, r, y, ws)
+    assert bm.moe_check_status(ws) == 0 and torch.equal(y, good)
+
+
+def test_new_memory_under_the_same_objects():
+    """A BlkMat and a BlkAct whose tensors move are taken as they are now."""
+    rng = np.random.default_rng(6)
+    M, N, K = 4, 300, 256
+    v, s = blk_ref.quantise(rng.standard_normal((M, K)))
+    a, m = _act(v, s), _mat(blk_ref.draw_matrix(rng, 1, N, K))
+    y, ws = torch.empty((M, N), dtype=torch.float32, device="cuda"), bm.workspace(256)
+    bm.moe_blk_matmul(a, m, y, ws)
+    first = y.clone()
+    for t in (a.q, a.s, m.q, m.s):
+        old = t.clone()
+        t.set_(old)                                                    # other memory, the same tensor object
+    bm.moe_blk_matmul(a, m, y, ws)
+    assert torch.equal(y, first)
+    m.q = m.q.view(torch.float8_e4m3fn)
+    bm.moe_blk_matmul(a, m, y, ws)
+    assert torch.equal(y, first)
+
+
+# ------------------------------------------------------------------ sizes past 2^31 elements
+
+def test_rows_past_2_to_the_31_elements():
+    rows, K = 270_000, 8192
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(rows, K, device="cuda", generator=gen, dtype=torch.bfloat16)
+    a, b = bm.BlkAct.empty(rows, K), bm.BlkAct.empty(rows, K)
+    bm.moe_blk_quantize(x, a)
+    some = np.r_[0:5, rows // 2:rows // 2 + 5, rows - 5:rows]
+    x64 = x[some].double().cpu().numpy()
+    _check_codes(a.q[some].cpu().numpy(), a.s[:, some].cpu().numpy().T, *blk_ref.quantise(x64))
+    y = torch.empty_like(x)
+    bm.moe_blk_dequant(a, y)
+    np.testing.assert_array_equal(y[some].double().cpu().numpy(), blk_ref.rounded(x64))
+    gamma = torch.ones(K, device="cuda")
+    bm.moe_rmsnorm(x, gamma, 1e-6, residual=x, stream_out=y, out=b)
+    res = (2 * x[some].double()).cpu().numpy()                        # exact in bf16
+    np.testing.assert_array_equal(y[some].double().cpu().numpy(), res)
+    values = blk_ref.decode(b.q[some].cpu().numpy()) * blk_ref.spread(b.s[:, some].cpu().numpy().T.astype(np.float64), K)
+    np.testing.assert_array_equal(values, blk_ref.rounded(blk_ref.norm(res, np.ones(K), 1e-6)))
+
+
+def test_weights_past_2_to_the_31_elements():
+    E, N, K = 5, 55_000, 8192
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randn(E, N, K, device="cuda", generator=gen, dtype=torch.bfloat16)
+    m = bm.BlkMat.empty(E, N, K)
+    bm.moe_blk_quantize_weights(w, m)
+    at = slice(N // 128 * 128, N)                                     # the last block's rows of the last matrix
+    v, s = blk_ref.quantise_weights(w[-1:, at].double().cpu().numpy())
+    np.testing.assert_array_equal(m.s[-1:, -1:].cpu().numpy(), s)
+    np.testing.assert_array_equal(blk_ref.decode(m.q[-1:, at].cpu().numpy()), v)
+    bm.moe_blk_dequant(m, w)
+    np.testing.assert_array_equal(w[-1:, at].double().cpu().numpy(), blk_ref.weights((blk_ref.encode(v), s)))
+
+
+@pytest.mark.parametrize("M,N", [(16, 150_000_000), (40, 60_000_000), (70_000, 33_000)])
+def test_products_past_2_to_the_31_elements(M, N):
+    """Few tokens, narrow tiles, wide tiles: results past 2^31 elements."""
+    K = 64
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(M, K, device="cuda", generator=gen, dtype=torch.bfloat16)
+    a = bm.BlkAct.empty(M, K)
+    bm.moe_blk_quantize(x, a)
+    m = bm.BlkMat.empty(1, N, K)
+    m.q.copy_(torch.randint(0, 120, (1, N, K), device="cuda", generator=gen, dtype=torch.uint8))
+    m.s.copy_(torch.rand(m.s.shape, device="cuda", generator=gen) + 0.5)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws = bm.workspace(256)
+    bm.moe_blk_matmul(a, m, y, ws)
+    assert bm.moe_check_status(ws) == 0
+    rows, cols = np.r_[0, M - 1], np.r_[0:40, N // 2:N // 2 + 40, N - 40:N]
+    xv = blk_ref.rounded(x[rows].double().cpu().numpy())
+    s = m.s[0, cols // 128].double().cpu().numpy()
+    _assert_product(y[rows][:, cols], xv, blk_ref.decode(m.q[0, cols].cpu().numpy()) * s, K)
+
+
+def test_experts_rows_past_2_to_the_31_elements():
+    """Rows of the experts' outputs past 2^31 elements: a token's result does not change with the tokens around it."""
+    T, d, I, E, k = 34_000, 8192, 32, 8, 8
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(T, d, device="cuda", generator=gen, dtype=torch.bfloat16)
+    rng = np.random.default_rng(7)
+    _, routed = _experts(rng, E, d, I)
+
+    def run(x):
+        n = x.shape[0]
+        r = bm.Routing.empty(n, E, k, 128)
+        ws = bm.workspace(bm.moe_blk_layer_workspace_bytes(n, d, I, E, k, 0, 128))
+        y = torch.empty_like(x)
+        logits = (x[:, :E].float() * 3).contiguous()
+        bm.moe_blk_layer(logits, bm.Scoring("softmax"), x, routed, None, k, 128, r, y, ws)
+        assert bm.moe_check_status(ws) == 0
+        return y
+
+    y = run(x)
+    some = torch.cat([torch.arange(300), torch.arange(T - 300, T)]).cuda()
+    assert torch.isfinite(y).all() and torch.equal(y[some], run(x[some].contiguous()))
