@@ -67,12 +67,19 @@ bool few_linear_wins(int M, int N, int K) {
   return M <= kBlkFewLinear && 0.52e-6 * N * K < 2.5 + 0.00207 * K;
 }
 
-// Height of the dense product's token tiles.
+// Height of the dense product's token tiles, by a modelled time in microseconds: a CTA's tiles in turn, each a block of
+// 128 columns after another, then the epilogue.  Measured (tiles of 64 x 128 / of 128 x 256): 512 x 2048 -> 2048 7.1 / 10.9
+// us, 1024 x 2048 -> 2048 12.0 / 10.5, 256 x 8192 -> 8192 38.6 / 32.7, 4096 x 4096 -> 4096 - / 66.
 int linear_tile(int M, int N, int K, int num_sms) {
-  (void)K;
-  const long long wide = static_cast<long long>((N + 255) / 256) * ((M + 127) / 128);
-  if (2 * wide >= num_sms) return 128;
-  return M <= kBlkNarrow ? round16(M) : kBlkNarrow;
+  if (M <= kBlkNarrow) return round16(M);
+  auto turns = [&](int rows, int cols) {
+    const long long tiles = static_cast<long long>((N + rows - 1) / rows) * ((M + cols - 1) / cols);
+    return static_cast<double>((tiles + num_sms - 1) / num_sms);
+  };
+  const int blocks = blk_count(K);
+  const double narrow = turns(kBlk, kBlkNarrow) * (0.29 * blocks + 0.4);
+  const double wide = turns(2 * kBlk, 128) * (0.48 * blocks + 1.2);
+  return wide < narrow ? 128 : kBlkNarrow;
 }
 
 moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
