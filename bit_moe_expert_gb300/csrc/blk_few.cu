@@ -26,8 +26,12 @@ constexpr int kThreads = kWarps * 32;
 // A warp's blocks whose weights are in flight together.  Two CTAs an SM hold 128
 // KB of them: with 16 warps of one block each (and one CTA's registers an SM) one
 // token's expert layer took 13.6 us, 1 x 8192 -> 8192 21.8.
-constexpr int kDepth = 4;       // linear, down
+constexpr int kDepth = 4;       // linear
 constexpr int kDepthGU = 2;     // gate/up: of both matrices
+// The down product has fewer CTAs than there are SMs and as many (expert, block)
+// pairs in each as one token has: 16 warps of three at a time.
+constexpr int kWarpsDown = 16;
+constexpr int kDepthDown = 3;
 
 // D += A B, m16n8k32, E4M3 operands four to a register (lowest index in the
 // lowest byte), fp32 accumulators; g = lane/4, q = lane%4:
@@ -154,9 +158,10 @@ struct Columns {
   }
 };
 
+template <int kW, int kSums>
 struct Shared {
-  uint32_t codes[kWarps][kTokens * 32];
-  float sums[2][kWarps][kRows * kTokens];
+  uint32_t codes[kW][kTokens * 32];
+  float sums[kSums][kW][kRows * kTokens];
 };
 
 // A warp's accumulators to its place; element (row, token) at 8 row + token.
@@ -165,10 +170,11 @@ __device__ __forceinline__ void put_sums(float* to, const float (&acc)[4], int l
   *reinterpret_cast<float2*>(to + kTokens * g + 2 * q) = make_float2(acc[0], acc[1]);
   *reinterpret_cast<float2*>(to + kTokens * (g + 8) + 2 * q) = make_float2(acc[2], acc[3]);
 }
-__device__ __forceinline__ float take_sum(const float (&sums)[kWarps][kRows * kTokens], int i) {
+template <int kW>
+__device__ __forceinline__ float take_sum(const float (&sums)[kW][kRows * kTokens], int i) {
   float v = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += sums[w][i];
+  for (int w = 0; w < kW; ++w) v += sums[w][i];
   return v;
 }
 __device__ __forceinline__ void add(float (&acc)[4], const float (&d)[4], float s0, float s1) {
@@ -183,7 +189,7 @@ __device__ __forceinline__ void add(float (&acc)[4], const float (&d)[4], float 
 // 26.7 us, quantised by a kernel of its own 16.)
 template <int kType>
 __global__ void __launch_bounds__(kThreads, 2) blk_one_linear_kernel(const BlkFewLinearArgs a) {
-  __shared__ Shared sm;
+  __shared__ Shared<kWarps, 1> sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, blocks = blk_count(a.K);
   const float* sw = a.sw + static_cast<size_t>(n0 / kBlk) * blocks;
@@ -319,7 +325,7 @@ __device__ __forceinline__ Tile get_tile(const BlkFewArgs& a, int i) {
 
 template <int kType>
 __global__ void __launch_bounds__(kThreads, 2) blk_few_gate_up_kernel(const BlkFewArgs a) {
-  __shared__ Shared sm;
+  __shared__ Shared<kWarps, 2> sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, blocks = blk_count(a.d);
   const bool early = a.I_shared > 0 && blockIdx.y == 0;  // the shared expert's weights are known before the wait
@@ -404,19 +410,19 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_gate_up_kernel(const BlkF
 
 constexpr int kMaxRouted = kTokens * kMaxK;  // tiles and assignments of the routed experts at most
 struct SharedDown {
-  Shared p;
+  Shared<kWarpsDown, 1> p;
   int e[kMaxRouted], row0[kMaxRouted], rows[kMaxRouted];  // of a routed tile; no rows: malformed
   int token[kMaxRouted];                                  // of an assignment's row; -1: malformed
   float w[kMaxRouted];
 };
-__global__ void __launch_bounds__(kThreads, 2) blk_few_down_kernel(const BlkFewArgs a) {
+__global__ void __launch_bounds__(32 * kWarpsDown) blk_few_down_kernel(const BlkFewArgs a) {
   __shared__ SharedDown sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * kRows, A = a.T * a.k;
   const int blocks_r = blk_count(a.I), blocks_s = a.I_shared > 0 ? blk_count(a.I_shared) : 0;
   // (the routing has completed: see above)
   const int nb = routed_tiles(a);
-  for (int i = threadIdx.x; i < max(nb, A); i += kThreads) {
+  for (int i = threadIdx.x; i < max(nb, A); i += 32 * kWarpsDown) {
     if (i < nb) {
       const Tile t = get_tile(a, i + (a.I_shared > 0 ? 1 : 0));
       sm.e[i] = t.e;
@@ -433,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_down_kernel(const BlkFewA
   }
   __syncthreads();
   const int units = blocks_s + nb * blocks_r;
-  ABlock w[kDepth];
-  float sw[kDepth];
+  ABlock w[kDepthDown];
+  float sw[kDepthDown];
   auto load = [&](int u, ABlock& to, float& s) {
     if (u >= units) return;
     const bool shared = u < blocks_s;
@@ -446,34 +452,36 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_down_kernel(const BlkFewA
     s = __ldg(m.s_down + (static_cast<size_t>(e) * blk_count(a.d) + n0 / kBlk) * blk_count(K) + kb);
   };
 #pragma unroll
-  for (int j = 0; j < kDepth; ++j) load(warp + j * kWarps, w[j], sw[j]);
+  for (int j = 0; j < kDepthDown; ++j) load(warp + j * kWarpsDown, w[j], sw[j]);
   pdl_wait();
   pdl_launch_dependents();
   const int pitch = max(a.I, a.I_shared);
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto take = [&](int u, const ABlock& m, float s) {
+  // h's values of row r of unit u
+  auto ask = [&](int u, int r) {
+    if (u >= units) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool shared = u < blocks_s;
     const int i = shared ? 0 : (u - blocks_s) / blocks_r, kb = shared ? u : u - blocks_s - i * blocks_r;
-    const int K = shared ? a.I_shared : a.I, rows = shared ? a.T : sm.rows[i], row0 = shared ? 0 : sm.row0[i];
+    const int K = shared ? a.I_shared : a.I, rows = shared ? a.T : sm.rows[i], row0 = shared ? A : sm.row0[i];
+    const int c = kb * kBlk + 4 * lane;
+    if (r >= rows || c >= K) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return __ldcg(reinterpret_cast<const float4*>(a.h + (row0 + r) * static_cast<size_t>(pitch) + c));
+  };
+  auto take = [&](int u, const ABlock& m, float s, float4 v) {  // v: the first row's
+    const bool shared = u < blocks_s;
+    const int i = shared ? 0 : (u - blocks_s) / blocks_r;
+    const int rows = shared ? a.T : sm.rows[i];
     if (rows == 0) return;
-    const int c0 = kb * kBlk + 4 * lane;
     Columns c(sm.p.codes[warp], lane);
-    for (int r0 = 0; r0 < rows; r0 += 2) {  // two rows' loads in flight
-      float4 v[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        v[j] = r0 + j < rows && c0 < K ? __ldcg(reinterpret_cast<const float4*>(a.h + ((shared ? A : row0) + r0 + j) * static_cast<size_t>(pitch) + c0))
-                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (r0 + j >= rows) break;
-        const int t = shared ? r0 + j : sm.token[row0 + r0 + j];
-        const float wt = shared ? 1.0f : sm.w[row0 + r0 + j];
-        const float f[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-        float sx;
-        const uint32_t q = quantize4(f, sx);
-        if (t >= 0) c.put(t, q, sx * s * wt);
-      }
+    for (int r = 0; r < rows; ++r) {
+      const float4 next = r + 1 < rows ? ask(u, r + 1) : v;
+      const int at = shared ? 0 : sm.row0[i] + r;
+      const int t = shared ? r : sm.token[at];
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      float sx;
+      const uint32_t q = quantize4(f, sx);
+      if (t >= 0) c.put(t, q, sx * s * (shared ? 1.0f : sm.w[at]));
+      v = next;
     }
     Piece b;
     float d[4];
@@ -481,13 +489,16 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_down_kernel(const BlkFewA
     multiply(d, m, b);
     add(acc, d, c.sa[0], c.sa[1]);
   };
-  for (int u0 = warp; u0 < units; u0 += kDepth * kWarps) {
+  for (int u0 = warp; u0 < units; u0 += kDepthDown * kWarpsDown) {
+    float4 v[kDepthDown];
 #pragma unroll
-    for (int j = 0; j < kDepth; ++j) {
-      const int u = u0 + j * kWarps;
+    for (int j = 0; j < kDepthDown; ++j) v[j] = ask(u0 + j * kWarpsDown, 0);
+#pragma unroll
+    for (int j = 0; j < kDepthDown; ++j) {
+      const int u = u0 + j * kWarpsDown;
       if (u >= units) break;
-      take(u, w[j], sw[j]);
-      load(u + kDepth * kWarps, w[j], sw[j]);
+      take(u, w[j], sw[j], v[j]);
+      load(u + kDepthDown * kWarpsDown, w[j], sw[j]);
     }
   }
   put_sums(sm.p.sums[0][warp], acc, lane);
@@ -500,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_down_kernel(const BlkFewA
 }
 
 template <typename A>
-cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, cudaStream_t stream, bool pdl, const A& a) {
+cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, int threads, cudaStream_t stream, bool pdl, const A& a) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -525,15 +536,15 @@ cudaError_t launch_blk_few_linear(const BlkFewLinearArgs& a, cudaStream_t stream
                       : a.T <= kTokens    ? blk_few_linear_kernel<1>
                       : a.T <= 2 * kTokens ? blk_few_linear_kernel<2>
                                            : blk_few_linear_kernel<4>;
-  return launch(kKBlkGemm, kernel, dim3((a.N + kRows - 1) / kRows), stream, pdl, a);
+  return launch(kKBlkGemm, kernel, dim3((a.N + kRows - 1) / kRows), kThreads, stream, pdl, a);
 }
 
 cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl) {
   const int tiles = a.tiles + (a.I_shared > 0 ? 1 : 0), I = a.I > a.I_shared ? a.I : a.I_shared;
   const auto gate_up = a.x.type == kBlkCodes ? blk_few_gate_up_kernel<kBlkCodes> : blk_few_gate_up_kernel<kBf16>;
-  const cudaError_t e = launch(kKBlkGateUp, gate_up, dim3((I + kRows - 1) / kRows, tiles), stream, pdl, a);
+  const cudaError_t e = launch(kKBlkGateUp, gate_up, dim3((I + kRows - 1) / kRows, tiles), kThreads, stream, pdl, a);
   if (e != cudaSuccess) return e;
-  return launch(kKBlkDown, blk_few_down_kernel, dim3((a.d + kRows - 1) / kRows), stream, pdl, a);
+  return launch(kKBlkDown, blk_few_down_kernel, dim3((a.d + kRows - 1) / kRows), 32 * kWarpsDown, stream, pdl, a);
 }
 
 }  // namespace bm
