@@ -134,7 +134,8 @@ struct XBlock {
 };
 
 // A warp's B fragments of a block of up to eight tokens, a column each: put() for
-// the columns that there are, then take().  `buf`: 8 x 128 bytes of the warp's own.
+// the columns that there are, then take().  A column that is put again (the same
+// codes: an expert that a token takes twice) adds its scale.  `buf`: 8 x 128 bytes of the warp's own.
 struct Columns {
   uint32_t* buf;
   int lane;
@@ -144,8 +145,8 @@ struct Columns {
   __device__ __forceinline__ void put(int column, uint32_t codes, float scale) {
     buf[32 * column + lane] = codes;
     there |= 1u << column;
-    if (column == 2 * (lane & 3)) sa[0] = scale;
-    if (column == 2 * (lane & 3) + 1) sa[1] = scale;
+    if (column == 2 * (lane & 3)) sa[0] += scale;
+    if (column == 2 * (lane & 3) + 1) sa[1] += scale;
   }
   __device__ __forceinline__ void take(Piece& b) const {
     __syncwarp();
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_linear_kernel(const BlkFe
 
 // ------------------------------------------------------------------ experts
 // Two launches after the routing.  gate/up: a CTA 16 columns of h of one tile (at
-// most eight rows: a token takes an expert once), fp32 h to memory.  down: a CTA
+// most eight rows), fp32 h to memory.  down: a CTA
 // 16 columns of Y over all experts: its warps take the (expert, block of h) pairs
 // in turn, quantise h, and add each token's column with its routing weight, so that
 // nothing is added up between CTAs.  The gate/up kernel lets the down kernel start
@@ -319,7 +320,7 @@ __device__ __forceinline__ Tile get_tile(const BlkFewArgs& a, int i) {
   t.row0 = b[1];
   t.rows = b[2];
   t.some = i < routed_tiles(a);
-  t.ok = t.some && t.e >= 0 && t.e < a.E && t.rows >= 1 && t.rows <= a.T && t.row0 >= 0 && t.row0 <= a.T * a.k - t.rows;
+  t.ok = t.some && t.e >= 0 && t.e < a.E && t.rows >= 1 && t.rows <= kTokens && t.row0 >= 0 && t.row0 <= a.T * a.k - t.rows;
   return t;
 }
 

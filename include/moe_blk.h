@@ -122,7 +122,10 @@ size_t moe_blk_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_
  *   X, XQ   bf16 X [T][d], or the activations XQ [T][d] that moe_rmsnorm or
  *           moe_blk_quantize wrote, taken as they are: one of them, the other
  *           NULL
- * Other arguments as for moe_forward; d, I and I_shared multiples of 32.
+ * Other arguments as for moe_forward; d, I and I_shared multiples of 32.  In
+ * tables of the caller's own a token may take an expert more than once (for T <=
+ * 2 a tile then has at most 8 rows: MOE_ERR_INVALID_ARG in the status word
+ * above).
  * MOE_ERR_UNSUPPORTED also where moe_route_max_blocks times ceil(max(d, I) /
  * 128), plus the shared expert's tiles likewise, is above 2^30. */
 moe_status moe_blk_forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I, int k,

@@ -296,6 +296,35 @@ def test_forward_with_experts_that_nobody_takes_and_one_that_all_take():
     _assert_layer(y, blk_ref.layer(blk_ref.rounded(x.double().cpu().numpy()), host, None, ids, w.astype(np.float64)), I)
 
 
+@pytest.mark.parametrize("T,rows", [(1, 16), (2, 16), (2, 2), (40, 16), (40, 96)])
+def test_forward_with_an_expert_that_a_token_takes_twice(T, rows):
+    """Tables of the caller's own: both weights count."""
+    rng = np.random.default_rng(T + rows)
+    d, I, E, k = 256, 160, 4, 3
+    ids = np.stack([np.full(T, 2), np.arange(T) % 2, np.full(T, 2)], 1)
+    w = rng.random((T, k)).astype(np.float32)
+    r = _routing(ids, w, E, rows)
+    host, routed = _experts(rng, E, d, I)
+    x = _to(rng.standard_normal((T, d)), "bf16")
+    ws = bm.workspace(bm.moe_blk_forward_workspace_bytes(T, d, I, E, k, 0, rows))
+    y = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    bm.moe_blk_forward(x, routed, None, r, y, ws)
+    assert bm.moe_check_status(ws) == 0
+    _assert_layer(y, blk_ref.layer(blk_ref.rounded(x.double().cpu().numpy()), host, None, ids, w.astype(np.float64)), I)
+
+
+def test_more_rows_of_one_expert_than_a_tile_of_few_tokens_takes():
+    rng = np.random.default_rng(0)
+    T, d, I, E, k = 2, 256, 128, 8, 5
+    ids = np.full((T, k), 3)
+    _, routed = _experts(rng, E, d, I)
+    x = _to(rng.standard_normal((T, d)), "bf16")
+    y = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    ws = bm.workspace(bm.moe_blk_forward_workspace_bytes(T, d, I, E, k, 0, 16))
+    bm.moe_blk_forward(x, routed, None, _routing(ids, np.ones((T, k), np.float32), E, 16), y, ws)
+    assert bm.moe_check_status(ws) == 1
+
+
 # ------------------------------------------------------------------ calls in a program
 
 def _forward_buffers(T, d, I, E, k, I_shared, rows):
