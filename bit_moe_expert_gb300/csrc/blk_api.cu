@@ -140,8 +140,9 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
     return at;
   };
   L.few = T <= kBlkFewT;
+  const size_t h_bytes = static_cast<size_t>(I > I_shared ? I : I_shared) * 4;
   if (L.few) {
-    L.h = take(rows * (I > I_shared ? I : I_shared) * 4);
+    L.h = take(rows * h_bytes);
     L.total = o;
     return L;
   }
@@ -152,13 +153,15 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
   L.h_s = take(static_cast<size_t>(T) * I_shared);
   L.sh_r = take(static_cast<size_t>(L.max_blocks) * blk_count(I) * L.pitch * 4);
   L.sh_s = take(tiles_s * blk_count(I_shared) * L.pitch * 4);
-  L.total = o;
+  // a workspace for T tokens is one for fewer: the few tokens' fp32 h may be larger than all of the above
+  const size_t few = sizeof(WsHeader) + round256(static_cast<size_t>(kBlkFewT) * (k + (I_shared > 0 ? 1 : 0)) * h_bytes);
+  L.total = o > few ? o : few;
   return L;
 }
 
 bool expert_cols_ok(int n) { return n >= 32 && n % 32 == 0 && n <= kBlkMaxCols; }
 bool sizes_valid(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
-  return T >= 0 && expert_cols_ok(d) && expert_cols_ok(I) && (I_shared == 0 || expert_cols_ok(I_shared)) && E >= 1 && k >= 1 &&
+  return T >= 0 && T <= kMaxRows && expert_cols_ok(d) && expert_cols_ok(I) && (I_shared == 0 || expert_cols_ok(I_shared)) && E >= 1 && k >= 1 &&
          block_rows >= 1 && block_rows <= kMaxBlockRows;
 }
 

@@ -161,3 +161,13 @@ def test_reference_quantisation_against_a_search():
     np.testing.assert_array_equal(blk_ref.encode(blk_ref.decode(q[ok])), q[ok])
     torch = pytest.importorskip("torch")
     np.testing.assert_array_equal(blk_ref.decode(q), torch.from_numpy(q).view(torch.float8_e4m3fn).double().numpy())
+
+
+@pytest.mark.parametrize("d,I,E,k,I_shared,rows", [(32, 4096, 8, 8, 0, 16), (2048, 512, 256, 8, 512, 16), (64, 1024, 4, 1, 8192, 128)])
+def test_a_workspace_for_some_tokens_is_one_for_fewer(L, d, I, E, k, I_shared, rows):
+    for f in (bm.moe_blk_forward_workspace_bytes, bm.moe_blk_layer_workspace_bytes):
+        need = [f(T, d, I, E, k, I_shared, rows) for T in range(200)]
+        assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))
+        assert f((1 << 30) + 1, d, I, E, k, I_shared, rows) == 0
+    need = [bm.moe_blk_linear_workspace_bytes(T, I, d) for T in range(200)]
+    assert all(a <= b for a, b in zip(need, need[1:]))
