@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(kThreads)
 // block of 128 columns is a half warp).  Everything is fp32; what has to be more
 // exact is a pair (hi, lo) of fp32 numbers whose sum is the value:
 //   the sum of squares   eight at a time in fp32, the sums of eight added as
-//                        pairs (the addition's error by Knuth's two-sum), about
-//                        2^-28 of it in all;
+//                        pairs (the addition's error by Knuth's two-sum): the
+//                        errors of about 2^-24 of each sum of eight average
+//                        out, to some 2^-28 of a row of 2048;
 //   1 / sqrt(mean + eps) the hardware's estimate y0 and one Newton step, y0 (1 +
 //                        (1 - v y0^2) / 2), whose residual is formed with fused
 //                        multiply-adds.
@@ -280,15 +281,17 @@ __global__ void __launch_bounds__(1024)
   pdl_wait();
   pdl_launch_dependents();
   const char* x = static_cast<const char*>(a.x) + row * static_cast<size_t>(a.ldx) * (kType == kFp32 ? 4 : 2);
+  // (the residual, and X where Y is in its place, are read and written by each of several such kernels in a row, whose
+  // CTAs share SMs: no read-only loads)
   {
     Load8<kType> v[kChunks];
     Load8<kRType> w[kResidual == kNone ? 1 : kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      if (c + i * stride < a.d) v[i].load(x, c + i * stride); else v[i].zero();
+      if (c + i * stride < a.d) v[i].load_l2(x, c + i * stride); else v[i].zero();
       if constexpr (kResidual != kNone) {
         const char* p = static_cast<const char*>(a.residual) + row * a.d * (kRType == kFp32 ? 4 : 2);
-        if (c + i * stride < a.d) w[i].load(p, c + i * stride); else w[i].zero();
+        if (c + i * stride < a.d) w[i].load_l2(p, c + i * stride); else w[i].zero();
       }
     }
     if constexpr (kGammaEarly) {

@@ -46,6 +46,13 @@ struct Load8 {
     v[0] = __ldg(p);
     if constexpr (kType == kFp32) v[1] = __ldg(p + 1);
   }
+  // the same of memory that is written while this kernel may already be resident and that its SM may hold an older line
+  // of: past L1
+  __device__ __forceinline__ void load_l2(const void* row, int c) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<size_t>(c) * (kType == kFp32 ? 4 : 2));
+    v[0] = __ldcg(p);
+    if constexpr (kType == kFp32) v[1] = __ldcg(p + 1);
+  }
   __device__ __forceinline__ void zero() {
     v[0] = make_uint4(0, 0, 0, 0);
     if constexpr (kType == kFp32) v[1] = v[0];

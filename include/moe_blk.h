@@ -93,9 +93,13 @@ moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long lo
  *   X          [T][d] of x_type, rows ldx elements apart
  *   residual   NULL, or [T][d] contiguous; residual_type is x_type or MOE_FP32
  *   gamma      [d], bf16 or fp32 (gamma_type)
+ * Y may be X itself where their types are the same and ldx = d.
+ *
  * y is off by less than 2^-21 of itself; where that leaves a code or a scale
- * open, y is evaluated to 2^-27.  A row whose sum of squares is not finite in
- * fp32 (or 0, with eps = 0) is NaN.
+ * open, y is evaluated to about 2^-27 (2^-24 where a few values make up the
+ * row's sum of squares).  A row whose sum of squares is not finite in
+ * fp32 (or 0, with eps = 0) is NaN.  (That is where mean(r^2) + eps is at least
+ * 2^-80: the squares of smaller numbers lose bits in fp32.)
  * Preconditions: T >= 0 (0 does nothing), d a positive multiple of 16 up to
  * 32768 (MOE_ERR_UNSUPPORTED above), eps >= 0 and finite, X and the row pitch
  * multiples of 16 bytes. */

@@ -121,3 +121,31 @@ def test_edges():
     assert (np.abs(yh[good] - y64) <= np.abs(y64) * (2.0 ** -21 + 2.0 ** -24)).all()
     assert np.isnan(yh[4:7]).all() and torch.isnan(values[4:7]).all()
     np.testing.assert_array_equal(values.double().cpu().numpy()[good], blk_ref.rounded(y64))
+
+
+@pytest.mark.parametrize("T,d", [(1, 2048), (300, 512), (4001, 2048), (1300, 8192)])
+@pytest.mark.parametrize("x_kind,r_kind", [("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "fp32")])
+def test_norms_in_place_one_after_another(T, d, x_kind, r_kind):
+    """Each call reads the stream, and the X, that the one before it wrote where it had read them: the results of a program
+    that waits for each."""
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    x0 = torch.randn(T, d, device="cuda", generator=gen).to(TYPES[x_kind])
+    res0 = torch.randn(T, d, device="cuda", generator=gen).to(TYPES[r_kind])
+    gamma = 1 + 0.1 * torch.randn(d, device="cuda", generator=gen)
+    got = {}
+    for wait in (True, False):
+        x, res, a = x0.clone(), res0.clone(), bm.BlkAct.empty(T, d)
+        for _ in range(12):
+            bm.moe_rmsnorm(x, gamma, 1e-6, residual=res, Y=x, out=a)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got[wait] = x, res, a.q, a.s[:, :T]
+    assert torch.isfinite(got[True][1]).all()
+    assert all(torch.equal(p, q) for p, q in zip(got[True], got[False]))
+    # the first call against 64 bits
+    x, res = x0.clone(), res0.clone()
+    bm.moe_rmsnorm(x, gamma, 1e-6, residual=res, Y=x)
+    r = (x0.double() + res0.double()).to(res0.dtype)
+    assert torch.equal(res, r)
+    _check_y(x, blk_ref.norm(r.double().cpu().numpy(), gamma.double().cpu().numpy(), 1e-6))
