@@ -232,6 +232,20 @@ __device__ __forceinline__ float odd_float(double x) {
   return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
+// The sums of eight bf16 or fp16 values each.
+template <int kType>
+__device__ __forceinline__ uint4 add_packed(uint4 a, uint4 b) {
+  auto add2 = [](uint32_t x, uint32_t y) {
+    uint32_t r;
+    if constexpr (kType == kBf16)
+      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    else
+      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+  };
+  return make_uint4(add2(a.x, b.x), add2(a.y, b.y), add2(a.z, b.z), add2(a.w, b.w));
+}
+
 enum Residual { kNone, kSame, kWide };
 struct NormArgs {
   const void* x;
@@ -300,17 +314,17 @@ __global__ void __launch_bounds__(1024)
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
+      if constexpr (kResidual == kSame && kType != kFp32) {  // packed additions, each rounded once
+        v[i].v[0] = add_packed<kType>(v[i].v[0], w[i].v[0]);
+        if (c + i * stride < a.d) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + row * a.d + c + i * stride) = v[i].v[0];
+      }
       v[i].floats(r[i]);
-      if constexpr (kResidual != kNone) {
+      if constexpr (kRType == kFp32 && kResidual != kNone) {
         float f[8];
         w[i].floats(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          r[i][j] += f[j];
-          if constexpr (kRType == kBf16) r[i][j] = __bfloat162float(__float2bfloat16_rn(r[i][j]));
-          if constexpr (kRType == kFp16) r[i][j] = __half2float(__float2half_rn(r[i][j]));
-        }
-        if (c + i * stride < a.d) store8<kRType>(static_cast<char*>(a.residual_out) + (row * a.d + c + i * stride) * (kRType == kFp32 ? 4 : 2), r[i]);
+        for (int j = 0; j < 8; ++j) r[i][j] += f[j];
+        if (c + i * stride < a.d) store8<kFp32>(static_cast<float*>(a.residual_out) + row * a.d + c + i * stride, r[i]);
       }
     }
   }
