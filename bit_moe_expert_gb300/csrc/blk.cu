@@ -204,10 +204,13 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
   return Pair{s.hi, s.lo + (a.lo + b.lo)};
 }
-__device__ __forceinline__ Pair warp_sum(Pair a) {
+// over n neighbouring lanes, n a power of two; the same bits in all of them (the error of an addition is exact)
+__device__ __forceinline__ Pair lanes_sum(Pair a, int n) {
 #pragma unroll
-  for (int i = 16; i > 0; i /= 2)
+  for (int i = 1; i < 32; i *= 2) {
+    if (i == n) break;
     a = add(a, Pair{__shfl_xor_sync(0xffffffffu, a.hi, i), __shfl_xor_sync(0xffffffffu, a.lo, i)});
+  }
   return a;
 }
 // 1 / sqrt(sum / d + eps)
@@ -267,56 +270,57 @@ __device__ __forceinline__ double exact_value(float r, float g, Pair inv) {
   return static_cast<double>(r) * (static_cast<double>(inv.hi) + static_cast<double>(inv.lo)) * static_cast<double>(g);
 }
 
+// A warp has 256 kChunks neighbouring columns, a chunk of 256 after another: from a
+// lane's first column on all places are constants apart.
 template <int kType, int kResidual, int kChunks>
 __global__ void __launch_bounds__(1024)
     rmsnorm_kernel(const NormArgs a) {
   constexpr int kRType = kResidual == kWide ? kFp32 : kType;
+  constexpr int kStep = 256;
   __shared__ Pair s_sum[32];
-  const int warps = blockDim.x >> 5;
-  const size_t row = blockIdx.x;
-  const int stride = 8 * blockDim.x;
-  int c = 8 * threadIdx.x;
-  constexpr bool kGammaEarly = kChunks < 4;  // more would not fit the registers of 1024 threads
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const int c = (threadIdx.x >> 5) * kChunks * kStep + 8 * lane;
+  const size_t at = blockIdx.x * static_cast<size_t>(a.d) + c;  // of the lane's first column in what has d columns
+  constexpr bool kGammaEarly = kChunks == 1;  // registers: an SM holds more rows without (16384 rows of 2048: 59.5 / 57.7 us with the inverse)
   float g[kGammaEarly ? kChunks : 1][8], r[kChunks][8];
-  auto load_gamma = [&](int i, int to) {
-    if (c + i * stride >= a.d) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[to][j] = 0.0f;
-    } else if (a.gamma_fp32) {
+  auto load_gamma = [&](int i, float (&to)[8]) {
+    if (a.gamma_fp32) {
       Load8<kFp32> v;
-      v.load(a.gamma, c + i * stride);
-      v.floats(g[to]);
+      if (c + i * kStep < a.d) v.load(a.gamma, c + i * kStep); else v.zero();
+      v.floats(to);
     } else {
       Load8<kBf16> v;
-      v.load(a.gamma, c + i * stride);
-      v.floats(g[to]);
+      if (c + i * kStep < a.d) v.load(a.gamma, c + i * kStep); else v.zero();
+      v.floats(to);
     }
   };
   pdl_wait();
   pdl_launch_dependents();
-  const char* x = static_cast<const char*>(a.x) + row * static_cast<size_t>(a.ldx) * (kType == kFp32 ? 4 : 2);
   // (the residual, and X where Y is in its place, are read and written by each of several such kernels in a row, whose
   // CTAs share SMs: no read-only loads)
   {
+    const char* x = static_cast<const char*>(a.x) + (blockIdx.x * static_cast<size_t>(a.ldx) + c) * (kType == kFp32 ? 4 : 2);
+    const char* res = static_cast<const char*>(a.residual) + at * (kRType == kFp32 ? 4 : 2);
+    char* out = static_cast<char*>(a.residual_out) + at * (kRType == kFp32 ? 4 : 2);
     Load8<kType> v[kChunks];
     Load8<kRType> w[kResidual == kNone ? 1 : kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      if (c + i * stride < a.d) v[i].load_l2(x, c + i * stride); else v[i].zero();
+      const bool in = c + i * kStep < a.d;
+      if (in) v[i].load_l2(x, i * kStep); else v[i].zero();
       if constexpr (kResidual != kNone) {
-        const char* p = static_cast<const char*>(a.residual) + row * a.d * (kRType == kFp32 ? 4 : 2);
-        if (c + i * stride < a.d) w[i].load_l2(p, c + i * stride); else w[i].zero();
+        if (in) w[i].load_l2(res, i * kStep); else w[i].zero();
       }
     }
     if constexpr (kGammaEarly) {
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) load_gamma(i, i);
+      for (int i = 0; i < kChunks; ++i) load_gamma(i, g[i]);
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       if constexpr (kResidual == kSame && kType != kFp32) {  // packed additions, each rounded once
         v[i].v[0] = add_packed<kType>(v[i].v[0], w[i].v[0]);
-        if (c + i * stride < a.d) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + row * a.d + c + i * stride) = v[i].v[0];
+        if (c + i * kStep < a.d) *reinterpret_cast<uint4*>(out + 2 * i * kStep) = v[i].v[0];
       }
       v[i].floats(r[i]);
       if constexpr (kRType == kFp32 && kResidual != kNone) {
@@ -324,46 +328,59 @@ __global__ void __launch_bounds__(1024)
         w[i].floats(f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[i][j] += f[j];
-        if (c + i * stride < a.d) store8<kFp32>(static_cast<float*>(a.residual_out) + row * a.d + c + i * stride, r[i]);
+        if (c + i * kStep < a.d) store8<kFp32>(out + 4 * i * kStep, r[i]);
       }
     }
   }
   Pair sum{0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    float q = r[i][0] * r[i][0];
+    uint64_t q2 = 0;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) q = fmaf(r[i][j], r[i][j], q);
-    sum = add(sum, Pair{q, 0.0f});
+    for (int j = 0; j < 8; j += 2) {
+      const uint64_t v = pack2(__float_as_uint(r[i][j]), __float_as_uint(r[i][j + 1]));
+      if (j == 0) q2 = mul2(v, v); else fma2(q2, v, v);
+    }
+    float q, p;
+    unpack2(q2, q, p);
+    sum = add(sum, Pair{q + p, 0.0f});
   }
-  sum = warp_sum(sum);
+  sum = lanes_sum(sum, 32);
   if (warps > 1) {
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+    if (lane == 0) s_sum[threadIdx.x >> 5] = sum;
     __syncthreads();
-    const int l = threadIdx.x & 31;
-    sum = warp_sum(l < warps ? s_sum[l] : Pair{0.0f, 0.0f});
+    int group = 2;  // lanes that add up the warps' sums, each group for itself
+    while (group < warps) group *= 2;
+    const int l = lane & (group - 1);
+    sum = lanes_sum(l < warps ? s_sum[l] : Pair{0.0f, 0.0f}, group);
   }
   const Pair inv = inverse_root(sum, static_cast<float>(a.d), a.eps);
+  const size_t pitch = blk_scale_rows(a.T);
+  float* s_at = a.s + (c / kBlk) * pitch + blockIdx.x;  // used where a.q is there
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int col = c + i * stride;
-    if (col - 8 * static_cast<int>(threadIdx.x & 31) >= a.d) break;  // the same for the whole warp
+    const int col = c + i * kStep;
+    if (col - 8 * lane >= a.d) break;  // the same for the whole warp
     const int gi = kGammaEarly ? i : 0;
-    if constexpr (!kGammaEarly) load_gamma(i, 0);
+    if constexpr (!kGammaEarly) load_gamma(i, g[0]);
     float y[8];
+    const uint64_t inv2 = pack2(__float_as_uint(inv.hi), __float_as_uint(inv.hi));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = r[i][j] * inv.hi * g[gi][j];
-    if (a.y && col < a.d) store8(a.y_type, a.y, row * a.d + col, y);
+    for (int j = 0; j < 8; j += 2)
+      unpack2(mul2(mul2(pack2(__float_as_uint(r[i][j]), __float_as_uint(r[i][j + 1])), inv2),
+                   pack2(__float_as_uint(g[gi][j]), __float_as_uint(g[gi][j + 1]))), y[j], y[j + 1]);
+    if (a.y && col < a.d) store8(a.y_type, a.y, at + i * kStep, y);
     if (!a.q) continue;
-    const float m = __uint_as_float(half_warp_max(largest_bits(y)));
-    float s = blk_scale(__float_as_uint(m * (1.0f - kNormError)));
-    if (__any_sync(0xffffffffu, __float_as_uint(s) != __float_as_uint(blk_scale(__float_as_uint(m * (1.0f + kNormError)))))) {
+    const uint32_t m = half_warp_max(largest_bits(y));
+    float s = blk_scale(m);
+    // a largest magnitude within 8 last places (more than 2^-21 of it) of where the scale steps up
+    if (__any_sync(0xffffffffu, ((m + 0x1FFFFFu + 8u) & 0x7FFFFFu) <= 16u)) {
       double most = 0.0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmax(most, fabs(exact_value(r[i][j], g[gi][j], inv)));
 #pragma unroll
       for (int k = 1; k < 16; k *= 2) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, k));
-      if (m == m) s = blk_scale(__float_as_uint(odd_float(most)));
+      if (m <= 0x7F800000u) s = blk_scale(__float_as_uint(odd_float(most)));
     }
     const float t = blk_inverse(s);
     uint2 code = blk_codes8(y, t * (1.0f - kNormError));
@@ -374,8 +391,8 @@ __global__ void __launch_bounds__(1024)
       code = blk_codes8(y, 1.0f);
     }
     if (col < a.d) {
-      *reinterpret_cast<uint2*>(a.q + row * a.d + col) = code;
-      if ((threadIdx.x & 15) == 0) a.s[static_cast<size_t>(col / kBlk) * blk_scale_rows(a.T) + row] = s;
+      *reinterpret_cast<uint2*>(a.q + at + i * kStep) = code;
+      if ((lane & 15) == 0) s_at[2 * i * pitch] = s;
     }
   }
 }
