@@ -58,33 +58,59 @@ moe_status few_linear(const BlkX& x, int M, const moe_blk_mat* W, int N, int K, 
 
 int round16(int x) { return (x + 15) & ~15; }
 
-// Whether the product for few tokens is the faster one: its time grows with the weights' bytes and, past two MMAs' tokens,
-// with the tokens that go with them, the tensor cores' with the depth.  Measured (us, few / tensor cores; 32 tokens): 2048
-// x 2048 4.3 / 8.4, 4096 x 4096 10.2 / 12.9, 2048 -> 8192 11.0 / 8.5, 8192 x 8192 38 / 22; 8 tokens 2.8 / 8.3 and 18.8 /
-// 20.7 of the first and the last, 16 tokens 21.9 / 21.0 of the last.
-bool few_linear_wins(int M, int N, int K) {
-  if (M <= kBlkFewLinear / 2) return true;
-  return M <= kBlkFewLinear && 0.52e-6 * N * K < 2.5 + 0.00207 * K;
-}
-
-// Height of the dense product's token tiles, by a modelled time in microseconds: a CTA's tiles in turn, each a block of
-// 128 columns after another, then the epilogue.  Measured (tiles of 64 x 128 / of 128 x 256): 512 x 2048 -> 2048 7.1 / 10.9
-// us, 1024 x 2048 -> 2048 12.0 / 10.5, 256 x 8192 -> 8192 38.6 / 32.7, 4096 x 4096 -> 4096 - / 66.
-int linear_tile(int M, int N, int K, int num_sms) {
-  if (M <= kBlkNarrow) return round16(M);
-  auto turns = [&](int rows, int cols) {
-    const long long tiles = static_cast<long long>((N + rows - 1) / rows) * ((M + cols - 1) / cols);
-    return static_cast<double>((tiles + num_sms - 1) / num_sms);
-  };
+// How a dense product is computed, by modelled times in microseconds (a kernel of its own on the GPU).
+struct LinearPlan {
+  bool few;   // the products for few tokens
+  int bn;     // else the height of the tiles of tokens (more than kBlkNarrow: the wide kernel's)
+  int split;  // and the CTAs that share a tile's blocks of 128 columns
+};
+LinearPlan linear_plan(int M, int N, int K, int num_sms) {
   const int blocks = blk_count(K);
-  const double narrow = turns(kBlk, kBlkNarrow) * (0.29 * blocks + 0.4);
-  const double wide = turns(2 * kBlk, 128) * (0.48 * blocks + 1.2);
-  return wide < narrow ? 128 : kBlkNarrow;
+  const double stream = static_cast<double>(N) * K / 5.5e6;  // the weights' bytes, as fast as these kernels get them
+  LinearPlan best{};
+  double time = 1e30;
+  auto consider = [&](double t, bool few, int bn, int split) {
+    if (t >= time) return;
+    time = t;
+    best = LinearPlan{few, bn, split};
+  };
+  if (M <= kBlkFewLinear) {
+    // a CTA's eight warps take a block each in turn.  Measured, 2048 -> 2048 / 5120 -> 1024 / 8192 -> 8192: 8 tokens 2.9 /
+    // 5.0 / 18.9 us, 16 tokens 3.1 / 5.7 / 22.2, 32 tokens 4.4 / 9.9 / 38
+    const double ctas = 0.9 * N / (16.0 * num_sms);  // an SM's, which share its loads
+    const double per_block = M <= 8 ? 0.7 : M <= 16 ? 0.87 : 1.7;
+    consider(1.4 + per_block * blocks / 8 * (ctas > 1 ? ctas : 1), true, 0, 1);
+  }
+  auto tiles = [&](int rows, int cols) { return static_cast<long long>((N + rows - 1) / rows) * ((M + cols - 1) / cols); };
+  auto turns = [&](long long n) { return static_cast<double>((n + num_sms - 1) / num_sms); };
+  // Tiles of up to 16 / 32 / 64 tokens (and 128 weight rows): 0.235 / 0.25 / 0.33 us a block.  A cluster's CTAs lie in one
+  // GPC and join their sums in 2 us.  Measured, tokens x K -> N, tile / CTAs: 333 x 2816 -> 1001 32/1 8.0, 64/1 9.0, 64/2 8.1,
+  // 64/3 (144 CTAs, which do not all fit their GPCs) 12.1; 64 x 2048 -> 2048 64/1 7.1, 64/4 5.1, 64/8 10.3; 64 x 8192 ->
+  // 1024 64/1 21.9, 64/4 8.7, 64/8 7.1; 16 x 8192 -> 8192 16/1 18.2, 16/2 14.7
+  for (int most = 16; most <= kBlkNarrow; most *= 2) {
+    const int bn = round16(M) < most ? round16(M) : most;
+    const double per_block = bn <= 16 ? 0.235 : bn <= 32 ? 0.25 : 0.33;
+    const long long n = tiles(kBlk, bn);
+    for (int split = 1; split <= 8 && split <= blocks; split *= 2) {
+      // CTAs whose clusters of 2 / 4 / 8 find a place at once
+      const int room = split == 2 ? num_sms : split == 4 ? num_sms - num_sms / 8 : num_sms / 2;
+      if (split > 1 && n * split > room) break;
+      const double work = turns(n * split) * (per_block * ((blocks + split - 1) / split) + 0.4);
+      consider(1.7 + (work > stream ? work : stream) + (split > 1 ? 2.0 : 0.0), false, bn, split);
+    }
+    if (bn < most) break;
+  }
+  // 128 tokens x 256 weight rows: 256 x 8192 -> 8192 32.7 us (64/1 43.9), 300 x 2048 -> 4096 10.3 (64/1 12.7)
+  if (M > kBlkNarrow) consider(1.8 + turns(tiles(2 * kBlk, 128)) * (0.44 * blocks + 1.2), false, 128, 1);
+  return best;
 }
 
 moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
                   uint32_t* status, moe_stream stream) {
-  if (few_linear_wins(M, N, K)) return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
+  const int num_sms = device_sms();
+  if (num_sms <= 0) return MOE_ERR_CUDA;
+  const LinearPlan plan = linear_plan(M, N, K, num_sms);
+  if (plan.few) return few_linear(BlkX{A.q, A.s, K, blk_scale_rows(M), kBlkCodes}, M, W, N, K, Y, y_type, stream);
   BlkLinearArgs a{};
   a.sw = W->s;
   a.sx = A.s;
@@ -95,9 +121,9 @@ moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int 
   a.N = N;
   a.K = K;
   a.y_type = y_type;
-  a.num_sms = device_sms();
-  if (a.num_sms <= 0) return MOE_ERR_CUDA;
-  a.bn = linear_tile(M, N, K, a.num_sms);
+  a.num_sms = num_sms;
+  a.bn = plan.bn;
+  a.split = plan.split;
   const bool wide = a.bn > kBlkNarrow;
   BlkLinearMaps maps;
   if (!encode_mx_weights(&maps.w, W->q, 1, N, K, kBlk) || !encode_mx_codes(&maps.x, A.q, M, K, a.bn)) return MOE_ERR_CUDA;

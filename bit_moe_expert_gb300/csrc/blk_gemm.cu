@@ -186,6 +186,35 @@ __device__ __forceinline__ bool epilogue(const BlkLinearArgs& a, const Item& m, 
   return true;
 }
 
+// A tile whose blocks a cluster's CTAs share: a warp's sums to shared memory, [token][kBlk rows], and the CTAs' sums of
+// every a.split-th token, added up in the CTAs' order, to Y.
+template <typename V>
+__device__ __forceinline__ void put_sums(float* to, int rows, const Sums<V>& acc, int quarter, int part, int lane) {
+#pragma unroll
+  for (int g = 0; g < V::kGroups; ++g) {
+    const int c0 = V::kGroup * (g * kParts + part);
+#pragma unroll
+    for (int c = 0; c < V::kGroup; ++c)
+      if (c0 + c < rows) to[(c0 + c) * kBlk + 32 * quarter + lane] = acc.get(0, g, c);
+  }
+}
+__device__ __forceinline__ void join_sums(const BlkLinearArgs& a, const Item& m, const float* sums, int warp, int lane) {
+  const int rank = static_cast<int>(cluster_ctarank()), n = m.row_m + 4 * lane;
+  for (int t = rank + a.split * warp; t < m.rows; t += a.split * kSumWarps) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < a.split; ++p) {
+      const float4 f = ld_shared_cluster_f4(mapa_shared(sums + t * kBlk + 4 * lane, p));
+      v[0] += f.x;
+      v[1] += f.y;
+      v[2] += f.z;
+      v[3] += f.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < a.N) store1(a.y_type, a.y, static_cast<size_t>(m.row_n + t) * a.N + n + j, v[j]);
+  }
+}
+
 __device__ __forceinline__ void prefetch_maps(const BlkLinearMaps& m) {
   tma_prefetch_desc(&m.w);
   tma_prefetch_desc(&m.x);
@@ -270,11 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* bar = &full[stage];
             if (weights) {
               mbar_arrive_expect_tx(bar, kMats * kMatBytes);
-              tma_load_3d(st, m.m0, bar, kb * kBlk, m.row_m, m.e);
-              if (kGU) tma_load_3d(st + kMatBytes, m.m1, bar, kb * kBlk, m.row_m, m.e);
+              tma_load_3d(st, m.m0, bar, (m.kb0 + kb) * kBlk, m.row_m, m.e);
+              if (kGU) tma_load_3d(st + kMatBytes, m.m1, bar, (m.kb0 + kb) * kBlk, m.row_m, m.e);
             } else if (warp == kActivationsWarp) {
               mbar_arrive_expect_tx(bar, m.box * 128);
-              tma_load_2d(st + kMats * kMatBytes, m.n, bar, kb * kBlk, m.row_n);
+              tma_load_2d(st + kMats * kMatBytes, m.n, bar, (m.kb0 + kb) * kBlk, m.row_n);
             } else {
               mbar_arrive_expect_tx(bar, m.sn_bytes);
               bulk_g2s(scales + slot * p.bn, sn, m.sn_bytes, bar);
@@ -436,6 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      if constexpr (V::kMode == kLinear) {
+        if (a.split > 1) {  // every MMA of the item has completed: the stages' memory is free
+          put_sums<V>(reinterpret_cast<float*>(stages), m.rows, acc, quarter, part, lane);
+          continue;
+        }
+      }
       ok = epilogue<V>(a, m, acc, quarter, part, lane, maxima + 4 * parity, [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&part_met[part]);
@@ -448,6 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (V::kMode == kLinear) {
+    if (a.split > 1) {
+      cluster_arrive_release();
+      cluster_wait();
+      if (warp >= kSumWarp0) join_sums(a, item(0), reinterpret_cast<const float*>(stages), warp - kSumWarp0, lane);
+      cluster_arrive_release();  // (the others' shared memory has been read)
+      cluster_wait();
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -456,21 +500,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename V>
 cudaError_t launch(int kind, const typename Args<V::kMode>::maps& maps, const typename Args<V::kMode>::type& a, int bn,
-                   int grid, cudaStream_t stream, bool pdl) {
+                   int grid, int cluster, cudaStream_t stream, bool pdl) {
   const Plan p = make_plan(V::kMats, bn);
   const int smem = plan_smem(p);
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(blk_gemm_kernel<V>), smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   timer_begin(kind, stream);
   e = cudaLaunchKernelEx(&cfg, blk_gemm_kernel<V>, maps, a, p);
   timer_end(kind, stream);
@@ -480,10 +527,10 @@ cudaError_t launch(int kind, const typename Args<V::kMode>::maps& maps, const ty
 // The variant for tiles of bn tokens.
 template <int kMode>
 cudaError_t launch_for(int kind, const typename Args<kMode>::maps& maps, const typename Args<kMode>::type& a, int bn,
-                       int grid, cudaStream_t stream, bool pdl) {
-  if (bn <= 16) return launch<Variant<kMode, 16>>(kind, maps, a, bn, grid, stream, pdl);
-  if (bn <= 32) return launch<Variant<kMode, 32>>(kind, maps, a, bn, grid, stream, pdl);
-  return launch<Variant<kMode, 64>>(kind, maps, a, bn, grid, stream, pdl);
+                       int grid, int cluster, cudaStream_t stream, bool pdl) {
+  if (bn <= 16) return launch<Variant<kMode, 16>>(kind, maps, a, bn, grid, cluster, stream, pdl);
+  if (bn <= 32) return launch<Variant<kMode, 32>>(kind, maps, a, bn, grid, cluster, stream, pdl);
+  return launch<Variant<kMode, 64>>(kind, maps, a, bn, grid, cluster, stream, pdl);
 }
 
 }  // namespace
@@ -491,13 +538,14 @@ cudaError_t launch_for(int kind, const typename Args<kMode>::maps& maps, const t
 cudaError_t launch_blk_linear(const BlkLinearArgs& a, const BlkLinearMaps& maps, cudaStream_t stream, bool pdl) {
   const long long items = static_cast<long long>(blk_count(a.N)) * ((a.M + a.bn - 1) / a.bn);
   if (items > (1ll << 30)) return cudaErrorInvalidValue;
-  return launch_for<kLinear>(kKBlkGemm, maps, a, a.bn, static_cast<int>(items < a.num_sms ? items : a.num_sms), stream, pdl);
+  const int grid = static_cast<int>(a.split > 1 ? items * a.split : items < a.num_sms ? items : a.num_sms);
+  return launch_for<kLinear>(kKBlkGemm, maps, a, a.bn, grid, a.split, stream, pdl);
 }
 
 cudaError_t launch_blk_experts(const BlkExpertArgs& a, const BlkExpertMaps& maps, cudaStream_t stream, bool pdl) {
-  cudaError_t e = launch_for<kGateUp>(kKBlkGateUp, maps, a, a.pitch, a.num_sms, stream, pdl);
+  cudaError_t e = launch_for<kGateUp>(kKBlkGateUp, maps, a, a.pitch, a.num_sms, 1, stream, pdl);
   if (e != cudaSuccess) return e;
-  e = launch_for<kDown>(kKBlkDown, maps, a, a.pitch, a.num_sms, stream, pdl);
+  e = launch_for<kDown>(kKBlkDown, maps, a, a.pitch, a.num_sms, 1, stream, pdl);
   if (e != cudaSuccess) return e;
   return launch_mx_combine(a.ypart, a.inv_perm, a.w, a.T, a.d, a.k, a.I_shared > 0, a.y, a.status, a.num_sms, stream);
 }

@@ -22,6 +22,7 @@ struct Item {
   uint32_t sn_bytes;
   int e, row_m, row_n;             // matrix of the M side; first rows of the codes
   int mt, rows, K, box;            // M tile, valid tokens, depth, tokens that the TMA box brings
+  int kb0;                         // first block of columns
   int row0, slot;                  // experts: first row among the assignments (or tokens), tile slot
   bool shared, ok;
 };
@@ -56,8 +57,9 @@ __device__ __forceinline__ Sched make_sched(const BlkLinearArgs& a, int bn, bool
   Sched s{};
   s.mt_r = (a.N + kRows - 1) / kRows;
   const int total = s.mt_r * ((a.M + bn - 1) / bn);
-  s.first = blockIdx.x;
-  s.step = gridDim.x;
+  const unsigned split = kRows == kBlk ? a.split : 1;
+  s.first = blockIdx.x / split;
+  s.step = gridDim.x / split;
   s.n = (total - s.first + s.step - 1) / s.step;
   return s;
 }
@@ -81,6 +83,13 @@ __device__ __forceinline__ Item get_item(const BlkLinearArgs& a, const BlkLinear
   m.sn = a.sx + m.row_n;
   m.sn_step = a.sx_pitch;
   m.sn_bytes = 4 * static_cast<uint32_t>(min(static_cast<long long>(bn), a.sx_pitch - m.row_n));
+  if (kRows == kBlk && a.split > 1) {  // this CTA's share of the blocks
+    const int blocks = blk_count(a.K), rank = blockIdx.x % static_cast<unsigned>(a.split);
+    m.kb0 = blocks * rank / a.split;
+    m.K = min(a.K, blocks * (rank + 1) / a.split * kBlk) - m.kb0 * kBlk;
+    m.s0 += m.kb0;
+    m.sn += m.kb0 * m.sn_step;
+  }
   m.ok = true;
   return m;
 }

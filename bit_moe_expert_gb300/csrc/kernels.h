@@ -405,6 +405,7 @@ struct BlkLinearArgs {
   int M, N, K, y_type;
   int bn;  // height of the tokens' tiles: a multiple of 16 up to 128 (wide: 128)
   int num_sms;
+  int split;    // narrow: CTAs, a cluster, that share a tile's blocks of columns
   int y_boxed;  // wide: maps.y is there
 };
 struct BlkLinearMaps {

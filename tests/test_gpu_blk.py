@@ -169,6 +169,26 @@ def test_matmul(M, N, K, y_kind):
     _assert_product(y[:M], v * blk_ref.spread(s.astype(np.float64), K), blk_ref.weights(mat)[0], K)
 
 
+@pytest.mark.parametrize("M,N,K", [(8, 8192, 8192), (16, 2049, 8208), (33, 130, 4112), (48, 1000, 1040), (64, 640, 2064), (70, 1001, 1040),
+                                   (96, 129, 272), (100, 300, 20016), (333, 1001, 2816), (500, 256, 1168)])
+def test_matmul_whose_blocks_several_ctas_share(M, N, K):
+    """Few tiles and many blocks of columns, a short last one among them; the same bits in every call."""
+    rng = np.random.default_rng(M + N + K)
+    v, s = blk_ref.quantise(rng.standard_normal((M, K)) * np.exp(rng.standard_normal((M, 1))))
+    s = (s * rng.uniform(0.6, 1.7, s.shape)).astype(np.float32)
+    mat = blk_ref.draw_matrix(rng, 1, N, K)
+    a, m, ws = _act(v, s), _mat(mat), bm.workspace(256)
+    y = torch.full((M + 1, N), 7.0, dtype=torch.float32, device="cuda")
+    first = None
+    for _ in range(4):
+        bm.moe_blk_matmul(a, m, y[:M], ws)
+        assert first is None or torch.equal(y, first)
+        first = y.clone()
+    assert bm.moe_check_status(ws) == 0
+    assert (y[M] == 7).all()
+    _assert_product(y[:M], v * blk_ref.spread(s.astype(np.float64), K), blk_ref.weights(mat)[0], K)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 2048, 2048), (1, 17, 16), (5, 100, 1040), (8, 2048, 512), (9, 300, 272), (333, 1001, 2816)])
 @pytest.mark.parametrize("x_kind", list(TYPES))
 def test_linear(T, N, K, x_kind):
