@@ -87,46 +87,58 @@ __device__ __forceinline__ void put_box(uint8_t* box, const Sums& acc, int c, in
   }
 }
 
-// The warp's columns of its 32 tokens, of which `rows` exist, from column n0 of the result on: by boxes and TMA stores
-// where `boxed`, through a box where the result's rows are `aligned` to 16 bytes, else by each lane.  `first`: the first
-// token's row of the result, whose rows are N elements long; `turn`: the warp's next box.
+// The warp's columns of its 32 tokens, of which `rows` exist, from column n0 of the result on, through boxes: by TMA stores
+// where `boxed`, by 16-byte stores where the result's rows are `aligned` to them, else by a word or a 16-bit value a lane,
+// 64 bytes of a row at a time (4000 x 2048 -> 4000 / 4002 / 4001 of bf16: 37 / 42 / 48 us by the three; 187 where each lane
+// wrote its token's elements).  `first`:
+// the first token's row of the result, whose rows are N elements long; `turn`: the warp's next box.
 template <int kType>
 __device__ __forceinline__ void store_rows(const Sums& acc, const CUtensorMap* map, uint8_t* boxes, int& turn, bool boxed, bool aligned,
                                            void* y, long long first, int rows, int n0, int N, int lane) {
   constexpr int kBytes = kType == kFp32 ? 4 : 2, kWide = 64 / kBytes;  // columns of a box
-  if (aligned) {
 #pragma unroll
-    for (int c = 0; c < kOwn; c += kWide) {
-      if (n0 + c >= N) break;
-      uint8_t* box = boxes + turn * kBoxBytes;
-      turn = turn + 1 == kBoxes ? 0 : turn + 1;
-      if (lane == 0) bulk_wait_group_read<kBoxes - 1>();  // this box has been read
+  for (int c = 0; c < kOwn; c += kWide) {
+    if (n0 + c >= N) break;
+    uint8_t* box = boxes + turn * kBoxBytes;
+    turn = turn + 1 == kBoxes ? 0 : turn + 1;
+    if (lane == 0) bulk_wait_group_read<kBoxes - 1>();  // this box has been read
+    __syncwarp();
+    put_box<kType>(box, acc, c, lane);
+    if (boxed) {
+      fence_proxy_async_smem();
       __syncwarp();
-      put_box<kType>(box, acc, c, lane);
-      if (boxed) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(map, box, n0 + c, static_cast<int>(first));
-          bulk_commit_group();
-        }
-      } else {
-        __syncwarp();
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 8) {  // four lanes a row
-          const int r = r0 + (lane >> 2), col = n0 + c + (lane & 3) * (16 / kBytes);
-          const uint4 v = *reinterpret_cast<const uint4*>(box + 64 * r + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
-          if (r < rows && col < N) *reinterpret_cast<uint4*>(static_cast<char*>(y) + ((first + r) * N + col) * kBytes) = v;
-        }
-        __syncwarp();
-        if (lane == 0) bulk_commit_group();  // an empty one: a box's turn is a group's
+      if (lane == 0) {
+        tma_store_2d(map, box, n0 + c, static_cast<int>(first));
+        bulk_commit_group();
       }
+      continue;
     }
-  } else if (lane < rows) {
-    const size_t at = static_cast<size_t>(first + lane) * N + n0;
+    __syncwarp();
+    if (aligned) {
 #pragma unroll
-    for (int c = 0; c < kOwn; ++c)
-      if (n0 + c < N) store1(kType, y, at + c, acc.get(c));
+      for (int r0 = 0; r0 < 32; r0 += 8) {  // four lanes a row
+        const int r = r0 + (lane >> 2), col = n0 + c + (lane & 3) * (16 / kBytes);
+        const uint4 v = *reinterpret_cast<const uint4*>(box + 64 * r + 16 * ((lane & 3) ^ ((r >> 1) & 3)));
+        if (r < rows && col < N) *reinterpret_cast<uint4*>(static_cast<char*>(y) + ((first + r) * N + col) * kBytes) = v;
+      }
+    } else {
+      // words of the box's rows, two rows at a time, or 16-bit values of odd N
+      auto store = [&](auto element) {
+        using Element = decltype(element);
+        constexpr int kSize = sizeof(Element), kRow = 64 / kSize;
+        const int at = lane % kRow * kSize, col = n0 + c + at / kBytes;
+        char* to = static_cast<char*>(y) + ((first + lane / kRow) * N + col) * kBytes;
+#pragma unroll 8
+        for (int i = 0; i < kRow; ++i, to += static_cast<size_t>(32 / kRow) * N * kBytes) {
+          const int r = lane / kRow + i * (32 / kRow);
+          const Element v = *reinterpret_cast<const Element*>(box + 64 * r + 16 * ((at >> 4) ^ ((r >> 1) & 3)) + (at & 15));
+          if (r < rows && col < N) *reinterpret_cast<Element*>(to) = v;
+        }
+      };
+      if (kBytes == 4 || N % 2 == 0) store(uint32_t{}); else store(uint16_t{});
+    }
+    __syncwarp();
+    if (lane == 0) bulk_commit_group();  // an empty one: a box's turn is a group's
   }
 }
 
