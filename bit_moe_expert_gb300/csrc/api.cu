@@ -65,9 +65,13 @@ bool encode(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* ptr,
     key.rank = rank;
     key.dt = static_cast<int>(dt);
     key.sw = static_cast<int>(sw);
-    uint64_t h = 1469598103934665603ull;  // FNV-1a over the key's bytes
-    const unsigned char* kb = reinterpret_cast<const unsigned char*>(&key);
-    for (size_t i = 0; i < sizeof(key); ++i) h = (h ^ kb[i]) * 1099511628211ull;
+    uint64_t words[sizeof(key) / 8], h = 1469598103934665603ull;
+    static_assert(sizeof(key) % 8 == 0, "hashed by 64-bit words");
+    std::memcpy(words, &key, sizeof(key));
+    for (const uint64_t w : words) {
+      h = (h ^ w) * 1099511628211ull;
+      h ^= h >> 29;
+    }
     const int slot = static_cast<int>(h % kMapCache);
     {
       std::lock_guard<std::mutex> lock(g_maps_mu);
