@@ -139,10 +139,25 @@ moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int 
 }
 
 // Tile heights of an expert call in MMA columns.
-int routed_rows(int block_rows) { return round16(block_rows); }
+int routed_rows(int T, int k, int block_rows) {
+  const long long most = T < 1 ? 1 : static_cast<long long>(T) * k;  // a tile's rows are assignments
+  return round16(most < block_rows ? static_cast<int>(most) : block_rows);
+}
 int shared_tile_rows(int T, int block_rows) {
-  const int rows = routed_rows(block_rows), most = round16(T < 1 ? 1 : T);
+  const int rows = round16(block_rows), most = round16(T < 1 ? 1 : T);
   return most < rows ? most : rows;
+}
+
+// Whether the products for few tokens are the faster ones: two launches instead of four, but a down product whose CTAs (16
+// columns of Y, one an SM) go through every assignment's blocks of h.  Those, times the CTAs' turns, against the
+// difference measured (us; T, d, I, k, s: a shared expert): 16 (6, 1600, 128, 2) -4.4; 32 (8, 1024, 256, 2) -1.7; 68 (2, 2048,
+// 512, 8, s) -0.9; 72 (1, 2560, 704, 5, s) -0.7; 96 (8, 1856, 288, 4) 2.7; 100 (3, 2048, 512, 8, s) 2.1; 108 (4, 2560, 704, 2, s)
+// 2.7; 132 (2, 2048, 1408, 6) 5.8; 156 (1, 2560, 704, 12, s) 5.3; 288 (1, 4096, 2048, 8, s) 18.5.
+bool few_experts_win(int T, int d, int I, int k, int I_shared) {
+  if (T > kBlkFewT) return false;
+  const long long units = static_cast<long long>(T) * k * blk_count(I) + blk_count(I_shared);
+  const int sms = 152;  // (a workspace's size does not depend on the current device)
+  return units * ((d / 16 + sms - 1) / sms) <= 72;
 }
 
 struct ExpertLayout {
@@ -154,7 +169,7 @@ struct ExpertLayout {
 ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
   ExpertLayout L{};
   L.max_blocks = moe_route_max_blocks(T, E, k, block_rows);
-  L.bn_r = routed_rows(block_rows);
+  L.bn_r = routed_rows(T, k, block_rows);
   L.bn_s = shared_tile_rows(T, block_rows);
   L.pitch = L.bn_r > L.bn_s ? L.bn_r : L.bn_s;
   const size_t A = static_cast<size_t>(T) * k, rows = A + (I_shared > 0 ? T : 0);
@@ -165,7 +180,7 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
     o = round256(o + bytes);
     return at;
   };
-  L.few = T <= kBlkFewT;
+  L.few = few_experts_win(T, d, I, k, I_shared);
   const size_t h_bytes = static_cast<size_t>(I > I_shared ? I : I_shared) * 4;
   if (L.few) {
     L.h = take(rows * h_bytes);
@@ -180,8 +195,11 @@ ExpertLayout expert_layout(int T, int d, int I, int E, int k, int I_shared, int 
   L.sh_r = take(static_cast<size_t>(L.max_blocks) * blk_count(I) * L.pitch * 4);
   L.sh_s = take(tiles_s * blk_count(I_shared) * L.pitch * 4);
   // a workspace for T tokens is one for fewer: the few tokens' fp32 h may be larger than all of the above
-  const size_t few = sizeof(WsHeader) + round256(static_cast<size_t>(kBlkFewT) * (k + (I_shared > 0 ? 1 : 0)) * h_bytes);
-  L.total = o > few ? o : few;
+  for (size_t t = 1; t <= kBlkFewT && few_experts_win(static_cast<int>(t), d, I, k, I_shared); ++t) {
+    const size_t few = sizeof(WsHeader) + round256(t * (k + (I_shared > 0 ? 1 : 0)) * h_bytes);
+    if (few > o) o = few;
+  }
+  L.total = o;
   return L;
 }
 

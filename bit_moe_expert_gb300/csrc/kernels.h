@@ -367,8 +367,8 @@ struct BlkX {
   int type;
 };
 // Few tokens: weights straight into the registers of warp-level MMAs.  One token of any type, or up to kBlkFewLinear
-// that are codes; experts up to kBlkFewT (an MMA's eight columns are the most).
-constexpr int kBlkFewT = 2;
+// that are codes; experts up to kBlkFewT (an MMA's columns).
+constexpr int kBlkFewT = 8;
 constexpr int kBlkFewLinear = 32;
 struct BlkFewLinearArgs {
   BlkX x;

@@ -128,8 +128,8 @@ size_t moe_blk_forward_workspace_bytes(int T, int d, int I, int E, int k, int I_
  *           NULL
  * Other arguments as for moe_forward; d, I and I_shared multiples of 32.  In
  * tables of the caller's own a token may take an expert more than once (for T <=
- * 2 a tile then has at most 8 rows: MOE_ERR_INVALID_ARG in the status word
- * above).
+ * 8 a tile then has at most 8 rows: MOE_ERR_INVALID_ARG in the status word
+ * above, by some of the paths that sizes take).
  * MOE_ERR_UNSUPPORTED also where moe_route_max_blocks times ceil(max(d, I) /
  * 128), plus the shared expert's tiles likewise, is above 2^30. */
 moe_status moe_blk_forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I, int k,

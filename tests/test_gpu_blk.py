@@ -298,6 +298,15 @@ def test_forward(T, d, I, I_shared, E, k, rows, quantised):
     _assert_layer(y[:T], blk_ref.layer(v * blk_ref.spread(s, d), routed_host, shared_host, ids, w.astype(np.float64)), I)
 
 
+@pytest.mark.parametrize("T,d,I,I_shared,E,k,rows", [(1, 256, 1184, 0, 12, 8, 16), (2, 256, 608, 96, 8, 8, 33), (2, 320, 1216, 0, 9, 7, 128),
+                                                     (8, 256, 96, 0, 16, 1, 16), (5, 2464, 64, 32, 12, 3, 16), (7, 512, 352, 0, 4, 3, 3),
+                                                     (1, 2560, 704, 704, 40, 12, 64), (8, 1024, 256, 0, 3, 2, 16)])
+@pytest.mark.parametrize("quantised", [False, True])
+def test_forward_of_few_tokens(T, d, I, I_shared, E, k, rows, quantised):
+    """Either way of computing few tokens, at sizes on both sides of where one follows on the other."""
+    test_forward(T, d, I, I_shared, E, k, rows, quantised)
+
+
 def test_forward_with_experts_that_nobody_takes_and_one_that_all_take():
     rng = np.random.default_rng(8)
     T, d, I, E, k, rows = 100, 256, 128, 9, 2, 32
