@@ -410,11 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the stage's barrier tells that its MMAs have completed, to the loads that take its place and to the sums: it
         // cannot be a phase further before these have released the accumulator (there are no more of them than stages)
-        if (!mbar_wait(&empty[stage], phase, abort_flag)) {
-          if (lane == 0) fail();
-          ok = false;
-          break;
-        }
+        // (where the wait gives up the warp goes on with what is there: its lanes stay together, and it meets the flag again)
+        mbar_wait_issue(&empty[stage], phase, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
         const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + accb * kMats * p.bn;
@@ -474,9 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = epilogue<V>(a, m, acc, quarter, part, lane, maxima + 4 * parity, [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&part_met[part]);
-        const bool met = mbar_wait(&part_met[part], parity, abort_flag);
+        const bool met = mbar_wait_warp(&part_met[part], parity, abort_flag);
         if (!met && lane == 0) fail();
-        __syncwarp();
         return met;
       });
       parity ^= 1;  // a warp two items ahead has met all the others in between: two sets of maxima are enough

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return kGU ? c / (kOwn / 2) * kBlk + kOwn / 2 * part + c % (kOwn / 2) : kOwn * part + c;
     };
     auto wait_full = [&]() {
-      if (mbar_wait(&acc_full[acc], accphase, abort_flag)) return true;
+      if (mbar_wait_warp(&acc_full[acc], accphase, abort_flag)) return true;
       if (lane == 0) fail();
       return false;
     };
@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        __syncwarp();
         tc_fence_after();
         uint64_t w[2];
         {
@@ -444,9 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = epilogue_gate_up(a, m, sum, quarter, part, lane, maxima + kParts * parity, [&]() {
           __syncwarp();
           if (lane == 0) mbar_arrive(&met[quarter]);
-          const bool m2 = mbar_wait(&met[quarter], parity, abort_flag);
+          const bool m2 = mbar_wait_warp(&met[quarter], parity, abort_flag);
           if (!m2 && lane == 0) fail();
-          __syncwarp();
           return m2;
         });
         parity ^= 1;  // a warp two items ahead has met the other one in between: two sets of maxima are enough

@@ -595,11 +595,10 @@ __global__ void __launch_bounds__(V::kThreads, 1)
         if (lane == 0) record_status(a.status, MOE_ERR_INVALID_ARG);
         continue;
       }
-      if (!mbar_wait(&acc_full[accb], accphase, abort_flag)) {
+      if (!mbar_wait_warp(&acc_full[accb], accphase, abort_flag)) {
         if (lane == 0) fail();
         break;
       }
-      __syncwarp();
       tc_fence_after();
       const uint32_t tbase = tmem + (static_cast<uint32_t>(lanegrp * 32) << 16) + accb * kMats * p.bn;
       auto release = [&]() {
@@ -803,11 +802,10 @@ __global__ void __launch_bounds__(PairVariant::kThreads, 1)
     const uint32_t acc_empty0 = mapa_shared(acc_empty, 0);
     uint32_t accphase = 0;
     for (int it = first; it < items; it += step) {
-      if (!mbar_wait(acc_full, accphase, abort_flag)) {
+      if (!mbar_wait_warp(acc_full, accphase, abort_flag)) {
         if (lane == 0) fail();
         break;
       }
-      __syncwarp();
       tc_fence_after();
       auto release = [&]() {
         tc_fence_before();

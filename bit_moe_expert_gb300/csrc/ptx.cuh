@@ -89,6 +89,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same wait of a whole warp, which ends alike in all lanes: what follows it (loads of tensor memory, shuffles) is for all
+// of them, and where one gives up another may have seen the phase complete.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // The same wait for loops that issue tensor-core work, everything but the first
 // try out of line (inline, with the record of a failure, it cost up to 140
 // clocks an iteration even where the phase had completed).  A wait that gives
