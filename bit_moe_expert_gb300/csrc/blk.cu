@@ -508,8 +508,8 @@ constexpr size_t kMaxUnits = 0x7FFFFFFFu / (kThreads / 32);  // a unit's number 
 template <int kType>
 cudaError_t launch_norm(const NormArgs& a, int residual, cudaStream_t stream, bool pdl) {
   // one chunk a thread for few rows, where latency counts; more of them where there are many, so that an SM has more
-  // CTAs, which wait for their sums at different times (8192 rows of 8192 with the residual, 1 / 2 / 4 chunks: 159 / 113
-  // / 90 us; 4096 of 2048 25.0 / 23.5 / 24.4)
+  // CTAs, which wait for their sums at different times (8192 rows of 8192 with the residual, 1 / 2 / 4 chunks: 160 / 107
+  // / 84 us; 4096 of 2048, with the inverse, 22.3 / 20.8 / 23.3; 16 of 4096, with the inverse, 4.0 / 4.6 / 5.4)
   int chunks = a.T < 512 ? 1 : a.d <= 2048 ? 2 : 4;
   while (a.d > 8 * 1024 * chunks) chunks *= 2;
   const int threads = ((a.d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32;

@@ -18,6 +18,11 @@
 // the activations and of their scales, warp 2 the MMAs' issue, warps 4 to 11 the sums: two per
 // quarter of the tensor-memory lanes, the tokens' groups in turn.  Every wait is
 // bounded and records MOE_ERR_TIMEOUT.
+//
+// A block after another takes 0.23 to 0.33 us, for the most part the way from MMA
+// to sums.  So a dense product of few tiles divides each tile's blocks among the
+// CTAs of a cluster, which leave their sums in shared memory and add them up, every
+// CTA some tokens', in the CTAs' order.
 #include <cuda_runtime.h>
 
 #include "blk_items.cuh"

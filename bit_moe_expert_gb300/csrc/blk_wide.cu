@@ -12,7 +12,7 @@
 // quarter of the tensor-memory lanes (32 tokens), 128 columns each.  Rows of
 // results leave through shared memory as TMA stores, 64 bytes of 32 rows at a time
 // (a lane's own stores would touch a line each); the last, partial 32 rows of an
-// expert by plain stores.  Every wait is bounded and records MOE_ERR_TIMEOUT.
+// expert, and rows that are not 16-byte aligned, by plain stores from there.  Every wait is bounded and records MOE_ERR_TIMEOUT.
 #include <cuda_runtime.h>
 
 #include "blk_items.cuh"
