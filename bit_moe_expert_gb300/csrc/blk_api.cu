@@ -148,6 +148,22 @@ int shared_tile_rows(int T, int block_rows) {
   return most < rows ? most : rows;
 }
 
+constexpr int kSms = 152;  // (a workspace's size does not depend on the current device)
+long long few_units(int T, int I, int k, int I_shared) { return static_cast<long long>(T) * k * blk_count(I) + blk_count(I_shared); }
+// CTAs, a cluster, that share the down product's work on their columns: while there is work for their 16 warps each, and room
+// for the clusters (see linear_plan).
+int few_split(int T, int d, int I, int k, int I_shared) {
+  const int ctas = (d + kBlkFewRows - 1) / kBlkFewRows;
+  const long long units = few_units(T, I, k, I_shared);
+  int split = 1;
+  for (int next = 2; next <= 8; next *= 2) {
+    const int room = next == 2 ? kSms : next == 4 ? kSms - kSms / 8 : kSms / 2;
+    if (ctas * next > room || units <= 16 * split) break;
+    split = next;
+  }
+  return split;
+}
+
 // Whether the products for few tokens are the faster ones: two launches instead of four, but a down product whose CTAs (16
 // columns of Y, one an SM) go through every assignment's blocks of h.  Those, times the CTAs' turns, against the
 // difference measured (us; T, d, I, k, s: a shared expert): 16 (6, 1600, 128, 2) -4.4; 32 (8, 1024, 256, 2) -1.7; 68 (2, 2048,
@@ -155,9 +171,10 @@ int shared_tile_rows(int T, int block_rows) {
 // 2.7; 132 (2, 2048, 1408, 6) 5.8; 156 (1, 2560, 704, 12, s) 5.3; 288 (1, 4096, 2048, 8, s) 18.5.
 bool few_experts_win(int T, int d, int I, int k, int I_shared) {
   if (T > kBlkFewT) return false;
-  const long long units = static_cast<long long>(T) * k * blk_count(I) + blk_count(I_shared);
-  const int sms = 152;  // (a workspace's size does not depend on the current device)
-  return units * ((d / 16 + sms - 1) / sms) <= 72;
+  const int turns = (d / kBlkFewRows + kSms - 1) / kSms;
+  // (one or two tokens gain from CTAs that share the work, 1, 1152, 704, 12: 15.5 against 16.9 us; of more the gate/up product
+  // takes longer than that gives, 4, 320, 416, 7, s: 13.4 against 11.4)
+  return few_units(T, I, k, I_shared) * turns <= 72 * (T <= 2 ? few_split(T, d, I, k, I_shared) : 1);
 }
 
 struct ExpertLayout {
@@ -268,6 +285,7 @@ moe_status forward(const uint16_t* X, const moe_blk_mat* XQ, int T, int d, int I
     a.I_shared = I_shared;
     a.E = E;
     a.tiles = T * k < L.max_blocks ? T * k : L.max_blocks;
+    a.split = few_split(T, d, I, k, I_shared);
     return done(launch_blk_few_experts(a, cuda(stream), pdl_enabled()));
   }
 

@@ -19,7 +19,7 @@
 namespace bm {
 namespace {
 
-constexpr int kRows = 16;     // weight rows of a CTA
+constexpr int kRows = kBlkFewRows;  // weight rows of a CTA
 constexpr int kTokens = 8;    // an MMA's N
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 2) blk_few_linear_kernel(const BlkFe
 // most eight rows), fp32 h to memory.  down: a CTA
 // 16 columns of Y over all experts: its warps take the (expert, block of h) pairs
 // in turn, quantise h, and add each token's column with its routing weight, so that
-// nothing is added up between CTAs.  The gate/up kernel lets the down kernel start
+// nothing is added up between CTAs (but those of a cluster, which share the pairs
+// where d alone makes few CTAs: one token, d = 320, 8 experts 7.6 -> 7.0 us).  The gate/up kernel lets the down kernel start
 // after its own wait, when the routing has completed: the down kernel asks for its
 // first weights before it waits for h.
 
@@ -415,11 +416,14 @@ struct SharedDown {
   int e[kMaxRouted], row0[kMaxRouted], rows[kMaxRouted];  // of a routed tile; no rows: malformed
   int token[kMaxRouted];                                  // of an assignment's row; -1: malformed
   float w[kMaxRouted];
+  float sums[kRows * kTokens];                            // of the CTA, for the cluster's first
 };
 __global__ void __launch_bounds__(32 * kWarpsDown) blk_few_down_kernel(const BlkFewArgs a) {
   __shared__ SharedDown sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * kRows, A = a.T * a.k;
+  const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.split));
+  const int n0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.split)) * kRows, A = a.T * a.k;
+  const int u_first = rank * kWarpsDown + warp, u_step = a.split * kWarpsDown;  // this warp's units
   const int blocks_r = blk_count(a.I), blocks_s = a.I_shared > 0 ? blk_count(a.I_shared) : 0;
   // (the routing has completed: see above)
   const int nb = routed_tiles(a);
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown) blk_few_down_kernel(const Blk
     s = __ldg(m.s_down + (static_cast<size_t>(e) * blk_count(a.d) + n0 / kBlk) * blk_count(K) + kb);
   };
 #pragma unroll
-  for (int j = 0; j < kDepthDown; ++j) load(warp + j * kWarpsDown, w[j], sw[j]);
+  for (int j = 0; j < kDepthDown; ++j) load(u_first + j * u_step, w[j], sw[j]);
   pdl_wait();
   pdl_launch_dependents();
   const int pitch = max(a.I, a.I_shared);
@@ -490,30 +494,42 @@ __global__ void __launch_bounds__(32 * kWarpsDown) blk_few_down_kernel(const Blk
     multiply(d, m, b);
     add(acc, d, c.sa[0], c.sa[1]);
   };
-  for (int u0 = warp; u0 < units; u0 += kDepthDown * kWarpsDown) {
+  for (int u0 = u_first; u0 < units; u0 += kDepthDown * u_step) {
     float4 v[kDepthDown];
 #pragma unroll
-    for (int j = 0; j < kDepthDown; ++j) v[j] = ask(u0 + j * kWarpsDown, 0);
+    for (int j = 0; j < kDepthDown; ++j) v[j] = ask(u0 + j * u_step, 0);
 #pragma unroll
     for (int j = 0; j < kDepthDown; ++j) {
-      const int u = u0 + j * kWarpsDown;
+      const int u = u0 + j * u_step;
       if (u >= units) break;
       take(u, w[j], sw[j], v[j]);
-      load(u + kDepthDown * kWarpsDown, w[j], sw[j]);
+      load(u + kDepthDown * u_step, w[j], sw[j]);
     }
   }
   put_sums(sm.p.sums[0][warp], acc, lane);
   __syncthreads();
-  if (threadIdx.x < kRows * kTokens) {
-    const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-    if (t < a.T && n0 + r < a.d)
-      a.y[static_cast<size_t>(t) * a.d + n0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(take_sum(sm.p.sums[0], kTokens * r + t)));
+  const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
+  const bool mine = threadIdx.x < kRows * kTokens;
+  float v = mine ? take_sum(sm.p.sums[0], kTokens * r + t) : 0.0f;
+  if (a.split > 1) {  // the CTAs' sums, in their order
+    if (mine) sm.sums[threadIdx.x] = v;
+    cluster_arrive_release();
+    cluster_wait();
+    if (mine && rank == 0)
+      for (int p = 1; p < a.split; ++p) v += ld_shared_cluster_f1(mapa_shared(&sm.sums[threadIdx.x], p));
+    cluster_arrive_release();  // (the others' shared memory has been read)
+    cluster_wait();
   }
+  if (mine && rank == 0 && t < a.T && n0 + r < a.d)
+    a.y[static_cast<size_t>(t) * a.d + n0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 template <typename A>
-cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, int threads, cudaStream_t stream, bool pdl, const A& a) {
-  cudaLaunchAttribute attr[1];
+cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, int threads, int cluster, cudaStream_t stream, bool pdl, const A& a) {
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
@@ -521,7 +537,7 @@ cudaError_t launch(int kind, void (*kernel)(A), dim3 grid, int threads, cudaStre
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   timer_begin(kind, stream);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   timer_end(kind, stream);
@@ -537,15 +553,15 @@ cudaError_t launch_blk_few_linear(const BlkFewLinearArgs& a, cudaStream_t stream
                       : a.T <= kTokens    ? blk_few_linear_kernel<1>
                       : a.T <= 2 * kTokens ? blk_few_linear_kernel<2>
                                            : blk_few_linear_kernel<4>;
-  return launch(kKBlkGemm, kernel, dim3((a.N + kRows - 1) / kRows), kThreads, stream, pdl, a);
+  return launch(kKBlkGemm, kernel, dim3((a.N + kRows - 1) / kRows), kThreads, 1, stream, pdl, a);
 }
 
 cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl) {
   const int tiles = a.tiles + (a.I_shared > 0 ? 1 : 0), I = a.I > a.I_shared ? a.I : a.I_shared;
   const auto gate_up = a.x.type == kBlkCodes ? blk_few_gate_up_kernel<kBlkCodes> : blk_few_gate_up_kernel<kBf16>;
-  const cudaError_t e = launch(kKBlkGateUp, gate_up, dim3((I + kRows - 1) / kRows, tiles), kThreads, stream, pdl, a);
+  const cudaError_t e = launch(kKBlkGateUp, gate_up, dim3((I + kRows - 1) / kRows, tiles), kThreads, 1, stream, pdl, a);
   if (e != cudaSuccess) return e;
-  return launch(kKBlkDown, blk_few_down_kernel, dim3((a.d + kRows - 1) / kRows), 32 * kWarpsDown, stream, pdl, a);
+  return launch(kKBlkDown, blk_few_down_kernel, dim3((a.d + kRows - 1) / kRows * a.split), 32 * kWarpsDown, a.split, stream, pdl, a);
 }
 
 }  // namespace bm

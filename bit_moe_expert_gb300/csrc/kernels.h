@@ -393,7 +393,10 @@ struct BlkFewArgs {
   uint32_t* status;
   int T, d, I, k, I_shared, E;
   int tiles;  // tiles of the routed experts launched
+  int split;  // CTAs, a cluster, that share a down tile's work
 };
+// A few-token down product covers this many columns of Y a CTA.
+constexpr int kBlkFewRows = 16;
 cudaError_t launch_blk_few_experts(const BlkFewArgs& a, cudaStream_t stream, bool pdl);
 
 // Tensor-core products.

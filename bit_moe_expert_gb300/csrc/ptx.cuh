@@ -516,6 +516,11 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ float ld_shared_cluster_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 // The shared::cluster address of this CTA's shared-memory location p in the
 // CTA of rank `rank`.
 __device__ __forceinline__ uint32_t mapa_shared(const void* p, uint32_t rank) {

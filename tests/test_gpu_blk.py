@@ -300,7 +300,8 @@ def test_forward(T, d, I, I_shared, E, k, rows, quantised):
 
 @pytest.mark.parametrize("T,d,I,I_shared,E,k,rows", [(1, 256, 1184, 0, 12, 8, 16), (2, 256, 608, 96, 8, 8, 33), (2, 320, 1216, 0, 9, 7, 128),
                                                      (8, 256, 96, 0, 16, 1, 16), (5, 2464, 64, 32, 12, 3, 16), (7, 512, 352, 0, 4, 3, 3),
-                                                     (1, 2560, 704, 704, 40, 12, 64), (8, 1024, 256, 0, 3, 2, 16)])
+                                                     (1, 2560, 704, 704, 40, 12, 64), (8, 1024, 256, 0, 3, 2, 16),
+                                                     (1, 320, 416, 416, 20, 7, 16), (2, 544, 608, 96, 9, 9, 16), (1, 1152, 704, 0, 16, 12, 16)])
 @pytest.mark.parametrize("quantised", [False, True])
 def test_forward_of_few_tokens(T, d, I, I_shared, E, k, rows, quantised):
     """Either way of computing few tokens, at sizes on both sides of where one follows on the other."""
