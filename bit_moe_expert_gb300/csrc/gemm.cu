@@ -455,19 +455,17 @@ __global__ void __launch_bounds__(Cfg<kGateUp, kBits>::kThreads, 1)
     const int swz = (row >> 2) & 1;
     int stage = 0, astage = 0;
     uint32_t phase = 0, aphase = 0;
-    bool ok = true;
-    for (int it = blockIdx.x; it < s.n_total && ok; it += gridDim.x) {
+    for (int it = blockIdx.x; it < s.n_total; it += gridDim.x) {
       const Item m = get_item(a, s, it, kGateUp);
       if (!m.ok) continue;
       for (int ks = 0; ks < n_stages<C::kG>(m.nk); ++ks) {
         // every warp waits for itself: no warp holds the others back, and the
         // warps drift apart, so their bursts do not all compete for issue
         // slots with the MMA issuer at once
-        if (!mbar_wait(&full[stage], phase, abort_flag) || !mbar_wait(&a_empty[astage], aphase ^ 1, abort_flag)) {
-          if (lane == 0) fail();
-          ok = false;
-          break;
-        }
+        // (where a wait gives up the warp goes on with what is there: its lanes stay together for the stores to tensor memory)
+        mbar_wait_issue(&full[stage], phase, abort_flag, a.status);
+        mbar_wait_issue(&a_empty[astage], aphase ^ 1, abort_flag, a.status);
+        __syncwarp();
         tc_fence_after();
         const uint8_t* st = stages + stage * C::kStageBytes;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(lanegrp * 32) << 16) + C::kABase + astage * C::kACols +
