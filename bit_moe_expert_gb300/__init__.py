@@ -271,9 +271,13 @@ class Experts:
         return st, self.__dict__["_cc"][10]
 
 
+_READS, _READS_IDS, _WRITES = range(3)  # what a call does with a Routing's buffers
+
+
 @dataclasses.dataclass
 class Routing:
-    """Device buffers written by moe_route."""
+    """Device buffers written by moe_route, as large as include/moe.h says or larger: a call that needs more than there
+    is raises ValueError."""
     ids: "object"
     w: "object"
     counts: "object"
@@ -307,14 +311,47 @@ class Routing:
                                     self.block_map, self.num_blocks)]
         if c[0] != at:
             st = _Routing(*at, self.block_rows)
-            c = self._known = (at, st, C.byref(st))
+            c = self._known = (at, st, C.byref(st), set())
         c[1].block_rows = self.block_rows
         return c
 
-    _known = (None, None, None)
+    _known = (None, None, None, None)
+
+    def __setattr__(self, name, value):
+        # a buffer put in another's place may start where that one did and be shorter
+        if name != "block_rows" and name != "_known":
+            self.__dict__.pop("_known", None)
+        object.__setattr__(self, name, value)
 
     def _c(self) -> _Routing:
         return self._cached()[1]
+
+    def _for(self, T: int, E: int, k: int, block_rows: int, use: int):
+        """What _cached gives, for a call of these sizes: the buffers that it uses (_WRITES: all; _READS_IDS, _READS:
+        what expert calls may read) have to be as large as include/moe.h says."""
+        c = self._cached()
+        call = (T, E, k, block_rows, use)
+        if call not in c[3]:  # (sizes found to fit, until a buffer changes)
+            A = T * k
+            tiles = -(-A // block_rows) + E if A > 0 and block_rows > 0 else 0
+            need = [("w", A), ("perm", A), ("inv_perm", A), ("block_map", 3 * tiles), ("num_blocks", 1)]
+            if use >= _READS_IDS:
+                need.append(("ids", A))
+            if use == _WRITES:
+                need += [("counts", E), ("offsets", E + 1)]
+            for name, n in need:
+                b = getattr(self, name)
+                if b is None:  # the library refuses the call where it needs it
+                    continue
+                if not b.is_cuda or b.element_size() != 4 or not b.is_contiguous():
+                    raise ValueError(f"routing: {name} ({b.dtype} on {b.device}), expected contiguous 32-bit values on a CUDA device")
+                if b.numel() < n:
+                    raise ValueError(f"routing: {name} has {b.numel()} elements, expected {n} or more for {T} tokens, "
+                                     f"{k} of {E} experts each, in tiles of {block_rows} rows")
+            if len(c[3]) >= 64:
+                c[3].clear()
+            c[3].add(call)
+        return c
 
 
 def workspace(nbytes: int, device="cuda"):
@@ -362,7 +399,7 @@ def moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
 
 def moe_route(logits, k: int, block_rows: int, out: Routing, ws, stream=None) -> None:
     T, E = logits.shape
-    r = out._c()
+    r = out._for(T, E, k, block_rows, _WRITES)[1]
     _check("moe_route", lib().moe_route(_ptr(logits), T, E, k, block_rows, C.byref(r), _ptr(ws), ws.numel(),
                                         _stream(stream)))
     out.block_rows = r.block_rows
@@ -379,7 +416,7 @@ def moe_route_x(X, W_r, k: int, block_rows: int, out: Routing, ws, logits, strea
     """moe_router_logits into `logits`, then moe_route on them."""
     T, d = X.shape
     E = W_r.shape[0]
-    r = out._c()
+    r = out._for(T, E, k, block_rows, _WRITES)[1]
     _check("moe_route_x", lib().moe_route_x(_ptr(X), T, d, _ptr(W_r), E, k, block_rows, _ptr(logits), C.byref(r),
                                             _ptr(ws), ws.numel(), _stream(stream)))
     out.block_rows = r.block_rows
@@ -396,7 +433,7 @@ def moe_route_noalloc(logits, k: int, block_rows: int, out: Routing, stream=None
     memory): uses the library's built-in scratch array; calls must not overlap
     on the GPU."""
     T, E = logits.shape
-    r = out._c()
+    r = out._for(T, E, k, block_rows, _WRITES)[1]
     _check("moe_route_noalloc", lib().moe_route_noalloc(_ptr(logits), T, E, k, block_rows, C.byref(r),
                                                         _stream(stream)))
     out.block_rows = r.block_rows
@@ -418,7 +455,7 @@ def moe_forward(X, routed: Experts, shared: Optional[Experts], routing: Routing,
     re = routed._c()
     se = shared._c() if shared is not None else None
     I_sh = shared.I if shared is not None else 0
-    rr = routing._c()
+    rr = routing._for(T, re.n_experts, k, routing.block_rows, _READS_IDS)[1]
     _check("moe_forward", lib().moe_forward(_ptr(X), T, d, routed.I, k, C.byref(re),
                                             C.byref(se) if se is not None else None, I_sh, C.byref(rr), _ptr(Y),
                                             _ptr(ws), ws.numel(), _stream(stream)))
@@ -434,7 +471,7 @@ def moe_layer(logits, X, routed: Experts, shared: Optional[Experts], k: int, blo
     T, d = X.shape
     re, I = routed._c_and_I()
     se, I_sh = shared._c_and_I() if shared is not None else (None, 0)
-    r = out._c()
+    r = out._for(T, re.n_experts, k, block_rows, _WRITES)[1]
     _check("moe_layer", lib().moe_layer(_ptr(logits), _ptr(X), T, d, I, k, block_rows, C.byref(re),
                                         C.byref(se) if se is not None else None, I_sh, C.byref(r), _ptr(Y),
                                         _ptr(ws), ws.numel(), _stream(stream)))
@@ -448,7 +485,7 @@ def moe_layer_x(X, W_r, routed: Experts, shared: Optional[Experts], k: int, bloc
     re = routed._c()
     se = shared._c() if shared is not None else None
     I_sh = shared.I if shared is not None else 0
-    r = out._c()
+    r = out._for(T, re.n_experts, k, block_rows, _WRITES)[1]
     _check("moe_layer_x", lib().moe_layer_x(_ptr(X), T, d, _ptr(W_r), routed.I, k, block_rows, C.byref(re),
                                             C.byref(se) if se is not None else None, I_sh, _ptr(logits), C.byref(r),
                                             _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)))
@@ -644,7 +681,7 @@ def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Rou
     """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
     _tensor("logits", logits, _ONLY_FP32)
     T, E = logits.shape
-    r = out._cached()[2]
+    r = out._for(T, E, k, block_rows, _WRITES)[2]
     status = lib().moe_route_scored(logits.data_ptr(), scoring._ref(E), T, E, k, block_rows, r, ws.data_ptr(),
                                     ws.numel(), _stream(stream))
     if status:
@@ -745,8 +782,9 @@ def _mx_sets(X, routed: MxExperts, shared: Optional[MxExperts], Y):
 def moe_mx_forward(X, routed: MxExperts, shared: Optional[MxExperts], routing: Routing, Y, ws, stream=None) -> None:
     """The expert layer on MXFP4 weights, for a routing of moe_route or moe_route_scored."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
-    rr = routing._cached()[2]
-    status = lib().moe_mx_forward(X.data_ptr(), T, d, I, int(routing.ids.shape[1]), re, se, I_sh, rr,
+    k = routing.ids.shape[1]
+    rr = routing._for(T, E, k, routing.block_rows, _READS)[2]
+    status = lib().moe_mx_forward(X.data_ptr(), T, d, I, k, re, se, I_sh, rr,
                                   Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
         _check("moe_mx_forward", status)
@@ -761,7 +799,7 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
     """moe_route_scored + moe_mx_forward in one call."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
     _tensor("logits", logits, _ONLY_FP32, (T, E))
-    r = out._cached()[2]
+    r = out._for(T, E, k, block_rows, _WRITES)[2]
     status = lib().moe_mx_layer(logits.data_ptr(), scoring._ref(E), X.data_ptr(), T, d, I, k, block_rows, re, se, I_sh,
                                 r, Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
@@ -990,8 +1028,9 @@ def _blk_sets(X, routed: BlkExperts, shared: Optional[BlkExperts], Y):
 def moe_blk_forward(X, routed: BlkExperts, shared: Optional[BlkExperts], routing: Routing, Y, ws, stream=None) -> None:
     """The expert layer on block-scaled 8-bit weights; X: bf16 [T][d], or a BlkAct taken as it is."""
     T, d, E, I, I_sh, re, se, xp, xq = _blk_sets(X, routed, shared, Y)
-    rr = routing._cached()[2]
-    status = lib().moe_blk_forward(xp, xq, T, d, I, int(routing.ids.shape[1]), re, se, I_sh, rr, Y.data_ptr(),
+    k = routing.ids.shape[1]
+    rr = routing._for(T, E, k, routing.block_rows, _READS)[2]
+    status = lib().moe_blk_forward(xp, xq, T, d, I, k, re, se, I_sh, rr, Y.data_ptr(),
                                    ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
         _check("moe_blk_forward", status)
@@ -1006,7 +1045,7 @@ def moe_blk_layer(logits, scoring: Scoring, X, routed: BlkExperts, shared: Optio
     """moe_route_scored + moe_blk_forward in one call."""
     T, d, E, I, I_sh, re, se, xp, xq = _blk_sets(X, routed, shared, Y)
     _tensor("logits", logits, _ONLY_FP32, (T, E))
-    r = out._cached()[2]
+    r = out._for(T, E, k, block_rows, _WRITES)[2]
     status = lib().moe_blk_layer(logits.data_ptr(), scoring._ref(E), xp, xq, T, d, I, k, block_rows, re, se, I_sh, r,
                                  Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
