@@ -246,7 +246,10 @@ moe_status check_experts(const uint16_t* X, const moe_blk_mat* XQ, int T, int d,
 bool items_ok(int T, int d, int I, int E, int k, int I_shared, int block_rows) {
   auto m_tiles = [](int a, int b) { return static_cast<long long>(blk_count(a > b ? a : b)); };
   long long items = moe_route_max_blocks(T, E, k, block_rows) * m_tiles(d, I);
-  if (I_shared > 0) items += blk_count(T < 1 ? 1 : T) * m_tiles(d, I_shared);
+  if (I_shared > 0) {
+    const int rows = shared_tile_rows(T, block_rows);
+    items += (T + rows - 1) / rows * m_tiles(d, I_shared);
+  }
   return items <= kBlkMaxItems;
 }
 

@@ -132,6 +132,22 @@ def test_expert_calls_refuse_more_items_than_are_counted(L, layer):
     assert call(T=(1 << 17) - 4, d=1 << 20, k=1, E=4, I_sh=32, br=1) == UNSUPPORTED  # the shared expert's tiles
 
 
+@pytest.mark.parametrize("layer", [False, True])
+def test_items_of_the_shared_expert_are_counted_in_tiles_of_its_height(L, layer):
+    def call(T, I_sh, br):
+        ex, sh = bm._BlkExperts(M, M, M, 4), bm._BlkExperts(M, M, M, 1)
+        a = (C.byref(ex), C.byref(sh), I_sh, C.byref(bm._Routing(*([FAKE] * 8), br)), FAKE, FAKE, 0, None)  # no workspace
+        if layer:
+            return L.moe_blk_layer(FAKE, C.byref(_scoring()), FAKE, None, T, 32, 32, 1, br, *a)
+        return L.moe_blk_forward(FAKE, None, T, 32, 32, 1, *a)
+
+    # tiles of 16 tokens, 2^13 M tiles each, and ceil(T/16) + 4 routed ones of one M tile: 2^30 - 12, then 2^30 + 8181
+    assert call((1 << 21) - 16 * 16, 1 << 20, 16) == WORKSPACE
+    assert call((1 << 21) - 16 * 15, 1 << 20, 16) == UNSUPPORTED
+    assert call((1 << 21) - 16 * 15, 1 << 20, 1) == UNSUPPORTED
+    assert call((1 << 21) - 16 * 15, 1 << 20, 32) == WORKSPACE
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError, match="CUDA"):
