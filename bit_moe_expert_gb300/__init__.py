@@ -633,13 +633,14 @@ class MxMat:
         E, N, half = self.q.shape
         return int(E), int(N), 2 * int(half)
 
-    _known = (None, None, 0, 0, 0, None)  # q, sp, their addresses, q's size, what _ref_and_shape gives
+    _known = (None, None, 0, 0, None, 0, None)  # q, sp, their addresses, q's shape, sp's size, what _ref_and_shape gives
 
     def _ref_and_shape(self):
-        """A reference to the C struct, (E, N, K), and the struct: rebuilt where a tensor, its memory or size changed."""
+        """A reference to the C struct, (E, N, K), and the struct: rebuilt where a tensor, its memory or layout changed."""
         q, sp = self.q, self.sp
-        kq, ks, aq, asp, size, known = self._known
-        if q is not kq or sp is not ks or q.data_ptr() != aq or sp.data_ptr() != asp or q.numel() != size:
+        kq, ks, aq, asp, qshape, size, known = self._known
+        if (q is not kq or sp is not ks or q.data_ptr() != aq or sp.data_ptr() != asp or q.shape != qshape
+                or sp.numel() != size or not q.is_contiguous()):
             _tensor("q", q, (_U8,))
             if q.dim() != 3:
                 raise ValueError(f"q: shape {tuple(q.shape)}, expected [E][N][K/2]")
@@ -647,7 +648,7 @@ class MxMat:
             _tensor("sp", sp, (_U8,), (E, -(-N // 128), -(-K // 128), 512))
             st = _MxMat(_ptr(q), _ptr(sp))
             known = (C.byref(st), (E, N, K), st)
-            self._known = (q, sp, st.q, st.sp, q.numel(), known)
+            self._known = (q, sp, st.q, st.sp, q.shape, sp.numel(), known)
         return known
 
     def _c(self) -> _MxMat:
@@ -818,20 +819,21 @@ class _BlkCodes:
     q: "object"
     s: "object"
 
-    _known = (None, None, 0, 0, 0, None)  # q, s, their addresses, q's size, what _ref_and_shape gives
+    _known = (None, None, 0, 0, None, 0, None)  # q, s, their addresses, q's shape, s's size, what _ref_and_shape gives
 
     def _ref_and_shape(self):
-        """A reference to the C struct, the shape, and the struct: rebuilt where a tensor, its memory or size changed."""
+        """A reference to the C struct, the shape, and the struct: rebuilt where a tensor, its memory or layout changed."""
         q, s = self.q, self.s
-        kq, ks, aq, at, size, known = self._known
-        if q is not kq or s is not ks or q.data_ptr() != aq or s.data_ptr() != at or q.numel() != size:
+        kq, ks, aq, at, qshape, size, known = self._known
+        if (q is not kq or s is not ks or q.data_ptr() != aq or s.data_ptr() != at or q.shape != qshape
+                or s.numel() != size or not q.is_contiguous()):
             _tensor("q", q, _CODES)
             shape, scales = self._shapes()
             _tensor("s", s, _ONLY_FP32, scales)
             aq, at = q.data_ptr(), s.data_ptr()
             st = _BlkMat(aq, at)
             known = (C.byref(st), shape, st)
-            self._known = (q, s, aq, at, q.numel(), known)
+            self._known = (q, s, aq, at, q.shape, s.numel(), known)
         return known
 
 
