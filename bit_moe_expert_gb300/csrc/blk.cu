@@ -380,7 +380,8 @@ __global__ void __launch_bounds__(1024)
       for (int j = 0; j < 8; ++j) most = fmax(most, fabs(exact_value(r[i][j], g[gi][j], inv)));
 #pragma unroll
       for (int k = 1; k < 16; k *= 2) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, k));
-      if (m <= 0x7F800000u) s = blk_scale(__float_as_uint(odd_float(most)));
+      // (a y past fp32's range is infinite whatever the warp's other block asks for)
+      if (m < 0x7F800000u) s = blk_scale(__float_as_uint(odd_float(most)));
     }
     const float t = blk_inverse(s);
     uint2 code = blk_codes8(y, t * (1.0f - kNormError));

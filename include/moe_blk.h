@@ -99,7 +99,9 @@ moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long lo
  * open, y is evaluated to about 2^-27 (2^-24 where a few values make up the
  * row's sum of squares).  A row whose sum of squares is not finite in
  * fp32 (or 0, with eps = 0) is NaN.  (That is where mean(r^2) + eps is at least
- * 2^-80: the squares of smaller numbers lose bits in fp32.)
+ * 2^-80, the squares of smaller numbers lose bits in fp32, and where neither y
+ * nor r / sqrt(..) is below fp32's normal numbers.)  A y past fp32's range is
+ * infinite, and so its block's scale NaN.
  * Preconditions: T >= 0 (0 does nothing), d a positive multiple of 16 up to
  * 32768 (MOE_ERR_UNSUPPORTED above), eps >= 0 and finite, X and the row pitch
  * multiples of 16 bytes. */
