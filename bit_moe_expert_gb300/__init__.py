@@ -300,25 +300,28 @@ class Routing:
                        block_map=torch.empty((mb, 3), **i32), num_blocks=torch.zeros(1, **i32),
                        block_rows=block_rows)
 
-    def _cached(self):
-        """The buffers' addresses, the C struct and a reference to it: rebuilt where an address changed."""
+    def _cached(self, call=None):
+        """The buffers' addresses, the C struct and a reference to it: rebuilt where an address changed.  call: (T, E, k,
+        block_rows, use) of a call, for which they have to be large enough."""
         c = self._known
-        try:
-            at = [self.ids.data_ptr(), self.w.data_ptr(), self.counts.data_ptr(), self.offsets.data_ptr(),
-                  self.perm.data_ptr(), self.inv_perm.data_ptr(), self.block_map.data_ptr(), self.num_blocks.data_ptr()]
-        except AttributeError:  # a buffer that is None
-            at = [_ptr(b) for b in (self.ids, self.w, self.counts, self.offsets, self.perm, self.inv_perm,
-                                    self.block_map, self.num_blocks)]
+        at = [b.data_ptr() for b in c[4]]
         if c[0] != at:
-            st = _Routing(*at, self.block_rows)
-            c = self._known = (at, st, C.byref(st), set())
+            every = (self.ids, self.w, self.counts, self.offsets, self.perm, self.inv_perm, self.block_map, self.num_blocks)
+            st = _Routing(*(_ptr(b) for b in every), self.block_rows)
+            there = [b for b in every if b is not None]
+            c = self._known = ([b.data_ptr() for b in there], st, C.byref(st), set(), there)
         c[1].block_rows = self.block_rows
+        if call is not None and call not in c[3]:  # (calls found to fit, until a buffer changes)
+            self._check(*call)
+            if len(c[3]) >= 64:
+                c[3].clear()
+            c[3].add(call)
         return c
 
-    _known = (None, None, None, None)
+    _known = (None, None, None, None, ())  # addresses, struct, reference, calls, the buffers that there are
 
     def __setattr__(self, name, value):
-        # a buffer put in another's place may start where that one did and be shorter
+        # (a buffer put in another's place may start where that one did and be shorter)
         if name != "block_rows" and name != "_known":
             self.__dict__.pop("_known", None)
         object.__setattr__(self, name, value)
@@ -326,32 +329,25 @@ class Routing:
     def _c(self) -> _Routing:
         return self._cached()[1]
 
-    def _for(self, T: int, E: int, k: int, block_rows: int, use: int):
-        """What _cached gives, for a call of these sizes: the buffers that it uses (_WRITES: all; _READS_IDS, _READS:
-        what expert calls may read) have to be as large as include/moe.h says."""
-        c = self._cached()
-        call = (T, E, k, block_rows, use)
-        if call not in c[3]:  # (sizes found to fit, until a buffer changes)
-            A = T * k
-            tiles = -(-A // block_rows) + E if A > 0 and block_rows > 0 else 0
-            need = [("w", A), ("perm", A), ("inv_perm", A), ("block_map", 3 * tiles), ("num_blocks", 1)]
-            if use >= _READS_IDS:
-                need.append(("ids", A))
-            if use == _WRITES:
-                need += [("counts", E), ("offsets", E + 1)]
-            for name, n in need:
-                b = getattr(self, name)
-                if b is None:  # the library refuses the call where it needs it
-                    continue
-                if not b.is_cuda or b.element_size() != 4 or not b.is_contiguous():
-                    raise ValueError(f"routing: {name} ({b.dtype} on {b.device}), expected contiguous 32-bit values on a CUDA device")
-                if b.numel() < n:
-                    raise ValueError(f"routing: {name} has {b.numel()} elements, expected {n} or more for {T} tokens, "
-                                     f"{k} of {E} experts each, in tiles of {block_rows} rows")
-            if len(c[3]) >= 64:
-                c[3].clear()
-            c[3].add(call)
-        return c
+    def _check(self, T: int, E: int, k: int, block_rows: int, use: int) -> None:
+        """The buffers that a call uses (_WRITES: all; _READS_IDS, _READS: what expert calls may read) are as large as
+        include/moe.h says."""
+        A = T * k
+        tiles = -(-A // block_rows) + E if A > 0 and block_rows > 0 else 0
+        need = [("w", A), ("perm", A), ("inv_perm", A), ("block_map", 3 * tiles), ("num_blocks", 1)]
+        if use >= _READS_IDS:
+            need.append(("ids", A))
+        if use == _WRITES:
+            need += [("counts", E), ("offsets", E + 1)]
+        for name, n in need:
+            b = getattr(self, name)
+            if b is None:  # the library refuses the call where it needs it
+                continue
+            if not b.is_cuda or b.element_size() != 4 or not b.is_contiguous():
+                raise ValueError(f"routing: {name} ({b.dtype} on {b.device}), expected contiguous 32-bit values on a CUDA device")
+            if b.numel() < n:
+                raise ValueError(f"routing: {name} has {b.numel()} elements, expected {n} or more for {T} tokens, "
+                                 f"{k} of {E} experts each, in tiles of {block_rows} rows")
 
 
 def workspace(nbytes: int, device="cuda"):
@@ -399,7 +395,7 @@ def moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
 
 def moe_route(logits, k: int, block_rows: int, out: Routing, ws, stream=None) -> None:
     T, E = logits.shape
-    r = out._for(T, E, k, block_rows, _WRITES)[1]
+    r = out._cached((T, E, k, block_rows, _WRITES))[1]
     _check("moe_route", lib().moe_route(_ptr(logits), T, E, k, block_rows, C.byref(r), _ptr(ws), ws.numel(),
                                         _stream(stream)))
     out.block_rows = r.block_rows
@@ -416,7 +412,7 @@ def moe_route_x(X, W_r, k: int, block_rows: int, out: Routing, ws, logits, strea
     """moe_router_logits into `logits`, then moe_route on them."""
     T, d = X.shape
     E = W_r.shape[0]
-    r = out._for(T, E, k, block_rows, _WRITES)[1]
+    r = out._cached((T, E, k, block_rows, _WRITES))[1]
     _check("moe_route_x", lib().moe_route_x(_ptr(X), T, d, _ptr(W_r), E, k, block_rows, _ptr(logits), C.byref(r),
                                             _ptr(ws), ws.numel(), _stream(stream)))
     out.block_rows = r.block_rows
@@ -433,7 +429,7 @@ def moe_route_noalloc(logits, k: int, block_rows: int, out: Routing, stream=None
     memory): uses the library's built-in scratch array; calls must not overlap
     on the GPU."""
     T, E = logits.shape
-    r = out._for(T, E, k, block_rows, _WRITES)[1]
+    r = out._cached((T, E, k, block_rows, _WRITES))[1]
     _check("moe_route_noalloc", lib().moe_route_noalloc(_ptr(logits), T, E, k, block_rows, C.byref(r),
                                                         _stream(stream)))
     out.block_rows = r.block_rows
@@ -455,7 +451,7 @@ def moe_forward(X, routed: Experts, shared: Optional[Experts], routing: Routing,
     re = routed._c()
     se = shared._c() if shared is not None else None
     I_sh = shared.I if shared is not None else 0
-    rr = routing._for(T, re.n_experts, k, routing.block_rows, _READS_IDS)[1]
+    rr = routing._cached((T, re.n_experts, k, routing.block_rows, _READS_IDS))[1]
     _check("moe_forward", lib().moe_forward(_ptr(X), T, d, routed.I, k, C.byref(re),
                                             C.byref(se) if se is not None else None, I_sh, C.byref(rr), _ptr(Y),
                                             _ptr(ws), ws.numel(), _stream(stream)))
@@ -471,7 +467,7 @@ def moe_layer(logits, X, routed: Experts, shared: Optional[Experts], k: int, blo
     T, d = X.shape
     re, I = routed._c_and_I()
     se, I_sh = shared._c_and_I() if shared is not None else (None, 0)
-    r = out._for(T, re.n_experts, k, block_rows, _WRITES)[1]
+    r = out._cached((T, re.n_experts, k, block_rows, _WRITES))[1]
     _check("moe_layer", lib().moe_layer(_ptr(logits), _ptr(X), T, d, I, k, block_rows, C.byref(re),
                                         C.byref(se) if se is not None else None, I_sh, C.byref(r), _ptr(Y),
                                         _ptr(ws), ws.numel(), _stream(stream)))
@@ -485,7 +481,7 @@ def moe_layer_x(X, W_r, routed: Experts, shared: Optional[Experts], k: int, bloc
     re = routed._c()
     se = shared._c() if shared is not None else None
     I_sh = shared.I if shared is not None else 0
-    r = out._for(T, re.n_experts, k, block_rows, _WRITES)[1]
+    r = out._cached((T, re.n_experts, k, block_rows, _WRITES))[1]
     _check("moe_layer_x", lib().moe_layer_x(_ptr(X), T, d, _ptr(W_r), routed.I, k, block_rows, C.byref(re),
                                             C.byref(se) if se is not None else None, I_sh, _ptr(logits), C.byref(r),
                                             _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)))
@@ -682,7 +678,7 @@ def moe_route_scored(logits, scoring: Scoring, k: int, block_rows: int, out: Rou
     """moe_route with softmax or sigmoid scores, a selection bias and groups (fp32 logits [T][E])."""
     _tensor("logits", logits, _ONLY_FP32)
     T, E = logits.shape
-    r = out._for(T, E, k, block_rows, _WRITES)[2]
+    r = out._cached((T, E, k, block_rows, _WRITES))[2]
     status = lib().moe_route_scored(logits.data_ptr(), scoring._ref(E), T, E, k, block_rows, r, ws.data_ptr(),
                                     ws.numel(), _stream(stream))
     if status:
@@ -784,7 +780,7 @@ def moe_mx_forward(X, routed: MxExperts, shared: Optional[MxExperts], routing: R
     """The expert layer on MXFP4 weights, for a routing of moe_route or moe_route_scored."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
     k = routing.ids.shape[1]
-    rr = routing._for(T, E, k, routing.block_rows, _READS)[2]
+    rr = routing._cached((T, E, k, routing.block_rows, _READS))[2]
     status = lib().moe_mx_forward(X.data_ptr(), T, d, I, k, re, se, I_sh, rr,
                                   Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
@@ -800,7 +796,7 @@ def moe_mx_layer(logits, scoring: Scoring, X, routed: MxExperts, shared: Optiona
     """moe_route_scored + moe_mx_forward in one call."""
     T, d, E, I, I_sh, re, se = _mx_sets(X, routed, shared, Y)
     _tensor("logits", logits, _ONLY_FP32, (T, E))
-    r = out._for(T, E, k, block_rows, _WRITES)[2]
+    r = out._cached((T, E, k, block_rows, _WRITES))[2]
     status = lib().moe_mx_layer(logits.data_ptr(), scoring._ref(E), X.data_ptr(), T, d, I, k, block_rows, re, se, I_sh,
                                 r, Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
@@ -819,26 +815,28 @@ class _BlkCodes:
     q: "object"
     s: "object"
 
-    _known = (None, None, 0, 0, None, 0, None)  # q, s, their addresses, q's shape, s's size, what _ref_and_shape gives
+    _known = (None, None, 0, 0, None, 0, 0, None, None)  # q, s, what they were like, what _ref_and_shape gives
 
     def _ref_and_shape(self):
         """A reference to the C struct, the shape, and the struct: rebuilt where a tensor, its memory or layout changed."""
         q, s = self.q, self.s
-        kq, ks, aq, at, qshape, size, known = self._known
-        if (q is not kq or s is not ks or q.data_ptr() != aq or s.data_ptr() != at or q.shape != qshape
-                or s.numel() != size or not q.is_contiguous()):
+        kq, ks, aq, at, strides, size, sn, stype, known = self._known
+        # (the strides of a contiguous q say all but its first size; a stack's is that of s too)
+        if (q is not kq or s is not ks or q.data_ptr() != aq or s.data_ptr() != at or q.stride() != strides
+                or s.numel() != sn or s.dtype is not stype or self._rows and q.numel() != size):
             _tensor("q", q, _CODES)
             shape, scales = self._shapes()
             _tensor("s", s, _ONLY_FP32, scales)
             aq, at = q.data_ptr(), s.data_ptr()
             st = _BlkMat(aq, at)
             known = (C.byref(st), shape, st)
-            self._known = (q, s, aq, at, q.shape, s.numel(), known)
+            self._known = (q, s, aq, at, q.stride(), q.numel(), s.numel(), s.dtype, known)
         return known
 
 
 class BlkMat(_BlkCodes):
     """A stack of weight matrices: q [E][N][K], s [E][ceil(N/128)][ceil(K/128)], as checkpoints hold them."""
+    _rows = False
 
     @staticmethod
     def empty(E: int, N: int, K: int, device="cuda") -> "BlkMat":
@@ -856,6 +854,7 @@ class BlkMat(_BlkCodes):
 
 class BlkAct(_BlkCodes):
     """Activations: q [rows][K], s [ceil(K/128)][rows up to a multiple of 4]."""
+    _rows = True
 
     @staticmethod
     def empty(rows: int, K: int, device="cuda") -> "BlkAct":
@@ -1031,7 +1030,7 @@ def moe_blk_forward(X, routed: BlkExperts, shared: Optional[BlkExperts], routing
     """The expert layer on block-scaled 8-bit weights; X: bf16 [T][d], or a BlkAct taken as it is."""
     T, d, E, I, I_sh, re, se, xp, xq = _blk_sets(X, routed, shared, Y)
     k = routing.ids.shape[1]
-    rr = routing._for(T, E, k, routing.block_rows, _READS)[2]
+    rr = routing._cached((T, E, k, routing.block_rows, _READS))[2]
     status = lib().moe_blk_forward(xp, xq, T, d, I, k, re, se, I_sh, rr, Y.data_ptr(),
                                    ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
@@ -1047,7 +1046,7 @@ def moe_blk_layer(logits, scoring: Scoring, X, routed: BlkExperts, shared: Optio
     """moe_route_scored + moe_blk_forward in one call."""
     T, d, E, I, I_sh, re, se, xp, xq = _blk_sets(X, routed, shared, Y)
     _tensor("logits", logits, _ONLY_FP32, (T, E))
-    r = out._for(T, E, k, block_rows, _WRITES)[2]
+    r = out._cached((T, E, k, block_rows, _WRITES))[2]
     status = lib().moe_blk_layer(logits.data_ptr(), scoring._ref(E), xp, xq, T, d, I, k, block_rows, re, se, I_sh, r,
                                  Y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     if status:

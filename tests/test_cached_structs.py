@@ -36,6 +36,8 @@ def test_a_new_shape_of_the_same_size_is_the_calls_shape():
         a._ref_and_shape()
     a.s.resize_(1, 8)
     assert a._ref_and_shape()[1] == (8, 128)
+    a.q.resize_(6, 128)                                          # as many rows of scales
+    assert a._ref_and_shape()[1] == (6, 128)
     m.q.resize_(2, 512, 256)
     with pytest.raises(ValueError, match="s: shape"):
         m._ref_and_shape()
@@ -77,3 +79,11 @@ def test_a_transposed_matrix_or_a_shorter_table_of_scales_is_refused(make, scale
         m._ref_and_shape()
     s.resize_(shape)
     m._ref_and_shape()
+
+
+def test_scales_of_another_type_at_the_same_address_are_refused():
+    for m in (_blk(1, 256, 256), _act(8, 256)):
+        m._ref_and_shape()
+        m.s.data = m.s.view(torch.int32)
+        with pytest.raises(ValueError, match="s: torch.int32"):
+            m._ref_and_shape()

@@ -28,6 +28,9 @@ class _Tensor:
     def numel(self):
         return int(np.prod(self.shape))
 
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
     def element_size(self):
         return self.dtype.itemsize
 
