@@ -63,16 +63,18 @@ struct LinearPlan {
   bool few;   // the products for few tokens
   int bn;     // else the height of the tiles of tokens (more than kBlkNarrow: the wide kernel's)
   int split;  // and the CTAs that share a tile's blocks of 128 columns
+  double time;
 };
+constexpr double kStream = 5.5e6;  // the weights' bytes a microsecond, as fast as these kernels get them
 LinearPlan linear_plan(int M, int N, int K, int num_sms) {
   const int blocks = blk_count(K);
-  const double stream = static_cast<double>(N) * K / 5.5e6;  // the weights' bytes, as fast as these kernels get them
+  const double stream = static_cast<double>(N) * K / kStream;
   LinearPlan best{};
   double time = 1e30;
   auto consider = [&](double t, bool few, int bn, int split) {
     if (t >= time) return;
     time = t;
-    best = LinearPlan{few, bn, split};
+    best = LinearPlan{few, bn, split, t};
   };
   if (M <= kBlkFewLinear) {
     // a CTA's eight warps take a block each in turn.  Measured, 2048 -> 2048 / 5120 -> 1024 / 8192 -> 8192: 8 tokens 2.9 /
@@ -103,6 +105,16 @@ LinearPlan linear_plan(int M, int N, int K, int num_sms) {
   // 128 tokens x 256 weight rows: 256 x 8192 -> 8192 32.7 us (64/1 43.9), 300 x 2048 -> 4096 10.3 (64/1 12.7)
   if (M > kBlkNarrow) consider(1.8 + turns(tiles(2 * kBlk, 128)) * (0.44 * blocks + 1.2), false, 128, 1);
   return best;
+}
+
+// Whether one token of a linear layer is quantised in the warps that multiply it (a launch less, but each CTA's eight warps
+// go through all of K) rather than by a launch before the product.  Measured, K -> N, so / the other way: 2048 -> 2048 1.9 /
+// 4.0 us, 2048 -> 24576 12.7 / 14.6, 8192 -> 512 6.5 / 7.5, 8192 -> 8192 16.6 / 16.1, 4096 -> 60000 48 / 45, 16384 -> 1024
+// 14.0 / 9.7, 16384 -> 16384 64 / 45, 65536 -> 128 54 / 20
+bool one_launch_wins(int N, int K, int num_sms) {
+  const double ctas = 0.9 * N / (16.0 * num_sms), time = 1.0 + 0.6 * blk_count(K) / 8 * (ctas > 1 ? ctas : 1);
+  // (no plan takes less than 1.7 us and the weights' stream, but the same warps': those sizes need no look at the others)
+  return time <= 3.7 + static_cast<double>(N) * K / kStream || time <= linear_plan(1, N, K, num_sms).time + 2.0;
 }
 
 moe_status matmul(const moe_blk_mat& A, int M, const moe_blk_mat* W, int N, int K, void* Y, moe_dtype y_type,
@@ -403,7 +415,11 @@ moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long lo
   if (T == 0) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
   const moe_blk_mat xq{w, reinterpret_cast<float*>(w + round256(static_cast<size_t>(T) * K))};
-  if (T == 1) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
+  if (T == 1) {
+    const int num_sms = device_sms();
+    if (num_sms <= 0) return MOE_ERR_CUDA;
+    if (one_launch_wins(N, K, num_sms)) return few_linear(BlkX{X, nullptr, ldx, 0, x_type}, T, W, N, K, Y, y_type, stream);
+  }
   if (launch_blk_quantize(X, x_type, T, K, ldx, xq.q, xq.s, cuda(stream), pdl_enabled()) != cudaSuccess) return MOE_ERR_CUDA;
   return matmul(xq, T, W, N, K, Y, y_type, &static_cast<WsHeader*>(ws)->status, stream);
 }

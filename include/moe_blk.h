@@ -78,7 +78,9 @@ moe_status moe_blk_matmul(const moe_blk_mat* A, int M, const moe_blk_mat* W, int
 /* Workspace bytes of moe_blk_linear (the quantised X); 0 for a bad size. */
 size_t moe_blk_linear_workspace_bytes(int T, int N, int K);
 
-/* A linear layer: moe_blk_quantize(X [T][K]), then moe_blk_matmul. */
+/* A linear layer: moe_blk_quantize(X [T][K]), then moe_blk_matmul.  (One token
+ * may be quantised within the product, whose sums are then added in another
+ * order than that of moe_blk_matmul.) */
 moe_status moe_blk_linear(const void* X, moe_dtype x_type, int T, int K, long long ldx, const moe_blk_mat* W, int N,
                           void* Y, moe_dtype y_type, void* ws, size_t ws_bytes, moe_stream stream);
 
