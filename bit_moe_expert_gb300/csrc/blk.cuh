@@ -83,10 +83,10 @@ __device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
 
-// n (8, 16 or 32) columns of each lane's own row of tensor memory.
+// n (8 or 16) columns of each lane's own row of tensor memory.
 template <int n>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[n]) {
-  if constexpr (n == 8) tmem_ld8(taddr, v); else if constexpr (n == 16) tmem_ld16(taddr, v); else tmem_ld32(taddr, v);
+  if constexpr (n == 8) tmem_ld8(taddr, v); else tmem_ld16(taddr, v);
 }
 
 // |x| of the largest of the lane's values, as bits; a NaN's are above infinity's.

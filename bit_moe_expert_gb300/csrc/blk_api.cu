@@ -160,7 +160,9 @@ int shared_tile_rows(int T, int block_rows) {
   return most < rows ? most : rows;
 }
 
-constexpr int kSms = 152;  // (a workspace's size does not depend on the current device)
+// The experts' rules below take the SMs of the GPU that this is compiled for, where a dense product's plan asks the device:
+// they decide the workspace's layout, which a host may ask for on another device, or without one.
+constexpr int kSms = 152;
 long long few_units(int T, int I, int k, int I_shared) { return static_cast<long long>(T) * k * blk_count(I) + blk_count(I_shared); }
 // CTAs, a cluster, that share the down product's work on their columns: while there is work for their 16 warps each, and room
 // for the clusters (see linear_plan).

@@ -6,10 +6,13 @@
 // turn.  A lane loads 32 consecutive bytes of each of two rows straight from
 // global memory into the A fragments of four warp-level MMAs (m16n8k32, E4M3,
 // fp32 accumulate): which columns an MMA takes together is free as long as both
-// operands agree, so no byte is moved between lanes.  Up to eight tokens are the
-// MMA's N.  The activations are quantised in the warp that needs them, a block is its
-// 32 lanes' four values each.  The blocks' sums are scaled and added in fp32, the
-// warps' at the end through shared memory in a fixed order.
+// operands agree, so no byte is moved between lanes.  Eight tokens are an MMA's N.
+// Linear products: one token is quantised in the warp that needs the block (its 32
+// lanes' four values each), up to 32 tokens come as codes, in groups of eight, a
+// lane's bytes of its column's token being the B fragments.  Experts: up to eight
+// tokens, bf16 or codes, and h, quantised likewise in the warp that needs them.  The
+// blocks' sums are scaled and added in fp32, the warps' at the end through shared
+// memory in a fixed order.
 #include <cuda_runtime.h>
 
 #include "blk.cuh"
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) blk_one_linear_kernel(const BlkFe
 
 // Up to 8 kGroups tokens that are quantised already: a lane's 32 bytes of its
 // column's token are the B fragments, as its bytes of two rows are the A fragments.
+// (Four groups do not quite fit the 128 registers of two CTAs an SM: 108 bytes go through the stack.)
 template <int kGroups>
 __global__ void __launch_bounds__(kThreads, 2) blk_few_linear_kernel(const BlkFewLinearArgs a) {
   __shared__ float sums[kGroups][kWarps][kRows * kTokens];

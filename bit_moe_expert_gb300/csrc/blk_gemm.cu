@@ -466,7 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1;
         }
       }
-      if (!ok) break;
       if constexpr (V::kMode == kLinear) {
         if (a.split > 1) {  // every MMA of the item has completed: the stages' memory is free
           put_sums<V>(reinterpret_cast<float*>(stages), m.rows, acc, quarter, part, lane);
